@@ -71,6 +71,17 @@ SIGNATURES = {
     "foak_linear_ce_workspace_size": (_sz, [_i64, _i64, _i64, _i64]),
     "foak_linear_ce_chunked": (_i32, [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _f32, _f32, _vp, _vp, _vp, _vp,
                                       _vp, _vp, _sz, _vp]),
+    "foak_logprobs_workspace_size": (_sz, []),
+    "foak_logprobs_forward": (_i32, [_vp, _i32, _i64, _vp, _i64, _i64, _i64, _f32, _i64, _vp, _vp, _vp, _vp, _vp, _vp,
+                                     _vp, _vp, _sz, _vp]),
+    "foak_logprobs_backward": (_i32, [_vp, _vp, _i32, _i64, _vp, _i64, _i64, _i64, _f32, _vp, _vp, _vp, _vp, _vp,
+                                      _vp]),
+    "foak_distill_forward": (_i32, [_vp, _i32, _i64, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _i32, _f32, _f32,
+                                    _f32, _f32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "foak_distill_fwd_bwd": (_i32, [_vp, _vp, _i32, _i64, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _i32, _f32,
+                                    _f32, _f32, _f32, _f32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "foak_distill_backward": (_i32, [_vp, _vp, _i32, _i64, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _i32, _f32,
+                                     _f32, _f32, _vp, _vp, _f32, _vp, _vp]),
     "foak_test_fail_next_launches": (None, [_i32]),
     "foak_test_set_wait_limit_ns": (None, [ctypes.c_uint64]),
     "foak_test_skip_row_load": (None, [_i64]),
@@ -590,3 +601,197 @@ def foak_rope_apply_qk(q, k, positions, cache, *, inverse: bool = False, stream=
                                 cache.max_pos, 1 if inverse else 0, _ptr(err), _stream(q.device, stream))
     _check(st, "foak_rope_apply_qk")
     return err
+
+
+# --------------------------------------------------------------------- log probabilities
+FOAK_LOGPROBS_MAX_K = 256
+
+
+def _labels_or_none(labels, N, device):
+    return None if labels is None else _labels_arg(labels, N, device)
+
+
+def _row_vector(t, n, device, name):
+    if t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous float32 tensor of {n} elements on the logits' device")
+    return t
+
+
+def _dlogits_arg(dlogits, logits, N, V, ld):
+    """``dlogits``, or a new tensor of the logits' strides and offset modulo 16 bytes."""
+    if dlogits is None:
+        shift = (logits.data_ptr() % 16) // logits.element_size()
+        n = ((N - 1) * ld + V + shift) if N > 0 else 1
+        base = torch.empty(n, dtype=logits.dtype, device=logits.device)
+        return base.as_strided((N, V), (ld, 1), storage_offset=shift)
+    if dlogits.shape != logits.shape or dlogits.stride() != logits.stride() or dlogits.dtype != logits.dtype:
+        raise ValueError("dlogits must match logits in shape, strides and dtype")
+    if dlogits.device != logits.device:
+        raise ValueError("dlogits must live on the logits' device")
+    return dlogits
+
+
+def foak_logprobs_forward(logits, labels=None, *, top_k: int = 0, temperature: float = 1.0, ignore_index: int = -100,
+                          want_entropy: bool = True, want_lse: bool = True, want_stats: bool = True,
+                          workspace_tensor=None, stream=None):
+    """Log probability of each row's token, entropy, log-sum-exp and the top_k most likely tokens.
+
+    ``labels`` (int64 [N]) are the given tokens; None computes every row and leaves logp out.
+    Returns dict(logp, entropy, lse, stats, top_logprobs, top_ids, err): float32 [N] each,
+    stats [N, 2] for :func:`foak_logprobs_backward`, the tops [N, top_k] (ids int32, in
+    descending order, equal logits by the lower id); what was not asked for is None.  Rows
+    whose label is ``ignore_index`` are not read: 0, and top ids -1.
+    """
+    N, V, ld, dt = _logits_args(logits)
+    dev = logits.device
+    labels = _labels_or_none(labels, N, dev)
+    K = int(top_k)
+    if K < 0 or K > min(V, FOAK_LOGPROBS_MAX_K):
+        raise ValueError(f"top_k must be between 0 and min(V, {FOAK_LOGPROBS_MAX_K})")
+    f32 = torch.float32
+    logp = torch.empty(N, dtype=f32, device=dev) if labels is not None else None
+    entropy = torch.empty(N, dtype=f32, device=dev) if want_entropy else None
+    lse = torch.empty(N, dtype=f32, device=dev) if want_lse else None
+    stats = torch.empty(N, 2, dtype=f32, device=dev) if want_stats else None
+    top_lp = torch.empty(N, K, dtype=f32, device=dev) if K else None
+    top_ids = torch.empty(N, K, dtype=torch.int32, device=dev) if K else None
+    err = torch.empty(1, dtype=torch.int32, device=dev)
+    ws = workspace(0, dev) if workspace_tensor is None else workspace_tensor
+    st = lib.foak_logprobs_forward(_ptr(logits), dt, ld, _ptr(labels), N, V, int(ignore_index), float(temperature), K,
+                                   _ptr(logp), _ptr(entropy), _ptr(lse), _ptr(stats), _ptr(top_lp), _ptr(top_ids),
+                                   _ptr(err), _ptr(ws), ws.numel(), _stream(dev, stream))
+    _check(st, "foak_logprobs_forward")
+    return dict(logp=logp, entropy=entropy, lse=lse, stats=stats, top_logprobs=top_lp, top_ids=top_ids, err=err)
+
+
+def foak_logprobs_backward(logits, labels, stats, grad_logp=None, entropy=None, grad_entropy=None, *,
+                           temperature: float = 1.0, ignore_index: int = -100, dlogits=None, stream=None):
+    """Gradient of sum(grad_logp * logp + grad_entropy * entropy); returns (dlogits, err).
+
+    ``stats`` and ``entropy`` come from :func:`foak_logprobs_forward` at the same temperature;
+    a gradient that is None is zero.  Pass ``dlogits=logits`` to overwrite in place.
+    """
+    N, V, ld, dt = _logits_args(logits)
+    dev = logits.device
+    labels = _labels_arg(labels, N, dev)
+    _row_vector(stats, 2 * N, dev, "stats")
+    for t, name in ((grad_logp, "grad_logp"), (entropy, "entropy"), (grad_entropy, "grad_entropy")):
+        if t is not None:
+            _row_vector(t, N, dev, name)
+    if grad_entropy is not None and entropy is None:
+        raise ValueError("grad_entropy needs the forward's entropy")
+    dlogits = _dlogits_arg(dlogits, logits, N, V, ld)
+    err = torch.empty(1, dtype=torch.int32, device=dev)
+    st = lib.foak_logprobs_backward(_ptr(dlogits), _ptr(logits), dt, ld, _ptr(labels), N, V, int(ignore_index),
+                                    float(temperature), _ptr(stats), _ptr(grad_logp), _ptr(entropy),
+                                    _ptr(grad_entropy), _ptr(err), _stream(dev, stream))
+    _check(st, "foak_logprobs_backward")
+    return dlogits, err
+
+
+# --------------------------------------------------------------------- distillation
+FOAK_DISTILL_MAX_K = 256
+
+
+def _teacher_args(ids, logprobs, N, device):
+    if ids.dim() != 2 or ids.dtype != torch.int32 or logprobs.dim() != 2 or logprobs.dtype != torch.float32:
+        raise ValueError("teacher_ids must be int32 and teacher_logprobs float32, both N x K")
+    if ids.shape != logprobs.shape or ids.shape[0] != N:
+        raise ValueError("teacher_ids, teacher_logprobs and the logits disagree on the rows or K")
+    if ids.device != device or logprobs.device != device:
+        raise ValueError("the teacher's tensors must live on the logits' device")
+    K = ids.shape[1]
+    if K < 1 or K > FOAK_DISTILL_MAX_K:
+        raise ValueError(f"K must be between 1 and {FOAK_DISTILL_MAX_K}")
+    if K > 1 and (ids.stride(1) != 1 or logprobs.stride(1) != 1):
+        raise ValueError("the teacher's rows must have unit column stride")
+    if N > 1 and ids.stride(0) != logprobs.stride(0):
+        raise ValueError("teacher_ids and teacher_logprobs must have the same row stride")
+    return K, (ids.stride(0) if N > 1 else K)
+
+
+def foak_distill_forward(logits, labels, teacher_ids, teacher_logprobs, *, ce_weight: float = 0.0,
+                         kd_weight: float = 1.0, temperature: float = 1.0, normalize: bool = True,
+                         ignore_index: int = -100, denom: float = 0.0, want_rows: bool = False,
+                         want_stats: bool = True, workspace_tensor=None, stream=None):
+    """Mean over valid rows of ce_weight CE + kd_weight KD against the teacher's top tokens.
+
+    ``teacher_ids`` (int32 [N, K], negative: padding) and ``teacher_logprobs`` (float32 [N, K])
+    are the top_ids and top_logprobs of :func:`foak_logprobs_forward` at ``temperature``, or
+    rows of the same row stride; ``normalize`` rescales each row's K probabilities to sum 1.
+    ``labels`` may be None (every row counts) when ``ce_weight`` is 0.  Returns dict(loss,
+    row_ce, row_kd, stats, n_valid, err); stats is for :func:`foak_distill_backward`.
+    """
+    N, V, ld, dt = _logits_args(logits)
+    dev = logits.device
+    labels = _labels_or_none(labels, N, dev)
+    K, ldt = _teacher_args(teacher_ids, teacher_logprobs, N, dev)
+    f32 = torch.float32
+    loss = torch.empty(1, dtype=f32, device=dev)
+    row_ce = torch.empty(N, dtype=f32, device=dev) if want_rows else None
+    row_kd = torch.empty(N, dtype=f32, device=dev) if want_rows else None
+    stats = torch.empty(N, 4, dtype=f32, device=dev) if want_stats else None
+    n_valid = torch.empty(1, dtype=torch.int32, device=dev)
+    err = torch.empty(1, dtype=torch.int32, device=dev)
+    ws = workspace(N, dev) if workspace_tensor is None else workspace_tensor
+    st = lib.foak_distill_forward(_ptr(logits), dt, ld, _ptr(labels), N, V, int(ignore_index), _ptr(teacher_ids),
+                                  _ptr(teacher_logprobs), ldt, K, int(bool(normalize)), float(ce_weight),
+                                  float(kd_weight), float(temperature), float(denom), _ptr(loss), _ptr(row_ce),
+                                  _ptr(row_kd), _ptr(stats), _ptr(n_valid), _ptr(err), _ptr(ws), ws.numel(),
+                                  _stream(dev, stream))
+    _check(st, "foak_distill_forward")
+    return dict(loss=loss, row_ce=row_ce, row_kd=row_kd, stats=stats, n_valid=n_valid, err=err)
+
+
+def foak_distill_fwd_bwd(logits, labels, teacher_ids, teacher_logprobs, *, ce_weight: float = 0.0,
+                         kd_weight: float = 1.0, temperature: float = 1.0, normalize: bool = True, g: float = 1.0,
+                         ignore_index: int = -100, denom: float = 0.0, dlogits=None, want_rows: bool = False,
+                         workspace_tensor=None, stream=None):
+    """:func:`foak_distill_forward` and its gradient times ``g`` in one call.
+
+    The gradient overwrites ``logits``, or goes to ``dlogits`` (same strides) if given.
+    Returns dict(loss, dlogits, row_ce, row_kd, n_valid, err).
+    """
+    N, V, ld, dt = _logits_args(logits)
+    dev = logits.device
+    labels = _labels_or_none(labels, N, dev)
+    K, ldt = _teacher_args(teacher_ids, teacher_logprobs, N, dev)
+    dlogits = logits if dlogits is None else _dlogits_arg(dlogits, logits, N, V, ld)
+    f32 = torch.float32
+    loss = torch.empty(1, dtype=f32, device=dev)
+    row_ce = torch.empty(N, dtype=f32, device=dev) if want_rows else None
+    row_kd = torch.empty(N, dtype=f32, device=dev) if want_rows else None
+    n_valid = torch.empty(1, dtype=torch.int32, device=dev)
+    err = torch.empty(1, dtype=torch.int32, device=dev)
+    ws = workspace(N, dev) if workspace_tensor is None else workspace_tensor
+    st = lib.foak_distill_fwd_bwd(_ptr(logits), _ptr(dlogits), dt, ld, _ptr(labels), N, V, int(ignore_index),
+                                  _ptr(teacher_ids), _ptr(teacher_logprobs), ldt, K, int(bool(normalize)),
+                                  float(ce_weight), float(kd_weight), float(temperature), float(g), float(denom),
+                                  _ptr(loss), _ptr(row_ce), _ptr(row_kd), _ptr(n_valid), _ptr(err), _ptr(ws),
+                                  ws.numel(), _stream(dev, stream))
+    _check(st, "foak_distill_fwd_bwd")
+    return dict(loss=loss, dlogits=dlogits, row_ce=row_ce, row_kd=row_kd, n_valid=n_valid, err=err)
+
+
+def foak_distill_backward(logits, labels, teacher_ids, teacher_logprobs, stats, grad_out=None, *,
+                          ce_weight: float = 0.0, kd_weight: float = 1.0, temperature: float = 1.0,
+                          normalize: bool = True, ignore_index: int = -100, denom: float = 0.0, dlogits=None,
+                          stream=None):
+    """The gradient of :func:`foak_distill_forward` from its ``stats``, times ``grad_out`` (a
+    float32 scalar tensor, or None for 1); the other arguments as given there.  Returns
+    (dlogits, err).  Pass ``dlogits=logits`` to overwrite in place."""
+    N, V, ld, dt = _logits_args(logits)
+    dev = logits.device
+    labels = _labels_or_none(labels, N, dev)
+    K, ldt = _teacher_args(teacher_ids, teacher_logprobs, N, dev)
+    _row_vector(stats, 4 * N, dev, "stats")
+    if grad_out is not None and (grad_out.dtype != torch.float32 or grad_out.numel() != 1 or grad_out.device != dev):
+        raise ValueError("grad_out must be a float32 scalar tensor on the logits' device")
+    dlogits = _dlogits_arg(dlogits, logits, N, V, ld)
+    err = torch.empty(1, dtype=torch.int32, device=dev)
+    st = lib.foak_distill_backward(_ptr(dlogits), _ptr(logits), dt, ld, _ptr(labels), N, V, int(ignore_index),
+                                   _ptr(teacher_ids), _ptr(teacher_logprobs), ldt, K, int(bool(normalize)),
+                                   float(ce_weight), float(kd_weight), float(temperature), _ptr(stats),
+                                   _ptr(grad_out), float(denom), _ptr(err), _stream(dev, stream))
+    _check(st, "foak_distill_backward")
+    return dlogits, err

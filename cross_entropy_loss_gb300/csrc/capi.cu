@@ -3,6 +3,7 @@
 // include/foak_ce.h.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <map>
 #include <cstdlib>
 #include <cstring>
@@ -204,6 +205,58 @@ NormLinWs norm_lin_layout(void* base, int64_t N, int64_t V, int64_t D, int64_t c
     off += rmsnorm_workspace_bytes(D);
     w.bytes = off;
     return w;
+}
+
+// ---- log probabilities and distillation
+bool temperature_ok(float t) { return t >= 1e-6f && t <= 1e6f; }  // also refuses NaN
+
+// dlogits shares the logits' row geometry: the same offset modulo 16 bytes
+bool same_geometry(const void* dlogits, const void* logits, int es) {
+    return aligned(dlogits, static_cast<size_t>(es)) &&
+           (reinterpret_cast<uintptr_t>(dlogits) & 15u) == (reinterpret_cast<uintptr_t>(logits) & 15u);
+}
+
+// Checks common to the distillation calls (labels may be null when ce_weight is 0).
+foak_status check_distill(const void* logits, int32_t dtype, int64_t ld, const int64_t* labels, int64_t N, int64_t V,
+                          const int32_t* ids, const float* logp, int64_t ld_teacher, int64_t K, float ce_weight,
+                          float kd_weight, float temperature, int* es) {
+    static const int64_t no_labels = 0;
+    const foak_status st = check_rows(logits, dtype, ld, labels ? labels : &no_labels, N, V, es);
+    if (st != FOAK_OK) return st;
+    if (!std::isfinite(ce_weight) || !std::isfinite(kd_weight) || !temperature_ok(temperature))
+        return FOAK_ERR_INVALID_ARG;
+    if (K < 1 || ld_teacher < K) return FOAK_ERR_INVALID_ARG;
+    if (K > FOAK_DISTILL_MAX_K) return FOAK_ERR_UNSUPPORTED;
+    if (N > 0 && !labels && ce_weight != 0.f) return FOAK_ERR_INVALID_ARG;
+    if (N > 0 && (!ids || !logp)) return FOAK_ERR_INVALID_ARG;
+    if ((ids && !aligned(ids, 4)) || (logp && !aligned(logp, 4))) return FOAK_ERR_INVALID_ARG;
+    return FOAK_OK;
+}
+
+foak_status distill_rows(bool grad, const void* logits, void* dlogits, int32_t dtype, int64_t ld, const int64_t* labels,
+                         int64_t N, int64_t V, int64_t ignore_index, const int32_t* ids, const float* logp,
+                         int64_t ld_teacher, int64_t K, int32_t normalize, float ce_weight, float kd_weight,
+                         float temperature, float g, float denom, float* loss, float* row_ce, float* row_kd,
+                         float* stats, int32_t* n_valid, int32_t* err, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+    int es = 0;
+    const foak_status st = check_distill(logits, dtype, ld, labels, N, V, ids, logp, ld_teacher, K, ce_weight,
+                                         kd_weight, temperature, &es);
+    if (st != FOAK_OK) return st;
+    if (!loss || !aligned(loss, 4) || (row_ce && !aligned(row_ce, 4)) || (row_kd && !aligned(row_kd, 4)) ||
+        (stats && !aligned(stats, 16)) || (n_valid && !aligned(n_valid, 4)) || (err && !aligned(err, 4)))
+        return FOAK_ERR_INVALID_ARG;
+    if (grad && N > 0 && (!dlogits || !same_geometry(dlogits, logits, es))) return FOAK_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, kCeWsAlign) || workspace_bytes < ce_workspace_bytes(N))
+        return FOAK_ERR_WORKSPACE;
+    if (take_injected_failure()) return FOAK_ERR_CUDA;
+    CeWsHeader* ws = static_cast<CeWsHeader*>(workspace);
+    float* rl = reinterpret_cast<float*>(static_cast<char*>(workspace) + sizeof(CeWsHeader));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return finish(launch_distill(grad, es, logits, dlogits, ld, labels, N, V, ignore_index, ids, logp, ld_teacher,
+                                 static_cast<int>(K), normalize != 0, ce_weight, kd_weight, temperature, g, denom, loss,
+                                 rl, row_ce, row_kd, stats, n_valid, err, ws, s),
+                  err, s);
 }
 
 // Argument checks of one product (foak_gemm_bf16 / foak_gemm_bf16_group).
@@ -488,6 +541,98 @@ foak_status foak_rope_apply_qk(void* Q, int64_t Hq, int64_t ldq, void* K, int64_
                               static_cast<int>(Hk), ldk, static_cast<int>(d), positions, cache, max_pos, inverse != 0,
                               err, s);
     return finish(e, err, s);
+}
+
+size_t foak_logprobs_workspace_size(void) { return ce_workspace_bytes(0); }
+
+foak_status foak_logprobs_forward(const void* logits, int32_t dtype, int64_t ld, const int64_t* labels, int64_t N,
+                                  int64_t V, int64_t ignore_index, float temperature, int64_t top_k, float* logp,
+                                  float* entropy, float* lse, float* stats, float* top_logprobs, int32_t* top_ids,
+                                  int32_t* err, void* workspace, size_t workspace_bytes, void* stream) {
+    static const int64_t no_labels = 0;
+    int es = 0;
+    const foak_status st = check_rows(logits, dtype, ld, labels ? labels : &no_labels, N, V, &es);
+    if (st != FOAK_OK) return st;
+    if (!temperature_ok(temperature) || top_k < 0 || top_k > V) return FOAK_ERR_INVALID_ARG;
+    if (top_k > FOAK_LOGPROBS_MAX_K || (top_k > 0 && V > kTopKMaxVocab)) return FOAK_ERR_UNSUPPORTED;
+    if (N > 0 && logp && !labels) return FOAK_ERR_INVALID_ARG;
+    if (N > 0 && top_k > 0 && (!top_logprobs || !top_ids)) return FOAK_ERR_INVALID_ARG;
+    if ((logp && !aligned(logp, 4)) || (entropy && !aligned(entropy, 4)) || (lse && !aligned(lse, 4)) ||
+        (stats && !aligned(stats, 8)) || (top_logprobs && !aligned(top_logprobs, 4)) ||
+        (top_ids && !aligned(top_ids, 4)) || (err && !aligned(err, 4)))
+        return FOAK_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, kCeWsAlign) || workspace_bytes < ce_workspace_bytes(0))
+        return FOAK_ERR_WORKSPACE;
+    if (take_injected_failure()) return FOAK_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return finish(launch_logprobs(es, logits, ld, labels, N, V, ignore_index, temperature, static_cast<int>(top_k), logp,
+                                  entropy, lse, stats, top_logprobs, top_ids, err, static_cast<CeWsHeader*>(workspace),
+                                  s),
+                  err, s);
+}
+
+foak_status foak_logprobs_backward(void* dlogits, const void* logits, int32_t dtype, int64_t ld, const int64_t* labels,
+                                   int64_t N, int64_t V, int64_t ignore_index, float temperature, const float* stats,
+                                   const float* grad_logp, const float* entropy, const float* grad_entropy,
+                                   int32_t* err, void* stream) {
+    int es = 0;
+    const foak_status st = check_rows(logits, dtype, ld, labels, N, V, &es);
+    if (st != FOAK_OK) return st;
+    if (!temperature_ok(temperature)) return FOAK_ERR_INVALID_ARG;
+    if (N > 0 && (!dlogits || !stats || !same_geometry(dlogits, logits, es))) return FOAK_ERR_INVALID_ARG;
+    if (grad_entropy && !entropy) return FOAK_ERR_INVALID_ARG;
+    if ((stats && !aligned(stats, 8)) || (grad_logp && !aligned(grad_logp, 4)) || (entropy && !aligned(entropy, 4)) ||
+        (grad_entropy && !aligned(grad_entropy, 4)) || (err && !aligned(err, 4)))
+        return FOAK_ERR_INVALID_ARG;
+    if (take_injected_failure()) return FOAK_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (N == 0) return finish(err ? cudaMemsetAsync(err, 0, sizeof(int32_t), s) : cudaSuccess, err, s);
+    return finish(launch_logprobs_grad(es, logits, dlogits, ld, labels, N, V, ignore_index, temperature, stats,
+                                       grad_logp, entropy, grad_entropy, err, s),
+                  err, s);
+}
+
+foak_status foak_distill_forward(const void* logits, int32_t dtype, int64_t ld, const int64_t* labels, int64_t N,
+                                 int64_t V, int64_t ignore_index, const int32_t* teacher_ids,
+                                 const float* teacher_logprobs, int64_t ld_teacher, int64_t K, int32_t normalize,
+                                 float ce_weight, float kd_weight, float temperature, float denom, float* loss,
+                                 float* row_ce, float* row_kd, float* stats, int32_t* n_valid, int32_t* err,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+    return distill_rows(false, logits, nullptr, dtype, ld, labels, N, V, ignore_index, teacher_ids, teacher_logprobs,
+                        ld_teacher, K, normalize, ce_weight, kd_weight, temperature, 1.f, denom, loss, row_ce, row_kd,
+                        stats, n_valid, err, workspace, workspace_bytes, stream);
+}
+
+foak_status foak_distill_fwd_bwd(const void* logits, void* dlogits, int32_t dtype, int64_t ld, const int64_t* labels,
+                                 int64_t N, int64_t V, int64_t ignore_index, const int32_t* teacher_ids,
+                                 const float* teacher_logprobs, int64_t ld_teacher, int64_t K, int32_t normalize,
+                                 float ce_weight, float kd_weight, float temperature, float g, float denom,
+                                 float* loss, float* row_ce, float* row_kd, int32_t* n_valid, int32_t* err,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+    return distill_rows(true, logits, dlogits, dtype, ld, labels, N, V, ignore_index, teacher_ids, teacher_logprobs,
+                        ld_teacher, K, normalize, ce_weight, kd_weight, temperature, g, denom, loss, row_ce, row_kd,
+                        nullptr, n_valid, err, workspace, workspace_bytes, stream);
+}
+
+foak_status foak_distill_backward(void* dlogits, const void* logits, int32_t dtype, int64_t ld, const int64_t* labels,
+                                  int64_t N, int64_t V, int64_t ignore_index, const int32_t* teacher_ids,
+                                  const float* teacher_logprobs, int64_t ld_teacher, int64_t K, int32_t normalize,
+                                  float ce_weight, float kd_weight, float temperature, const float* stats,
+                                  const float* grad_out, float denom, int32_t* err, void* stream) {
+    int es = 0;
+    const foak_status st = check_distill(logits, dtype, ld, labels, N, V, teacher_ids, teacher_logprobs, ld_teacher, K,
+                                         ce_weight, kd_weight, temperature, &es);
+    if (st != FOAK_OK) return st;
+    if (N > 0 && (!dlogits || !stats || !same_geometry(dlogits, logits, es))) return FOAK_ERR_INVALID_ARG;
+    if ((stats && !aligned(stats, 16)) || (grad_out && !aligned(grad_out, 4)) || (err && !aligned(err, 4)))
+        return FOAK_ERR_INVALID_ARG;
+    if (take_injected_failure()) return FOAK_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (N == 0) return finish(err ? cudaMemsetAsync(err, 0, sizeof(int32_t), s) : cudaSuccess, err, s);
+    return finish(launch_distill_grad(es, logits, dlogits, ld, labels, N, V, ignore_index, teacher_ids,
+                                      teacher_logprobs, ld_teacher, static_cast<int>(K), normalize != 0, ce_weight,
+                                      kd_weight, temperature, stats, grad_out, denom, err, s),
+                  err, s);
 }
 
 foak_status foak_gemm_bf16_group(const foak_gemm_problem* problems, int32_t n, int32_t* err, void* stream) {

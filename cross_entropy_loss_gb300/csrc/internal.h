@@ -111,6 +111,32 @@ cudaError_t launch_rope_apply(int es, void* X, int64_t T, int H, int64_t ldt, vo
                               const int64_t* positions, const void* cache, int64_t max_pos, bool inverse,
                               int32_t* err, cudaStream_t s);
 
+// Log probability of the given token, entropy and top tokens of every row (logprobs.cu).
+// Any output may be null; top_lp and top_ids are [N][top_k].  Takes the workspace header alone.
+constexpr int kTopKMax = 256;
+constexpr int64_t kTopKMaxVocab = 262144;  // the block maxima of a row are kept in shared memory
+cudaError_t launch_logprobs(int es, const void* x, int64_t ld, const int64_t* labels, int64_t N, int64_t V,
+                            int64_t ignore_index, float temperature, int top_k, float* logp, float* entropy, float* lse,
+                            float* stats, float* top_lp, int32_t* top_ids, int32_t* err, CeWsHeader* ws,
+                            cudaStream_t stream);
+// Distillation from a teacher's top tokens (distill.cu); grad: fused with the gradient
+// into dx.  row_loss must be non-null (caller buffer or the workspace's row area).
+cudaError_t launch_distill(bool grad, int es, const void* x, void* dx, int64_t ld, const int64_t* labels, int64_t N,
+                           int64_t V, int64_t ignore_index, const int32_t* ids, const float* logp, int64_t ld_teacher,
+                           int K, bool normalize, float ce_w, float kd_w, float temperature, float g, float denom,
+                           float* loss, float* row_loss, float* row_ce, float* row_kd, float* stats, int32_t* n_valid,
+                           int32_t* err, CeWsHeader* ws, cudaStream_t stream);
+// Their backward passes from saved row statistics (rows_grad.cu).
+cudaError_t launch_logprobs_grad(int es, const void* x, void* dx, int64_t ld, const int64_t* labels, int64_t N,
+                                 int64_t V, int64_t ignore_index, float temperature, const float* stats,
+                                 const float* grad_logp, const float* entropy, const float* grad_entropy, int32_t* err,
+                                 cudaStream_t stream);
+cudaError_t launch_distill_grad(int es, const void* x, void* dx, int64_t ld, const int64_t* labels, int64_t N,
+                                int64_t V, int64_t ignore_index, const int32_t* ids, const float* logp,
+                                int64_t ld_teacher, int K, bool normalize, float ce_w, float kd_w, float temperature,
+                                const float* stats, const float* grad_out, float denom, int32_t* err,
+                                cudaStream_t stream);
+
 uint64_t test_wait_limit_ns();
 int64_t test_skip_load_row();
 int32_t test_row_path();  // 0 automatic, 1 one pass (CTA / clusters), 2 two-pass streaming, 3 independent warps

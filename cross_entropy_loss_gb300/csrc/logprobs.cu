@@ -1,0 +1,508 @@
+// Log probability of a given token, entropy and the K most likely tokens of every row
+// of logits -- what a server answering with log probabilities, a policy-gradient step
+// or a teacher writing down its distribution takes from the LM head.  With z = x / T:
+//
+//   m = max_j x_j     S = sum_j e^{(x_j - m) / T}     A = sum_j e^{(x_j - m) / T} (x_j - m) / T
+//   lse = m / T + ln S     logp_j = (x_j - m) / T - ln S     H = ln S - A / S
+//
+// One read of the row gives m, S and A (running sums per thread, rescaled at a new
+// maximum).  The top K come out of the same read: a thread's 64-byte block of a chunk
+// has one maximum, which the sums need anyway and which is kept as an ordered integer
+// key.  Blocks are contiguous, so the K largest blocks by (maximum, lower index first)
+// hold the K largest elements by (value, lower index first): with a total order an
+// element outside those blocks has K larger ones before it.  So a row's end is
+//
+//   1. a threshold on the block maxima with at least K and at most 256 blocks at or
+//      above it (bisection on the keys, a count over the CTA each step; ties beyond 256
+//      blocks are cut by a second bisection on the block index);
+//   2. one block a thread, re-read (from L2: the row just went through), and its elements
+//      at or above the threshold put on a list;
+//   3. each listed element's rank = the number of larger ones, its place in the output.
+//
+// Rows go to CTAs round-robin; when there are fewer rows than SMs a cluster shares each
+// row, joins its sums and lists through distributed shared memory, and ranks every
+// CTA's K candidates against the others'.
+#include <algorithm>
+#include <map>
+#include <mutex>
+
+#include "row_stream.cuh"
+
+namespace foak {
+
+namespace {
+
+constexpr int kListCap = 1024;  // listed elements of a row (or of a CTA's share of it)
+
+struct LogprobParams {
+    StreamSrc src;
+    float inv_t;       // 1 / T
+    float c;           // log2(e) / T
+    int top_k;
+    float* logp;       // [N] or null
+    float* entropy;    // [N] or null
+    float* lse;        // [N] or null
+    float2* stats;     // [N] or null: (m, ln S)
+    float* top_lp;     // [N][top_k]
+    int32_t* top_ids;  // [N][top_k]
+    int32_t* err;
+    CeWsHeader* ws;
+};
+
+// Unsigned integers in the order of the floats; -0 and +0 are the same key, 0 is no float's key.
+__device__ __forceinline__ uint32_t key_of(float f) {
+    const uint32_t b = __float_as_uint(f == 0.f ? 0.f : f);
+    return b ^ (b >> 31 ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float float_of_key(uint32_t k) {
+    return __uint_as_float(k ^ (k >> 31 ? 0x80000000u : 0xffffffffu));
+}
+// Block maxima are kept as the key's upper half for bf16 (whose lower half is constant) and whole for fp32.
+template <int ES>
+struct BlockKey {
+    using type = uint32_t;
+    static __device__ __forceinline__ uint32_t of(float f) { return key_of(f); }
+    static __device__ __forceinline__ uint32_t element(uint32_t k) { return k; }  // the smallest element key
+};
+template <>
+struct BlockKey<2> {
+    using type = uint16_t;
+    static __device__ __forceinline__ uint32_t of(float f) { return key_of(f) >> 16; }
+    static __device__ __forceinline__ uint32_t element(uint32_t k) { return k << 16; }
+};
+
+struct TopScratch {
+    int count[2][kStreamWarps];        // partial counts, by the parity of the count
+    float warp_min[kStreamWarps];      // least thread maximum of each warp
+    int n_sel, n_list;
+    int sel[kStreamThreads];           // the chosen blocks
+    unsigned long long list[kListCap]; // (key << 32) | ~column
+    unsigned long long best[kStreamThreads];  // this CTA's top K in order (clusters)
+};
+
+// The sum of n over the consumer threads; one consumer barrier.
+__device__ __forceinline__ int consumers_count(int n, TopScratch& t, uint32_t& turn) {
+    n = __reduce_add_sync(0xffffffffu, n);
+    const uint32_t b = turn++ & 1u;
+    if ((threadIdx.x & 31) == 0) t.count[b][threadIdx.x >> 5] = n;
+    consumers_sync();
+    int s = 0;
+#pragma unroll
+    for (int w = 0; w < kStreamWarps; ++w) s += t.count[b][w];
+    return s;
+}
+
+// Block `id` of the slice: 0 the head scalars, 1 .. nblk the body's blocks, nblk + 1 the tail scalars.
+template <int ES>
+struct BlockElements {
+    static constexpr int EPV = 16 / ES;
+    static constexpr int N = kBlockVec * EPV;
+    uint32_t w[kBlockVec * 4];  // the elements as they lie in memory
+    int n;
+    int64_t col;
+
+    __device__ __forceinline__ void load(const Slice& s, int id, int nblk) {
+#pragma unroll
+        for (int i = 0; i < kBlockVec * 4; ++i) w[i] = 0;
+        if (id > 0 && id <= nblk) {
+            const int v0 = (id - 1) * kBlockVec;
+            const int nv = min(kBlockVec, s.nv - v0);
+            col = s.col0 + static_cast<int64_t>(v0) * EPV;
+            n = nv * EPV;
+            const uint4* v = reinterpret_cast<const uint4*>(s.body) + v0;
+#pragma unroll
+            for (int i = 0; i < kBlockVec; ++i) {
+                if (i < nv) {
+                    const uint4 q = ld_global_v4(v + i);
+                    w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
+                }
+            }
+            return;
+        }
+        col = id ? s.tail_col : 0;
+        n = id ? s.t : s.h;
+#pragma unroll
+        for (int e = 0; e < kMaxScalars; ++e) {
+            if (e >= n) continue;
+            if constexpr (ES == 2)
+                w[e / 2] |= static_cast<uint32_t>(*reinterpret_cast<const unsigned short*>(s.rowp + (col + e) * 2)) << (e & 1) * 16;
+            else w[e] = *reinterpret_cast<const uint32_t*>(s.rowp + (col + e) * 4);
+        }
+    }
+    // element e as (key << 32) | ~column, 0 where there is none
+    __device__ __forceinline__ unsigned long long item(int e) const {
+        float f;
+        if constexpr (ES == 2) f = e & 1 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
+        else f = __uint_as_float(w[e]);
+        return e < n ? (static_cast<unsigned long long>(key_of(f)) << 32) | static_cast<uint32_t>(~static_cast<uint32_t>(col + e))
+                     : 0ull;
+    }
+};
+
+// This CTA's largest elements of its slice onto t.list: at least the min(K, all) largest
+// ones, at most kListCap.  Returns how many.  keys[1 .. nblk] are the block maxima, least
+// the maximum of the thread's own blocks, cta_max the slice's (-FLT_MAX at the least).
+template <int ES>
+__device__ __forceinline__ int top_list(const Slice& s, typename BlockKey<ES>::type* keys, int K, float least,
+                                        float cta_max, TopScratch& t) {
+    using BK = BlockKey<ES>;
+    const int tid = threadIdx.x;
+    const int nblk = (s.nv + kBlockVec - 1) / kBlockVec;
+    const int nreal = nblk + (s.h > 0) + (s.t > 0);
+    uint32_t turn = 0;
+    // the head's and tail's maxima; also the least thread maximum of the CTA
+    if (tid == 0 || tid == 32) {
+        const int n = tid == 0 ? s.h : s.t;
+        const char* at = s.rowp + (tid == 0 ? 0 : s.tail_col * ES);
+        float m = kNegInf;
+        for (int e = 0; e < n; ++e) m = fmaxf(m, load_scalar<ES>(at + e * ES));
+        keys[tid == 0 ? 0 : nblk + 1] = n > 0 ? BK::of(m) : 0;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) least = fminf(least, __shfl_xor_sync(0xffffffffu, least, off));
+    if ((tid & 31) == 0) t.warp_min[tid >> 5] = least;
+    if (tid == 0) {
+        t.n_sel = 0;
+        t.n_list = 0;
+    }
+    consumers_sync();
+
+    // ---- 1. the blocks: keys >= lo, and of those equal to lo only the ids up to last
+    uint32_t lo = 1;
+    int last = 0x7fffffff;
+    if (nreal > K) {
+        const int most = min(kStreamThreads, K + K / 2 + 24);
+        auto at_least = [&](uint32_t k) {
+            int n = 0;
+            for (int b = tid; b < nblk + 2; b += kStreamThreads) n += keys[b] >= k;
+            return consumers_count(n, t, turn);
+        };
+        uint32_t hi = BK::of(cta_max) + 1;
+        int c_lo = nreal, c_hi = 0;  // blocks at or above lo and hi
+        if (nblk >= kStreamThreads) {  // every thread has seen a block: 256 >= K maxima at or above the least of theirs
+            float l = t.warp_min[0];
+#pragma unroll
+            for (int w = 1; w < kStreamWarps; ++w) l = fminf(l, t.warp_min[w]);
+            const uint32_t k = BK::of(l);
+            if (l > -FLT_MAX && k > lo && k < hi) {  // (-FLT_MAX: perhaps nothing but -inf)
+                lo = k;
+                c_lo = 0x7fffffff;  // at least 256, not counted
+            }
+        }
+        while (hi - lo > 1 && c_lo > most) {
+            const uint32_t mid = lo + (hi - lo) / 2;
+            const int n = at_least(mid);
+            if (n >= K) {
+                lo = mid;
+                c_lo = n;
+            } else {
+                hi = mid;
+                c_hi = n;
+            }
+        }
+        if (c_lo == 0x7fffffff) c_lo = at_least(lo);
+        if (c_lo > kStreamThreads) {  // then hi == lo + 1: ties at lo, the first need of them
+            const int need = K - c_hi;
+            int j0 = -1, j1 = nblk + 1;  // fewer than need ties up to j0, enough up to j1
+            while (j1 - j0 > 1) {
+                const int mid = j0 + (j1 - j0) / 2;
+                int n = 0;
+                for (int b = tid; b <= mid; b += kStreamThreads) n += keys[b] == lo;
+                if (consumers_count(n, t, turn) >= need) j1 = mid;
+                else j0 = mid;
+            }
+            last = j1;
+        }
+    }
+    for (int b = tid; b < nblk + 2; b += kStreamThreads) {
+        const uint32_t k = keys[b];
+        if (k > lo || (k == lo && b <= last)) {
+            const int i = atomicAdd(&t.n_sel, 1);
+            if (i < kStreamThreads) t.sel[i] = b;
+        }
+    }
+    consumers_sync();
+
+    // ---- 2. their elements at or above the threshold
+    const int n_sel = min(t.n_sel, kStreamThreads);
+    BlockElements<ES> el;
+    if (tid < n_sel) el.load(s, t.sel[tid], nblk);
+    else el.n = 0;
+    unsigned long long floor = static_cast<unsigned long long>(BK::element(lo)) << 32;
+    int mine = 0;
+#pragma unroll
+    for (int e = 0; e < BlockElements<ES>::N; ++e) mine += el.item(e) >= floor;
+    const int total = consumers_count(mine, t, turn);
+    if (total > kListCap) {
+        // Many ties, or few blocks of many elements: bisection for the exact K-th largest item (items are
+        // distinct).  Every count is at least K at b0 and less than K at b1.
+        unsigned long long b0 = floor, b1 = static_cast<unsigned long long>(key_of(cta_max) + 1u) << 32;
+        while (b1 - b0 > 1) {
+            const unsigned long long mid = b0 + (b1 - b0) / 2;
+            int n = 0;
+#pragma unroll
+            for (int e = 0; e < BlockElements<ES>::N; ++e) n += el.item(e) >= mid;
+            const int c = consumers_count(n, t, turn);
+            if (c >= K) {
+                b0 = mid;
+                if (c <= kListCap) break;
+            } else {
+                b1 = mid;
+            }
+        }
+        floor = b0;
+    }
+#pragma unroll
+    for (int e = 0; e < BlockElements<ES>::N; ++e) {
+        const unsigned long long it = el.item(e);
+        if (it >= floor) {
+            const int i = atomicAdd(&t.n_list, 1);
+            if (i < kListCap) t.list[i] = it;
+        }
+    }
+    consumers_sync();
+    return min(t.n_list, kListCap);
+}
+
+template <int ES, bool ENT, bool TOPK>
+__global__ void __launch_bounds__(kStreamBlock, 3) logprobs_kernel(const LogprobParams p) {
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ StreamBars bars;
+    __shared__ StatExchange ex;
+    __shared__ TopScratch top;
+    using KeyT = typename BlockKey<ES>::type;
+    unsigned char* ring = smem;
+    KeyT* keys = reinterpret_cast<KeyT*>(smem + p.src.stages * kStreamStageBytes);
+
+    const int tid = threadIdx.x, k = p.src.k;
+    const int rank = k > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int64_t cid = blockIdx.x / k, ncl = gridDim.x / k;
+    const int64_t n_it = p.src.N > cid ? (p.src.N - 1 - cid) / ncl + 1 : 0;
+    stream_init(bars, p.src.stages);
+    griddep_launch_dependents();  // programmatic dependent launch: no global access before the wait
+    griddep_wait();
+    __syncthreads();
+    if (k > 1) cluster_sync();  // every CTA's shared memory is there to be written to
+
+    bool bad = false, aborted = false;
+    if (tid >= kStreamThreads) {
+        stream_produce<ES>(p.src, bars, ring, 1, cid, ncl, rank, k > 1 ? (TOPK ? 3 : 1) : 0);
+    } else {
+        StreamPos pos{0, 0, false};
+        uint32_t parity = 0;
+        int64_t y_next = p.src.labels && n_it > 0 ? __ldg(p.src.labels + cid) : 0;
+        for (int64_t it = 0; it < n_it; ++it) {
+            const int64_t row = cid + it * ncl;
+            const int64_t y = y_next;
+            if (p.src.labels && it + 1 < n_it) y_next = __ldg(p.src.labels + row + ncl);
+            if (!stream_row_valid(y, p.src)) {
+                bad |= y != p.src.ignore_index;
+                if (rank == 0) {
+                    if (tid == 0) {
+                        if (p.logp) p.logp[row] = 0.f;
+                        if (p.entropy) p.entropy[row] = 0.f;
+                        if (p.lse) p.lse[row] = 0.f;
+                        if (p.stats) p.stats[row] = make_float2(0.f, 0.f);
+                    }
+                    if (TOPK) {
+                        for (int i = tid; i < p.top_k; i += kStreamThreads) {
+                            p.top_lp[row * p.top_k + i] = 0.f;
+                            p.top_ids[row * p.top_k + i] = -1;
+                        }
+                    }
+                }
+                continue;
+            }
+            const Slice s = slice_of<ES>(p.src, row, rank);
+            float x_y = 0.f;
+            if (tid == 0 && rank == 0 && p.logp) x_y = load_scalar<ES>(s.rowp + y * ES);
+            RunStat<ENT, false> st;
+            for (int c0 = 0; c0 < s.nv; c0 += kStreamChunk) {
+                const int nl = min(kStreamChunk, s.nv - c0);
+                uint4 v[kBlockVec];
+                stream_chunk(p.src, bars, ring, pos, [&](const unsigned char* stage) { load_block<ES>(stage, nl, v); });
+                const float bmax = vec_max<ES>(v);
+                if (TOPK && tid * kBlockVec < nl) keys[1 + c0 / kBlockVec + tid] = static_cast<KeyT>(BlockKey<ES>::of(bmax));
+                st.template add_vecs<ES>(v, bmax, p.c, 0.f);
+            }
+            const float least = st.m;  // of the thread's blocks
+            if (tid == 0)
+                for (int e = 0; e < s.h; ++e) st.add(load_scalar<ES>(s.rowp + e * ES), p.c, 0.f);
+            if (tid == 32)
+                for (int e = 0; e < s.t; ++e) st.add(load_scalar<ES>(s.rowp + (s.tail_col + e) * ES), p.c, 0.f);
+            float cta_m;
+            stat_reduce(st, ex, parity, k, rank, p.c, 0.f, &cta_m);
+            parity ^= 1u;
+            const float ln_s = logf(st.s);
+            const bool empty = st.s == 0.f;
+            const float lse = empty ? kNegInf : fmaf(st.m, p.inv_t, ln_s);
+            if (tid == 0 && rank == 0 && !pos.aborted) {
+                if (p.logp) p.logp[row] = empty ? kNegInf : (x_y - st.m) * p.inv_t - ln_s;
+                if (ENT) {
+                    const float h = ln_s - st.a * kLn2 / st.s;
+                    p.entropy[row] = empty || h < 0.f ? 0.f : h;
+                }
+                if (p.lse) p.lse[row] = lse;
+                if (p.stats) p.stats[row] = make_float2(empty ? kNegInf : st.m, ln_s);
+            }
+            if constexpr (TOPK) {
+                const int K = p.top_k;
+                const bool none = !(st.s == st.s);  // a NaN or +inf in the row: no order to speak of
+                int n = 0;
+                if (!none) n = top_list<ES>(s, keys, K, least, cta_m, top);
+                float* olp = p.top_lp + row * K;
+                int32_t* oid = p.top_ids + row * K;
+                auto write = [&](int r, unsigned long long item) {
+                    olp[r] = empty ? kNegInf : (float_of_key(static_cast<uint32_t>(item >> 32)) - st.m) * p.inv_t - ln_s;
+                    oid[r] = static_cast<int32_t>(~static_cast<uint32_t>(item));
+                };
+                // ranks within this CTA's list
+                if (k > 1) {
+                    if (tid < K) top.best[tid] = 0ull;
+                    consumers_sync();
+                }
+                for (int i = tid; i < n; i += kStreamThreads) {
+                    const unsigned long long item = top.list[i];
+                    int r = 0;
+                    for (int j = 0; j < n; ++j) r += top.list[j] > item;
+                    if (r < K) {
+                        if (k > 1) top.best[r] = item;
+                        else if (!pos.aborted) write(r, item);
+                    }
+                }
+                if (k > 1) {
+                    cluster_sync_converged();  // every CTA's best are in place
+                    if (tid < K && !none && top.best[tid] != 0ull) {
+                        const unsigned long long item = top.best[tid];
+                        int r = tid;
+                        for (int o = 0; o < k; ++o) {
+                            if (o == rank) continue;
+                            const uint32_t base = mapa_u32(top.best, static_cast<uint32_t>(o));
+                            int a = 0, b = K;  // entries before a are larger, from b on they are not
+                            while (a < b) {
+                                const int mid = (a + b) / 2;
+                                unsigned long long v;
+                                asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(base + mid * 8) : "memory");
+                                if (v > item) a = mid + 1;
+                                else b = mid;
+                            }
+                            r += a;
+                        }
+                        if (r < K && !pos.aborted) write(r, item);
+                    }
+                    cluster_sync_converged();  // every CTA has read them
+                }
+                if (none && rank == 0) {
+                    for (int i = tid; i < K; i += kStreamThreads) {
+                        olp[i] = st.s;
+                        oid[i] = -1;
+                    }
+                }
+                consumers_sync();  // the keys and lists may be overwritten
+            }
+        }
+        aborted = pos.aborted;
+    }
+    // The error word: every CTA adds its bits; the last one publishes and resets them.
+    __syncthreads();
+    if (tid == 0) {
+        unsigned e = 0;
+        if (aborted || stream_aborted(bars)) e |= FOAK_ERRBIT_TIMEOUT;
+        if (bad) e |= FOAK_ERRBIT_LABEL_RANGE;
+        if (e) atomicOr(&p.ws->err, e);
+        if (atom_add_acq_rel_gpu(&p.ws->done, 1u) == gridDim.x - 1) {
+            e = atomicExch(&p.ws->err, 0u);
+            atomicExch(&p.ws->done, 0u);
+            if (p.err) *p.err = static_cast<int32_t>(e);
+        }
+    }
+    if (k > 1) cluster_sync_converged();  // no CTA leaves while its shared memory may be read
+}
+
+std::mutex g_lp_mu;
+std::map<std::pair<int, const void*>, size_t> g_lp_attr;  // (device, kernel): dynamic shared memory allowed
+
+template <int ES, bool ENT, bool TOPK>
+cudaError_t launch_typed(LogprobParams prm, cudaStream_t stream) {
+    auto* kern = &logprobs_kernel<ES, ENT, TOPK>;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    StreamSrc& s = prm.src;
+    const int sms = device_sm_count();
+    const int64_t nb = s.V * ES / 16 + 1;
+    // Few rows: a cluster per row, as long as its CTAs are all on SMs of their own and
+    // have at least half a chunk each.
+    s.k = kStreamMaxCluster;
+    while (s.k > 1 && (s.N * s.k > sms || 2 * nb < static_cast<int64_t>(s.k) * kStreamChunk)) s.k /= 2;
+    const int64_t nblk = ((nb + kBlockVec - 1) / kBlockVec + s.k - 1) / s.k + 3;
+    const size_t key_bytes = TOPK ? (static_cast<size_t>(nblk) * sizeof(typename BlockKey<ES>::type) + 127) / 128 * 128 : 0;
+    // Three CTAs an SM when each gets a ring of three stages, else two.
+    const size_t fixed = 1024 + sizeof(StreamBars) + sizeof(StatExchange) + sizeof(TopScratch) + 256 + key_bytes;
+    int per_sm = 3;
+    while (per_sm > 1 && (228 * 1024) / per_sm < fixed + 3 * kStreamStageBytes) --per_sm;
+    const size_t room = std::min<size_t>((228 * 1024) / per_sm, 227 * 1024) - fixed;
+    s.stages = static_cast<int>(std::min<size_t>(kStreamMaxStages, room / kStreamStageBytes));
+    if (s.stages < 1) return cudaErrorInvalidValue;
+    const size_t smem = static_cast<size_t>(s.stages) * kStreamStageBytes + key_bytes;
+    {
+        std::lock_guard<std::mutex> lock(g_lp_mu);
+        size_t& set = g_lp_attr[std::make_pair(dev, reinterpret_cast<const void*>(kern))];
+        if (set < smem) {
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+            if (e != cudaSuccess) return e;
+            set = smem;
+        }
+    }
+    const int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(s.N, static_cast<int64_t>(sms) * per_sm / s.k));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters * s.k), 1, 1);
+    cfg.blockDim = dim3(kStreamBlock, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0] = pdl_attribute();
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(s.k);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = s.k > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, prm);
+}
+
+}  // namespace
+
+cudaError_t launch_logprobs(int es, const void* x, int64_t ld, const int64_t* labels, int64_t N, int64_t V,
+                            int64_t ignore_index, float temperature, int top_k, float* logp, float* entropy, float* lse,
+                            float* stats, float* top_lp, int32_t* top_ids, int32_t* err, CeWsHeader* ws,
+                            cudaStream_t stream) {
+    LogprobParams p = {};
+    p.src.x = static_cast<const char*>(x);
+    p.src.ld = ld;
+    p.src.labels = labels;
+    p.src.N = N;
+    p.src.V = V;
+    p.src.ignore_index = ignore_index;
+    p.src.wait_ns = test_wait_limit_ns();
+    p.src.skip_load_row = test_skip_load_row();
+    p.inv_t = 1.f / temperature;
+    p.c = kLog2e / temperature;
+    p.top_k = top_k;
+    p.logp = logp;
+    p.entropy = entropy;
+    p.lse = lse;
+    p.stats = reinterpret_cast<float2*>(stats);
+    p.top_lp = top_lp;
+    p.top_ids = top_ids;
+    p.err = err;
+    p.ws = ws;
+    if (es == 2) {
+        if (top_k > 0) return entropy ? launch_typed<2, true, true>(p, stream) : launch_typed<2, false, true>(p, stream);
+        return entropy ? launch_typed<2, true, false>(p, stream) : launch_typed<2, false, false>(p, stream);
+    }
+    if (top_k > 0) return entropy ? launch_typed<4, true, true>(p, stream) : launch_typed<4, false, true>(p, stream);
+    return entropy ? launch_typed<4, true, false>(p, stream) : launch_typed<4, false, false>(p, stream);
+}
+
+}  // namespace foak

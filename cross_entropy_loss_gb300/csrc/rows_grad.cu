@@ -1,0 +1,323 @@
+// Backward passes from saved row statistics: the gradient of log probabilities and
+// entropies (logprobs.cu), and of the distillation loss (distill.cu).  With the
+// statistics known every element is independent, so this is a stream over (row, 32 KB
+// segment) work items, 256 threads each, eight 16-byte loads in flight per thread
+// before the arithmetic.  Rows that do not count are only written (+0.0).
+//
+//   log probabilities, entropy (d = (x - m) / T - ln S = ln p):
+//     dx_j = ([j = y] - p_j) g_l / T - p_j (d_j + H) g_h / T = p_j (A + B d_j) + [j = y] g_l / T
+//   distillation: a1 e^{x_j - m} + aT e^{(x_j - m) / T}, and the label's and the teacher's
+//     tokens rewritten after a barrier, from logits read before it (the gradient may
+//     replace the logits).
+//
+// The statistics are (m, ln S), not their sum: at |m| past 2^24 ln n the sum has lost
+// ln S, and a row of n equal lowest values would get p = 1 instead of 1 / n.
+#include <algorithm>
+
+#include "common.cuh"
+#include "foak_ce.h"
+#include "internal.h"
+#include "row_stream.cuh"
+#include "teacher.cuh"
+
+namespace foak {
+
+namespace {
+
+constexpr int kGradThreads = 256;
+constexpr int kGradVpt = 8;
+constexpr int kGradSegVec = kGradThreads * kGradVpt;  // 32 KB
+constexpr int kGradBlocksPerSm = 4;
+
+struct RowsGradParams {
+    StreamSrc src;
+    char* dx;
+    int64_t nseg;
+    float inv_t, c;
+    int32_t* err;
+    // log probabilities and entropy
+    const float2* stats2;
+    const float* entropy;
+    const float* grad_logp;     // null: 0
+    const float* grad_entropy;  // null: 0
+    // distillation
+    const float4* stats4;
+    TeacherSrc teacher;
+    const float* g_ptr;  // null: 1
+    float denom, ce_w, kd_w;
+};
+
+// One segment of a row: its vectors, and the row's scalars if they are its.
+struct Segment {
+    int64_t row;
+    const char* rowp;
+    char* drow;
+    int vbeg, vend;   // vectors of the row's body
+    int h;            // the row's head scalars
+    int n_edge;       // head and tail scalars of this segment
+    int64_t col_lo, col_hi, tail_col;
+    bool first;
+};
+
+template <int ES>
+__device__ __forceinline__ Segment segment_of(const RowsGradParams& p, int64_t item) {
+    constexpr int EPV = 16 / ES;
+    Segment s;
+    s.row = item / p.nseg;
+    const int seg = static_cast<int>(item - s.row * p.nseg);
+    s.rowp = p.src.x + s.row * p.src.ld * ES;
+    s.drow = p.dx + s.row * p.src.ld * ES;
+    const RowGeom g = row_geom<ES>(s.rowp, p.src.V);
+    const int nb = static_cast<int>(g.nb);
+    s.first = seg == 0;
+    const bool last = seg == p.nseg - 1;
+    s.vbeg = min(nb, seg * kGradSegVec);
+    s.vend = last ? nb : min(nb, s.vbeg + kGradSegVec);
+    s.h = g.h;
+    s.tail_col = g.h + static_cast<int64_t>(nb) * EPV;
+    s.n_edge = (s.first ? g.h : 0) + (last ? g.t : 0);
+    s.col_lo = s.first ? 0 : g.h + static_cast<int64_t>(s.vbeg) * EPV;
+    s.col_hi = last ? p.src.V : g.h + static_cast<int64_t>(s.vend) * EPV;
+    return s;
+}
+
+__device__ __forceinline__ int64_t edge_column(const Segment& s, int i) {
+    const int h = s.first ? s.h : 0;
+    return i < h ? i : s.tail_col + (i - h);
+}
+
+template <int ES>
+__device__ __forceinline__ void zero_segment(const Segment& s) {
+    uint4* dst = reinterpret_cast<uint4*>(s.drow + static_cast<int64_t>(s.h) * ES);
+    for (int v = s.vbeg + threadIdx.x; v < s.vend; v += kGradThreads) st_global_cs_v4(dst + v, make_uint4(0u, 0u, 0u, 0u));
+    if (static_cast<int>(threadIdx.x) < s.n_edge) store_scalar<ES>(s.drow + edge_column(s, threadIdx.x) * ES, 0.f);
+}
+
+template <int ES>
+__device__ __forceinline__ void load_segment(const Segment& s, uint4 (&v)[kGradVpt], float& edge) {
+    const uint4* src = reinterpret_cast<const uint4*>(s.rowp + static_cast<int64_t>(s.h) * ES);
+#pragma unroll
+    for (int i = 0; i < kGradVpt; ++i) {
+        const int vv = s.vbeg + threadIdx.x + i * kGradThreads;
+        v[i] = RowMath<ES>::pad();
+        if (vv < s.vend) v[i] = ld_global_v4(src + vv);
+    }
+    edge = 0.f;
+    if (static_cast<int>(threadIdx.x) < s.n_edge) edge = load_scalar<ES>(s.rowp + edge_column(s, threadIdx.x) * ES);
+}
+
+// f maps a pair of logits to the pair of their gradients
+template <int ES, typename F>
+__device__ __forceinline__ void store_segment(const Segment& s, const uint4 (&v)[kGradVpt], float edge, F&& f) {
+    uint4* dst = reinterpret_cast<uint4*>(s.drow + static_cast<int64_t>(s.h) * ES);
+#pragma unroll
+    for (int i = 0; i < kGradVpt; ++i) {
+        const int vv = s.vbeg + threadIdx.x + i * kGradThreads;
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < (ES == 2 ? 4 : 2); ++j) {
+            const f32x2_t e = f(vec_pair<ES>(v[i], j));
+            if constexpr (ES == 2) {
+                o[j] = f2_to_bf16x2(e);
+            } else {
+                float lo, hi;
+                f2_unpack(e, lo, hi);
+                o[2 * j] = __float_as_uint(lo);
+                o[2 * j + 1] = __float_as_uint(hi);
+            }
+        }
+        if (vv < s.vend) st_global_cs_v4(dst + vv, make_uint4(o[0], o[1], o[2], o[3]));
+    }
+    if (static_cast<int>(threadIdx.x) < s.n_edge) {
+        float lo, hi;
+        f2_unpack(f(f2_pack(edge, edge)), lo, hi);
+        store_scalar<ES>(s.drow + edge_column(s, threadIdx.x) * ES, lo);
+    }
+}
+
+// 2^x and x with x kept above where 2^x is 0, so that 0 * x is 0; NaN passes
+__device__ __forceinline__ f32x2_t clamp_exponent(f32x2_t x) {
+    float lo, hi;
+    f2_unpack(x, lo, hi);
+    return f2_pack(max_nan(lo, kMinExp2), max_nan(hi, kMinExp2));
+}
+
+template <int ES, bool ENT>
+__global__ void __launch_bounds__(kGradThreads, kGradBlocksPerSm) logprobs_grad_kernel(const RowsGradParams p) {
+    griddep_launch_dependents();  // programmatic dependent launch: no global access before the wait
+    griddep_wait();
+    __shared__ int scratch[2 * (kGradThreads / 32)];
+    if (blockIdx.x == 0 && p.err) {
+        int n_valid, n_bad;
+        count_labels(p.src.labels, p.src.N, p.src.V, p.src.ignore_index, scratch, n_valid, n_bad);
+        if (threadIdx.x == 0) *p.err = n_bad > 0 ? FOAK_ERRBIT_LABEL_RANGE : 0;
+    }
+    const int64_t items = p.src.N * p.nseg;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const Segment s = segment_of<ES>(p, item);
+        const int64_t y = __ldg(p.src.labels + s.row);
+        if (!stream_row_valid(y, p.src)) {
+            zero_segment<ES>(s);
+            continue;
+        }
+        uint4 v[kGradVpt];
+        float edge;
+        load_segment<ES>(s, v, edge);
+        const float2 ms = __ldg(p.stats2 + s.row);
+        const float gl = (p.grad_logp ? __ldg(p.grad_logp + s.row) : 0.f) * p.inv_t;
+        const float gh = ENT ? __ldg(p.grad_entropy + s.row) * p.inv_t : 0.f;
+        const float hrow = ENT ? __ldg(p.entropy + s.row) : 0.f;
+        const bool empty = ms.x == kNegInf;  // nothing but -inf: p = 0
+        const float m = empty ? 0.f : ms.x, l2s = empty ? 0.f : ms.y * kLog2e;
+        const float a = -(gl + gh * hrow), b = -gh * kLn2;
+        const f32x2_t M = f2_pack(-m, -m), C = f2_pack(p.c, p.c), S = f2_pack(-l2s, -l2s);
+        const f32x2_t A = f2_pack(a, a), B = f2_pack(b, b);
+        const int64_t y_vec = y >= s.h && y < s.tail_col ? (y - s.h) / (16 / ES) : -1;
+        float x_y = 0.f;
+        const bool mine = y >= s.col_lo && y < s.col_hi &&
+                          (y_vec >= 0 ? (y_vec - s.vbeg) % kGradThreads == threadIdx.x
+                                      : static_cast<int>(threadIdx.x) < s.n_edge && edge_column(s, threadIdx.x) == y);
+        if (mine) x_y = load_scalar<ES>(s.rowp + y * ES);
+        auto grad = [&](f32x2_t x) {
+            f32x2_t d = f2_fma(f2_add(x, M), C, S);  // log2 p
+            if (ENT) d = clamp_exponent(d);
+            return f2_mul(f2_ex2(d), ENT ? f2_fma(B, d, A) : A);
+        };
+        store_segment<ES>(s, v, edge, grad);
+        if (mine) {  // after this thread's own store of that place
+            float lo, hi;
+            f2_unpack(grad(f2_pack(x_y, x_y)), lo, hi);
+            store_scalar<ES>(s.drow + y * ES, lo + gl);
+        }
+    }
+}
+
+template <int ES, bool TWO>
+__global__ void __launch_bounds__(kGradThreads, kGradBlocksPerSm) distill_grad_kernel(const RowsGradParams p) {
+    griddep_launch_dependents();
+    griddep_wait();
+    __shared__ int scratch[2 * (kGradThreads / 32)];
+    __shared__ TeacherRow teach;
+    __shared__ float s_xy;
+    int n_valid = static_cast<int>(p.src.N), n_bad = 0;
+    if (p.src.labels && (p.denom <= 0.f || (blockIdx.x == 0 && p.err)))
+        count_labels(p.src.labels, p.src.N, p.src.V, p.src.ignore_index, scratch, n_valid, n_bad);
+    if (blockIdx.x == 0 && threadIdx.x == 0 && p.err) *p.err = n_bad > 0 ? FOAK_ERRBIT_LABEL_RANGE : 0;
+    const float scale = (p.g_ptr ? __ldg(p.g_ptr) : 1.f) / (p.denom > 0.f ? p.denom : static_cast<float>(n_valid));
+    const float w1 = scale * p.ce_w, wt = scale * p.kd_w * p.inv_t;
+    const int64_t items = p.src.N * p.nseg;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const Segment s = segment_of<ES>(p, item);
+        const int64_t y = p.src.labels ? __ldg(p.src.labels + s.row) : -1;
+        if (!stream_row_valid(y, p.src)) {
+            zero_segment<ES>(s);
+            continue;
+        }
+        uint4 v[kGradVpt];
+        float edge;
+        load_segment<ES>(s, v, edge);
+        const float4 st = __ldg(p.stats4 + s.row);
+        if (threadIdx.x < 32) {
+            teacher_row<ES>(p.teacher, s.row, p.src.V, s.rowp, s.col_lo, s.col_hi, teach);
+            if (threadIdx.x == 0 && y >= s.col_lo && y < s.col_hi) s_xy = load_scalar<ES>(s.rowp + y * ES);
+        }
+        __syncthreads();  // the teacher's row is in place, and the logits it needs are read
+        const bool empty = st.x == kNegInf;  // nothing but -inf: p = 0
+        const float m = empty ? 0.f : st.x;
+        const float l1 = empty ? 0.f : st.y * kLog2e, lt = empty ? 0.f : st.z * kLog2e;
+        const float at = wt * teach.total, a1 = w1;
+        // one exponential where both parts share it
+        const float a = TWO ? at : at + (p.ce_w != 0.f ? a1 : 0.f);
+        const f32x2_t M = f2_pack(-m, -m), C = f2_pack(p.c, p.c), L = f2_pack(kLog2e, kLog2e);
+        const f32x2_t ST = f2_pack(-lt, -lt), S1 = f2_pack(-l1, -l1), A = f2_pack(a, a), A1 = f2_pack(a1, a1);
+        auto grad = [&](f32x2_t x) {
+            const f32x2_t d = f2_add(x, M);
+            f32x2_t e = f2_mul(f2_ex2(f2_fma(d, C, ST)), A);
+            if (TWO) e = f2_fma(f2_ex2(f2_fma(d, L, S1)), A1, e);
+            return e;
+        };
+        store_segment<ES>(s, v, edge, grad);
+        __syncthreads();  // the places that differ follow the segment's plain stores
+        for (int j = threadIdx.x; j <= p.teacher.K; j += kGradThreads) {
+            const bool is_label = j == p.teacher.K;
+            const int64_t id = is_label ? y : teach.id[j];
+            if (id < 0 || id < s.col_lo || id >= s.col_hi) continue;
+            const float x = is_label ? s_xy : teach.x[j];
+            float lo, hi;
+            f2_unpack(grad(f2_pack(x, x)), lo, hi);
+            lo -= wt * teacher_mass(teach, p.teacher.K, static_cast<int>(id));
+            if (id == y) lo -= w1;
+            store_scalar<ES>(s.drow + id * ES, lo);
+        }
+        __syncthreads();  // the teacher's row may be overwritten
+    }
+}
+
+RowsGradParams common_params(int es, const void* x, void* dx, int64_t ld, const int64_t* labels, int64_t N, int64_t V,
+                             int64_t ignore_index, float temperature, int32_t* err) {
+    RowsGradParams p = {};
+    p.src.x = static_cast<const char*>(x);
+    p.src.ld = ld;
+    p.src.labels = labels;
+    p.src.N = N;
+    p.src.V = V;
+    p.src.ignore_index = ignore_index;
+    p.src.k = 1;
+    p.dx = static_cast<char*>(dx);
+    p.nseg = std::max<int64_t>(1, (V * es / 16 + kGradSegVec - 1) / kGradSegVec);
+    p.inv_t = 1.f / temperature;
+    p.c = kLog2e / temperature;
+    p.err = err;
+    return p;
+}
+
+dim3 grad_grid(const RowsGradParams& p) {
+    const int64_t full = static_cast<int64_t>(device_sm_count()) * kGradBlocksPerSm;
+    return dim3(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(full, p.src.N * p.nseg))));
+}
+
+}  // namespace
+
+cudaError_t launch_logprobs_grad(int es, const void* x, void* dx, int64_t ld, const int64_t* labels, int64_t N,
+                                 int64_t V, int64_t ignore_index, float temperature, const float* stats,
+                                 const float* grad_logp, const float* entropy, const float* grad_entropy, int32_t* err,
+                                 cudaStream_t stream) {
+    RowsGradParams p = common_params(es, x, dx, ld, labels, N, V, ignore_index, temperature, err);
+    p.stats2 = reinterpret_cast<const float2*>(stats);
+    p.entropy = entropy;
+    p.grad_logp = grad_logp;
+    p.grad_entropy = grad_entropy;
+    const dim3 grid = grad_grid(p), block(kGradThreads);
+    if (es == 2)
+        return grad_entropy ? launch_dependent(logprobs_grad_kernel<2, true>, grid, block, 0, stream, p)
+                            : launch_dependent(logprobs_grad_kernel<2, false>, grid, block, 0, stream, p);
+    return grad_entropy ? launch_dependent(logprobs_grad_kernel<4, true>, grid, block, 0, stream, p)
+                        : launch_dependent(logprobs_grad_kernel<4, false>, grid, block, 0, stream, p);
+}
+
+cudaError_t launch_distill_grad(int es, const void* x, void* dx, int64_t ld, const int64_t* labels, int64_t N,
+                                int64_t V, int64_t ignore_index, const int32_t* ids, const float* logp,
+                                int64_t ld_teacher, int K, bool normalize, float ce_w, float kd_w, float temperature,
+                                const float* stats, const float* grad_out, float denom, int32_t* err,
+                                cudaStream_t stream) {
+    RowsGradParams p = common_params(es, x, dx, ld, labels, N, V, ignore_index, temperature, err);
+    p.stats4 = reinterpret_cast<const float4*>(stats);
+    p.teacher.ids = ids;
+    p.teacher.logp = logp;
+    p.teacher.ld = ld_teacher;
+    p.teacher.K = K;
+    p.teacher.normalize = normalize;
+    p.g_ptr = grad_out;
+    p.denom = denom;
+    p.ce_w = ce_w;
+    p.kd_w = kd_w;
+    const dim3 grid = grad_grid(p), block(kGradThreads);
+    const bool two = ce_w != 0.f && temperature != 1.f;
+    if (es == 2)
+        return two ? launch_dependent(distill_grad_kernel<2, true>, grid, block, 0, stream, p)
+                   : launch_dependent(distill_grad_kernel<2, false>, grid, block, 0, stream, p);
+    return two ? launch_dependent(distill_grad_kernel<4, true>, grid, block, 0, stream, p)
+               : launch_dependent(distill_grad_kernel<4, false>, grid, block, 0, stream, p);
+}
+
+}  // namespace foak

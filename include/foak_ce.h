@@ -335,6 +335,106 @@ foak_status foak_rope_apply_qk(void* Q, int64_t Hq, int64_t ldq, void* K, int64_
                                int32_t inverse, int32_t* err, void* stream);
 
 /*
+ * Log probabilities, entropy and most likely tokens of the rows of a logits matrix:
+ * what sits beside the loss once a model is served, trained by policy gradients or
+ * used as a teacher.  The pages have no counterpart.  With z = x / temperature:
+ *     lse_i = log sum_j exp(z_ij)          logp_i = z_{i,y_i} - lse_i
+ *     H_i   = -sum_j p_ij log p_ij         p_ij = exp(z_ij - lse_i)
+ * and the top_k largest logits of the row in descending order (equal logits: the
+ * lower token id first) with their z_ij - lse_i.  One read of each row.
+ *   logits, dtype, ld    as for foak_ce_forward
+ *   labels (device)      int64[N], the given tokens, or NULL: every row is computed,
+ *                        and logp must be NULL.  A row whose label is ignore_index, or
+ *                        out of range (error bit FOAK_ERRBIT_LABEL_RANGE), is not read:
+ *                        its outputs are 0 and its top ids -1
+ *   temperature          in [1e-6, 1e6]
+ *   top_k                0 .. min(V, FOAK_LOGPROBS_MAX_K); with top_k > 0, V <= 262144
+ *   logp, entropy, lse (device)  float[N] each, or NULL
+ *   stats (device)       float[N][2], 8-byte aligned, or NULL: (max_j x_ij, log sum_j
+ *                        exp((x_ij - max) / temperature)), for foak_logprobs_backward
+ *   top_logprobs (device) float[N][top_k];  top_ids (device) int32[N][top_k]
+ *   err (device)         int32[1] or NULL
+ *   workspace (device)   foak_logprobs_workspace_size() bytes, with the rules of
+ *                        foak_ce_workspace_size (a buffer of that kind serves too)
+ * Masked logits: an element of -inf has probability 0 and adds nothing to the entropy.
+ * A row of nothing but -inf has lse -inf, log probabilities -inf, entropy 0 and top ids
+ * 0 .. top_k - 1.  A row that holds NaN or +inf gives NaN, and top ids -1.
+ */
+#define FOAK_LOGPROBS_MAX_K 256
+size_t foak_logprobs_workspace_size(void);
+foak_status foak_logprobs_forward(const void* logits, int32_t dtype, int64_t ld, const int64_t* labels, int64_t N,
+                                  int64_t V, int64_t ignore_index, float temperature, int64_t top_k, float* logp,
+                                  float* entropy, float* lse, float* stats, float* top_logprobs, int32_t* top_ids,
+                                  int32_t* err, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of sum_i (grad_logp_i logp_i + grad_entropy_i H_i) with respect to the logits:
+ *     dx_ij = (grad_logp_i ([j == y_i] - p_ij) - grad_entropy_i p_ij (log p_ij + H_i)) / temperature
+ * Rows that do not count get +0.0 and are not read; a row of nothing but -inf has p = 0.
+ *   dlogits (device)     N x V, ld and dtype of the logits and the same offset modulo 16
+ *                        bytes; may equal logits (in place)
+ *   stats (device)       float[N][2] from the forward at the same temperature
+ *   grad_logp (device)   float[N] or NULL (zero)
+ *   entropy (device)     float[N] from the forward; needed with grad_entropy
+ *   grad_entropy (device) float[N] or NULL (zero)
+ *   err (device)         int32[1] or NULL
+ */
+foak_status foak_logprobs_backward(void* dlogits, const void* logits, int32_t dtype, int64_t ld, const int64_t* labels,
+                                   int64_t N, int64_t V, int64_t ignore_index, float temperature, const float* stats,
+                                   const float* grad_logp, const float* entropy, const float* grad_entropy,
+                                   int32_t* err, void* stream);
+
+/*
+ * Distillation from a teacher's top tokens, mixed with the labels' cross-entropy.  The
+ * teacher's row is K token ids with their log probabilities t (at the distillation
+ * temperature: top_ids and top_logprobs of foak_logprobs_forward called with it).
+ *     q_k  = exp(t_k) / sum_l exp(t_l)  (normalize != 0; t may then also be logits / temperature),  else exp(t_k)
+ *     KD_i = sum_k q_k (log q_k - log p_{id_k}),  p = softmax(x_i / temperature)
+ *     CE_i = log sum_j exp(x_ij) - x_{i,y_i}
+ *     loss = sum_{valid i} (ce_weight CE_i + kd_weight KD_i) / D,   D = denom > 0 ? denom : n_valid
+ *     dx_ij = (g / D) (ce_weight (softmax(x_i)_j - [j == y_i])
+ *                      + kd_weight / temperature (p_ij sum_k q_k - sum_k q_k [j == id_k]))
+ * (the customary factor temperature^2 is the caller's to put into kd_weight).
+ *   logits, dtype, ld, ignore_index, denom, loss, n_valid, err, workspace: as for
+ *                        foak_ce_forward (foak_ce_workspace_size(N) bytes)
+ *   labels (device)      int64[N]; rows whose label is ignore_index do not count.  NULL:
+ *                        every row counts, and ce_weight must be 0
+ *   teacher_ids (device) int32[N][ld_teacher]: K ids a row.  A negative id is padding; an
+ *                        id >= V counts as padding and sets FOAK_ERRBIT_LABEL_RANGE.  An
+ *                        id may be listed more than once; its shares add up
+ *   teacher_logprobs (device) float[N][ld_teacher]; -inf: no share
+ *   K                    1 .. FOAK_DISTILL_MAX_K
+ *   temperature          in [1e-6, 1e6]; ce_weight and kd_weight finite
+ *   row_ce, row_kd (device) float[N] or NULL: the rows' terms (row_ce is 0 when
+ *                        ce_weight is 0; 0 on rows that do not count)
+ *   stats (device)       float[N][4], 16-byte aligned, or NULL: what foak_distill_backward
+ *                        needs (max, log sum exp(x - max), log sum exp((x - max) / temperature),
+ *                        sum of q)
+ *   dlogits (device)     as for foak_logprobs_backward; may equal logits
+ * foak_distill_fwd_bwd reads each logit once from device memory and writes its gradient;
+ * foak_distill_backward recomputes it from stats, times *grad_out (device float[1], NULL = 1).
+ * A student that gives a listed token probability 0 (a masked logit) has an infinite loss.
+ */
+#define FOAK_DISTILL_MAX_K 256
+foak_status foak_distill_forward(const void* logits, int32_t dtype, int64_t ld, const int64_t* labels, int64_t N,
+                                 int64_t V, int64_t ignore_index, const int32_t* teacher_ids,
+                                 const float* teacher_logprobs, int64_t ld_teacher, int64_t K, int32_t normalize,
+                                 float ce_weight, float kd_weight, float temperature, float denom, float* loss,
+                                 float* row_ce, float* row_kd, float* stats, int32_t* n_valid, int32_t* err,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+foak_status foak_distill_fwd_bwd(const void* logits, void* dlogits, int32_t dtype, int64_t ld, const int64_t* labels,
+                                 int64_t N, int64_t V, int64_t ignore_index, const int32_t* teacher_ids,
+                                 const float* teacher_logprobs, int64_t ld_teacher, int64_t K, int32_t normalize,
+                                 float ce_weight, float kd_weight, float temperature, float g, float denom,
+                                 float* loss, float* row_ce, float* row_kd, int32_t* n_valid, int32_t* err,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+foak_status foak_distill_backward(void* dlogits, const void* logits, int32_t dtype, int64_t ld, const int64_t* labels,
+                                  int64_t N, int64_t V, int64_t ignore_index, const int32_t* teacher_ids,
+                                  const float* teacher_logprobs, int64_t ld_teacher, int64_t K, int32_t normalize,
+                                  float ce_weight, float kd_weight, float temperature, const float* stats,
+                                  const float* grad_out, float denom, int32_t* err, void* stream);
+
+/*
  * Bytes of device workspace foak_linear_ce_chunked needs: the batch's label
  * count, N float32 per-row loss terms, a few error words, one chunk's per-tile
  * softmax statistics (chunk x ceil(V / 256) float pairs), its label logits and
