@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kStreamBlock, 3) distill_kernel(const DistillP
                 edge = load_scalar<ES>(s.rowp + edge_col * ES);
                 st.add(edge, p.c, kLog2e);
             }
-            stat_reduce(st, ex, parity, k, rank, p.c, kLog2e, nullptr);
+            stat_reduce(st, ex, parity, k, rank, p.c, kLog2e);
             parity ^= 1u;
             const float s1 = TWO ? st.s2 : st.s;  // at T = 1 they are the same; without w_ce it is not used
             if (rank == 0 && warp == 0 && !pos.aborted) {

@@ -33,6 +33,7 @@ namespace foak {
 namespace {
 
 constexpr int kListCap = 1024;  // listed elements of a row (or of a CTA's share of it)
+constexpr int kSelCap = 256;    // blocks they are taken from
 
 struct LogprobParams {
     StreamSrc src;
@@ -62,22 +63,26 @@ template <int ES>
 struct BlockKey {
     using type = uint32_t;
     static __device__ __forceinline__ uint32_t of(float f) { return key_of(f); }
-    static __device__ __forceinline__ uint32_t element(uint32_t k) { return k; }  // the smallest element key
+    static __device__ __forceinline__ uint32_t element(uint32_t k) { return k; }  // no element of it has a smaller key
+    static __device__ __forceinline__ float value(uint32_t k) { return float_of_key(k); }
 };
 template <>
 struct BlockKey<2> {
     using type = uint16_t;
     static __device__ __forceinline__ uint32_t of(float f) { return key_of(f) >> 16; }
     static __device__ __forceinline__ uint32_t element(uint32_t k) { return k << 16; }
+    static __device__ __forceinline__ float value(uint32_t k) {  // the lower half of a negative number's key is ones
+        return float_of_key(k >> 15 ? k << 16 : k << 16 | 0xffffu);
+    }
 };
 
 struct TopScratch {
-    int count[2][kStreamWarps];        // partial counts, by the parity of the count
-    float warp_min[kStreamWarps];      // least thread maximum of each warp
-    int n_sel, n_list;
-    int sel[kStreamThreads];           // the chosen blocks
-    unsigned long long list[kListCap]; // (key << 32) | ~column
-    unsigned long long best[kStreamThreads];  // this CTA's top K in order (clusters)
+    int count[2][kStreamWarps];                // partial counts, by the parity of the count
+    int n_sel, n_list, n_tied;
+    uint32_t thread_max[kStreamThreads];       // key of the largest of a thread's blocks; 0: it has none
+    int sel[kSelCap];                          // the chosen blocks
+    alignas(16) unsigned long long list[kListCap];  // (key << 32) | ~column
+    unsigned long long best[kStreamThreads];   // this CTA's top K in order (clusters)
 };
 
 // The sum of n over the consumer threads; one consumer barrier.
@@ -139,59 +144,33 @@ struct BlockElements {
     }
 };
 
-// This CTA's largest elements of its slice onto t.list: at least the min(K, all) largest
-// ones, at most kListCap.  Returns how many.  keys[1 .. nblk] are the block maxima, least
-// the maximum of the thread's own blocks, cta_max the slice's (-FLT_MAX at the least).
+// The slow way to the list, for rows in which the fast one meets more blocks or elements
+// than it has room for (many equal values, or a share of few blocks): exact bisections,
+// first for the K-th largest block by (maximum, lower index first), then, if need be, for
+// the K-th largest element.  nreal > K blocks, or all of them are taken.
 template <int ES>
-__device__ __forceinline__ int top_list(const Slice& s, typename BlockKey<ES>::type* keys, int K, float least,
-                                        float cta_max, TopScratch& t) {
+__device__ __noinline__ void top_list_exact(const Slice s, const typename BlockKey<ES>::type* keys, int K, TopScratch& t) {
     using BK = BlockKey<ES>;
     const int tid = threadIdx.x;
     const int nblk = (s.nv + kBlockVec - 1) / kBlockVec;
     const int nreal = nblk + (s.h > 0) + (s.t > 0);
     uint32_t turn = 0;
-    // the head's and tail's maxima; also the least thread maximum of the CTA
-    if (tid == 0 || tid == 32) {
-        const int n = tid == 0 ? s.h : s.t;
-        const char* at = s.rowp + (tid == 0 ? 0 : s.tail_col * ES);
-        float m = kNegInf;
-        for (int e = 0; e < n; ++e) m = fmaxf(m, load_scalar<ES>(at + e * ES));
-        keys[tid == 0 ? 0 : nblk + 1] = n > 0 ? BK::of(m) : 0;
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) least = fminf(least, __shfl_xor_sync(0xffffffffu, least, off));
-    if ((tid & 31) == 0) t.warp_min[tid >> 5] = least;
+    consumers_sync();
     if (tid == 0) {
         t.n_sel = 0;
         t.n_list = 0;
     }
-    consumers_sync();
-
-    // ---- 1. the blocks: keys >= lo, and of those equal to lo only the ids up to last
+    // ---- the blocks: keys above lo, and of those equal to lo the ids up to last
     uint32_t lo = 1;
     int last = 0x7fffffff;
     if (nreal > K) {
-        const int most = min(kStreamThreads, K + K / 2 + 24);
-        auto at_least = [&](uint32_t k) {
-            int n = 0;
-            for (int b = tid; b < nblk + 2; b += kStreamThreads) n += keys[b] >= k;
-            return consumers_count(n, t, turn);
-        };
-        uint32_t hi = BK::of(cta_max) + 1;
-        int c_lo = nreal, c_hi = 0;  // blocks at or above lo and hi
-        if (nblk >= kStreamThreads) {  // every thread has seen a block: 256 >= K maxima at or above the least of theirs
-            float l = t.warp_min[0];
-#pragma unroll
-            for (int w = 1; w < kStreamWarps; ++w) l = fminf(l, t.warp_min[w]);
-            const uint32_t k = BK::of(l);
-            if (l > -FLT_MAX && k > lo && k < hi) {  // (-FLT_MAX: perhaps nothing but -inf)
-                lo = k;
-                c_lo = 0x7fffffff;  // at least 256, not counted
-            }
-        }
-        while (hi - lo > 1 && c_lo > most) {
+        uint32_t hi = ES == 2 ? 0x10000u : 0xffffffffu;  // no key is as large (a NaN's would be)
+        int c_lo = nreal, c_hi = 0;                      // blocks at or above lo and hi
+        while (hi - lo > 1 && c_lo > kSelCap) {
             const uint32_t mid = lo + (hi - lo) / 2;
-            const int n = at_least(mid);
+            int n = 0;
+            for (int b = tid; b < nblk + 2; b += kStreamThreads) n += keys[b] >= mid;
+            n = consumers_count(n, t, turn);
             if (n >= K) {
                 lo = mid;
                 c_lo = n;
@@ -200,8 +179,7 @@ __device__ __forceinline__ int top_list(const Slice& s, typename BlockKey<ES>::t
                 c_hi = n;
             }
         }
-        if (c_lo == 0x7fffffff) c_lo = at_least(lo);
-        if (c_lo > kStreamThreads) {  // then hi == lo + 1: ties at lo, the first need of them
+        if (c_lo > kSelCap) {  // hi == lo + 1: ties at lo, the first `need` of them
             const int need = K - c_hi;
             int j0 = -1, j1 = nblk + 1;  // fewer than need ties up to j0, enough up to j1
             while (j1 - j0 > 1) {
@@ -214,35 +192,33 @@ __device__ __forceinline__ int top_list(const Slice& s, typename BlockKey<ES>::t
             last = j1;
         }
     }
+    consumers_sync();
     for (int b = tid; b < nblk + 2; b += kStreamThreads) {
         const uint32_t k = keys[b];
         if (k > lo || (k == lo && b <= last)) {
             const int i = atomicAdd(&t.n_sel, 1);
-            if (i < kStreamThreads) t.sel[i] = b;
+            if (i < kSelCap) t.sel[i] = b;
         }
     }
     consumers_sync();
-
-    // ---- 2. their elements at or above the threshold
-    const int n_sel = min(t.n_sel, kStreamThreads);
+    // ---- one block a thread, and its elements
+    const int n_sel = min(t.n_sel, kSelCap);
     BlockElements<ES> el;
+    el.n = 0;
+    el.col = 0;
     if (tid < n_sel) el.load(s, t.sel[tid], nblk);
-    else el.n = 0;
-    unsigned long long floor = static_cast<unsigned long long>(BK::element(lo)) << 32;
-    int mine = 0;
+    auto at_least = [&](unsigned long long f) {
+        int n = 0;
 #pragma unroll
-    for (int e = 0; e < BlockElements<ES>::N; ++e) mine += el.item(e) >= floor;
-    const int total = consumers_count(mine, t, turn);
-    if (total > kListCap) {
-        // Many ties, or few blocks of many elements: bisection for the exact K-th largest item (items are
-        // distinct).  Every count is at least K at b0 and less than K at b1.
-        unsigned long long b0 = floor, b1 = static_cast<unsigned long long>(key_of(cta_max) + 1u) << 32;
+        for (int e = 0; e < BlockElements<ES>::N; ++e) n += el.item(e) >= f;
+        return consumers_count(n, t, turn);
+    };
+    // every count is at least K at b0 (or takes every element) and less than K at b1
+    unsigned long long b0 = static_cast<unsigned long long>(BK::element(lo)) << 32, b1 = ~0ull;
+    if (at_least(b0) > kListCap) {
         while (b1 - b0 > 1) {
             const unsigned long long mid = b0 + (b1 - b0) / 2;
-            int n = 0;
-#pragma unroll
-            for (int e = 0; e < BlockElements<ES>::N; ++e) n += el.item(e) >= mid;
-            const int c = consumers_count(n, t, turn);
+            const int c = at_least(mid);
             if (c >= K) {
                 b0 = mid;
                 if (c <= kListCap) break;
@@ -250,17 +226,154 @@ __device__ __forceinline__ int top_list(const Slice& s, typename BlockKey<ES>::t
                 b1 = mid;
             }
         }
-        floor = b0;
     }
 #pragma unroll
     for (int e = 0; e < BlockElements<ES>::N; ++e) {
         const unsigned long long it = el.item(e);
-        if (it >= floor) {
+        if (it >= b0) {
             const int i = atomicAdd(&t.n_list, 1);
             if (i < kListCap) t.list[i] = it;
         }
     }
     consumers_sync();
+}
+
+// This CTA's largest elements of its slice onto t.list: at least the min(K, all) largest
+// ones, at most kListCap.  Returns how many.  keys[1 .. nblk] are the block maxima, keys[0]
+// and keys[nblk + 1] those of the head and tail (0: none), t.thread_max the threads'; all
+// of them written before a barrier.
+template <int ES>
+__device__ __forceinline__ int top_list(const Slice& s, const typename BlockKey<ES>::type* keys, int K, TopScratch& t) {
+    using BK = BlockKey<ES>;
+    constexpr int EPV = 16 / ES;
+    constexpr int PER = kStreamThreads / 32;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int nblk = (s.nv + kBlockVec - 1) / kBlockVec;
+    // A threshold that K threads' maxima, so K blocks, reach: the K-th largest of the 256
+    // thread maxima, or a little below it.  Every warp finds it for itself, without a
+    // barrier.  Of blocks in random order about -256 ln(1 - K / 256) are at or above it.
+    uint32_t lo = 1;
+    if (min(nblk, kStreamThreads) >= K) {
+        uint32_t v[PER], least = 0xffffffffu, hi = 0;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            v[j] = t.thread_max[lane + 32 * j];
+            if (v[j]) least = min(least, v[j]);
+            hi = max(hi, v[j]);
+        }
+        lo = __reduce_min_sync(0xffffffffu, least);
+        hi = __reduce_max_sync(0xffffffffu, hi) + 1;
+        const int most = K + K / 8 + 4;
+        while (hi - lo > 1) {
+            const uint32_t mid = lo + (hi - lo) / 2;
+            int n = 0;
+#pragma unroll
+            for (int j = 0; j < PER; ++j) n += v[j] >= mid;
+            n = __reduce_add_sync(0xffffffffu, n);
+            if (n >= K) {
+                lo = mid;
+                if (n <= most) break;
+            } else {
+                hi = mid;
+            }
+        }
+    }
+    for (int b = 1 + tid; b <= nblk; b += kStreamThreads) {
+        if (keys[b] >= lo) {
+            const int i = atomicAdd(&t.n_sel, 1);
+            if (i < kSelCap) t.sel[i] = b;
+        }
+    }
+    consumers_sync();
+    int n_sel = t.n_sel, need = 0x7fffffff, strict = 0x7fffffff;  // sel[strict ..]: blocks whose maximum is lo, in order
+    if (n_sel > kSelCap) {
+        // Ties at the threshold (a mask that leaves fewer than K tokens): the blocks above
+        // it, and the first blocks that reach it, as many as can matter.
+        consumers_sync();
+        if (tid == 0) t.n_sel = 0;
+        consumers_sync();
+        for (int b = 1 + tid; b <= nblk; b += kStreamThreads) {
+            if (keys[b] > lo) {
+                const int i = atomicAdd(&t.n_sel, 1);
+                if (i < kSelCap) t.sel[i] = b;
+            }
+        }
+        consumers_sync();
+        strict = t.n_sel;
+        need = K - strict;
+        if (strict < K) {
+            if (tid < 32) {
+                int have = 0;
+                for (int b0 = 1; b0 <= nblk && have < need; b0 += 32) {
+                    const bool tie = b0 + lane <= nblk && keys[b0 + lane] == lo;
+                    const unsigned m = __ballot_sync(0xffffffffu, tie);
+                    const int at = have + __popc(m & ((1u << lane) - 1u));
+                    if (tie && at < need) t.sel[strict + at] = b0 + lane;
+                    have += __popc(m);
+                }
+                if (lane == 0) t.n_tied = min(have, need);
+            }
+            consumers_sync();
+            n_sel = strict + t.n_tied;
+        } else {
+            n_sel = kSelCap + 1;  // more than K blocks above the K-th thread maximum: the slow way
+        }
+    }
+    if (n_sel <= kSelCap) {
+        // Four threads a block, one vector each (re-read from L2); the elements at or above the threshold.
+        const float floor = lo == 1 ? kNegInf : BK::value(lo);
+        const uint4* body = reinterpret_cast<const uint4*>(s.body);
+        for (int i0 = 0; i0 < n_sel * kBlockVec; i0 += kStreamThreads) {
+            const int i = i0 + tid, j = i / kBlockVec;
+            const int vec = j < n_sel ? (t.sel[j] - 1) * kBlockVec + (i & (kBlockVec - 1)) : s.nv;
+            uint4 w = RowMath<ES>::pad();
+            const bool real = vec < s.nv;
+            if (real) w = ld_global_v4(body + vec);
+            float f[EPV];
+            int ties = 0;
+            bool any = false;
+#pragma unroll
+            for (int e = 0; e < EPV / 2; ++e) f2_unpack(vec_pair<ES>(w, e), f[2 * e], f[2 * e + 1]);
+#pragma unroll
+            for (int e = 0; e < EPV; ++e) {
+                any |= f[e] >= floor;
+                ties += f[e] == floor;
+            }
+            if (!real) ties = 0;
+            int before = 0;  // ties of the same block in earlier vectors
+            if (strict != 0x7fffffff) {
+                int sum = ties;
+#pragma unroll
+                for (int off = 1; off < kBlockVec; off <<= 1) {
+                    const int o = __shfl_up_sync(0xffffffffu, sum, off, kBlockVec);
+                    if ((tid & (kBlockVec - 1)) >= off) sum += o;
+                }
+                before = sum - ties + max(0, j - strict);  // and one at least in each tied block before
+            }
+            if (real && any) {
+#pragma unroll
+                for (int e = 0; e < EPV; ++e) {
+                    if (!(f[e] >= floor)) continue;
+                    if (f[e] == floor && before++ >= need) continue;  // enough equal ones come before it
+                    const int at = atomicAdd(&t.n_list, 1);
+                    const uint32_t col = static_cast<uint32_t>(s.col0 + static_cast<int64_t>(vec) * EPV + e);
+                    if (at < kListCap) t.list[at] = (static_cast<unsigned long long>(key_of(f[e])) << 32) | ~col;
+                }
+            }
+        }
+        if (tid < s.h + s.t) {
+            const int64_t col = tid < s.h ? tid : s.tail_col + (tid - s.h);
+            const float f = load_scalar<ES>(s.rowp + col * ES);
+            if (f >= floor) {
+                const int at = atomicAdd(&t.n_list, 1);
+                if (at < kListCap)
+                    t.list[at] = (static_cast<unsigned long long>(key_of(f)) << 32) | ~static_cast<uint32_t>(col);
+            }
+        }
+        consumers_sync();
+        if (t.n_list <= kListCap) return t.n_list;
+    }
+    top_list_exact<ES>(s, keys, K, t);
     return min(t.n_list, kListCap);
 }
 
@@ -317,21 +430,34 @@ __global__ void __launch_bounds__(kStreamBlock, 3) logprobs_kernel(const Logprob
             float x_y = 0.f;
             if (tid == 0 && rank == 0 && p.logp) x_y = load_scalar<ES>(s.rowp + y * ES);
             RunStat<ENT, false> st;
+            float most = kNegInf;  // of the thread's blocks
             for (int c0 = 0; c0 < s.nv; c0 += kStreamChunk) {
                 const int nl = min(kStreamChunk, s.nv - c0);
                 uint4 v[kBlockVec];
                 stream_chunk(p.src, bars, ring, pos, [&](const unsigned char* stage) { load_block<ES>(stage, nl, v); });
                 const float bmax = vec_max<ES>(v);
-                if (TOPK && tid * kBlockVec < nl) keys[1 + c0 / kBlockVec + tid] = static_cast<KeyT>(BlockKey<ES>::of(bmax));
+                if (TOPK) {
+                    if (tid * kBlockVec < nl) keys[1 + c0 / kBlockVec + tid] = static_cast<KeyT>(BlockKey<ES>::of(bmax));
+                    most = fmaxf(most, bmax);
+                }
                 st.template add_vecs<ES>(v, bmax, p.c, 0.f);
             }
-            const float least = st.m;  // of the thread's blocks
-            if (tid == 0)
-                for (int e = 0; e < s.h; ++e) st.add(load_scalar<ES>(s.rowp + e * ES), p.c, 0.f);
-            if (tid == 32)
-                for (int e = 0; e < s.t; ++e) st.add(load_scalar<ES>(s.rowp + (s.tail_col + e) * ES), p.c, 0.f);
-            float cta_m;
-            stat_reduce(st, ex, parity, k, rank, p.c, 0.f, &cta_m);
+            if (tid == 0 || tid == 32) {  // the head's and the tail's scalars
+                const int n = tid == 0 ? s.h : s.t;
+                const int64_t col = tid == 0 ? 0 : s.tail_col;
+                float m = kNegInf;
+                for (int e = 0; e < n; ++e) {
+                    const float x = load_scalar<ES>(s.rowp + (col + e) * ES);
+                    st.add(x, p.c, 0.f);
+                    m = fmaxf(m, x);
+                }
+                if (TOPK) keys[tid == 0 ? 0 : 1 + (s.nv + kBlockVec - 1) / kBlockVec] = n > 0 ? BlockKey<ES>::of(m) : 0;
+            }
+            if (TOPK) {
+                top.thread_max[tid] = tid * kBlockVec < s.nv ? BlockKey<ES>::of(most) : 0u;
+                if (tid == 0) top.n_sel = top.n_list = 0;
+            }
+            stat_reduce(st, ex, parity, k, rank, p.c, 0.f);
             parity ^= 1u;
             const float ln_s = logf(st.s);
             const bool empty = st.s == 0.f;
@@ -349,46 +475,66 @@ __global__ void __launch_bounds__(kStreamBlock, 3) logprobs_kernel(const Logprob
                 const int K = p.top_k;
                 const bool none = !(st.s == st.s);  // a NaN or +inf in the row: no order to speak of
                 int n = 0;
-                if (!none) n = top_list<ES>(s, keys, K, least, cta_m, top);
+                if (!none) n = top_list<ES>(s, keys, K, top);
                 float* olp = p.top_lp + row * K;
                 int32_t* oid = p.top_ids + row * K;
                 auto write = [&](int r, unsigned long long item) {
+                    if (pos.aborted) return;
                     olp[r] = empty ? kNegInf : (float_of_key(static_cast<uint32_t>(item >> 32)) - st.m) * p.inv_t - ln_s;
                     oid[r] = static_cast<int32_t>(~static_cast<uint32_t>(item));
                 };
-                // ranks within this CTA's list
+                // Ranks within this CTA's list: `ways` neighbouring threads an item, each comparing it with
+                // its share of the list, two items a 16-byte read.
                 if (k > 1) {
                     if (tid < K) top.best[tid] = 0ull;
                     consumers_sync();
                 }
-                for (int i = tid; i < n; i += kStreamThreads) {
-                    const unsigned long long item = top.list[i];
+                const int ways = n <= kStreamThreads / 8 ? 8 : n <= kStreamThreads / 4 ? 4 : n <= kStreamThreads / 2 ? 2 : 1;
+                const int part = tid & (ways - 1);
+                for (int i0 = 0; i0 < n; i0 += kStreamThreads / ways) {
+                    const int i = i0 + tid / ways;
+                    const unsigned long long item = i < n ? top.list[i] : ~0ull;
                     int r = 0;
-                    for (int j = 0; j < n; ++j) r += top.list[j] > item;
-                    if (r < K) {
+                    for (int j = 2 * part; j < n; j += 2 * ways) {
+                        const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(top.list + j);
+                        r += o.x > item;
+                        if (j + 1 < n) r += o.y > item;
+                    }
+                    for (int off = 1; off < ways; off <<= 1) r += __shfl_xor_sync(0xffffffffu, r, off);
+                    if (i < n && part == 0 && r < K) {
                         if (k > 1) top.best[r] = item;
-                        else if (!pos.aborted) write(r, item);
+                        else write(r, item);
                     }
                 }
                 if (k > 1) {
+                    // The cluster's lists, each in order: an item's rank is the sum of its places in them,
+                    // one thread an item and list.  They are copied here first when there is room.
                     cluster_sync_converged();  // every CTA's best are in place
-                    if (tid < K && !none && top.best[tid] != 0ull) {
-                        const unsigned long long item = top.best[tid];
-                        int r = tid;
-                        for (int o = 0; o < k; ++o) {
-                            if (o == rank) continue;
-                            const uint32_t base = mapa_u32(top.best, static_cast<uint32_t>(o));
-                            int a = 0, b = K;  // entries before a are larger, from b on they are not
-                            while (a < b) {
-                                const int mid = (a + b) / 2;
-                                unsigned long long v;
-                                asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(base + mid * 8) : "memory");
-                                if (v > item) a = mid + 1;
-                                else b = mid;
-                            }
-                            r += a;
+                    const bool copy = K * k <= kListCap;
+                    if (copy && !none) {
+                        for (int i = tid; i < K * k; i += kStreamThreads) {
+                            const uint32_t from = mapa_u32(top.best, static_cast<uint32_t>(i / K)) + (i % K) * 8;
+                            asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(top.list[i]) : "r"(from) : "memory");
                         }
-                        if (r < K && !pos.aborted) write(r, item);
+                    }
+                    consumers_sync();
+                    for (int i0 = 0; !none && i0 < K * k; i0 += kStreamThreads) {
+                        const int i = i0 + tid;
+                        const int o = i & (k - 1);
+                        const unsigned long long item = i < K * k ? top.best[i / k] : 0ull;
+                        int a = 0, b = item ? K : 0;  // of list o: before a larger, from b on not
+                        const uint32_t remote = mapa_u32(top.best, static_cast<uint32_t>(o));
+                        while (a < b) {
+                            const int mid = (a + b) / 2;
+                            unsigned long long v;
+                            if (copy) v = top.list[o * K + mid];
+                            else asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(remote + mid * 8) : "memory");
+                            if (v > item) a = mid + 1;
+                            else b = mid;
+                        }
+                        __syncwarp();
+                        for (int off = 1; off < k; off <<= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
+                        if (o == 0 && item && a < K) write(a, item);
                     }
                     cluster_sync_converged();  // every CTA has read them
                 }

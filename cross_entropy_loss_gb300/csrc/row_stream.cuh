@@ -351,10 +351,10 @@ struct StatExchange {
 };
 
 // Every consumer thread's set as the row's.  One consumer barrier, and with a cluster
-// one cluster barrier.  *cta_m (if given) gets this CTA's own maximum.
+// one cluster barrier.
 template <bool ENT, bool TWO>
 __device__ __forceinline__ void stat_reduce(RunStat<ENT, TWO>& st, StatExchange& ex, uint32_t parity, int k, int rank,
-                                            float c, float c2, float* cta_m) {
+                                            float c, float c2) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     st.warp_merge(c, c2);
     if (lane == 0) ex.warp[parity][warp] = make_float4(st.m, st.s, st.a, st.s2);
@@ -371,7 +371,6 @@ __device__ __forceinline__ void stat_reduce(RunStat<ENT, TWO>& st, StatExchange&
         if (ENT) st.a += __shfl_xor_sync(0xffffffffu, st.a, off);
         if (TWO) st.s2 += __shfl_xor_sync(0xffffffffu, st.s2, off);
     }
-    if (cta_m) *cta_m = st.m;
     if (k > 1) {
         if (threadIdx.x < static_cast<unsigned>(k)) {
             const uint32_t to = mapa_u32(&ex.cta[parity][rank], threadIdx.x);
