@@ -30,7 +30,8 @@ struct DistillParams {
     TeacherSrc teacher;
     char* dx;
     float ce_w, kd_w;
-    float inv_t, c;    // 1 / T, log2(e) / T
+    float inv_t;       // 1 / T
+    ExpScale scale;
     float g;
     float* row_ce;     // [N] or null
     float* row_kd;     // [N] or null
@@ -71,13 +72,14 @@ __global__ void __launch_bounds__(kStreamBlock, 3) distill_kernel(const DistillP
         }
         const float w1 = scale * p.ce_w, wt = scale * p.kd_w * p.inv_t;
         StreamPos pos{0, 0, false};
+        Slice s = slice_of<ES>(p.src, cid, rank);
         uint32_t parity = 0;
         int64_t y_next = p.src.labels && n_it > 0 ? __ldg(p.src.labels + cid) : 0;
         for (int64_t it = 0; it < n_it; ++it) {
             const int64_t row = cid + it * ncl;
             const int64_t y = y_next;
             if (p.src.labels && it + 1 < n_it) y_next = __ldg(p.src.labels + row + ncl);
-            const Slice s = slice_of<ES>(p.src, row, rank);
+            move_slice<ES>(p.src, row, rank, s);
             char* drow = GRAD ? p.dx + row * p.src.ld * ES : nullptr;
             uint4* dv = reinterpret_cast<uint4*>(drow + s.col0 * ES);
             if (!stream_row_valid(y, p.src)) {
@@ -110,22 +112,30 @@ __global__ void __launch_bounds__(kStreamBlock, 3) distill_kernel(const DistillP
                     }
                 }
             }
-            RunStat<false, TWO> st;
+            RunStat<false, TWO> st(p.scale);
             for (int c0 = 0; c0 < s.nv; c0 += kStreamChunk) {
                 const int nl = min(kStreamChunk, s.nv - c0);
                 uint4 v[kBlockVec];
-                stream_chunk(p.src, bars, smem, pos, [&](const unsigned char* stage) { load_block<ES>(stage, nl, v); });
-                st.template add_vecs<ES>(v, vec_max<ES>(v), p.c, kLog2e);
+                stream_chunk(p.src, bars, smem, pos, [&](const unsigned char* stage) { load_strided<ES>(stage, nl, v); });
+                st.template add_vecs<ES>(v, p.scale);
             }
             // the head and tail scalars, one a thread; kept for the gradient
             const int n_edge = s.h + s.t;
             const int64_t edge_col = tid < s.h ? tid : s.tail_col + (tid - s.h);
-            float edge = 0.f;
-            if (tid < n_edge) {
-                edge = load_scalar<ES>(s.rowp + edge_col * ES);
-                st.add(edge, p.c, kLog2e);
+            float edge = kNegInf;
+            if (n_edge > 0 && tid < 32) {
+                if (tid < n_edge) edge = load_scalar<ES>(s.rowp + edge_col * ES);
+                st.add(edge, p.scale);
             }
-            stat_reduce(st, ex, parity, k, rank, p.c, kLog2e);
+            stat_publish(st, ex, parity);
+            consumers_sync();
+            stat_collect(st, ex, parity, p.scale);
+            if (k > 1) {
+                stat_send(st, ex, parity, k, rank);
+                cluster_sync_converged();
+                stat_merge(st, ex, parity, k, p.scale);
+            }
+            st.correct(p.scale);
             parity ^= 1u;
             const float s1 = TWO ? st.s2 : st.s;  // at T = 1 they are the same; without w_ce it is not used
             if (rank == 0 && warp == 0 && !pos.aborted) {
@@ -150,18 +160,12 @@ __global__ void __launch_bounds__(kStreamBlock, 3) distill_kernel(const DistillP
                 const float at = st.s == 0.f ? 0.f : wt * teach.total / st.s;
                 const float a1 = p.ce_w != 0.f && s1 != 0.f ? w1 / s1 : 0.f;
                 const float a = TWO ? at : at + a1;
-                const f32x2_t M = f2_pack(-st.m, -st.m), C = f2_pack(p.c, p.c), L = f2_pack(kLog2e, kLog2e);
+                const f32x2_t M = f2_pack(-st.m, -st.m), C = f2_pack(p.scale.c, p.scale.c), L = f2_pack(kLog2e, kLog2e);
                 const f32x2_t A = f2_pack(a, a), A1 = f2_pack(a1, a1);
                 for (int c0 = 0; c0 < s.nv; c0 += kStreamChunk) {
                     const int nl = min(kStreamChunk, s.nv - c0);
                     uint4 v[kBlockVec];
-                    stream_chunk(p.src, bars, smem, pos, [&](const unsigned char* stage) {
-#pragma unroll
-                        for (int i = 0; i < kBlockVec; ++i) {
-                            const int lv = tid + i * kStreamThreads;
-                            v[i] = lv < nl ? reinterpret_cast<const uint4*>(stage)[lv] : RowMath<ES>::pad();
-                        }
-                    });
+                    stream_chunk(p.src, bars, smem, pos, [&](const unsigned char* stage) { load_strided<ES>(stage, nl, v); });
                     if (pos.aborted) continue;
 #pragma unroll
                     for (int i = 0; i < kBlockVec; ++i) {
@@ -186,7 +190,7 @@ __global__ void __launch_bounds__(kStreamBlock, 3) distill_kernel(const DistillP
                 }
                 auto grad_at = [&](float x) {
                     const float d = x - st.m;
-                    float e = ex2(d * p.c) * a;
+                    float e = ex2(d * p.scale.c) * a;
                     if (TWO) e = fmaf(ex2(d * kLog2e), a1, e);
                     return e;
                 };
@@ -224,8 +228,9 @@ cudaError_t launch_typed(DistillParams prm, cudaStream_t stream) {
     StreamSrc& s = prm.src;
     const int sms = device_sm_count();
     const int64_t nb = s.V * ES / 16 + 1;
-    s.k = kStreamMaxCluster;
-    while (s.k > 1 && (s.N * s.k > sms || 2 * nb < static_cast<int64_t>(s.k) * kStreamChunk)) s.k /= 2;
+    int k = kStreamMaxCluster;
+    while (k > 1 && (s.N * k > sms || 2 * nb < static_cast<int64_t>(k) * kStreamChunk)) k /= 2;
+    set_cluster(s, k);
     const size_t fixed = 1024 + sizeof(StreamBars) + sizeof(StatExchange) + sizeof(TeacherRow) + 512;
     const int per_sm = 3;
     const size_t room = (228 * 1024) / per_sm - fixed;
@@ -296,7 +301,7 @@ cudaError_t launch_distill(bool grad, int es, const void* x, void* dx, int64_t l
     p.ce_w = ce_w;
     p.kd_w = kd_w;
     p.inv_t = 1.f / temperature;
-    p.c = kLog2e / temperature;
+    p.scale = exp_scale(temperature);
     p.g = g;
     p.row_ce = row_ce;
     p.row_kd = row_kd;

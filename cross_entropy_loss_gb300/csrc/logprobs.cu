@@ -38,7 +38,7 @@ constexpr int kSelCap = 256;    // blocks they are taken from
 struct LogprobParams {
     StreamSrc src;
     float inv_t;       // 1 / T
-    float c;           // log2(e) / T
+    ExpScale scale;
     int top_k;
     float* logp;       // [N] or null
     float* entropy;    // [N] or null
@@ -95,6 +95,21 @@ __device__ __forceinline__ int consumers_count(int n, TopScratch& t, uint32_t& t
 #pragma unroll
     for (int w = 0; w < kStreamWarps; ++w) s += t.count[b][w];
     return s;
+}
+
+// Places for n entries of each lane in a list whose length is *len: one atomic a warp.
+// Returns the lane's first place.
+__device__ __forceinline__ int warp_places(int n, int* len) {
+    const int lane = threadIdx.x & 31;
+    int sum = n;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, sum, off);
+        if (lane >= off) sum += o;
+    }
+    int base = 0;
+    if (lane == 31 && sum) base = atomicAdd(len, sum);
+    return __shfl_sync(0xffffffffu, base, 31) + sum - n;
 }
 
 // Block `id` of the slice: 0 the head scalars, 1 .. nblk the body's blocks, nblk + 1 the tail scalars.
@@ -278,10 +293,14 @@ __device__ __forceinline__ int top_list(const Slice& s, const typename BlockKey<
             }
         }
     }
-    for (int b = 1 + tid; b <= nblk; b += kStreamThreads) {
-        if (keys[b] >= lo) {
-            const int i = atomicAdd(&t.n_sel, 1);
-            if (i < kSelCap) t.sel[i] = b;
+    for (int b0 = 1; b0 <= nblk; b0 += 32 * kStreamThreads) {
+        uint32_t hit = 0;
+        for (int j = 0, b = b0 + tid; j < 32 && b <= nblk; ++j, b += kStreamThreads)
+            hit |= static_cast<uint32_t>(keys[b] >= lo) << j;
+        if (__any_sync(0xffffffffu, hit != 0)) {
+            int at = warp_places(__popc(hit), &t.n_sel);
+            for (; hit; hit &= hit - 1, ++at)
+                if (at < kSelCap) t.sel[at] = b0 + tid + (__ffs(hit) - 1) * kStreamThreads;
         }
     }
     consumers_sync();
@@ -323,41 +342,52 @@ __device__ __forceinline__ int top_list(const Slice& s, const typename BlockKey<
         // Four threads a block, one vector each (re-read from L2); the elements at or above the threshold.
         const float floor = lo == 1 ? kNegInf : BK::value(lo);
         const uint4* body = reinterpret_cast<const uint4*>(s.body);
-        for (int i0 = 0; i0 < n_sel * kBlockVec; i0 += kStreamThreads) {
-            const int i = i0 + tid, j = i / kBlockVec;
-            const int vec = j < n_sel ? (t.sel[j] - 1) * kBlockVec + (i & (kBlockVec - 1)) : s.nv;
-            uint4 w = RowMath<ES>::pad();
-            const bool real = vec < s.nv;
-            if (real) w = ld_global_v4(body + vec);
-            float f[EPV];
-            int ties = 0;
-            bool any = false;
+        constexpr int TURNS = kSelCap * kBlockVec / kStreamThreads;
+        uint4 w[TURNS];
+        int vec[TURNS];
 #pragma unroll
-            for (int e = 0; e < EPV / 2; ++e) f2_unpack(vec_pair<ES>(w, e), f[2 * e], f[2 * e + 1]);
+        for (int q = 0; q < TURNS; ++q) {  // every turn's load goes out before the first is looked at
+            const int j = (q * kStreamThreads + tid) / kBlockVec;
+            vec[q] = j < n_sel ? (t.sel[j] - 1) * kBlockVec + (tid & (kBlockVec - 1)) : s.nv;
+            w[q] = RowMath<ES>::pad();
+            if (vec[q] < s.nv) w[q] = ld_global_v4(body + vec[q]);
+        }
 #pragma unroll
-            for (int e = 0; e < EPV; ++e) {
-                any |= f[e] >= floor;
-                ties += f[e] == floor;
+        for (int q = 0; q < TURNS; ++q) {
+            if (q * kStreamThreads >= n_sel * kBlockVec) break;
+            uint32_t hit = 0, tie = 0;
+#pragma unroll
+            for (int e = 0; e < EPV / 2; ++e) {
+                float lo2, hi2;
+                f2_unpack(vec_pair<ES>(w[q], e), lo2, hi2);
+                hit |= static_cast<uint32_t>(lo2 >= floor) << 2 * e | static_cast<uint32_t>(hi2 >= floor) << (2 * e + 1);
+                tie |= static_cast<uint32_t>(lo2 == floor) << 2 * e | static_cast<uint32_t>(hi2 == floor) << (2 * e + 1);
             }
-            if (!real) ties = 0;
-            int before = 0;  // ties of the same block in earlier vectors
+            if (vec[q] >= s.nv) hit = tie = 0;
             if (strict != 0x7fffffff) {
-                int sum = ties;
+                // an equal one counts only if fewer than `need` come before it: those of its block's
+                // earlier vectors, and one at least in each tied block before
+                int sum = __popc(tie);
 #pragma unroll
                 for (int off = 1; off < kBlockVec; off <<= 1) {
                     const int o = __shfl_up_sync(0xffffffffu, sum, off, kBlockVec);
                     if ((tid & (kBlockVec - 1)) >= off) sum += o;
                 }
-                before = sum - ties + max(0, j - strict);  // and one at least in each tied block before
+                int room = need - (sum - __popc(tie)) - max(0, (q * kStreamThreads + tid) / kBlockVec - strict);
+                for (uint32_t m = tie; m; m &= m - 1)
+                    if (--room < 0) hit &= ~(m & -m);
             }
-            if (real && any) {
+            if (__any_sync(0xffffffffu, hit != 0)) {
+                int at = warp_places(__popc(hit), &t.n_list);
+                const uint32_t col = static_cast<uint32_t>(s.col0) + static_cast<uint32_t>(vec[q]) * EPV;
 #pragma unroll
                 for (int e = 0; e < EPV; ++e) {
-                    if (!(f[e] >= floor)) continue;
-                    if (f[e] == floor && before++ >= need) continue;  // enough equal ones come before it
-                    const int at = atomicAdd(&t.n_list, 1);
-                    const uint32_t col = static_cast<uint32_t>(s.col0 + static_cast<int64_t>(vec) * EPV + e);
-                    if (at < kListCap) t.list[at] = (static_cast<unsigned long long>(key_of(f[e])) << 32) | ~col;
+                    if (!(hit >> e & 1u)) continue;
+                    float lo2, hi2;
+                    f2_unpack(vec_pair<ES>(w[q], e / 2), lo2, hi2);
+                    const uint32_t key = key_of(e & 1 ? hi2 : lo2);
+                    if (at < kListCap) t.list[at] = (static_cast<unsigned long long>(key) << 32) | ~(col + e);
+                    ++at;
                 }
             }
         }
@@ -383,6 +413,7 @@ __global__ void __launch_bounds__(kStreamBlock, 3) logprobs_kernel(const Logprob
     __shared__ StreamBars bars;
     __shared__ StatExchange ex;
     __shared__ TopScratch top;
+    __shared__ float4 fin;
     using KeyT = typename BlockKey<ES>::type;
     unsigned char* ring = smem;
     KeyT* keys = reinterpret_cast<KeyT*>(smem + p.src.stages * kStreamStageBytes);
@@ -402,6 +433,7 @@ __global__ void __launch_bounds__(kStreamBlock, 3) logprobs_kernel(const Logprob
         stream_produce<ES>(p.src, bars, ring, 1, cid, ncl, rank, k > 1 ? (TOPK ? 3 : 1) : 0);
     } else {
         StreamPos pos{0, 0, false};
+        Slice s = slice_of<ES>(p.src, cid, rank);
         uint32_t parity = 0;
         int64_t y_next = p.src.labels && n_it > 0 ? __ldg(p.src.labels + cid) : 0;
         for (int64_t it = 0; it < n_it; ++it) {
@@ -426,61 +458,79 @@ __global__ void __launch_bounds__(kStreamBlock, 3) logprobs_kernel(const Logprob
                 }
                 continue;
             }
-            const Slice s = slice_of<ES>(p.src, row, rank);
+            move_slice<ES>(p.src, row, rank, s);
             float x_y = 0.f;
             if (tid == 0 && rank == 0 && p.logp) x_y = load_scalar<ES>(s.rowp + y * ES);
-            RunStat<ENT, false> st;
+            RunStat<ENT, false> st(p.scale);
             float most = kNegInf;  // of the thread's blocks
             for (int c0 = 0; c0 < s.nv; c0 += kStreamChunk) {
                 const int nl = min(kStreamChunk, s.nv - c0);
                 uint4 v[kBlockVec];
-                stream_chunk(p.src, bars, ring, pos, [&](const unsigned char* stage) { load_block<ES>(stage, nl, v); });
-                const float bmax = vec_max<ES>(v);
+                stream_chunk(p.src, bars, ring, pos, [&](const unsigned char* stage) {
+                    if constexpr (TOPK) load_block<ES>(stage, nl, v);
+                    else load_strided<ES>(stage, nl, v);
+                });
+                const float bmax = st.template add_vecs<ES>(v, p.scale);
                 if (TOPK) {
                     if (tid * kBlockVec < nl) keys[1 + c0 / kBlockVec + tid] = static_cast<KeyT>(BlockKey<ES>::of(bmax));
                     most = fmaxf(most, bmax);
                 }
-                st.template add_vecs<ES>(v, bmax, p.c, 0.f);
             }
-            if (tid == 0 || tid == 32) {  // the head's and the tail's scalars
-                const int n = tid == 0 ? s.h : s.t;
-                const int64_t col = tid == 0 ? 0 : s.tail_col;
-                float m = kNegInf;
-                for (int e = 0; e < n; ++e) {
-                    const float x = load_scalar<ES>(s.rowp + (col + e) * ES);
-                    st.add(x, p.c, 0.f);
-                    m = fmaxf(m, x);
+            if (s.h + s.t > 0 && tid < 32) {  // the head's and the tail's scalars, one a lane
+                float e = kNegInf;
+                if (tid < s.h + s.t) e = load_scalar<ES>(s.rowp + (tid < s.h ? tid : s.tail_col + (tid - s.h)) * ES);
+                st.add(e, p.scale);
+                if (TOPK) {
+                    const float hm = warp_max_redux(tid < s.h ? e : kNegInf), tm = warp_max_redux(tid < s.h ? kNegInf : e);
+                    if (tid == 0) {
+                        keys[0] = s.h > 0 ? BlockKey<ES>::of(hm) : 0;
+                        keys[1 + (s.nv + kBlockVec - 1) / kBlockVec] = s.t > 0 ? BlockKey<ES>::of(tm) : 0;
+                    }
                 }
-                if (TOPK) keys[tid == 0 ? 0 : 1 + (s.nv + kBlockVec - 1) / kBlockVec] = n > 0 ? BlockKey<ES>::of(m) : 0;
+            } else if (TOPK && tid == 0) {
+                keys[0] = keys[1 + (s.nv + kBlockVec - 1) / kBlockVec] = 0;
             }
             if (TOPK) {
                 top.thread_max[tid] = tid * kBlockVec < s.nv ? BlockKey<ES>::of(most) : 0u;
                 if (tid == 0) top.n_sel = top.n_list = 0;
             }
-            stat_reduce(st, ex, parity, k, rank, p.c, 0.f);
+            stat_publish(st, ex, parity);
+            consumers_sync();
+            if (tid < 32) stat_collect(st, ex, parity, p.scale);
+            if (k > 1) {
+                if (tid < 32) stat_send(st, ex, parity, k, rank);
+                cluster_sync_converged();
+                if (tid < 32) stat_merge(st, ex, parity, k, p.scale);
+            }
             parity ^= 1u;
-            const float ln_s = logf(st.s);
-            const bool empty = st.s == 0.f;
-            const float lse = empty ? kNegInf : fmaf(st.m, p.inv_t, ln_s);
-            if (tid == 0 && rank == 0 && !pos.aborted) {
-                if (p.logp) p.logp[row] = empty ? kNegInf : (x_y - st.m) * p.inv_t - ln_s;
-                if (ENT) {
-                    const float h = ln_s - st.a * kLn2 / st.s;
-                    p.entropy[row] = empty || h < 0.f ? 0.f : h;
+            if (tid < 32) {  // the row's results; the rest of the CTA goes on to the top tokens
+                st.correct(p.scale);
+                const float ln_s = logf(st.s);
+                const bool empty = st.s == 0.f;
+                if (tid == 0) {
+                    if (TOPK) fin = make_float4(st.m, ln_s, st.s, 0.f);
+                    if (rank == 0 && !pos.aborted) {
+                        if (p.logp) p.logp[row] = empty ? kNegInf : (x_y - st.m) * p.inv_t - ln_s;
+                        if (ENT) {
+                            const float h = ln_s - st.a * kLn2 / st.s;
+                            p.entropy[row] = empty || h < 0.f ? 0.f : h;
+                        }
+                        if (p.lse) p.lse[row] = empty ? kNegInf : fmaf(st.m, p.inv_t, ln_s);
+                        if (p.stats) p.stats[row] = make_float2(empty ? kNegInf : st.m, ln_s);
+                    }
                 }
-                if (p.lse) p.lse[row] = lse;
-                if (p.stats) p.stats[row] = make_float2(empty ? kNegInf : st.m, ln_s);
             }
             if constexpr (TOPK) {
                 const int K = p.top_k;
-                const bool none = !(st.s == st.s);  // a NaN or +inf in the row: no order to speak of
-                int n = 0;
-                if (!none) n = top_list<ES>(s, keys, K, top);
+                const int n = top_list<ES>(s, keys, K, top);
+                const float4 f = fin;  // (m, ln S, S): written before the barriers of top_list
+                const bool none = !(f.z == f.z);  // a NaN or +inf in the row: no order to speak of
+                const bool empty = f.z == 0.f;
                 float* olp = p.top_lp + row * K;
                 int32_t* oid = p.top_ids + row * K;
                 auto write = [&](int r, unsigned long long item) {
-                    if (pos.aborted) return;
-                    olp[r] = empty ? kNegInf : (float_of_key(static_cast<uint32_t>(item >> 32)) - st.m) * p.inv_t - ln_s;
+                    if (pos.aborted || none) return;
+                    olp[r] = empty ? kNegInf : (float_of_key(static_cast<uint32_t>(item >> 32)) - f.x) * p.inv_t - f.y;
                     oid[r] = static_cast<int32_t>(~static_cast<uint32_t>(item));
                 };
                 // Ranks within this CTA's list: `ways` neighbouring threads an item, each comparing it with
@@ -511,14 +561,14 @@ __global__ void __launch_bounds__(kStreamBlock, 3) logprobs_kernel(const Logprob
                     // one thread an item and list.  They are copied here first when there is room.
                     cluster_sync_converged();  // every CTA's best are in place
                     const bool copy = K * k <= kListCap;
-                    if (copy && !none) {
+                    if (copy) {
                         for (int i = tid; i < K * k; i += kStreamThreads) {
                             const uint32_t from = mapa_u32(top.best, static_cast<uint32_t>(i / K)) + (i % K) * 8;
                             asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(top.list[i]) : "r"(from) : "memory");
                         }
                     }
                     consumers_sync();
-                    for (int i0 = 0; !none && i0 < K * k; i0 += kStreamThreads) {
+                    for (int i0 = 0; i0 < K * k; i0 += kStreamThreads) {
                         const int i = i0 + tid;
                         const int o = i & (k - 1);
                         const unsigned long long item = i < K * k ? top.best[i / k] : 0ull;
@@ -540,7 +590,7 @@ __global__ void __launch_bounds__(kStreamBlock, 3) logprobs_kernel(const Logprob
                 }
                 if (none && rank == 0) {
                     for (int i = tid; i < K; i += kStreamThreads) {
-                        olp[i] = st.s;
+                        olp[i] = f.z;
                         oid[i] = -1;
                     }
                 }
@@ -579,8 +629,9 @@ cudaError_t launch_typed(LogprobParams prm, cudaStream_t stream) {
     const int64_t nb = s.V * ES / 16 + 1;
     // Few rows: a cluster per row, as long as its CTAs are all on SMs of their own and
     // have at least half a chunk each.
-    s.k = kStreamMaxCluster;
-    while (s.k > 1 && (s.N * s.k > sms || 2 * nb < static_cast<int64_t>(s.k) * kStreamChunk)) s.k /= 2;
+    int k = kStreamMaxCluster;
+    while (k > 1 && (s.N * k > sms || 2 * nb < static_cast<int64_t>(k) * kStreamChunk)) k /= 2;
+    set_cluster(s, k);
     const int64_t nblk = ((nb + kBlockVec - 1) / kBlockVec + s.k - 1) / s.k + 3;
     const size_t key_bytes = TOPK ? (static_cast<size_t>(nblk) * sizeof(typename BlockKey<ES>::type) + 127) / 128 * 128 : 0;
     // Three CTAs an SM when each gets a ring of three stages, else two.
@@ -633,7 +684,7 @@ cudaError_t launch_logprobs(int es, const void* x, int64_t ld, const int64_t* la
     p.src.wait_ns = test_wait_limit_ns();
     p.src.skip_load_row = test_skip_load_row();
     p.inv_t = 1.f / temperature;
-    p.c = kLog2e / temperature;
+    p.scale = exp_scale(temperature);
     p.top_k = top_k;
     p.logp = logp;
     p.entropy = entropy;

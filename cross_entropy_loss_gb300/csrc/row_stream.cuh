@@ -8,11 +8,14 @@
 // runs ahead of the consumers over the row's end, so the copies of the next row are in
 // flight while the consumers finish this one.
 //
-// Each thread keeps a running (max, sum exp, sum d exp) over the elements it has seen
-// (d the exponent), rescaled when a new maximum arrives; the threads' triples meet
-// once a row.  Exponents are formed as (x - max) * c, never as x * c - max * c: at
-// logits of the type's lowest value the products would overflow and their difference
-// would be NaN, and the subtraction is exact where it matters (x near max).
+// Each thread keeps running sums (of 2^d and d 2^d) below a maximum that its warp shares:
+// one warp-wide reduction a chunk, and a rescaling only when the warp meets a new maximum
+// (rarer and rarer along a row); the warps' sets meet once a row.  The exponent is
+// one FMA, d = x c + r with r = -max c rounded once: the sums are then exact for that r,
+// and the row's end corrects for its rounding (max c + r, which an FMA gives exactly).
+// The rounding of r is an exponent of 64 at most while |max c| < 2^30.  Above that two
+// different float32 logits are at least 2^6 apart in the exponent, so an element that is
+// not the maximum counts nothing and no exponent is formed.
 #pragma once
 
 #include <float.h>
@@ -33,6 +36,7 @@ constexpr uint32_t kStreamStageBytes = kStreamChunk * 16;
 constexpr int kStreamMaxStages = 12;
 constexpr int kStreamMaxCluster = 8;
 constexpr float kMinExp2 = -16384.f;  // 2^x is 0 from far above this; keeps products with it finite
+constexpr float kFarExp = 1073741824.f;  // 2^30: max c past which two logits differ by an exponent of 64 at least
 
 struct StreamSrc {
     const char* x;
@@ -41,7 +45,7 @@ struct StreamSrc {
     int64_t N, V, ignore_index;
     uint64_t wait_ns;       // limit of every shared-memory barrier wait
     int64_t skip_load_row;  // test hook: this row's first chunk is never loaded (-1: none)
-    int k;                  // CTAs of a row's cluster
+    int k, log2_k;          // CTAs of a row's cluster
     int stages;
 };
 
@@ -67,6 +71,12 @@ __device__ __forceinline__ void cluster_sync_converged() {
     cluster_sync();
 }
 
+// Launch the work of a cluster size that is a power of two.
+inline void set_cluster(StreamSrc& p, int k) {
+    p.k = k;
+    for (p.log2_k = 0; (1 << p.log2_k) < k;) ++p.log2_k;
+}
+
 __device__ __forceinline__ bool stream_row_valid(int64_t y, const StreamSrc& p) {
     return !p.labels || (y != p.ignore_index && y >= 0 && y < p.V);
 }
@@ -89,7 +99,7 @@ __device__ __forceinline__ Slice slice_of(const StreamSrc& p, int64_t row, int r
     s.rowp = p.x + row * p.ld * ES;
     const RowGeom g = row_geom<ES>(s.rowp, p.V);
     const int nb = static_cast<int>(g.nb);
-    const int per = ((nb + kBlockVec - 1) / kBlockVec + p.k - 1) / p.k * kBlockVec;
+    const int per = (((nb + kBlockVec - 1) / kBlockVec + p.k - 1) >> p.log2_k) * kBlockVec;
     const int v0 = min(nb, rank * per), v1 = min(nb, v0 + per);
     s.h = rank == 0 ? g.h : 0;
     s.t = rank == p.k - 1 ? g.t : 0;
@@ -98,6 +108,17 @@ __device__ __forceinline__ Slice slice_of(const StreamSrc& p, int64_t row, int r
     s.body = s.rowp + s.col0 * ES;
     s.tail_col = g.h + static_cast<int64_t>(nb) * EPV;
     return s;
+}
+// The slice of another row, from one whose row starts at the same offset modulo 16 bytes
+// (every row does when the row stride is a multiple of 16 bytes).
+template <int ES>
+__device__ __forceinline__ void move_slice(const StreamSrc& p, int64_t row, int rank, Slice& s) {
+    if ((p.ld * ES & 15) == 0) {
+        s.rowp = p.x + row * p.ld * ES;
+        s.body = s.rowp + s.col0 * ES;
+    } else {
+        s = slice_of<ES>(p, row, rank);
+    }
 }
 
 struct StreamBars {
@@ -144,6 +165,7 @@ __device__ __forceinline__ void stream_produce(const StreamSrc& p, StreamBars& b
     const int lane = threadIdx.x & 31;
     const int64_t n_it = p.N > cid ? (p.N - 1 - cid) / ncl + 1 : 0;
     const uint32_t S = static_cast<uint32_t>(p.stages);
+    Slice s = slice_of<ES>(p, cid, rank);
     uint32_t st = 0, par = 0;  // the next stage, and the parity of its use
     bool wrapped = false, stop = false;
     uint32_t armed = 0;  // stages whose last copy was issued
@@ -157,7 +179,7 @@ __device__ __forceinline__ void stream_produce(const StreamSrc& p, StreamBars& b
             if (!stream_row_valid(y, p)) continue;
             const int64_t row = cid + (base + j) * ncl;
             if (lane == 0 && !stop) {
-                const Slice s = slice_of<ES>(p, row, rank);
+                move_slice<ES>(p, row, rank, s);
                 for (int pass = 0; pass < passes && !stop; ++pass) {
                     for (int c0 = 0; c0 < s.nv; c0 += kStreamChunk) {
                         if (wrapped && !stream_wait(bars, &bars.empty[st], par ^ 1u, p.wait_ns)) stop = true;
@@ -223,12 +245,28 @@ __device__ __forceinline__ void stream_chunk(const StreamSrc& p, StreamBars& bar
 // 128-byte shared-memory access touch all 32 banks; v is left in that turned order.
 template <int ES>
 __device__ __forceinline__ void load_block(const unsigned char* stage, int nl, uint4 (&v)[kBlockVec]) {
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, turn = tid >> 1 & (kBlockVec - 1);
     const uint4* sb = reinterpret_cast<const uint4*>(stage) + tid * kBlockVec;
+    if (nl == kStreamChunk) {
 #pragma unroll
-    for (int i = 0; i < kBlockVec; ++i) {
-        const int j = (i + (tid >> 1)) & (kBlockVec - 1);
-        v[i] = tid * kBlockVec + j < nl ? sb[j] : RowMath<ES>::pad();
+        for (int i = 0; i < kBlockVec; ++i) v[i] = sb[i ^ turn];
+    } else {
+#pragma unroll
+        for (int i = 0; i < kBlockVec; ++i) v[i] = tid * kBlockVec + (i ^ turn) < nl ? sb[i ^ turn] : RowMath<ES>::pad();
+    }
+}
+// Four vectors of a chunk without a block's order: tid, tid + 256, ...
+template <int ES>
+__device__ __forceinline__ void load_strided(const unsigned char* stage, int nl, uint4 (&v)[kBlockVec]) {
+    const int tid = threadIdx.x;
+    const uint4* sb = reinterpret_cast<const uint4*>(stage) + tid;
+    if (nl == kStreamChunk) {
+#pragma unroll
+        for (int i = 0; i < kBlockVec; ++i) v[i] = sb[i * kStreamThreads];
+    } else {
+#pragma unroll
+        for (int i = 0; i < kBlockVec; ++i)
+            v[i] = tid + i * kStreamThreads < nl ? sb[i * kStreamThreads] : RowMath<ES>::pad();
     }
 }
 
@@ -240,86 +278,116 @@ __device__ __forceinline__ f32x2_t vec_pair(const uint4& v, int j) {
     else return f2_pack(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
 }
 
-// Maximum of the vectors' elements; NaN if one of them is.
-template <int ES, int NV>
-__device__ __forceinline__ float vec_max(const uint4 (&v)[NV]) {
-    if constexpr (ES == 2) {
-        uint32_t m = bf16x2_max_nan(bf16x2_max_nan(v[0].x, v[0].y), bf16x2_max_nan(v[0].z, v[0].w));
-#pragma unroll
-        for (int i = 1; i < NV; ++i)
-            m = bf16x2_max_nan(m, bf16x2_max_nan(bf16x2_max_nan(v[i].x, v[i].y), bf16x2_max_nan(v[i].z, v[i].w)));
-        return max_nan(bf16_lo(m), bf16_hi(m));
-    } else {
-        float m = kNegInf;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            m = max_nan(m, max_nan(max_nan(__uint_as_float(v[i].x), __uint_as_float(v[i].y)),
-                                   max_nan(__uint_as_float(v[i].z), __uint_as_float(v[i].w))));
-        return m;
-    }
+// Scales of the exponents: c = log2(e) / T, a second one for a second temperature, and the
+// value below which a logit's exponential is 0 whatever the maximum (see RunStat::far).
+struct ExpScale {
+    float c, c2, low;
+};
+__host__ __device__ __forceinline__ ExpScale exp_scale(float temperature) {
+    ExpScale s;
+    s.c = kLog2e / temperature;
+    s.c2 = kLog2e;
+    s.low = -4.f * kFarExp / s.c;
+    return s;
 }
 
-// Running softmax statistics of a set of elements: m the maximum (-FLT_MAX while no
-// element above -inf was seen), s = sum 2^d, a = sum 2^d d with d = (x - m) c, and
-// s2 = sum 2^((x - m) c2) for a second temperature.  NaN and +inf make s NaN.
+// Running softmax statistics.  m is the warp's maximum (-FLT_MAX while no element above
+// -inf was seen), s = sum 2^d, a = sum 2^d d the thread's sums, with d = x c + r, r = -m c,
+// and s2 = sum 2^(x c2 + r2) for a second temperature.  NaN and +inf make s NaN.
 template <bool ENT, bool TWO>
 struct RunStat {
-    float m = -FLT_MAX, s = 0.f, a = 0.f, s2 = 0.f;
+    float m = -FLT_MAX, r, r2, s = 0.f, a = 0.f, s2 = 0.f;
 
-    __device__ __forceinline__ void raise(float mn, float c, float c2) {
-        const float dm = max_nan((m - mn) * c, kMinExp2);
+    __device__ __forceinline__ explicit RunStat(const ExpScale& x) : r(FLT_MAX * x.c), r2(FLT_MAX * x.c2) {}
+
+    __device__ __forceinline__ bool far(const ExpScale& x) const { return far(m, x.c) || (TWO && far(m, x.c2)); }
+    static __device__ __forceinline__ bool far(float m, float c) { return fabsf(m) * c >= kFarExp && fabsf(m) <= FLT_MAX; }
+
+    // r has to be this rounded product wherever it is used: not to be contracted into an FMA
+    static __device__ __forceinline__ float minus_product(float m, float c) { return __fmul_rn(-m, c); }
+
+    // The same sums below a maximum mn >= m (fmaxf also turns a NaN into 2^-16384 = 0: it is in the sums).
+    __device__ __forceinline__ void raise(float mn, const ExpScale& x) {
+        const float rn = minus_product(mn, x.c);
+        const float dm = mn == m ? 0.f : far(mn, x.c) ? kMinExp2 : fmaxf(rn - r, kMinExp2);
         const float f = ex2(dm);
         if (ENT) a = f * fmaf(dm, s, a);
         s *= f;
-        if (TWO) s2 *= ex2(max_nan((m - mn) * c2, kMinExp2));
+        if (TWO) {
+            const float rn2 = minus_product(mn, x.c2);
+            s2 *= mn == m ? 1.f : far(mn, x.c2) ? 0.f : ex2(fmaxf(rn2 - r2, kMinExp2));
+            r2 = rn2;
+        }
         m = mn;
+        r = rn;
     }
-    __device__ __forceinline__ void merge(float m2, float sx, float ax, float s2x, float c, float c2) {
-        const float mn = max_nan(m, m2);
-        raise(mn, c, c2);
-        RunStat o;
-        o.m = m2;
-        o.s = sx;
-        o.a = ax;
-        o.s2 = s2x;
-        o.raise(mn, c, c2);
+    __device__ __forceinline__ void set(const float4& w, const ExpScale& x) {
+        m = w.x, s = w.y, a = w.z, s2 = w.w;
+        r = minus_product(m, x.c);
+        if (TWO) r2 = minus_product(m, x.c2);
+    }
+    __device__ __forceinline__ void merge(const float4& w, const ExpScale& x) {
+        RunStat o(x);
+        o.set(w, x);
+        const float mn = fmaxf(m, o.m);
+        raise(mn, x);
+        o.raise(mn, x);
         s += o.s;
         if (ENT) a += o.a;
         if (TWO) s2 += o.s2;
     }
-    __device__ __forceinline__ void add(float x, float c, float c2) {
-        if (x == kNegInf) return;
-        const float mn = max_nan(m, x);
-        if (!(mn == m)) raise(mn, c, c2);
-        const float d = max_nan((x - m) * c, kMinExp2);
+    // One element a lane (-inf: none), by the whole warp.
+    __device__ __forceinline__ void add(float v, const ExpScale& x) {
+        const float mn = fmaxf(m, warp_max_redux(v));
+        if (mn > m) raise(mn, x);
+        if (v == kNegInf) return;
+        if (far(x)) {
+            const float one = v == m ? 1.f : v == v ? 0.f : v;
+            s += one;
+            if (TWO) s2 += one;
+            return;
+        }
+        const float d = max_nan(fmaf(v, x.c, r), kMinExp2);
         const float e = ex2(d);
         s += e;
         if (ENT) a = fmaf(e, d, a);
-        if (TWO) s2 += ex2((x - m) * c2);
+        if (TWO) s2 += ex2(fmaf(v, x.c2, r2));
     }
-    // NV vectors whose maximum is bmax
+    // NV vectors a lane, by the whole warp; returns the maximum of the lane's (NaN aside).
     template <int ES, int NV>
-    __device__ __forceinline__ void add_vecs(const uint4 (&v)[NV], float bmax, float c, float c2) {
-        if (bmax == kNegInf) return;
-        const float mn = max_nan(m, bmax);
-        if (!(mn == m)) raise(mn, c, c2);
-        const f32x2_t M = f2_pack(-m, -m), C = f2_pack(c, c), C2 = f2_pack(c2, c2);
+    __device__ __forceinline__ float add_vecs(const uint4 (&v)[NV], const ExpScale& x) {
+        const float bmax = RowMath<ES>::template vmax<NV>(v);
+        const float mn = fmaxf(m, warp_max_redux(bmax));
+        if (mn > m) raise(mn, x);
+        if (far(x)) {
+            add_far<ES, NV>(v);
+            return bmax;
+        }
+        const f32x2_t C = f2_pack(x.c, x.c), R = f2_pack(r, r), C2 = f2_pack(x.c2, x.c2), R2 = f2_pack(r2, r2);
         f32x2_t ss[2] = {0, 0}, aa[2] = {0, 0}, tt[2] = {0, 0};
+        const uint32_t low2 = pack_bf16x2(x.low, x.low);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
+            uint4 w = v[i];
+            // -inf, and what is as far below, to where 2^d is 0 and d finite: 0 * -inf would be NaN
+            if (ENT && ES == 2) {
+                w.x = bf16x2_max_nan(w.x, low2), w.y = bf16x2_max_nan(w.y, low2);
+                w.z = bf16x2_max_nan(w.z, low2), w.w = bf16x2_max_nan(w.w, low2);
+            }
+            if (ENT && ES == 4) {
+                w.x = __float_as_uint(max_nan(__uint_as_float(w.x), x.low));
+                w.y = __float_as_uint(max_nan(__uint_as_float(w.y), x.low));
+                w.z = __float_as_uint(max_nan(__uint_as_float(w.z), x.low));
+                w.w = __float_as_uint(max_nan(__uint_as_float(w.w), x.low));
+            }
 #pragma unroll
             for (int j = 0; j < (ES == 2 ? 4 : 2); ++j) {
-                const f32x2_t x = f2_add(vec_pair<ES>(v[i], j), M);
-                float lo, hi;
-                f2_unpack(f2_mul(x, C), lo, hi);
-                if (ENT) {
-                    lo = max_nan(lo, kMinExp2);  // 2^-inf * -inf would be NaN
-                    hi = max_nan(hi, kMinExp2);
-                }
-                const f32x2_t e = f2_pack(ex2(lo), ex2(hi));
-                ss[j & 1] = f2_add(ss[j & 1], e);
-                if (ENT) aa[j & 1] = f2_fma(e, f2_pack(lo, hi), aa[j & 1]);
-                if (TWO) tt[j & 1] = f2_add(tt[j & 1], f2_ex2(f2_mul(x, C2)));
+                const f32x2_t e = vec_pair<ES>(w, j);
+                const f32x2_t d = f2_fma(e, C, R);
+                const f32x2_t p = f2_ex2(d);
+                ss[j & 1] = f2_add(ss[j & 1], p);
+                if (ENT) aa[j & 1] = f2_fma(p, d, aa[j & 1]);
+                if (TWO) tt[j & 1] = f2_add(tt[j & 1], f2_ex2(f2_fma(e, C2, R2)));
             }
         }
         float lo, hi;
@@ -333,59 +401,77 @@ struct RunStat {
             f2_unpack(f2_add(tt[0], tt[1]), lo, hi);
             s2 += lo + hi;
         }
+        return bmax;
     }
-    // all 32 lanes' sets as one; every lane gets it
-    __device__ __forceinline__ void warp_merge(float c, float c2) {
-        const float M = warp_max(m);  // drops NaN; the sums below keep it
-        raise(M, c, c2);
-        s = warp_sum(s);
-        if (ENT) a = warp_sum(a);
-        if (TWO) s2 = warp_sum(s2);
+    // the elements equal to a far maximum
+    template <int ES, int NV>
+    __device__ __forceinline__ void add_far(const uint4 (&v)[NV]) {
+        float n = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+#pragma unroll
+            for (int j = 0; j < (ES == 2 ? 4 : 2); ++j) {
+                float lo, hi;
+                f2_unpack(vec_pair<ES>(v[i], j), lo, hi);
+                n += lo == m ? 1.f : lo == lo ? 0.f : lo;
+                n += hi == m ? 1.f : hi == hi ? 0.f : hi;
+            }
+        }
+        s += n;
+        if (TWO) s2 += n;
+    }
+    // The sums as those of exponents (x - m) c, for an r that is m c exactly.
+    __device__ __forceinline__ void correct(const ExpScale& x) {
+        if (far(x)) return;
+        const float e = fmaf(m, x.c, r), f = ex2(-e);
+        if (ENT) a = f * fmaf(-e, s, a);
+        s *= f;
+        if (TWO) s2 *= ex2(-fmaf(m, x.c2, r2));
     }
 };
 
 // Shared memory through which the consumers' (and the cluster's) sets meet.
 struct StatExchange {
-    float4 warp[2][kStreamWarps];           // (m, s, a, s2), by row parity
-    float4 cta[2][kStreamMaxCluster];       // the cluster's CTAs' sets, by row parity
+    float4 warp[2][kStreamWarps];      // (m, s, a, s2), by row parity
+    float4 cta[2][kStreamMaxCluster];  // the cluster's CTAs' sets, by row parity
 };
 
-// Every consumer thread's set as the row's.  One consumer barrier, and with a cluster
-// one cluster barrier.
+// Every warp's set put into the exchange; a consumer barrier has to follow.
 template <bool ENT, bool TWO>
-__device__ __forceinline__ void stat_reduce(RunStat<ENT, TWO>& st, StatExchange& ex, uint32_t parity, int k, int rank,
-                                            float c, float c2) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    st.warp_merge(c, c2);
-    if (lane == 0) ex.warp[parity][warp] = make_float4(st.m, st.s, st.a, st.s2);
-    consumers_sync();
-    float4 w = ex.warp[parity][lane & (kStreamWarps - 1)];
-    st.m = w.x, st.s = w.y, st.a = w.z, st.s2 = w.w;
-    float M = st.m;
-#pragma unroll
-    for (int off = kStreamWarps / 2; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    st.raise(M, c, c2);
+__device__ __forceinline__ void stat_publish(RunStat<ENT, TWO>& st, StatExchange& ex, uint32_t parity) {
+    st.s = warp_sum(st.s);
+    if (ENT) st.a = warp_sum(st.a);
+    if (TWO) st.s2 = warp_sum(st.s2);
+    if ((threadIdx.x & 31) == 0) ex.warp[parity][threadIdx.x >> 5] = make_float4(st.m, st.s, st.a, st.s2);
+}
+// The CTA's set from its warps', by whole warps; every lane gets it.
+template <bool ENT, bool TWO>
+__device__ __forceinline__ void stat_collect(RunStat<ENT, TWO>& st, const StatExchange& ex, uint32_t parity,
+                                             const ExpScale& x) {
+    st.set(ex.warp[parity][threadIdx.x & (kStreamWarps - 1)], x);
+    st.raise(warp_max_redux(st.m), x);
 #pragma unroll
     for (int off = kStreamWarps / 2; off > 0; off >>= 1) {
         st.s += __shfl_xor_sync(0xffffffffu, st.s, off);
         if (ENT) st.a += __shfl_xor_sync(0xffffffffu, st.a, off);
         if (TWO) st.s2 += __shfl_xor_sync(0xffffffffu, st.s2, off);
     }
-    if (k > 1) {
-        if (threadIdx.x < static_cast<unsigned>(k)) {
-            const uint32_t to = mapa_u32(&ex.cta[parity][rank], threadIdx.x);
-            asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(st.m), "f"(st.s), "f"(st.a),
-                         "f"(st.s2)
-                         : "memory");
-        }
-        cluster_sync_converged();
-        w = ex.cta[parity][0];
-        st.m = w.x, st.s = w.y, st.a = w.z, st.s2 = w.w;
-        for (int r = 1; r < k; ++r) {
-            w = ex.cta[parity][r];
-            st.merge(w.x, w.y, w.z, w.w, c, c2);
-        }
+}
+// In a cluster: the CTA's set to every CTA (by warp 0), then, after a cluster barrier, the row's from all.
+template <bool ENT, bool TWO>
+__device__ __forceinline__ void stat_send(const RunStat<ENT, TWO>& st, StatExchange& ex, uint32_t parity, int k, int rank) {
+    if (threadIdx.x < static_cast<unsigned>(k)) {
+        const uint32_t to = mapa_u32(&ex.cta[parity][rank], threadIdx.x);
+        asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(st.m), "f"(st.s), "f"(st.a),
+                     "f"(st.s2)
+                     : "memory");
     }
+}
+template <bool ENT, bool TWO>
+__device__ __forceinline__ void stat_merge(RunStat<ENT, TWO>& st, const StatExchange& ex, uint32_t parity, int k,
+                                           const ExpScale& x) {
+    st.set(ex.cta[parity][0], x);
+    for (int o = 1; o < k; ++o) st.merge(ex.cta[parity][o], x);
 }
 
 // Number of valid labels, counted by the consumer threads; scratch: kStreamWarps ints.
