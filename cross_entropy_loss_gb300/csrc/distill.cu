@@ -8,9 +8,9 @@
 //
 // The gradient is the softmax of the whole row times a constant, except at K + 1 places.
 // So the kernel is a row kernel with two sweeps -- sums, then gradient -- whose second
-// one writes a1 e^{x - m} + aT e^{(x - m) / T} everywhere, after which the K + 1 places
-// are overwritten (after a barrier, from logits kept when the row began, so that the
-// gradient may replace the logits).  The second sweep re-reads the row from L2: HBM sees
+// one writes a1 e^{x - m} + aT e^{(x - m) / T} everywhere, after which the closing warp
+// overwrites the K + 1 places (from logits fetched before the sweep began, so that the
+// gradient may replace the logits) while the others are on the next row.  The second sweep re-reads the row from L2: HBM sees
 // each logit read once and written once.  T = 1, or no cross-entropy part, needs one
 // exponential an element; otherwise there are two sums and two exponentials.
 #include <algorithm>
@@ -38,6 +38,11 @@ struct DistillParams {
     float4* stats;     // [N] or null: (m, ln sum e^(x-m), ln sum e^((x-m)/T), Q)
 };
 
+// What the second sweep takes from the closing warp: the maximum, and the factors of the two exponentials.
+struct SweepFactors {
+    float m, a, a1;
+};
+
 template <int ES, bool GRAD, bool TWO>
 __global__ void __launch_bounds__(kStreamBlock, 3) distill_kernel(const DistillParams p) {
     constexpr int EPV = 16 / ES;
@@ -45,51 +50,42 @@ __global__ void __launch_bounds__(kStreamBlock, 3) distill_kernel(const DistillP
     __shared__ StreamBars bars;
     __shared__ StatExchange ex;
     __shared__ TeacherRow teach;
-    __shared__ float s_xy;
+    __shared__ SweepFactors factors[kMaxBuffers];
     __shared__ int s_count[kStreamWarps];
-    __shared__ int s_last;
+    __shared__ int s_valid, s_bad, s_last;
     __shared__ DFloat dred[kStreamBlock / 32];
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = p.src.k;
     const int rank = k > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-    const int64_t cid = blockIdx.x / k, ncl = gridDim.x / k;
+    const int64_t cid = blockIdx.x >> p.src.log2_k, ncl = gridDim.x >> p.src.log2_k;
     const int64_t n_it = p.src.N > cid ? (p.src.N - 1 - cid) / ncl + 1 : 0;
-    stream_init(bars, p.src.stages);
+    stream_init(bars, p.src.stages, k);
     griddep_launch_dependents();  // programmatic dependent launch: no global access before the wait
     griddep_wait();
     __syncthreads();
-    if (k > 1) cluster_sync();
+    if (k > 1) cluster_sync();  // every CTA's shared memory is there to be written to
 
-    int n_valid = 0, n_bad = 0;
-    bool aborted = false;
-    if (tid >= kStreamThreads) {
-        stream_produce<ES>(p.src, bars, smem, GRAD ? 2 : 1, cid, ncl, rank, k > 1 ? 1 : 0);
-    } else {
-        float scale = 0.f;
-        if constexpr (GRAD) {
-            const bool given = p.fin.denom > 0.f;
-            scale = p.g / (given ? p.fin.denom : static_cast<float>(count_valid_consumers(p.src, s_count)));
+    const ExpScale& sc = p.scale;
+    if (warp == kStreamWarps) {
+        stream_produce<ES>(p.src, bars, smem, GRAD ? 2 : 1, cid, ncl, rank);
+    } else if (warp < kStreamWarps) {
+        if (GRAD && p.fin.denom <= 0.f) {
+            const int n = count_valid_consumers(p.src, s_count);
+            if (tid == 0) s_valid = n;
+            scale_known();
         }
-        const float w1 = scale * p.ce_w, wt = scale * p.kd_w * p.inv_t;
         StreamPos pos{0, 0, false};
+        RowPos rp;
         Slice s = slice_of<ES>(p.src, cid, rank);
-        uint32_t parity = 0;
         int64_t y_next = p.src.labels && n_it > 0 ? __ldg(p.src.labels + cid) : 0;
         for (int64_t it = 0; it < n_it; ++it) {
             const int64_t row = cid + it * ncl;
             const int64_t y = y_next;
             if (p.src.labels && it + 1 < n_it) y_next = __ldg(p.src.labels + row + ncl);
             move_slice<ES>(p.src, row, rank, s);
-            char* drow = GRAD ? p.dx + row * p.src.ld * ES : nullptr;
+            char* drow = p.dx + row * p.src.ld * ES;
             uint4* dv = reinterpret_cast<uint4*>(drow + s.col0 * ES);
             if (!stream_row_valid(y, p.src)) {
-                if (rank == 0 && tid == 0) {
-                    n_bad += y != p.src.ignore_index;
-                    p.fin.row_loss[row] = 0.f;
-                    if (p.row_ce) p.row_ce[row] = 0.f;
-                    if (p.row_kd) p.row_kd[row] = 0.f;
-                    if (p.stats) p.stats[row] = make_float4(0.f, 0.f, 0.f, 0.f);
-                }
                 if constexpr (GRAD) {
                     const uint4 z = make_uint4(0u, 0u, 0u, 0u);
                     for (int i = tid; i < s.nv; i += kStreamThreads) st_global_cs_v4(dv + i, z);
@@ -98,70 +94,39 @@ __global__ void __launch_bounds__(kStreamBlock, 3) distill_kernel(const DistillP
                 }
                 continue;
             }
-            const int64_t col_lo = rank == 0 ? 0 : s.col0;
-            const int64_t col_hi = rank == k - 1 ? p.src.V : s.col0 + static_cast<int64_t>(s.nv) * EPV;
-            if (warp == 0) {
-                // rank 0 takes all the listed logits (for the loss), the others those of their share
-                const bool bad = teacher_row<ES>(p.teacher, row, p.src.V, s.rowp, rank == 0 ? 0 : col_lo,
-                                                 rank == 0 ? p.src.V : col_hi, teach);
-                if (lane == 0) {
-                    s_xy = p.src.labels ? load_scalar<ES>(s.rowp + y * ES) : 0.f;
-                    if (rank == 0) {
-                        ++n_valid;
-                        n_bad += bad;
-                    }
-                }
-            }
-            RunStat<false, TWO> st(p.scale);
+            // With a second sweep the buffer's last use is long over: the sweep before this row waited for
+            // the closing warp.
+            if (!GRAD) row_begin(p.src, bars, rp, pos);
+            RunStat<false, TWO> st(sc);
             for (int c0 = 0; c0 < s.nv; c0 += kStreamChunk) {
                 const int nl = min(kStreamChunk, s.nv - c0);
                 uint4 v[kBlockVec];
                 stream_chunk(p.src, bars, smem, pos, [&](const unsigned char* stage) { load_strided<ES>(stage, nl, v); });
-                st.template add_vecs<ES>(v, p.scale);
+                st.template add_vecs<ES>(v, sc);
             }
-            // the head and tail scalars, one a thread; kept for the gradient
+            // the head and tail scalars, one a lane of the first warp; kept for the gradient
             const int n_edge = s.h + s.t;
             const int64_t edge_col = tid < s.h ? tid : s.tail_col + (tid - s.h);
             float edge = kNegInf;
-            if (n_edge > 0 && tid < 32) {
+            if (n_edge > 0 && warp == 0) {
                 if (tid < n_edge) edge = load_scalar<ES>(s.rowp + edge_col * ES);
-                st.add(edge, p.scale);
+                st.add(edge, sc);
             }
-            stat_publish(st, ex, parity);
-            consumers_sync();
-            stat_collect(st, ex, parity, p.scale);
-            if (k > 1) {
-                stat_send(st, ex, parity, k, rank);
-                cluster_sync_converged();
-                stat_merge(st, ex, parity, k, p.scale);
-            }
-            st.correct(p.scale);
-            parity ^= 1u;
-            const float s1 = TWO ? st.s2 : st.s;  // at T = 1 they are the same; without w_ce it is not used
-            if (rank == 0 && warp == 0 && !pos.aborted) {
-                const bool empty = st.s == 0.f;  // nothing but -inf: every token has log probability -inf
-                const float ln_t = logf(st.s), ln_1 = logf(s1);
-                float kd = 0.f;
-                for (int j = lane; j < p.teacher.K; j += 32) {
-                    const float q = teach.q[j];
-                    if (!(q == 0.f)) kd += q * (teach.lnq[j] - (empty ? kNegInf : (teach.x[j] - st.m) * p.inv_t - ln_t));
-                }
-                kd = warp_sum(kd);
-                if (lane == 0) {
-                    const float ce = p.ce_w != 0.f ? (empty ? -kNegInf : ln_1 - (s_xy - st.m)) : 0.f;
-                    p.fin.row_loss[row] = (p.ce_w != 0.f ? p.ce_w * ce : 0.f) + (p.kd_w != 0.f ? p.kd_w * kd : 0.f);
-                    if (p.row_ce) p.row_ce[row] = ce;
-                    if (p.row_kd) p.row_kd[row] = kd;
-                    if (p.stats) p.stats[row] = make_float4(st.s == 0.f ? kNegInf : st.m, ln_1, ln_t, teach.total);
-                }
-            }
+            const int buf = rp.buf(p.src);
+            stat_publish(st, ex, buf);
+            row_end(bars, buf);
             if constexpr (GRAD) {
-                // a row of -inf alone has p = 0
-                const float at = st.s == 0.f ? 0.f : wt * teach.total / st.s;
-                const float a1 = p.ce_w != 0.f && s1 != 0.f ? w1 / s1 : 0.f;
-                const float a = TWO ? at : at + a1;
-                const f32x2_t M = f2_pack(-st.m, -st.m), C = f2_pack(p.scale.c, p.scale.c), L = f2_pack(kLog2e, kLog2e);
-                const f32x2_t A = f2_pack(a, a), A1 = f2_pack(a1, a1);
+                if (!pos.aborted && !stream_wait(bars, &bars.row_ready[buf], rp.use(p.src) & 1u, p.src.wait_ns))
+                    pos.aborted = true;
+                const SweepFactors f = factors[buf];
+                const f32x2_t M = f2_pack(-f.m, -f.m), C = f2_pack(sc.c, sc.c), L = f2_pack(kLog2e, kLog2e);
+                const f32x2_t A = f2_pack(f.a, f.a), A1 = f2_pack(f.a1, f.a1);
+                auto grad = [&](f32x2_t x) {
+                    const f32x2_t d = f2_add(x, M);
+                    f32x2_t e = f2_mul(f2_ex2(f2_mul(d, C)), A);
+                    if (TWO) e = f2_fma(f2_ex2(f2_mul(d, L)), A1, e);
+                    return e;
+                };
                 for (int c0 = 0; c0 < s.nv; c0 += kStreamChunk) {
                     const int nl = min(kStreamChunk, s.nv - c0);
                     uint4 v[kBlockVec];
@@ -172,9 +137,7 @@ __global__ void __launch_bounds__(kStreamBlock, 3) distill_kernel(const DistillP
                         uint32_t o[4];
 #pragma unroll
                         for (int j = 0; j < EPV / 2; ++j) {
-                            const f32x2_t d = f2_add(vec_pair<ES>(v[i], j), M);
-                            f32x2_t e = f2_mul(f2_ex2(f2_mul(d, C)), A);
-                            if (TWO) e = f2_fma(f2_ex2(f2_mul(d, L)), A1, e);
+                            const f32x2_t e = grad(vec_pair<ES>(v[i], j));
                             if constexpr (ES == 2) {
                                 o[j] = f2_to_bf16x2(e);
                             } else {
@@ -185,34 +148,158 @@ __global__ void __launch_bounds__(kStreamBlock, 3) distill_kernel(const DistillP
                             }
                         }
                         const int lv = tid + i * kStreamThreads;
-                        if (lv < nl) st_global_cs_v4(dv + c0 + lv, make_uint4(o[0], o[1], o[2], o[3]));
+                        if (nl == kStreamChunk || lv < nl) st_global_cs_v4(dv + c0 + lv, make_uint4(o[0], o[1], o[2], o[3]));
                     }
                 }
-                auto grad_at = [&](float x) {
-                    const float d = x - st.m;
-                    float e = ex2(d * p.scale.c) * a;
-                    if (TWO) e = fmaf(ex2(d * kLog2e), a1, e);
-                    return e;
-                };
-                if (tid < n_edge && !pos.aborted) store_scalar<ES>(drow + edge_col * ES, grad_at(edge));
-                consumers_sync();  // every plain store of this CTA is made: the places that differ may follow
-                for (int j = tid; j <= p.teacher.K; j += kStreamThreads) {
-                    const bool is_label = j == p.teacher.K;
-                    if (is_label && !p.src.labels) continue;
-                    const int64_t id = is_label ? y : teach.id[j];
-                    if (id < 0 || id < col_lo || id >= col_hi || pos.aborted) continue;
-                    // a token listed twice, or listed and the label, gets the same value from each
-                    float e = grad_at(is_label ? s_xy : teach.x[j]) - wt * teacher_mass(teach, p.teacher.K, static_cast<int>(id));
-                    if (p.src.labels && id == y) e -= w1;
-                    store_scalar<ES>(drow + id * ES, e);
+                if (tid < n_edge && !pos.aborted) {
+                    float lo, hi;
+                    f2_unpack(grad(f2_pack(edge, edge)), lo, hi);
+                    store_scalar<ES>(drow + edge_col * ES, lo);
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.row_stored[buf]);
             }
-            consumers_sync();  // the teacher's row may be overwritten
+            ++rp.n;
         }
-        aborted = pos.aborted;
+    } else {  // the closing warp
+        float scale = 0.f;
+        if (GRAD) {
+            if (p.fin.denom <= 0.f) scale_known();
+            scale = p.g / (p.fin.denom > 0.f ? p.fin.denom : static_cast<float>(s_valid));
+        }
+        const float w1 = scale * p.ce_w, wt = scale * p.kd_w * p.inv_t;
+        const int K = p.teacher.K;
+        RowPos rp;
+        Slice s = slice_of<ES>(p.src, cid, rank);
+        int n_valid = 0, n_bad = 0;
+        bool aborted = false;
+        for (int64_t base = 0; base < n_it; base += 32) {
+            // 32 rows' labels and their logits at once, a row a lane.  (A row's gradient is not begun before
+            // this warp has made it ready, so the logits are still there.)
+            int64_t lab = 0;
+            float x_lab = 0.f;
+            if (p.src.labels && base + lane < n_it) {
+                const int64_t row = cid + (base + lane) * ncl;
+                lab = __ldg(p.src.labels + row);
+                if (stream_row_valid(lab, p.src)) x_lab = load_scalar<ES>(p.src.x + (row * p.src.ld + lab) * ES);
+                else n_bad += lab != p.src.ignore_index;
+            }
+            const int nj = static_cast<int>(min(static_cast<int64_t>(32), n_it - base));
+            for (int j = 0; j < nj; ++j) {
+                const int64_t row = cid + (base + j) * ncl;
+                const int64_t y = __shfl_sync(0xffffffffu, lab, j);
+                const float x_y = __shfl_sync(0xffffffffu, x_lab, j);
+                if (!stream_row_valid(y, p.src)) {
+                    if (rank == 0 && lane == 0) {
+                        p.fin.row_loss[row] = 0.f;
+                        if (p.row_ce) p.row_ce[row] = 0.f;
+                        if (p.row_kd) p.row_kd[row] = 0.f;
+                        if (p.stats) p.stats[row] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+                    continue;
+                }
+                ++n_valid;
+                move_slice<ES>(p.src, row, rank, s);
+                const int64_t col_lo = rank == 0 ? 0 : s.col0;
+                const int64_t col_hi = rank == k - 1 ? p.src.V : s.col0 + static_cast<int64_t>(s.nv) * EPV;
+                // rank 0 takes all the listed logits (for the loss), the others those of their share
+                __syncwarp();
+                const bool bad = teacher_row<ES>(p.teacher, row, p.src.V, s.rowp, rank == 0 ? 0 : col_lo,
+                                                 rank == 0 ? p.src.V : col_hi, teach);
+                __syncwarp();
+                if (lane == 0) n_bad += bad;
+                const int buf = rp.buf(p.src);
+                const uint32_t use = rp.use(p.src);
+                if (!aborted && !stream_wait(bars, &bars.row_full[buf], use & 1u, p.src.wait_ns)) aborted = true;
+                RunStat<false, TWO> st(sc);
+                stat_collect(st, ex, buf, sc);
+                if (!GRAD) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars.row_empty[buf]);
+                }
+                if (k > 1 && !stat_cluster(st, ex, bars, buf, use, use, k, rank, sc, aborted ? 0 : p.src.wait_ns)) aborted = true;
+                st.correct(sc);
+                const bool empty = st.s == 0.f;  // nothing but -inf: p = 0, and every token's log probability is -inf
+                const float s1 = TWO ? st.s2 : st.s;  // at T = 1 they are the same; without w_ce it is not used
+                SweepFactors f;
+                f.m = st.m;
+                const float at = empty ? 0.f : wt * teach.total / st.s;
+                f.a1 = p.ce_w != 0.f && s1 != 0.f ? w1 / s1 : 0.f;
+                f.a = TWO ? at : at + f.a1;
+                if (GRAD) {
+                    if (lane == 0) {
+                        factors[buf] = f;
+                        mbar_arrive(&bars.row_ready[buf]);
+                    }
+                }
+                if (rank == 0 && !aborted) {
+                    const float ln_t = logf(st.s), ln_1 = logf(s1);
+                    float kd = 0.f;
+                    for (int i = lane; i < K; i += 32) {
+                        const float q = teach.q[i];
+                        if (!(q == 0.f)) kd += q * (teach.lnq[i] - (empty ? kNegInf : (teach.x[i] - st.m) * p.inv_t - ln_t));
+                    }
+                    kd = warp_sum(kd);
+                    if (lane == 0) {
+                        const float ce = p.ce_w != 0.f ? (empty ? -kNegInf : ln_1 - (x_y - st.m)) : 0.f;
+                        p.fin.row_loss[row] = (p.ce_w != 0.f ? p.ce_w * ce : 0.f) + (p.kd_w != 0.f ? p.kd_w * kd : 0.f);
+                        if (p.row_ce) p.row_ce[row] = ce;
+                        if (p.row_kd) p.row_kd[row] = kd;
+                        if (p.stats) p.stats[row] = make_float4(empty ? kNegInf : st.m, ln_1, ln_t, teach.total);
+                    }
+                }
+                if constexpr (GRAD) {
+                    // The K + 1 places that differ, after the consumers' stores of the row.
+                    auto grad_at = [&](float x) {
+                        const float d = x - f.m;
+                        float e = ex2(d * sc.c) * f.a;
+                        if (TWO) e = fmaf(ex2(d * kLog2e), f.a1, e);
+                        return e;
+                    };
+                    constexpr int OWN = 4;
+                    bool waited = false, listed = false;
+                    char* drow = p.dx + row * p.src.ld * ES;
+                    for (int i0 = 0; i0 < K; i0 += 32 * OWN) {
+                        int id[OWN];
+                        float mass[OWN];
+#pragma unroll
+                        for (int q = 0; q < OWN; ++q) {
+                            id[q] = i0 + 32 * q + lane < K ? teach.id[i0 + 32 * q + lane] : -1;
+                            if (id[q] < col_lo || id[q] >= col_hi) id[q] = -1;
+                        }
+                        // a token listed twice gets the same value from each of its places
+                        teacher_mass(teach, K, id, mass);
+                        if (!waited) {
+                            if (!aborted && !stream_wait(bars, &bars.row_stored[buf], use & 1u, p.src.wait_ns)) aborted = true;
+                            waited = true;
+                        }
+#pragma unroll
+                        for (int q = 0; q < OWN; ++q) {
+                            if (id[q] < 0 || aborted) continue;
+                            float e = grad_at(teach.x[i0 + 32 * q + lane]) - wt * mass[q];
+                            if (p.src.labels && id[q] == y) {
+                                e -= w1;
+                                listed = true;
+                            }
+                            store_scalar<ES>(drow + static_cast<int64_t>(id[q]) * ES, e);
+                        }
+                    }
+                    listed = __any_sync(0xffffffffu, listed);
+                    if (lane == 0 && p.src.labels && !listed && y >= col_lo && y < col_hi && !aborted)
+                        store_scalar<ES>(drow + y * ES, grad_at(x_y) - w1);
+                }
+                ++rp.n;
+            }
+        }
+        n_bad = __reduce_add_sync(0xffffffffu, n_bad);
+        if (lane == 0) {
+            s_valid = rank == 0 ? n_valid : 0;
+            s_bad = rank == 0 ? n_bad : 0;
+            if (aborted) bars.abort = 1;
+        }
     }
     __syncthreads();
-    rows_finish<kStreamBlock>(p.fin, aborted || stream_aborted(bars), n_valid, n_bad, &s_last, dred, true);
+    rows_finish<kStreamBlock>(p.fin, stream_aborted(bars), s_valid, s_bad, &s_last, dred, true);
     if (k > 1) cluster_sync_converged();  // no CTA leaves while its shared memory may be written
 }
 
@@ -231,6 +318,7 @@ cudaError_t launch_typed(DistillParams prm, cudaStream_t stream) {
     int k = kStreamMaxCluster;
     while (k > 1 && (s.N * k > sms || 2 * nb < static_cast<int64_t>(k) * kStreamChunk)) k /= 2;
     set_cluster(s, k);
+    s.log2_buffers = 1;
     const size_t fixed = 1024 + sizeof(StreamBars) + sizeof(StatExchange) + sizeof(TeacherRow) + 512;
     const int per_sm = 3;
     const size_t room = (228 * 1024) / per_sm - fixed;

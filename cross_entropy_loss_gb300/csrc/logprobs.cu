@@ -10,14 +10,13 @@
 // has one maximum, which the sums need anyway and which is kept as an ordered integer
 // key.  Blocks are contiguous, so the K largest blocks by (maximum, lower index first)
 // hold the K largest elements by (value, lower index first): with a total order an
-// element outside those blocks has K larger ones before it.  So a row's end is
+// element outside those blocks has K larger ones before it.  A row's end, by the CTA's
+// one closing warp while the others are on the next rows, is
 //
-//   1. a threshold on the block maxima with at least K and at most 256 blocks at or
-//      above it (bisection on the keys, a count over the CTA each step; ties beyond 256
-//      blocks are cut by a second bisection on the block index);
-//   2. one block a thread, re-read (from L2: the row just went through), and its elements
-//      at or above the threshold put on a list;
-//   3. each listed element's rank = the number of larger ones, its place in the output.
+//   1. a threshold that at least K blocks reach, from the consumer threads' maxima;
+//   2. the blocks at or above it, re-read (from L2: the row just went through), and their
+//      elements at or above the threshold put on a list;
+//   3. the list put in order, in registers.
 //
 // Rows go to CTAs round-robin; when there are fewer rows than SMs a cluster shares each
 // row, joins its sums and lists through distributed shared memory, and ranks every
@@ -32,14 +31,22 @@ namespace foak {
 
 namespace {
 
-constexpr int kListCap = 1024;  // listed elements of a row (or of a CTA's share of it)
+constexpr int kListCap = 512;   // listed elements of a row (or of a CTA's share of it): at least kTopKMax
 constexpr int kSelCap = 256;    // blocks they are taken from
+constexpr int kAll = 0x7fffffff;
+constexpr int kKeyBody = 8;     // place of the first body block's key; before it the head's and the tail's
+// Closing warps of a CTA.  The work on a row's top tokens is a chain of some 6000 cycles
+// (K = 20), so four take rows in turn; without top tokens one keeps up.
+template <bool TOPK>
+constexpr int kClosers = TOPK ? 4 : 1;
 
 struct LogprobParams {
     StreamSrc src;
     float inv_t;       // 1 / T
     ExpScale scale;
     int top_k;
+    int key_stride;    // places of a row's block maxima in shared memory
+    int log2_closers;  // closing warps at work
     float* logp;       // [N] or null
     float* entropy;    // [N] or null
     float* lse;        // [N] or null
@@ -76,41 +83,13 @@ struct BlockKey<2> {
     }
 };
 
+// A closing warp's scratch.
 struct TopScratch {
-    int count[2][kStreamWarps];                // partial counts, by the parity of the count
-    int n_sel, n_list, n_tied;
-    uint32_t thread_max[kStreamThreads];       // key of the largest of a thread's blocks; 0: it has none
-    int sel[kSelCap];                          // the chosen blocks
     alignas(16) unsigned long long list[kListCap];  // (key << 32) | ~column
-    unsigned long long best[kStreamThreads];   // this CTA's top K in order (clusters)
+    uint16_t sel[kSelCap];                          // the chosen blocks
 };
 
-// The sum of n over the consumer threads; one consumer barrier.
-__device__ __forceinline__ int consumers_count(int n, TopScratch& t, uint32_t& turn) {
-    n = __reduce_add_sync(0xffffffffu, n);
-    const uint32_t b = turn++ & 1u;
-    if ((threadIdx.x & 31) == 0) t.count[b][threadIdx.x >> 5] = n;
-    consumers_sync();
-    int s = 0;
-#pragma unroll
-    for (int w = 0; w < kStreamWarps; ++w) s += t.count[b][w];
-    return s;
-}
-
-// Places for n entries of each lane in a list whose length is *len: one atomic a warp.
-// Returns the lane's first place.
-__device__ __forceinline__ int warp_places(int n, int* len) {
-    const int lane = threadIdx.x & 31;
-    int sum = n;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, sum, off);
-        if (lane >= off) sum += o;
-    }
-    int base = 0;
-    if (lane == 31 && sum) base = atomicAdd(len, sum);
-    return __shfl_sync(0xffffffffu, base, 31) + sum - n;
-}
+__device__ __forceinline__ unsigned lanes_below() { return (1u << (threadIdx.x & 31)) - 1u; }
 
 // Block `id` of the slice: 0 the head scalars, 1 .. nblk the body's blocks, nblk + 1 the tail scalars.
 template <int ES>
@@ -159,33 +138,30 @@ struct BlockElements {
     }
 };
 
+// Everything from here to the kernel is one warp's work.
+
 // The slow way to the list, for rows in which the fast one meets more blocks or elements
 // than it has room for (many equal values, or a share of few blocks): exact bisections,
 // first for the K-th largest block by (maximum, lower index first), then, if need be, for
-// the K-th largest element.  nreal > K blocks, or all of them are taken.
+// the K-th largest element.  Up to K blocks, all of them are taken.
 template <int ES>
-__device__ __noinline__ void top_list_exact(const Slice s, const typename BlockKey<ES>::type* keys, int K, TopScratch& t) {
+__device__ __noinline__ int top_list_exact(const Slice s, const typename BlockKey<ES>::type* keys, int K, TopScratch& t) {
     using BK = BlockKey<ES>;
-    const int tid = threadIdx.x;
+    const int lane = threadIdx.x & 31;
     const int nblk = (s.nv + kBlockVec - 1) / kBlockVec;
     const int nreal = nblk + (s.h > 0) + (s.t > 0);
-    uint32_t turn = 0;
-    consumers_sync();
-    if (tid == 0) {
-        t.n_sel = 0;
-        t.n_list = 0;
-    }
+    auto key = [&](int b) -> uint32_t { return keys[b == 0 ? 0 : b > nblk ? 1 : kKeyBody - 1 + b]; };
     // ---- the blocks: keys above lo, and of those equal to lo the ids up to last
     uint32_t lo = 1;
-    int last = 0x7fffffff;
+    int last = kAll;
     if (nreal > K) {
-        uint32_t hi = ES == 2 ? 0x10000u : 0xffffffffu;  // no key is as large (a NaN's would be)
+        uint32_t hi = ES == 2 ? 0x10000u : 0xffffffffu;  // above every key but a NaN's
         int c_lo = nreal, c_hi = 0;                      // blocks at or above lo and hi
         while (hi - lo > 1 && c_lo > kSelCap) {
             const uint32_t mid = lo + (hi - lo) / 2;
             int n = 0;
-            for (int b = tid; b < nblk + 2; b += kStreamThreads) n += keys[b] >= mid;
-            n = consumers_count(n, t, turn);
+            for (int b = lane; b < nblk + 2; b += 32) n += key(b) >= mid;
+            n = __reduce_add_sync(0xffffffffu, n);
             if (n >= K) {
                 lo = mid;
                 c_lo = n;
@@ -200,33 +176,40 @@ __device__ __noinline__ void top_list_exact(const Slice s, const typename BlockK
             while (j1 - j0 > 1) {
                 const int mid = j0 + (j1 - j0) / 2;
                 int n = 0;
-                for (int b = tid; b <= mid; b += kStreamThreads) n += keys[b] == lo;
-                if (consumers_count(n, t, turn) >= need) j1 = mid;
+                for (int b = lane; b <= mid; b += 32) n += key(b) == lo;
+                if (__reduce_add_sync(0xffffffffu, n) >= need) j1 = mid;
                 else j0 = mid;
             }
             last = j1;
         }
     }
-    consumers_sync();
-    for (int b = tid; b < nblk + 2; b += kStreamThreads) {
-        const uint32_t k = keys[b];
-        if (k > lo || (k == lo && b <= last)) {
-            const int i = atomicAdd(&t.n_sel, 1);
-            if (i < kSelCap) t.sel[i] = b;
-        }
+    int n_sel = 0;
+    for (int b0 = 0; b0 < nblk + 2; b0 += 32) {
+        const int b = b0 + lane;
+        const uint32_t k = b < nblk + 2 ? key(b) : 0;
+        const bool hit = k > lo || (k == lo && b <= last);
+        const unsigned m = __ballot_sync(0xffffffffu, hit);
+        const int at = n_sel + __popc(m & lanes_below());
+        if (hit && at < kSelCap) t.sel[at] = static_cast<uint16_t>(b);
+        n_sel += __popc(m);
     }
-    consumers_sync();
-    // ---- one block a thread, and its elements
-    const int n_sel = min(t.n_sel, kSelCap);
-    BlockElements<ES> el;
-    el.n = 0;
-    el.col = 0;
-    if (tid < n_sel) el.load(s, t.sel[tid], nblk);
+    n_sel = min(n_sel, kSelCap);
+    __syncwarp();
+    // ---- their elements: a block a lane and turn, read again for every count
+    auto for_each = [&](auto&& f) {
+        for (int i0 = 0; i0 < n_sel; i0 += 32) {
+            BlockElements<ES> el;
+            el.n = 0;
+            el.col = 0;
+            if (i0 + lane < n_sel) el.load(s, t.sel[i0 + lane], nblk);
+#pragma unroll
+            for (int e = 0; e < BlockElements<ES>::N; ++e) f(el.item(e));
+        }
+    };
     auto at_least = [&](unsigned long long f) {
         int n = 0;
-#pragma unroll
-        for (int e = 0; e < BlockElements<ES>::N; ++e) n += el.item(e) >= f;
-        return consumers_count(n, t, turn);
+        for_each([&](unsigned long long it) { n += it >= f; });
+        return __reduce_add_sync(0xffffffffu, n);
     };
     // every count is at least K at b0 (or takes every element) and less than K at b1
     unsigned long long b0 = static_cast<unsigned long long>(BK::element(lo)) << 32, b1 = ~0ull;
@@ -242,42 +225,43 @@ __device__ __noinline__ void top_list_exact(const Slice s, const typename BlockK
             }
         }
     }
-#pragma unroll
-    for (int e = 0; e < BlockElements<ES>::N; ++e) {
-        const unsigned long long it = el.item(e);
-        if (it >= b0) {
-            const int i = atomicAdd(&t.n_list, 1);
-            if (i < kListCap) t.list[i] = it;
-        }
-    }
-    consumers_sync();
+    int n = 0;
+    for_each([&](unsigned long long it) {
+        const bool hit = it >= b0;
+        const unsigned m = __ballot_sync(0xffffffffu, hit);
+        const int at = n + __popc(m & lanes_below());
+        if (hit && at < kListCap) t.list[at] = it;
+        n += __popc(m);
+    });
+    __syncwarp();
+    return min(n, kListCap);
 }
 
 // This CTA's largest elements of its slice onto t.list: at least the min(K, all) largest
-// ones, at most kListCap.  Returns how many.  keys[1 .. nblk] are the block maxima, keys[0]
-// and keys[nblk + 1] those of the head and tail (0: none), t.thread_max the threads'; all
-// of them written before a barrier.
+// ones, at most kListCap.  Returns how many.  keys are the block maxima (kKeyBody the first
+// body block's; 0 and 1 the head's and tail's, 0 where there is none), thread_max the threads'.
 template <int ES>
-__device__ __forceinline__ int top_list(const Slice& s, const typename BlockKey<ES>::type* keys, int K, TopScratch& t) {
+__device__ __noinline__ int top_list(const Slice s, const typename BlockKey<ES>::type* keys,
+                                        const uint32_t* thread_max, int K, TopScratch& t) {
     using BK = BlockKey<ES>;
     constexpr int EPV = 16 / ES;
     constexpr int PER = kStreamThreads / 32;
-    const int tid = threadIdx.x, lane = tid & 31;
+    const int lane = threadIdx.x & 31;
     const int nblk = (s.nv + kBlockVec - 1) / kBlockVec;
     // A threshold that K threads' maxima, so K blocks, reach: the K-th largest of the 256
-    // thread maxima, or a little below it.  Every warp finds it for itself, without a
-    // barrier.  Of blocks in random order about -256 ln(1 - K / 256) are at or above it.
+    // thread maxima, or a little below it.  Of blocks in random order about
+    // -256 ln(1 - K / 256) are at or above it.
     uint32_t lo = 1;
     if (min(nblk, kStreamThreads) >= K) {
         uint32_t v[PER], least = 0xffffffffu, hi = 0;
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-            v[j] = t.thread_max[lane + 32 * j];
-            if (v[j]) least = min(least, v[j]);
+            v[j] = thread_max[lane + 32 * j];
+            least = min(least, v[j] - 1u);  // 0, no block, becomes the largest
             hi = max(hi, v[j]);
         }
-        lo = __reduce_min_sync(0xffffffffu, least);
-        hi = __reduce_max_sync(0xffffffffu, hi) + 1;
+        lo = __reduce_min_sync(0xffffffffu, least) + 1u;
+        hi = __reduce_max_sync(0xffffffffu, hi) + 1u;
         const int most = K + K / 8 + 4;
         while (hi - lo > 1) {
             const uint32_t mid = lo + (hi - lo) / 2;
@@ -293,174 +277,240 @@ __device__ __forceinline__ int top_list(const Slice& s, const typename BlockKey<
             }
         }
     }
-    for (int b0 = 1; b0 <= nblk; b0 += 32 * kStreamThreads) {
-        uint32_t hit = 0;
-        for (int j = 0, b = b0 + tid; j < 32 && b <= nblk; ++j, b += kStreamThreads)
-            hit |= static_cast<uint32_t>(keys[b] >= lo) << j;
-        if (__any_sync(0xffffffffu, hit != 0)) {
-            int at = warp_places(__popc(hit), &t.n_sel);
-            for (; hit; hit &= hit - 1, ++at)
-                if (at < kSelCap) t.sel[at] = b0 + tid + (__ffs(hit) - 1) * kStreamThreads;
+    // The blocks that reach a threshold, 16 bytes of keys a lane and turn.
+    auto blocks_from = [&](uint32_t least) {
+        constexpr int KPV = 16 / sizeof(typename BK::type);
+        const uint4* kv = reinterpret_cast<const uint4*>(keys + kKeyBody);
+        int n = 0;
+#pragma unroll 2
+        for (int b0 = 0; b0 < nblk; b0 += 32 * KPV) {
+            const int b = b0 + lane * KPV;
+            uint4 w = make_uint4(0u, 0u, 0u, 0u);
+            if (b < nblk) w = kv[b / KPV];
+            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+            uint32_t hit = 0;
+#pragma unroll
+            for (int e = 0; e < KPV; ++e) {
+                const uint32_t key = ES == 2 ? (e & 1 ? x[e / 2] >> 16 : x[e / 2] & 0xffffu) : x[e];
+                hit |= key >= least ? 1u << e : 0u;
+            }
+            if (b + KPV > nblk) hit &= b < nblk ? (1u << (nblk - b)) - 1u : 0u;
+            for (unsigned m = __ballot_sync(0xffffffffu, hit != 0); m; m = __ballot_sync(0xffffffffu, hit != 0)) {
+                const int at = n + __popc(m & lanes_below());
+                if (hit && at < kSelCap) t.sel[at] = static_cast<uint16_t>(b + __ffs(hit));
+                hit &= hit - 1;
+                n += __popc(m);
+            }
+            if (n > kSelCap) break;
         }
-    }
-    consumers_sync();
-    int n_sel = t.n_sel, need = 0x7fffffff, strict = 0x7fffffff;  // sel[strict ..]: blocks whose maximum is lo, in order
+        __syncwarp();
+        return n;
+    };
+    int n_sel = blocks_from(lo), need = kAll, strict = kAll;  // sel[strict ..]: blocks whose maximum is lo, in order
     if (n_sel > kSelCap) {
         // Ties at the threshold (a mask that leaves fewer than K tokens): the blocks above
         // it, and the first blocks that reach it, as many as can matter.
-        consumers_sync();
-        if (tid == 0) t.n_sel = 0;
-        consumers_sync();
-        for (int b = 1 + tid; b <= nblk; b += kStreamThreads) {
-            if (keys[b] > lo) {
-                const int i = atomicAdd(&t.n_sel, 1);
-                if (i < kSelCap) t.sel[i] = b;
-            }
-        }
-        consumers_sync();
-        strict = t.n_sel;
-        need = K - strict;
+        strict = blocks_from(lo + 1);
         if (strict < K) {
-            if (tid < 32) {
-                int have = 0;
-                for (int b0 = 1; b0 <= nblk && have < need; b0 += 32) {
-                    const bool tie = b0 + lane <= nblk && keys[b0 + lane] == lo;
-                    const unsigned m = __ballot_sync(0xffffffffu, tie);
-                    const int at = have + __popc(m & ((1u << lane) - 1u));
-                    if (tie && at < need) t.sel[strict + at] = b0 + lane;
-                    have += __popc(m);
-                }
-                if (lane == 0) t.n_tied = min(have, need);
+            need = K - strict;
+            int have = 0;
+            for (int b0 = 0; b0 < nblk && have < need; b0 += 32) {
+                const bool tie = b0 + lane < nblk && keys[kKeyBody + b0 + lane] == lo;
+                const unsigned m = __ballot_sync(0xffffffffu, tie);
+                const int at = have + __popc(m & lanes_below());
+                if (tie && at < need) t.sel[strict + at] = static_cast<uint16_t>(1 + b0 + lane);
+                have += __popc(m);
             }
-            consumers_sync();
-            n_sel = strict + t.n_tied;
-        } else {
-            n_sel = kSelCap + 1;  // more than K blocks above the K-th thread maximum: the slow way
+            n_sel = strict + min(have, need);
+            __syncwarp();
         }
     }
     if (n_sel <= kSelCap) {
-        // Four threads a block, one vector each (re-read from L2); the elements at or above the threshold.
+        // Four lanes a block, one vector each (re-read from L2); the elements at or above the threshold.
+        constexpr int TURNS = 4;  // loads that go out before the first is looked at
         const float floor = lo == 1 ? kNegInf : BK::value(lo);
         const uint4* body = reinterpret_cast<const uint4*>(s.body);
-        constexpr int TURNS = kSelCap * kBlockVec / kStreamThreads;
-        uint4 w[TURNS];
-        int vec[TURNS];
+        int n = 0;
+        for (int i0 = 0; i0 < n_sel * kBlockVec; i0 += 32 * TURNS) {
+            uint4 w[TURNS];
+            int vec[TURNS];
 #pragma unroll
-        for (int q = 0; q < TURNS; ++q) {  // every turn's load goes out before the first is looked at
-            const int j = (q * kStreamThreads + tid) / kBlockVec;
-            vec[q] = j < n_sel ? (t.sel[j] - 1) * kBlockVec + (tid & (kBlockVec - 1)) : s.nv;
-            w[q] = RowMath<ES>::pad();
-            if (vec[q] < s.nv) w[q] = ld_global_v4(body + vec[q]);
-        }
-#pragma unroll
-        for (int q = 0; q < TURNS; ++q) {
-            if (q * kStreamThreads >= n_sel * kBlockVec) break;
-            uint32_t hit = 0, tie = 0;
-#pragma unroll
-            for (int e = 0; e < EPV / 2; ++e) {
-                float lo2, hi2;
-                f2_unpack(vec_pair<ES>(w[q], e), lo2, hi2);
-                hit |= static_cast<uint32_t>(lo2 >= floor) << 2 * e | static_cast<uint32_t>(hi2 >= floor) << (2 * e + 1);
-                tie |= static_cast<uint32_t>(lo2 == floor) << 2 * e | static_cast<uint32_t>(hi2 == floor) << (2 * e + 1);
+            for (int q = 0; q < TURNS; ++q) {
+                const int j = (i0 + 32 * q + lane) / kBlockVec;
+                vec[q] = j < n_sel ? (t.sel[j] - 1) * kBlockVec + (lane & (kBlockVec - 1)) : s.nv;
+                w[q] = RowMath<ES>::pad();
+                if (vec[q] < s.nv) w[q] = ld_global_v4(body + vec[q]);
             }
-            if (vec[q] >= s.nv) hit = tie = 0;
-            if (strict != 0x7fffffff) {
-                // an equal one counts only if fewer than `need` come before it: those of its block's
-                // earlier vectors, and one at least in each tied block before
-                int sum = __popc(tie);
 #pragma unroll
-                for (int off = 1; off < kBlockVec; off <<= 1) {
-                    const int o = __shfl_up_sync(0xffffffffu, sum, off, kBlockVec);
-                    if ((tid & (kBlockVec - 1)) >= off) sum += o;
+            for (int q = 0; q < TURNS; ++q) {
+                if (i0 + 32 * q >= n_sel * kBlockVec) break;
+                uint32_t hit = 0, tie = 0;
+#pragma unroll
+                for (int e = 0; e < EPV / 2; ++e) {
+                    float a, b;
+                    f2_unpack(vec_pair<ES>(w[q], e), a, b);
+                    hit |= (a >= floor ? 1u << 2 * e : 0u) | (b >= floor ? 2u << 2 * e : 0u);
                 }
-                int room = need - (sum - __popc(tie)) - max(0, (q * kStreamThreads + tid) / kBlockVec - strict);
-                for (uint32_t m = tie; m; m &= m - 1)
-                    if (--room < 0) hit &= ~(m & -m);
-            }
-            if (__any_sync(0xffffffffu, hit != 0)) {
-                int at = warp_places(__popc(hit), &t.n_list);
+                if (vec[q] >= s.nv) hit = 0;
+                if (strict != kAll) {
+                    // an equal one counts only if fewer than `need` come before it: those of its block's
+                    // earlier vectors, and one at least in each tied block before
+#pragma unroll
+                    for (int e = 0; e < EPV / 2; ++e) {
+                        float a, b;
+                        f2_unpack(vec_pair<ES>(w[q], e), a, b);
+                        tie |= (a == floor ? 1u << 2 * e : 0u) | (b == floor ? 2u << 2 * e : 0u);
+                    }
+                    tie &= hit;
+                    int sum = __popc(tie);
+#pragma unroll
+                    for (int off = 1; off < kBlockVec; off <<= 1) {
+                        const int o = __shfl_up_sync(0xffffffffu, sum, off, kBlockVec);
+                        if ((lane & (kBlockVec - 1)) >= off) sum += o;
+                    }
+                    int room = need - (sum - __popc(tie)) - max(0, (i0 + 32 * q + lane) / kBlockVec - strict);
+                    for (uint32_t m = tie; m; m &= m - 1)
+                        if (--room < 0) hit &= ~(m & -m);
+                }
                 const uint32_t col = static_cast<uint32_t>(s.col0) + static_cast<uint32_t>(vec[q]) * EPV;
-#pragma unroll
-                for (int e = 0; e < EPV; ++e) {
-                    if (!(hit >> e & 1u)) continue;
-                    float lo2, hi2;
-                    f2_unpack(vec_pair<ES>(w[q], e / 2), lo2, hi2);
-                    const uint32_t key = key_of(e & 1 ? hi2 : lo2);
-                    if (at < kListCap) t.list[at] = (static_cast<unsigned long long>(key) << 32) | ~(col + e);
-                    ++at;
+                for (unsigned m = __ballot_sync(0xffffffffu, hit != 0); m; m = __ballot_sync(0xffffffffu, hit != 0)) {
+                    const int at = n + __popc(m & lanes_below());
+                    n += __popc(m);
+                    if (hit) {
+                        const int e = __ffs(hit) - 1;
+                        hit &= hit - 1;
+                        const uint32_t x = ES == 2 ? e >> 1 : e;
+                        const uint32_t word = x & 2 ? (x & 1 ? w[q].w : w[q].z) : (x & 1 ? w[q].y : w[q].x);
+                        const float f = ES == 2 ? (e & 1 ? bf16_hi(word) : bf16_lo(word)) : __uint_as_float(word);
+                        if (at < kListCap) t.list[at] = (static_cast<unsigned long long>(key_of(f)) << 32) | ~(col + e);
+                    }
                 }
             }
         }
-        if (tid < s.h + s.t) {
-            const int64_t col = tid < s.h ? tid : s.tail_col + (tid - s.h);
-            const float f = load_scalar<ES>(s.rowp + col * ES);
-            if (f >= floor) {
-                const int at = atomicAdd(&t.n_list, 1);
-                if (at < kListCap)
-                    t.list[at] = (static_cast<unsigned long long>(key_of(f)) << 32) | ~static_cast<uint32_t>(col);
-            }
+        if (s.h + s.t > 0) {
+            const int64_t col = lane < s.h ? lane : s.tail_col + (lane - s.h);
+            float f = kNegInf;
+            if (lane < s.h + s.t) f = load_scalar<ES>(s.rowp + col * ES);
+            const bool hit = lane < s.h + s.t && f >= floor;
+            const unsigned m = __ballot_sync(0xffffffffu, hit);
+            const int at = n + __popc(m & lanes_below());
+            if (hit && at < kListCap)
+                t.list[at] = (static_cast<unsigned long long>(key_of(f)) << 32) | ~static_cast<uint32_t>(col);
+            n += __popc(m);
         }
-        consumers_sync();
-        if (t.n_list <= kListCap) return t.n_list;
+        __syncwarp();
+        if (n <= kListCap) return n;
     }
-    top_list_exact<ES>(s, keys, K, t);
-    return min(t.n_list, kListCap);
+    return top_list_exact<ES>(s, keys, K, t);
 }
 
+// The list in descending order, R items a lane: a bitonic sort in registers, lane l
+// holding the places l R .. l R + R - 1; the places from n to 32 R get 0.
+template <int R>
+__device__ __noinline__ void sort_list(unsigned long long* list, int n) {
+    const int lane = threadIdx.x & 31;
+    unsigned long long v[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) v[r] = r * 32 + lane < n ? list[r * 32 + lane] : 0ull;  // any order will do
+#pragma unroll
+    for (int size = 2; size <= 32 * R; size *= 2) {
+#pragma unroll
+        for (int stride = size / 2; stride > 0; stride /= 2) {
+            if (stride >= R) {
+                const int d = stride / R;
+                const bool lower = (lane & d) == 0;
+                const bool down = size >= 32 * R || ((lane * R) & size) == 0;  // this run descends
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const unsigned long long o = __shfl_xor_sync(0xffffffffu, v[r], d);
+                    v[r] = (lower == down) == (o > v[r]) ? o : v[r];
+                }
+            } else {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    if (r & stride) continue;
+                    const bool down = size >= 32 * R || ((lane * R + r) & size) == 0;
+                    const unsigned long long a = v[r], b = v[r + stride];
+                    const bool swap = down ? a < b : b < a;
+                    v[r] = swap ? b : a;
+                    v[r + stride] = swap ? a : b;
+                }
+            }
+        }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < R; ++r) list[lane * R + r] = v[r];
+}
+// The same for lists of up to kListCap, by counting the larger ones of each.
+__device__ __noinline__ void sort_long_list(unsigned long long* list, int n) {
+    constexpr int OWN = kListCap / 32;
+    const int lane = threadIdx.x & 31;
+    unsigned long long v[OWN];
+    int r[OWN];
+#pragma unroll
+    for (int q = 0; q < OWN; ++q) {
+        v[q] = q * 32 + lane < n ? list[q * 32 + lane] : ~0ull;
+        r[q] = 0;
+    }
+    for (int j = 0; j < n; ++j) {
+        const unsigned long long o = list[j];
+#pragma unroll
+        for (int q = 0; q < OWN; ++q) r[q] += o > v[q];
+    }
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < OWN; ++q)
+        if (q * 32 + lane < n) list[r[q]] = v[q];
+}
+__device__ __forceinline__ void top_ordered(unsigned long long* list, int n) {
+    if (n <= 32) sort_list<1>(list, n);
+    else if (n <= 64) sort_list<2>(list, n);
+    else if (n <= 256) sort_list<8>(list, n);
+    else sort_long_list(list, n);
+    __syncwarp();
+}
+
+template <bool TOPK>
+constexpr int kLogprobThreads = kFirstCloser + 32 * kClosers<TOPK>;
+
 template <int ES, bool ENT, bool TOPK>
-__global__ void __launch_bounds__(kStreamBlock, 3) logprobs_kernel(const LogprobParams p) {
+__global__ void __launch_bounds__(kLogprobThreads<TOPK>, TOPK ? 2 : 3) logprobs_kernel(const LogprobParams p) {
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ StreamBars bars;
     __shared__ StatExchange ex;
-    __shared__ TopScratch top;
-    __shared__ float4 fin;
+    __shared__ TopScratch top[TOPK ? kClosers<TOPK> : 1];
+    __shared__ uint32_t thread_max[TOPK ? kMaxBuffers : 1][kStreamThreads];  // key of the largest of a thread's blocks, 0: it has none
     using KeyT = typename BlockKey<ES>::type;
     unsigned char* ring = smem;
-    KeyT* keys = reinterpret_cast<KeyT*>(smem + p.src.stages * kStreamStageBytes);
+    KeyT* keys = reinterpret_cast<KeyT*>(smem + p.src.stages * kStreamStageBytes);  // key_stride a buffer
 
-    const int tid = threadIdx.x, k = p.src.k;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = p.src.k;
     const int rank = k > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-    const int64_t cid = blockIdx.x / k, ncl = gridDim.x / k;
+    const int64_t cid = blockIdx.x >> p.src.log2_k, ncl = gridDim.x >> p.src.log2_k;
     const int64_t n_it = p.src.N > cid ? (p.src.N - 1 - cid) / ncl + 1 : 0;
-    stream_init(bars, p.src.stages);
+    stream_init(bars, p.src.stages, k);
     griddep_launch_dependents();  // programmatic dependent launch: no global access before the wait
     griddep_wait();
     __syncthreads();
     if (k > 1) cluster_sync();  // every CTA's shared memory is there to be written to
 
-    bool bad = false, aborted = false;
-    if (tid >= kStreamThreads) {
-        stream_produce<ES>(p.src, bars, ring, 1, cid, ncl, rank, k > 1 ? (TOPK ? 3 : 1) : 0);
-    } else {
+    if (warp == kStreamWarps) {
+        stream_produce<ES>(p.src, bars, ring, 1, cid, ncl, rank);
+    } else if (warp < kStreamWarps) {
         StreamPos pos{0, 0, false};
+        RowPos rp;
         Slice s = slice_of<ES>(p.src, cid, rank);
-        uint32_t parity = 0;
         int64_t y_next = p.src.labels && n_it > 0 ? __ldg(p.src.labels + cid) : 0;
         for (int64_t it = 0; it < n_it; ++it) {
             const int64_t row = cid + it * ncl;
             const int64_t y = y_next;
             if (p.src.labels && it + 1 < n_it) y_next = __ldg(p.src.labels + row + ncl);
-            if (!stream_row_valid(y, p.src)) {
-                bad |= y != p.src.ignore_index;
-                if (rank == 0) {
-                    if (tid == 0) {
-                        if (p.logp) p.logp[row] = 0.f;
-                        if (p.entropy) p.entropy[row] = 0.f;
-                        if (p.lse) p.lse[row] = 0.f;
-                        if (p.stats) p.stats[row] = make_float2(0.f, 0.f);
-                    }
-                    if (TOPK) {
-                        for (int i = tid; i < p.top_k; i += kStreamThreads) {
-                            p.top_lp[row * p.top_k + i] = 0.f;
-                            p.top_ids[row * p.top_k + i] = -1;
-                        }
-                    }
-                }
-                continue;
-            }
+            if (!stream_row_valid(y, p.src)) continue;
             move_slice<ES>(p.src, row, rank, s);
-            float x_y = 0.f;
-            if (tid == 0 && rank == 0 && p.logp) x_y = load_scalar<ES>(s.rowp + y * ES);
+            row_begin(p.src, bars, rp, pos);
+            const int buf = rp.buf(p.src);
+            KeyT* rk = keys + buf * p.key_stride;
             RunStat<ENT, false> st(p.scale);
             float most = kNegInf;  // of the thread's blocks
             for (int c0 = 0; c0 < s.nv; c0 += kStreamChunk) {
@@ -472,142 +522,170 @@ __global__ void __launch_bounds__(kStreamBlock, 3) logprobs_kernel(const Logprob
                 });
                 const float bmax = st.template add_vecs<ES>(v, p.scale);
                 if (TOPK) {
-                    if (tid * kBlockVec < nl) keys[1 + c0 / kBlockVec + tid] = static_cast<KeyT>(BlockKey<ES>::of(bmax));
+                    if (tid * kBlockVec < nl) rk[kKeyBody + c0 / kBlockVec + tid] = static_cast<KeyT>(BlockKey<ES>::of(bmax));
                     most = fmaxf(most, bmax);
                 }
             }
-            if (s.h + s.t > 0 && tid < 32) {  // the head's and the tail's scalars, one a lane
+            if (s.h + s.t > 0 && warp == 0) {  // the head's and the tail's scalars, one a lane
                 float e = kNegInf;
                 if (tid < s.h + s.t) e = load_scalar<ES>(s.rowp + (tid < s.h ? tid : s.tail_col + (tid - s.h)) * ES);
                 st.add(e, p.scale);
                 if (TOPK) {
                     const float hm = warp_max_redux(tid < s.h ? e : kNegInf), tm = warp_max_redux(tid < s.h ? kNegInf : e);
                     if (tid == 0) {
-                        keys[0] = s.h > 0 ? BlockKey<ES>::of(hm) : 0;
-                        keys[1 + (s.nv + kBlockVec - 1) / kBlockVec] = s.t > 0 ? BlockKey<ES>::of(tm) : 0;
+                        rk[0] = s.h > 0 ? BlockKey<ES>::of(hm) : 0;
+                        rk[1] = s.t > 0 ? BlockKey<ES>::of(tm) : 0;
                     }
                 }
             } else if (TOPK && tid == 0) {
-                keys[0] = keys[1 + (s.nv + kBlockVec - 1) / kBlockVec] = 0;
+                rk[0] = rk[1] = 0;
             }
-            if (TOPK) {
-                top.thread_max[tid] = tid * kBlockVec < s.nv ? BlockKey<ES>::of(most) : 0u;
-                if (tid == 0) top.n_sel = top.n_list = 0;
+            if (TOPK) thread_max[buf][tid] = tid * kBlockVec < s.nv ? BlockKey<ES>::of(most) : 0u;
+            stat_publish(st, ex, buf);
+            row_end(bars, buf);
+            ++rp.n;
+        }
+    } else if (warp - (kStreamWarps + 1) < 1 << p.log2_closers) {  // a closing warp
+        const uint32_t me = warp - (kStreamWarps + 1), turn = (1u << p.log2_closers) - 1u;
+        RowPos rp;
+        Slice s = slice_of<ES>(p.src, cid, rank);
+        bool bad = false, aborted = false;
+        for (int64_t base = 0; base < n_it; base += 32) {
+            // 32 rows' labels at once, and the logits of this warp's rows, a row a lane
+            int64_t lab = 0;
+            bool ok = false;
+            if (base + lane < n_it) {
+                if (p.src.labels) lab = __ldg(p.src.labels + cid + (base + lane) * ncl);
+                ok = stream_row_valid(lab, p.src);
+                bad |= !ok && lab != p.src.ignore_index;
             }
-            stat_publish(st, ex, parity);
-            consumers_sync();
-            if (tid < 32) stat_collect(st, ex, parity, p.scale);
-            if (k > 1) {
-                if (tid < 32) stat_send(st, ex, parity, k, rank);
-                cluster_sync_converged();
-                if (tid < 32) stat_merge(st, ex, parity, k, p.scale);
-            }
-            parity ^= 1u;
-            if (tid < 32) {  // the row's results; the rest of the CTA goes on to the top tokens
+            const unsigned valid = __ballot_sync(0xffffffffu, ok);
+            float x_lab = 0.f;
+            if (p.logp && rank == 0 && ok && ((rp.n + __popc(valid & lanes_below())) & turn) == me)
+                x_lab = load_scalar<ES>(p.src.x + ((cid + (base + lane) * ncl) * p.src.ld + lab) * ES);
+            const int nj = static_cast<int>(min(static_cast<int64_t>(32), n_it - base));
+            for (int j = 0; j < nj; ++j) {
+                const int64_t row = cid + (base + j) * ncl;
+                if (!(valid >> j & 1u)) {
+                    if (rank == 0 && me == 0) {
+                        if (lane == 0) {
+                            if (p.logp) p.logp[row] = 0.f;
+                            if (p.entropy) p.entropy[row] = 0.f;
+                            if (p.lse) p.lse[row] = 0.f;
+                            if (p.stats) p.stats[row] = make_float2(0.f, 0.f);
+                        }
+                        if (TOPK) {
+                            for (int i = lane; i < p.top_k; i += 32) {
+                                p.top_lp[row * p.top_k + i] = 0.f;
+                                p.top_ids[row * p.top_k + i] = -1;
+                            }
+                        }
+                    }
+                    continue;
+                }
+                if ((rp.n & turn) != me) {
+                    ++rp.n;
+                    continue;
+                }
+                const float x_y = __shfl_sync(0xffffffffu, x_lab, j);
+                const int buf = rp.buf(p.src);
+                const uint32_t use = rp.use(p.src);
+                const uint32_t phase = TOPK ? 2 * use : use;  // exchanges of the buffer with the cluster so far
+                if (!aborted && !stream_wait(bars, &bars.row_full[buf], use & 1u, p.src.wait_ns)) aborted = true;
+                RunStat<ENT, false> st(p.scale);
+                stat_collect(st, ex, buf, p.scale);
+                if (!TOPK) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars.row_empty[buf]);
+                }
+                if (k > 1 && !stat_cluster(st, ex, bars, buf, use, phase, k, rank, p.scale, aborted ? 0 : p.src.wait_ns))
+                    aborted = true;
                 st.correct(p.scale);
                 const float ln_s = logf(st.s);
                 const bool empty = st.s == 0.f;
-                if (tid == 0) {
-                    if (TOPK) fin = make_float4(st.m, ln_s, st.s, 0.f);
-                    if (rank == 0 && !pos.aborted) {
-                        if (p.logp) p.logp[row] = empty ? kNegInf : (x_y - st.m) * p.inv_t - ln_s;
-                        if (ENT) {
-                            const float h = ln_s - st.a * kLn2 / st.s;
-                            p.entropy[row] = empty || h < 0.f ? 0.f : h;
-                        }
-                        if (p.lse) p.lse[row] = empty ? kNegInf : fmaf(st.m, p.inv_t, ln_s);
-                        if (p.stats) p.stats[row] = make_float2(empty ? kNegInf : st.m, ln_s);
+                if (lane == 0 && rank == 0 && !aborted) {
+                    if (p.logp) p.logp[row] = empty ? kNegInf : (x_y - st.m) * p.inv_t - ln_s;
+                    if (ENT) {
+                        const float h = ln_s - st.a * kLn2 / st.s;
+                        p.entropy[row] = empty || h < 0.f ? 0.f : h;
                     }
+                    if (p.lse) p.lse[row] = empty ? kNegInf : fmaf(st.m, p.inv_t, ln_s);
+                    if (p.stats) p.stats[row] = make_float2(empty ? kNegInf : st.m, ln_s);
                 }
-            }
-            if constexpr (TOPK) {
-                const int K = p.top_k;
-                const int n = top_list<ES>(s, keys, K, top);
-                const float4 f = fin;  // (m, ln S, S): written before the barriers of top_list
-                const bool none = !(f.z == f.z);  // a NaN or +inf in the row: no order to speak of
-                const bool empty = f.z == 0.f;
-                float* olp = p.top_lp + row * K;
-                int32_t* oid = p.top_ids + row * K;
-                auto write = [&](int r, unsigned long long item) {
-                    if (pos.aborted || none) return;
-                    olp[r] = empty ? kNegInf : (float_of_key(static_cast<uint32_t>(item >> 32)) - f.x) * p.inv_t - f.y;
-                    oid[r] = static_cast<int32_t>(~static_cast<uint32_t>(item));
-                };
-                // Ranks within this CTA's list: `ways` neighbouring threads an item, each comparing it with
-                // its share of the list, two items a 16-byte read.
-                if (k > 1) {
-                    if (tid < K) top.best[tid] = 0ull;
-                    consumers_sync();
-                }
-                const int ways = n <= kStreamThreads / 8 ? 8 : n <= kStreamThreads / 4 ? 4 : n <= kStreamThreads / 2 ? 2 : 1;
-                const int part = tid & (ways - 1);
-                for (int i0 = 0; i0 < n; i0 += kStreamThreads / ways) {
-                    const int i = i0 + tid / ways;
-                    const unsigned long long item = i < n ? top.list[i] : ~0ull;
-                    int r = 0;
-                    for (int j = 2 * part; j < n; j += 2 * ways) {
-                        const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(top.list + j);
-                        r += o.x > item;
-                        if (j + 1 < n) r += o.y > item;
-                    }
-                    for (int off = 1; off < ways; off <<= 1) r += __shfl_xor_sync(0xffffffffu, r, off);
-                    if (i < n && part == 0 && r < K) {
-                        if (k > 1) top.best[r] = item;
-                        else write(r, item);
-                    }
-                }
-                if (k > 1) {
-                    // The cluster's lists, each in order: an item's rank is the sum of its places in them,
-                    // one thread an item and list.  They are copied here first when there is room.
-                    cluster_sync_converged();  // every CTA's best are in place
-                    const bool copy = K * k <= kListCap;
-                    if (copy) {
-                        for (int i = tid; i < K * k; i += kStreamThreads) {
-                            const uint32_t from = mapa_u32(top.best, static_cast<uint32_t>(i / K)) + (i % K) * 8;
-                            asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(top.list[i]) : "r"(from) : "memory");
-                        }
-                    }
-                    consumers_sync();
-                    for (int i0 = 0; i0 < K * k; i0 += kStreamThreads) {
-                        const int i = i0 + tid;
-                        const int o = i & (k - 1);
-                        const unsigned long long item = i < K * k ? top.best[i / k] : 0ull;
-                        int a = 0, b = item ? K : 0;  // of list o: before a larger, from b on not
-                        const uint32_t remote = mapa_u32(top.best, static_cast<uint32_t>(o));
-                        while (a < b) {
-                            const int mid = (a + b) / 2;
-                            unsigned long long v;
-                            if (copy) v = top.list[o * K + mid];
-                            else asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(remote + mid * 8) : "memory");
-                            if (v > item) a = mid + 1;
-                            else b = mid;
+                if constexpr (TOPK) {
+                    TopScratch& t = top[me];
+                    const int K = p.top_k;
+                    const bool none = !(st.s == st.s);  // a NaN or +inf in the row: no order to speak of
+                    move_slice<ES>(p.src, row, rank, s);
+                    int n = 0;
+                    if (!none) n = top_list<ES>(s, keys + buf * p.key_stride, thread_max[buf], K, t);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars.row_empty[buf]);
+                    float* olp = p.top_lp + row * K;
+                    int32_t* oid = p.top_ids + row * K;
+                    auto write = [&](int r, unsigned long long item) {
+                        if (aborted) return;
+                        olp[r] = empty ? kNegInf : (float_of_key(static_cast<uint32_t>(item >> 32)) - st.m) * p.inv_t - ln_s;
+                        oid[r] = static_cast<int32_t>(~static_cast<uint32_t>(item));
+                    };
+                    unsigned long long* best = t.list;
+                    top_ordered(best, n);
+                    if (k == 1) {
+                        for (int i = lane; i < min(n, K); i += 32) write(i, best[i]);
+                    } else {
+                        // The cluster's lists, each in order and K long: an item's rank is the sum of its places in
+                        // them, one lane an item and list.  They are copied here first when there is room.
+                        for (int i = n + lane; i < K; i += 32) best[i] = 0ull;
+                        if (!peers_meet(bars, buf, phase + 1, k, aborted ? 0 : p.src.wait_ns)) aborted = true;
+                        unsigned long long* copies = t.list + kTopKMax;
+                        const bool copy = K * k <= kListCap - kTopKMax;
+                        if (copy) {
+                            for (int i = lane; i < K * k; i += 32) {
+                                const uint32_t from = mapa_u32(best, static_cast<uint32_t>(i / K)) + (i % K) * 8;
+                                asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(copies[i]) : "r"(from) : "memory");
+                            }
                         }
                         __syncwarp();
-                        for (int off = 1; off < k; off <<= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
-                        if (o == 0 && item && a < K) write(a, item);
+                        for (int i0 = 0; i0 < K * k; i0 += 32) {
+                            const int i = i0 + lane;
+                            const int o = i & (k - 1);
+                            const unsigned long long item = i < K * k ? best[i >> p.src.log2_k] : 0ull;
+                            int a = 0, b = item ? K : 0;  // of list o: before a larger, from b on not
+                            const uint32_t remote = mapa_u32(best, static_cast<uint32_t>(o));
+                            while (a < b) {
+                                const int mid = (a + b) / 2;
+                                unsigned long long v;
+                                if (copy) v = copies[o * K + mid];
+                                else asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(remote + mid * 8) : "memory");
+                                if (v > item) a = mid + 1;
+                                else b = mid;
+                            }
+                            __syncwarp();
+                            for (int off = 1; off < k; off <<= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
+                            if (o == 0 && item && a < K) write(a, item);
+                        }
                     }
-                    cluster_sync_converged();  // every CTA has read them
-                }
-                if (none && rank == 0) {
-                    for (int i = tid; i < K; i += kStreamThreads) {
-                        olp[i] = f.z;
-                        oid[i] = -1;
+                    if (none && rank == 0) {
+                        for (int i = lane; i < K; i += 32) {
+                            olp[i] = st.s;
+                            oid[i] = -1;
+                        }
                     }
+                    __syncwarp();
                 }
-                consumers_sync();  // the keys and lists may be overwritten
+                ++rp.n;
             }
         }
-        aborted = pos.aborted;
+        if (aborted) bars.abort = 1;
+        bad = __any_sync(0xffffffffu, bad);
+        if (bad && me == 0 && lane == 0) atomicOr(&p.ws->err, static_cast<unsigned>(FOAK_ERRBIT_LABEL_RANGE));
     }
     // The error word: every CTA adds its bits; the last one publishes and resets them.
     __syncthreads();
-    if (tid == 0) {
-        unsigned e = 0;
-        if (aborted || stream_aborted(bars)) e |= FOAK_ERRBIT_TIMEOUT;
-        if (bad) e |= FOAK_ERRBIT_LABEL_RANGE;
-        if (e) atomicOr(&p.ws->err, e);
+    if (tid == kFirstCloser) {
+        if (stream_aborted(bars)) atomicOr(&p.ws->err, static_cast<unsigned>(FOAK_ERRBIT_TIMEOUT));
         if (atom_add_acq_rel_gpu(&p.ws->done, 1u) == gridDim.x - 1) {
-            e = atomicExch(&p.ws->err, 0u);
+            const unsigned e = atomicExch(&p.ws->err, 0u);
             atomicExch(&p.ws->done, 0u);
             if (p.err) *p.err = static_cast<int32_t>(e);
         }
@@ -632,15 +710,23 @@ cudaError_t launch_typed(LogprobParams prm, cudaStream_t stream) {
     int k = kStreamMaxCluster;
     while (k > 1 && (s.N * k > sms || 2 * nb < static_cast<int64_t>(k) * kStreamChunk)) k /= 2;
     set_cluster(s, k);
-    const int64_t nblk = ((nb + kBlockVec - 1) / kBlockVec + s.k - 1) / s.k + 3;
-    const size_t key_bytes = TOPK ? (static_cast<size_t>(nblk) * sizeof(typename BlockKey<ES>::type) + 127) / 128 * 128 : 0;
-    // Three CTAs an SM when each gets a ring of three stages, else two.
-    const size_t fixed = 1024 + sizeof(StreamBars) + sizeof(StatExchange) + sizeof(TopScratch) + 256 + key_bytes;
-    int per_sm = 3;
-    while (per_sm > 1 && (228 * 1024) / per_sm < fixed + 3 * kStreamStageBytes) --per_sm;
-    const size_t room = std::min<size_t>((228 * 1024) / per_sm, 227 * 1024) - fixed;
+    const int64_t nblk = ((nb + kBlockVec - 1) / kBlockVec + s.k - 1) / s.k + 1;
+    prm.key_stride = static_cast<int>((kKeyBody + nblk + 63) / 64 * 64);
+    const size_t buffer = TOPK ? prm.key_stride * sizeof(typename BlockKey<ES>::type) : 0;
+    // A buffer for each closing warp, fewer where the keys are large; CTAs an SM as the
+    // registers allow, fewer where a ring of two stages would not fit.
+    const size_t fixed = 1024 + 256 + sizeof(StreamBars) + sizeof(StatExchange) +
+                         (TOPK ? kClosers<TOPK> * sizeof(TopScratch) + kMaxBuffers * kStreamThreads * 4 : 0);
+    int per_sm = TOPK ? 2 : 3;
+    s.log2_buffers = TOPK ? 2 : 1;
+    auto room_for = [&] { return std::min<int64_t>(228 * 1024 / per_sm, 227 * 1024) - static_cast<int64_t>(fixed + (buffer << s.log2_buffers)); };
+    while (s.log2_buffers > 1 && room_for() < 2 * static_cast<int64_t>(kStreamStageBytes)) --s.log2_buffers;
+    while (per_sm > 1 && room_for() < 2 * static_cast<int64_t>(kStreamStageBytes)) --per_sm;
+    prm.log2_closers = TOPK ? s.log2_buffers : 0;
+    const int64_t room = room_for();
+    if (room < static_cast<int64_t>(kStreamStageBytes)) return cudaErrorInvalidValue;
+    const size_t key_bytes = buffer << s.log2_buffers;
     s.stages = static_cast<int>(std::min<size_t>(kStreamMaxStages, room / kStreamStageBytes));
-    if (s.stages < 1) return cudaErrorInvalidValue;
     const size_t smem = static_cast<size_t>(s.stages) * kStreamStageBytes + key_bytes;
     {
         std::lock_guard<std::mutex> lock(g_lp_mu);
@@ -654,7 +740,7 @@ cudaError_t launch_typed(LogprobParams prm, cudaStream_t stream) {
     const int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(s.N, static_cast<int64_t>(sms) * per_sm / s.k));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(clusters * s.k), 1, 1);
-    cfg.blockDim = dim3(kStreamBlock, 1, 1);
+    cfg.blockDim = dim3(kLogprobThreads<TOPK>, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];

@@ -1,12 +1,16 @@
 // Rows of logits streamed through shared memory by one CTA, or by a cluster of CTAs
 // that share a row: the pieces common to the log-probability and distillation kernels.
 //
-// A CTA has kStreamThreads consumer threads and one producer warp.  The producer
-// copies the row in chunks of kStreamChunk 16-byte vectors (one-dimensional bulk
+// A CTA has kStreamThreads consumer threads, a producer warp and one or more closing
+// warps.  The
+// producer copies the row in chunks of kStreamChunk 16-byte vectors (one-dimensional bulk
 // copies) into a ring of stages; a stage completes on its `full` barrier and is handed
-// back by one arrival of every consumer warp on its `empty` barrier.  The producer
-// runs ahead of the consumers over the row's end, so the copies of the next row are in
-// flight while the consumers finish this one.
+// back by one arrival of every consumer warp on its `empty` barrier.  It runs ahead of the
+// consumers over the row's end.  The consumers leave each row's partial results in one of
+// a few buffers and go on to the next row; a closing warp joins them, with the cluster's
+// other CTAs if a row is shared, and does what a row needs once (logarithms, gathers, top
+// tokens), so that neither the copies nor the sums wait for it.  That work is a chain of
+// latencies: several closing warps take rows in turn.
 //
 // Each thread keeps running sums (of 2^d and d 2^d) below a maximum that its warp shares:
 // one warp-wide reduction a chunk, and a rescaling only when the warp meets a new maximum
@@ -29,7 +33,9 @@ namespace foak {
 
 constexpr int kStreamThreads = 256;                       // consumers
 constexpr int kStreamWarps = kStreamThreads / 32;
-constexpr int kStreamBlock = kStreamThreads + 32;         // and the producer warp
+constexpr int kStreamBlock = kStreamThreads + 64;         // and the producer and one closing warp
+constexpr int kFirstCloser = kStreamThreads + 32;         // the first closing warp's first thread
+constexpr int kMaxBuffers = 4;                            // rows between the consumers and the closing warps
 constexpr int kBlockVec = 4;                              // a thread's vectors of a chunk: one 64-byte block
 constexpr int kStreamChunk = kStreamThreads * kBlockVec;  // vectors of a chunk (16 KB)
 constexpr uint32_t kStreamStageBytes = kStreamChunk * 16;
@@ -46,6 +52,7 @@ struct StreamSrc {
     uint64_t wait_ns;       // limit of every shared-memory barrier wait
     int64_t skip_load_row;  // test hook: this row's first chunk is never loaded (-1: none)
     int k, log2_k;          // CTAs of a row's cluster
+    int log2_buffers;
     int stages;
 };
 
@@ -64,6 +71,12 @@ __device__ __forceinline__ uint32_t bf16x2_max_nan(uint32_t a, uint32_t b) {
 __device__ __forceinline__ void consumers_sync() {
     __syncwarp();
     asm volatile("bar.sync 1, %0;" ::"n"(kStreamThreads) : "memory");
+}
+// Consumers (who do not wait) and closing warp (which does): the number of valid rows is in shared memory.
+__device__ __forceinline__ void scale_known() {
+    __syncwarp();
+    if (threadIdx.x < kStreamThreads) asm volatile("bar.arrive 2, %0;" ::"n"(kStreamThreads + 32) : "memory");
+    else asm volatile("bar.sync 2, %0;" ::"n"(kStreamThreads + 32) : "memory");
 }
 // The cluster's barrier, from code whose lanes may have parted.
 __device__ __forceinline__ void cluster_sync_converged() {
@@ -124,14 +137,26 @@ __device__ __forceinline__ void move_slice(const StreamSrc& p, int64_t row, int 
 struct StreamBars {
     uint64_t full[kStreamMaxStages];
     uint64_t empty[kStreamMaxStages];
-    int abort;  // a wait gave up: everyone stops waiting and winds down
+    uint64_t row_full[kMaxBuffers];    // the consumers' part of a row is in its buffer: one arrival a consumer warp
+    uint64_t row_empty[kMaxBuffers];   // the closing warp has taken it
+    uint64_t row_ready[kMaxBuffers];   // the closing warp has what the second sweep needs
+    uint64_t row_stored[kMaxBuffers];  // the second sweep's stores are made: one arrival a consumer warp
+    uint64_t peers[kMaxBuffers];       // the cluster's CTAs have sent their part: one arrival a CTA
+    int abort;              // a wait gave up: everyone stops waiting and winds down
 };
 
-__device__ __forceinline__ void stream_init(StreamBars& b, int stages) {
+__device__ __forceinline__ void stream_init(StreamBars& b, int stages, int cluster) {
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; ++s) {
             mbar_init(&b.full[s], 1);
             mbar_init(&b.empty[s], kStreamWarps);
+        }
+        for (int i = 0; i < kMaxBuffers; ++i) {
+            mbar_init(&b.row_full[i], kStreamWarps);
+            mbar_init(&b.row_empty[i], 1);
+            mbar_init(&b.row_ready[i], 1);
+            mbar_init(&b.row_stored[i], kStreamWarps);
+            mbar_init(&b.peers[i], cluster);
         }
         b.abort = 0;
         fence_mbar_init();
@@ -157,11 +182,9 @@ __device__ __forceinline__ bool stream_wait(StreamBars& b, uint64_t* bar, uint32
 }
 
 // The producer warp: rows cid, cid + ncl, ...; every valid row's chunks `passes` times.
-// row_syncs: cluster barriers the consumers pass in every valid row (0 without a
-// cluster); the producer warp takes part in them.
 template <int ES>
 __device__ __forceinline__ void stream_produce(const StreamSrc& p, StreamBars& bars, unsigned char* ring, int passes,
-                                               int64_t cid, int64_t ncl, int rank, int row_syncs) {
+                                               int64_t cid, int64_t ncl, int rank) {
     const int lane = threadIdx.x & 31;
     const int64_t n_it = p.N > cid ? (p.N - 1 - cid) / ncl + 1 : 0;
     const uint32_t S = static_cast<uint32_t>(p.stages);
@@ -206,7 +229,6 @@ __device__ __forceinline__ void stream_produce(const StreamSrc& p, StreamBars& b
                 }
             }
             __syncwarp();
-            for (int i = 0; i < row_syncs; ++i) cluster_sync();
         }
     }
     // the CTA must not end, nor its shared memory be given away, under a copy in flight
@@ -237,6 +259,51 @@ __device__ __forceinline__ void stream_chunk(const StreamSrc& p, StreamBars& bar
     if (++pos.st == static_cast<uint32_t>(p.stages)) {
         pos.st = 0;
         pos.par ^= 1u;
+    }
+}
+
+// A row's place in the exchange between the consumers and the closing warps.
+struct RowPos {
+    uint32_t n = 0;  // valid rows so far
+    __device__ __forceinline__ int buf(const StreamSrc& p) const { return n & ((1u << p.log2_buffers) - 1u); }
+    __device__ __forceinline__ uint32_t use(const StreamSrc& p) const { return n >> p.log2_buffers; }  // of the buffer
+};
+// Consumers, before they write into the row's buffer: its last use is taken.
+__device__ __forceinline__ void row_begin(const StreamSrc& p, StreamBars& bars, const RowPos& row, StreamPos& pos) {
+    const uint32_t use = row.use(p);
+    if (use > 0 && !pos.aborted && !stream_wait(bars, &bars.row_empty[row.buf(p)], (use & 1u) ^ 1u, p.wait_ns))
+        pos.aborted = true;
+}
+// Consumers: the warp's part of the row is written.
+__device__ __forceinline__ void row_end(StreamBars& bars, int buf) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&bars.row_full[buf]);
+}
+
+// One arrival on the barrier `bar` of another CTA of the cluster, releasing this thread's writes to it.
+__device__ __forceinline__ void remote_arrive(uint64_t* bar, uint32_t rank) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapa_u32(bar, rank)) : "memory");
+}
+// Bounded wait for the cluster's arrivals, acquiring what they released.
+__device__ __forceinline__ bool peers_wait(StreamBars& b, uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t i = 1;; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if ((i & 255u) == 0) {
+            if (stream_aborted(b)) return false;
+            if (globaltimer_ns() - t0 > limit_ns) {
+                b.abort = 1;
+                return false;
+            }
+        }
     }
 }
 
@@ -432,23 +499,23 @@ struct RunStat {
 
 // Shared memory through which the consumers' (and the cluster's) sets meet.
 struct StatExchange {
-    float4 warp[2][kStreamWarps];      // (m, s, a, s2), by row parity
-    float4 cta[2][kStreamMaxCluster];  // the cluster's CTAs' sets, by row parity
+    float4 warp[kMaxBuffers][kStreamWarps];         // (m, s, a, s2), by row buffer
+    float4 cta[kMaxBuffers][2][kStreamMaxCluster];  // the cluster's CTAs' sets, by buffer and parity of its use
 };
 
 // Every warp's set put into the exchange; a consumer barrier has to follow.
 template <bool ENT, bool TWO>
-__device__ __forceinline__ void stat_publish(RunStat<ENT, TWO>& st, StatExchange& ex, uint32_t parity) {
+__device__ __forceinline__ void stat_publish(RunStat<ENT, TWO>& st, StatExchange& ex, int buf) {
     st.s = warp_sum(st.s);
     if (ENT) st.a = warp_sum(st.a);
     if (TWO) st.s2 = warp_sum(st.s2);
-    if ((threadIdx.x & 31) == 0) ex.warp[parity][threadIdx.x >> 5] = make_float4(st.m, st.s, st.a, st.s2);
+    if ((threadIdx.x & 31) == 0) ex.warp[buf][threadIdx.x >> 5] = make_float4(st.m, st.s, st.a, st.s2);
 }
 // The CTA's set from its warps', by whole warps; every lane gets it.
 template <bool ENT, bool TWO>
-__device__ __forceinline__ void stat_collect(RunStat<ENT, TWO>& st, const StatExchange& ex, uint32_t parity,
+__device__ __forceinline__ void stat_collect(RunStat<ENT, TWO>& st, const StatExchange& ex, int buf,
                                              const ExpScale& x) {
-    st.set(ex.warp[parity][threadIdx.x & (kStreamWarps - 1)], x);
+    st.set(ex.warp[buf][threadIdx.x & (kStreamWarps - 1)], x);
     st.raise(warp_max_redux(st.m), x);
 #pragma unroll
     for (int off = kStreamWarps / 2; off > 0; off >>= 1) {
@@ -457,21 +524,32 @@ __device__ __forceinline__ void stat_collect(RunStat<ENT, TWO>& st, const StatEx
         if (TWO) st.s2 += __shfl_xor_sync(0xffffffffu, st.s2, off);
     }
 }
-// In a cluster: the CTA's set to every CTA (by warp 0), then, after a cluster barrier, the row's from all.
+// In a cluster, by the closing warps of a row: this CTA's set to every CTA, then the row's
+// from all.  A slot's next use but one follows an exchange that every CTA enters only after
+// it has read the slot.
+__device__ __forceinline__ bool peers_meet(StreamBars& bars, int buf, uint32_t phase, int k, uint64_t limit_ns) {
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+    if (lane < k) remote_arrive(&bars.peers[buf], static_cast<uint32_t>(lane));
+    __syncwarp();
+    return peers_wait(bars, &bars.peers[buf], phase & 1u, limit_ns);
+}
 template <bool ENT, bool TWO>
-__device__ __forceinline__ void stat_send(const RunStat<ENT, TWO>& st, StatExchange& ex, uint32_t parity, int k, int rank) {
-    if (threadIdx.x < static_cast<unsigned>(k)) {
-        const uint32_t to = mapa_u32(&ex.cta[parity][rank], threadIdx.x);
+__device__ __forceinline__ bool stat_cluster(RunStat<ENT, TWO>& st, StatExchange& ex, StreamBars& bars, int buf,
+                                             uint32_t use, uint32_t phase, int k, int rank, const ExpScale& x,
+                                             uint64_t limit_ns) {
+    const int lane = threadIdx.x & 31;
+    if (lane < k) {
+        const uint32_t to = mapa_u32(&ex.cta[buf][use & 1u][rank], static_cast<uint32_t>(lane));
         asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(st.m), "f"(st.s), "f"(st.a),
                      "f"(st.s2)
                      : "memory");
     }
-}
-template <bool ENT, bool TWO>
-__device__ __forceinline__ void stat_merge(RunStat<ENT, TWO>& st, const StatExchange& ex, uint32_t parity, int k,
-                                           const ExpScale& x) {
-    st.set(ex.cta[parity][0], x);
-    for (int o = 1; o < k; ++o) st.merge(ex.cta[parity][o], x);
+    if (!peers_meet(bars, buf, phase, k, limit_ns)) return false;
+    const float4* from = ex.cta[buf][use & 1u];
+    st.set(from[0], x);
+    for (int o = 1; o < k; ++o) st.merge(from[o], x);
+    return true;
 }
 
 // Number of valid labels, counted by the consumer threads; scratch: kStreamWarps ints.

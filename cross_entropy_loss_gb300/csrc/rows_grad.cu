@@ -245,7 +245,10 @@ __global__ void __launch_bounds__(kGradThreads, kGradBlocksPerSm) distill_grad_k
             const float x = is_label ? s_xy : teach.x[j];
             float lo, hi;
             f2_unpack(grad(f2_pack(x, x)), lo, hi);
-            lo -= wt * teacher_mass(teach, p.teacher.K, static_cast<int>(id));
+            const int one[1] = {static_cast<int>(id)};
+            float mass[1];
+            teacher_mass(teach, p.teacher.K, one, mass);
+            lo -= wt * mass[0];
             if (id == y) lo -= w1;
             store_scalar<ES>(s.drow + id * ES, lo);
         }

@@ -18,8 +18,8 @@ struct TeacherSrc {
 };
 
 struct TeacherRow {
-    int id[kTeacherMax];     // -1: no entry
-    float q[kTeacherMax];
+    alignas(16) int id[kTeacherMax];   // -1: no entry (also past K, up to a multiple of 4)
+    alignas(16) float q[kTeacherMax];
     float lnq[kTeacherMax];
     float x[kTeacherMax];    // the student's logit of the token (only where col_lo <= id < col_hi)
     float total;             // sum of q
@@ -49,6 +49,10 @@ __device__ __forceinline__ bool teacher_row(const TeacherSrc& p, int64_t row, in
             if (there) t[j] = v;
             if (there && id >= col_lo && id < col_hi) out.x[k] = load_scalar<ES>(rowp + static_cast<int64_t>(id) * ES);
         }
+        if (k >= p.K && k < (p.K + 3) / 4 * 4) {
+            out.id[k] = -1;
+            out.q[k] = 0.f;
+        }
         top = fmaxf(top, t[j]);
     }
     top = warp_max(top);
@@ -73,11 +77,19 @@ __device__ __forceinline__ bool teacher_row(const TeacherSrc& p, int64_t row, in
     return __any_sync(0xffffffffu, bad);
 }
 
-// Sum of q over the entries with this id (an id may be listed more than once).
-__device__ __forceinline__ float teacher_mass(const TeacherRow& t, int K, int id) {
-    float s = 0.f;
-    for (int k = 0; k < K; ++k) s += t.id[k] == id ? t.q[k] : 0.f;
-    return s;
+// Sums of q over the entries with each of these ids (an id may be listed more than once).
+template <int N>
+__device__ __forceinline__ void teacher_mass(const TeacherRow& t, int K, const int (&id)[N], float (&mass)[N]) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) mass[n] = 0.f;
+    for (int k = 0; k < K; k += 4) {
+        const int4 i = *reinterpret_cast<const int4*>(t.id + k);
+        const float4 q = *reinterpret_cast<const float4*>(t.q + k);
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            mass[n] += ((i.x == id[n] ? q.x : 0.f) + (i.y == id[n] ? q.y : 0.f)) +
+                       ((i.z == id[n] ? q.z : 0.f) + (i.w == id[n] ? q.w : 0.f));
+    }
 }
 
 }  // namespace foak
