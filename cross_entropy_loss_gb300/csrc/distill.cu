@@ -38,41 +38,64 @@ struct DistillParams {
     float4* stats;     // [N] or null: (m, ln sum e^(x-m), ln sum e^((x-m)/T), Q)
 };
 
-// What the second sweep takes from the closing warp: the maximum, and the factors of the two exponentials.
+// What the second sweep works with: the maximum, and the factors of the two exponentials.
 struct SweepFactors {
     float m, a, a1;
 };
+template <bool TWO>
+__device__ __forceinline__ SweepFactors sweep_factors(const RunStat<false, TWO>& st, float total, float w1, float wt) {
+    const float s1 = TWO ? st.s2 : st.s;  // at T = 1 they are the same; without w_ce it is not used
+    SweepFactors f;
+    f.m = st.m;
+    const float at = st.s == 0.f ? 0.f : wt * total / st.s;  // nothing but -inf: p = 0
+    f.a1 = w1 != 0.f && s1 != 0.f ? w1 / s1 : 0.f;
+    f.a = TWO ? at : at + f.a1;
+    return f;
+}
 
-template <int ES, bool GRAD, bool TWO>
-__global__ void __launch_bounds__(kStreamBlock, 3) distill_kernel(const DistillParams p) {
+// Closing warps of a CTA, which take rows in turn.
+template <int NT>
+constexpr int kClosers = NT == 512 ? 2 : 1;
+template <int NT>
+constexpr int kDistillThreads = NT + 32 + 32 * kClosers<NT>;
+
+template <int ES, bool GRAD, bool TWO, int NT>
+__global__ void __launch_bounds__(kDistillThreads<NT>, NT == 256 ? 3 : 1) distill_kernel(const DistillParams p) {
     constexpr int EPV = 16 / ES;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ StreamBars bars;
     __shared__ StatExchange ex;
-    __shared__ TeacherRow teach;
+    __shared__ TeacherRow teacher[kClosers<NT>];
     __shared__ SweepFactors factors[kMaxBuffers];
-    __shared__ int s_count[kStreamWarps];
+    __shared__ float total[kMaxBuffers];  // of the teacher's row
+    __shared__ int s_count[kMaxWarps];
     __shared__ int s_valid, s_bad, s_last;
-    __shared__ DFloat dred[kStreamBlock / 32];
+    __shared__ DFloat dred[kDistillThreads<NT> / 32];
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = p.src.k;
     const int rank = k > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int64_t cid = blockIdx.x >> p.src.log2_k, ncl = gridDim.x >> p.src.log2_k;
     const int64_t n_it = p.src.N > cid ? (p.src.N - 1 - cid) / ncl + 1 : 0;
-    stream_init(bars, p.src.stages, k);
+    stream_init<NT>(bars, p.src.stages, k);
+    if (tid == 0) s_bad = 0;
     griddep_launch_dependents();  // programmatic dependent launch: no global access before the wait
     griddep_wait();
     __syncthreads();
     if (k > 1) cluster_sync();  // every CTA's shared memory is there to be written to
 
     const ExpScale& sc = p.scale;
-    if (warp == kStreamWarps) {
-        stream_produce<ES>(p.src, bars, smem, GRAD ? 2 : 1, cid, ncl, rank);
-    } else if (warp < kStreamWarps) {
-        if (GRAD && p.fin.denom <= 0.f) {
-            const int n = count_valid_consumers(p.src, s_count);
-            if (tid == 0) s_valid = n;
-            scale_known();
+    if (warp == Shape<NT>::kWarps) {
+        stream_produce<ES, NT>(p.src, bars, smem, GRAD ? 2 : 1, cid, ncl, rank);
+    } else if (warp < Shape<NT>::kWarps) {
+        float scale = 0.f;
+        if (GRAD) {
+            scale = p.g / p.fin.denom;
+            if (p.fin.denom <= 0.f) {
+                const int n = count_valid_consumers<NT>(p.src, s_count);
+                scale = p.g / static_cast<float>(n);
+                if (tid == 0) s_valid = n;
+                scale_known<NT, kClosers<NT>>();
+            }
         }
         StreamPos pos{0, 0, false};
         RowPos rp;
@@ -88,20 +111,18 @@ __global__ void __launch_bounds__(kStreamBlock, 3) distill_kernel(const DistillP
             if (!stream_row_valid(y, p.src)) {
                 if constexpr (GRAD) {
                     const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-                    for (int i = tid; i < s.nv; i += kStreamThreads) st_global_cs_v4(dv + i, z);
+                    for (int i = tid; i < s.nv; i += NT) st_global_cs_v4(dv + i, z);
                     if (tid < s.h) store_scalar<ES>(drow + tid * ES, 0.f);
                     if (tid < s.t) store_scalar<ES>(drow + (s.tail_col + tid) * ES, 0.f);
                 }
                 continue;
             }
-            // With a second sweep the buffer's last use is long over: the sweep before this row waited for
-            // the closing warp.
-            if (!GRAD) row_begin(p.src, bars, rp, pos);
+            row_begin(p.src, bars, rp, pos);
             RunStat<false, TWO> st(sc);
-            for (int c0 = 0; c0 < s.nv; c0 += kStreamChunk) {
-                const int nl = min(kStreamChunk, s.nv - c0);
+            for (int c0 = 0; c0 < s.nv; c0 += Shape<NT>::kChunk) {
+                const int nl = min(Shape<NT>::kChunk, s.nv - c0);
                 uint4 v[kBlockVec];
-                stream_chunk(p.src, bars, smem, pos, [&](const unsigned char* stage) { load_strided<ES>(stage, nl, v); });
+                stream_chunk<NT>(p.src, bars, smem, pos, [&](const unsigned char* stage) { load_strided<ES, NT>(stage, nl, v); });
                 st.template add_vecs<ES>(v, sc);
             }
             // the head and tail scalars, one a lane of the first warp; kept for the gradient
@@ -118,7 +139,17 @@ __global__ void __launch_bounds__(kStreamBlock, 3) distill_kernel(const DistillP
             if constexpr (GRAD) {
                 if (!pos.aborted && !stream_wait(bars, &bars.row_ready[buf], rp.use(p.src) & 1u, p.src.wait_ns))
                     pos.aborted = true;
-                const SweepFactors f = factors[buf];
+                SweepFactors f;
+                if (k == 1) {
+                    // Every warp joins the row's sums for itself: no way to the closing warp and back.
+                    if (!pos.aborted && !stream_wait(bars, &bars.row_full[buf], rp.use(p.src) & 1u, p.src.wait_ns))
+                        pos.aborted = true;
+                    stat_collect<NT>(st, ex, buf, sc);
+                    st.correct(sc);
+                    f = sweep_factors(st, total[buf], scale * p.ce_w, scale * p.kd_w * p.inv_t);
+                } else {
+                    f = factors[buf];
+                }
                 const f32x2_t M = f2_pack(-f.m, -f.m), C = f2_pack(sc.c, sc.c), L = f2_pack(kLog2e, kLog2e);
                 const f32x2_t A = f2_pack(f.a, f.a), A1 = f2_pack(f.a1, f.a1);
                 auto grad = [&](f32x2_t x) {
@@ -127,10 +158,10 @@ __global__ void __launch_bounds__(kStreamBlock, 3) distill_kernel(const DistillP
                     if (TWO) e = f2_fma(f2_ex2(f2_mul(d, L)), A1, e);
                     return e;
                 };
-                for (int c0 = 0; c0 < s.nv; c0 += kStreamChunk) {
-                    const int nl = min(kStreamChunk, s.nv - c0);
+                for (int c0 = 0; c0 < s.nv; c0 += Shape<NT>::kChunk) {
+                    const int nl = min(Shape<NT>::kChunk, s.nv - c0);
                     uint4 v[kBlockVec];
-                    stream_chunk(p.src, bars, smem, pos, [&](const unsigned char* stage) { load_strided<ES>(stage, nl, v); });
+                    stream_chunk<NT>(p.src, bars, smem, pos, [&](const unsigned char* stage) { load_strided<ES, NT>(stage, nl, v); });
                     if (pos.aborted) continue;
 #pragma unroll
                     for (int i = 0; i < kBlockVec; ++i) {
@@ -147,8 +178,8 @@ __global__ void __launch_bounds__(kStreamBlock, 3) distill_kernel(const DistillP
                                 o[2 * j + 1] = __float_as_uint(hi);
                             }
                         }
-                        const int lv = tid + i * kStreamThreads;
-                        if (nl == kStreamChunk || lv < nl) st_global_cs_v4(dv + c0 + lv, make_uint4(o[0], o[1], o[2], o[3]));
+                        const int lv = tid + i * NT;
+                        if (nl == Shape<NT>::kChunk || lv < nl) st_global_cs_v4(dv + c0 + lv, make_uint4(o[0], o[1], o[2], o[3]));
                     }
                 }
                 if (tid < n_edge && !pos.aborted) {
@@ -161,36 +192,39 @@ __global__ void __launch_bounds__(kStreamBlock, 3) distill_kernel(const DistillP
             }
             ++rp.n;
         }
-    } else {  // the closing warp
+    } else {  // a closing warp
+        const uint32_t me = warp - (Shape<NT>::kWarps + 1), turn = kClosers<NT> - 1;
+        TeacherRow& teach = teacher[me];
         float scale = 0.f;
         if (GRAD) {
-            if (p.fin.denom <= 0.f) scale_known();
+            if (p.fin.denom <= 0.f) scale_known<NT, kClosers<NT>>();
             scale = p.g / (p.fin.denom > 0.f ? p.fin.denom : static_cast<float>(s_valid));
         }
         const float w1 = scale * p.ce_w, wt = scale * p.kd_w * p.inv_t;
         const int K = p.teacher.K;
         RowPos rp;
         Slice s = slice_of<ES>(p.src, cid, rank);
-        int n_valid = 0, n_bad = 0;
+        int n_bad = 0;
         bool aborted = false;
         for (int64_t base = 0; base < n_it; base += 32) {
-            // 32 rows' labels and their logits at once, a row a lane.  (A row's gradient is not begun before
-            // this warp has made it ready, so the logits are still there.)
+            // 32 rows' labels at once, and the logits of this warp's rows, a row a lane.  (A row's gradient is
+            // not begun before its closing warp has made it ready, so the logits are still there.)
             int64_t lab = 0;
-            float x_lab = 0.f;
-            if (p.src.labels && base + lane < n_it) {
-                const int64_t row = cid + (base + lane) * ncl;
-                lab = __ldg(p.src.labels + row);
-                if (stream_row_valid(lab, p.src)) x_lab = load_scalar<ES>(p.src.x + (row * p.src.ld + lab) * ES);
-                else n_bad += lab != p.src.ignore_index;
+            bool ok = false;
+            if (base + lane < n_it) {
+                if (p.src.labels) lab = __ldg(p.src.labels + cid + (base + lane) * ncl);
+                ok = stream_row_valid(lab, p.src);
+                n_bad += !ok && lab != p.src.ignore_index && me == 0;
             }
+            const unsigned valid = __ballot_sync(0xffffffffu, ok);
+            float x_lab = 0.f;
+            if (p.src.labels && ok && ((rp.n + __popc(valid & ((1u << lane) - 1u))) & turn) == me)
+                x_lab = load_scalar<ES>(p.src.x + ((cid + (base + lane) * ncl) * p.src.ld + lab) * ES);
             const int nj = static_cast<int>(min(static_cast<int64_t>(32), n_it - base));
             for (int j = 0; j < nj; ++j) {
                 const int64_t row = cid + (base + j) * ncl;
-                const int64_t y = __shfl_sync(0xffffffffu, lab, j);
-                const float x_y = __shfl_sync(0xffffffffu, x_lab, j);
-                if (!stream_row_valid(y, p.src)) {
-                    if (rank == 0 && lane == 0) {
+                if (!(valid >> j & 1u)) {
+                    if (rank == 0 && me == 0 && lane == 0) {
                         p.fin.row_loss[row] = 0.f;
                         if (p.row_ce) p.row_ce[row] = 0.f;
                         if (p.row_kd) p.row_kd[row] = 0.f;
@@ -198,39 +232,38 @@ __global__ void __launch_bounds__(kStreamBlock, 3) distill_kernel(const DistillP
                     }
                     continue;
                 }
-                ++n_valid;
+                if ((rp.n & turn) != me) {
+                    ++rp.n;
+                    continue;
+                }
+                const int64_t y = p.src.labels ? __shfl_sync(0xffffffffu, lab, j) : -1;
+                const float x_y = __shfl_sync(0xffffffffu, x_lab, j);
+                const int buf = rp.buf(p.src);
+                const uint32_t use = rp.use(p.src);
                 move_slice<ES>(p.src, row, rank, s);
                 const int64_t col_lo = rank == 0 ? 0 : s.col0;
                 const int64_t col_hi = rank == k - 1 ? p.src.V : s.col0 + static_cast<int64_t>(s.nv) * EPV;
                 // rank 0 takes all the listed logits (for the loss), the others those of their share
-                __syncwarp();
                 const bool bad = teacher_row<ES>(p.teacher, row, p.src.V, s.rowp, rank == 0 ? 0 : col_lo,
                                                  rank == 0 ? p.src.V : col_hi, teach);
-                __syncwarp();
-                if (lane == 0) n_bad += bad;
-                const int buf = rp.buf(p.src);
-                const uint32_t use = rp.use(p.src);
+                n_bad += bad && lane == 0;
+                if (GRAD && k == 1 && lane == 0) {  // all that the second sweep needs from here
+                    total[buf] = teach.total;
+                    mbar_arrive(&bars.row_ready[buf]);
+                }
                 if (!aborted && !stream_wait(bars, &bars.row_full[buf], use & 1u, p.src.wait_ns)) aborted = true;
                 RunStat<false, TWO> st(sc);
-                stat_collect(st, ex, buf, sc);
-                if (!GRAD) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars.row_empty[buf]);
-                }
+                stat_collect<NT>(st, ex, buf, sc);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.row_empty[buf]);
                 if (k > 1 && !stat_cluster(st, ex, bars, buf, use, use, k, rank, sc, aborted ? 0 : p.src.wait_ns)) aborted = true;
                 st.correct(sc);
-                const bool empty = st.s == 0.f;  // nothing but -inf: p = 0, and every token's log probability is -inf
-                const float s1 = TWO ? st.s2 : st.s;  // at T = 1 they are the same; without w_ce it is not used
-                SweepFactors f;
-                f.m = st.m;
-                const float at = empty ? 0.f : wt * teach.total / st.s;
-                f.a1 = p.ce_w != 0.f && s1 != 0.f ? w1 / s1 : 0.f;
-                f.a = TWO ? at : at + f.a1;
-                if (GRAD) {
-                    if (lane == 0) {
-                        factors[buf] = f;
-                        mbar_arrive(&bars.row_ready[buf]);
-                    }
+                const bool empty = st.s == 0.f;  // nothing but -inf: every token's log probability is -inf
+                const float s1 = TWO ? st.s2 : st.s;
+                const SweepFactors f = sweep_factors(st, teach.total, w1, wt);
+                if (GRAD && k > 1 && lane == 0) {
+                    factors[buf] = f;
+                    mbar_arrive(&bars.row_ready[buf]);
                 }
                 if (rank == 0 && !aborted) {
                     const float ln_t = logf(st.s), ln_1 = logf(s1);
@@ -250,80 +283,47 @@ __global__ void __launch_bounds__(kStreamBlock, 3) distill_kernel(const DistillP
                 }
                 if constexpr (GRAD) {
                     // The K + 1 places that differ, after the consumers' stores of the row.
-                    auto grad_at = [&](float x) {
-                        const float d = x - f.m;
-                        float e = ex2(d * sc.c) * f.a;
-                        if (TWO) e = fmaf(ex2(d * kLog2e), f.a1, e);
-                        return e;
-                    };
-                    constexpr int OWN = 4;
-                    bool waited = false, listed = false;
-                    char* drow = p.dx + row * p.src.ld * ES;
-                    for (int i0 = 0; i0 < K; i0 += 32 * OWN) {
-                        int id[OWN];
-                        float mass[OWN];
-#pragma unroll
-                        for (int q = 0; q < OWN; ++q) {
-                            id[q] = i0 + 32 * q + lane < K ? teach.id[i0 + 32 * q + lane] : -1;
-                            if (id[q] < col_lo || id[q] >= col_hi) id[q] = -1;
-                        }
-                        // a token listed twice gets the same value from each of its places
-                        teacher_mass(teach, K, id, mass);
-                        if (!waited) {
-                            if (!aborted && !stream_wait(bars, &bars.row_stored[buf], use & 1u, p.src.wait_ns)) aborted = true;
-                            waited = true;
-                        }
-#pragma unroll
-                        for (int q = 0; q < OWN; ++q) {
-                            if (id[q] < 0 || aborted) continue;
-                            float e = grad_at(teach.x[i0 + 32 * q + lane]) - wt * mass[q];
-                            if (p.src.labels && id[q] == y) {
-                                e -= w1;
-                                listed = true;
-                            }
-                            store_scalar<ES>(drow + static_cast<int64_t>(id[q]) * ES, e);
-                        }
+                    if (!aborted && !stream_wait(bars, &bars.row_stored[buf], use & 1u, p.src.wait_ns)) aborted = true;
+                    if (!aborted) {
+                        teacher_correct<ES>(teach, K, col_lo, col_hi, y, x_y, w1, wt, p.dx + row * p.src.ld * ES, [&](float x) {
+                            const float d = x - f.m;
+                            float e = ex2(d * sc.c) * f.a;
+                            if (TWO) e = fmaf(ex2(d * kLog2e), f.a1, e);
+                            return e;
+                        });
                     }
-                    listed = __any_sync(0xffffffffu, listed);
-                    if (lane == 0 && p.src.labels && !listed && y >= col_lo && y < col_hi && !aborted)
-                        store_scalar<ES>(drow + y * ES, grad_at(x_y) - w1);
                 }
+                __syncwarp();
                 ++rp.n;
             }
         }
         n_bad = __reduce_add_sync(0xffffffffu, n_bad);
         if (lane == 0) {
-            s_valid = rank == 0 ? n_valid : 0;
-            s_bad = rank == 0 ? n_bad : 0;
+            if (me == 0) s_valid = rank == 0 ? static_cast<int>(rp.n) : 0;
+            if (rank == 0 && n_bad) atomicAdd(&s_bad, n_bad);
             if (aborted) bars.abort = 1;
         }
     }
     __syncthreads();
-    rows_finish<kStreamBlock>(p.fin, stream_aborted(bars), s_valid, s_bad, &s_last, dred, true);
+    rows_finish<kDistillThreads<NT>>(p.fin, stream_aborted(bars), s_valid, s_bad, &s_last, dred, true);
     if (k > 1) cluster_sync_converged();  // no CTA leaves while its shared memory may be written
 }
 
 std::mutex g_ds_mu;
 std::map<std::pair<int, const void*>, size_t> g_ds_attr;  // (device, kernel): dynamic shared memory allowed
 
-template <int ES, bool GRAD, bool TWO>
-cudaError_t launch_typed(DistillParams prm, cudaStream_t stream) {
-    auto* kern = &distill_kernel<ES, GRAD, TWO>;
+template <int ES, bool GRAD, bool TWO, int NT>
+cudaError_t launch_typed(DistillParams prm, int per_sm, cudaStream_t stream) {
+    auto* kern = &distill_kernel<ES, GRAD, TWO, NT>;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     StreamSrc& s = prm.src;
-    const int sms = device_sm_count();
-    const int64_t nb = s.V * ES / 16 + 1;
-    int k = kStreamMaxCluster;
-    while (k > 1 && (s.N * k > sms || 2 * nb < static_cast<int64_t>(k) * kStreamChunk)) k /= 2;
-    set_cluster(s, k);
     s.log2_buffers = 1;
-    const size_t fixed = 1024 + sizeof(StreamBars) + sizeof(StatExchange) + sizeof(TeacherRow) + 512;
-    const int per_sm = 3;
-    const size_t room = (228 * 1024) / per_sm - fixed;
-    s.stages = static_cast<int>(std::min<size_t>(kStreamMaxStages, room / kStreamStageBytes));
-    const size_t smem = static_cast<size_t>(s.stages) * kStreamStageBytes;
+    const size_t fixed = 1024 + 512 + sizeof(StreamBars) + sizeof(StatExchange) + kClosers<NT> * sizeof(TeacherRow);
+    const size_t room = std::min<size_t>((228 * 1024) / per_sm, 227 * 1024) - fixed;
+    s.stages = static_cast<int>(std::min<size_t>(kStreamMaxStages, room / Shape<NT>::kStageBytes));
+    const size_t smem = static_cast<size_t>(s.stages) * Shape<NT>::kStageBytes;
     {
         std::lock_guard<std::mutex> lock(g_ds_mu);
         size_t& set = g_ds_attr[std::make_pair(dev, reinterpret_cast<const void*>(kern))];
@@ -333,10 +333,10 @@ cudaError_t launch_typed(DistillParams prm, cudaStream_t stream) {
             set = smem;
         }
     }
-    const int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(s.N, static_cast<int64_t>(sms) * per_sm / s.k));
+    const int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(s.N, static_cast<int64_t>(device_sm_count()) * per_sm / s.k));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(clusters * s.k), 1, 1);
-    cfg.blockDim = dim3(kStreamBlock, 1, 1);
+    cfg.blockDim = dim3(kDistillThreads<NT>, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -350,11 +350,32 @@ cudaError_t launch_typed(DistillParams prm, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, kern, prm);
 }
 
+template <int ES, bool GRAD, bool TWO>
+cudaError_t launch_shape(DistillParams p, cudaStream_t stream) {
+    StreamSrc& s = p.src;
+    const int sms = device_sm_count();
+    const int64_t nb = s.V * ES / 16 + 1;
+    // Few rows: a cluster per row, as long as its CTAs are all on SMs of their own and
+    // have at least half a chunk each.
+    int k = kStreamMaxCluster;
+    while (k > 1 && (s.N * k > sms || 2 * nb < static_cast<int64_t>(k) * Shape<256>::kChunk)) k /= 2;
+    set_cluster(s, k);
+    int per_sm = 3;
+    if constexpr (GRAD) {
+        // The rows between their two sweeps wait in L2 (129 MB, which the gradient's lines share): CTAs of
+        // an SM while those rows stay within 64 MB, then one CTA of twice the threads.
+        while (per_sm > 1 && static_cast<double>(sms) * per_sm / k * static_cast<double>(s.V) * ES > 64e6) --per_sm;
+        s.evict_last_pass = true;
+        if (per_sm == 1 && k == 1) return launch_typed<ES, GRAD, TWO, 512>(p, 1, stream);
+    }
+    return launch_typed<ES, GRAD, TWO, 256>(p, per_sm, stream);
+}
+
 template <int ES, bool GRAD>
 cudaError_t launch_two(const DistillParams& p, float temperature, cudaStream_t stream) {
     // a second sum only where both parts are wanted at different temperatures
-    return p.ce_w != 0.f && temperature != 1.f ? launch_typed<ES, GRAD, true>(p, stream)
-                                               : launch_typed<ES, GRAD, false>(p, stream);
+    return p.ce_w != 0.f && temperature != 1.f ? launch_shape<ES, GRAD, true>(p, stream)
+                                               : launch_shape<ES, GRAD, false>(p, stream);
 }
 
 }  // namespace

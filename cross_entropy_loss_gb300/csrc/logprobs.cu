@@ -34,6 +34,8 @@ namespace {
 constexpr int kListCap = 512;   // listed elements of a row (or of a CTA's share of it): at least kTopKMax
 constexpr int kSelCap = 256;    // blocks they are taken from
 constexpr int kAll = 0x7fffffff;
+constexpr int kThreads = 256;   // consumers
+using Sh = Shape<kThreads>;
 constexpr int kKeyBody = 8;     // place of the first body block's key; before it the head's and the tail's
 // Closing warps of a CTA.  The work on a row's top tokens is a chain of some 6000 cycles
 // (K = 20), so four take rows in turn; without top tokens one keeps up.
@@ -245,14 +247,14 @@ __device__ __noinline__ int top_list(const Slice s, const typename BlockKey<ES>:
                                         const uint32_t* thread_max, int K, TopScratch& t) {
     using BK = BlockKey<ES>;
     constexpr int EPV = 16 / ES;
-    constexpr int PER = kStreamThreads / 32;
+    constexpr int PER = kThreads / 32;
     const int lane = threadIdx.x & 31;
     const int nblk = (s.nv + kBlockVec - 1) / kBlockVec;
     // A threshold that K threads' maxima, so K blocks, reach: the K-th largest of the 256
     // thread maxima, or a little below it.  Of blocks in random order about
     // -256 ln(1 - K / 256) are at or above it.
     uint32_t lo = 1;
-    if (min(nblk, kStreamThreads) >= K) {
+    if (min(nblk, kThreads) >= K) {
         uint32_t v[PER], least = 0xffffffffu, hi = 0;
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
@@ -472,7 +474,7 @@ __device__ __forceinline__ void top_ordered(unsigned long long* list, int n) {
 }
 
 template <bool TOPK>
-constexpr int kLogprobThreads = kFirstCloser + 32 * kClosers<TOPK>;
+constexpr int kLogprobThreads = Sh::kFirstCloser + 32 * kClosers<TOPK>;
 
 template <int ES, bool ENT, bool TOPK>
 __global__ void __launch_bounds__(kLogprobThreads<TOPK>, TOPK ? 2 : 3) logprobs_kernel(const LogprobParams p) {
@@ -480,24 +482,24 @@ __global__ void __launch_bounds__(kLogprobThreads<TOPK>, TOPK ? 2 : 3) logprobs_
     __shared__ StreamBars bars;
     __shared__ StatExchange ex;
     __shared__ TopScratch top[TOPK ? kClosers<TOPK> : 1];
-    __shared__ uint32_t thread_max[TOPK ? kMaxBuffers : 1][kStreamThreads];  // key of the largest of a thread's blocks, 0: it has none
+    __shared__ uint32_t thread_max[TOPK ? kMaxBuffers : 1][kThreads];  // key of the largest of a thread's blocks, 0: it has none
     using KeyT = typename BlockKey<ES>::type;
     unsigned char* ring = smem;
-    KeyT* keys = reinterpret_cast<KeyT*>(smem + p.src.stages * kStreamStageBytes);  // key_stride a buffer
+    KeyT* keys = reinterpret_cast<KeyT*>(smem + p.src.stages * Sh::kStageBytes);  // key_stride a buffer
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = p.src.k;
     const int rank = k > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int64_t cid = blockIdx.x >> p.src.log2_k, ncl = gridDim.x >> p.src.log2_k;
     const int64_t n_it = p.src.N > cid ? (p.src.N - 1 - cid) / ncl + 1 : 0;
-    stream_init(bars, p.src.stages, k);
+    stream_init<kThreads>(bars, p.src.stages, k);
     griddep_launch_dependents();  // programmatic dependent launch: no global access before the wait
     griddep_wait();
     __syncthreads();
     if (k > 1) cluster_sync();  // every CTA's shared memory is there to be written to
 
-    if (warp == kStreamWarps) {
-        stream_produce<ES>(p.src, bars, ring, 1, cid, ncl, rank);
-    } else if (warp < kStreamWarps) {
+    if (warp == Sh::kWarps) {
+        stream_produce<ES, kThreads>(p.src, bars, ring, 1, cid, ncl, rank);
+    } else if (warp < Sh::kWarps) {
         StreamPos pos{0, 0, false};
         RowPos rp;
         Slice s = slice_of<ES>(p.src, cid, rank);
@@ -513,12 +515,12 @@ __global__ void __launch_bounds__(kLogprobThreads<TOPK>, TOPK ? 2 : 3) logprobs_
             KeyT* rk = keys + buf * p.key_stride;
             RunStat<ENT, false> st(p.scale);
             float most = kNegInf;  // of the thread's blocks
-            for (int c0 = 0; c0 < s.nv; c0 += kStreamChunk) {
-                const int nl = min(kStreamChunk, s.nv - c0);
+            for (int c0 = 0; c0 < s.nv; c0 += Sh::kChunk) {
+                const int nl = min(Sh::kChunk, s.nv - c0);
                 uint4 v[kBlockVec];
-                stream_chunk(p.src, bars, ring, pos, [&](const unsigned char* stage) {
-                    if constexpr (TOPK) load_block<ES>(stage, nl, v);
-                    else load_strided<ES>(stage, nl, v);
+                stream_chunk<kThreads>(p.src, bars, ring, pos, [&](const unsigned char* stage) {
+                    if constexpr (TOPK) load_block<ES, kThreads>(stage, nl, v);
+                    else load_strided<ES, kThreads>(stage, nl, v);
                 });
                 const float bmax = st.template add_vecs<ES>(v, p.scale);
                 if (TOPK) {
@@ -545,8 +547,8 @@ __global__ void __launch_bounds__(kLogprobThreads<TOPK>, TOPK ? 2 : 3) logprobs_
             row_end(bars, buf);
             ++rp.n;
         }
-    } else if (warp - (kStreamWarps + 1) < 1 << p.log2_closers) {  // a closing warp
-        const uint32_t me = warp - (kStreamWarps + 1), turn = (1u << p.log2_closers) - 1u;
+    } else if (warp - (Sh::kWarps + 1) < 1 << p.log2_closers) {  // a closing warp
+        const uint32_t me = warp - (Sh::kWarps + 1), turn = (1u << p.log2_closers) - 1u;
         RowPos rp;
         Slice s = slice_of<ES>(p.src, cid, rank);
         bool bad = false, aborted = false;
@@ -593,7 +595,7 @@ __global__ void __launch_bounds__(kLogprobThreads<TOPK>, TOPK ? 2 : 3) logprobs_
                 const uint32_t phase = TOPK ? 2 * use : use;  // exchanges of the buffer with the cluster so far
                 if (!aborted && !stream_wait(bars, &bars.row_full[buf], use & 1u, p.src.wait_ns)) aborted = true;
                 RunStat<ENT, false> st(p.scale);
-                stat_collect(st, ex, buf, p.scale);
+                stat_collect<kThreads>(st, ex, buf, p.scale);
                 if (!TOPK) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars.row_empty[buf]);
@@ -682,7 +684,7 @@ __global__ void __launch_bounds__(kLogprobThreads<TOPK>, TOPK ? 2 : 3) logprobs_
     }
     // The error word: every CTA adds its bits; the last one publishes and resets them.
     __syncthreads();
-    if (tid == kFirstCloser) {
+    if (tid == Sh::kFirstCloser) {
         if (stream_aborted(bars)) atomicOr(&p.ws->err, static_cast<unsigned>(FOAK_ERRBIT_TIMEOUT));
         if (atom_add_acq_rel_gpu(&p.ws->done, 1u) == gridDim.x - 1) {
             const unsigned e = atomicExch(&p.ws->err, 0u);
@@ -708,7 +710,7 @@ cudaError_t launch_typed(LogprobParams prm, cudaStream_t stream) {
     // Few rows: a cluster per row, as long as its CTAs are all on SMs of their own and
     // have at least half a chunk each.
     int k = kStreamMaxCluster;
-    while (k > 1 && (s.N * k > sms || 2 * nb < static_cast<int64_t>(k) * kStreamChunk)) k /= 2;
+    while (k > 1 && (s.N * k > sms || 2 * nb < static_cast<int64_t>(k) * Sh::kChunk)) k /= 2;
     set_cluster(s, k);
     const int64_t nblk = ((nb + kBlockVec - 1) / kBlockVec + s.k - 1) / s.k + 1;
     prm.key_stride = static_cast<int>((kKeyBody + nblk + 63) / 64 * 64);
@@ -716,18 +718,18 @@ cudaError_t launch_typed(LogprobParams prm, cudaStream_t stream) {
     // A buffer for each closing warp, fewer where the keys are large; CTAs an SM as the
     // registers allow, fewer where a ring of two stages would not fit.
     const size_t fixed = 1024 + 256 + sizeof(StreamBars) + sizeof(StatExchange) +
-                         (TOPK ? kClosers<TOPK> * sizeof(TopScratch) + kMaxBuffers * kStreamThreads * 4 : 0);
+                         (TOPK ? kClosers<TOPK> * sizeof(TopScratch) + kMaxBuffers * kThreads * 4 : 0);
     int per_sm = TOPK ? 2 : 3;
     s.log2_buffers = TOPK ? 2 : 1;
     auto room_for = [&] { return std::min<int64_t>(228 * 1024 / per_sm, 227 * 1024) - static_cast<int64_t>(fixed + (buffer << s.log2_buffers)); };
-    while (s.log2_buffers > 1 && room_for() < 2 * static_cast<int64_t>(kStreamStageBytes)) --s.log2_buffers;
-    while (per_sm > 1 && room_for() < 2 * static_cast<int64_t>(kStreamStageBytes)) --per_sm;
+    while (s.log2_buffers > 1 && room_for() < 2 * static_cast<int64_t>(Sh::kStageBytes)) --s.log2_buffers;
+    while (per_sm > 1 && room_for() < 2 * static_cast<int64_t>(Sh::kStageBytes)) --per_sm;
     prm.log2_closers = TOPK ? s.log2_buffers : 0;
     const int64_t room = room_for();
-    if (room < static_cast<int64_t>(kStreamStageBytes)) return cudaErrorInvalidValue;
+    if (room < static_cast<int64_t>(Sh::kStageBytes)) return cudaErrorInvalidValue;
     const size_t key_bytes = buffer << s.log2_buffers;
-    s.stages = static_cast<int>(std::min<size_t>(kStreamMaxStages, room / kStreamStageBytes));
-    const size_t smem = static_cast<size_t>(s.stages) * kStreamStageBytes + key_bytes;
+    s.stages = static_cast<int>(std::min<size_t>(kStreamMaxStages, room / Sh::kStageBytes));
+    const size_t smem = static_cast<size_t>(s.stages) * Sh::kStageBytes + key_bytes;
     {
         std::lock_guard<std::mutex> lock(g_lp_mu);
         size_t& set = g_lp_attr[std::make_pair(dev, reinterpret_cast<const void*>(kern))];

@@ -1,9 +1,8 @@
 // Rows of logits streamed through shared memory by one CTA, or by a cluster of CTAs
 // that share a row: the pieces common to the log-probability and distillation kernels.
 //
-// A CTA has kStreamThreads consumer threads, a producer warp and one or more closing
-// warps.  The
-// producer copies the row in chunks of kStreamChunk 16-byte vectors (one-dimensional bulk
+// A CTA has NT consumer threads (256 or 512), a producer warp and one or more closing
+// warps.  The producer copies the row in chunks of 4 NT 16-byte vectors (one-dimensional bulk
 // copies) into a ring of stages; a stage completes on its `full` barrier and is handed
 // back by one arrival of every consumer warp on its `empty` barrier.  It runs ahead of the
 // consumers over the row's end.  The consumers leave each row's partial results in one of
@@ -31,14 +30,17 @@
 
 namespace foak {
 
-constexpr int kStreamThreads = 256;                       // consumers
-constexpr int kStreamWarps = kStreamThreads / 32;
-constexpr int kStreamBlock = kStreamThreads + 64;         // and the producer and one closing warp
-constexpr int kFirstCloser = kStreamThreads + 32;         // the first closing warp's first thread
+constexpr int kBlockVec = 4;  // a thread's vectors of a chunk: one 64-byte block
+// What follows from the number of consumer threads.
+template <int NT>
+struct Shape {
+    static constexpr int kWarps = NT / 32;
+    static constexpr int kFirstCloser = NT + 32;         // the first closing warp's first thread
+    static constexpr int kChunk = NT * kBlockVec;        // vectors of a chunk (16 KB of 256 threads)
+    static constexpr uint32_t kStageBytes = kChunk * 16;
+};
+constexpr int kMaxWarps = 16;
 constexpr int kMaxBuffers = 4;                            // rows between the consumers and the closing warps
-constexpr int kBlockVec = 4;                              // a thread's vectors of a chunk: one 64-byte block
-constexpr int kStreamChunk = kStreamThreads * kBlockVec;  // vectors of a chunk (16 KB)
-constexpr uint32_t kStreamStageBytes = kStreamChunk * 16;
 constexpr int kStreamMaxStages = 12;
 constexpr int kStreamMaxCluster = 8;
 constexpr float kMinExp2 = -16384.f;  // 2^x is 0 from far above this; keeps products with it finite
@@ -53,6 +55,7 @@ struct StreamSrc {
     int64_t skip_load_row;  // test hook: this row's first chunk is never loaded (-1: none)
     int k, log2_k;          // CTAs of a row's cluster
     int log2_buffers;
+    bool evict_last_pass;
     int stages;
 };
 
@@ -68,15 +71,17 @@ __device__ __forceinline__ uint32_t bf16x2_max_nan(uint32_t a, uint32_t b) {
 }
 
 // Barrier of the consumer threads alone (whole warps arrive).
+template <int NT>
 __device__ __forceinline__ void consumers_sync() {
     __syncwarp();
-    asm volatile("bar.sync 1, %0;" ::"n"(kStreamThreads) : "memory");
+    asm volatile("bar.sync 1, %0;" ::"n"(NT) : "memory");
 }
-// Consumers (who do not wait) and closing warp (which does): the number of valid rows is in shared memory.
+// Consumers (who do not wait) and closing warps (which do): the number of valid rows is in shared memory.
+template <int NT, int CLOSERS>
 __device__ __forceinline__ void scale_known() {
     __syncwarp();
-    if (threadIdx.x < kStreamThreads) asm volatile("bar.arrive 2, %0;" ::"n"(kStreamThreads + 32) : "memory");
-    else asm volatile("bar.sync 2, %0;" ::"n"(kStreamThreads + 32) : "memory");
+    if (threadIdx.x < NT) asm volatile("bar.arrive 2, %0;" ::"n"(NT + 32 * CLOSERS) : "memory");
+    else asm volatile("bar.sync 2, %0;" ::"n"(NT + 32 * CLOSERS) : "memory");
 }
 // The cluster's barrier, from code whose lanes may have parted.
 __device__ __forceinline__ void cluster_sync_converged() {
@@ -145,17 +150,18 @@ struct StreamBars {
     int abort;              // a wait gave up: everyone stops waiting and winds down
 };
 
+template <int NT>
 __device__ __forceinline__ void stream_init(StreamBars& b, int stages, int cluster) {
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; ++s) {
             mbar_init(&b.full[s], 1);
-            mbar_init(&b.empty[s], kStreamWarps);
+            mbar_init(&b.empty[s], Shape<NT>::kWarps);
         }
         for (int i = 0; i < kMaxBuffers; ++i) {
-            mbar_init(&b.row_full[i], kStreamWarps);
+            mbar_init(&b.row_full[i], Shape<NT>::kWarps);
             mbar_init(&b.row_empty[i], 1);
             mbar_init(&b.row_ready[i], 1);
-            mbar_init(&b.row_stored[i], kStreamWarps);
+            mbar_init(&b.row_stored[i], Shape<NT>::kWarps);
             mbar_init(&b.peers[i], cluster);
         }
         b.abort = 0;
@@ -182,7 +188,7 @@ __device__ __forceinline__ bool stream_wait(StreamBars& b, uint64_t* bar, uint32
 }
 
 // The producer warp: rows cid, cid + ncl, ...; every valid row's chunks `passes` times.
-template <int ES>
+template <int ES, int NT>
 __device__ __forceinline__ void stream_produce(const StreamSrc& p, StreamBars& bars, unsigned char* ring, int passes,
                                                int64_t cid, int64_t ncl, int rank) {
     const int lane = threadIdx.x & 31;
@@ -204,18 +210,23 @@ __device__ __forceinline__ void stream_produce(const StreamSrc& p, StreamBars& b
             if (lane == 0 && !stop) {
                 move_slice<ES>(p, row, rank, s);
                 for (int pass = 0; pass < passes && !stop; ++pass) {
-                    for (int c0 = 0; c0 < s.nv; c0 += kStreamChunk) {
+                    for (int c0 = 0; c0 < s.nv; c0 += Shape<NT>::kChunk) {
                         if (wrapped && !stream_wait(bars, &bars.empty[st], par ^ 1u, p.wait_ns)) stop = true;
                         if (stop || stream_aborted(bars)) {
                             stop = true;
                             break;
                         }
                         if (!(p.skip_load_row == row && pass == 0 && c0 == 0)) {
-                            const uint32_t bytes = static_cast<uint32_t>(min(kStreamChunk, s.nv - c0)) * 16u;
+                            const uint32_t bytes = static_cast<uint32_t>(min(Shape<NT>::kChunk, s.nv - c0)) * 16u;
                             fence_proxy_async_smem();
                             mbar_arrive_expect_tx(&bars.full[st], bytes);
-                            bulk_g2s(ring + st * kStreamStageBytes, s.body + static_cast<int64_t>(c0) * 16, bytes,
-                                     &bars.full[st]);
+                            const char* from = s.body + static_cast<int64_t>(c0) * 16;
+                            // the last sweep's reads let the row go from L2, where the rows between two sweeps wait
+                            if (p.evict_last_pass && pass == passes - 1)
+                                bulk_g2s_hint(ring + st * Shape<NT>::kStageBytes, from, bytes, &bars.full[st],
+                                              l2_policy_evict_first());
+                            else
+                                bulk_g2s(ring + st * Shape<NT>::kStageBytes, from, bytes, &bars.full[st]);
                             armed |= 1u << st;
                         } else {
                             armed &= ~(1u << st);
@@ -249,11 +260,11 @@ struct StreamPos {
 };
 
 // Waits for the next chunk, then read(stage pointer), then hands the stage back.
-template <typename F>
+template <int NT, typename F>
 __device__ __forceinline__ void stream_chunk(const StreamSrc& p, StreamBars& bars, const unsigned char* ring,
                                              StreamPos& pos, F&& read) {
     if (!pos.aborted && !stream_wait(bars, &bars.full[pos.st], pos.par, p.wait_ns)) pos.aborted = true;
-    read(ring + pos.st * kStreamStageBytes);
+    read(ring + pos.st * Shape<NT>::kStageBytes);
     __syncwarp();
     if ((threadIdx.x & 31) == 0 && !pos.aborted) mbar_arrive(&bars.empty[pos.st]);
     if (++pos.st == static_cast<uint32_t>(p.stages)) {
@@ -310,11 +321,11 @@ __device__ __forceinline__ bool peers_wait(StreamBars& b, uint64_t* bar, uint32_
 // The thread's block of a chunk: vectors 4 tid .. 4 tid + 3, -inf past the chunk's end.
 // They are read in an order turned by tid / 2, so that the eight threads that share a
 // 128-byte shared-memory access touch all 32 banks; v is left in that turned order.
-template <int ES>
+template <int ES, int NT>
 __device__ __forceinline__ void load_block(const unsigned char* stage, int nl, uint4 (&v)[kBlockVec]) {
     const int tid = threadIdx.x, turn = tid >> 1 & (kBlockVec - 1);
     const uint4* sb = reinterpret_cast<const uint4*>(stage) + tid * kBlockVec;
-    if (nl == kStreamChunk) {
+    if (nl == Shape<NT>::kChunk) {
 #pragma unroll
         for (int i = 0; i < kBlockVec; ++i) v[i] = sb[i ^ turn];
     } else {
@@ -322,18 +333,18 @@ __device__ __forceinline__ void load_block(const unsigned char* stage, int nl, u
         for (int i = 0; i < kBlockVec; ++i) v[i] = tid * kBlockVec + (i ^ turn) < nl ? sb[i ^ turn] : RowMath<ES>::pad();
     }
 }
-// Four vectors of a chunk without a block's order: tid, tid + 256, ...
-template <int ES>
+// Four vectors of a chunk without a block's order: tid, tid + NT, ...
+template <int ES, int NT>
 __device__ __forceinline__ void load_strided(const unsigned char* stage, int nl, uint4 (&v)[kBlockVec]) {
     const int tid = threadIdx.x;
     const uint4* sb = reinterpret_cast<const uint4*>(stage) + tid;
-    if (nl == kStreamChunk) {
+    if (nl == Shape<NT>::kChunk) {
 #pragma unroll
-        for (int i = 0; i < kBlockVec; ++i) v[i] = sb[i * kStreamThreads];
+        for (int i = 0; i < kBlockVec; ++i) v[i] = sb[i * NT];
     } else {
 #pragma unroll
         for (int i = 0; i < kBlockVec; ++i)
-            v[i] = tid + i * kStreamThreads < nl ? sb[i * kStreamThreads] : RowMath<ES>::pad();
+            v[i] = tid + i * NT < nl ? sb[i * NT] : RowMath<ES>::pad();
     }
 }
 
@@ -499,7 +510,7 @@ struct RunStat {
 
 // Shared memory through which the consumers' (and the cluster's) sets meet.
 struct StatExchange {
-    float4 warp[kMaxBuffers][kStreamWarps];         // (m, s, a, s2), by row buffer
+    float4 warp[kMaxBuffers][kMaxWarps];            // (m, s, a, s2), by row buffer
     float4 cta[kMaxBuffers][2][kStreamMaxCluster];  // the cluster's CTAs' sets, by buffer and parity of its use
 };
 
@@ -512,13 +523,13 @@ __device__ __forceinline__ void stat_publish(RunStat<ENT, TWO>& st, StatExchange
     if ((threadIdx.x & 31) == 0) ex.warp[buf][threadIdx.x >> 5] = make_float4(st.m, st.s, st.a, st.s2);
 }
 // The CTA's set from its warps', by whole warps; every lane gets it.
-template <bool ENT, bool TWO>
+template <int NT, bool ENT, bool TWO>
 __device__ __forceinline__ void stat_collect(RunStat<ENT, TWO>& st, const StatExchange& ex, int buf,
                                              const ExpScale& x) {
-    st.set(ex.warp[buf][threadIdx.x & (kStreamWarps - 1)], x);
+    st.set(ex.warp[buf][threadIdx.x & (Shape<NT>::kWarps - 1)], x);
     st.raise(warp_max_redux(st.m), x);
 #pragma unroll
-    for (int off = kStreamWarps / 2; off > 0; off >>= 1) {
+    for (int off = Shape<NT>::kWarps / 2; off > 0; off >>= 1) {
         st.s += __shfl_xor_sync(0xffffffffu, st.s, off);
         if (ENT) st.a += __shfl_xor_sync(0xffffffffu, st.a, off);
         if (TWO) st.s2 += __shfl_xor_sync(0xffffffffu, st.s2, off);
@@ -552,15 +563,16 @@ __device__ __forceinline__ bool stat_cluster(RunStat<ENT, TWO>& st, StatExchange
     return true;
 }
 
-// Number of valid labels, counted by the consumer threads; scratch: kStreamWarps ints.
+// Number of valid labels, counted by the consumer threads; scratch: an int a warp.
+template <int NT>
 __device__ __forceinline__ int count_valid_consumers(const StreamSrc& p, int* scratch) {
     if (!p.labels) return static_cast<int>(p.N);
     int cv = 0;
-    for (int64_t i0 = threadIdx.x; i0 < p.N; i0 += 8 * kStreamThreads) {
+    for (int64_t i0 = threadIdx.x; i0 < p.N; i0 += 8 * NT) {
         int64_t y[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const int64_t i = i0 + static_cast<int64_t>(k) * kStreamThreads;
+            const int64_t i = i0 + static_cast<int64_t>(k) * NT;
             y[k] = i < p.N ? __ldg(p.labels + i) : p.ignore_index;
         }
 #pragma unroll
@@ -568,17 +580,11 @@ __device__ __forceinline__ int count_valid_consumers(const StreamSrc& p, int* sc
     }
     cv = __reduce_add_sync(0xffffffffu, cv);
     if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = cv;
-    consumers_sync();
+    consumers_sync<NT>();
     int t = 0;
 #pragma unroll
-    for (int w = 0; w < kStreamWarps; ++w) t += scratch[w];
+    for (int w = 0; w < Shape<NT>::kWarps; ++w) t += scratch[w];
     return t;
 }
-
-// How a stream kernel is launched: CTAs of a row's cluster, CTAs of an SM, stages.
-struct StreamPlan {
-    int k, per_sm, stages;
-    int64_t grid;
-};
 
 }  // namespace foak

@@ -28,6 +28,7 @@ constexpr int kGradThreads = 256;
 constexpr int kGradVpt = 8;
 constexpr int kGradSegVec = kGradThreads * kGradVpt;  // 32 KB
 constexpr int kGradBlocksPerSm = 4;
+constexpr int kTeacherBlocksPerSm = 3;
 
 struct RowsGradParams {
     StreamSrc src;
@@ -192,68 +193,132 @@ __global__ void __launch_bounds__(kGradThreads, kGradBlocksPerSm) logprobs_grad_
     }
 }
 
+// Distillation: a CTA takes a run of consecutive segments, so mostly of whole rows.  A
+// ninth warp fetches the teacher's row and the logits it needs before the first store of a
+// row (bar `gathered`), and makes the row's corrections after the last one (`stored`),
+// while the other warps are on the next row.
 template <int ES, bool TWO>
-__global__ void __launch_bounds__(kGradThreads, kGradBlocksPerSm) distill_grad_kernel(const RowsGradParams p) {
-    griddep_launch_dependents();
+__global__ void __launch_bounds__(kGradThreads + 32, kTeacherBlocksPerSm) distill_grad_kernel(const RowsGradParams p) {
+    __shared__ int scratch[2 * (kGradThreads / 32 + 1)];
+    __shared__ TeacherRow teacher[2];
+    __shared__ uint64_t gathered[2], stored[2];
+    __shared__ int s_abort;
+    const int tid = threadIdx.x, lane = tid & 31;
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&gathered[i], 1);
+            mbar_init(&stored[i], kGradThreads / 32);
+        }
+        fence_mbar_init();
+        s_abort = 0;
+    }
+    griddep_launch_dependents();  // programmatic dependent launch: no global access before the wait
     griddep_wait();
-    __shared__ int scratch[2 * (kGradThreads / 32)];
-    __shared__ TeacherRow teach;
-    __shared__ float s_xy;
+    __syncthreads();
     int n_valid = static_cast<int>(p.src.N), n_bad = 0;
     if (p.src.labels && (p.denom <= 0.f || (blockIdx.x == 0 && p.err)))
         count_labels(p.src.labels, p.src.N, p.src.V, p.src.ignore_index, scratch, n_valid, n_bad);
-    if (blockIdx.x == 0 && threadIdx.x == 0 && p.err) *p.err = n_bad > 0 ? FOAK_ERRBIT_LABEL_RANGE : 0;
+    if (blockIdx.x == 0 && tid == 0 && p.err) *p.err = n_bad > 0 ? FOAK_ERRBIT_LABEL_RANGE : 0;
     const float scale = (p.g_ptr ? __ldg(p.g_ptr) : 1.f) / (p.denom > 0.f ? p.denom : static_cast<float>(n_valid));
     const float w1 = scale * p.ce_w, wt = scale * p.kd_w * p.inv_t;
     const int64_t items = p.src.N * p.nseg;
-    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-        const Segment s = segment_of<ES>(p, item);
-        const int64_t y = p.src.labels ? __ldg(p.src.labels + s.row) : -1;
-        if (!stream_row_valid(y, p.src)) {
-            zero_segment<ES>(s);
-            continue;
-        }
-        uint4 v[kGradVpt];
-        float edge;
-        load_segment<ES>(s, v, edge);
-        const float4 st = __ldg(p.stats4 + s.row);
-        if (threadIdx.x < 32) {
-            teacher_row<ES>(p.teacher, s.row, p.src.V, s.rowp, s.col_lo, s.col_hi, teach);
-            if (threadIdx.x == 0 && y >= s.col_lo && y < s.col_hi) s_xy = load_scalar<ES>(s.rowp + y * ES);
-        }
-        __syncthreads();  // the teacher's row is in place, and the logits it needs are read
-        const bool empty = st.x == kNegInf;  // nothing but -inf: p = 0
-        const float m = empty ? 0.f : st.x;
-        const float l1 = empty ? 0.f : st.y * kLog2e, lt = empty ? 0.f : st.z * kLog2e;
-        const float at = wt * teach.total, a1 = w1;
-        // one exponential where both parts share it
-        const float a = TWO ? at : at + (p.ce_w != 0.f ? a1 : 0.f);
-        const f32x2_t M = f2_pack(-m, -m), C = f2_pack(p.c, p.c), L = f2_pack(kLog2e, kLog2e);
-        const f32x2_t ST = f2_pack(-lt, -lt), S1 = f2_pack(-l1, -l1), A = f2_pack(a, a), A1 = f2_pack(a1, a1);
-        auto grad = [&](f32x2_t x) {
-            const f32x2_t d = f2_add(x, M);
-            f32x2_t e = f2_mul(f2_ex2(f2_fma(d, C, ST)), A);
-            if (TWO) e = f2_fma(f2_ex2(f2_fma(d, L, S1)), A1, e);
+    const int64_t beg = items * blockIdx.x / gridDim.x, end = items * (blockIdx.x + 1) / gridDim.x;
+    uint32_t visit = 0;  // valid rows begun
+    bool aborted = false;
+
+    // the row's plain gradient
+    struct Row {
+        float m, c, lt, l1, a, a1;
+        __device__ __forceinline__ f32x2_t at(f32x2_t x) const {
+            const f32x2_t d = f2_add(x, f2_pack(-m, -m));
+            f32x2_t e = f2_mul(f2_ex2(f2_fma(d, f2_pack(c, c), f2_pack(-lt, -lt))), f2_pack(a, a));
+            if (TWO) e = f2_fma(f2_ex2(f2_fma(d, f2_pack(kLog2e, kLog2e), f2_pack(-l1, -l1))), f2_pack(a1, a1), e);
             return e;
-        };
-        store_segment<ES>(s, v, edge, grad);
-        __syncthreads();  // the places that differ follow the segment's plain stores
-        for (int j = threadIdx.x; j <= p.teacher.K; j += kGradThreads) {
-            const bool is_label = j == p.teacher.K;
-            const int64_t id = is_label ? y : teach.id[j];
-            if (id < 0 || id < s.col_lo || id >= s.col_hi) continue;
-            const float x = is_label ? s_xy : teach.x[j];
-            float lo, hi;
-            f2_unpack(grad(f2_pack(x, x)), lo, hi);
-            const int one[1] = {static_cast<int>(id)};
-            float mass[1];
-            teacher_mass(teach, p.teacher.K, one, mass);
-            lo -= wt * mass[0];
-            if (id == y) lo -= w1;
-            store_scalar<ES>(s.drow + id * ES, lo);
         }
-        __syncthreads();  // the teacher's row may be overwritten
+    };
+    auto row_of = [&](int64_t row) {
+        const float4 st = __ldg(p.stats4 + row);
+        const bool empty = st.x == kNegInf;  // nothing but -inf: p = 0
+        Row r;
+        r.m = empty ? 0.f : st.x;
+        r.c = p.c;
+        r.l1 = empty ? 0.f : st.y * kLog2e;
+        r.lt = empty ? 0.f : st.z * kLog2e;
+        r.a1 = w1;
+        r.a = wt * st.w + (!TWO && p.ce_w != 0.f ? w1 : 0.f);  // one exponential where both parts share it
+        return r;
+    };
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (!aborted && (*reinterpret_cast<volatile int*>(&s_abort) || !mbar_wait_bounded(bar, parity, p.src.wait_ns))) {
+            s_abort = 1;
+            aborted = true;
+        }
+    };
+
+    if (tid < kGradThreads) {
+        Row r = {};
+        bool valid = false;
+        for (int64_t item = beg; item < end; ++item) {
+            const Segment s = segment_of<ES>(p, item);
+            const bool first = item == beg || s.first;
+            if (first) valid = stream_row_valid(p.src.labels ? __ldg(p.src.labels + s.row) : -1, p.src);
+            if (!valid) {
+                zero_segment<ES>(s);
+                continue;
+            }
+            uint4 v[kGradVpt];
+            float edge;
+            load_segment<ES>(s, v, edge);
+            if (first) {
+                r = row_of(s.row);
+                wait(&gathered[visit & 1u], visit >> 1 & 1u);
+                ++visit;
+            }
+            if (!aborted) store_segment<ES>(s, v, edge, [&](f32x2_t x) { return r.at(x); });
+            if (item + 1 == end || (item + 1) % p.nseg == 0) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&stored[(visit - 1) & 1u]);
+            }
+        }
+    } else {
+        struct Visit {
+            int64_t row, col_lo, col_hi, y;
+            float x_y;
+        } now = {}, before = {};
+        auto correct = [&](const Visit& u, uint32_t n) {
+            wait(&stored[n & 1u], n >> 1 & 1u);
+            const Row r = row_of(u.row);
+            if (!aborted)
+                teacher_correct<ES>(teacher[n & 1u], p.teacher.K, u.col_lo, u.col_hi, u.y, u.x_y, w1, wt,
+                                    p.dx + u.row * p.src.ld * ES, [&](float x) {
+                                        float lo, hi;
+                                        f2_unpack(r.at(f2_pack(x, x)), lo, hi);
+                                        return lo;
+                                    });
+            __syncwarp();
+        };
+        for (int64_t item = beg; item < end;) {
+            Segment s = segment_of<ES>(p, item);
+            const int64_t next = min(end, (s.row + 1) * p.nseg);
+            now.row = s.row;
+            now.y = p.src.labels ? __ldg(p.src.labels + s.row) : -1;
+            if (stream_row_valid(now.y, p.src)) {
+                now.col_lo = s.col_lo;
+                now.col_hi = segment_of<ES>(p, next - 1).col_hi;
+                teacher_row<ES>(p.teacher, s.row, p.src.V, s.rowp, now.col_lo, now.col_hi, teacher[visit & 1u]);
+                now.x_y = now.y >= now.col_lo && now.y < now.col_hi ? load_scalar<ES>(s.rowp + now.y * ES) : 0.f;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&gathered[visit & 1u]);
+                if (visit > 0) correct(before, visit - 1);
+                before = now;
+                ++visit;
+            }
+            item = next;
+        }
+        if (visit > 0) correct(before, visit - 1);
     }
+    __syncthreads();
+    if (s_abort && tid == 0 && p.err) atomicOr(reinterpret_cast<unsigned*>(p.err), FOAK_ERRBIT_TIMEOUT);
 }
 
 RowsGradParams common_params(int es, const void* x, void* dx, int64_t ld, const int64_t* labels, int64_t N, int64_t V,
@@ -266,6 +331,7 @@ RowsGradParams common_params(int es, const void* x, void* dx, int64_t ld, const 
     p.src.V = V;
     p.src.ignore_index = ignore_index;
     p.src.k = 1;
+    p.src.wait_ns = test_wait_limit_ns();
     p.dx = static_cast<char*>(dx);
     p.nseg = std::max<int64_t>(1, (V * es / 16 + kGradSegVec - 1) / kGradSegVec);
     p.inv_t = 1.f / temperature;
@@ -274,8 +340,8 @@ RowsGradParams common_params(int es, const void* x, void* dx, int64_t ld, const 
     return p;
 }
 
-dim3 grad_grid(const RowsGradParams& p) {
-    const int64_t full = static_cast<int64_t>(device_sm_count()) * kGradBlocksPerSm;
+dim3 grad_grid(const RowsGradParams& p, int per_sm) {
+    const int64_t full = static_cast<int64_t>(device_sm_count()) * per_sm;
     return dim3(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(full, p.src.N * p.nseg))));
 }
 
@@ -290,7 +356,7 @@ cudaError_t launch_logprobs_grad(int es, const void* x, void* dx, int64_t ld, co
     p.entropy = entropy;
     p.grad_logp = grad_logp;
     p.grad_entropy = grad_entropy;
-    const dim3 grid = grad_grid(p), block(kGradThreads);
+    const dim3 grid = grad_grid(p, kGradBlocksPerSm), block(kGradThreads);
     if (es == 2)
         return grad_entropy ? launch_dependent(logprobs_grad_kernel<2, true>, grid, block, 0, stream, p)
                             : launch_dependent(logprobs_grad_kernel<2, false>, grid, block, 0, stream, p);
@@ -314,7 +380,7 @@ cudaError_t launch_distill_grad(int es, const void* x, void* dx, int64_t ld, con
     p.denom = denom;
     p.ce_w = ce_w;
     p.kd_w = kd_w;
-    const dim3 grid = grad_grid(p), block(kGradThreads);
+    const dim3 grid = grad_grid(p, kTeacherBlocksPerSm), block(kGradThreads + 32);
     const bool two = ce_w != 0.f && temperature != 1.f;
     if (es == 2)
         return two ? launch_dependent(distill_grad_kernel<2, true>, grid, block, 0, stream, p)

@@ -18,14 +18,16 @@ struct TeacherSrc {
 };
 
 struct TeacherRow {
-    alignas(16) int id[kTeacherMax];   // -1: no entry (also past K, up to a multiple of 4)
+    alignas(16) int id[kTeacherMax];      // -1: no entry (also past K, up to a multiple of 4)
     alignas(16) float q[kTeacherMax];
     float lnq[kTeacherMax];
-    float x[kTeacherMax];    // the student's logit of the token (only where col_lo <= id < col_hi)
-    float total;             // sum of q
+    float x[kTeacherMax];                 // the student's logit of the token (only where col_lo <= id < col_hi)
+    alignas(16) int seen[2 * kTeacherMax];  // hash table of the ids
+    float total;                          // sum of q
+    bool repeated;                        // a token is listed more than once
 };
 
-// Filled by a whole warp; the caller synchronises.  Returns whether an id was V or more
+// Filled by a whole warp, which is in step afterwards.  Returns whether an id was V or more
 // (such an entry, like one with a negative id, counts as absent).  The student's logits
 // are fetched for the ids in [col_lo, col_hi).
 template <int ES>
@@ -34,27 +36,46 @@ __device__ __forceinline__ bool teacher_row(const TeacherSrc& p, int64_t row, in
     constexpr int PER = kTeacherMax / 32;
     const int lane = threadIdx.x & 31;
     float t[PER];
-    bool bad = false;
+    int id[PER];
+    // all loads of a kind go out together: two latencies, not two for each 32 entries
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int k = lane + 32 * j;
+        id[j] = -1;
+        t[j] = kNegInf;
+        if (k < p.K) {
+            id[j] = __ldg(p.ids + row * p.ld + k);
+            t[j] = __ldg(p.logp + row * p.ld + k);
+        }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 2 * kTeacherMax / 128; ++j)
+        reinterpret_cast<int4*>(out.seen)[lane + 32 * j] = make_int4(-1, -1, -1, -1);
+    __syncwarp();
+    bool bad = false, twice = false;
     float top = kNegInf;
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
         const int k = lane + 32 * j;
-        t[j] = kNegInf;
-        if (k < p.K) {
-            const int id = __ldg(p.ids + row * p.ld + k);
-            const float v = __ldg(p.logp + row * p.ld + k);
-            bad |= id >= V;
-            const bool there = id >= 0 && id < V;
-            out.id[k] = there ? id : -1;
-            if (there) t[j] = v;
-            if (there && id >= col_lo && id < col_hi) out.x[k] = load_scalar<ES>(rowp + static_cast<int64_t>(id) * ES);
+        if (32 * j >= p.K) break;
+        bad |= id[j] >= V;
+        if (id[j] < 0 || id[j] >= V) {
+            id[j] = -1;
+            t[j] = kNegInf;
         }
-        if (k >= p.K && k < (p.K + 3) / 4 * 4) {
-            out.id[k] = -1;
-            out.q[k] = 0.f;
+        if (k < (p.K + 3) / 4 * 4) out.id[k] = id[j];
+        if (id[j] >= col_lo && id[j] < col_hi) out.x[k] = load_scalar<ES>(rowp + static_cast<int64_t>(id[j]) * ES);
+        if (id[j] >= 0) {  // at most half of the table fills
+            for (unsigned h = (static_cast<unsigned>(id[j]) * 2654435761u) >> 23;; h = (h + 1) & (2 * kTeacherMax - 1)) {
+                const int before = atomicCAS(out.seen + h, -1, id[j]);
+                twice |= before == id[j];
+                if (before == -1 || before == id[j]) break;
+            }
         }
         top = fmaxf(top, t[j]);
     }
+    static_assert(2 * kTeacherMax == 1 << (32 - 23), "the hash takes the table's bits");
     top = warp_max(top);
     // q = e^t, or that over its sum; the sum is taken below the largest so that it cannot overflow
     float sum = 0.f;
@@ -66,30 +87,47 @@ __device__ __forceinline__ bool teacher_row(const TeacherSrc& p, int64_t row, in
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
         const int k = lane + 32 * j;
-        if (k < p.K) {
-            const float l = t[j] - ln_norm;
-            out.lnq[k] = l;
+        if (32 * j < p.K && k < (p.K + 3) / 4 * 4) {
+            out.lnq[k] = t[j] - ln_norm;
             // the quotient, not e^(t - ln norm): its rounding stays relative to q
             out.q[k] = t[j] == kNegInf ? 0.f : (p.normalize ? expf(t[j] - top) / sum : expf(t[j]));
         }
     }
-    if (lane == 0) out.total = p.normalize && sum > 0.f ? 1.f : sum;
-    return __any_sync(0xffffffffu, bad);
+    twice = __any_sync(0xffffffffu, twice);
+    if (lane == 0) {
+        out.total = p.normalize && sum > 0.f ? 1.f : sum;
+        out.repeated = twice;
+    }
+    bad = __any_sync(0xffffffffu, bad);
+    __syncwarp();
+    return bad;
 }
 
-// Sums of q over the entries with each of these ids (an id may be listed more than once).
-template <int N>
-__device__ __forceinline__ void teacher_mass(const TeacherRow& t, int K, const int (&id)[N], float (&mass)[N]) {
-#pragma unroll
-    for (int n = 0; n < N; ++n) mass[n] = 0.f;
-    for (int k = 0; k < K; k += 4) {
-        const int4 i = *reinterpret_cast<const int4*>(t.id + k);
-        const float4 q = *reinterpret_cast<const float4*>(t.q + k);
-#pragma unroll
-        for (int n = 0; n < N; ++n)
-            mass[n] += ((i.x == id[n] ? q.x : 0.f) + (i.y == id[n] ? q.y : 0.f)) +
-                       ((i.z == id[n] ? q.z : 0.f) + (i.w == id[n] ? q.w : 0.f));
+// A warp's corrections of a row's gradient in the columns [col_lo, col_hi): what the K
+// listed tokens and the label y (-1: none; its logit x_y) take off the plain gradient
+// `grad_at` of their logits.  A token listed twice gets the same value from each place.
+template <int ES, typename F>
+__device__ __forceinline__ void teacher_correct(const TeacherRow& t, int K, int64_t col_lo, int64_t col_hi, int64_t y,
+                                                float x_y, float w1, float wt, char* drow, F&& grad_at) {
+    const int lane = threadIdx.x & 31;
+    bool listed = false;
+    for (int k = lane; k < K; k += 32) {
+        const int id = t.id[k];
+        if (id < 0 || id < col_lo || id >= col_hi) continue;
+        float mass = t.q[k];
+        if (t.repeated) {
+            mass = 0.f;
+            for (int j = 0; j < K; ++j) mass += t.id[j] == id ? t.q[j] : 0.f;
+        }
+        float e = grad_at(t.x[k]) - wt * mass;
+        if (id == y) {
+            e -= w1;
+            listed = true;
+        }
+        store_scalar<ES>(drow + static_cast<int64_t>(id) * ES, e);
     }
+    listed = __any_sync(0xffffffffu, listed);
+    if (lane == 0 && !listed && y >= col_lo && y < col_hi) store_scalar<ES>(drow + y * ES, grad_at(x_y) - w1);
 }
 
 }  // namespace foak

@@ -68,7 +68,7 @@ def _check(ce, x, y, ids, t, T=1.0, ce_w=0.0, kd_w=1.0, normalize=True, g=1.0, d
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("N,V,K", [(1, 1, 1), (3, 2, 2), (5, 7, 3), (4, 31, 31), (9, 1000, 64), (6, 8192, 20),
                                    (5, 32000, 256), (3, 50257, 100), (1, 128256, 20), (40, 32000, 20), (90, 50257, 7),
-                                   (400, 9001, 50)])
+                                   (400, 9001, 50), (170, 128263, 30)])
 @pytest.mark.parametrize("T,ce_w,normalize", [(1.0, 0.0, True), (1.0, 0.4, False), (2.0, 0.5, True), (0.5, 0.0, False)])
 def test_shapes(cuda_lib, dtype, N, V, K, T, ce_w, normalize):
     x = ref.make_logits(N, V, dtype, seed=N + V)
