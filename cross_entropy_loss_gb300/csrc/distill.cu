@@ -54,18 +54,17 @@ __device__ __forceinline__ SweepFactors sweep_factors(const RunStat<false, TWO>&
 }
 
 // Closing warps of a CTA, which take rows in turn.
+constexpr int kClosers = 2;
 template <int NT>
-constexpr int kClosers = NT == 512 ? 2 : 1;
-template <int NT>
-constexpr int kDistillThreads = NT + 32 + 32 * kClosers<NT>;
+constexpr int kDistillThreads = NT + 32 + 32 * kClosers;
 
 template <int ES, bool GRAD, bool TWO, int NT>
-__global__ void __launch_bounds__(kDistillThreads<NT>, NT == 256 ? 3 : 1) distill_kernel(const DistillParams p) {
+__global__ void __launch_bounds__(kDistillThreads<NT>, NT == 256 ? 2 : 1) distill_kernel(const DistillParams p) {
     constexpr int EPV = 16 / ES;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ StreamBars bars;
     __shared__ StatExchange ex;
-    __shared__ TeacherRow teacher[kClosers<NT>];
+    __shared__ TeacherRow teacher[kClosers];
     __shared__ SweepFactors factors[kMaxBuffers];
     __shared__ float total[kMaxBuffers];  // of the teacher's row
     __shared__ int s_count[kMaxWarps];
@@ -94,7 +93,7 @@ __global__ void __launch_bounds__(kDistillThreads<NT>, NT == 256 ? 3 : 1) distil
                 const int n = count_valid_consumers<NT>(p.src, s_count);
                 scale = p.g / static_cast<float>(n);
                 if (tid == 0) s_valid = n;
-                scale_known<NT, kClosers<NT>>();
+                scale_known<NT, kClosers>();
             }
         }
         StreamPos pos{0, 0, false};
@@ -193,11 +192,11 @@ __global__ void __launch_bounds__(kDistillThreads<NT>, NT == 256 ? 3 : 1) distil
             ++rp.n;
         }
     } else {  // a closing warp
-        const uint32_t me = warp - (Shape<NT>::kWarps + 1), turn = kClosers<NT> - 1;
+        const uint32_t me = warp - (Shape<NT>::kWarps + 1), turn = kClosers - 1;
         TeacherRow& teach = teacher[me];
         float scale = 0.f;
         if (GRAD) {
-            if (p.fin.denom <= 0.f) scale_known<NT, kClosers<NT>>();
+            if (p.fin.denom <= 0.f) scale_known<NT, kClosers>();
             scale = p.g / (p.fin.denom > 0.f ? p.fin.denom : static_cast<float>(s_valid));
         }
         const float w1 = scale * p.ce_w, wt = scale * p.kd_w * p.inv_t;
@@ -256,7 +255,11 @@ __global__ void __launch_bounds__(kDistillThreads<NT>, NT == 256 ? 3 : 1) distil
                 stat_collect<NT>(st, ex, buf, sc);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars.row_empty[buf]);
-                if (k > 1 && !stat_cluster(st, ex, bars, buf, use, use, k, rank, sc, aborted ? 0 : p.src.wait_ns)) aborted = true;
+                if (k > 1) {
+                    stat_send(st, ex, buf, use, k, rank);
+                    if (!peers_meet(bars, buf, use, k, aborted ? 0 : p.src.wait_ns)) aborted = true;
+                    stat_merge(st, ex, buf, use, k, sc);
+                }
                 st.correct(sc);
                 const bool empty = st.s == 0.f;  // nothing but -inf: every token's log probability is -inf
                 const float s1 = TWO ? st.s2 : st.s;
@@ -320,7 +323,7 @@ cudaError_t launch_typed(DistillParams prm, int per_sm, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     StreamSrc& s = prm.src;
     s.log2_buffers = 1;
-    const size_t fixed = 1024 + 512 + sizeof(StreamBars) + sizeof(StatExchange) + kClosers<NT> * sizeof(TeacherRow);
+    const size_t fixed = 1024 + 512 + sizeof(StreamBars) + sizeof(StatExchange) + kClosers * sizeof(TeacherRow);
     const size_t room = std::min<size_t>((228 * 1024) / per_sm, 227 * 1024) - fixed;
     s.stages = static_cast<int>(std::min<size_t>(kStreamMaxStages, room / Shape<NT>::kStageBytes));
     const size_t smem = static_cast<size_t>(s.stages) * Shape<NT>::kStageBytes;
@@ -360,7 +363,7 @@ cudaError_t launch_shape(DistillParams p, cudaStream_t stream) {
     int k = kStreamMaxCluster;
     while (k > 1 && (s.N * k > sms || 2 * nb < static_cast<int64_t>(k) * Shape<256>::kChunk)) k /= 2;
     set_cluster(s, k);
-    int per_sm = 3;
+    int per_sm = 2;
     if constexpr (GRAD) {
         // The rows between their two sweeps wait in L2 (129 MB, which the gradient's lines share): CTAs of
         // an SM while those rows stay within 64 MB, then one CTA of twice the threads.

@@ -36,7 +36,7 @@ constexpr int kSelCap = 256;    // blocks they are taken from
 constexpr int kAll = 0x7fffffff;
 constexpr int kThreads = 256;   // consumers
 using Sh = Shape<kThreads>;
-constexpr int kKeyBody = 8;     // place of the first body block's key; before it the head's and the tail's
+constexpr int kBodyAt = 8;      // place of the first body block's maximum; before it the head's and the tail's
 // Closing warps of a CTA.  The work on a row's top tokens is a chain of some 6000 cycles
 // (K = 20), so four take rows in turn; without top tokens one keeps up.
 template <bool TOPK>
@@ -47,7 +47,7 @@ struct LogprobParams {
     float inv_t;       // 1 / T
     ExpScale scale;
     int top_k;
-    int key_stride;    // places of a row's block maxima in shared memory
+    int max_stride;    // places of a row's block maxima in shared memory
     int log2_closers;  // closing warps at work
     float* logp;       // [N] or null
     float* entropy;    // [N] or null
@@ -67,23 +67,36 @@ __device__ __forceinline__ uint32_t key_of(float f) {
 __device__ __forceinline__ float float_of_key(uint32_t k) {
     return __uint_as_float(k ^ (k >> 31 ? 0x80000000u : 0xffffffffu));
 }
-// Block maxima are kept as the key's upper half for bf16 (whose lower half is constant) and whole for fp32.
+// A block: 32 elements.  Its maximum is kept as the float it is (bf16: its upper half), NaN
+// for a block that is not there.
 template <int ES>
-struct BlockKey {
+struct Block {
     using type = uint32_t;
-    static __device__ __forceinline__ uint32_t of(float f) { return key_of(f); }
-    static __device__ __forceinline__ uint32_t element(uint32_t k) { return k; }  // no element of it has a smaller key
-    static __device__ __forceinline__ float value(uint32_t k) { return float_of_key(k); }
+    static constexpr int kVec = 8;         // its 16-byte vectors
+    static constexpr int kPieces = 2;      // its 64-byte pieces, a thread's share of a chunk
+    static constexpr uint32_t kNone = 0x7fffffffu;
+    static __device__ __forceinline__ uint32_t pack(float f) { return __float_as_uint(f); }
+    static __device__ __forceinline__ float value(uint32_t v) { return __uint_as_float(v); }
 };
 template <>
-struct BlockKey<2> {
+struct Block<2> {
     using type = uint16_t;
-    static __device__ __forceinline__ uint32_t of(float f) { return key_of(f) >> 16; }
-    static __device__ __forceinline__ uint32_t element(uint32_t k) { return k << 16; }
-    static __device__ __forceinline__ float value(uint32_t k) {  // the lower half of a negative number's key is ones
-        return float_of_key(k >> 15 ? k << 16 : k << 16 | 0xffffu);
-    }
+    static constexpr int kVec = 4;
+    static constexpr int kPieces = 1;
+    static constexpr uint32_t kNone = 0x7fffu;
+    static __device__ __forceinline__ uint16_t pack(float f) { return static_cast<uint16_t>(__float_as_uint(f) >> 16); }
+    static __device__ __forceinline__ float value(uint32_t v) { return __uint_as_float(v << 16); }
 };
+// Keys of the thread maxima: of bf16 the upper half alone, whose lower half is constant.
+template <int ES>
+__device__ __forceinline__ uint32_t short_key(float f) {
+    return ES == 2 ? key_of(f) >> 16 : key_of(f);
+}
+template <int ES>
+__device__ __forceinline__ float float_of_short_key(uint32_t k) {
+    if constexpr (ES == 4) return float_of_key(k);
+    else return float_of_key(k >> 15 ? k << 16 : k << 16 | 0xffffu);  // a negative number's lower half is ones
+}
 
 // A closing warp's scratch.
 struct TopScratch {
@@ -97,22 +110,23 @@ __device__ __forceinline__ unsigned lanes_below() { return (1u << (threadIdx.x &
 template <int ES>
 struct BlockElements {
     static constexpr int EPV = 16 / ES;
-    static constexpr int N = kBlockVec * EPV;
-    uint32_t w[kBlockVec * 4];  // the elements as they lie in memory
+    static constexpr int VEC = Block<ES>::kVec;
+    static constexpr int N = VEC * EPV;
+    uint32_t w[VEC * 4];  // the elements as they lie in memory
     int n;
     int64_t col;
 
     __device__ __forceinline__ void load(const Slice& s, int id, int nblk) {
 #pragma unroll
-        for (int i = 0; i < kBlockVec * 4; ++i) w[i] = 0;
+        for (int i = 0; i < VEC * 4; ++i) w[i] = 0;
         if (id > 0 && id <= nblk) {
-            const int v0 = (id - 1) * kBlockVec;
-            const int nv = min(kBlockVec, s.nv - v0);
+            const int v0 = (id - 1) * VEC;
+            const int nv = min(VEC, s.nv - v0);
             col = s.col0 + static_cast<int64_t>(v0) * EPV;
             n = nv * EPV;
             const uint4* v = reinterpret_cast<const uint4*>(s.body) + v0;
 #pragma unroll
-            for (int i = 0; i < kBlockVec; ++i) {
+            for (int i = 0; i < VEC; ++i) {
                 if (i < nv) {
                     const uint4 q = ld_global_v4(v + i);
                     w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
@@ -147,18 +161,20 @@ struct BlockElements {
 // first for the K-th largest block by (maximum, lower index first), then, if need be, for
 // the K-th largest element.  Up to K blocks, all of them are taken.
 template <int ES>
-__device__ __noinline__ int top_list_exact(const Slice s, const typename BlockKey<ES>::type* keys, int K, TopScratch& t) {
-    using BK = BlockKey<ES>;
+__device__ __noinline__ int top_list_exact(const Slice s, const typename Block<ES>::type* maxima, int K, TopScratch& t) {
     const int lane = threadIdx.x & 31;
-    const int nblk = (s.nv + kBlockVec - 1) / kBlockVec;
+    const int nblk = (s.nv + Block<ES>::kVec - 1) / Block<ES>::kVec;
     const int nreal = nblk + (s.h > 0) + (s.t > 0);
-    auto key = [&](int b) -> uint32_t { return keys[b == 0 ? 0 : b > nblk ? 1 : kKeyBody - 1 + b]; };
+    auto key = [&](int b) -> uint32_t {
+        const float f = Block<ES>::value(maxima[b == 0 ? 0 : b > nblk ? 1 : kBodyAt - 1 + b]);
+        return f == f ? key_of(f) : 0u;
+    };
     // ---- the blocks: keys above lo, and of those equal to lo the ids up to last
     uint32_t lo = 1;
     int last = kAll;
     if (nreal > K) {
-        uint32_t hi = ES == 2 ? 0x10000u : 0xffffffffu;  // above every key but a NaN's
-        int c_lo = nreal, c_hi = 0;                      // blocks at or above lo and hi
+        uint32_t hi = 0xffffffffu;   // above every key
+        int c_lo = nreal, c_hi = 0;  // blocks at or above lo and hi
         while (hi - lo > 1 && c_lo > kSelCap) {
             const uint32_t mid = lo + (hi - lo) / 2;
             int n = 0;
@@ -214,7 +230,7 @@ __device__ __noinline__ int top_list_exact(const Slice s, const typename BlockKe
         return __reduce_add_sync(0xffffffffu, n);
     };
     // every count is at least K at b0 (or takes every element) and less than K at b1
-    unsigned long long b0 = static_cast<unsigned long long>(BK::element(lo)) << 32, b1 = ~0ull;
+    unsigned long long b0 = static_cast<unsigned long long>(lo) << 32, b1 = ~0ull;
     if (at_least(b0) > kListCap) {
         while (b1 - b0 > 1) {
             const unsigned long long mid = b0 + (b1 - b0) / 2;
@@ -239,30 +255,65 @@ __device__ __noinline__ int top_list_exact(const Slice s, const typename BlockKe
     return min(n, kListCap);
 }
 
-// This CTA's largest elements of its slice onto t.list: at least the min(K, all) largest
-// ones, at most kListCap.  Returns how many.  keys are the block maxima (kKeyBody the first
-// body block's; 0 and 1 the head's and tail's, 0 where there is none), thread_max the threads'.
+// Of the elements of a 16-byte word group: a bit for each that is >= floor (or == floor).
+// bf16: bit k the lower and bit 16 + k the upper element of word k; fp32: bit k element k.
+template <int ES, bool EQUAL, int WORDS>
+__device__ __forceinline__ uint32_t hit_bits(const uint32_t (&w)[WORDS], float floor) {
+    uint32_t bits = 0;
+    if constexpr (ES == 2) {
+        const __nv_bfloat162 f = __float2bfloat162_rn(floor);
+#pragma unroll
+        for (int k = 0; k < WORDS; ++k) {
+            const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&w[k]);
+            bits |= (EQUAL ? __heq2_mask(x, f) : __hge2_mask(x, f)) & (0x10001u << k);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < WORDS; ++k) {
+            const float x = __uint_as_float(w[k]);
+            bits |= (EQUAL ? x == floor : x >= floor) ? 1u << k : 0u;
+        }
+    }
+    return bits;
+}
 template <int ES>
-__device__ __noinline__ int top_list(const Slice s, const typename BlockKey<ES>::type* keys,
-                                        const uint32_t* thread_max, int K, TopScratch& t) {
-    using BK = BlockKey<ES>;
-    constexpr int EPV = 16 / ES;
+__device__ __forceinline__ int bit_of_element(int e) {
+    return ES == 2 ? (e >> 1) | (e & 1) << 4 : e;
+}
+template <int ES>
+__device__ __forceinline__ int element_of_bit(int b) {
+    return ES == 2 ? (b & 15) << 1 | b >> 4 : b;
+}
+// the bits of the first n elements
+template <int ES>
+__device__ __forceinline__ uint32_t first_bits(int n) {
+    if constexpr (ES == 2) return ((1u << (n + 1) / 2) - 1u) | ((1u << n / 2) - 1u) << 16;
+    else return (1u << n) - 1u;
+}
+
+// This CTA's largest elements of its slice onto t.list: at least the min(K, all) largest
+// ones, at most kListCap.  Returns how many.  maxima are the blocks' (kBodyAt the first of
+// the body; 0 and 1 the head's and tail's), thread_max the keys of the threads'.
+template <int ES>
+__device__ __noinline__ int top_list(const Slice s, const typename Block<ES>::type* maxima, const uint32_t* thread_max,
+                                     int K, TopScratch& t) {
+    using B = Block<ES>;
     constexpr int PER = kThreads / 32;
     const int lane = threadIdx.x & 31;
-    const int nblk = (s.nv + kBlockVec - 1) / kBlockVec;
-    // A threshold that K threads' maxima, so K blocks, reach: the K-th largest of the 256
-    // thread maxima, or a little below it.  Of blocks in random order about
+    const int nblk = (s.nv + B::kVec - 1) / B::kVec;
+    // A threshold that K threads' maxima, so K elements, reach: the K-th largest of the 256
+    // thread maxima, or a little below it.  Of 64-byte pieces in random order about
     // -256 ln(1 - K / 256) are at or above it.
-    uint32_t lo = 1;
-    if (min(nblk, kThreads) >= K) {
+    float floor = kNegInf;
+    if (min((s.nv + kBlockVec - 1) / kBlockVec, kThreads) >= K) {
         uint32_t v[PER], least = 0xffffffffu, hi = 0;
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
             v[j] = thread_max[lane + 32 * j];
-            least = min(least, v[j] - 1u);  // 0, no block, becomes the largest
+            least = min(least, v[j] - 1u);  // 0, no piece, becomes the largest
             hi = max(hi, v[j]);
         }
-        lo = __reduce_min_sync(0xffffffffu, least) + 1u;
+        uint32_t lo = __reduce_min_sync(0xffffffffu, least) + 1u;
         hi = __reduce_max_sync(0xffffffffu, hi) + 1u;
         const int most = K + K / 8 + 4;
         while (hi - lo > 1) {
@@ -278,46 +329,43 @@ __device__ __noinline__ int top_list(const Slice s, const typename BlockKey<ES>:
                 hi = mid;
             }
         }
+        floor = float_of_short_key<ES>(lo);
     }
-    // The blocks that reach a threshold, 16 bytes of keys a lane and turn.
-    auto blocks_from = [&](uint32_t least) {
-        constexpr int KPV = 16 / sizeof(typename BK::type);
-        const uint4* kv = reinterpret_cast<const uint4*>(keys + kKeyBody);
+    // The blocks that reach it (above: that are above it), 16 bytes of maxima a lane and turn.
+    auto blocks_from = [&](bool above) {
+        constexpr int PACK = 16 / sizeof(typename B::type);
+        const uint4* mv = reinterpret_cast<const uint4*>(maxima + kBodyAt);
         int n = 0;
-#pragma unroll 2
-        for (int b0 = 0; b0 < nblk; b0 += 32 * KPV) {
-            const int b = b0 + lane * KPV;
-            uint4 w = make_uint4(0u, 0u, 0u, 0u);
-            if (b < nblk) w = kv[b / KPV];
-            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+        for (int b0 = 0; b0 < nblk && n <= kSelCap; b0 += 32 * PACK) {
+            const int b = b0 + lane * PACK;
             uint32_t hit = 0;
-#pragma unroll
-            for (int e = 0; e < KPV; ++e) {
-                const uint32_t key = ES == 2 ? (e & 1 ? x[e / 2] >> 16 : x[e / 2] & 0xffffu) : x[e];
-                hit |= key >= least ? 1u << e : 0u;
+            if (b < nblk) {
+                const uint4 q = mv[b / PACK];
+                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+                hit = hit_bits<ES, false>(w, floor);
+                if (above) hit &= ~hit_bits<ES, true>(w, floor);
+                if (nblk - b < PACK) hit &= first_bits<ES>(nblk - b);
             }
-            if (b + KPV > nblk) hit &= b < nblk ? (1u << (nblk - b)) - 1u : 0u;
             for (unsigned m = __ballot_sync(0xffffffffu, hit != 0); m; m = __ballot_sync(0xffffffffu, hit != 0)) {
                 const int at = n + __popc(m & lanes_below());
-                if (hit && at < kSelCap) t.sel[at] = static_cast<uint16_t>(b + __ffs(hit));
+                if (hit && at < kSelCap) t.sel[at] = static_cast<uint16_t>(1 + b + element_of_bit<ES>(__ffs(hit) - 1));
                 hit &= hit - 1;
                 n += __popc(m);
             }
-            if (n > kSelCap) break;
         }
         __syncwarp();
         return n;
     };
-    int n_sel = blocks_from(lo), need = kAll, strict = kAll;  // sel[strict ..]: blocks whose maximum is lo, in order
+    int n_sel = blocks_from(false), need = kAll, strict = kAll;  // sel[strict ..]: blocks whose maximum is the floor, in order
     if (n_sel > kSelCap) {
         // Ties at the threshold (a mask that leaves fewer than K tokens): the blocks above
         // it, and the first blocks that reach it, as many as can matter.
-        strict = blocks_from(lo + 1);
+        strict = blocks_from(true);
         if (strict < K) {
             need = K - strict;
             int have = 0;
             for (int b0 = 0; b0 < nblk && have < need; b0 += 32) {
-                const bool tie = b0 + lane < nblk && keys[kKeyBody + b0 + lane] == lo;
+                const bool tie = b0 + lane < nblk && B::value(maxima[kBodyAt + b0 + lane]) == floor;
                 const unsigned m = __ballot_sync(0xffffffffu, tie);
                 const int at = have + __popc(m & lanes_below());
                 if (tie && at < need) t.sel[strict + at] = static_cast<uint16_t>(1 + b0 + lane);
@@ -328,65 +376,51 @@ __device__ __noinline__ int top_list(const Slice s, const typename BlockKey<ES>:
         }
     }
     if (n_sel <= kSelCap) {
-        // Four lanes a block, one vector each (re-read from L2); the elements at or above the threshold.
-        constexpr int TURNS = 4;  // loads that go out before the first is looked at
-        const float floor = lo == 1 ? kNegInf : BK::value(lo);
+        // A 64-byte piece a lane and turn (re-read from L2); its elements at or above the threshold.
+        constexpr int EPV = 16 / ES;
         const uint4* body = reinterpret_cast<const uint4*>(s.body);
         int n = 0;
-        for (int i0 = 0; i0 < n_sel * kBlockVec; i0 += 32 * TURNS) {
-            uint4 w[TURNS];
-            int vec[TURNS];
+        for (int i0 = 0; i0 < n_sel * B::kPieces; i0 += 32) {
+            const int i = i0 + lane, j = i / B::kPieces;
+            const bool there = j < n_sel;
+            const int vec = there ? (t.sel[j] - 1) * B::kVec + i % B::kPieces * kBlockVec : 0;
+            const int nv = there ? min(kBlockVec, s.nv - vec) : 0;
+            uint32_t w[4 * kBlockVec];
 #pragma unroll
-            for (int q = 0; q < TURNS; ++q) {
-                const int j = (i0 + 32 * q + lane) / kBlockVec;
-                vec[q] = j < n_sel ? (t.sel[j] - 1) * kBlockVec + (lane & (kBlockVec - 1)) : s.nv;
-                w[q] = RowMath<ES>::pad();
-                if (vec[q] < s.nv) w[q] = ld_global_v4(body + vec[q]);
+            for (int q = 0; q < kBlockVec; ++q) {
+                uint4 r = RowMath<ES>::pad();
+                if (q < nv) r = ld_global_v4(body + vec + q);
+                w[4 * q] = r.x, w[4 * q + 1] = r.y, w[4 * q + 2] = r.z, w[4 * q + 3] = r.w;
             }
-#pragma unroll
-            for (int q = 0; q < TURNS; ++q) {
-                if (i0 + 32 * q >= n_sel * kBlockVec) break;
-                uint32_t hit = 0, tie = 0;
-#pragma unroll
-                for (int e = 0; e < EPV / 2; ++e) {
-                    float a, b;
-                    f2_unpack(vec_pair<ES>(w[q], e), a, b);
-                    hit |= (a >= floor ? 1u << 2 * e : 0u) | (b >= floor ? 2u << 2 * e : 0u);
+            uint32_t hit = hit_bits<ES, false>(w, floor);
+            if (nv < kBlockVec) hit &= nv > 0 ? first_bits<ES>(nv * EPV) : 0u;
+            if (strict != kAll) {
+                // an equal one counts only if fewer than `need` come before it: those of its block, and
+                // one at least in each tied block before
+                const uint32_t tie = hit & hit_bits<ES, true>(w, floor);
+                int before = max(0, j - strict);
+                if (B::kPieces > 1) {
+                    const int o = __shfl_up_sync(0xffffffffu, __popc(tie), 1);
+                    if (i % B::kPieces) before += o;
                 }
-                if (vec[q] >= s.nv) hit = 0;
-                if (strict != kAll) {
-                    // an equal one counts only if fewer than `need` come before it: those of its block's
-                    // earlier vectors, and one at least in each tied block before
+                for (int e = 0; e < 64 / ES; ++e)
+                    if (tie >> bit_of_element<ES>(e) & 1u && before++ >= need) hit &= ~(1u << bit_of_element<ES>(e));
+            }
+            int at = __popc(hit);  // then the places before the lane's
 #pragma unroll
-                    for (int e = 0; e < EPV / 2; ++e) {
-                        float a, b;
-                        f2_unpack(vec_pair<ES>(w[q], e), a, b);
-                        tie |= (a == floor ? 1u << 2 * e : 0u) | (b == floor ? 2u << 2 * e : 0u);
-                    }
-                    tie &= hit;
-                    int sum = __popc(tie);
-#pragma unroll
-                    for (int off = 1; off < kBlockVec; off <<= 1) {
-                        const int o = __shfl_up_sync(0xffffffffu, sum, off, kBlockVec);
-                        if ((lane & (kBlockVec - 1)) >= off) sum += o;
-                    }
-                    int room = need - (sum - __popc(tie)) - max(0, (i0 + 32 * q + lane) / kBlockVec - strict);
-                    for (uint32_t m = tie; m; m &= m - 1)
-                        if (--room < 0) hit &= ~(m & -m);
-                }
-                const uint32_t col = static_cast<uint32_t>(s.col0) + static_cast<uint32_t>(vec[q]) * EPV;
-                for (unsigned m = __ballot_sync(0xffffffffu, hit != 0); m; m = __ballot_sync(0xffffffffu, hit != 0)) {
-                    const int at = n + __popc(m & lanes_below());
-                    n += __popc(m);
-                    if (hit) {
-                        const int e = __ffs(hit) - 1;
-                        hit &= hit - 1;
-                        const uint32_t x = ES == 2 ? e >> 1 : e;
-                        const uint32_t word = x & 2 ? (x & 1 ? w[q].w : w[q].z) : (x & 1 ? w[q].y : w[q].x);
-                        const float f = ES == 2 ? (e & 1 ? bf16_hi(word) : bf16_lo(word)) : __uint_as_float(word);
-                        if (at < kListCap) t.list[at] = (static_cast<unsigned long long>(key_of(f)) << 32) | ~(col + e);
-                    }
-                }
+            for (int off = 1; off < 32; off <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, at, off);
+                if (lane >= off) at += o;
+            }
+            const int end = n + __shfl_sync(0xffffffffu, at, 31);
+            at += n - __popc(hit);
+            n = end;
+            for (; hit; hit &= hit - 1, ++at) {
+                const int e = element_of_bit<ES>(__ffs(hit) - 1);
+                const int64_t col = s.col0 + static_cast<int64_t>(vec) * EPV + e;
+                const float f = load_scalar<ES>(s.rowp + col * ES);  // it is in L1
+                if (at < kListCap)
+                    t.list[at] = (static_cast<unsigned long long>(key_of(f)) << 32) | ~static_cast<uint32_t>(col);
             }
         }
         if (s.h + s.t > 0) {
@@ -403,7 +437,7 @@ __device__ __noinline__ int top_list(const Slice s, const typename BlockKey<ES>:
         __syncwarp();
         if (n <= kListCap) return n;
     }
-    return top_list_exact<ES>(s, keys, K, t);
+    return top_list_exact<ES>(s, maxima, K, t);
 }
 
 // The list in descending order, R items a lane: a bitonic sort in registers, lane l
@@ -468,6 +502,7 @@ __device__ __noinline__ void sort_long_list(unsigned long long* list, int n) {
 __device__ __forceinline__ void top_ordered(unsigned long long* list, int n) {
     if (n <= 32) sort_list<1>(list, n);
     else if (n <= 64) sort_list<2>(list, n);
+    else if (n <= 128) sort_list<4>(list, n);
     else if (n <= 256) sort_list<8>(list, n);
     else sort_long_list(list, n);
     __syncwarp();
@@ -483,9 +518,9 @@ __global__ void __launch_bounds__(kLogprobThreads<TOPK>, TOPK ? 2 : 3) logprobs_
     __shared__ StatExchange ex;
     __shared__ TopScratch top[TOPK ? kClosers<TOPK> : 1];
     __shared__ uint32_t thread_max[TOPK ? kMaxBuffers : 1][kThreads];  // key of the largest of a thread's blocks, 0: it has none
-    using KeyT = typename BlockKey<ES>::type;
+    using MaxT = typename Block<ES>::type;
     unsigned char* ring = smem;
-    KeyT* keys = reinterpret_cast<KeyT*>(smem + p.src.stages * Sh::kStageBytes);  // key_stride a buffer
+    MaxT* maxima = reinterpret_cast<MaxT*>(smem + p.src.stages * Sh::kStageBytes);  // of the blocks, max_stride a buffer
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = p.src.k;
     const int rank = k > 1 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -512,7 +547,7 @@ __global__ void __launch_bounds__(kLogprobThreads<TOPK>, TOPK ? 2 : 3) logprobs_
             move_slice<ES>(p.src, row, rank, s);
             row_begin(p.src, bars, rp, pos);
             const int buf = rp.buf(p.src);
-            KeyT* rk = keys + buf * p.key_stride;
+            MaxT* rm = maxima + buf * p.max_stride;
             RunStat<ENT, false> st(p.scale);
             float most = kNegInf;  // of the thread's blocks
             for (int c0 = 0; c0 < s.nv; c0 += Sh::kChunk) {
@@ -522,10 +557,12 @@ __global__ void __launch_bounds__(kLogprobThreads<TOPK>, TOPK ? 2 : 3) logprobs_
                     if constexpr (TOPK) load_block<ES, kThreads>(stage, nl, v);
                     else load_strided<ES, kThreads>(stage, nl, v);
                 });
-                const float bmax = st.template add_vecs<ES>(v, p.scale);
+                const float mine = st.template add_vecs<ES>(v, p.scale);
                 if (TOPK) {
-                    if (tid * kBlockVec < nl) rk[kKeyBody + c0 / kBlockVec + tid] = static_cast<KeyT>(BlockKey<ES>::of(bmax));
-                    most = fmaxf(most, bmax);
+                    most = fmaxf(most, mine);
+                    const float both = Block<ES>::kPieces > 1 ? fmaxf(mine, __shfl_xor_sync(0xffffffffu, mine, 1)) : mine;
+                    if (tid * kBlockVec < nl && tid % Block<ES>::kPieces == 0)
+                        rm[kBodyAt + (c0 / kBlockVec + tid) / Block<ES>::kPieces] = static_cast<MaxT>(Block<ES>::pack(both));
                 }
             }
             if (s.h + s.t > 0 && warp == 0) {  // the head's and the tail's scalars, one a lane
@@ -535,14 +572,14 @@ __global__ void __launch_bounds__(kLogprobThreads<TOPK>, TOPK ? 2 : 3) logprobs_
                 if (TOPK) {
                     const float hm = warp_max_redux(tid < s.h ? e : kNegInf), tm = warp_max_redux(tid < s.h ? kNegInf : e);
                     if (tid == 0) {
-                        rk[0] = s.h > 0 ? BlockKey<ES>::of(hm) : 0;
-                        rk[1] = s.t > 0 ? BlockKey<ES>::of(tm) : 0;
+                        rm[0] = s.h > 0 ? Block<ES>::pack(hm) : Block<ES>::kNone;
+                        rm[1] = s.t > 0 ? Block<ES>::pack(tm) : Block<ES>::kNone;
                     }
                 }
             } else if (TOPK && tid == 0) {
-                rk[0] = rk[1] = 0;
+                rm[0] = rm[1] = Block<ES>::kNone;
             }
-            if (TOPK) thread_max[buf][tid] = tid * kBlockVec < s.nv ? BlockKey<ES>::of(most) : 0u;
+            if (TOPK) thread_max[buf][tid] = tid * kBlockVec < s.nv ? short_key<ES>(most) : 0u;
             stat_publish(st, ex, buf);
             row_end(bars, buf);
             ++rp.n;
@@ -592,7 +629,6 @@ __global__ void __launch_bounds__(kLogprobThreads<TOPK>, TOPK ? 2 : 3) logprobs_
                 const float x_y = __shfl_sync(0xffffffffu, x_lab, j);
                 const int buf = rp.buf(p.src);
                 const uint32_t use = rp.use(p.src);
-                const uint32_t phase = TOPK ? 2 * use : use;  // exchanges of the buffer with the cluster so far
                 if (!aborted && !stream_wait(bars, &bars.row_full[buf], use & 1u, p.src.wait_ns)) aborted = true;
                 RunStat<ENT, false> st(p.scale);
                 stat_collect<kThreads>(st, ex, buf, p.scale);
@@ -600,8 +636,27 @@ __global__ void __launch_bounds__(kLogprobThreads<TOPK>, TOPK ? 2 : 3) logprobs_
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars.row_empty[buf]);
                 }
-                if (k > 1 && !stat_cluster(st, ex, bars, buf, use, phase, k, rank, p.scale, aborted ? 0 : p.src.wait_ns))
-                    aborted = true;
+                int n = 0;
+                const int K = p.top_k;
+                unsigned long long* best = top[TOPK ? me : 0].list;
+                if constexpr (TOPK) {  // this CTA's largest, in order
+                    TopScratch& t = top[me];
+                    // the last row's list may still be read by the cluster's other CTAs
+                    if (k > 1 && use > 0 && !peers_wait(bars, &bars.peers_done[buf], (use & 1u) ^ 1u, aborted ? 0 : p.src.wait_ns))
+                        aborted = true;
+                    move_slice<ES>(p.src, row, rank, s);
+                    if (st.s == st.s) n = top_list<ES>(s, maxima + buf * p.max_stride, thread_max[buf], K, t);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars.row_empty[buf]);
+                    top_ordered(best, n);
+                    if (k > 1)
+                        for (int i = n + lane; i < K; i += 32) best[i] = 0ull;
+                }
+                if (k > 1) {
+                    stat_send(st, ex, buf, use, k, rank);
+                    if (!peers_meet(bars, buf, use, k, aborted ? 0 : p.src.wait_ns)) aborted = true;
+                    stat_merge(st, ex, buf, use, k, p.scale);
+                }
                 st.correct(p.scale);
                 const float ln_s = logf(st.s);
                 const bool empty = st.s == 0.f;
@@ -615,31 +670,20 @@ __global__ void __launch_bounds__(kLogprobThreads<TOPK>, TOPK ? 2 : 3) logprobs_
                     if (p.stats) p.stats[row] = make_float2(empty ? kNegInf : st.m, ln_s);
                 }
                 if constexpr (TOPK) {
-                    TopScratch& t = top[me];
-                    const int K = p.top_k;
                     const bool none = !(st.s == st.s);  // a NaN or +inf in the row: no order to speak of
-                    move_slice<ES>(p.src, row, rank, s);
-                    int n = 0;
-                    if (!none) n = top_list<ES>(s, keys + buf * p.key_stride, thread_max[buf], K, t);
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars.row_empty[buf]);
                     float* olp = p.top_lp + row * K;
                     int32_t* oid = p.top_ids + row * K;
                     auto write = [&](int r, unsigned long long item) {
-                        if (aborted) return;
+                        if (aborted || none) return;
                         olp[r] = empty ? kNegInf : (float_of_key(static_cast<uint32_t>(item >> 32)) - st.m) * p.inv_t - ln_s;
                         oid[r] = static_cast<int32_t>(~static_cast<uint32_t>(item));
                     };
-                    unsigned long long* best = t.list;
-                    top_ordered(best, n);
                     if (k == 1) {
                         for (int i = lane; i < min(n, K); i += 32) write(i, best[i]);
                     } else {
                         // The cluster's lists, each in order and K long: an item's rank is the sum of its places in
                         // them, one lane an item and list.  They are copied here first when there is room.
-                        for (int i = n + lane; i < K; i += 32) best[i] = 0ull;
-                        if (!peers_meet(bars, buf, phase + 1, k, aborted ? 0 : p.src.wait_ns)) aborted = true;
-                        unsigned long long* copies = t.list + kTopKMax;
+                        unsigned long long* copies = best + kTopKMax;
                         const bool copy = K * k <= kListCap - kTopKMax;
                         if (copy) {
                             for (int i = lane; i < K * k; i += 32) {
@@ -666,6 +710,8 @@ __global__ void __launch_bounds__(kLogprobThreads<TOPK>, TOPK ? 2 : 3) logprobs_
                             for (int off = 1; off < k; off <<= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
                             if (o == 0 && item && a < K) write(a, item);
                         }
+                        __syncwarp();
+                        if (lane < k) remote_arrive(&bars.peers_done[buf], static_cast<uint32_t>(lane));
                     }
                     if (none && rank == 0) {
                         for (int i = lane; i < K; i += 32) {
@@ -687,8 +733,8 @@ __global__ void __launch_bounds__(kLogprobThreads<TOPK>, TOPK ? 2 : 3) logprobs_
     if (tid == Sh::kFirstCloser) {
         if (stream_aborted(bars)) atomicOr(&p.ws->err, static_cast<unsigned>(FOAK_ERRBIT_TIMEOUT));
         if (atom_add_acq_rel_gpu(&p.ws->done, 1u) == gridDim.x - 1) {
+            p.ws->done = 0u;  // every other CTA is past its own access
             const unsigned e = atomicExch(&p.ws->err, 0u);
-            atomicExch(&p.ws->done, 0u);
             if (p.err) *p.err = static_cast<int32_t>(e);
         }
     }
@@ -712,9 +758,9 @@ cudaError_t launch_typed(LogprobParams prm, cudaStream_t stream) {
     int k = kStreamMaxCluster;
     while (k > 1 && (s.N * k > sms || 2 * nb < static_cast<int64_t>(k) * Sh::kChunk)) k /= 2;
     set_cluster(s, k);
-    const int64_t nblk = ((nb + kBlockVec - 1) / kBlockVec + s.k - 1) / s.k + 1;
-    prm.key_stride = static_cast<int>((kKeyBody + nblk + 63) / 64 * 64);
-    const size_t buffer = TOPK ? prm.key_stride * sizeof(typename BlockKey<ES>::type) : 0;
+    const int64_t nblk = (((nb + kBlockVec - 1) / kBlockVec + s.k - 1) / s.k + 1) / Block<ES>::kPieces + 1;
+    prm.max_stride = static_cast<int>((kBodyAt + nblk + 63) / 64 * 64);
+    const size_t buffer = TOPK ? prm.max_stride * sizeof(typename Block<ES>::type) : 0;
     // A buffer for each closing warp, fewer where the keys are large; CTAs an SM as the
     // registers allow, fewer where a ring of two stages would not fit.
     const size_t fixed = 1024 + 256 + sizeof(StreamBars) + sizeof(StatExchange) +

@@ -147,6 +147,7 @@ struct StreamBars {
     uint64_t row_ready[kMaxBuffers];   // the closing warp has what the second sweep needs
     uint64_t row_stored[kMaxBuffers];  // the second sweep's stores are made: one arrival a consumer warp
     uint64_t peers[kMaxBuffers];       // the cluster's CTAs have sent their part: one arrival a CTA
+    uint64_t peers_done[kMaxBuffers];  // and have read this CTA's
     int abort;              // a wait gave up: everyone stops waiting and winds down
 };
 
@@ -163,6 +164,7 @@ __device__ __forceinline__ void stream_init(StreamBars& b, int stages, int clust
             mbar_init(&b.row_ready[i], 1);
             mbar_init(&b.row_stored[i], Shape<NT>::kWarps);
             mbar_init(&b.peers[i], cluster);
+            mbar_init(&b.peers_done[i], cluster);
         }
         b.abort = 0;
         fence_mbar_init();
@@ -538,17 +540,15 @@ __device__ __forceinline__ void stat_collect(RunStat<ENT, TWO>& st, const StatEx
 // In a cluster, by the closing warps of a row: this CTA's set to every CTA, then the row's
 // from all.  A slot's next use but one follows an exchange that every CTA enters only after
 // it has read the slot.
-__device__ __forceinline__ bool peers_meet(StreamBars& bars, int buf, uint32_t phase, int k, uint64_t limit_ns) {
+__device__ __forceinline__ bool peers_meet(StreamBars& bars, int buf, uint32_t use, int k, uint64_t limit_ns) {
     const int lane = threadIdx.x & 31;
     __syncwarp();
     if (lane < k) remote_arrive(&bars.peers[buf], static_cast<uint32_t>(lane));
     __syncwarp();
-    return peers_wait(bars, &bars.peers[buf], phase & 1u, limit_ns);
+    return peers_wait(bars, &bars.peers[buf], use & 1u, limit_ns);
 }
 template <bool ENT, bool TWO>
-__device__ __forceinline__ bool stat_cluster(RunStat<ENT, TWO>& st, StatExchange& ex, StreamBars& bars, int buf,
-                                             uint32_t use, uint32_t phase, int k, int rank, const ExpScale& x,
-                                             uint64_t limit_ns) {
+__device__ __forceinline__ void stat_send(const RunStat<ENT, TWO>& st, StatExchange& ex, int buf, uint32_t use, int k, int rank) {
     const int lane = threadIdx.x & 31;
     if (lane < k) {
         const uint32_t to = mapa_u32(&ex.cta[buf][use & 1u][rank], static_cast<uint32_t>(lane));
@@ -556,11 +556,13 @@ __device__ __forceinline__ bool stat_cluster(RunStat<ENT, TWO>& st, StatExchange
                      "f"(st.s2)
                      : "memory");
     }
-    if (!peers_meet(bars, buf, phase, k, limit_ns)) return false;
+}
+template <bool ENT, bool TWO>
+__device__ __forceinline__ void stat_merge(RunStat<ENT, TWO>& st, const StatExchange& ex, int buf, uint32_t use, int k,
+                                           const ExpScale& x) {
     const float4* from = ex.cta[buf][use & 1u];
     st.set(from[0], x);
     for (int o = 1; o < k; ++o) st.merge(from[o], x);
-    return true;
 }
 
 // Number of valid labels, counted by the consumer threads; scratch: an int a warp.
