@@ -145,6 +145,23 @@ def _stream(device, stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+# The current stream's handle without a Stream object, where torch has it (a call of a few
+# microseconds' work spends two of them on the object).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_handle(device, stream):
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _logits_args(logits):
     if logits.dim() != 2 or logits.stride(1) != 1:
         raise ValueError("logits must be a 2-D tensor with unit column stride (N x V, row stride ld)")
@@ -163,6 +180,12 @@ def _labels_arg(labels, N, device):
     if labels.device != device:
         raise ValueError("labels must live on the logits' device")
     return labels
+
+
+def _header_workspace(device) -> torch.Tensor:
+    """The cached workspace of calls that need its header alone."""
+    ws = _ws_cache.get(device)
+    return workspace(0, device) if ws is None else ws
 
 
 def workspace(N: int, device) -> torch.Tensor:
@@ -656,10 +679,10 @@ def foak_logprobs_forward(logits, labels=None, *, top_k: int = 0, temperature: f
     top_lp = torch.empty(N, K, dtype=f32, device=dev) if K else None
     top_ids = torch.empty(N, K, dtype=torch.int32, device=dev) if K else None
     err = torch.empty(1, dtype=torch.int32, device=dev)
-    ws = workspace(0, dev) if workspace_tensor is None else workspace_tensor
-    st = lib.foak_logprobs_forward(_ptr(logits), dt, ld, _ptr(labels), N, V, int(ignore_index), float(temperature), K,
-                                   _ptr(logp), _ptr(entropy), _ptr(lse), _ptr(stats), _ptr(top_lp), _ptr(top_ids),
-                                   _ptr(err), _ptr(ws), ws.numel(), _stream(dev, stream))
+    ws = _header_workspace(dev) if workspace_tensor is None else workspace_tensor
+    st = lib.foak_logprobs_forward(_addr(logits), dt, ld, _addr(labels), N, V, int(ignore_index), float(temperature), K,
+                                   _addr(logp), _addr(entropy), _addr(lse), _addr(stats), _addr(top_lp),
+                                   _addr(top_ids), _addr(err), _addr(ws), ws.numel(), _stream_handle(dev, stream))
     _check(st, "foak_logprobs_forward")
     return dict(logp=logp, entropy=entropy, lse=lse, stats=stats, top_logprobs=top_lp, top_ids=top_ids, err=err)
 
@@ -682,9 +705,9 @@ def foak_logprobs_backward(logits, labels, stats, grad_logp=None, entropy=None, 
         raise ValueError("grad_entropy needs the forward's entropy")
     dlogits = _dlogits_arg(dlogits, logits, N, V, ld)
     err = torch.empty(1, dtype=torch.int32, device=dev)
-    st = lib.foak_logprobs_backward(_ptr(dlogits), _ptr(logits), dt, ld, _ptr(labels), N, V, int(ignore_index),
-                                    float(temperature), _ptr(stats), _ptr(grad_logp), _ptr(entropy),
-                                    _ptr(grad_entropy), _ptr(err), _stream(dev, stream))
+    st = lib.foak_logprobs_backward(_addr(dlogits), _addr(logits), dt, ld, _addr(labels), N, V, int(ignore_index),
+                                    float(temperature), _addr(stats), _addr(grad_logp), _addr(entropy),
+                                    _addr(grad_entropy), _addr(err), _stream_handle(dev, stream))
     _check(st, "foak_logprobs_backward")
     return dlogits, err
 
@@ -734,11 +757,11 @@ def foak_distill_forward(logits, labels, teacher_ids, teacher_logprobs, *, ce_we
     n_valid = torch.empty(1, dtype=torch.int32, device=dev)
     err = torch.empty(1, dtype=torch.int32, device=dev)
     ws = workspace(N, dev) if workspace_tensor is None else workspace_tensor
-    st = lib.foak_distill_forward(_ptr(logits), dt, ld, _ptr(labels), N, V, int(ignore_index), _ptr(teacher_ids),
-                                  _ptr(teacher_logprobs), ldt, K, int(bool(normalize)), float(ce_weight),
-                                  float(kd_weight), float(temperature), float(denom), _ptr(loss), _ptr(row_ce),
-                                  _ptr(row_kd), _ptr(stats), _ptr(n_valid), _ptr(err), _ptr(ws), ws.numel(),
-                                  _stream(dev, stream))
+    st = lib.foak_distill_forward(_addr(logits), dt, ld, _addr(labels), N, V, int(ignore_index), _addr(teacher_ids),
+                                  _addr(teacher_logprobs), ldt, K, int(bool(normalize)), float(ce_weight),
+                                  float(kd_weight), float(temperature), float(denom), _addr(loss), _addr(row_ce),
+                                  _addr(row_kd), _addr(stats), _addr(n_valid), _addr(err), _addr(ws), ws.numel(),
+                                  _stream_handle(dev, stream))
     _check(st, "foak_distill_forward")
     return dict(loss=loss, row_ce=row_ce, row_kd=row_kd, stats=stats, n_valid=n_valid, err=err)
 
@@ -764,11 +787,11 @@ def foak_distill_fwd_bwd(logits, labels, teacher_ids, teacher_logprobs, *, ce_we
     n_valid = torch.empty(1, dtype=torch.int32, device=dev)
     err = torch.empty(1, dtype=torch.int32, device=dev)
     ws = workspace(N, dev) if workspace_tensor is None else workspace_tensor
-    st = lib.foak_distill_fwd_bwd(_ptr(logits), _ptr(dlogits), dt, ld, _ptr(labels), N, V, int(ignore_index),
-                                  _ptr(teacher_ids), _ptr(teacher_logprobs), ldt, K, int(bool(normalize)),
+    st = lib.foak_distill_fwd_bwd(_addr(logits), _addr(dlogits), dt, ld, _addr(labels), N, V, int(ignore_index),
+                                  _addr(teacher_ids), _addr(teacher_logprobs), ldt, K, int(bool(normalize)),
                                   float(ce_weight), float(kd_weight), float(temperature), float(g), float(denom),
-                                  _ptr(loss), _ptr(row_ce), _ptr(row_kd), _ptr(n_valid), _ptr(err), _ptr(ws),
-                                  ws.numel(), _stream(dev, stream))
+                                  _addr(loss), _addr(row_ce), _addr(row_kd), _addr(n_valid), _addr(err), _addr(ws),
+                                  ws.numel(), _stream_handle(dev, stream))
     _check(st, "foak_distill_fwd_bwd")
     return dict(loss=loss, dlogits=dlogits, row_ce=row_ce, row_kd=row_kd, n_valid=n_valid, err=err)
 
@@ -789,9 +812,9 @@ def foak_distill_backward(logits, labels, teacher_ids, teacher_logprobs, stats, 
         raise ValueError("grad_out must be a float32 scalar tensor on the logits' device")
     dlogits = _dlogits_arg(dlogits, logits, N, V, ld)
     err = torch.empty(1, dtype=torch.int32, device=dev)
-    st = lib.foak_distill_backward(_ptr(dlogits), _ptr(logits), dt, ld, _ptr(labels), N, V, int(ignore_index),
-                                   _ptr(teacher_ids), _ptr(teacher_logprobs), ldt, K, int(bool(normalize)),
-                                   float(ce_weight), float(kd_weight), float(temperature), _ptr(stats),
-                                   _ptr(grad_out), float(denom), _ptr(err), _stream(dev, stream))
+    st = lib.foak_distill_backward(_addr(dlogits), _addr(logits), dt, ld, _addr(labels), N, V, int(ignore_index),
+                                   _addr(teacher_ids), _addr(teacher_logprobs), ldt, K, int(bool(normalize)),
+                                   float(ce_weight), float(kd_weight), float(temperature), _addr(stats),
+                                   _addr(grad_out), float(denom), _addr(err), _stream_handle(dev, stream))
     _check(st, "foak_distill_backward")
     return dlogits, err
