@@ -32,8 +32,10 @@ namespace foak {
 namespace {
 
 constexpr int kListCap = 512;   // listed elements of a row (or of a CTA's share of it): at least kTopKMax
+constexpr int kPushCap = 256;
 constexpr int kSelCap = 256;    // blocks they are taken from
 constexpr int kAll = 0x7fffffff;
+constexpr int kSearch = 5;      // bisections of a lane in flight
 constexpr int kThreads = 256;   // consumers
 using Sh = Shape<kThreads>;
 constexpr int kBodyAt = 8;      // place of the first body block's maximum; before it the head's and the tail's
@@ -101,6 +103,7 @@ __device__ __forceinline__ float float_of_short_key(uint32_t k) {
 // A closing warp's scratch.
 struct TopScratch {
     alignas(16) unsigned long long list[kListCap];  // (key << 32) | ~column
+    unsigned long long pushed[kPushCap];            // the cluster's lists, if they fit; written by the other CTAs
     uint16_t sel[kSelCap];                          // the chosen blocks
 };
 
@@ -499,8 +502,18 @@ __device__ __noinline__ void sort_long_list(unsigned long long* list, int n) {
     for (int q = 0; q < OWN; ++q)
         if (q * 32 + lane < n) list[r[q]] = v[q];
 }
+// Up to 32 items: each lane counts the larger ones of its own.
+__device__ __forceinline__ void sort_short_list(unsigned long long* list, int n) {
+    const int lane = threadIdx.x & 31;
+    const unsigned long long v = lane < n ? list[lane] : 0ull;
+    int r = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) r += list[j] > v;
+    __syncwarp();
+    if (lane < n) list[r] = v;
+}
 __device__ __forceinline__ void top_ordered(unsigned long long* list, int n) {
-    if (n <= 32) sort_list<1>(list, n);
+    if (n <= 32) sort_short_list(list, n);
     else if (n <= 64) sort_list<2>(list, n);
     else if (n <= 128) sort_list<4>(list, n);
     else if (n <= 256) sort_list<8>(list, n);
@@ -639,9 +652,11 @@ __global__ void __launch_bounds__(kLogprobThreads<TOPK>, TOPK ? 2 : 3) logprobs_
                 int n = 0;
                 const int K = p.top_k;
                 unsigned long long* best = top[TOPK ? me : 0].list;
+                unsigned long long* pushed = top[TOPK ? me : 0].pushed;
+                const bool push = k > 1 && K * k <= kPushCap;
                 if constexpr (TOPK) {  // this CTA's largest, in order
                     TopScratch& t = top[me];
-                    // the last row's list may still be read by the cluster's other CTAs
+                    // the last row's list may still be read by the cluster's other CTAs, and theirs written over ours
                     if (k > 1 && use > 0 && !peers_wait(bars, &bars.peers_done[buf], (use & 1u) ^ 1u, aborted ? 0 : p.src.wait_ns))
                         aborted = true;
                     move_slice<ES>(p.src, row, rank, s);
@@ -649,8 +664,16 @@ __global__ void __launch_bounds__(kLogprobThreads<TOPK>, TOPK ? 2 : 3) logprobs_
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars.row_empty[buf]);
                     top_ordered(best, n);
-                    if (k > 1)
+                    if (k > 1) {
                         for (int i = n + lane; i < K; i += 32) best[i] = 0ull;
+                        __syncwarp();
+                        if (push) {
+                            for (int i = lane; i < K * k; i += 32) {
+                                const uint32_t to = mapa_u32(pushed + rank * K + i % K, static_cast<uint32_t>(i / K));
+                                asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to), "l"(best[i % K]) : "memory");
+                            }
+                        }
+                    }
                 }
                 if (k > 1) {
                     stat_send(st, ex, buf, use, k, rank);
@@ -682,33 +705,39 @@ __global__ void __launch_bounds__(kLogprobThreads<TOPK>, TOPK ? 2 : 3) logprobs_
                         for (int i = lane; i < min(n, K); i += 32) write(i, best[i]);
                     } else {
                         // The cluster's lists, each in order and K long: an item's rank is the sum of its places in
-                        // them, one lane an item and list.  They are copied here first when there is room.
-                        unsigned long long* copies = best + kTopKMax;
-                        const bool copy = K * k <= kListCap - kTopKMax;
-                        if (copy) {
-                            for (int i = lane; i < K * k; i += 32) {
-                                const uint32_t from = mapa_u32(best, static_cast<uint32_t>(i / K)) + (i % K) * 8;
-                                asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(copies[i]) : "r"(from) : "memory");
+                        // them, one lane an item and list, by bisection in lists that are here already (pushed before
+                        // the exchange) or else in the other CTAs' memory.
+                        for (int i0 = 0; i0 < K * k; i0 += 32 * kSearch) {
+                            unsigned long long item[kSearch];
+                            int lo[kSearch], hi[kSearch];  // of list o: before lo larger, from hi on not
+#pragma unroll
+                            for (int q = 0; q < kSearch; ++q) {
+                                const int i = i0 + 32 * q + lane;
+                                item[q] = i < K * k ? best[i >> p.src.log2_k] : 0ull;
+                                lo[q] = 0;
+                                hi[q] = item[q] ? K : 0;
                             }
-                        }
-                        __syncwarp();
-                        for (int i0 = 0; i0 < K * k; i0 += 32) {
-                            const int i = i0 + lane;
-                            const int o = i & (k - 1);
-                            const unsigned long long item = i < K * k ? best[i >> p.src.log2_k] : 0ull;
-                            int a = 0, b = item ? K : 0;  // of list o: before a larger, from b on not
+                            const int o = lane & (k - 1);
                             const uint32_t remote = mapa_u32(best, static_cast<uint32_t>(o));
-                            while (a < b) {
-                                const int mid = (a + b) / 2;
-                                unsigned long long v;
-                                if (copy) v = copies[o * K + mid];
-                                else asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(remote + mid * 8) : "memory");
-                                if (v > item) a = mid + 1;
-                                else b = mid;
+                            for (int span = K; span > 0; span >>= 1) {
+#pragma unroll
+                                for (int q = 0; q < kSearch; ++q) {
+                                    if (lo[q] >= hi[q]) continue;
+                                    const int mid = (lo[q] + hi[q]) / 2;
+                                    unsigned long long v;
+                                    if (push) v = pushed[o * K + mid];
+                                    else asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(remote + mid * 8) : "memory");
+                                    if (v > item[q]) lo[q] = mid + 1;
+                                    else hi[q] = mid;
+                                }
                             }
                             __syncwarp();
-                            for (int off = 1; off < k; off <<= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
-                            if (o == 0 && item && a < K) write(a, item);
+#pragma unroll
+                            for (int q = 0; q < kSearch; ++q) {
+                                if (i0 + 32 * q >= K * k) break;
+                                for (int off = 1; off < k; off <<= 1) lo[q] += __shfl_xor_sync(0xffffffffu, lo[q], off);
+                                if (o == 0 && item[q] && lo[q] < K) write(lo[q], item[q]);
+                            }
                         }
                         __syncwarp();
                         if (lane < k) remote_arrive(&bars.peers_done[buf], static_cast<uint32_t>(lane));

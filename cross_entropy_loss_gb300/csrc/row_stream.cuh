@@ -406,16 +406,6 @@ struct RunStat {
         r = minus_product(m, x.c);
         if (TWO) r2 = minus_product(m, x.c2);
     }
-    __device__ __forceinline__ void merge(const float4& w, const ExpScale& x) {
-        RunStat o(x);
-        o.set(w, x);
-        const float mn = fmaxf(m, o.m);
-        raise(mn, x);
-        o.raise(mn, x);
-        s += o.s;
-        if (ENT) a += o.a;
-        if (TWO) s2 += o.s2;
-    }
     // One element a lane (-inf: none), by the whole warp.
     __device__ __forceinline__ void add(float v, const ExpScale& x) {
         const float mn = fmaxf(m, warp_max_redux(v));
@@ -560,9 +550,13 @@ __device__ __forceinline__ void stat_send(const RunStat<ENT, TWO>& st, StatExcha
 template <bool ENT, bool TWO>
 __device__ __forceinline__ void stat_merge(RunStat<ENT, TWO>& st, const StatExchange& ex, int buf, uint32_t use, int k,
                                            const ExpScale& x) {
-    const float4* from = ex.cta[buf][use & 1u];
-    st.set(from[0], x);
-    for (int o = 1; o < k; ++o) st.merge(from[o], x);
+    st.set(ex.cta[buf][use & 1u][threadIdx.x & (k - 1)], x);
+    st.raise(warp_max_redux(st.m), x);
+    for (int off = k / 2; off > 0; off >>= 1) {
+        st.s += __shfl_xor_sync(0xffffffffu, st.s, off);
+        if (ENT) st.a += __shfl_xor_sync(0xffffffffu, st.a, off);
+        if (TWO) st.s2 += __shfl_xor_sync(0xffffffffu, st.s2, off);
+    }
 }
 
 // Number of valid labels, counted by the consumer threads; scratch: an int a warp.
