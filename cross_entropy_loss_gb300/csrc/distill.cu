@@ -79,12 +79,15 @@ __global__ void __launch_bounds__(kDistillThreads<NT>, NT == 256 ? 2 : 1) distil
     if (tid == 0) s_bad = 0;
     griddep_launch_dependents();  // programmatic dependent launch: no global access before the wait
     griddep_wait();
+    // the producer's and closing warps' first 32 rows, the consumers' first one
+    const int64_t label0 = first_label(p.src, cid, ncl, warp < Shape<NT>::kWarps ? 0 : lane);
     __syncthreads();
-    if (k > 1) cluster_sync();  // every CTA's shared memory is there to be written to
+    if (k > 1) cluster_arrive_release();  // waited for before the cluster's memory is written to
 
     const ExpScale& sc = p.scale;
     if (warp == Shape<NT>::kWarps) {
-        stream_produce<ES, NT>(p.src, bars, smem, GRAD ? 2 : 1, cid, ncl, rank);
+        stream_produce<ES, NT>(p.src, bars, smem, GRAD ? 2 : 1, cid, ncl, rank, label0);
+        if (k > 1) cluster_wait_acquire();
     } else if (warp < Shape<NT>::kWarps) {
         float scale = 0.f;
         if (GRAD) {
@@ -99,7 +102,7 @@ __global__ void __launch_bounds__(kDistillThreads<NT>, NT == 256 ? 2 : 1) distil
         StreamPos pos{0, 0, false};
         RowPos rp;
         Slice s = slice_of<ES>(p.src, cid, rank);
-        int64_t y_next = p.src.labels && n_it > 0 ? __ldg(p.src.labels + cid) : 0;
+        int64_t y_next = label0;
         for (int64_t it = 0; it < n_it; ++it) {
             const int64_t row = cid + it * ncl;
             const int64_t y = y_next;
@@ -191,7 +194,10 @@ __global__ void __launch_bounds__(kDistillThreads<NT>, NT == 256 ? 2 : 1) distil
             }
             ++rp.n;
         }
+        __syncwarp();
+        if (k > 1) cluster_wait_acquire();
     } else {  // a closing warp
+        if (k > 1) cluster_wait_acquire();
         const uint32_t me = warp - (Shape<NT>::kWarps + 1), turn = kClosers - 1;
         TeacherRow& teach = teacher[me];
         float scale = 0.f;
@@ -208,10 +214,10 @@ __global__ void __launch_bounds__(kDistillThreads<NT>, NT == 256 ? 2 : 1) distil
         for (int64_t base = 0; base < n_it; base += 32) {
             // 32 rows' labels at once, and the logits of this warp's rows, a row a lane.  (A row's gradient is
             // not begun before its closing warp has made it ready, so the logits are still there.)
-            int64_t lab = 0;
+            int64_t lab = label0;
             bool ok = false;
             if (base + lane < n_it) {
-                if (p.src.labels) lab = __ldg(p.src.labels + cid + (base + lane) * ncl);
+                if (base > 0 && p.src.labels) lab = __ldg(p.src.labels + cid + (base + lane) * ncl);
                 ok = stream_row_valid(lab, p.src);
                 n_bad += !ok && lab != p.src.ignore_index && me == 0;
             }

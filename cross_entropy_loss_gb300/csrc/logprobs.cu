@@ -35,7 +35,6 @@ constexpr int kListCap = 512;   // listed elements of a row (or of a CTA's share
 constexpr int kPushCap = 256;
 constexpr int kSelCap = 256;    // blocks they are taken from
 constexpr int kAll = 0x7fffffff;
-constexpr int kSearch = 5;      // bisections of a lane in flight
 constexpr int kThreads = 256;   // consumers
 using Sh = Shape<kThreads>;
 constexpr int kBodyAt = 8;      // place of the first body block's maximum; before it the head's and the tail's
@@ -382,7 +381,7 @@ __device__ __noinline__ int top_list(const Slice s, const typename Block<ES>::ty
         // A 64-byte piece a lane and turn (re-read from L2); its elements at or above the threshold.
         constexpr int EPV = 16 / ES;
         const uint4* body = reinterpret_cast<const uint4*>(s.body);
-        int n = 0;
+        int n = 0, ties = 0;
         for (int i0 = 0; i0 < n_sel * B::kPieces; i0 += 32) {
             const int i = i0 + lane, j = i / B::kPieces;
             const bool there = j < n_sel;
@@ -398,14 +397,23 @@ __device__ __noinline__ int top_list(const Slice s, const typename Block<ES>::ty
             uint32_t hit = hit_bits<ES, false>(w, floor);
             if (nv < kBlockVec) hit &= nv > 0 ? first_bits<ES>(nv * EPV) : 0u;
             if (strict != kAll) {
-                // an equal one counts only if fewer than `need` come before it: those of its block, and
-                // one at least in each tied block before
+                // an equal one counts only if fewer than `need` come before it: those of its block, and all
+                // those of the tied blocks before, which are in order
                 const uint32_t tie = hit & hit_bits<ES, true>(w, floor);
-                int before = max(0, j - strict);
-                if (B::kPieces > 1) {
-                    const int o = __shfl_up_sync(0xffffffffu, __popc(tie), 1);
-                    if (i % B::kPieces) before += o;
+                const int mine = __popc(tie);
+                const bool tied = j >= strict;
+                int sum = tied ? mine : 0;
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const int o = __shfl_up_sync(0xffffffffu, sum, off);
+                    if (lane >= off) sum += o;
                 }
+                int before = tied ? ties + sum - mine : 0;
+                if (B::kPieces > 1) {
+                    const int o = __shfl_up_sync(0xffffffffu, mine, 1);
+                    if (!tied && i % B::kPieces) before = o;
+                }
+                ties += __shfl_sync(0xffffffffu, sum, 31);
                 for (int e = 0; e < 64 / ES; ++e)
                     if (tie >> bit_of_element<ES>(e) & 1u && before++ >= need) hit &= ~(1u << bit_of_element<ES>(e));
             }
@@ -542,16 +550,30 @@ __global__ void __launch_bounds__(kLogprobThreads<TOPK>, TOPK ? 2 : 3) logprobs_
     stream_init<kThreads>(bars, p.src.stages, k);
     griddep_launch_dependents();  // programmatic dependent launch: no global access before the wait
     griddep_wait();
+    // the producer's and closing warps' first 32 rows, the consumers' first one
+    const int64_t label0 = first_label(p.src, cid, ncl, warp < Sh::kWarps ? 0 : lane);
     __syncthreads();
-    if (k > 1) cluster_sync();  // every CTA's shared memory is there to be written to
+    if (k > 1) cluster_arrive_release();  // waited for before the cluster's memory is written to
 
     if (warp == Sh::kWarps) {
-        stream_produce<ES, kThreads>(p.src, bars, ring, 1, cid, ncl, rank);
+        const bool bad = stream_produce<ES, kThreads>(p.src, bars, ring, 1, cid, ncl, rank, label0);
+        // The error word: every CTA adds its labels' bit; the last one publishes and resets.
+        if (lane == 0) {
+            if (bad) atomicOr(&p.ws->err, static_cast<unsigned>(FOAK_ERRBIT_LABEL_RANGE));
+            if (atom_add_acq_rel_gpu(&p.ws->done, 1u) == gridDim.x - 1) {
+                const unsigned e = atomicExch(&p.ws->err, 0u);
+                if (p.err) *p.err = static_cast<int32_t>(e);
+                __threadfence();
+                atomicExch(&p.ws->done, 0u);
+            }
+        }
+        __syncwarp();
+        if (k > 1) cluster_wait_acquire();
     } else if (warp < Sh::kWarps) {
         StreamPos pos{0, 0, false};
         RowPos rp;
         Slice s = slice_of<ES>(p.src, cid, rank);
-        int64_t y_next = p.src.labels && n_it > 0 ? __ldg(p.src.labels + cid) : 0;
+        int64_t y_next = label0;
         for (int64_t it = 0; it < n_it; ++it) {
             const int64_t row = cid + it * ncl;
             const int64_t y = y_next;
@@ -597,20 +619,19 @@ __global__ void __launch_bounds__(kLogprobThreads<TOPK>, TOPK ? 2 : 3) logprobs_
             row_end(bars, buf);
             ++rp.n;
         }
+        __syncwarp();
+        if (k > 1) cluster_wait_acquire();
     } else if (warp - (Sh::kWarps + 1) < 1 << p.log2_closers) {  // a closing warp
         const uint32_t me = warp - (Sh::kWarps + 1), turn = (1u << p.log2_closers) - 1u;
         RowPos rp;
         Slice s = slice_of<ES>(p.src, cid, rank);
-        bool bad = false, aborted = false;
+        bool aborted = false;
+        if (k > 1) cluster_wait_acquire();
         for (int64_t base = 0; base < n_it; base += 32) {
             // 32 rows' labels at once, and the logits of this warp's rows, a row a lane
-            int64_t lab = 0;
-            bool ok = false;
-            if (base + lane < n_it) {
-                if (p.src.labels) lab = __ldg(p.src.labels + cid + (base + lane) * ncl);
-                ok = stream_row_valid(lab, p.src);
-                bad |= !ok && lab != p.src.ignore_index;
-            }
+            int64_t lab = label0;
+            if (base > 0 && p.src.labels && base + lane < n_it) lab = __ldg(p.src.labels + cid + (base + lane) * ncl);
+            const bool ok = base + lane < n_it && stream_row_valid(lab, p.src);
             const unsigned valid = __ballot_sync(0xffffffffu, ok);
             float x_lab = 0.f;
             if (p.logp && rank == 0 && ok && ((rp.n + __popc(valid & lanes_below())) & turn) == me)
@@ -668,9 +689,12 @@ __global__ void __launch_bounds__(kLogprobThreads<TOPK>, TOPK ? 2 : 3) logprobs_
                         for (int i = n + lane; i < K; i += 32) best[i] = 0ull;
                         __syncwarp();
                         if (push) {
-                            for (int i = lane; i < K * k; i += 32) {
-                                const uint32_t to = mapa_u32(pushed + rank * K + i % K, static_cast<uint32_t>(i / K));
-                                asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to), "l"(best[i % K]) : "memory");
+                            for (int i = lane; i < K; i += 32) {
+                                const unsigned long long v = best[i];
+                                for (int o = 0; o < k; ++o) {
+                                    const uint32_t to = mapa_u32(pushed + rank * K + i, static_cast<uint32_t>(o));
+                                    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to), "l"(v) : "memory");
+                                }
                             }
                         }
                     }
@@ -704,40 +728,29 @@ __global__ void __launch_bounds__(kLogprobThreads<TOPK>, TOPK ? 2 : 3) logprobs_
                     if (k == 1) {
                         for (int i = lane; i < min(n, K); i += 32) write(i, best[i]);
                     } else {
-                        // The cluster's lists, each in order and K long: an item's rank is the sum of its places in
-                        // them, one lane an item and list, by bisection in lists that are here already (pushed before
-                        // the exchange) or else in the other CTAs' memory.
-                        for (int i0 = 0; i0 < K * k; i0 += 32 * kSearch) {
-                            unsigned long long item[kSearch];
-                            int lo[kSearch], hi[kSearch];  // of list o: before lo larger, from hi on not
-#pragma unroll
-                            for (int q = 0; q < kSearch; ++q) {
-                                const int i = i0 + 32 * q + lane;
-                                item[q] = i < K * k ? best[i >> p.src.log2_k] : 0ull;
-                                lo[q] = 0;
-                                hi[q] = item[q] ? K : 0;
-                            }
-                            const int o = lane & (k - 1);
-                            const uint32_t remote = mapa_u32(best, static_cast<uint32_t>(o));
-                            for (int span = K; span > 0; span >>= 1) {
-#pragma unroll
-                                for (int q = 0; q < kSearch; ++q) {
-                                    if (lo[q] >= hi[q]) continue;
-                                    const int mid = (lo[q] + hi[q]) / 2;
-                                    unsigned long long v;
-                                    if (push) v = pushed[o * K + mid];
-                                    else asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(remote + mid * 8) : "memory");
-                                    if (v > item[q]) lo[q] = mid + 1;
-                                    else hi[q] = mid;
+                        // The rank of each of this CTA's best among the cluster's: by counting where the lists are
+                        // here (pushed before the exchange), else by bisection in the other CTAs' lists.
+                        for (int i = lane; i < K; i += 32) {
+                            const unsigned long long item = best[i];
+                            int r = 0;
+                            if (push) {
+#pragma unroll 4
+                                for (int j = 0; j < K * k; ++j) r += pushed[j] > item;
+                            } else {
+                                for (int o = 0; o < k; ++o) {
+                                    const uint32_t remote = mapa_u32(best, static_cast<uint32_t>(o));
+                                    int a = 0, b = K;  // of list o: before a larger, from b on not
+                                    while (a < b) {
+                                        const int mid = (a + b) / 2;
+                                        unsigned long long v;
+                                        asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(remote + mid * 8) : "memory");
+                                        if (v > item) a = mid + 1;
+                                        else b = mid;
+                                    }
+                                    r += a;
                                 }
                             }
-                            __syncwarp();
-#pragma unroll
-                            for (int q = 0; q < kSearch; ++q) {
-                                if (i0 + 32 * q >= K * k) break;
-                                for (int off = 1; off < k; off <<= 1) lo[q] += __shfl_xor_sync(0xffffffffu, lo[q], off);
-                                if (o == 0 && item[q] && lo[q] < K) write(lo[q], item[q]);
-                            }
+                            if (item && r < K) write(r, item);
                         }
                         __syncwarp();
                         if (lane < k) remote_arrive(&bars.peers_done[buf], static_cast<uint32_t>(lane));
@@ -754,18 +767,16 @@ __global__ void __launch_bounds__(kLogprobThreads<TOPK>, TOPK ? 2 : 3) logprobs_
             }
         }
         if (aborted) bars.abort = 1;
-        bad = __any_sync(0xffffffffu, bad);
-        if (bad && me == 0 && lane == 0) atomicOr(&p.ws->err, static_cast<unsigned>(FOAK_ERRBIT_LABEL_RANGE));
+    } else if (k > 1) {
+        cluster_wait_acquire();
     }
-    // The error word: every CTA adds its bits; the last one publishes and resets them.
     __syncthreads();
-    if (tid == Sh::kFirstCloser) {
-        if (stream_aborted(bars)) atomicOr(&p.ws->err, static_cast<unsigned>(FOAK_ERRBIT_TIMEOUT));
-        if (atom_add_acq_rel_gpu(&p.ws->done, 1u) == gridDim.x - 1) {
-            p.ws->done = 0u;  // every other CTA is past its own access
-            const unsigned e = atomicExch(&p.ws->err, 0u);
-            if (p.err) *p.err = static_cast<int32_t>(e);
+    if (tid == 0 && stream_aborted(bars) && p.err) {
+        // A wait that gave up: its bit follows the word's publication, which is waited for (with a limit).
+        const uint64_t t0 = globaltimer_ns();
+        while (*reinterpret_cast<volatile unsigned*>(&p.ws->done) != 0 && globaltimer_ns() - t0 < p.src.wait_ns) {
         }
+        atomicOr(reinterpret_cast<unsigned*>(p.err), static_cast<unsigned>(FOAK_ERRBIT_TIMEOUT));
     }
     if (k > 1) cluster_sync_converged();  // no CTA leaves while its shared memory may be read
 }

@@ -190,9 +190,11 @@ __device__ __forceinline__ bool stream_wait(StreamBars& b, uint64_t* bar, uint32
 }
 
 // The producer warp: rows cid, cid + ncl, ...; every valid row's chunks `passes` times.
+// first: the label of the lane's first row (the first 32 rows are loaded ahead).  Returns
+// whether a label was bad.
 template <int ES, int NT>
-__device__ __forceinline__ void stream_produce(const StreamSrc& p, StreamBars& bars, unsigned char* ring, int passes,
-                                               int64_t cid, int64_t ncl, int rank) {
+__device__ __forceinline__ bool stream_produce(const StreamSrc& p, StreamBars& bars, unsigned char* ring, int passes,
+                                               int64_t cid, int64_t ncl, int rank, int64_t first) {
     const int lane = threadIdx.x & 31;
     const int64_t n_it = p.N > cid ? (p.N - 1 - cid) / ncl + 1 : 0;
     const uint32_t S = static_cast<uint32_t>(p.stages);
@@ -200,14 +202,17 @@ __device__ __forceinline__ void stream_produce(const StreamSrc& p, StreamBars& b
     uint32_t st = 0, par = 0;  // the next stage, and the parity of its use
     bool wrapped = false, stop = false;
     uint32_t armed = 0;  // stages whose last copy was issued
+    bool bad = false;
     for (int64_t base = 0; base < n_it; base += 32) {
         // 32 rows' labels at once: no copy waits for a label of its own
-        int64_t lab = 0;
-        if (p.labels && base + lane < n_it) lab = __ldg(p.labels + cid + (base + lane) * ncl);
+        int64_t lab = first;
+        if (base > 0 && p.labels && base + lane < n_it) lab = __ldg(p.labels + cid + (base + lane) * ncl);
+        const bool ok = base + lane < n_it && stream_row_valid(lab, p);
+        bad |= base + lane < n_it && !ok && lab != p.ignore_index;
+        const unsigned valid = __ballot_sync(0xffffffffu, ok);
         const int nj = static_cast<int>(min(static_cast<int64_t>(32), n_it - base));
         for (int j = 0; j < nj; ++j) {
-            const int64_t y = __shfl_sync(0xffffffffu, lab, j);
-            if (!stream_row_valid(y, p)) continue;
+            if (!(valid >> j & 1u)) continue;
             const int64_t row = cid + (base + j) * ncl;
             if (lane == 0 && !stop) {
                 move_slice<ES>(p, row, rank, s);
@@ -252,7 +257,12 @@ __device__ __forceinline__ void stream_produce(const StreamSrc& p, StreamBars& b
             (void)mbar_wait_bounded(&bars.full[s], last, p.wait_ns);
         }
     }
-    __syncwarp();
+    return __any_sync(0xffffffffu, bad);
+}
+// The label of a lane's or thread's first row.
+__device__ __forceinline__ int64_t first_label(const StreamSrc& p, int64_t cid, int64_t ncl, int it) {
+    const int64_t row = cid + it * ncl;
+    return p.labels && row < p.N ? __ldg(p.labels + row) : 0;
 }
 
 // A consumer thread's place in the chunk sequence.
