@@ -102,7 +102,7 @@ __device__ __forceinline__ float float_of_short_key(uint32_t k) {
 // A closing warp's scratch.
 struct TopScratch {
     alignas(16) unsigned long long list[kListCap];  // (key << 32) | ~column
-    unsigned long long pushed[kPushCap];            // the cluster's lists, if they fit; written by the other CTAs
+    alignas(16) unsigned long long pushed[kPushCap];  // the cluster's lists, if they fit; written by the other CTAs
     uint16_t sel[kSelCap];                          // the chosen blocks
 };
 
@@ -510,13 +510,36 @@ __device__ __noinline__ void sort_long_list(unsigned long long* list, int n) {
     for (int q = 0; q < OWN; ++q)
         if (q * 32 + lane < n) list[r[q]] = v[q];
 }
+// How many of list[0, n) are larger than the item; the list is on a 16-byte boundary of
+// shared memory.  Sixteen at a time: the loads of a group go out together.
+__device__ __forceinline__ int count_larger(const unsigned long long* list, int n, unsigned long long item) {
+    const uint32_t at = smem_u32(list);
+    int r = 0, j = 0;
+    for (; j + 16 <= n; j += 16) {
+        unsigned long long v[16];
+#pragma unroll
+        for (int q = 0; q < 16; q += 2)
+            asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(v[q]), "=l"(v[q + 1]) : "r"(at + (j + q) * 8) : "memory");
+#pragma unroll
+        for (int q = 0; q < 16; ++q) r += v[q] > item;
+    }
+    if (j < n) {
+        unsigned long long v[16];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+            v[q] = 0ull;
+            if (j + q < n) asm volatile("ld.shared.u64 %0, [%1];" : "=l"(v[q]) : "r"(at + (j + q) * 8) : "memory");
+        }
+#pragma unroll
+        for (int q = 0; q < 16; ++q) r += v[q] > item;
+    }
+    return r;
+}
 // Up to 32 items: each lane counts the larger ones of its own.
 __device__ __forceinline__ void sort_short_list(unsigned long long* list, int n) {
     const int lane = threadIdx.x & 31;
     const unsigned long long v = lane < n ? list[lane] : 0ull;
-    int r = 0;
-#pragma unroll 4
-    for (int j = 0; j < n; ++j) r += list[j] > v;
+    const int r = count_larger(list, n, v);
     __syncwarp();
     if (lane < n) list[r] = v;
 }
@@ -734,8 +757,7 @@ __global__ void __launch_bounds__(kLogprobThreads<TOPK>, TOPK ? 2 : 3) logprobs_
                             const unsigned long long item = best[i];
                             int r = 0;
                             if (push) {
-#pragma unroll 4
-                                for (int j = 0; j < K * k; ++j) r += pushed[j] > item;
+                                r = count_larger(pushed, K * k, item);
                             } else {
                                 for (int o = 0; o < k; ++o) {
                                     const uint32_t remote = mapa_u32(best, static_cast<uint32_t>(o));
