@@ -555,8 +555,174 @@ __device__ __forceinline__ void top_ordered(unsigned long long* list, int n) {
 template <bool TOPK>
 constexpr int kLogprobThreads = Sh::kFirstCloser + 32 * kClosers<TOPK>;
 
+// A closing warp's rows.  Not inlined: its registers are not the consumers' concern.
 template <int ES, bool ENT, bool TOPK>
-__global__ void __launch_bounds__(kLogprobThreads<TOPK>, TOPK ? 2 : 3) logprobs_kernel(const LogprobParams p) {
+__device__ __noinline__ void close_rows(const LogprobParams& p, StreamBars& bars, StatExchange& ex, TopScratch* top,
+                                        const uint32_t (*thread_max)[kThreads], const typename Block<ES>::type* maxima,
+                                        int64_t label0) {
+    const int lane = threadIdx.x & 31, k = p.src.k;
+    const int rank = k > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int64_t cid = blockIdx.x >> p.src.log2_k, ncl = gridDim.x >> p.src.log2_k;
+    const int64_t n_it = p.src.N > cid ? (p.src.N - 1 - cid) / ncl + 1 : 0;
+    const uint32_t me = (threadIdx.x >> 5) - (Sh::kWarps + 1), turn = (1u << p.log2_closers) - 1u;
+    RowPos rp;
+    Slice s = slice_of<ES>(p.src, cid, rank);
+    bool aborted = false;
+    for (int64_t base = 0; base < n_it; base += 32) {
+        // 32 rows' labels at once, and the logits of this warp's rows, a row a lane
+        int64_t lab = label0;
+        if (base > 0 && p.src.labels && base + lane < n_it) lab = __ldg(p.src.labels + cid + (base + lane) * ncl);
+        const bool ok = base + lane < n_it && stream_row_valid(lab, p.src);
+        const unsigned valid = __ballot_sync(0xffffffffu, ok);
+        float x_lab = 0.f;
+        if (p.logp && rank == 0 && ok && ((rp.n + __popc(valid & lanes_below())) & turn) == me)
+            x_lab = load_scalar<ES>(p.src.x + ((cid + (base + lane) * ncl) * p.src.ld + lab) * ES);
+        const int nj = static_cast<int>(min(static_cast<int64_t>(32), n_it - base));
+        for (int j = 0; j < nj; ++j) {
+            const int64_t row = cid + (base + j) * ncl;
+            if (!(valid >> j & 1u)) {
+                if (rank == 0 && me == 0) {
+                    if (lane == 0) {
+                        if (p.logp) p.logp[row] = 0.f;
+                        if (p.entropy) p.entropy[row] = 0.f;
+                        if (p.lse) p.lse[row] = 0.f;
+                        if (p.stats) p.stats[row] = make_float2(0.f, 0.f);
+                    }
+                    if (TOPK) {
+                        for (int i = lane; i < p.top_k; i += 32) {
+                            p.top_lp[row * p.top_k + i] = 0.f;
+                            p.top_ids[row * p.top_k + i] = -1;
+                        }
+                    }
+                }
+                continue;
+            }
+            if ((rp.n & turn) != me) {
+                ++rp.n;
+                continue;
+            }
+            const float x_y = __shfl_sync(0xffffffffu, x_lab, j);
+            const int buf = rp.buf(p.src);
+            const uint32_t use = rp.use(p.src);
+            if (!aborted && !stream_wait(bars, &bars.row_full[buf], use & 1u, p.src.wait_ns)) aborted = true;
+            RunStat<ENT, false> st(p.scale);
+            stat_collect<kThreads>(st, ex, buf, p.scale);
+            if (!TOPK) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.row_empty[buf]);
+            }
+            int n = 0;
+            const int K = p.top_k;
+            unsigned long long* best = top[TOPK ? me : 0].list;
+            unsigned long long* pushed = top[TOPK ? me : 0].pushed;
+            const bool push = k > 1 && K * k <= kPushCap;
+            if constexpr (TOPK) {  // this CTA's largest, in order
+                TopScratch& t = top[me];
+                // the last row's list may still be read by the cluster's other CTAs, and theirs written over ours
+                if (k > 1 && use > 0 && !peers_wait(bars, &bars.peers_done[buf], (use & 1u) ^ 1u, aborted ? 0 : p.src.wait_ns))
+                    aborted = true;
+                move_slice<ES>(p.src, row, rank, s);
+                if (st.s == st.s) n = top_list<ES>(s, maxima + buf * p.max_stride, thread_max[buf], K, t);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.row_empty[buf]);
+                top_ordered(best, n);
+                if (k > 1) {
+                    for (int i = n + lane; i < K; i += 32) best[i] = 0ull;
+                    __syncwarp();
+                    if (push) {
+                        for (int i = lane; i < K; i += 32) {
+                            const unsigned long long v = best[i];
+                            for (int o = 0; o < k; ++o) {
+                                const uint32_t to = mapa_u32(pushed + rank * K + i, static_cast<uint32_t>(o));
+                                asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to), "l"(v) : "memory");
+                            }
+                        }
+                    }
+                }
+            }
+            if (k > 1) {
+                stat_send(st, ex, buf, use, k, rank);
+                if (!peers_meet(bars, buf, use, k, aborted ? 0 : p.src.wait_ns)) aborted = true;
+                stat_merge(st, ex, buf, use, k, p.scale);
+            }
+            st.correct(p.scale);
+            const float ln_s = logf(st.s);
+            const bool empty = st.s == 0.f;
+            if (lane == 0 && rank == 0 && !aborted) {
+                if (p.logp) p.logp[row] = empty ? kNegInf : (x_y - st.m) * p.inv_t - ln_s;
+                if (ENT) {
+                    const float h = ln_s - st.a * kLn2 / st.s;
+                    p.entropy[row] = empty || h < 0.f ? 0.f : h;
+                }
+                if (p.lse) p.lse[row] = empty ? kNegInf : fmaf(st.m, p.inv_t, ln_s);
+                if (p.stats) p.stats[row] = make_float2(empty ? kNegInf : st.m, ln_s);
+            }
+            if constexpr (TOPK) {
+                const bool none = !(st.s == st.s);  // a NaN or +inf in the row: no order to speak of
+                float* olp = p.top_lp + row * K;
+                int32_t* oid = p.top_ids + row * K;
+                auto write = [&](int r, unsigned long long item) {
+                    if (aborted || none) return;
+                    olp[r] = empty ? kNegInf : (float_of_key(static_cast<uint32_t>(item >> 32)) - st.m) * p.inv_t - ln_s;
+                    oid[r] = static_cast<int32_t>(~static_cast<uint32_t>(item));
+                };
+                if (k == 1) {
+                    for (int i = lane; i < min(n, K); i += 32) write(i, best[i]);
+                } else {
+                    // The rank of each of this CTA's best among the cluster's: the sum of its places in the
+                    // lists, by bisection in all of them at once where they are here (pushed before the
+                    // exchange), else in one after the other in the other CTAs' memory.
+                    for (int i = lane; i < K; i += 32) {
+                        const unsigned long long item = best[i];
+                        int r = 0;
+                        if (push) {
+                            int at[kStreamMaxCluster];  // so many of a list are larger
+#pragma unroll
+                            for (int o = 0; o < kStreamMaxCluster; ++o) at[o] = 0;
+                            for (int step = 1 << (31 - __clz(K)); step > 0; step >>= 1) {
+#pragma unroll
+                                for (int o = 0; o < kStreamMaxCluster; ++o) {
+                                    const int to = at[o] + step;
+                                    if (o < k && to <= K && pushed[o * K + to - 1] > item) at[o] = to;
+                                }
+                            }
+#pragma unroll
+                            for (int o = 0; o < kStreamMaxCluster; ++o) r += at[o];
+                        } else {
+                            for (int o = 0; o < k; ++o) {
+                                const uint32_t remote = mapa_u32(best, static_cast<uint32_t>(o));
+                                int a = 0, b = K;  // of list o: before a larger, from b on not
+                                while (a < b) {
+                                    const int mid = (a + b) / 2;
+                                    unsigned long long v;
+                                    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(remote + mid * 8) : "memory");
+                                    if (v > item) a = mid + 1;
+                                    else b = mid;
+                                }
+                                r += a;
+                            }
+                        }
+                        if (item && r < K) write(r, item);
+                    }
+                    __syncwarp();
+                    if (lane < k) remote_arrive(&bars.peers_done[buf], static_cast<uint32_t>(lane));
+                }
+                if (none && rank == 0) {
+                    for (int i = lane; i < K; i += 32) {
+                        olp[i] = st.s;
+                        oid[i] = -1;
+                    }
+                }
+                __syncwarp();
+            }
+            ++rp.n;
+        }
+    }
+    if (aborted) bars.abort = 1;
+}
+
+template <int ES, bool ENT, bool TOPK>
+__global__ void __launch_bounds__(kLogprobThreads<TOPK>, TOPK ? 2 : 3) logprobs_kernel(const __grid_constant__ LogprobParams p) {
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ StreamBars bars;
     __shared__ StatExchange ex;
@@ -644,153 +810,10 @@ __global__ void __launch_bounds__(kLogprobThreads<TOPK>, TOPK ? 2 : 3) logprobs_
         }
         __syncwarp();
         if (k > 1) cluster_wait_acquire();
-    } else if (warp - (Sh::kWarps + 1) < 1 << p.log2_closers) {  // a closing warp
-        const uint32_t me = warp - (Sh::kWarps + 1), turn = (1u << p.log2_closers) - 1u;
-        RowPos rp;
-        Slice s = slice_of<ES>(p.src, cid, rank);
-        bool aborted = false;
+    } else {
         if (k > 1) cluster_wait_acquire();
-        for (int64_t base = 0; base < n_it; base += 32) {
-            // 32 rows' labels at once, and the logits of this warp's rows, a row a lane
-            int64_t lab = label0;
-            if (base > 0 && p.src.labels && base + lane < n_it) lab = __ldg(p.src.labels + cid + (base + lane) * ncl);
-            const bool ok = base + lane < n_it && stream_row_valid(lab, p.src);
-            const unsigned valid = __ballot_sync(0xffffffffu, ok);
-            float x_lab = 0.f;
-            if (p.logp && rank == 0 && ok && ((rp.n + __popc(valid & lanes_below())) & turn) == me)
-                x_lab = load_scalar<ES>(p.src.x + ((cid + (base + lane) * ncl) * p.src.ld + lab) * ES);
-            const int nj = static_cast<int>(min(static_cast<int64_t>(32), n_it - base));
-            for (int j = 0; j < nj; ++j) {
-                const int64_t row = cid + (base + j) * ncl;
-                if (!(valid >> j & 1u)) {
-                    if (rank == 0 && me == 0) {
-                        if (lane == 0) {
-                            if (p.logp) p.logp[row] = 0.f;
-                            if (p.entropy) p.entropy[row] = 0.f;
-                            if (p.lse) p.lse[row] = 0.f;
-                            if (p.stats) p.stats[row] = make_float2(0.f, 0.f);
-                        }
-                        if (TOPK) {
-                            for (int i = lane; i < p.top_k; i += 32) {
-                                p.top_lp[row * p.top_k + i] = 0.f;
-                                p.top_ids[row * p.top_k + i] = -1;
-                            }
-                        }
-                    }
-                    continue;
-                }
-                if ((rp.n & turn) != me) {
-                    ++rp.n;
-                    continue;
-                }
-                const float x_y = __shfl_sync(0xffffffffu, x_lab, j);
-                const int buf = rp.buf(p.src);
-                const uint32_t use = rp.use(p.src);
-                if (!aborted && !stream_wait(bars, &bars.row_full[buf], use & 1u, p.src.wait_ns)) aborted = true;
-                RunStat<ENT, false> st(p.scale);
-                stat_collect<kThreads>(st, ex, buf, p.scale);
-                if (!TOPK) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars.row_empty[buf]);
-                }
-                int n = 0;
-                const int K = p.top_k;
-                unsigned long long* best = top[TOPK ? me : 0].list;
-                unsigned long long* pushed = top[TOPK ? me : 0].pushed;
-                const bool push = k > 1 && K * k <= kPushCap;
-                if constexpr (TOPK) {  // this CTA's largest, in order
-                    TopScratch& t = top[me];
-                    // the last row's list may still be read by the cluster's other CTAs, and theirs written over ours
-                    if (k > 1 && use > 0 && !peers_wait(bars, &bars.peers_done[buf], (use & 1u) ^ 1u, aborted ? 0 : p.src.wait_ns))
-                        aborted = true;
-                    move_slice<ES>(p.src, row, rank, s);
-                    if (st.s == st.s) n = top_list<ES>(s, maxima + buf * p.max_stride, thread_max[buf], K, t);
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars.row_empty[buf]);
-                    top_ordered(best, n);
-                    if (k > 1) {
-                        for (int i = n + lane; i < K; i += 32) best[i] = 0ull;
-                        __syncwarp();
-                        if (push) {
-                            for (int i = lane; i < K; i += 32) {
-                                const unsigned long long v = best[i];
-                                for (int o = 0; o < k; ++o) {
-                                    const uint32_t to = mapa_u32(pushed + rank * K + i, static_cast<uint32_t>(o));
-                                    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to), "l"(v) : "memory");
-                                }
-                            }
-                        }
-                    }
-                }
-                if (k > 1) {
-                    stat_send(st, ex, buf, use, k, rank);
-                    if (!peers_meet(bars, buf, use, k, aborted ? 0 : p.src.wait_ns)) aborted = true;
-                    stat_merge(st, ex, buf, use, k, p.scale);
-                }
-                st.correct(p.scale);
-                const float ln_s = logf(st.s);
-                const bool empty = st.s == 0.f;
-                if (lane == 0 && rank == 0 && !aborted) {
-                    if (p.logp) p.logp[row] = empty ? kNegInf : (x_y - st.m) * p.inv_t - ln_s;
-                    if (ENT) {
-                        const float h = ln_s - st.a * kLn2 / st.s;
-                        p.entropy[row] = empty || h < 0.f ? 0.f : h;
-                    }
-                    if (p.lse) p.lse[row] = empty ? kNegInf : fmaf(st.m, p.inv_t, ln_s);
-                    if (p.stats) p.stats[row] = make_float2(empty ? kNegInf : st.m, ln_s);
-                }
-                if constexpr (TOPK) {
-                    const bool none = !(st.s == st.s);  // a NaN or +inf in the row: no order to speak of
-                    float* olp = p.top_lp + row * K;
-                    int32_t* oid = p.top_ids + row * K;
-                    auto write = [&](int r, unsigned long long item) {
-                        if (aborted || none) return;
-                        olp[r] = empty ? kNegInf : (float_of_key(static_cast<uint32_t>(item >> 32)) - st.m) * p.inv_t - ln_s;
-                        oid[r] = static_cast<int32_t>(~static_cast<uint32_t>(item));
-                    };
-                    if (k == 1) {
-                        for (int i = lane; i < min(n, K); i += 32) write(i, best[i]);
-                    } else {
-                        // The rank of each of this CTA's best among the cluster's: by counting where the lists are
-                        // here (pushed before the exchange), else by bisection in the other CTAs' lists.
-                        for (int i = lane; i < K; i += 32) {
-                            const unsigned long long item = best[i];
-                            int r = 0;
-                            if (push) {
-                                r = count_larger(pushed, K * k, item);
-                            } else {
-                                for (int o = 0; o < k; ++o) {
-                                    const uint32_t remote = mapa_u32(best, static_cast<uint32_t>(o));
-                                    int a = 0, b = K;  // of list o: before a larger, from b on not
-                                    while (a < b) {
-                                        const int mid = (a + b) / 2;
-                                        unsigned long long v;
-                                        asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(remote + mid * 8) : "memory");
-                                        if (v > item) a = mid + 1;
-                                        else b = mid;
-                                    }
-                                    r += a;
-                                }
-                            }
-                            if (item && r < K) write(r, item);
-                        }
-                        __syncwarp();
-                        if (lane < k) remote_arrive(&bars.peers_done[buf], static_cast<uint32_t>(lane));
-                    }
-                    if (none && rank == 0) {
-                        for (int i = lane; i < K; i += 32) {
-                            olp[i] = st.s;
-                            oid[i] = -1;
-                        }
-                    }
-                    __syncwarp();
-                }
-                ++rp.n;
-            }
-        }
-        if (aborted) bars.abort = 1;
-    } else if (k > 1) {
-        cluster_wait_acquire();
+        if (warp - (Sh::kWarps + 1) < 1 << p.log2_closers)
+            close_rows<ES, ENT, TOPK>(p, bars, ex, top, thread_max, maxima, label0);
     }
     __syncthreads();
     if (tid == 0 && stream_aborted(bars) && p.err) {
