@@ -135,16 +135,16 @@ __global__ void __launch_bounds__(kDistillThreads<NT>, NT == 256 ? 2 : 1) distil
                 if (tid < n_edge) edge = load_scalar<ES>(s.rowp + edge_col * ES);
                 st.add(edge, sc);
             }
-            const int buf = rp.buf(p.src);
+            const int buf = rp.buf;
             stat_publish(st, ex, buf);
             row_end(bars, buf);
             if constexpr (GRAD) {
-                if (!pos.aborted && !stream_wait(bars, &bars.row_ready[buf], rp.use(p.src) & 1u, p.src.wait_ns))
+                if (!pos.aborted && !stream_wait(bars, &bars.row_ready[buf], rp.use & 1u, p.src.wait_ns))
                     pos.aborted = true;
                 SweepFactors f;
                 if (k == 1) {
                     // Every warp joins the row's sums for itself: no way to the closing warp and back.
-                    if (!pos.aborted && !stream_wait(bars, &bars.row_full[buf], rp.use(p.src) & 1u, p.src.wait_ns))
+                    if (!pos.aborted && !stream_wait(bars, &bars.row_full[buf], rp.use & 1u, p.src.wait_ns))
                         pos.aborted = true;
                     stat_collect<NT>(st, ex, buf, sc);
                     st.correct(sc);
@@ -192,13 +192,13 @@ __global__ void __launch_bounds__(kDistillThreads<NT>, NT == 256 ? 2 : 1) distil
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars.row_stored[buf]);
             }
-            ++rp.n;
+            rp.next(p.src);
         }
         __syncwarp();
         if (k > 1) cluster_wait_acquire();
     } else {  // a closing warp
         if (k > 1) cluster_wait_acquire();
-        const uint32_t me = warp - (Shape<NT>::kWarps + 1), turn = kClosers - 1;
+        const int me = warp - (Shape<NT>::kWarps + 1);  // buffer `me` is this warp's
         TeacherRow& teach = teacher[me];
         float scale = 0.f;
         if (GRAD) {
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kDistillThreads<NT>, NT == 256 ? 2 : 1) distil
             }
             const unsigned valid = __ballot_sync(0xffffffffu, ok);
             float x_lab = 0.f;
-            if (p.src.labels && ok && ((rp.n + __popc(valid & ((1u << lane) - 1u))) & turn) == me)
+            if (p.src.labels && ok && (rp.buf + __popc(valid & ((1u << lane) - 1u))) % kClosers == me)
                 x_lab = load_scalar<ES>(p.src.x + ((cid + (base + lane) * ncl) * p.src.ld + lab) * ES);
             const int nj = static_cast<int>(min(static_cast<int64_t>(32), n_it - base));
             for (int j = 0; j < nj; ++j) {
@@ -237,14 +237,14 @@ __global__ void __launch_bounds__(kDistillThreads<NT>, NT == 256 ? 2 : 1) distil
                     }
                     continue;
                 }
-                if ((rp.n & turn) != me) {
-                    ++rp.n;
+                if (rp.buf != me) {
+                    rp.next(p.src);
                     continue;
                 }
                 const int64_t y = p.src.labels ? __shfl_sync(0xffffffffu, lab, j) : -1;
                 const float x_y = __shfl_sync(0xffffffffu, x_lab, j);
-                const int buf = rp.buf(p.src);
-                const uint32_t use = rp.use(p.src);
+                const int buf = rp.buf;
+                const uint32_t use = rp.use;
                 move_slice<ES>(p.src, row, rank, s);
                 const int64_t col_lo = rank == 0 ? 0 : s.col0;
                 const int64_t col_hi = rank == k - 1 ? p.src.V : s.col0 + static_cast<int64_t>(s.nv) * EPV;
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kDistillThreads<NT>, NT == 256 ? 2 : 1) distil
                     }
                 }
                 __syncwarp();
-                ++rp.n;
+                rp.next(p.src);
             }
         }
         n_bad = __reduce_add_sync(0xffffffffu, n_bad);
@@ -328,7 +328,7 @@ cudaError_t launch_typed(DistillParams prm, int per_sm, cudaStream_t stream) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     StreamSrc& s = prm.src;
-    s.log2_buffers = 1;
+    s.buffers = kClosers;
     const size_t fixed = 1024 + 512 + sizeof(StreamBars) + sizeof(StatExchange) + kClosers * sizeof(TeacherRow);
     const size_t room = std::min<size_t>((228 * 1024) / per_sm, 227 * 1024) - fixed;
     s.stages = static_cast<int>(std::min<size_t>(kStreamMaxStages, room / Shape<NT>::kStageBytes));

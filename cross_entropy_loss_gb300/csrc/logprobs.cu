@@ -31,17 +31,17 @@ namespace foak {
 
 namespace {
 
-constexpr int kListCap = 512;   // listed elements of a row (or of a CTA's share of it): at least kTopKMax
-constexpr int kPushCap = 256;
+constexpr int kListCap = 384;   // listed elements of a row (or of a CTA's share of it): at least kTopKMax
+constexpr int kPushCap = 256;   // the cluster's lists, where they are pushed into every CTA
 constexpr int kSelCap = 256;    // blocks they are taken from
 constexpr int kAll = 0x7fffffff;
 constexpr int kThreads = 256;   // consumers
 using Sh = Shape<kThreads>;
 constexpr int kBodyAt = 8;      // place of the first body block's maximum; before it the head's and the tail's
 // Closing warps of a CTA.  The work on a row's top tokens is a chain of some 6000 cycles
-// (K = 20), so four take rows in turn; without top tokens one keeps up.
+// (K = 20), so three take rows in turn; without top tokens one keeps up.
 template <bool TOPK>
-constexpr int kClosers = TOPK ? 4 : 1;
+constexpr int kClosers = TOPK ? 3 : 1;
 
 struct LogprobParams {
     StreamSrc src;
@@ -49,7 +49,7 @@ struct LogprobParams {
     ExpScale scale;
     int top_k;
     int max_stride;    // places of a row's block maxima in shared memory
-    int log2_closers;  // closing warps at work
+    int max_bytes;     // of all buffers'; a shared row's lists follow
     float* logp;       // [N] or null
     float* entropy;    // [N] or null
     float* lse;        // [N] or null
@@ -102,7 +102,6 @@ __device__ __forceinline__ float float_of_short_key(uint32_t k) {
 // A closing warp's scratch.
 struct TopScratch {
     alignas(16) unsigned long long list[kListCap];  // (key << 32) | ~column
-    alignas(16) unsigned long long pushed[kPushCap];  // the cluster's lists, if they fit; written by the other CTAs
     uint16_t sel[kSelCap];                          // the chosen blocks
 };
 
@@ -559,12 +558,12 @@ constexpr int kLogprobThreads = Sh::kFirstCloser + 32 * kClosers<TOPK>;
 template <int ES, bool ENT, bool TOPK>
 __device__ __noinline__ void close_rows(const LogprobParams& p, StreamBars& bars, StatExchange& ex, TopScratch* top,
                                         const uint32_t (*thread_max)[kThreads], const typename Block<ES>::type* maxima,
-                                        int64_t label0) {
+                                        unsigned char* smem_pushed, int64_t label0) {
     const int lane = threadIdx.x & 31, k = p.src.k;
     const int rank = k > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int64_t cid = blockIdx.x >> p.src.log2_k, ncl = gridDim.x >> p.src.log2_k;
     const int64_t n_it = p.src.N > cid ? (p.src.N - 1 - cid) / ncl + 1 : 0;
-    const uint32_t me = (threadIdx.x >> 5) - (Sh::kWarps + 1), turn = (1u << p.log2_closers) - 1u;
+    const int me = (threadIdx.x >> 5) - (Sh::kWarps + 1);  // with several closing warps, buffer `me` is this one's
     RowPos rp;
     Slice s = slice_of<ES>(p.src, cid, rank);
     bool aborted = false;
@@ -575,7 +574,7 @@ __device__ __noinline__ void close_rows(const LogprobParams& p, StreamBars& bars
         const bool ok = base + lane < n_it && stream_row_valid(lab, p.src);
         const unsigned valid = __ballot_sync(0xffffffffu, ok);
         float x_lab = 0.f;
-        if (p.logp && rank == 0 && ok && ((rp.n + __popc(valid & lanes_below())) & turn) == me)
+        if (p.logp && rank == 0 && ok && (!TOPK || (rp.buf + __popc(valid & lanes_below())) % p.src.buffers == me))
             x_lab = load_scalar<ES>(p.src.x + ((cid + (base + lane) * ncl) * p.src.ld + lab) * ES);
         const int nj = static_cast<int>(min(static_cast<int64_t>(32), n_it - base));
         for (int j = 0; j < nj; ++j) {
@@ -597,13 +596,13 @@ __device__ __noinline__ void close_rows(const LogprobParams& p, StreamBars& bars
                 }
                 continue;
             }
-            if ((rp.n & turn) != me) {
-                ++rp.n;
+            if (TOPK && rp.buf != me) {
+                rp.next(p.src);
                 continue;
             }
             const float x_y = __shfl_sync(0xffffffffu, x_lab, j);
-            const int buf = rp.buf(p.src);
-            const uint32_t use = rp.use(p.src);
+            const int buf = rp.buf;
+            const uint32_t use = rp.use;
             if (!aborted && !stream_wait(bars, &bars.row_full[buf], use & 1u, p.src.wait_ns)) aborted = true;
             RunStat<ENT, false> st(p.scale);
             stat_collect<kThreads>(st, ex, buf, p.scale);
@@ -614,7 +613,7 @@ __device__ __noinline__ void close_rows(const LogprobParams& p, StreamBars& bars
             int n = 0;
             const int K = p.top_k;
             unsigned long long* best = top[TOPK ? me : 0].list;
-            unsigned long long* pushed = top[TOPK ? me : 0].pushed;
+            unsigned long long* pushed = reinterpret_cast<unsigned long long*>(smem_pushed) + (TOPK ? me : 0) * kPushCap;
             const bool push = k > 1 && K * k <= kPushCap;
             if constexpr (TOPK) {  // this CTA's largest, in order
                 TopScratch& t = top[me];
@@ -715,19 +714,19 @@ __device__ __noinline__ void close_rows(const LogprobParams& p, StreamBars& bars
                 }
                 __syncwarp();
             }
-            ++rp.n;
+            rp.next(p.src);
         }
     }
     if (aborted) bars.abort = 1;
 }
 
 template <int ES, bool ENT, bool TOPK>
-__global__ void __launch_bounds__(kLogprobThreads<TOPK>, TOPK ? 2 : 3) logprobs_kernel(const __grid_constant__ LogprobParams p) {
+__global__ void __launch_bounds__(kLogprobThreads<TOPK>, 3) logprobs_kernel(const __grid_constant__ LogprobParams p) {
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ StreamBars bars;
     __shared__ StatExchange ex;
     __shared__ TopScratch top[TOPK ? kClosers<TOPK> : 1];
-    __shared__ uint32_t thread_max[TOPK ? kMaxBuffers : 1][kThreads];  // key of the largest of a thread's blocks, 0: it has none
+    __shared__ uint32_t thread_max[TOPK ? kClosers<TOPK> : 1][kThreads];  // key of the largest of a thread's blocks, 0: it has none
     using MaxT = typename Block<ES>::type;
     unsigned char* ring = smem;
     MaxT* maxima = reinterpret_cast<MaxT*>(smem + p.src.stages * Sh::kStageBytes);  // of the blocks, max_stride a buffer
@@ -770,7 +769,7 @@ __global__ void __launch_bounds__(kLogprobThreads<TOPK>, TOPK ? 2 : 3) logprobs_
             if (!stream_row_valid(y, p.src)) continue;
             move_slice<ES>(p.src, row, rank, s);
             row_begin(p.src, bars, rp, pos);
-            const int buf = rp.buf(p.src);
+            const int buf = rp.buf;
             MaxT* rm = maxima + buf * p.max_stride;
             RunStat<ENT, false> st(p.scale);
             float most = kNegInf;  // of the thread's blocks
@@ -806,14 +805,15 @@ __global__ void __launch_bounds__(kLogprobThreads<TOPK>, TOPK ? 2 : 3) logprobs_
             if (TOPK) thread_max[buf][tid] = tid * kBlockVec < s.nv ? short_key<ES>(most) : 0u;
             stat_publish(st, ex, buf);
             row_end(bars, buf);
-            ++rp.n;
+            rp.next(p.src);
         }
         __syncwarp();
         if (k > 1) cluster_wait_acquire();
     } else {
         if (k > 1) cluster_wait_acquire();
-        if (warp - (Sh::kWarps + 1) < 1 << p.log2_closers)
-            close_rows<ES, ENT, TOPK>(p, bars, ex, top, thread_max, maxima, label0);
+        if (!TOPK || warp - (Sh::kWarps + 1) < p.src.buffers)
+            close_rows<ES, ENT, TOPK>(p, bars, ex, top, thread_max, maxima,
+                                      smem + p.src.stages * Sh::kStageBytes + p.max_bytes, label0);
     }
     __syncthreads();
     if (tid == 0 && stream_aborted(bars) && p.err) {
@@ -846,21 +846,27 @@ cudaError_t launch_typed(LogprobParams prm, cudaStream_t stream) {
     const int64_t nblk = (((nb + kBlockVec - 1) / kBlockVec + s.k - 1) / s.k + 1) / Block<ES>::kPieces + 1;
     prm.max_stride = static_cast<int>((kBodyAt + nblk + 63) / 64 * 64);
     const size_t buffer = TOPK ? prm.max_stride * sizeof(typename Block<ES>::type) : 0;
-    // A buffer for each closing warp, fewer where the keys are large; CTAs an SM as the
-    // registers allow, fewer where a ring of two stages would not fit.
-    const size_t fixed = 1024 + 256 + sizeof(StreamBars) + sizeof(StatExchange) +
-                         (TOPK ? kClosers<TOPK> * sizeof(TopScratch) + kMaxBuffers * kThreads * 4 : 0);
-    int per_sm = TOPK ? 2 : 3;
-    s.log2_buffers = TOPK ? 2 : 1;
-    auto room_for = [&] { return std::min<int64_t>(228 * 1024 / per_sm, 227 * 1024) - static_cast<int64_t>(fixed + (buffer << s.log2_buffers)); };
-    while (s.log2_buffers > 1 && room_for() < 2 * static_cast<int64_t>(Sh::kStageBytes)) --s.log2_buffers;
-    while (per_sm > 1 && room_for() < 2 * static_cast<int64_t>(Sh::kStageBytes)) --per_sm;
-    prm.log2_closers = TOPK ? s.log2_buffers : 0;
+    // As many CTAs an SM as the registers allow, and a buffer for each closing warp, or fewer
+    // of the first, then of the second, where a ring of two stages would not fit.
+    const size_t lists = TOPK && s.k > 1 ? kClosers<TOPK> * kPushCap * 8 : 0;
+    const size_t fixed = 1024 + 256 + sizeof(StreamBars) + sizeof(StatExchange) + lists +
+                         (TOPK ? kClosers<TOPK> * (sizeof(TopScratch) + kThreads * 4) : 0);
+    int per_sm = 3;
+    s.buffers = TOPK ? kClosers<TOPK> : 2;
+    auto room_for = [&] { return std::min<int64_t>(228 * 1024 / per_sm, 227 * 1024) - static_cast<int64_t>(fixed + buffer * s.buffers); };
+    while (room_for() < 2 * static_cast<int64_t>(Sh::kStageBytes) && (per_sm > 1 || s.buffers > 2)) {
+        if (per_sm > 1) {
+            --per_sm;
+        } else {
+            per_sm = 3;
+            --s.buffers;
+        }
+    }
     const int64_t room = room_for();
     if (room < static_cast<int64_t>(Sh::kStageBytes)) return cudaErrorInvalidValue;
-    const size_t key_bytes = buffer << s.log2_buffers;
     s.stages = static_cast<int>(std::min<size_t>(kStreamMaxStages, room / Sh::kStageBytes));
-    const size_t smem = static_cast<size_t>(s.stages) * Sh::kStageBytes + key_bytes;
+    prm.max_bytes = static_cast<int>(buffer * s.buffers);
+    const size_t smem = static_cast<size_t>(s.stages) * Sh::kStageBytes + prm.max_bytes + lists;
     {
         std::lock_guard<std::mutex> lock(g_lp_mu);
         size_t& set = g_lp_attr[std::make_pair(dev, reinterpret_cast<const void*>(kern))];

@@ -54,7 +54,7 @@ struct StreamSrc {
     uint64_t wait_ns;       // limit of every shared-memory barrier wait
     int64_t skip_load_row;  // test hook: this row's first chunk is never loaded (-1: none)
     int k, log2_k;          // CTAs of a row's cluster
-    int log2_buffers;
+    int buffers;            // rows between the consumers and the closing warps
     bool evict_last_pass;
     int stages;
 };
@@ -285,16 +285,22 @@ __device__ __forceinline__ void stream_chunk(const StreamSrc& p, StreamBars& bar
     }
 }
 
-// A row's place in the exchange between the consumers and the closing warps.
+// A valid row's place in the exchange between the consumers and the closing warps.
 struct RowPos {
-    uint32_t n = 0;  // valid rows so far
-    __device__ __forceinline__ int buf(const StreamSrc& p) const { return n & ((1u << p.log2_buffers) - 1u); }
-    __device__ __forceinline__ uint32_t use(const StreamSrc& p) const { return n >> p.log2_buffers; }  // of the buffer
+    uint32_t n = 0;    // valid rows so far
+    int buf = 0;       // the buffer
+    uint32_t use = 0;  // and which use of it
+    __device__ __forceinline__ void next(const StreamSrc& p) {
+        ++n;
+        if (++buf == p.buffers) {
+            buf = 0;
+            ++use;
+        }
+    }
 };
 // Consumers, before they write into the row's buffer: its last use is taken.
 __device__ __forceinline__ void row_begin(const StreamSrc& p, StreamBars& bars, const RowPos& row, StreamPos& pos) {
-    const uint32_t use = row.use(p);
-    if (use > 0 && !pos.aborted && !stream_wait(bars, &bars.row_empty[row.buf(p)], (use & 1u) ^ 1u, p.wait_ns))
+    if (row.use > 0 && !pos.aborted && !stream_wait(bars, &bars.row_empty[row.buf], (row.use & 1u) ^ 1u, p.wait_ns))
         pos.aborted = true;
 }
 // Consumers: the warp's part of the row is written.
