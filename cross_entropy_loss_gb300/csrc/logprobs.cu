@@ -838,10 +838,11 @@ cudaError_t launch_typed(LogprobParams prm, cudaStream_t stream) {
     StreamSrc& s = prm.src;
     const int sms = device_sm_count();
     const int64_t nb = s.V * ES / 16 + 1;
-    // Few rows: a cluster per row, as long as its CTAs are all on SMs of their own and
-    // have at least half a chunk each.
-    int k = kStreamMaxCluster;
-    while (k > 1 && (s.N * k > sms || 2 * nb < static_cast<int64_t>(k) * Sh::kChunk)) k /= 2;
+    // Two CTAs an SM and slices of 30000 elements for top tokens, whose lists cost a cluster more:
+    // with K = 20 rows of 128256 bf16 by 1, 2, 4 and 8 took 19.6, 18.1, 14.5, 14.4 us (1 row),
+    // 20.3, 18.9, 15.3, 16.8 (16), 21.8, 23.4, 20.5, 34.9 (64) and 27.3, 26.6, 35.5, 41.5 (130);
+    // without 10.5, 8.3, 6.6, 5.8 (1), 11.7, 11.5, 10.2, 13.8 (64), 16.6, 14.8, 16.9, 20.1 (130).
+    const int k = cluster_size(s, ES, TOPK ? 30000 : 8 * 1024, 2 * sms);
     set_cluster(s, k);
     const int64_t nblk = (((nb + kBlockVec - 1) / kBlockVec + s.k - 1) / s.k + 1) / Block<ES>::kPieces + 1;
     prm.max_stride = static_cast<int>((kBodyAt + nblk + 63) / 64 * 64);

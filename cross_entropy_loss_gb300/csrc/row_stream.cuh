@@ -95,6 +95,19 @@ inline void set_cluster(StreamSrc& p, int k) {
     for (p.log2_k = 0; (1 << p.log2_k) < k;) ++p.log2_k;
 }
 
+// How many CTAs share a row: all eight while the rows are few, for a cluster reads its row as
+// much faster, and one where there are rows for every SM.  A row of less than kWholeRowBytes
+// stays whole, as the exchange costs what the shorter read gains (1 x 32000 bf16: 5.1 us whole,
+// 5.4 by two, 5.2 by four or eight; 1 x 128256: 10.5, 8.3, 6.6 and 5.8), and so does a slice of
+// less than `least` elements.  `at_most` CTAs run at a time without waiting for one another.
+constexpr int64_t kWholeRowBytes = 96 * 1024;
+inline int cluster_size(const StreamSrc& p, int es, int64_t least, int64_t at_most) {
+    if (p.V * es < kWholeRowBytes) return 1;
+    int k = kStreamMaxCluster;
+    while (k > 1 && (p.N * k > at_most || p.V < k * least)) k /= 2;
+    return k;
+}
+
 __device__ __forceinline__ bool stream_row_valid(int64_t y, const StreamSrc& p) {
     return !p.labels || (y != p.ignore_index && y >= 0 && y < p.V);
 }

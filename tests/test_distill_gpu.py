@@ -68,7 +68,7 @@ def _check(ce, x, y, ids, t, T=1.0, ce_w=0.0, kd_w=1.0, normalize=True, g=1.0, d
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("N,V,K", [(1, 1, 1), (3, 2, 2), (5, 7, 3), (4, 31, 31), (9, 1000, 64), (6, 8192, 20),
                                    (5, 32000, 256), (3, 50257, 100), (1, 128256, 20), (40, 32000, 20), (90, 50257, 7),
-                                   (400, 9001, 50), (170, 128263, 30)])
+                                   (400, 9001, 50), (170, 128263, 30), (30, 128256, 50), (60, 128263, 30)])
 @pytest.mark.parametrize("T,ce_w,normalize", [(1.0, 0.0, True), (1.0, 0.4, False), (2.0, 0.5, True), (0.5, 0.0, False)])
 def test_shapes(cuda_lib, dtype, N, V, K, T, ce_w, normalize):
     x = ref.make_logits(N, V, dtype, seed=N + V)
@@ -78,7 +78,7 @@ def test_shapes(cuda_lib, dtype, N, V, K, T, ce_w, normalize):
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("ld_more,offset", [(0, 1), (1, 0), (3, 5), (13, 7)])
-@pytest.mark.parametrize("N,V", [(7, 5003), (300, 1031), (2, 100001)])
+@pytest.mark.parametrize("N,V", [(7, 5003), (300, 1031), (2, 100001), (30, 100001)])
 def test_strides_and_offsets(cuda_lib, dtype, ld_more, offset, N, V):
     x = ref.make_logits(N, V, dtype, seed=V + offset, ld=V + ld_more, offset=offset)
     ids, t = _teacher(x, 12, 1.5, V)
@@ -98,10 +98,10 @@ def test_strides_and_offsets(cuda_lib, dtype, ld_more, offset, N, V):
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("normalize", [True, False])
-@pytest.mark.parametrize("N", [3, 200])
-def test_padding_repeats_and_the_label(cuda_lib, dtype, normalize, N):
+@pytest.mark.parametrize("N,V", [(3, 4099), (200, 4099), (10, 100003)])
+def test_padding_repeats_and_the_label(cuda_lib, dtype, normalize, N, V):
     """Padded entries, rows without any entry, -inf entries, repeated tokens, the label among them."""
-    V, K = 4099, 9
+    K = 9
     x = ref.make_logits(N, V, dtype, seed=6)
     ids, t = _teacher(x, K, 1.0, 6)
     y = _labels(N, V, 6)
@@ -133,9 +133,8 @@ def test_teacher_logits_instead_of_log_probabilities(cuda_lib):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("N", [6, 200])
-def test_masks(cuda_lib, dtype, N):
-    V = 32003
+@pytest.mark.parametrize("N,V", [(6, 32003), (200, 32003), (12, 128259)])
+def test_masks(cuda_lib, dtype, N, V):
     low = torch.finfo(dtype).min
     x = ref.make_logits(N, V, dtype, seed=11)
     ids, t = _teacher(x, 10, 1.0, 11)
@@ -157,8 +156,8 @@ def test_masks(cuda_lib, dtype, N):
     _check(cuda_lib, x, y, ids, t, 1.0, 0.0, 1.0)
 
 
-def test_impossible_targets_give_an_infinite_loss_and_finite_gradients(cuda_lib):
-    V = 1000
+@pytest.mark.parametrize("V", [1000, 70001])
+def test_impossible_targets_give_an_infinite_loss_and_finite_gradients(cuda_lib, V):
     x = ref.make_logits(4, V, F32, seed=12)
     ids, t = _teacher(x, 5, 1.0, 12)
     x[1, ids[1, 2].long()] = -math.inf  # a listed token masked

@@ -65,7 +65,8 @@ def _check_backward(ce, x, xd, y, out, want, T, seed=0, entropy=True, in_place=F
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("N,V,K", [(1, 1, 1), (3, 2, 2), (5, 7, 3), (4, 31, 31), (2, 33, 20), (9, 1000, 64),
                                    (6, 8192, 20), (5, 32000, 5), (3, 50257, 128), (2, 128256, 20), (1, 128256, 256),
-                                   (40, 32000, 20), (90, 50257, 7), (400, 9001, 50), (1000, 2055, 8)])
+                                   (40, 32000, 20), (90, 50257, 7), (400, 9001, 50), (1000, 2055, 8),
+                                   (2, 128256, 100), (64, 128263, 20), (130, 128256, 200), (20, 64131, 3)])
 def test_shapes(cuda_lib, dtype, N, V, K):
     x = ref.make_logits(N, V, dtype, seed=N + V)
     y = _labels(N, V, N + V, n_ignore=N // 7)
@@ -76,7 +77,7 @@ def test_shapes(cuda_lib, dtype, N, V, K):
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("ld_more,offset", [(0, 1), (1, 0), (3, 5), (8, 0), (13, 7)])
-@pytest.mark.parametrize("N,V", [(7, 5003), (300, 1031), (2, 100001)])
+@pytest.mark.parametrize("N,V", [(7, 5003), (300, 1031), (2, 100001), (2, 128263)])
 def test_strides_and_offsets(cuda_lib, dtype, ld_more, offset, N, V):
     x = ref.make_logits(N, V, dtype, seed=V + offset, ld=V + ld_more, offset=offset)
     y = _labels(N, V, V, n_ignore=1)
@@ -85,7 +86,7 @@ def test_strides_and_offsets(cuda_lib, dtype, ld_more, offset, N, V):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("N,V", [(12, 32003), (200, 32003), (1, 128256)])
+@pytest.mark.parametrize("N,V", [(12, 32003), (200, 32003), (1, 128256), (12, 128259), (64, 128256)])
 def test_masks(cuda_lib, dtype, N, V):
     """Rows with -inf, the lowest value, one token left, nothing left; mixtures of both masks."""
     low = torch.finfo(dtype).min
@@ -126,7 +127,8 @@ def test_masks(cuda_lib, dtype, N, V):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("N,V,K", [(3, 32000, 20), (200, 32001, 128), (1, 128256, 50), (2, 700, 256), (160, 12000, 256)])
+@pytest.mark.parametrize("N,V,K", [(3, 32000, 20), (200, 32001, 128), (1, 128256, 50), (2, 700, 256), (160, 12000, 256),
+                                   (3, 128256, 200), (100, 128256, 20)])
 def test_ties_go_to_the_lowest_id(cuda_lib, dtype, N, V, K):
     r = np.random.default_rng(V)
     x = torch.empty(N, V, dtype=dtype)
@@ -146,9 +148,9 @@ def test_ties_go_to_the_lowest_id(cuda_lib, dtype, N, V, K):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-def test_magnitudes(cuda_lib, dtype):
+@pytest.mark.parametrize("V", [20011, 100003])
+def test_magnitudes(cuda_lib, dtype, V):
     """Very large, very small and very spread logits; an outlier far above the rest."""
-    V = 20011
     x = torch.empty(6, V, dtype=dtype)
     base = ref.make_logits(6, V, F32, seed=5)
     x[0] = base[0] * 1e-30
@@ -164,9 +166,8 @@ def test_magnitudes(cuda_lib, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("N", [4, 300])
-def test_nan_and_infinity_stay_in_their_row(cuda_lib, dtype, N):
-    V = 33000
+@pytest.mark.parametrize("N,V", [(4, 33000), (300, 33000), (4, 128256)])
+def test_nan_and_infinity_stay_in_their_row(cuda_lib, dtype, N, V):
     x = ref.make_logits(N, V, dtype, seed=2)
     y = _labels(N, V, 2)
     x[1, 20000] = math.nan
