@@ -176,9 +176,11 @@ __device__ __noinline__ int top_list_exact(const Slice s, const typename Block<E
     if (nreal > K) {
         uint32_t hi = 0xffffffffu;   // above every key
         int c_lo = nreal, c_hi = 0;  // blocks at or above lo and hi
+#pragma unroll 1
         while (hi - lo > 1 && c_lo > kSelCap) {
             const uint32_t mid = lo + (hi - lo) / 2;
             int n = 0;
+#pragma unroll 1
             for (int b = lane; b < nblk + 2; b += 32) n += key(b) >= mid;
             n = __reduce_add_sync(0xffffffffu, n);
             if (n >= K) {
@@ -192,9 +194,11 @@ __device__ __noinline__ int top_list_exact(const Slice s, const typename Block<E
         if (c_lo > kSelCap) {  // hi == lo + 1: ties at lo, the first `need` of them
             const int need = K - c_hi;
             int j0 = -1, j1 = nblk + 1;  // fewer than need ties up to j0, enough up to j1
+#pragma unroll 1
             while (j1 - j0 > 1) {
                 const int mid = j0 + (j1 - j0) / 2;
                 int n = 0;
+#pragma unroll 1
                 for (int b = lane; b <= mid; b += 32) n += key(b) == lo;
                 if (__reduce_add_sync(0xffffffffu, n) >= need) j1 = mid;
                 else j0 = mid;
@@ -203,6 +207,7 @@ __device__ __noinline__ int top_list_exact(const Slice s, const typename Block<E
         }
     }
     int n_sel = 0;
+#pragma unroll 1
     for (int b0 = 0; b0 < nblk + 2; b0 += 32) {
         const int b = b0 + lane;
         const uint32_t k = b < nblk + 2 ? key(b) : 0;
@@ -216,6 +221,7 @@ __device__ __noinline__ int top_list_exact(const Slice s, const typename Block<E
     __syncwarp();
     // ---- their elements: a block a lane and turn, read again for every count
     auto for_each = [&](auto&& f) {
+#pragma unroll 1
         for (int i0 = 0; i0 < n_sel; i0 += 32) {
             BlockElements<ES> el;
             el.n = 0;
@@ -233,6 +239,7 @@ __device__ __noinline__ int top_list_exact(const Slice s, const typename Block<E
     // every count is at least K at b0 (or takes every element) and less than K at b1
     unsigned long long b0 = static_cast<unsigned long long>(lo) << 32, b1 = ~0ull;
     if (at_least(b0) > kListCap) {
+#pragma unroll 1
         while (b1 - b0 > 1) {
             const unsigned long long mid = b0 + (b1 - b0) / 2;
             const int c = at_least(mid);
@@ -317,6 +324,7 @@ __device__ __noinline__ int top_list(const Slice s, const typename Block<ES>::ty
         uint32_t lo = __reduce_min_sync(0xffffffffu, least) + 1u;
         hi = __reduce_max_sync(0xffffffffu, hi) + 1u;
         const int most = K + K / 8 + 4;
+#pragma unroll 1
         while (hi - lo > 1) {
             const uint32_t mid = lo + (hi - lo) / 2;
             int n = 0;
@@ -337,6 +345,7 @@ __device__ __noinline__ int top_list(const Slice s, const typename Block<ES>::ty
         constexpr int PACK = 16 / sizeof(typename B::type);
         const uint4* mv = reinterpret_cast<const uint4*>(maxima + kBodyAt);
         int n = 0;
+#pragma unroll 1
         for (int b0 = 0; b0 < nblk && n <= kSelCap; b0 += 32 * PACK) {
             const int b = b0 + lane * PACK;
             uint32_t hit = 0;
@@ -347,6 +356,7 @@ __device__ __noinline__ int top_list(const Slice s, const typename Block<ES>::ty
                 if (above) hit &= ~hit_bits<ES, true>(w, floor);
                 if (nblk - b < PACK) hit &= first_bits<ES>(nblk - b);
             }
+#pragma unroll 1
             for (unsigned m = __ballot_sync(0xffffffffu, hit != 0); m; m = __ballot_sync(0xffffffffu, hit != 0)) {
                 const int at = n + __popc(m & lanes_below());
                 if (hit && at < kSelCap) t.sel[at] = static_cast<uint16_t>(1 + b + element_of_bit<ES>(__ffs(hit) - 1));
@@ -365,6 +375,7 @@ __device__ __noinline__ int top_list(const Slice s, const typename Block<ES>::ty
         if (strict < K) {
             need = K - strict;
             int have = 0;
+#pragma unroll 1
             for (int b0 = 0; b0 < nblk && have < need; b0 += 32) {
                 const bool tie = b0 + lane < nblk && B::value(maxima[kBodyAt + b0 + lane]) == floor;
                 const unsigned m = __ballot_sync(0xffffffffu, tie);
@@ -381,6 +392,7 @@ __device__ __noinline__ int top_list(const Slice s, const typename Block<ES>::ty
         constexpr int EPV = 16 / ES;
         const uint4* body = reinterpret_cast<const uint4*>(s.body);
         int n = 0, ties = 0;
+#pragma unroll 1
         for (int i0 = 0; i0 < n_sel * B::kPieces; i0 += 32) {
             const int i = i0 + lane, j = i / B::kPieces;
             const bool there = j < n_sel;
@@ -413,6 +425,7 @@ __device__ __noinline__ int top_list(const Slice s, const typename Block<ES>::ty
                     if (!tied && i % B::kPieces) before = o;
                 }
                 ties += __shfl_sync(0xffffffffu, sum, 31);
+#pragma unroll 1
                 for (int e = 0; e < 64 / ES; ++e)
                     if (tie >> bit_of_element<ES>(e) & 1u && before++ >= need) hit &= ~(1u << bit_of_element<ES>(e));
             }
@@ -425,6 +438,7 @@ __device__ __noinline__ int top_list(const Slice s, const typename Block<ES>::ty
             const int end = n + __shfl_sync(0xffffffffu, at, 31);
             at += n - __popc(hit);
             n = end;
+#pragma unroll 1
             for (; hit; hit &= hit - 1, ++at) {
                 const int e = element_of_bit<ES>(__ffs(hit) - 1);
                 const int64_t col = s.col0 + static_cast<int64_t>(vec) * EPV + e;
@@ -458,29 +472,28 @@ __device__ __noinline__ void sort_list(unsigned long long* list, int n) {
     unsigned long long v[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) v[r] = r * 32 + lane < n ? list[r * 32 + lane] : 0ull;  // any order will do
-#pragma unroll
+#pragma unroll 1
     for (int size = 2; size <= 32 * R; size *= 2) {
+#pragma unroll 1
+        for (int d = size / (2 * R); d > 0; d /= 2) {  // strides of whole lanes
+            const bool larger = ((lane & d) == 0) == ((lane * R & size) == 0 || size == 32 * R);
 #pragma unroll
-        for (int stride = size / 2; stride > 0; stride /= 2) {
-            if (stride >= R) {
-                const int d = stride / R;
-                const bool lower = (lane & d) == 0;
-                const bool down = size >= 32 * R || ((lane * R) & size) == 0;  // this run descends
+            for (int r = 0; r < R; ++r) {
+                const unsigned long long o = __shfl_xor_sync(0xffffffffu, v[r], d);
+                v[r] = larger == (o > v[r]) ? o : v[r];
+            }
+        }
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const unsigned long long o = __shfl_xor_sync(0xffffffffu, v[r], d);
-                    v[r] = (lower == down) == (o > v[r]) ? o : v[r];
-                }
-            } else {
+        for (int stride = R / 2; stride > 0; stride /= 2) {  // and inside a lane
+            if (stride >= size) continue;
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    if (r & stride) continue;
-                    const bool down = size >= 32 * R || ((lane * R + r) & size) == 0;
-                    const unsigned long long a = v[r], b = v[r + stride];
-                    const bool swap = down ? a < b : b < a;
-                    v[r] = swap ? b : a;
-                    v[r + stride] = swap ? a : b;
-                }
+            for (int r = 0; r < R; ++r) {
+                if (r & stride) continue;
+                const bool down = ((lane * R + r) & size) == 0 || size == 32 * R;  // this run descends
+                const unsigned long long a = v[r], b = v[r + stride];
+                const bool swap = down ? a < b : b < a;
+                v[r] = swap ? b : a;
+                v[r + stride] = swap ? a : b;
             }
         }
     }
@@ -499,6 +512,7 @@ __device__ __noinline__ void sort_long_list(unsigned long long* list, int n) {
         v[q] = q * 32 + lane < n ? list[q * 32 + lane] : ~0ull;
         r[q] = 0;
     }
+#pragma unroll 1
     for (int j = 0; j < n; ++j) {
         const unsigned long long o = list[j];
 #pragma unroll
@@ -514,6 +528,7 @@ __device__ __noinline__ void sort_long_list(unsigned long long* list, int n) {
 __device__ __forceinline__ int count_larger(const unsigned long long* list, int n, unsigned long long item) {
     const uint32_t at = smem_u32(list);
     int r = 0, j = 0;
+#pragma unroll 1
     for (; j + 16 <= n; j += 16) {
         unsigned long long v[16];
 #pragma unroll
@@ -567,6 +582,7 @@ __device__ __noinline__ void close_rows(const LogprobParams& p, StreamBars& bars
     RowPos rp;
     Slice s = slice_of<ES>(p.src, cid, rank);
     bool aborted = false;
+#pragma unroll 1
     for (int64_t base = 0; base < n_it; base += 32) {
         // 32 rows' labels at once, and the logits of this warp's rows, a row a lane
         int64_t lab = label0;
@@ -577,6 +593,7 @@ __device__ __noinline__ void close_rows(const LogprobParams& p, StreamBars& bars
         if (p.logp && rank == 0 && ok && (!TOPK || (rp.buf + __popc(valid & lanes_below())) % p.src.buffers == me))
             x_lab = load_scalar<ES>(p.src.x + ((cid + (base + lane) * ncl) * p.src.ld + lab) * ES);
         const int nj = static_cast<int>(min(static_cast<int64_t>(32), n_it - base));
+#pragma unroll 1
         for (int j = 0; j < nj; ++j) {
             const int64_t row = cid + (base + j) * ncl;
             if (!(valid >> j & 1u)) {
@@ -588,6 +605,7 @@ __device__ __noinline__ void close_rows(const LogprobParams& p, StreamBars& bars
                         if (p.stats) p.stats[row] = make_float2(0.f, 0.f);
                     }
                     if (TOPK) {
+#pragma unroll 1
                         for (int i = lane; i < p.top_k; i += 32) {
                             p.top_lp[row * p.top_k + i] = 0.f;
                             p.top_ids[row * p.top_k + i] = -1;
@@ -626,11 +644,14 @@ __device__ __noinline__ void close_rows(const LogprobParams& p, StreamBars& bars
                 if (lane == 0) mbar_arrive(&bars.row_empty[buf]);
                 top_ordered(best, n);
                 if (k > 1) {
+#pragma unroll 1
                     for (int i = n + lane; i < K; i += 32) best[i] = 0ull;
                     __syncwarp();
                     if (push) {
+#pragma unroll 1
                         for (int i = lane; i < K; i += 32) {
                             const unsigned long long v = best[i];
+#pragma unroll 1
                             for (int o = 0; o < k; ++o) {
                                 const uint32_t to = mapa_u32(pushed + rank * K + i, static_cast<uint32_t>(o));
                                 asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to), "l"(v) : "memory");
@@ -666,11 +687,13 @@ __device__ __noinline__ void close_rows(const LogprobParams& p, StreamBars& bars
                     oid[r] = static_cast<int32_t>(~static_cast<uint32_t>(item));
                 };
                 if (k == 1) {
+#pragma unroll 1
                     for (int i = lane; i < min(n, K); i += 32) write(i, best[i]);
                 } else {
                     // The rank of each of this CTA's best among the cluster's: the sum of its places in the
                     // lists, by bisection in all of them at once where they are here (pushed before the
                     // exchange), else in one after the other in the other CTAs' memory.
+#pragma unroll 1
                     for (int i = lane; i < K; i += 32) {
                         const unsigned long long item = best[i];
                         int r = 0;
@@ -678,6 +701,7 @@ __device__ __noinline__ void close_rows(const LogprobParams& p, StreamBars& bars
                             int at[kStreamMaxCluster];  // so many of a list are larger
 #pragma unroll
                             for (int o = 0; o < kStreamMaxCluster; ++o) at[o] = 0;
+#pragma unroll 1
                             for (int step = 1 << (31 - __clz(K)); step > 0; step >>= 1) {
 #pragma unroll
                                 for (int o = 0; o < kStreamMaxCluster; ++o) {
@@ -688,9 +712,11 @@ __device__ __noinline__ void close_rows(const LogprobParams& p, StreamBars& bars
 #pragma unroll
                             for (int o = 0; o < kStreamMaxCluster; ++o) r += at[o];
                         } else {
+#pragma unroll 1
                             for (int o = 0; o < k; ++o) {
                                 const uint32_t remote = mapa_u32(best, static_cast<uint32_t>(o));
                                 int a = 0, b = K;  // of list o: before a larger, from b on not
+#pragma unroll 1
                                 while (a < b) {
                                     const int mid = (a + b) / 2;
                                     unsigned long long v;
@@ -707,6 +733,7 @@ __device__ __noinline__ void close_rows(const LogprobParams& p, StreamBars& bars
                     if (lane < k) remote_arrive(&bars.peers_done[buf], static_cast<uint32_t>(lane));
                 }
                 if (none && rank == 0) {
+#pragma unroll 1
                     for (int i = lane; i < K; i += 32) {
                         olp[i] = st.s;
                         oid[i] = -1;
@@ -762,6 +789,7 @@ __global__ void __launch_bounds__(kLogprobThreads<TOPK>, 3) logprobs_kernel(cons
         RowPos rp;
         Slice s = slice_of<ES>(p.src, cid, rank);
         int64_t y_next = label0;
+#pragma unroll 1
         for (int64_t it = 0; it < n_it; ++it) {
             const int64_t row = cid + it * ncl;
             const int64_t y = y_next;
@@ -773,6 +801,7 @@ __global__ void __launch_bounds__(kLogprobThreads<TOPK>, 3) logprobs_kernel(cons
             MaxT* rm = maxima + buf * p.max_stride;
             RunStat<ENT, false> st(p.scale);
             float most = kNegInf;  // of the thread's blocks
+#pragma unroll 1
             for (int c0 = 0; c0 < s.nv; c0 += Sh::kChunk) {
                 const int nl = min(Sh::kChunk, s.nv - c0);
                 uint4 v[kBlockVec];

@@ -216,6 +216,7 @@ __device__ __forceinline__ bool stream_produce(const StreamSrc& p, StreamBars& b
     bool wrapped = false, stop = false;
     uint32_t armed = 0;  // stages whose last copy was issued
     bool bad = false;
+#pragma unroll 1
     for (int64_t base = 0; base < n_it; base += 32) {
         // 32 rows' labels at once: no copy waits for a label of its own
         int64_t lab = first;
@@ -224,12 +225,15 @@ __device__ __forceinline__ bool stream_produce(const StreamSrc& p, StreamBars& b
         bad |= base + lane < n_it && !ok && lab != p.ignore_index;
         const unsigned valid = __ballot_sync(0xffffffffu, ok);
         const int nj = static_cast<int>(min(static_cast<int64_t>(32), n_it - base));
+#pragma unroll 1
         for (int j = 0; j < nj; ++j) {
             if (!(valid >> j & 1u)) continue;
             const int64_t row = cid + (base + j) * ncl;
             if (lane == 0 && !stop) {
                 move_slice<ES>(p, row, rank, s);
+#pragma unroll 1
                 for (int pass = 0; pass < passes && !stop; ++pass) {
+#pragma unroll 1
                     for (int c0 = 0; c0 < s.nv; c0 += Shape<NT>::kChunk) {
                         if (wrapped && !stream_wait(bars, &bars.empty[st], par ^ 1u, p.wait_ns)) stop = true;
                         if (stop || stream_aborted(bars)) {
@@ -264,6 +268,7 @@ __device__ __forceinline__ bool stream_produce(const StreamSrc& p, StreamBars& b
     }
     // the CTA must not end, nor its shared memory be given away, under a copy in flight
     if (lane == 0) {
+#pragma unroll 1
         for (uint32_t s = 0; s < S; ++s) {
             if (!(armed >> s & 1u)) continue;
             const uint32_t last = s < st ? par : par ^ 1u;  // the parity of the stage's last use
@@ -581,6 +586,7 @@ __device__ __forceinline__ void stat_merge(RunStat<ENT, TWO>& st, const StatExch
                                            const ExpScale& x) {
     st.set(ex.cta[buf][use & 1u][threadIdx.x & (k - 1)], x);
     st.raise(warp_max_redux(st.m), x);
+#pragma unroll 1
     for (int off = k / 2; off > 0; off >>= 1) {
         st.s += __shfl_xor_sync(0xffffffffu, st.s, off);
         if (ENT) st.a += __shfl_xor_sync(0xffffffffu, st.a, off);
