@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kDistillThreads<NT>, NT == 256 ? 2 : 1) distil
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = p.src.k;
     const int rank = k > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int64_t cid = blockIdx.x >> p.src.log2_k, ncl = gridDim.x >> p.src.log2_k;
-    const int64_t n_it = p.src.N > cid ? (p.src.N - 1 - cid) / ncl + 1 : 0;
+    const int64_t n_it = stream_rows(p.src, cid);
     stream_init<NT>(bars, p.src.stages, k);
     if (tid == 0) s_bad = 0;
     griddep_launch_dependents();  // programmatic dependent launch: no global access before the wait
@@ -113,6 +113,7 @@ __global__ void __launch_bounds__(kDistillThreads<NT>, NT == 256 ? 2 : 1) distil
             if (!stream_row_valid(y, p.src)) {
                 if constexpr (GRAD) {
                     const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
                     for (int i = tid; i < s.nv; i += NT) st_global_cs_v4(dv + i, z);
                     if (tid < s.h) store_scalar<ES>(drow + tid * ES, 0.f);
                     if (tid < s.t) store_scalar<ES>(drow + (s.tail_col + tid) * ES, 0.f);
@@ -277,6 +278,7 @@ __global__ void __launch_bounds__(kDistillThreads<NT>, NT == 256 ? 2 : 1) distil
                 if (rank == 0 && !aborted) {
                     const float ln_t = logf(st.s), ln_1 = logf(s1);
                     float kd = 0.f;
+#pragma unroll 1
                     for (int i = lane; i < K; i += 32) {
                         const float q = teach.q[i];
                         if (!(q == 0.f)) kd += q * (teach.lnq[i] - (empty ? kNegInf : (teach.x[i] - st.m) * p.inv_t - ln_t));
@@ -343,6 +345,7 @@ cudaError_t launch_typed(DistillParams prm, int per_sm, cudaStream_t stream) {
         }
     }
     const int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(s.N, static_cast<int64_t>(device_sm_count()) * per_sm / s.k));
+    set_rows(s, clusters);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(clusters * s.k), 1, 1);
     cfg.blockDim = dim3(kDistillThreads<NT>, 1, 1);

@@ -368,7 +368,7 @@ __device__ __noinline__ int top_list(const Slice s, const typename Block<ES>::ty
         return n;
     };
     int n_sel = blocks_from(false), need = kAll, strict = kAll;  // sel[strict ..]: blocks whose maximum is the floor, in order
-    if (n_sel > kSelCap) {
+    if (__builtin_expect(n_sel > kSelCap, 0)) {
         // Ties at the threshold (a mask that leaves fewer than K tokens): the blocks above
         // it, and the first blocks that reach it, as many as can matter.
         strict = blocks_from(true);
@@ -407,7 +407,7 @@ __device__ __noinline__ int top_list(const Slice s, const typename Block<ES>::ty
             }
             uint32_t hit = hit_bits<ES, false>(w, floor);
             if (nv < kBlockVec) hit &= nv > 0 ? first_bits<ES>(nv * EPV) : 0u;
-            if (strict != kAll) {
+            if (__builtin_expect(strict != kAll, 0)) {
                 // an equal one counts only if fewer than `need` come before it: those of its block, and all
                 // those of the tied blocks before, which are in order
                 const uint32_t tie = hit & hit_bits<ES, true>(w, floor);
@@ -523,39 +523,26 @@ __device__ __noinline__ void sort_long_list(unsigned long long* list, int n) {
     for (int q = 0; q < OWN; ++q)
         if (q * 32 + lane < n) list[r[q]] = v[q];
 }
-// How many of list[0, n) are larger than the item; the list is on a 16-byte boundary of
-// shared memory.  Sixteen at a time: the loads of a group go out together.
-__device__ __forceinline__ int count_larger(const unsigned long long* list, int n, unsigned long long item) {
-    const uint32_t at = smem_u32(list);
-    int r = 0, j = 0;
-#pragma unroll 1
-    for (; j + 16 <= n; j += 16) {
-        unsigned long long v[16];
-#pragma unroll
-        for (int q = 0; q < 16; q += 2)
-            asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(v[q]), "=l"(v[q + 1]) : "r"(at + (j + q) * 8) : "memory");
-#pragma unroll
-        for (int q = 0; q < 16; ++q) r += v[q] > item;
-    }
-    if (j < n) {
-        unsigned long long v[16];
-#pragma unroll
-        for (int q = 0; q < 16; ++q) {
-            v[q] = 0ull;
-            if (j + q < n) asm volatile("ld.shared.u64 %0, [%1];" : "=l"(v[q]) : "r"(at + (j + q) * 8) : "memory");
-        }
-#pragma unroll
-        for (int q = 0; q < 16; ++q) r += v[q] > item;
-    }
-    return r;
-}
-// Up to 32 items: each lane counts the larger ones of its own.
+// Up to 32 items: each lane counts the larger ones of its own, eight at a time, whose loads
+// go out together.
 __device__ __forceinline__ void sort_short_list(unsigned long long* list, int n) {
     const int lane = threadIdx.x & 31;
-    const unsigned long long v = lane < n ? list[lane] : 0ull;
-    const int r = count_larger(list, n, v);
+    const unsigned long long mine = lane < n ? list[lane] : 0ull;
+    if (lane >= n) list[lane] = 0ull;
     __syncwarp();
-    if (lane < n) list[r] = v;
+    const uint32_t at = smem_u32(list);
+    int r = 0;
+#pragma unroll 1
+    for (int j = 0; j < n; j += 8) {
+        unsigned long long v[8];
+#pragma unroll
+        for (int q = 0; q < 8; q += 2)
+            asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(v[q]), "=l"(v[q + 1]) : "r"(at + (j + q) * 8) : "memory");
+#pragma unroll
+        for (int q = 0; q < 8; ++q) r += v[q] > mine;
+    }
+    __syncwarp();
+    if (lane < n) list[r] = mine;
 }
 __device__ __forceinline__ void top_ordered(unsigned long long* list, int n) {
     if (n <= 32) sort_short_list(list, n);
@@ -577,7 +564,7 @@ __device__ __noinline__ void close_rows(const LogprobParams& p, StreamBars& bars
     const int lane = threadIdx.x & 31, k = p.src.k;
     const int rank = k > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int64_t cid = blockIdx.x >> p.src.log2_k, ncl = gridDim.x >> p.src.log2_k;
-    const int64_t n_it = p.src.N > cid ? (p.src.N - 1 - cid) / ncl + 1 : 0;
+    const int64_t n_it = stream_rows(p.src, cid);
     const int me = (threadIdx.x >> 5) - (Sh::kWarps + 1);  // with several closing warps, buffer `me` is this one's
     RowPos rp;
     Slice s = slice_of<ES>(p.src, cid, rank);
@@ -691,41 +678,26 @@ __device__ __noinline__ void close_rows(const LogprobParams& p, StreamBars& bars
                     for (int i = lane; i < min(n, K); i += 32) write(i, best[i]);
                 } else {
                     // The rank of each of this CTA's best among the cluster's: the sum of its places in the
-                    // lists, by bisection in all of them at once where they are here (pushed before the
-                    // exchange), else in one after the other in the other CTAs' memory.
+                    // lists, by a bisection of each, here if they were pushed before the exchange, else in
+                    // the other CTAs' memory.
 #pragma unroll 1
                     for (int i = lane; i < K; i += 32) {
                         const unsigned long long item = best[i];
                         int r = 0;
-                        if (push) {
-                            int at[kStreamMaxCluster];  // so many of a list are larger
-#pragma unroll
-                            for (int o = 0; o < kStreamMaxCluster; ++o) at[o] = 0;
 #pragma unroll 1
-                            for (int step = 1 << (31 - __clz(K)); step > 0; step >>= 1) {
-#pragma unroll
-                                for (int o = 0; o < kStreamMaxCluster; ++o) {
-                                    const int to = at[o] + step;
-                                    if (o < k && to <= K && pushed[o * K + to - 1] > item) at[o] = to;
-                                }
+                        for (int o = 0; o < k; ++o) {
+                            const uint32_t list = push ? mapa_u32(pushed + o * K, static_cast<uint32_t>(rank))
+                                                       : mapa_u32(best, static_cast<uint32_t>(o));
+                            int a = 0, b = K;  // of list o: before a larger, from b on not
+#pragma unroll 1
+                            while (a < b) {
+                                const int mid = (a + b) / 2;
+                                unsigned long long v;
+                                asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(list + mid * 8) : "memory");
+                                if (v > item) a = mid + 1;
+                                else b = mid;
                             }
-#pragma unroll
-                            for (int o = 0; o < kStreamMaxCluster; ++o) r += at[o];
-                        } else {
-#pragma unroll 1
-                            for (int o = 0; o < k; ++o) {
-                                const uint32_t remote = mapa_u32(best, static_cast<uint32_t>(o));
-                                int a = 0, b = K;  // of list o: before a larger, from b on not
-#pragma unroll 1
-                                while (a < b) {
-                                    const int mid = (a + b) / 2;
-                                    unsigned long long v;
-                                    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(remote + mid * 8) : "memory");
-                                    if (v > item) a = mid + 1;
-                                    else b = mid;
-                                }
-                                r += a;
-                            }
+                            r += a;
                         }
                         if (item && r < K) write(r, item);
                     }
@@ -761,7 +733,7 @@ __global__ void __launch_bounds__(kLogprobThreads<TOPK>, 3) logprobs_kernel(cons
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = p.src.k;
     const int rank = k > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int64_t cid = blockIdx.x >> p.src.log2_k, ncl = gridDim.x >> p.src.log2_k;
-    const int64_t n_it = p.src.N > cid ? (p.src.N - 1 - cid) / ncl + 1 : 0;
+    const int64_t n_it = stream_rows(p.src, cid);
     stream_init<kThreads>(bars, p.src.stages, k);
     griddep_launch_dependents();  // programmatic dependent launch: no global access before the wait
     griddep_wait();
@@ -907,6 +879,7 @@ cudaError_t launch_typed(LogprobParams prm, cudaStream_t stream) {
         }
     }
     const int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(s.N, static_cast<int64_t>(sms) * per_sm / s.k));
+    set_rows(s, clusters);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(clusters * s.k), 1, 1);
     cfg.blockDim = dim3(kLogprobThreads<TOPK>, 1, 1);

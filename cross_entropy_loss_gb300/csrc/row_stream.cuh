@@ -54,6 +54,7 @@ struct StreamSrc {
     uint64_t wait_ns;       // limit of every shared-memory barrier wait
     int64_t skip_load_row;  // test hook: this row's first chunk is never loaded (-1: none)
     int k, log2_k;          // CTAs of a row's cluster
+    int64_t each, more;     // rows of every cluster, and how many of the clusters have one more
     int buffers;            // rows between the consumers and the closing warps
     bool evict_last_pass;
     int stages;
@@ -94,6 +95,13 @@ inline void set_cluster(StreamSrc& p, int k) {
     p.k = k;
     for (p.log2_k = 0; (1 << p.log2_k) < k;) ++p.log2_k;
 }
+
+// The rows shared out to `clusters`: cluster c takes c, c + clusters, ...
+inline void set_rows(StreamSrc& p, int64_t clusters) {
+    p.each = p.N / clusters;
+    p.more = p.N % clusters;
+}
+__device__ __forceinline__ int64_t stream_rows(const StreamSrc& p, int64_t cid) { return p.each + (cid < p.more); }
 
 // How many CTAs share a row: all eight while the rows are few, for a cluster reads its row as
 // much faster, and one where there are rows for every SM.  A row of less than kWholeRowBytes
@@ -209,7 +217,7 @@ template <int ES, int NT>
 __device__ __forceinline__ bool stream_produce(const StreamSrc& p, StreamBars& bars, unsigned char* ring, int passes,
                                                int64_t cid, int64_t ncl, int rank, int64_t first) {
     const int lane = threadIdx.x & 31;
-    const int64_t n_it = p.N > cid ? (p.N - 1 - cid) / ncl + 1 : 0;
+    const int64_t n_it = stream_rows(p, cid);
     const uint32_t S = static_cast<uint32_t>(p.stages);
     Slice s = slice_of<ES>(p, cid, rank);
     uint32_t st = 0, par = 0;  // the next stage, and the parity of its use

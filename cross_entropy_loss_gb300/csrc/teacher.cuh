@@ -111,12 +111,14 @@ __device__ __forceinline__ void teacher_correct(const TeacherRow& t, int K, int6
                                                 float x_y, float w1, float wt, char* drow, F&& grad_at) {
     const int lane = threadIdx.x & 31;
     bool listed = false;
+#pragma unroll 1
     for (int k = lane; k < K; k += 32) {
         const int id = t.id[k];
         if (id < 0 || id < col_lo || id >= col_hi) continue;
         float mass = t.q[k];
         if (t.repeated) {
             mass = 0.f;
+#pragma unroll 1
             for (int j = 0; j < K; ++j) mass += t.id[j] == id ? t.q[j] : 0.f;
         }
         float e = grad_at(t.x[k]) - wt * mass;
