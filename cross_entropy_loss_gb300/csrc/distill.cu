@@ -249,15 +249,21 @@ __global__ void __launch_bounds__(kDistillThreads<NT>, NT == 256 ? 2 : 1) distil
                 move_slice<ES>(p.src, row, rank, s);
                 const int64_t col_lo = rank == 0 ? 0 : s.col0;
                 const int64_t col_hi = rank == k - 1 ? p.src.V : s.col0 + static_cast<int64_t>(s.nv) * EPV;
-                // rank 0 takes all the listed logits (for the loss), the others those of their share
-                const bool bad = teacher_row<ES>(p.teacher, row, p.src.V, s.rowp, rank == 0 ? 0 : col_lo,
-                                                 rank == 0 ? p.src.V : col_hi, teach);
+                const bool bad = teacher_row(p.teacher, row, p.src.V, teach);
                 n_bad += bad && lane == 0;
+                // Rank 0 takes all the listed logits (for the loss), the others those of their share: ahead of
+                // the row where its gradient may overwrite it, else after it, when they are in L2 (4096 x 32000
+                // bf16, K = 64: 52.6 us, ahead of it 57.7; with the gradient both took 96).
+                auto gather = [&] {
+                    teacher_gather<ES>(K, s.rowp, rank == 0 ? 0 : col_lo, rank == 0 ? p.src.V : col_hi, teach);
+                };
+                if (GRAD) gather();
                 if (GRAD && k == 1 && lane == 0) {  // all that the second sweep needs from here
                     total[buf] = teach.total;
                     mbar_arrive(&bars.row_ready[buf]);
                 }
                 if (!aborted && !stream_wait(bars, &bars.row_full[buf], use & 1u, p.src.wait_ns)) aborted = true;
+                if (!GRAD) gather();
                 RunStat<false, TWO> st(sc);
                 stat_collect<NT>(st, ex, buf, sc);
                 __syncwarp();

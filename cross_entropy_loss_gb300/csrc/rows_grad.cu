@@ -305,7 +305,8 @@ __global__ void __launch_bounds__(kGradThreads + 32, kTeacherBlocksPerSm) distil
             if (stream_row_valid(now.y, p.src)) {
                 now.col_lo = s.col_lo;
                 now.col_hi = segment_of<ES>(p, next - 1).col_hi;
-                teacher_row<ES>(p.teacher, s.row, p.src.V, s.rowp, now.col_lo, now.col_hi, teacher[visit & 1u]);
+                teacher_row(p.teacher, s.row, p.src.V, teacher[visit & 1u]);
+                teacher_gather<ES>(p.teacher.K, s.rowp, now.col_lo, now.col_hi, teacher[visit & 1u]);
                 now.x_y = now.y >= now.col_lo && now.y < now.col_hi ? load_scalar<ES>(s.rowp + now.y * ES) : 0.f;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&gathered[visit & 1u]);

@@ -27,80 +27,98 @@ struct TeacherRow {
     bool repeated;                        // a token is listed more than once
 };
 
-// Filled by a whole warp, which is in step afterwards.  Returns whether an id was V or more
-// (such an entry, like one with a negative id, counts as absent).  The student's logits
-// are fetched for the ids in [col_lo, col_hi).
-template <int ES>
-__device__ __forceinline__ bool teacher_row(const TeacherSrc& p, int64_t row, int64_t V, const char* rowp,
-                                            int64_t col_lo, int64_t col_hi, TeacherRow& out) {
+// The row's targets, by a whole warp, which is in step afterwards.  Returns whether an id
+// was V or more (such an entry, like one with a negative id, counts as absent).
+// (Loops over shared memory: unrolled over a lane's eight entries in registers, the code
+// crowds the streaming warps' out of the instruction cache.)
+__device__ __forceinline__ bool teacher_row(const TeacherSrc& p, int64_t row, int64_t V, TeacherRow& out) {
     constexpr int PER = kTeacherMax / 32;
-    const int lane = threadIdx.x & 31;
-    float t[PER];
+    const int lane = threadIdx.x & 31, K4 = (p.K + 3) / 4 * 4;
+    const int32_t* ids = p.ids + row * p.ld;
+    const float* logp = p.logp + row * p.ld;
     int id[PER];
-    // all loads of a kind go out together: two latencies, not two for each 32 entries
+    float t[PER];
+    // all loads go out together
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
         const int k = lane + 32 * j;
         id[j] = -1;
         t[j] = kNegInf;
         if (k < p.K) {
-            id[j] = __ldg(p.ids + row * p.ld + k);
-            t[j] = __ldg(p.logp + row * p.ld + k);
+            id[j] = __ldg(ids + k);
+            t[j] = __ldg(logp + k);
         }
     }
     __syncwarp();
 #pragma unroll
-    for (int j = 0; j < 2 * kTeacherMax / 128; ++j)
-        reinterpret_cast<int4*>(out.seen)[lane + 32 * j] = make_int4(-1, -1, -1, -1);
+    for (int j = 0; j < PER; ++j) {
+        const int k = lane + 32 * j;
+        if (k < K4) {
+            out.id[k] = id[j];
+            out.lnq[k] = t[j];
+        }
+    }
+#pragma unroll 1
+    for (int j = lane; j < 2 * kTeacherMax / 4; j += 32) reinterpret_cast<int4*>(out.seen)[j] = make_int4(-1, -1, -1, -1);
     __syncwarp();
     bool bad = false, twice = false;
     float top = kNegInf;
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-        const int k = lane + 32 * j;
-        if (32 * j >= p.K) break;
-        bad |= id[j] >= V;
-        if (id[j] < 0 || id[j] >= V) {
-            id[j] = -1;
-            t[j] = kNegInf;
+#pragma unroll 1
+    for (int k = lane; k < K4; k += 32) {
+        const int i = out.id[k];
+        bad |= i >= V;
+        if (i < 0 || i >= V) {
+            out.id[k] = -1;
+            out.lnq[k] = kNegInf;
+            continue;
         }
-        if (k < (p.K + 3) / 4 * 4) out.id[k] = id[j];
-        if (id[j] >= col_lo && id[j] < col_hi) out.x[k] = load_scalar<ES>(rowp + static_cast<int64_t>(id[j]) * ES);
-        if (id[j] >= 0) {  // at most half of the table fills
-            for (unsigned h = (static_cast<unsigned>(id[j]) * 2654435761u) >> 23;; h = (h + 1) & (2 * kTeacherMax - 1)) {
-                const int before = atomicCAS(out.seen + h, -1, id[j]);
-                twice |= before == id[j];
-                if (before == -1 || before == id[j]) break;
-            }
+        // at most half of the table fills
+        for (unsigned h = (static_cast<unsigned>(i) * 2654435761u) >> 23;; h = (h + 1) & (2 * kTeacherMax - 1)) {
+            const int before = atomicCAS(out.seen + h, -1, i);
+            twice |= before == i;
+            if (before == -1 || before == i) break;
         }
-        top = fmaxf(top, t[j]);
+        top = fmaxf(top, out.lnq[k]);
     }
     static_assert(2 * kTeacherMax == 1 << (32 - 23), "the hash takes the table's bits");
-    top = warp_max(top);
+    __syncwarp();
+    top = p.normalize ? warp_max(top) : 0.f;
     // q = e^t, or that over its sum; the sum is taken below the largest so that it cannot overflow
     float sum = 0.f;
-#pragma unroll
-    for (int j = 0; j < PER; ++j)
-        if (32 * j < p.K) sum += t[j] == kNegInf ? 0.f : expf(p.normalize ? t[j] - top : t[j]);
+#pragma unroll 1
+    for (int k = lane; k < K4; k += 32) {
+        const float v = out.lnq[k], q = v == kNegInf ? 0.f : expf(v - top);
+        out.q[k] = q;
+        sum += q;
+    }
     sum = warp_sum(sum);
-    const float ln_norm = p.normalize && sum > 0.f ? top + logf(sum) : 0.f;
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-        const int k = lane + 32 * j;
-        if (32 * j < p.K && k < (p.K + 3) / 4 * 4) {
-            out.lnq[k] = t[j] - ln_norm;
-            // the quotient, not e^(t - ln norm): its rounding stays relative to q
-            out.q[k] = t[j] == kNegInf ? 0.f : (p.normalize ? expf(t[j] - top) / sum : expf(t[j]));
+    const bool over = p.normalize && sum > 0.f;
+    if (over) {
+        const float ln_norm = top + logf(sum);
+#pragma unroll 1
+        for (int k = lane; k < K4; k += 32) {
+            out.lnq[k] -= ln_norm;
+            out.q[k] /= sum;  // the quotient, not e^(t - ln norm): its rounding stays relative to q
         }
     }
     twice = __any_sync(0xffffffffu, twice);
     if (lane == 0) {
-        out.total = p.normalize && sum > 0.f ? 1.f : sum;
+        out.total = over ? 1.f : sum;
         out.repeated = twice;
     }
     bad = __any_sync(0xffffffffu, bad);
     __syncwarp();
     return bad;
+}
+// The student's logits of the listed tokens in [col_lo, col_hi), by a whole warp.
+template <int ES>
+__device__ __forceinline__ void teacher_gather(int K, const char* rowp, int64_t col_lo, int64_t col_hi, TeacherRow& out) {
+#pragma unroll 4
+    for (int k = threadIdx.x & 31; k < K; k += 32) {
+        const int id = out.id[k];
+        if (id >= col_lo && id < col_hi) out.x[k] = load_scalar<ES>(rowp + static_cast<int64_t>(id) * ES);
+    }
+    __syncwarp();
 }
 
 // A warp's corrections of a row's gradient in the columns [col_lo, col_hi): what the K
