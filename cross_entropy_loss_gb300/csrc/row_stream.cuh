@@ -196,7 +196,7 @@ __device__ __forceinline__ bool stream_aborted(const StreamBars& b) { return *re
 
 // Bounded wait that also ends when another thread has given up.
 __device__ __forceinline__ bool stream_wait(StreamBars& b, uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return true;
     const uint64_t t0 = globaltimer_ns();
     for (uint32_t i = 1;; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
@@ -453,7 +453,7 @@ struct RunStat {
         const float mn = fmaxf(m, warp_max_redux(v));
         if (mn > m) raise(mn, x);
         if (v == kNegInf) return;
-        if (far(x)) {
+        if (__builtin_expect(far(x), 0)) {
             const float one = v == m ? 1.f : v == v ? 0.f : v;
             s += one;
             if (TWO) s2 += one;
@@ -471,7 +471,7 @@ struct RunStat {
         const float bmax = RowMath<ES>::template vmax<NV>(v);
         const float mn = fmaxf(m, warp_max_redux(bmax));
         if (mn > m) raise(mn, x);
-        if (far(x)) {
+        if (__builtin_expect(far(x), 0)) {
             add_far<ES, NV>(v);
             return bmax;
         }
