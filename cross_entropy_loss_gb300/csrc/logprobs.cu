@@ -33,7 +33,7 @@ namespace {
 
 constexpr int kListCap = 384;   // listed elements of a row (or of a CTA's share of it): at least kTopKMax
 constexpr int kPushCap = 256;   // the cluster's lists, where they are pushed into every CTA
-constexpr int kSelCap = 256;    // blocks they are taken from
+constexpr int kSelCap = 320;    // blocks they are taken from
 constexpr int kAll = 0x7fffffff;
 constexpr int kThreads = 256;   // consumers
 using Sh = Shape<kThreads>;
@@ -299,6 +299,76 @@ __device__ __forceinline__ uint32_t first_bits(int n) {
     else return (1u << n) - 1u;
 }
 
+// The blocks of the body whose maximum reaches the floor (above: is above it) onto sel, 16
+// bytes of maxima a lane and turn.  Returns how many, or some number above kSelCap.
+template <int ES>
+__device__ __forceinline__ int blocks_from(const typename Block<ES>::type* maxima, int nblk, float floor, bool above,
+                                           uint16_t* sel) {
+    constexpr int PACK = 16 / sizeof(typename Block<ES>::type);
+    const int lane = threadIdx.x & 31;
+    const uint4* mv = reinterpret_cast<const uint4*>(maxima + kBodyAt);
+    int n = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < nblk && n <= kSelCap; b0 += 32 * PACK) {
+        const int b = b0 + lane * PACK;
+        uint32_t hit = 0;
+        if (b < nblk) {
+            const uint4 q = mv[b / PACK];
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+            hit = hit_bits<ES, false>(w, floor);
+            if (above) hit &= ~hit_bits<ES, true>(w, floor);
+            if (nblk - b < PACK) hit &= first_bits<ES>(nblk - b);
+        }
+#pragma unroll 1
+        for (unsigned m = __ballot_sync(0xffffffffu, hit != 0); m; m = __ballot_sync(0xffffffffu, hit != 0)) {
+            const int at = n + __popc(m & lanes_below());
+            if (hit && at < kSelCap) sel[at] = static_cast<uint16_t>(1 + b + element_of_bit<ES>(__ffs(hit) - 1));
+            hit &= hit - 1;
+            n += __popc(m);
+        }
+    }
+    __syncwarp();
+    return n;
+}
+// The same out of line, for the ways that few rows take.
+template <int ES>
+__device__ __noinline__ int blocks_again(const typename Block<ES>::type* maxima, int nblk, float floor, bool above,
+                                         uint16_t* sel) {
+    return blocks_from<ES>(maxima, nblk, floor, above, sel);
+}
+// A higher threshold for a row in which more blocks than sel has room for are above `floor`:
+// K blocks reach it, and no more than `most` unless they are equal there.
+template <int ES>
+__device__ __noinline__ float blocks_floor(const typename Block<ES>::type* maxima, int nblk, float floor, int K,
+                                           int most) {
+    constexpr int PACK = 16 / sizeof(typename Block<ES>::type);
+    const int lane = threadIdx.x & 31;
+    const uint4* mv = reinterpret_cast<const uint4*>(maxima + kBodyAt);
+    uint32_t lo = short_key<ES>(floor), hi = short_key<ES>(__uint_as_float(0x7f800000u)) + 1u;
+#pragma unroll 1
+    while (hi - lo > 1) {
+        const uint32_t mid = lo + (hi - lo) / 2;
+        const float f = float_of_short_key<ES>(mid);
+        int n = 0;
+#pragma unroll 1
+        for (int b = lane * PACK; b < nblk; b += 32 * PACK) {
+            const uint4 q = mv[b / PACK];
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+            uint32_t hit = hit_bits<ES, false>(w, f);
+            if (nblk - b < PACK) hit &= first_bits<ES>(nblk - b);
+            n += __popc(hit);
+        }
+        n = __reduce_add_sync(0xffffffffu, n);
+        if (n >= K) {
+            lo = mid;
+            if (n <= most) break;
+        } else {
+            hi = mid;
+        }
+    }
+    return float_of_short_key<ES>(lo);
+}
+
 // This CTA's largest elements of its slice onto t.list: at least the min(K, all) largest
 // ones, at most kListCap.  Returns how many.  maxima are the blocks' (kBodyAt the first of
 // the body; 0 and 1 the head's and tail's), thread_max the keys of the threads'.
@@ -313,6 +383,7 @@ __device__ __noinline__ int top_list(const Slice s, const typename Block<ES>::ty
     // thread maxima, or a little below it.  Of 64-byte pieces in random order about
     // -256 ln(1 - K / 256) are at or above it.
     float floor = kNegInf;
+    const int most = K + K / 16 + 4;  // so many reaching it will do
     if (min((s.nv + kBlockVec - 1) / kBlockVec, kThreads) >= K) {
         uint32_t v[PER], least = 0xffffffffu, hi = 0;
 #pragma unroll
@@ -323,7 +394,6 @@ __device__ __noinline__ int top_list(const Slice s, const typename Block<ES>::ty
         }
         uint32_t lo = __reduce_min_sync(0xffffffffu, least) + 1u;
         hi = __reduce_max_sync(0xffffffffu, hi) + 1u;
-        const int most = K + K / 8 + 4;
 #pragma unroll 1
         while (hi - lo > 1) {
             const uint32_t mid = lo + (hi - lo) / 2;
@@ -340,38 +410,16 @@ __device__ __noinline__ int top_list(const Slice s, const typename Block<ES>::ty
         }
         floor = float_of_short_key<ES>(lo);
     }
-    // The blocks that reach it (above: that are above it), 16 bytes of maxima a lane and turn.
-    auto blocks_from = [&](bool above) {
-        constexpr int PACK = 16 / sizeof(typename B::type);
-        const uint4* mv = reinterpret_cast<const uint4*>(maxima + kBodyAt);
-        int n = 0;
-#pragma unroll 1
-        for (int b0 = 0; b0 < nblk && n <= kSelCap; b0 += 32 * PACK) {
-            const int b = b0 + lane * PACK;
-            uint32_t hit = 0;
-            if (b < nblk) {
-                const uint4 q = mv[b / PACK];
-                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-                hit = hit_bits<ES, false>(w, floor);
-                if (above) hit &= ~hit_bits<ES, true>(w, floor);
-                if (nblk - b < PACK) hit &= first_bits<ES>(nblk - b);
-            }
-#pragma unroll 1
-            for (unsigned m = __ballot_sync(0xffffffffu, hit != 0); m; m = __ballot_sync(0xffffffffu, hit != 0)) {
-                const int at = n + __popc(m & lanes_below());
-                if (hit && at < kSelCap) t.sel[at] = static_cast<uint16_t>(1 + b + element_of_bit<ES>(__ffs(hit) - 1));
-                hit &= hit - 1;
-                n += __popc(m);
-            }
-        }
-        __syncwarp();
-        return n;
-    };
-    int n_sel = blocks_from(false), need = kAll, strict = kAll;  // sel[strict ..]: blocks whose maximum is the floor, in order
+    int n_sel = blocks_from<ES>(maxima, nblk, floor, false, t.sel), need = kAll, strict = kAll;  // sel[strict ..]: blocks whose maximum is the floor, in order
     if (__builtin_expect(n_sel > kSelCap, 0)) {
+        strict = blocks_again<ES>(maxima, nblk, floor, true, t.sel);
+        if (strict >= K) {  // the 256 maxima were no good guide: K near their number, or logits in no random order
+            floor = blocks_floor<ES>(maxima, nblk, floor, K, most);
+            n_sel = blocks_again<ES>(maxima, nblk, floor, false, t.sel);
+            strict = n_sel > kSelCap ? blocks_again<ES>(maxima, nblk, floor, true, t.sel) : kAll;
+        }
         // Ties at the threshold (a mask that leaves fewer than K tokens): the blocks above
         // it, and the first blocks that reach it, as many as can matter.
-        strict = blocks_from(true);
         if (strict < K) {
             need = K - strict;
             int have = 0;
@@ -465,7 +513,7 @@ __device__ __noinline__ int top_list(const Slice s, const typename Block<ES>::ty
 }
 
 // The list in descending order, R items a lane: a bitonic sort in registers, lane l
-// holding the places l R .. l R + R - 1; the places from n to 32 R get 0.
+// holding the places l R .. l R + R - 1; the places from n to 32 R (or the list's end) get 0.
 template <int R>
 __device__ __noinline__ void sort_list(unsigned long long* list, int n) {
     const int lane = threadIdx.x & 31;
@@ -499,29 +547,8 @@ __device__ __noinline__ void sort_list(unsigned long long* list, int n) {
     }
     __syncwarp();
 #pragma unroll
-    for (int r = 0; r < R; ++r) list[lane * R + r] = v[r];
-}
-// The same for lists of up to kListCap, by counting the larger ones of each.
-__device__ __noinline__ void sort_long_list(unsigned long long* list, int n) {
-    constexpr int OWN = kListCap / 32;
-    const int lane = threadIdx.x & 31;
-    unsigned long long v[OWN];
-    int r[OWN];
-#pragma unroll
-    for (int q = 0; q < OWN; ++q) {
-        v[q] = q * 32 + lane < n ? list[q * 32 + lane] : ~0ull;
-        r[q] = 0;
-    }
-#pragma unroll 1
-    for (int j = 0; j < n; ++j) {
-        const unsigned long long o = list[j];
-#pragma unroll
-        for (int q = 0; q < OWN; ++q) r[q] += o > v[q];
-    }
-    __syncwarp();
-#pragma unroll
-    for (int q = 0; q < OWN; ++q)
-        if (q * 32 + lane < n) list[r[q]] = v[q];
+    for (int r = 0; r < R; ++r)
+        if (32 * R <= kListCap || lane * R + r < kListCap) list[lane * R + r] = v[r];
 }
 // Up to 32 items: each lane counts the larger ones of its own, eight at a time, whose loads
 // go out together.
@@ -549,7 +576,7 @@ __device__ __forceinline__ void top_ordered(unsigned long long* list, int n) {
     else if (n <= 64) sort_list<2>(list, n);
     else if (n <= 128) sort_list<4>(list, n);
     else if (n <= 256) sort_list<8>(list, n);
-    else sort_long_list(list, n);
+    else sort_list<16>(list, n);
     __syncwarp();
 }
 

@@ -66,7 +66,8 @@ def _check_backward(ce, x, xd, y, out, want, T, seed=0, entropy=True, in_place=F
 @pytest.mark.parametrize("N,V,K", [(1, 1, 1), (3, 2, 2), (5, 7, 3), (4, 31, 31), (2, 33, 20), (9, 1000, 64),
                                    (6, 8192, 20), (5, 32000, 5), (3, 50257, 128), (2, 128256, 20), (1, 128256, 256),
                                    (40, 32000, 20), (90, 50257, 7), (400, 9001, 50), (1000, 2055, 8),
-                                   (2, 128256, 100), (64, 128263, 20), (130, 128256, 200), (20, 64131, 3)])
+                                   (2, 128256, 100), (64, 128263, 20), (130, 128256, 200), (20, 64131, 3),
+                                   (20, 32000, 256), (200, 40001, 161)])
 def test_shapes(cuda_lib, dtype, N, V, K):
     x = ref.make_logits(N, V, dtype, seed=N + V)
     y = _labels(N, V, N + V, n_ignore=N // 7)
