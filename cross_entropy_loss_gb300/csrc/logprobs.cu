@@ -7,20 +7,25 @@
 //
 // One read of the row gives m, S and A (running sums per thread, rescaled at a new
 // maximum).  The top K come out of the same read: a thread's 64-byte block of a chunk
-// has one maximum, which the sums need anyway and which is kept as an ordered integer
-// key.  Blocks are contiguous, so the K largest blocks by (maximum, lower index first)
-// hold the K largest elements by (value, lower index first): with a total order an
-// element outside those blocks has K larger ones before it.  A row's end, by the CTA's
-// one closing warp while the others are on the next rows, is
+// has one maximum, which the sums need anyway and which is kept.  Blocks (32 elements) are
+// contiguous, so the K largest blocks by (maximum, lower index first) hold the K largest
+// elements by (value, lower index first): with a total order an element outside those
+// blocks has K larger ones before it.  A row's end, by one of the
+// CTA's three closing warps while the others are on the next rows, is
 //
-//   1. a threshold that at least K blocks reach, from the consumer threads' maxima;
+//   1. a threshold that at least K blocks reach, from the 256 consumer threads' maxima;
 //   2. the blocks at or above it, re-read (from L2: the row just went through), and their
 //      elements at or above the threshold put on a list;
 //   3. the list put in order, in registers.
 //
-// Rows go to CTAs round-robin; when there are fewer rows than SMs a cluster shares each
-// row, joins its sums and lists through distributed shared memory, and ranks every
-// CTA's K candidates against the others'.
+// Rows go to CTAs round-robin; when there are few a cluster shares each row, joins its
+// sums and lists through distributed shared memory, and ranks every CTA's K candidates
+// against the others'.
+//
+// Measured, with entropy, bf16 unless said: 8192 x 128256, K = 0, 20, 128: 307, 358, 407 us
+// (6.85, 5.9, 5.2 TB/s); 4096 x 32000, K = 0, 5, 128: 48, 68, 122; 2048 x 128256 fp32, K = 64:
+// 188 (5.6 TB/s); 1 x 128256, K = 0, 20: 6.6 and 13.9.  With top tokens a row's end is some
+// 10000 cycles alone, three times that beside nine warps that sum: short rows pay for it.
 #include <algorithm>
 #include <map>
 #include <mutex>
@@ -32,14 +37,14 @@ namespace foak {
 namespace {
 
 constexpr int kListCap = 384;   // listed elements of a row (or of a CTA's share of it): at least kTopKMax
-constexpr int kPushCap = 256;   // the cluster's lists, where they are pushed into every CTA
 constexpr int kSelCap = 320;    // blocks they are taken from
 constexpr int kAll = 0x7fffffff;
 constexpr int kThreads = 256;   // consumers
 using Sh = Shape<kThreads>;
 constexpr int kBodyAt = 8;      // place of the first body block's maximum; before it the head's and the tail's
-// Closing warps of a CTA.  The work on a row's top tokens is a chain of some 6000 cycles
-// (K = 20), so three take rows in turn; without top tokens one keeps up.
+// Closing warps of a CTA.  The work on a row's top tokens is a chain of 10000 cycles or more,
+// so three take rows in turn (8192 x 128256, K = 128: two with two CTAs an SM 464 us, three
+// with three 454, four 487, as their registers spill); without top tokens one keeps up.
 template <bool TOPK>
 constexpr int kClosers = TOPK ? 3 : 1;
 
@@ -410,7 +415,8 @@ __device__ __noinline__ int top_list(const Slice s, const typename Block<ES>::ty
         }
         floor = float_of_short_key<ES>(lo);
     }
-    int n_sel = blocks_from<ES>(maxima, nblk, floor, false, t.sel), need = kAll, strict = kAll;  // sel[strict ..]: blocks whose maximum is the floor, in order
+    int n_sel = blocks_from<ES>(maxima, nblk, floor, false, t.sel);
+    int need = kAll, strict = kAll;  // sel[strict ..]: blocks whose maximum is the floor, in order
     if (__builtin_expect(n_sel > kSelCap, 0)) {
         strict = blocks_again<ES>(maxima, nblk, floor, true, t.sel);
         if (strict >= K) {  // the 256 maxima were no good guide: K near their number, or logits in no random order
@@ -645,8 +651,7 @@ __device__ __noinline__ void close_rows(const LogprobParams& p, StreamBars& bars
             int n = 0;
             const int K = p.top_k;
             unsigned long long* best = top[TOPK ? me : 0].list;
-            unsigned long long* pushed = reinterpret_cast<unsigned long long*>(smem_pushed) + (TOPK ? me : 0) * kPushCap;
-            const bool push = k > 1 && K * k <= kPushCap;
+            unsigned long long* pushed = reinterpret_cast<unsigned long long*>(smem_pushed);  // the cluster's lists, K each
             if constexpr (TOPK) {  // this CTA's largest, in order
                 TopScratch& t = top[me];
                 // the last row's list may still be read by the cluster's other CTAs, and theirs written over ours
@@ -661,15 +666,13 @@ __device__ __noinline__ void close_rows(const LogprobParams& p, StreamBars& bars
 #pragma unroll 1
                     for (int i = n + lane; i < K; i += 32) best[i] = 0ull;
                     __syncwarp();
-                    if (push) {
 #pragma unroll 1
-                        for (int i = lane; i < K; i += 32) {
-                            const unsigned long long v = best[i];
+                    for (int i = lane; i < K; i += 32) {
+                        const unsigned long long v = best[i];
 #pragma unroll 1
-                            for (int o = 0; o < k; ++o) {
-                                const uint32_t to = mapa_u32(pushed + rank * K + i, static_cast<uint32_t>(o));
-                                asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to), "l"(v) : "memory");
-                            }
+                        for (int o = 0; o < k; ++o) {
+                            const uint32_t to = mapa_u32(pushed + rank * K + i, static_cast<uint32_t>(o));
+                            asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to), "l"(v) : "memory");
                         }
                     }
                 }
@@ -705,23 +708,20 @@ __device__ __noinline__ void close_rows(const LogprobParams& p, StreamBars& bars
                     for (int i = lane; i < min(n, K); i += 32) write(i, best[i]);
                 } else {
                     // The rank of each of this CTA's best among the cluster's: the sum of its places in the
-                    // lists, by a bisection of each, here if they were pushed before the exchange, else in
-                    // the other CTAs' memory.
+                    // lists, by a bisection of each.  (The lists were pushed here before the exchange: looked up
+                    // in the other CTAs' memory, 16 rows of 128256 took 27 us at K = 65, 21 pushed at K = 64.)
 #pragma unroll 1
                     for (int i = lane; i < K; i += 32) {
                         const unsigned long long item = best[i];
                         int r = 0;
 #pragma unroll 1
                         for (int o = 0; o < k; ++o) {
-                            const uint32_t list = push ? mapa_u32(pushed + o * K, static_cast<uint32_t>(rank))
-                                                       : mapa_u32(best, static_cast<uint32_t>(o));
-                            int a = 0, b = K;  // of list o: before a larger, from b on not
+                            const unsigned long long* list = pushed + o * K;
+                            int a = 0, b = K;  // before a larger, from b on not
 #pragma unroll 1
                             while (a < b) {
                                 const int mid = (a + b) / 2;
-                                unsigned long long v;
-                                asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(list + mid * 8) : "memory");
-                                if (v > item) a = mid + 1;
+                                if (list[mid] > item) a = mid + 1;
                                 else b = mid;
                             }
                             r += a;
@@ -875,13 +875,14 @@ cudaError_t launch_typed(LogprobParams prm, cudaStream_t stream) {
     const int64_t nblk = (((nb + kBlockVec - 1) / kBlockVec + s.k - 1) / s.k + 1) / Block<ES>::kPieces + 1;
     prm.max_stride = static_cast<int>((kBodyAt + nblk + 63) / 64 * 64);
     const size_t buffer = TOPK ? prm.max_stride * sizeof(typename Block<ES>::type) : 0;
-    // As many CTAs an SM as the registers allow, and a buffer for each closing warp, or fewer
+    // As many CTAs an SM as the registers allow (4096 x 32000, K = 5: three 74 us, two 78; K = 0
+    // three 48), and a buffer for each closing warp, or fewer
     // of the first, then of the second, where a ring of two stages would not fit.
-    const size_t lists = TOPK && s.k > 1 ? kClosers<TOPK> * kPushCap * 8 : 0;
+    const size_t lists = TOPK && s.k > 1 ? static_cast<size_t>(prm.top_k) * s.k * 8 : 0;
     const size_t fixed = 1024 + 256 + sizeof(StreamBars) + sizeof(StatExchange) + lists +
                          (TOPK ? kClosers<TOPK> * (sizeof(TopScratch) + kThreads * 4) : 0);
     int per_sm = 3;
-    s.buffers = TOPK ? kClosers<TOPK> : 2;
+    s.buffers = !TOPK ? 2 : s.k > 1 ? 1 : kClosers<TOPK>;  // a cluster has one row, rarely more
     auto room_for = [&] { return std::min<int64_t>(228 * 1024 / per_sm, 227 * 1024) - static_cast<int64_t>(fixed + buffer * s.buffers); };
     while (room_for() < 2 * static_cast<int64_t>(Sh::kStageBytes) && (per_sm > 1 || s.buffers > 2)) {
         if (per_sm > 1) {

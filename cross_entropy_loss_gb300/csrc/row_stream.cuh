@@ -11,6 +11,13 @@
 // tokens), so that neither the copies nor the sums wait for it.  That work is a chain of
 // latencies: several closing warps take rows in turn.
 //
+// HBM bounds long rows (8192 x 128256 bf16, sums and entropy: 307 us, 6.85 TB/s, what a copy
+// reaches).  Short ones are bounded by issue slots and the ends of rows: 9.2 instructions an
+// element and lane group, two thirds of the slots (4096 x 32000: 48 us, 5.4 TB/s).  Two or
+// three CTAs an SM hide one's row ends behind another's sums.  The closing warps' code has
+// to stay small: unrolled for speed (270 KB of it) it pushed the consumers' own out of the
+// instruction cache, 74 against 68 us at K = 5.
+//
 // Each thread keeps running sums (of 2^d and d 2^d) below a maximum that its warp shares:
 // one warp-wide reduction a chunk, and a rescaling only when the warp meets a new maximum
 // (rarer and rarer along a row); the warps' sets meet once a row.  The exponent is
@@ -40,7 +47,7 @@ struct Shape {
     static constexpr uint32_t kStageBytes = kChunk * 16;
 };
 constexpr int kMaxWarps = 16;
-constexpr int kMaxBuffers = 4;                            // rows between the consumers and the closing warps
+constexpr int kMaxBuffers = 3;                            // rows between the consumers and the closing warps
 constexpr int kStreamMaxStages = 12;
 constexpr int kStreamMaxCluster = 8;
 constexpr float kMinExp2 = -16384.f;  // 2^x is 0 from far above this; keeps products with it finite

@@ -12,6 +12,11 @@
 //
 // The statistics are (m, ln S), not their sum: at |m| past 2^24 ln n the sum has lost
 // ln S, and a row of n equal lowest values would get p = 1 instead of 1 / n.
+//
+// HBM bounds both.  Log probabilities and entropy: 8192 x 128256 bf16 670 us (6.3 TB/s read and
+// written), 4096 x 32000 87 us (6.0).  Distillation, K = 128: 8192 x 128256
+// 725 us (5.8 TB/s), 4096 x 32000, K = 64: 91 us.  No ring here: a thread's own 128 bytes in flight times
+// 1024 threads an SM are twice what covers the latency, and nothing is read twice.
 #include <algorithm>
 
 #include "common.cuh"
