@@ -108,6 +108,7 @@ __device__ __forceinline__ float float_of_short_key(uint32_t k) {
 struct TopScratch {
     alignas(16) unsigned long long list[kListCap];  // (key << 32) | ~column
     uint16_t sel[kSelCap];                          // the chosen blocks
+    float floor;                                    // a threshold on its way to top_list_again
 };
 
 __device__ __forceinline__ unsigned lanes_below() { return (1u << (threadIdx.x & 31)) - 1u; }
@@ -290,10 +291,6 @@ __device__ __forceinline__ uint32_t hit_bits(const uint32_t (&w)[WORDS], float f
     return bits;
 }
 template <int ES>
-__device__ __forceinline__ int bit_of_element(int e) {
-    return ES == 2 ? (e >> 1) | (e & 1) << 4 : e;
-}
-template <int ES>
 __device__ __forceinline__ int element_of_bit(int b) {
     return ES == 2 ? (b & 15) << 1 | b >> 4 : b;
 }
@@ -374,21 +371,140 @@ __device__ __noinline__ float blocks_floor(const typename Block<ES>::type* maxim
     return float_of_short_key<ES>(lo);
 }
 
+// The first elements equal to the floor onto the list, which has n, until it has K: the
+// blocks whose maximum reaches the floor one by one, an element a lane.  (A block whose
+// maximum is the floor has one at least, and there are fewer than K others.)
+template <int ES>
+__device__ __noinline__ int list_equal(const Slice s, const typename Block<ES>::type* maxima, int nblk, float floor, int K,
+                                       int n, TopScratch& t) {
+    constexpr int EPV = 16 / ES;
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int b0 = 0; b0 < nblk + 2 && n < K; b0 += 32) {
+        const int b = b0 + lane;
+        const bool may = b < nblk + 2 && Block<ES>::value(maxima[b == 0 ? 0 : b > nblk ? 1 : kBodyAt - 1 + b]) >= floor;
+#pragma unroll 1
+        for (unsigned m = __ballot_sync(0xffffffffu, may); m && n < K; m &= m - 1) {
+            const int id = b0 + __ffs(m) - 1, v0 = (id - 1) * Block<ES>::kVec;
+            const int64_t col = lane + (id == 0 ? 0 : id > nblk ? s.tail_col : s.col0 + static_cast<int64_t>(v0) * EPV);
+            const bool there = lane < (id == 0 ? s.h : id > nblk ? s.t : min(Block<ES>::kVec, s.nv - v0) * EPV);
+            float f = 0.f;
+            if (there) f = load_scalar<ES>(s.rowp + col * ES);
+            const bool hit = there && f == floor;
+            const unsigned hits = __ballot_sync(0xffffffffu, hit);
+            const int at = n + __popc(hits & lanes_below());
+            if (hit && at < K) t.list[at] = (static_cast<unsigned long long>(key_of(f)) << 32) | ~static_cast<uint32_t>(col);
+            n += __popc(hits);
+        }
+    }
+    __syncwarp();
+    return min(n, K);
+}
+
+// The elements at or above the floor (above: above it) of the chosen blocks and of the head
+// and tail onto the list.  Returns how many there are, which may be more than it takes.
+template <int ES>
+__device__ __forceinline__ int list_from(const Slice& s, float floor, bool above, int n_sel, TopScratch& t) {
+    using B = Block<ES>;
+    constexpr int EPV = 16 / ES;
+    const int lane = threadIdx.x & 31;
+    const uint4* body = reinterpret_cast<const uint4*>(s.body);
+    int n = 0;
+    // a 64-byte piece a lane and turn (re-read from L2)
+#pragma unroll 1
+    for (int i0 = 0; i0 < n_sel * B::kPieces; i0 += 32) {
+        const int i = i0 + lane, j = i / B::kPieces;
+        const bool there = j < n_sel;
+        const int vec = there ? (t.sel[j] - 1) * B::kVec + i % B::kPieces * kBlockVec : 0;
+        const int nv = there ? min(kBlockVec, s.nv - vec) : 0;
+        uint32_t w[4 * kBlockVec];
+#pragma unroll
+        for (int q = 0; q < kBlockVec; ++q) {
+            uint4 r = RowMath<ES>::pad();
+            if (q < nv) r = ld_global_v4(body + vec + q);
+            w[4 * q] = r.x, w[4 * q + 1] = r.y, w[4 * q + 2] = r.z, w[4 * q + 3] = r.w;
+        }
+        uint32_t hit = hit_bits<ES, false>(w, floor);
+        if (nv < kBlockVec) hit &= nv > 0 ? first_bits<ES>(nv * EPV) : 0u;
+        if (above) hit &= ~hit_bits<ES, true>(w, floor);
+        int at = __popc(hit);  // then the places before the lane's
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, at, off);
+            if (lane >= off) at += o;
+        }
+        const int end = n + __shfl_sync(0xffffffffu, at, 31);
+        at += n - __popc(hit);
+        n = end;
+#pragma unroll 1
+        for (; hit; hit &= hit - 1, ++at) {
+            const int e = element_of_bit<ES>(__ffs(hit) - 1);
+            const int64_t col = s.col0 + static_cast<int64_t>(vec) * EPV + e;
+            const float f = load_scalar<ES>(s.rowp + col * ES);  // it is in L1
+            if (at < kListCap)
+                t.list[at] = (static_cast<unsigned long long>(key_of(f)) << 32) | ~static_cast<uint32_t>(col);
+        }
+    }
+    if (s.h + s.t > 0) {
+        const int64_t col = lane < s.h ? lane : s.tail_col + (lane - s.h);
+        float f = kNegInf;
+        if (lane < s.h + s.t) f = load_scalar<ES>(s.rowp + col * ES);
+        const bool hit = lane < s.h + s.t && (above ? f > floor : f >= floor);
+        const unsigned m = __ballot_sync(0xffffffffu, hit);
+        const int at = n + __popc(m & lanes_below());
+        if (hit && at < kListCap)
+            t.list[at] = (static_cast<unsigned long long>(key_of(f)) << 32) | ~static_cast<uint32_t>(col);
+        n += __popc(m);
+    }
+    __syncwarp();
+    return n;
+}
+
+// So many blocks or threads at or above a threshold for K tokens will do.
+__device__ __forceinline__ int enough(int K) { return K + K / 16 + 4; }
+
+// The list of a row for which a threshold from the threads' maxima is no good.  t.floor is
+// that threshold; K elements reach it, if the slice has so many.
+template <int ES>
+__device__ __noinline__ int top_list_again(const Slice s, const typename Block<ES>::type* maxima, int K, TopScratch& t) {
+    const int nblk = (s.nv + Block<ES>::kVec - 1) / Block<ES>::kVec;
+    float floor = t.floor;
+    // Many blocks reach it because they are equal there (a mask that leaves fewer than K tokens): the
+    // elements above it first, then the first ones that are equal.
+    bool above = true;
+    int n_sel = blocks_again<ES>(maxima, nblk, floor, true, t.sel);
+    if (n_sel >= K) {  // not so: K is near the threads' number, or the logits are in no random order
+        floor = blocks_floor<ES>(maxima, nblk, floor, K, enough(K));
+        n_sel = blocks_again<ES>(maxima, nblk, floor, false, t.sel);
+        above = n_sel > kSelCap;
+        if (above) n_sel = blocks_again<ES>(maxima, nblk, floor, true, t.sel);
+    }
+#pragma unroll 1
+    while (n_sel <= kSelCap) {
+        const int n = list_from<ES>(s, floor, above, n_sel, t);
+        if (n <= kListCap) return above && n < K ? list_equal<ES>(s, maxima, nblk, floor, K, n, t) : n;
+        if (above) break;
+        // Too many elements in a few blocks: perhaps equal ones.
+        above = true;
+        n_sel = blocks_again<ES>(maxima, nblk, floor, true, t.sel);
+        if (n_sel >= K) break;
+    }
+    return top_list_exact<ES>(s, maxima, K, t);
+}
+
 // This CTA's largest elements of its slice onto t.list: at least the min(K, all) largest
 // ones, at most kListCap.  Returns how many.  maxima are the blocks' (kBodyAt the first of
 // the body; 0 and 1 the head's and tail's), thread_max the keys of the threads'.
 template <int ES>
 __device__ __noinline__ int top_list(const Slice s, const typename Block<ES>::type* maxima, const uint32_t* thread_max,
                                      int K, TopScratch& t) {
-    using B = Block<ES>;
     constexpr int PER = kThreads / 32;
     const int lane = threadIdx.x & 31;
-    const int nblk = (s.nv + B::kVec - 1) / B::kVec;
+    const int nblk = (s.nv + Block<ES>::kVec - 1) / Block<ES>::kVec;
     // A threshold that K threads' maxima, so K elements, reach: the K-th largest of the 256
     // thread maxima, or a little below it.  Of 64-byte pieces in random order about
     // -256 ln(1 - K / 256) are at or above it.
     float floor = kNegInf;
-    const int most = K + K / 16 + 4;  // so many reaching it will do
     if (min((s.nv + kBlockVec - 1) / kBlockVec, kThreads) >= K) {
         uint32_t v[PER], least = 0xffffffffu, hi = 0;
 #pragma unroll
@@ -408,114 +524,23 @@ __device__ __noinline__ int top_list(const Slice s, const typename Block<ES>::ty
             n = __reduce_add_sync(0xffffffffu, n);
             if (n >= K) {
                 lo = mid;
-                if (n <= most) break;
+                if (n <= enough(K)) break;
             } else {
                 hi = mid;
             }
         }
         floor = float_of_short_key<ES>(lo);
     }
-    int n_sel = blocks_from<ES>(maxima, nblk, floor, false, t.sel);
-    int need = kAll, strict = kAll;  // sel[strict ..]: blocks whose maximum is the floor, in order
-    if (__builtin_expect(n_sel > kSelCap, 0)) {
-        strict = blocks_again<ES>(maxima, nblk, floor, true, t.sel);
-        if (strict >= K) {  // the 256 maxima were no good guide: K near their number, or logits in no random order
-            floor = blocks_floor<ES>(maxima, nblk, floor, K, most);
-            n_sel = blocks_again<ES>(maxima, nblk, floor, false, t.sel);
-            strict = n_sel > kSelCap ? blocks_again<ES>(maxima, nblk, floor, true, t.sel) : kAll;
-        }
-        // Ties at the threshold (a mask that leaves fewer than K tokens): the blocks above
-        // it, and the first blocks that reach it, as many as can matter.
-        if (strict < K) {
-            need = K - strict;
-            int have = 0;
-#pragma unroll 1
-            for (int b0 = 0; b0 < nblk && have < need; b0 += 32) {
-                const bool tie = b0 + lane < nblk && B::value(maxima[kBodyAt + b0 + lane]) == floor;
-                const unsigned m = __ballot_sync(0xffffffffu, tie);
-                const int at = have + __popc(m & lanes_below());
-                if (tie && at < need) t.sel[strict + at] = static_cast<uint16_t>(1 + b0 + lane);
-                have += __popc(m);
-            }
-            n_sel = strict + min(have, need);
-            __syncwarp();
+    if (floor > kNegInf) {
+        const int n_sel = blocks_from<ES>(maxima, nblk, floor, false, t.sel);
+        if (n_sel <= kSelCap) {
+            const int n = list_from<ES>(s, floor, false, n_sel, t);
+            if (n <= kListCap) return n;
         }
     }
-    if (n_sel <= kSelCap) {
-        // A 64-byte piece a lane and turn (re-read from L2); its elements at or above the threshold.
-        constexpr int EPV = 16 / ES;
-        const uint4* body = reinterpret_cast<const uint4*>(s.body);
-        int n = 0, ties = 0;
-#pragma unroll 1
-        for (int i0 = 0; i0 < n_sel * B::kPieces; i0 += 32) {
-            const int i = i0 + lane, j = i / B::kPieces;
-            const bool there = j < n_sel;
-            const int vec = there ? (t.sel[j] - 1) * B::kVec + i % B::kPieces * kBlockVec : 0;
-            const int nv = there ? min(kBlockVec, s.nv - vec) : 0;
-            uint32_t w[4 * kBlockVec];
-#pragma unroll
-            for (int q = 0; q < kBlockVec; ++q) {
-                uint4 r = RowMath<ES>::pad();
-                if (q < nv) r = ld_global_v4(body + vec + q);
-                w[4 * q] = r.x, w[4 * q + 1] = r.y, w[4 * q + 2] = r.z, w[4 * q + 3] = r.w;
-            }
-            uint32_t hit = hit_bits<ES, false>(w, floor);
-            if (nv < kBlockVec) hit &= nv > 0 ? first_bits<ES>(nv * EPV) : 0u;
-            if (__builtin_expect(strict != kAll, 0)) {
-                // an equal one counts only if fewer than `need` come before it: those of its block, and all
-                // those of the tied blocks before, which are in order
-                const uint32_t tie = hit & hit_bits<ES, true>(w, floor);
-                const int mine = __popc(tie);
-                const bool tied = j >= strict;
-                int sum = tied ? mine : 0;
-#pragma unroll
-                for (int off = 1; off < 32; off <<= 1) {
-                    const int o = __shfl_up_sync(0xffffffffu, sum, off);
-                    if (lane >= off) sum += o;
-                }
-                int before = tied ? ties + sum - mine : 0;
-                if (B::kPieces > 1) {
-                    const int o = __shfl_up_sync(0xffffffffu, mine, 1);
-                    if (!tied && i % B::kPieces) before = o;
-                }
-                ties += __shfl_sync(0xffffffffu, sum, 31);
-#pragma unroll 1
-                for (int e = 0; e < 64 / ES; ++e)
-                    if (tie >> bit_of_element<ES>(e) & 1u && before++ >= need) hit &= ~(1u << bit_of_element<ES>(e));
-            }
-            int at = __popc(hit);  // then the places before the lane's
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int o = __shfl_up_sync(0xffffffffu, at, off);
-                if (lane >= off) at += o;
-            }
-            const int end = n + __shfl_sync(0xffffffffu, at, 31);
-            at += n - __popc(hit);
-            n = end;
-#pragma unroll 1
-            for (; hit; hit &= hit - 1, ++at) {
-                const int e = element_of_bit<ES>(__ffs(hit) - 1);
-                const int64_t col = s.col0 + static_cast<int64_t>(vec) * EPV + e;
-                const float f = load_scalar<ES>(s.rowp + col * ES);  // it is in L1
-                if (at < kListCap)
-                    t.list[at] = (static_cast<unsigned long long>(key_of(f)) << 32) | ~static_cast<uint32_t>(col);
-            }
-        }
-        if (s.h + s.t > 0) {
-            const int64_t col = lane < s.h ? lane : s.tail_col + (lane - s.h);
-            float f = kNegInf;
-            if (lane < s.h + s.t) f = load_scalar<ES>(s.rowp + col * ES);
-            const bool hit = lane < s.h + s.t && f >= floor;
-            const unsigned m = __ballot_sync(0xffffffffu, hit);
-            const int at = n + __popc(m & lanes_below());
-            if (hit && at < kListCap)
-                t.list[at] = (static_cast<unsigned long long>(key_of(f)) << 32) | ~static_cast<uint32_t>(col);
-            n += __popc(m);
-        }
-        __syncwarp();
-        if (n <= kListCap) return n;
-    }
-    return top_list_exact<ES>(s, maxima, K, t);
+    if (lane == 0) t.floor = floor;
+    __syncwarp();
+    return top_list_again<ES>(s, maxima, K, t);
 }
 
 // The list in descending order, R items a lane: a bitonic sort in registers, lane l
