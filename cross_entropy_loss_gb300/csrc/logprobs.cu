@@ -611,6 +611,43 @@ __device__ __forceinline__ void top_ordered(unsigned long long* list, int n) {
     __syncwarp();
 }
 
+// A cluster's lists, out of line: rows that have a CTA to themselves do not pay for the code.
+//
+// This CTA's n largest, in order, into every CTA's `pushed`, which has K places for each.
+__device__ __noinline__ void push_list(unsigned long long* best, int n, int K, unsigned long long* pushed, int rank, int k) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int i = n + lane; i < K; i += 32) best[i] = 0ull;
+    __syncwarp();
+#pragma unroll 1
+    for (int i = lane; i < K; i += 32) {
+        const unsigned long long v = best[i];
+#pragma unroll 1
+        for (int o = 0; o < k; ++o) {
+            const uint32_t to = mapa_u32(pushed + rank * K + i, static_cast<uint32_t>(o));
+            asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to), "l"(v) : "memory");
+        }
+    }
+}
+// An item's rank among the cluster's: the sum of its places in the lists, by a bisection of
+// each.  (Looked up in the other CTAs' memory instead of here, 16 rows of 128256 took 27 us at
+// K = 65, 23 this way.)
+__device__ __noinline__ int pushed_rank(const unsigned long long* pushed, int K, int k, unsigned long long item) {
+    int r = 0;
+#pragma unroll 1
+    for (int o = 0; o < k; ++o, pushed += K) {
+        int a = 0, b = K;  // before a larger, from b on not
+#pragma unroll 1
+        while (a < b) {
+            const int mid = (a + b) / 2;
+            if (pushed[mid] > item) a = mid + 1;
+            else b = mid;
+        }
+        r += a;
+    }
+    return r;
+}
+
 template <bool TOPK>
 constexpr int kLogprobThreads = Sh::kFirstCloser + 32 * kClosers<TOPK>;
 
@@ -687,20 +724,7 @@ __device__ __noinline__ void close_rows(const LogprobParams& p, StreamBars& bars
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars.row_empty[buf]);
                 top_ordered(best, n);
-                if (k > 1) {
-#pragma unroll 1
-                    for (int i = n + lane; i < K; i += 32) best[i] = 0ull;
-                    __syncwarp();
-#pragma unroll 1
-                    for (int i = lane; i < K; i += 32) {
-                        const unsigned long long v = best[i];
-#pragma unroll 1
-                        for (int o = 0; o < k; ++o) {
-                            const uint32_t to = mapa_u32(pushed + rank * K + i, static_cast<uint32_t>(o));
-                            asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to), "l"(v) : "memory");
-                        }
-                    }
-                }
+                if (k > 1) push_list(best, n, K, pushed, rank, k);
             }
             if (k > 1) {
                 stat_send(st, ex, buf, use, k, rank);
@@ -728,31 +752,13 @@ __device__ __noinline__ void close_rows(const LogprobParams& p, StreamBars& bars
                     olp[r] = empty ? kNegInf : (float_of_key(static_cast<uint32_t>(item >> 32)) - st.m) * p.inv_t - ln_s;
                     oid[r] = static_cast<int32_t>(~static_cast<uint32_t>(item));
                 };
-                if (k == 1) {
 #pragma unroll 1
-                    for (int i = lane; i < min(n, K); i += 32) write(i, best[i]);
-                } else {
-                    // The rank of each of this CTA's best among the cluster's: the sum of its places in the
-                    // lists, by a bisection of each.  (The lists were pushed here before the exchange: looked up
-                    // in the other CTAs' memory, 16 rows of 128256 took 27 us at K = 65, 21 pushed at K = 64.)
-#pragma unroll 1
-                    for (int i = lane; i < K; i += 32) {
-                        const unsigned long long item = best[i];
-                        int r = 0;
-#pragma unroll 1
-                        for (int o = 0; o < k; ++o) {
-                            const unsigned long long* list = pushed + o * K;
-                            int a = 0, b = K;  // before a larger, from b on not
-#pragma unroll 1
-                            while (a < b) {
-                                const int mid = (a + b) / 2;
-                                if (list[mid] > item) a = mid + 1;
-                                else b = mid;
-                            }
-                            r += a;
-                        }
-                        if (item && r < K) write(r, item);
-                    }
+                for (int i = lane; i < min(n, K); i += 32) {
+                    const unsigned long long item = best[i];
+                    const int r = k > 1 ? pushed_rank(pushed, K, k, item) : i;
+                    if (r < K) write(r, item);
+                }
+                if (k > 1) {  // the lists here may be written over
                     __syncwarp();
                     if (lane < k) remote_arrive(&bars.peers_done[buf], static_cast<uint32_t>(lane));
                 }
