@@ -22,10 +22,11 @@
 // sums and lists through distributed shared memory, and ranks every CTA's K candidates
 // against the others'.
 //
-// Measured, with entropy, bf16 unless said: 8192 x 128256, K = 0, 20, 128: 307, 358, 407 us
-// (6.85, 5.9, 5.2 TB/s); 4096 x 32000, K = 0, 5, 128: 48, 68, 122; 2048 x 128256 fp32, K = 64:
-// 188 (5.6 TB/s); 1 x 128256, K = 0, 20: 6.6 and 13.9.  With top tokens a row's end is some
-// 10000 cycles alone, three times that beside nine warps that sum: short rows pay for it.
+// Measured, with entropy, bf16 unless said: 8192 x 128256, K = 0, 20, 128: 307, 357, 404 us
+// (6.85, 5.9, 5.2 TB/s); 4096 x 32000, K = 0, 5: 48.5 and 66; 2048 x 128256 fp32, K = 64: 188 (5.6
+// TB/s); 1 x 128256, K = 0, 20: 6.6 and 14; 64 x 128256 under a mask, K = 20: 22.  HBM bounds the
+// long rows.  With top tokens a row's end is some 10000 cycles alone, three times that
+// beside warps that sum: short rows and few rows pay for it.
 #include <algorithm>
 #include <map>
 #include <mutex>
