@@ -914,7 +914,9 @@ cudaError_t launch_typed(LogprobParams prm, cudaStream_t stream) {
     const size_t fixed = 1024 + 256 + sizeof(StreamBars) + sizeof(StatExchange) + lists +
                          (TOPK ? kClosers<TOPK> * (sizeof(TopScratch) + kThreads * 4) : 0);
     int per_sm = 3;
-    s.buffers = !TOPK ? 2 : s.k > 1 ? 1 : kClosers<TOPK>;  // a cluster has one row, rarely more
+    // One buffer where every CTA has one row: with three, 320 rows of 128256 fp32 left room for two CTAs
+    // an SM, so for two rounds (K = 20: 60 us, 46 with one).
+    s.buffers = !TOPK ? 2 : s.N * s.k <= static_cast<int64_t>(sms) * per_sm ? 1 : kClosers<TOPK>;
     auto room_for = [&] { return std::min<int64_t>(228 * 1024 / per_sm, 227 * 1024) - static_cast<int64_t>(fixed + buffer * s.buffers); };
     while (room_for() < 2 * static_cast<int64_t>(Sh::kStageBytes) && (per_sm > 1 || s.buffers > 2)) {
         if (per_sm > 1) {
