@@ -25,7 +25,8 @@
 // and the row's end corrects for its rounding (max c + r, which an FMA gives exactly).
 // The rounding of r is an exponent of 64 at most while |max c| < 2^30.  Above that two
 // different float32 logits are at least 2^6 apart in the exponent, so an element that is
-// not the maximum counts nothing and no exponent is formed.
+// not the maximum counts nothing and no exponent is formed.  With two temperatures each
+// sum goes by its own scale: at one the logits may be that far apart, at the other not.
 #pragma once
 
 #include <float.h>
@@ -429,6 +430,7 @@ struct RunStat {
 
     __device__ __forceinline__ explicit RunStat(const ExpScale& x) : r(FLT_MAX * x.c), r2(FLT_MAX * x.c2) {}
 
+    // one of the scales is far (each sum goes by its own)
     __device__ __forceinline__ bool far(const ExpScale& x) const { return far(m, x.c) || (TWO && far(m, x.c2)); }
     static __device__ __forceinline__ bool far(float m, float c) { return fabsf(m) * c >= kFarExp && fabsf(m) <= FLT_MAX; }
 
@@ -461,9 +463,7 @@ struct RunStat {
         if (mn > m) raise(mn, x);
         if (v == kNegInf) return;
         if (__builtin_expect(far(x), 0)) {
-            const float one = v == m ? 1.f : v == v ? 0.f : v;
-            s += one;
-            if (TWO) s2 += one;
+            add_far(v, far(m, x.c), TWO && far(m, x.c2), x);
             return;
         }
         const float d = max_nan(fmaf(v, x.c, r), kMinExp2);
@@ -479,7 +479,7 @@ struct RunStat {
         const float mn = fmaxf(m, warp_max_redux(bmax));
         if (mn > m) raise(mn, x);
         if (__builtin_expect(far(x), 0)) {
-            add_far<ES, NV>(v);
+            add_vecs_far<ES, NV>(v, x);
             return bmax;
         }
         const f32x2_t C = f2_pack(x.c, x.c), R = f2_pack(r, r), C2 = f2_pack(x.c2, x.c2), R2 = f2_pack(r2, r2);
@@ -522,30 +522,40 @@ struct RunStat {
         }
         return bmax;
     }
-    // the elements equal to a far maximum
+    // An element's term where its scale is far (1 if it is the maximum) or not.
+    __device__ __forceinline__ float term(float v, bool is_far, float c, float rc) const {
+        if (is_far) return v == m ? 1.f : v == v ? 0.f : v;
+        return ex2(max_nan(fmaf(v, c, rc), kMinExp2));
+    }
+    // An element where a scale is far: the entropy, which goes with the first, gets nothing
+    // from an element at the maximum.
+    __device__ __forceinline__ void add_far(float v, bool one, bool two, const ExpScale& x) {
+        static_assert(!(ENT && TWO), "a first scale that is not far would need its part of the entropy");
+        s += term(v, !TWO || one, x.c, r);
+        if (TWO) s2 += term(v, two, x.c2, r2);
+    }
     template <int ES, int NV>
-    __device__ __forceinline__ void add_far(const uint4 (&v)[NV]) {
-        float n = 0.f;
+    __device__ __forceinline__ void add_vecs_far(const uint4 (&v)[NV], const ExpScale& x) {
+        const bool one = far(m, x.c), two = TWO && far(m, x.c2);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
 #pragma unroll
             for (int j = 0; j < (ES == 2 ? 4 : 2); ++j) {
                 float lo, hi;
                 f2_unpack(vec_pair<ES>(v[i], j), lo, hi);
-                n += lo == m ? 1.f : lo == lo ? 0.f : lo;
-                n += hi == m ? 1.f : hi == hi ? 0.f : hi;
+                add_far(lo, one, two, x);
+                add_far(hi, one, two, x);
             }
         }
-        s += n;
-        if (TWO) s2 += n;
     }
     // The sums as those of exponents (x - m) c, for an r that is m c exactly.
     __device__ __forceinline__ void correct(const ExpScale& x) {
-        if (far(x)) return;
-        const float e = fmaf(m, x.c, r), f = ex2(-e);
-        if (ENT) a = f * fmaf(-e, s, a);
-        s *= f;
-        if (TWO) s2 *= ex2(-fmaf(m, x.c2, r2));
+        if (!far(m, x.c)) {
+            const float e = fmaf(m, x.c, r), f = ex2(-e);
+            if (ENT) a = f * fmaf(-e, s, a);
+            s *= f;
+        }
+        if (TWO && !far(m, x.c2)) s2 *= ex2(-fmaf(m, x.c2, r2));
     }
 };
 

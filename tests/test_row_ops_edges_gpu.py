@@ -1,0 +1,93 @@
+"""Ends of the ranges that the log-probability and distillation calls take: temperatures from
+2^-19 to 2^19, logits far from 0, rows of millions of elements, outputs left out, bad ids; bounds
+as in row_ops_ref.
+
+Gradients get one absolute term more than there: an exponential below the least normal float,
+2^-126, is 0, and the gradient has it times the weights over the temperature."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import row_ops_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+LEAST = 2.0 ** -126
+TEMPERATURES = (2.0 ** -19, 2.0 ** -10, 2.0 ** 10, 2.0 ** 19)
+
+
+def _labels(N, V, seed):
+    return torch.from_numpy(np.random.default_rng(seed + 1000).integers(0, V, N))
+
+
+def _far_rows(V, dtype):
+    """Logits at which the exponents of one temperature, of both or of none are far apart."""
+    base = ref.make_logits(7, V, F32, seed=V)
+    x = torch.empty(7, V, dtype=dtype)
+    x[0] = base[0]
+    x[1] = base[1] + 800
+    x[2] = base[2] - 5000
+    x[3] = base[3] * 1e-3 + 20
+    x[4] = base[4] * 1e4 + 2e9
+    x[5] = base[5] * 1e8
+    x[6] = base[6] * 100 - 3e9
+    return x
+
+
+def _close_gradient(got, want, size, flushed):
+    tol = ref.HALF_STEP[got.dtype] * want.abs() * 1.0001 + 4 * ref.EPS * size + flushed + 1e-37
+    ref.close(got, want, tol, "dlogits")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("V", [1201, 100003])
+@pytest.mark.parametrize("T", TEMPERATURES)
+@pytest.mark.parametrize("ce_w", [0.5, 0.0])
+def test_distillation_at_far_exponents(cuda_lib, dtype, V, T, ce_w):
+    """The cross-entropy part has temperature 1 whatever T is."""
+    ce = cuda_lib
+    x = _far_rows(V, dtype)
+    N, K, kd_w = x.shape[0], 8, 0.8
+    r = np.random.default_rng(V)
+    z = (x.double() + torch.from_numpy(r.standard_normal((N, V)))) / T
+    top = z.topk(K, dim=1)
+    ids, t = top.indices.int(), (top.values - z.logsumexp(1, keepdim=True)).float()
+    y = _labels(N, V, 3)
+    y[::2] = x.float().argmax(1)[::2]
+    want = ref.distill(x, y, ids, t, T, ce_w, kd_w, True)
+    flushed = LEAST * (abs(ce_w) + kd_w / T) / N
+    how = dict(ce_weight=ce_w, kd_weight=kd_w, temperature=T)
+    xd = ref.to_gpu(x)
+    a = ce.foak_distill_fwd_bwd(xd.clone(), y.cuda(), ids.cuda(), t.cuda(), want_rows=True, **how)
+    b = ce.foak_distill_forward(xd, y.cuda(), ids.cuda(), t.cuda(), want_rows=True, **how)
+    b["dlogits"], _ = ce.foak_distill_backward(xd, y.cuda(), ids.cuda(), t.cuda(), b["stats"], **how)
+    for out in (a, b):
+        ref.close(out["row_ce"], want["row_ce"], 2 * ref.EPS * want["ce_size"] + 1e-30, "row_ce")
+        ref.close(out["row_kd"], want["row_kd"], 2 * ref.EPS * want["kd_size"] + 1e-30, "row_kd")
+        _close_gradient(out["dlogits"], want["dlogits"], want["grad_size"], flushed)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("V", [1201, 100003])
+@pytest.mark.parametrize("T", TEMPERATURES)
+def test_log_probabilities_at_far_exponents(cuda_lib, dtype, V, T):
+    ce = cuda_lib
+    x = _far_rows(V, dtype)
+    N, K = x.shape[0], 9
+    y = _labels(N, V, 4)
+    y[::2] = x.float().argmax(1)[::2]
+    want = ref.logprobs(x, y, K, T)
+    xd = ref.to_gpu(x)
+    out = ce.foak_logprobs_forward(xd, y.cuda(), top_k=K, temperature=T)
+    for k in ("lse", "logp", "top_logprobs"):
+        ref.close(out[k], want[k], ref.value_tol(want[k]), k)
+    ref.close(out["entropy"], want["entropy"], ref.entropy_tol(V), "entropy")
+    assert torch.equal(out["top_ids"].cpu().long(), want["top_ids"])
+    gl, gh = torch.linspace(-1, 1, N), torch.linspace(0.5, -0.7, N)
+    dx, _ = ce.foak_logprobs_backward(xd, y.cuda(), out["stats"], gl.cuda(), out["entropy"], gh.cuda(), temperature=T)
+    g, size = ref.logprobs_grad(want, y, T, gl, gh)
+    # p (ln p + H) of a flushed p has a factor up to 126 ln 2 + ln V more
+    _close_gradient(dx, g, size, 101 * LEAST / T)
