@@ -91,3 +91,34 @@ def test_log_probabilities_at_far_exponents(cuda_lib, dtype, V, T):
     g, size = ref.logprobs_grad(want, y, T, gl, gh)
     # p (ln p + H) of a flushed p has a factor up to 126 ln 2 + ln V more
     _close_gradient(dx, g, size, 101 * LEAST / T)
+
+
+@pytest.mark.parametrize("N,V", [(40, 900), (3, 70001), (700, 1031)])
+def test_a_bad_teacher_id_is_reported_by_every_call(cuda_lib, N, V):
+    """By the backward call too, whichever rows it is in; the next call's word is clean again."""
+    ce = cuda_lib
+    x = ref.make_logits(N, V, F32, seed=16)
+    r = np.random.default_rng(1)
+    ids = torch.from_numpy(np.stack([r.permutation(V)[:5] for _ in range(N)])).int()
+    t = torch.log_softmax(torch.from_numpy(r.standard_normal((N, 5))), 1).float()
+    xd, td = ref.to_gpu(x), t.cuda()
+    for row in (0, N // 2, N - 1):
+        bad = ids.clone()
+        bad[row, 2] = V + 3 * row
+        want = ref.distill(x, None, bad, t, 1.0, 0.0, 1.0, True)
+        f = ce.foak_distill_forward(xd, None, bad.cuda(), td)
+        dx, err = ce.foak_distill_backward(xd, None, bad.cuda(), td, f["stats"])
+        both = ce.foak_distill_fwd_bwd(xd.clone(), None, bad.cuda(), td)
+        assert int(f["err"]) == int(both["err"]) == int(err) == ce.FOAK_ERRBIT_LABEL_RANGE
+        ref.grad_close(dx, want["dlogits"], want["grad_size"])
+        # not of a row that does not count
+        y = torch.zeros(N, dtype=torch.int64)
+        y[row] = -100
+        f = ce.foak_distill_forward(xd, y.cuda(), bad.cuda(), td)
+        _, err = ce.foak_distill_backward(xd, y.cuda(), bad.cuda(), td, f["stats"])
+        assert int(f["err"]) == int(err) == 0
+        y[0 if row else 1] = V
+        _, err = ce.foak_distill_backward(xd, y.cuda(), bad.cuda(), td, f["stats"])
+        assert int(err) == ce.FOAK_ERRBIT_LABEL_RANGE
+    _, err = ce.foak_distill_backward(xd, None, ids.cuda(), td, f["stats"])
+    assert int(err) == 0
