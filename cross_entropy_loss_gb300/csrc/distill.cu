@@ -71,6 +71,7 @@ __global__ void __launch_bounds__(kDistillThreads<NT>, NT == 256 ? 2 : 1) distil
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ StreamBars bars;
     __shared__ StatExchange ex;
+    __shared__ LongSums aside;
     __shared__ TeacherRow teacher[kClosers];
     __shared__ SweepFactors factors[kMaxBuffers];
     __shared__ float total[kMaxBuffers];  // of the teacher's row
@@ -129,11 +130,18 @@ __global__ void __launch_bounds__(kDistillThreads<NT>, NT == 256 ? 2 : 1) distil
             }
             row_begin(p.src, bars, rp, pos);
             RunStat<false, TWO> st(sc);
-            for (int c0 = 0; c0 < s.nv; c0 += Shape<NT>::kChunk) {
-                const int nl = min(Shape<NT>::kChunk, s.nv - c0);
-                uint4 v[kBlockVec];
-                stream_chunk<NT>(p.src, bars, smem, pos, [&](const unsigned char* stage) { load_strided<ES, NT>(stage, nl, v); });
-                st.template add_vecs<ES>(v, sc);
+            for (int run = 0; run < s.nv; run += kRunVec<NT>) {
+                if (run > 0) {
+                    stat_put_aside<false, TWO>(st, aside, run == kRunVec<NT>, sc);
+                    st.restart();
+                }
+                const int end = min(s.nv, run + kRunVec<NT>);
+                for (int c0 = run; c0 < end; c0 += Shape<NT>::kChunk) {
+                    const int nl = min(Shape<NT>::kChunk, s.nv - c0);
+                    uint4 v[kBlockVec];
+                    stream_chunk<NT>(p.src, bars, smem, pos, [&](const unsigned char* stage) { load_strided<ES, NT>(stage, nl, v); });
+                    st.template add_vecs<ES>(v, sc);
+                }
             }
             // the head and tail scalars, one a lane of the first warp; kept for the gradient
             const int n_edge = s.h + s.t;
@@ -144,7 +152,8 @@ __global__ void __launch_bounds__(kDistillThreads<NT>, NT == 256 ? 2 : 1) distil
                 st.add(edge, sc);
             }
             const int buf = rp.buf;
-            stat_publish(st, ex, buf);
+            if (s.nv <= kRunVec<NT>) stat_publish(st, ex, buf);
+            else stat_publish_long(st, aside, ex, buf, sc);
             row_end(bars, buf);
             if constexpr (GRAD) {
                 if (!pos.aborted && !stream_wait(bars, &bars.row_ready[buf], rp.use & 1u, p.src.wait_ns))
@@ -344,7 +353,8 @@ cudaError_t launch_typed(DistillParams prm, int per_sm, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     StreamSrc& s = prm.src;
     s.buffers = kClosers;
-    const size_t fixed = 1024 + 512 + sizeof(StreamBars) + sizeof(StatExchange) + kClosers * sizeof(TeacherRow);
+    const size_t fixed = 1024 + 512 + sizeof(StreamBars) + sizeof(StatExchange) + sizeof(LongSums) +
+                         kClosers * sizeof(TeacherRow);
     const size_t room = std::min<size_t>((228 * 1024) / per_sm, 227 * 1024) - fixed;
     s.stages = static_cast<int>(std::min<size_t>(kStreamMaxStages, room / Shape<NT>::kStageBytes));
     const size_t smem = static_cast<size_t>(s.stages) * Shape<NT>::kStageBytes;

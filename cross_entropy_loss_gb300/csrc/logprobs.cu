@@ -42,6 +42,7 @@ constexpr int kSelCap = 320;    // blocks they are taken from
 constexpr int kAll = 0x7fffffff;
 constexpr int kThreads = 256;   // consumers
 using Sh = Shape<kThreads>;
+static_assert(kTopKMaxVocab <= static_cast<int64_t>(kRunVec<kThreads>) * 4, "rows with top tokens are one run of chunks");
 constexpr int kBodyAt = 8;      // place of the first body block's maximum; before it the head's and the tail's
 // Closing warps of a CTA.  The work on a row's top tokens is a chain of 10000 cycles or more,
 // so three take rows in turn (8192 x 128256, K = 128: two with two CTAs an SM 464 us, three
@@ -783,6 +784,7 @@ __global__ void __launch_bounds__(kLogprobThreads<TOPK>, 3) logprobs_kernel(cons
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ StreamBars bars;
     __shared__ StatExchange ex;
+    __shared__ LongSums aside;  // not with top tokens: their rows are one run
     __shared__ TopScratch top[TOPK ? kClosers<TOPK> : 1];
     __shared__ uint32_t thread_max[TOPK ? kClosers<TOPK> : 1][kThreads];  // key of the largest of a thread's blocks, 0: it has none
     using MaxT = typename Block<ES>::type;
@@ -832,20 +834,34 @@ __global__ void __launch_bounds__(kLogprobThreads<TOPK>, 3) logprobs_kernel(cons
             MaxT* rm = maxima + buf * p.max_stride;
             RunStat<ENT, false> st(p.scale);
             float most = kNegInf;  // of the thread's blocks
+            auto chunks = [&](int from, int to) {
 #pragma unroll 1
-            for (int c0 = 0; c0 < s.nv; c0 += Sh::kChunk) {
-                const int nl = min(Sh::kChunk, s.nv - c0);
-                uint4 v[kBlockVec];
-                stream_chunk<kThreads>(p.src, bars, ring, pos, [&](const unsigned char* stage) {
-                    if constexpr (TOPK) load_block<ES, kThreads>(stage, nl, v);
-                    else load_strided<ES, kThreads>(stage, nl, v);
-                });
-                const float mine = st.template add_vecs<ES>(v, p.scale);
-                if (TOPK) {
-                    most = fmaxf(most, mine);
-                    const float both = Block<ES>::kPieces > 1 ? fmaxf(mine, __shfl_xor_sync(0xffffffffu, mine, 1)) : mine;
-                    if (tid * kBlockVec < nl && tid % Block<ES>::kPieces == 0)
-                        rm[kBodyAt + (c0 / kBlockVec + tid) / Block<ES>::kPieces] = static_cast<MaxT>(Block<ES>::pack(both));
+                for (int c0 = from; c0 < to; c0 += Sh::kChunk) {
+                    const int nl = min(Sh::kChunk, s.nv - c0);
+                    uint4 v[kBlockVec];
+                    stream_chunk<kThreads>(p.src, bars, ring, pos, [&](const unsigned char* stage) {
+                        if constexpr (TOPK) load_block<ES, kThreads>(stage, nl, v);
+                        else load_strided<ES, kThreads>(stage, nl, v);
+                    });
+                    const float mine = st.template add_vecs<ES>(v, p.scale);
+                    if (TOPK) {
+                        most = fmaxf(most, mine);
+                        const float both = Block<ES>::kPieces > 1 ? fmaxf(mine, __shfl_xor_sync(0xffffffffu, mine, 1)) : mine;
+                        if (tid * kBlockVec < nl && tid % Block<ES>::kPieces == 0)
+                            rm[kBodyAt + (c0 / kBlockVec + tid) / Block<ES>::kPieces] = static_cast<MaxT>(Block<ES>::pack(both));
+                    }
+                }
+            };
+            if constexpr (TOPK) {
+                chunks(0, s.nv);
+            } else {
+#pragma unroll 1
+                for (int run = 0; run < s.nv; run += kRunVec<kThreads>) {
+                    if (run > 0) {
+                        stat_put_aside<ENT, false>(st, aside, run == kRunVec<kThreads>, p.scale);
+                        st.restart();
+                    }
+                    chunks(run, min(s.nv, run + kRunVec<kThreads>));
                 }
             }
             if (s.h + s.t > 0 && warp == 0) {  // the head's and the tail's scalars, one a lane
@@ -863,7 +879,8 @@ __global__ void __launch_bounds__(kLogprobThreads<TOPK>, 3) logprobs_kernel(cons
                 rm[0] = rm[1] = Block<ES>::kNone;
             }
             if (TOPK) thread_max[buf][tid] = tid * kBlockVec < s.nv ? short_key<ES>(most) : 0u;
-            stat_publish(st, ex, buf);
+            if (TOPK || s.nv <= kRunVec<kThreads>) stat_publish(st, ex, buf);
+            else stat_publish_long(st, aside, ex, buf, p.scale);
             row_end(bars, buf);
             rp.next(p.src);
         }
@@ -912,7 +929,7 @@ cudaError_t launch_typed(LogprobParams prm, cudaStream_t stream) {
     // of the first, then of the second, where a ring of two stages would not fit.
     const size_t lists = TOPK && s.k > 1 ? static_cast<size_t>(prm.top_k) * s.k * 8 : 0;
     const size_t fixed = 1024 + 256 + sizeof(StreamBars) + sizeof(StatExchange) + lists +
-                         (TOPK ? kClosers<TOPK> * (sizeof(TopScratch) + kThreads * 4) : 0);
+                         (TOPK ? kClosers<TOPK> * (sizeof(TopScratch) + kThreads * 4) : sizeof(LongSums));
     int per_sm = 3;
     // One buffer where every CTA has one row: with three, 320 rows of 128256 fp32 left room for two CTAs
     // an SM, so for two rounds (K = 20: 60 us, 46 with one).

@@ -457,6 +457,8 @@ struct RunStat {
         r = minus_product(m, x.c);
         if (TWO) r2 = minus_product(m, x.c2);
     }
+    // Sums of 0 below the same maximum.
+    __device__ __forceinline__ void restart() { s = a = s2 = 0.f; }
     // One element a lane (-inf: none), by the whole warp.
     __device__ __forceinline__ void add(float v, const ExpScale& x) {
         const float mn = fmaxf(m, warp_max_redux(v));
@@ -565,6 +567,54 @@ struct StatExchange {
     float4 cta[kMaxBuffers][2][kStreamMaxCluster];  // the cluster's CTAs' sets, by buffer and parity of its use
 };
 
+// The sums of a long row's earlier runs of kRunChunks chunks, by consumer warp: each as two
+// floats (a sum and what its additions lost), below the maximum m.  A thread adds once a chunk, and
+// a chain of float additions of equal numbers rounds the same way for long: without the
+// runs, 134 million fp32 logits of two values (4096 chunks a CTA) left ln S off by 3.2e-5, 2^31
+// bf16 ones by 9.5e-5.
+constexpr int kRunChunks = 64;
+struct LongSums {
+    float m[kMaxWarps];
+    float2 s[kMaxWarps], a[kMaxWarps], s2[kMaxWarps];
+};
+template <int NT>
+constexpr int kRunVec = kRunChunks * Shape<NT>::kChunk;  // a run's vectors
+
+// x + y = sum + error exactly
+__device__ __forceinline__ void add_exactly(float2& x, float y) {
+    const float sum = __fadd_rn(x.x, y), b = __fsub_rn(sum, x.x);
+    x.y += __fadd_rn(__fsub_rn(x.x, __fsub_rn(sum, b)), __fsub_rn(y, b));
+    x.x = sum;
+}
+// The warp's sums since the last time put with the earlier ones (out of line: few rows are so long).
+template <bool ENT, bool TWO>
+__device__ __noinline__ void stat_put_aside(RunStat<ENT, TWO> st, LongSums& l, bool first, const ExpScale x) {
+    const int warp = threadIdx.x >> 5;
+    st.s = warp_sum(st.s);
+    if (ENT) st.a = warp_sum(st.a);
+    if (TWO) st.s2 = warp_sum(st.s2);
+    if ((threadIdx.x & 31) == 0) {
+        RunStat<ENT, TWO> sum(x), lost(x);
+        if (!first) {
+            sum.set(make_float4(l.m[warp], l.s[warp].x, l.a[warp].x, l.s2[warp].x), x);
+            lost.set(make_float4(l.m[warp], l.s[warp].y, l.a[warp].y, l.s2[warp].y), x);
+        }
+        sum.raise(st.m, x);
+        lost.raise(st.m, x);
+        l.m[warp] = st.m;
+        float2 t = make_float2(sum.s, lost.s);
+        add_exactly(t, st.s);
+        l.s[warp] = t;
+        t = make_float2(sum.a, lost.a);
+        if (ENT) add_exactly(t, st.a);
+        l.a[warp] = t;
+        t = make_float2(sum.s2, lost.s2);
+        if (TWO) add_exactly(t, st.s2);
+        l.s2[warp] = t;
+    }
+    __syncwarp();
+}
+
 // Every warp's set put into the exchange; a consumer barrier has to follow.
 template <bool ENT, bool TWO>
 __device__ __forceinline__ void stat_publish(RunStat<ENT, TWO>& st, StatExchange& ex, int buf) {
@@ -572,6 +622,16 @@ __device__ __forceinline__ void stat_publish(RunStat<ENT, TWO>& st, StatExchange
     if (ENT) st.a = warp_sum(st.a);
     if (TWO) st.s2 = warp_sum(st.s2);
     if ((threadIdx.x & 31) == 0) ex.warp[buf][threadIdx.x >> 5] = make_float4(st.m, st.s, st.a, st.s2);
+}
+// The same of a row of several runs, whose last one is in st.
+template <bool ENT, bool TWO>
+__device__ __forceinline__ void stat_publish_long(const RunStat<ENT, TWO>& st, LongSums& l, StatExchange& ex, int buf,
+                                                  const ExpScale& x) {
+    stat_put_aside<ENT, TWO>(st, l, false, x);
+    const int warp = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) == 0)
+        ex.warp[buf][warp] = make_float4(l.m[warp], l.s[warp].x + l.s[warp].y, l.a[warp].x + l.a[warp].y,
+                                         l.s2[warp].x + l.s2[warp].y);
 }
 // The CTA's set from its warps', by whole warps; every lane gets it.
 template <int NT, bool ENT, bool TWO>

@@ -93,6 +93,81 @@ def test_log_probabilities_at_far_exponents(cuda_lib, dtype, V, T):
     _close_gradient(dx, g, size, 101 * LEAST / T)
 
 
+# Rows with a logit 0 at every 64th place and a logit c at the others: every warp's maximum is 0
+# soon, and a thread adds the same number again and again.  A chain of float32 additions of one
+# number rounds the same way for long: 4096 of them may lose 5e-5 (at c = -0.369), 3e-5 (-0.898).
+FLAT = (-0.369140625, -0.8984375, -0.400390625)
+
+
+def _flat(V, c):
+    """ln S, entropy and the probabilities of a logit 0 and of a logit c."""
+    e, n = math.exp(c), (V + 63) // 64
+    s = n + (V - n) * e
+    return math.log(s), math.log(s) - (V - n) * e * c / s, 1 / s, e / s
+
+
+def _fill_flat(row, c):
+    row.fill_(c)
+    row[::64] = 0.0
+
+
+@pytest.mark.parametrize("dtype,V", [(F32, 134_217_733), (BF16, 268_435_471), (BF16, 2 ** 31 - 1)])
+def test_sums_of_very_long_rows(cuda_lib, dtype, V):
+    ce = cuda_lib
+    x = torch.empty(1, V, dtype=dtype, device="cuda")
+    y = torch.tensor([64 * 1001], device="cuda")
+    for c in FLAT if V < 2 ** 30 else FLAT[:1]:
+        _fill_flat(x[0], c)
+        ln_s, h, p0, pc = _flat(V, c)
+        for entropy in (True, False):
+            out = ce.foak_logprobs_forward(x, y, want_entropy=entropy)
+            tol = ref.EPS + 6 * ref.U * ln_s
+            assert abs(float(out["lse"]) - ln_s) < tol and abs(float(out["logp"]) + ln_s) < tol
+            if entropy:
+                assert abs(float(out["entropy"]) - h) < ref.entropy_tol(V)
+        out = ce.foak_distill_forward(x, y, y[:, None].int(), torch.zeros(1, 1, device="cuda"), ce_weight=1.0,
+                                      temperature=2.0, want_rows=True)
+        assert abs(float(out["row_ce"]) - ln_s) < 2 * ref.EPS * (1 + ln_s)
+        assert abs(float(out["row_kd"]) - _flat(V, c / 2)[0]) < 2 * ref.EPS * (1 + ln_s)
+
+
+def test_sums_of_long_rows_that_a_cta_has_to_itself(cuda_lib):
+    """More rows than clusters take, most of them ignored."""
+    ce = cuda_lib
+    N, V, K = 160, 16_777_221, 1
+    x = torch.zeros(N, V, dtype=F32, device="cuda")
+    y = torch.full((N,), -100, device="cuda")
+    ids, t = torch.zeros(N, K, dtype=torch.int32, device="cuda"), torch.zeros(N, K, device="cuda")
+    rows = (0, 70, 159)
+    cs = FLAT
+    for i, c in zip(rows, cs):
+        _fill_flat(x[i], c)
+        y[i] = 64
+        ids[i] = 6
+    out = ce.foak_logprobs_forward(x, y)
+    two = ce.foak_distill_forward(x, y, ids, t, ce_weight=0.5, temperature=2.0, want_rows=True)
+    one = ce.foak_distill_forward(x, y, ids, t, ce_weight=0.5, want_rows=True)
+    g2 = ce.foak_distill_fwd_bwd(x, y, ids, t, ce_weight=0.5, temperature=2.0, want_rows=True,
+                                 dlogits=torch.empty_like(x))
+    for i, c in zip(rows, cs):
+        ln_1, h, p0, pc = _flat(V, c)
+        ln_2, _, q0, qc = _flat(V, c / 2)
+        tol = 2 * ref.EPS * (1 + ln_1)
+        assert abs(float(out["lse"][i]) - ln_1) < ref.EPS + 6 * ref.U * ln_1
+        assert abs(float(out["entropy"][i]) - h) < ref.entropy_tol(V)
+        assert abs(float(one["row_ce"][i]) - ln_1) < tol and abs(float(one["row_kd"][i]) - (ln_1 - c)) < tol
+        for r in (two, g2):
+            assert abs(float(r["row_ce"][i]) - ln_1) < tol and abs(float(r["row_kd"][i]) - (ln_2 - c / 2)) < tol
+        size = (0.5 * pc + 0.5 * qc) / 3
+        far = g2["dlogits"][i, 7:64].double()
+        assert float((far - size).abs().max()) < (4 * ref.EPS + ref.HALF_STEP[F32]) * size
+    g1 = ce.foak_distill_fwd_bwd(x, y, ids, t, ce_weight=0.5)  # in place
+    for i, c in zip(rows, cs):
+        size = 1.5 * _flat(V, c)[3] / 3
+        far = g1["dlogits"][i, 7:64].double()
+        assert float((far - size).abs().max()) < (4 * ref.EPS + ref.HALF_STEP[F32]) * size
+
+
 @pytest.mark.parametrize("N,V", [(40, 900), (3, 70001), (700, 1031)])
 def test_a_bad_teacher_id_is_reported_by_every_call(cuda_lib, N, V):
     """By the backward call too, whichever rows it is in; the next call's word is clean again."""
