@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kDistillThreads<NT>, NT == 256 ? 2 : 1) distil
         float scale = 0.f;
         if (GRAD) {
             scale = p.g / p.fin.denom;
-            if (p.fin.denom <= 0.f) {
+            if (!(p.fin.denom > 0.f)) {
                 const int n = count_valid_consumers<NT>(p.src, s_count);
                 scale = p.g / static_cast<float>(n);
                 if (tid == 0) s_valid = n;
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kDistillThreads<NT>, NT == 256 ? 2 : 1) distil
         TeacherRow& teach = teacher[me];
         float scale = 0.f;
         if (GRAD) {
-            if (p.fin.denom <= 0.f) scale_known<NT, kClosers>();
+            if (!(p.fin.denom > 0.f)) scale_known<NT, kClosers>();
             scale = p.g / (p.fin.denom > 0.f ? p.fin.denom : static_cast<float>(s_valid));
         }
         const float w1 = scale * p.ce_w, wt = scale * p.kd_w * p.inv_t;

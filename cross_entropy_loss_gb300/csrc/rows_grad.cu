@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kGradThreads + 32, kTeacherBlocksPerSm) distil
     griddep_wait();
     __syncthreads();
     int n_valid = static_cast<int>(p.src.N), n_bad = 0;
-    if (p.src.labels && (p.denom <= 0.f || (blockIdx.x == 0 && p.err)))
+    if (p.src.labels && (!(p.denom > 0.f) || (blockIdx.x == 0 && p.err)))
         count_labels(p.src.labels, p.src.N, p.src.V, p.src.ignore_index, scratch, n_valid, n_bad);
     // The error word is 0 before the launch: each CTA adds the bits that it finds.
     if (blockIdx.x == 0 && tid == 0 && p.err && n_bad > 0)

@@ -197,3 +197,23 @@ def test_a_bad_teacher_id_is_reported_by_every_call(cuda_lib, N, V):
         assert int(err) == ce.FOAK_ERRBIT_LABEL_RANGE
     _, err = ce.foak_distill_backward(xd, None, ids.cuda(), td, f["stats"])
     assert int(err) == 0
+
+
+def test_a_denominator_that_is_no_number_is_none(cuda_lib):
+    """denom > 0, else the number of valid rows: for every place of the gradient."""
+    ce = cuda_lib
+    N, V = 400, 1031
+    x = ref.make_logits(N, V, F32, seed=5)
+    y = _labels(N, V, 5)
+    y[::3] = -100
+    ids = torch.arange(N * 4, dtype=torch.int32).reshape(N, 4) % V
+    t = torch.log_softmax(torch.from_numpy(np.random.default_rng(2).standard_normal((N, 4))), 1).float()
+    xd, yd, idd, td = ref.to_gpu(x), y.cuda(), ids.cuda(), t.cuda()
+    how = dict(ce_weight=0.5)
+    a = ce.foak_distill_fwd_bwd(xd.clone(), yd, idd, td, **how)
+    b = ce.foak_distill_fwd_bwd(xd.clone(), yd, idd, td, denom=math.nan, **how)
+    assert torch.equal(a["loss"], b["loss"]) and torch.equal(a["dlogits"], b["dlogits"])
+    f = ce.foak_distill_forward(xd, yd, idd, td, **how)
+    c, _ = ce.foak_distill_backward(xd, yd, idd, td, f["stats"], **how)
+    d, _ = ce.foak_distill_backward(xd, yd, idd, td, f["stats"], denom=math.nan, **how)
+    assert torch.equal(c, d)
