@@ -76,7 +76,8 @@ __global__ void __launch_bounds__(kDistillThreads<NT>, NT == 256 ? 2 : 1) distil
     __shared__ SweepFactors factors[kMaxBuffers];
     __shared__ float total[kMaxBuffers];  // of the teacher's row
     __shared__ int s_count[kMaxWarps];
-    __shared__ int s_valid, s_bad, s_last;
+    __shared__ int s_valid;  // valid rows of the call, for the scale: written once, read by the closing warps at any time
+    __shared__ int s_rows, s_bad, s_last;  // valid rows of this CTA
     __shared__ DFloat dred[kDistillThreads<NT> / 32];
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = p.src.k;
@@ -332,13 +333,13 @@ __global__ void __launch_bounds__(kDistillThreads<NT>, NT == 256 ? 2 : 1) distil
         }
         n_bad = __reduce_add_sync(0xffffffffu, n_bad);
         if (lane == 0) {
-            if (me == 0) s_valid = rank == 0 ? static_cast<int>(rp.n) : 0;
+            if (me == 0) s_rows = rank == 0 ? static_cast<int>(rp.n) : 0;
             if (rank == 0 && n_bad) atomicAdd(&s_bad, n_bad);
             if (aborted) bars.abort = 1;
         }
     }
     __syncthreads();
-    rows_finish<kDistillThreads<NT>>(p.fin, stream_aborted(bars), s_valid, s_bad, &s_last, dred, true);
+    rows_finish<kDistillThreads<NT>>(p.fin, stream_aborted(bars), s_rows, s_bad, &s_last, dred, true);
     if (k > 1) cluster_sync_converged();  // no CTA leaves while its shared memory may be written
 }
 

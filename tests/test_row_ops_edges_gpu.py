@@ -217,3 +217,21 @@ def test_a_denominator_that_is_no_number_is_none(cuda_lib):
     c, _ = ce.foak_distill_backward(xd, yd, idd, td, f["stats"], **how)
     d, _ = ce.foak_distill_backward(xd, yd, idd, td, f["stats"], denom=math.nan, **how)
     assert torch.equal(c, d)
+
+
+@pytest.mark.parametrize("per_sm", [2, 4, 6])
+@pytest.mark.parametrize("V,K", [(4099, 30), (1031, 200)])
+def test_a_few_rows_a_cta(cuda_lib, per_sm, V, K):
+    """The scale of every row is that of all rows, whichever closing warp takes it and however many rows a CTA
+    has: with two, one closing warp is done while the other has its row still before it."""
+    ce = cuda_lib
+    N = per_sm * torch.cuda.get_device_properties(0).multi_processor_count
+    x = ref.make_logits(N, V, BF16, seed=N)
+    ids = torch.from_numpy(np.random.default_rng(N).integers(0, V, (N, K))).int()
+    t = torch.log_softmax(torch.from_numpy(np.random.default_rng(N + 1).standard_normal((N, K))), 1).float()
+    want = ref.distill(x, None, ids, t, 2.0, 0.0, 1.0, True, g=0.25)
+    xd = ref.to_gpu(x)
+    for _ in range(5):
+        out = ce.foak_distill_fwd_bwd(xd.clone(), None, ids.cuda(), t.cuda(), temperature=2.0, g=0.25)
+        assert int(out["n_valid"]) == N
+        ref.grad_close(out["dlogits"], want["dlogits"], want["grad_size"])
