@@ -14,6 +14,7 @@ Build it with ``python -c "import __graft_entry__ as g; g.build()"`` (or
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -162,6 +163,45 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+def _tensors_of(out):
+    if isinstance(out, torch.Tensor):
+        return [out]
+    values = out.values() if isinstance(out, dict) else out if isinstance(out, (tuple, list)) else ()
+    return [t for t in values if isinstance(t, torch.Tensor)]
+
+
+def _on_stream(call):
+    """Run ``call`` with its ``stream`` argument as the current stream.
+
+    What the call allocates (outputs, error word, workspace) is written on that stream, so it
+    has to come from memory whose earlier uses that stream has behind it: memory of the
+    caller's stream may still be in use there, and an output that the caller drops at once
+    would be given out again while the kernel has yet to write it.  The outputs are held until
+    the caller's stream has passed its uses of them, too.  (The caller makes one stream wait
+    for the other, before the call and before reading its outputs.)
+    """
+    @functools.wraps(call)
+    def run(*args, stream=None, **kwargs):
+        if stream is None:
+            return call(*args, **kwargs)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(stream.cuda_stream)
+        before = torch.cuda.current_stream(stream.device)
+        if before.cuda_stream == stream.cuda_stream:
+            return call(*args, **kwargs)
+        with torch.cuda.stream(stream):
+            out = call(*args, **kwargs)
+        for t in _tensors_of(args) + _tensors_of(kwargs):
+            if t.is_cuda:
+                t.record_stream(stream)
+        for t in _tensors_of(out):
+            if t.is_cuda:
+                t.record_stream(before)
+        return out
+
+    return run
+
+
 def _logits_args(logits):
     if logits.dim() != 2 or logits.stride(1) != 1:
         raise ValueError("logits must be a 2-D tensor with unit column stride (N x V, row stride ld)")
@@ -204,6 +244,7 @@ def workspace(N: int, device) -> torch.Tensor:
     return ws
 
 
+@_on_stream
 def foak_ce_forward(logits, labels, *, ignore_index: int = -100, denom: float = 0.0, want_lse: bool = True,
                     want_row_loss: bool = False, workspace_tensor=None, stream=None):
     """Mean CE loss over non-ignored rows.  Returns dict(loss, lse, row_loss, n_valid, err)."""
@@ -223,6 +264,7 @@ def foak_ce_forward(logits, labels, *, ignore_index: int = -100, denom: float = 
     return dict(loss=loss, lse=lse, row_loss=row_loss, n_valid=n_valid, err=err)
 
 
+@_on_stream
 def foak_ce_backward(logits, labels, lse, grad_out=None, *, dlogits=None, ignore_index: int = -100,
                      denom: float = 0.0, stream=None):
     """dlogits = (softmax - onehot) * g / D.  Pass ``dlogits=logits`` to overwrite in place."""
@@ -249,6 +291,7 @@ def foak_ce_backward(logits, labels, lse, grad_out=None, *, dlogits=None, ignore
     return dlogits, err
 
 
+@_on_stream
 def foak_ce_fwd_bwd(logits, labels, *, g: float = 1.0, ignore_index: int = -100, denom: float = 0.0,
                     want_lse: bool = False, workspace_tensor=None, stream=None):
     """Fused forward + backward in place: ``logits`` is overwritten by dlogits.
@@ -270,6 +313,7 @@ def foak_ce_fwd_bwd(logits, labels, *, g: float = 1.0, ignore_index: int = -100,
     return dict(loss=loss, n_valid=n_valid, err=err, lse=lse)
 
 
+@_on_stream
 def foak_ce_count_valid(labels, V: int, *, ignore_index: int = -100, out=None, err=None, stream=None):
     """Number of labels in [0, V) (not ignore_index), as an int64 device tensor of one element
     (``out`` if given), e.g. this rank's term of a data-parallel all-reduced denominator."""
@@ -286,6 +330,7 @@ def foak_ce_count_valid(labels, V: int, *, ignore_index: int = -100, out=None, e
     return out
 
 
+@_on_stream
 def foak_ce_fwd_bwd_devdenom(logits, labels, denom_count, *, g: float = 1.0, ignore_index: int = -100,
                              want_lse: bool = False, workspace_tensor=None, stream=None):
     """foak_ce_fwd_bwd dividing by the int64 count in device memory ``denom_count`` (read when the
@@ -312,6 +357,7 @@ def foak_ce_host_workspace_size(N: int) -> int:
     return int(lib.foak_ce_host_workspace_size(int(N)))
 
 
+@_on_stream
 def foak_ce_fwd_bwd_host(host_logits, host_labels, dev_logits, dev_labels, *, g: float = 1.0,
                          ignore_index: int = -100, denom: float = 0.0, workspace_tensor=None, out=None, stream=None):
     """Fused forward + backward on HOST logits: the call copies labels and logits to
@@ -352,6 +398,7 @@ def foak_ce_fwd_bwd_host(host_logits, host_labels, dev_logits, dev_labels, *, g:
 FOAK_CE_NOALLOC_MAX_ROWS = 262144
 
 
+@_on_stream
 def foak_ce_fwd_bwd_noalloc(logits, labels, *, g: float = 1.0, ignore_index: int = -100, denom: float = 0.0,
                             want_lse: bool = False, stream=None):
     """Fused forward + backward in place, for callers that may not allocate device memory.
@@ -449,6 +496,7 @@ def foak_linear_ce_workspace_size(N: int, V: int, D: int, chunk: int) -> int:
 _lin_ws: dict = {}
 
 
+@_on_stream
 def foak_linear_ce_chunked(H, W, labels, *, chunk: int = 1024, g: float = 1.0, ignore_index: int = -100,
                            denom: float = 0.0, dH=None, dW=None, workspace_tensor=None, stream=None):
     """Loss, dH and dW of CE(H W^T) in chunks of rows on the tensor cores.
@@ -494,6 +542,7 @@ def _rows_arg(t, name):
     return t.shape[0], t.shape[1], (t.stride(0) if t.shape[0] > 1 else t.shape[1])
 
 
+@_on_stream
 def foak_rmsnorm_forward(X, gamma, *, eps: float = 1e-5, Y=None, want_rstd: bool = True, stream=None):
     """Y = X / sqrt(mean(X^2) + eps) * gamma per row (fp32 arithmetic, one rounding).
 
@@ -511,6 +560,7 @@ def foak_rmsnorm_forward(X, gamma, *, eps: float = 1e-5, Y=None, want_rstd: bool
     return Y, rstd
 
 
+@_on_stream
 def foak_rmsnorm_backward(dY, X, gamma, rstd, *, dX=None, want_dgamma: bool = True, stream=None):
     """dX (X's dtype) and dgamma (float32 [D], or None) of sum(dY * rmsnorm(X))."""
     N, D, lddy = _rows_arg(dY, "dY")
@@ -531,6 +581,7 @@ def foak_rmsnorm_backward(dY, X, gamma, rstd, *, dX=None, want_dgamma: bool = Tr
     return dX, dgamma
 
 
+@_on_stream
 def foak_rmsnorm_linear_ce_chunked(X, gamma, W, labels, *, eps: float = 1e-5, chunk: int = 1024, g: float = 1.0,
                                    ignore_index: int = -100, denom: float = 0.0, dX=None, dW=None,
                                    workspace_tensor=None, stream=None):
@@ -572,6 +623,7 @@ def foak_rmsnorm_linear_ce_chunked(X, gamma, W, labels, *, eps: float = 1e-5, ch
 
 
 # --------------------------------------------------------------------- RoPE
+@_on_stream
 def foak_rope_cache(max_pos: int, d: int, base: float = 10000.0, device="cuda", stream=None):
     """The cos/sin table for positions [0, max_pos) and head dimension d (uint8 device tensor)."""
     need = int(lib.foak_rope_cache_size(int(max_pos), int(d)))
@@ -585,6 +637,7 @@ def foak_rope_cache(max_pos: int, d: int, base: float = 10000.0, device="cuda", 
     return cache
 
 
+@_on_stream
 def foak_rope_apply(x, positions, cache, *, inverse: bool = False, stream=None):
     """Rotate ``x`` (T x H x d bf16/fp32 CUDA view, heads contiguous) in place by the
     angles of ``positions`` (int64 [T]); returns the device error word."""
@@ -603,6 +656,7 @@ def foak_rope_apply(x, positions, cache, *, inverse: bool = False, stream=None):
     return err
 
 
+@_on_stream
 def foak_rope_apply_qk(q, k, positions, cache, *, inverse: bool = False, stream=None):
     """Rotate Q (T x Hq x d) and K (T x Hk x d) in place in one launch; returns the error word."""
     views = []
@@ -654,6 +708,7 @@ def _dlogits_arg(dlogits, logits, N, V, ld):
     return dlogits
 
 
+@_on_stream
 def foak_logprobs_forward(logits, labels=None, *, top_k: int = 0, temperature: float = 1.0, ignore_index: int = -100,
                           want_entropy: bool = True, want_lse: bool = True, want_stats: bool = True,
                           workspace_tensor=None, stream=None):
@@ -687,6 +742,7 @@ def foak_logprobs_forward(logits, labels=None, *, top_k: int = 0, temperature: f
     return dict(logp=logp, entropy=entropy, lse=lse, stats=stats, top_logprobs=top_lp, top_ids=top_ids, err=err)
 
 
+@_on_stream
 def foak_logprobs_backward(logits, labels, stats, grad_logp=None, entropy=None, grad_entropy=None, *,
                            temperature: float = 1.0, ignore_index: int = -100, dlogits=None, stream=None):
     """Gradient of sum(grad_logp * logp + grad_entropy * entropy); returns (dlogits, err).
@@ -733,6 +789,7 @@ def _teacher_args(ids, logprobs, N, device):
     return K, (ids.stride(0) if N > 1 else K)
 
 
+@_on_stream
 def foak_distill_forward(logits, labels, teacher_ids, teacher_logprobs, *, ce_weight: float = 0.0,
                          kd_weight: float = 1.0, temperature: float = 1.0, normalize: bool = True,
                          ignore_index: int = -100, denom: float = 0.0, want_rows: bool = False,
@@ -766,6 +823,7 @@ def foak_distill_forward(logits, labels, teacher_ids, teacher_logprobs, *, ce_we
     return dict(loss=loss, row_ce=row_ce, row_kd=row_kd, stats=stats, n_valid=n_valid, err=err)
 
 
+@_on_stream
 def foak_distill_fwd_bwd(logits, labels, teacher_ids, teacher_logprobs, *, ce_weight: float = 0.0,
                          kd_weight: float = 1.0, temperature: float = 1.0, normalize: bool = True, g: float = 1.0,
                          ignore_index: int = -100, denom: float = 0.0, dlogits=None, want_rows: bool = False,
@@ -796,6 +854,7 @@ def foak_distill_fwd_bwd(logits, labels, teacher_ids, teacher_logprobs, *, ce_we
     return dict(loss=loss, dlogits=dlogits, row_ce=row_ce, row_kd=row_kd, n_valid=n_valid, err=err)
 
 
+@_on_stream
 def foak_distill_backward(logits, labels, teacher_ids, teacher_logprobs, stats, grad_out=None, *,
                           ce_weight: float = 0.0, kd_weight: float = 1.0, temperature: float = 1.0,
                           normalize: bool = True, ignore_index: int = -100, denom: float = 0.0, dlogits=None,

@@ -1,0 +1,82 @@
+"""Calls with a ``stream`` of their own: what they allocate is not shared with the caller's
+stream while either may still use it."""
+import pytest
+import torch
+
+import row_ops_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def _calls(ce, N=96, V=5003, K=4):
+    """Every row call as f(stream) -> outputs, on inputs that are complete."""
+    x = ref.to_gpu(ref.make_logits(N, V, BF16, seed=1))
+    y = torch.randint(0, V, (N,), generator=torch.Generator().manual_seed(1)).cuda()
+    top = ce.foak_logprobs_forward(x, y, top_k=K)
+    ids, t = top["top_ids"], top["top_logprobs"]
+    lse = ce.foak_ce_forward(x, y)["lse"]
+    ds = ce.foak_distill_forward(x, y, ids, t)
+    gl = torch.ones(N, device="cuda")
+    torch.cuda.synchronize()
+    return {
+        "logprobs_forward": lambda s: ce.foak_logprobs_forward(x, y, top_k=K, stream=s),
+        "logprobs_backward": lambda s: ce.foak_logprobs_backward(x, y, top["stats"], gl, top["entropy"], gl, stream=s),
+        "distill_forward": lambda s: ce.foak_distill_forward(x, y, ids, t, want_rows=True, stream=s),
+        "distill_fwd_bwd": lambda s: ce.foak_distill_fwd_bwd(x, y, ids, t, want_rows=True, stream=s,
+                                                             dlogits=torch.empty_like(x)),
+        "distill_backward": lambda s: ce.foak_distill_backward(x, y, ids, t, ds["stats"], stream=s),
+        "ce_forward": lambda s: ce.foak_ce_forward(x, y, want_row_loss=True, stream=s),
+        "ce_backward": lambda s: ce.foak_ce_backward(x, y, lse, stream=s),
+    }
+
+
+def _tensors(out):
+    return [t for t in (out.values() if isinstance(out, dict) else out) if t is not None]
+
+
+def test_the_outputs_are_those_of_the_current_stream(cuda_lib):
+    side = torch.cuda.Stream()
+    for name, call in _calls(cuda_lib).items():
+        a = _tensors(call(None))
+        side.wait_stream(torch.cuda.current_stream())
+        b = _tensors(call(side))
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda.synchronize()
+        for i, (p, q) in enumerate(zip(a, b, strict=True)):
+            assert torch.equal(p, q), (name, i)
+        assert torch.cuda.current_stream() == torch.cuda.default_stream()
+
+
+def test_outputs_dropped_at_once_are_not_given_out_before_they_are_written(cuda_lib):
+    side = torch.cuda.Stream()
+    for name, call in _calls(cuda_lib).items():
+        call(None)
+        torch.cuda.synchronize()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)  # the call's kernels are some 10 ms away
+        sizes = [t.numel() * t.element_size() for t in _tensors(call(side))]  # dropped here
+        keep = [torch.full((n,), 0x5A, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(2)]
+        torch.cuda.synchronize()
+        assert all(bool((k == 0x5A).all()) for k in keep), name
+
+
+def test_outputs_in_use_by_the_caller_are_not_given_out_to_the_stream(cuda_lib):
+    """Dropped while the caller's stream has yet to read them: the stream's next call takes other memory."""
+    ce = cuda_lib
+    side = torch.cuda.Stream()
+    call = _calls(ce)["distill_forward"]
+    want = call(None)["row_kd"].clone()
+    side.wait_stream(torch.cuda.current_stream())
+    out = call(side)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda._sleep(20_000_000)
+    read = out["row_kd"].clone()
+    sizes = [t.numel() * t.element_size() for t in _tensors(out)]
+    del out
+    with torch.cuda.stream(side):
+        other = [torch.full((n,), 0x5A, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(2)]
+    torch.cuda.synchronize()
+    assert torch.equal(read, want) and len(other) > 0
