@@ -222,26 +222,42 @@ def _labels_arg(labels, N, device):
     return labels
 
 
-def _header_workspace(device) -> torch.Tensor:
-    """The cached workspace of calls that need its header alone."""
-    ws = _ws_cache.get(device)
-    return workspace(0, device) if ws is None else ws
+def _cached_workspace(cache: dict, need: int, device, fill=torch.zeros) -> torch.Tensor:
+    """A buffer of ``need`` bytes or more, zeros before its first use: the current stream's own in
+    ``cache``, or a new one while that stream is captured into a graph.
+
+    The calls of a stream run one after another and leave the buffer zeroed; calls of
+    two streams may overlap, and must not count in one header.  A graph's replays overlap with
+    anything, and outlive a cached buffer that a larger call replaces: each captured call has a
+    buffer of the graph's memory, filled by the graph.
+    """
+    if torch.cuda.is_current_stream_capturing():
+        return fill(need, dtype=torch.uint8, device=device)
+    key = (device, _stream_handle(device, None))
+    ws = cache.get(key)
+    if ws is None or ws.numel() < need:
+        with _ws_lock:
+            ws = cache.get(key)
+            if ws is None or ws.numel() < need:
+                ws = cache[key] = fill(max(need, 4096), dtype=torch.uint8, device=device)
+    return ws
 
 
 def workspace(N: int, device) -> torch.Tensor:
-    """A zero-filled, reusable workspace of at least foak_ce_workspace_size(N) bytes.
+    """A zero-filled, reusable workspace of at least foak_ce_workspace_size(N) bytes for the
+    device's current stream.
 
-    Calls leave it zeroed again, so the cached buffer serves every stream-ordered
-    call on its device.  Calls on different streams should pass their own buffer.
+    Calls leave it zeroed again, so the cached buffer serves every call on that stream; calls
+    on another stream get another one.  While the stream is captured into a graph every call of
+    this function gives a new buffer, which the graph fills with zeros: pass ``workspace_tensor``
+    to captured calls to be without that step, one buffer for the graph's calls on one stream.
     """
-    need = foak_ce_workspace_size(N)
+    return _cached_workspace(_ws_cache, foak_ce_workspace_size(N), _device_of(device))
+
+
+def _device_of(device) -> torch.device:
     dev = torch.device(device)
-    with _ws_lock:
-        ws = _ws_cache.get(dev)
-        if ws is None or ws.numel() < need:
-            ws = torch.zeros(max(need, 4096), dtype=torch.uint8, device=dev)
-            _ws_cache[dev] = ws
-    return ws
+    return torch.device(dev.type, torch.cuda.current_device()) if dev.type == "cuda" and dev.index is None else dev
 
 
 @_on_stream
@@ -518,13 +534,7 @@ def foak_linear_ce_chunked(H, W, labels, *, chunk: int = 1024, g: float = 1.0, i
     n_valid = torch.empty(1, dtype=torch.int32, device=dev)
     err = torch.empty(1, dtype=torch.int32, device=dev)
     need = foak_linear_ce_workspace_size(N, V, D, chunk)
-    ws = workspace_tensor
-    if ws is None:
-        with _ws_lock:
-            ws = _lin_ws.get(dev)
-            if ws is None or ws.numel() < need:
-                ws = torch.zeros(need, dtype=torch.uint8, device=dev)
-                _lin_ws[dev] = ws
+    ws = _cached_workspace(_lin_ws, need, dev) if workspace_tensor is None else workspace_tensor
     st = lib.foak_linear_ce_chunked(_ptr(H), _ptr(W), _ptr(labels), N, V, D, int(ignore_index), int(chunk), float(g),
                                     float(denom), _ptr(loss), _ptr(dH), _ptr(dW), _ptr(n_valid), _ptr(err), _ptr(ws),
                                     ws.numel(), _stream(dev, stream))
@@ -534,6 +544,7 @@ def foak_linear_ce_chunked(H, W, labels, *, chunk: int = 1024, g: float = 1.0, i
 
 # --------------------------------------------------------------------- RMSNorm
 _norm_ws: dict = {}
+_norm_lin_ws: dict = {}
 
 
 def _rows_arg(t, name):
@@ -570,11 +581,7 @@ def foak_rmsnorm_backward(dY, X, gamma, rstd, *, dX=None, want_dgamma: bool = Tr
     dev = X.device
     dgamma = torch.empty(D, dtype=torch.float32, device=dev) if want_dgamma else None
     need = int(lib.foak_rmsnorm_workspace_size(D))
-    with _ws_lock:
-        ws = _norm_ws.get(dev)
-        if ws is None or ws.numel() < need:
-            ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-            _norm_ws[dev] = ws
+    ws = _cached_workspace(_norm_ws, need, dev, fill=torch.empty)  # partial sums only: each is written before it is read
     st = lib.foak_rmsnorm_backward(_ptr(dY), lddy, _ptr(X), ldx, _ptr(gamma), _ptr(rstd), _DT[X.dtype], N, D, _ptr(dX),
                                    lddx, _ptr(dgamma), _ptr(ws), ws.numel(), _stream(dev, stream))
     _check(st, "foak_rmsnorm_backward")
@@ -606,14 +613,7 @@ def foak_rmsnorm_linear_ce_chunked(X, gamma, W, labels, *, eps: float = 1e-5, ch
     n_valid = torch.empty(1, dtype=torch.int32, device=dev)
     err = torch.empty(1, dtype=torch.int32, device=dev)
     need = int(lib.foak_rmsnorm_linear_ce_workspace_size(N, V, D, chunk))
-    ws = workspace_tensor
-    if ws is None:
-        with _ws_lock:
-            key = ("norm_lin", dev)
-            ws = _norm_ws.get(key)
-            if ws is None or ws.numel() < need:
-                ws = torch.zeros(need, dtype=torch.uint8, device=dev)  # zero-filled before first use
-                _norm_ws[key] = ws
+    ws = _cached_workspace(_norm_lin_ws, need, dev) if workspace_tensor is None else workspace_tensor
     st = lib.foak_rmsnorm_linear_ce_chunked(_ptr(X), _ptr(gamma), _ptr(W), _ptr(labels), N, V, D, int(ignore_index),
                                             int(chunk), float(eps), float(g), float(denom), _ptr(loss), _ptr(dX),
                                             _ptr(dgamma), _ptr(dW), _ptr(n_valid), _ptr(err), _ptr(ws), ws.numel(),
@@ -682,6 +682,7 @@ def foak_rope_apply_qk(q, k, positions, cache, *, inverse: bool = False, stream=
 
 # --------------------------------------------------------------------- log probabilities
 FOAK_LOGPROBS_MAX_K = 256
+_HEADER_BYTES = int(lib.foak_logprobs_workspace_size())
 
 
 def _labels_or_none(labels, N, device):
@@ -734,7 +735,7 @@ def foak_logprobs_forward(logits, labels=None, *, top_k: int = 0, temperature: f
     top_lp = torch.empty(N, K, dtype=f32, device=dev) if K else None
     top_ids = torch.empty(N, K, dtype=torch.int32, device=dev) if K else None
     err = torch.empty(1, dtype=torch.int32, device=dev)
-    ws = _header_workspace(dev) if workspace_tensor is None else workspace_tensor
+    ws = _cached_workspace(_ws_cache, _HEADER_BYTES, dev) if workspace_tensor is None else workspace_tensor
     st = lib.foak_logprobs_forward(_addr(logits), dt, ld, _addr(labels), N, V, int(ignore_index), float(temperature), K,
                                    _addr(logp), _addr(entropy), _addr(lse), _addr(stats), _addr(top_lp),
                                    _addr(top_ids), _addr(err), _addr(ws), ws.numel(), _stream_handle(dev, stream))
