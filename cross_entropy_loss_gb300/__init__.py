@@ -255,6 +255,12 @@ def workspace(N: int, device) -> torch.Tensor:
     return _cached_workspace(_ws_cache, foak_ce_workspace_size(N), _device_of(device))
 
 
+def _workspace_arg(ws, device) -> torch.Tensor:
+    if ws.device != device:
+        raise ValueError("workspace_tensor must live on the logits' device")
+    return ws
+
+
 def _device_of(device) -> torch.device:
     dev = torch.device(device)
     return torch.device(dev.type, torch.cuda.current_device()) if dev.type == "cuda" and dev.index is None else dev
@@ -581,7 +587,8 @@ def foak_rmsnorm_backward(dY, X, gamma, rstd, *, dX=None, want_dgamma: bool = Tr
     dev = X.device
     dgamma = torch.empty(D, dtype=torch.float32, device=dev) if want_dgamma else None
     need = int(lib.foak_rmsnorm_workspace_size(D))
-    ws = _cached_workspace(_norm_ws, need, dev, fill=torch.empty)  # partial sums only: each is written before it is read
+    # partial sums only: each is written before it is read
+    ws = _cached_workspace(_norm_ws, need, dev, fill=torch.empty)
     st = lib.foak_rmsnorm_backward(_ptr(dY), lddy, _ptr(X), ldx, _ptr(gamma), _ptr(rstd), _DT[X.dtype], N, D, _ptr(dX),
                                    lddx, _ptr(dgamma), _ptr(ws), ws.numel(), _stream(dev, stream))
     _check(st, "foak_rmsnorm_backward")
@@ -735,7 +742,8 @@ def foak_logprobs_forward(logits, labels=None, *, top_k: int = 0, temperature: f
     top_lp = torch.empty(N, K, dtype=f32, device=dev) if K else None
     top_ids = torch.empty(N, K, dtype=torch.int32, device=dev) if K else None
     err = torch.empty(1, dtype=torch.int32, device=dev)
-    ws = _cached_workspace(_ws_cache, _HEADER_BYTES, dev) if workspace_tensor is None else workspace_tensor
+    ws = workspace_tensor
+    ws = _cached_workspace(_ws_cache, _HEADER_BYTES, dev) if ws is None else _workspace_arg(ws, dev)
     st = lib.foak_logprobs_forward(_addr(logits), dt, ld, _addr(labels), N, V, int(ignore_index), float(temperature), K,
                                    _addr(logp), _addr(entropy), _addr(lse), _addr(stats), _addr(top_lp),
                                    _addr(top_ids), _addr(err), _addr(ws), ws.numel(), _stream_handle(dev, stream))
@@ -814,7 +822,7 @@ def foak_distill_forward(logits, labels, teacher_ids, teacher_logprobs, *, ce_we
     stats = torch.empty(N, 4, dtype=f32, device=dev) if want_stats else None
     n_valid = torch.empty(1, dtype=torch.int32, device=dev)
     err = torch.empty(1, dtype=torch.int32, device=dev)
-    ws = workspace(N, dev) if workspace_tensor is None else workspace_tensor
+    ws = workspace(N, dev) if workspace_tensor is None else _workspace_arg(workspace_tensor, dev)
     st = lib.foak_distill_forward(_addr(logits), dt, ld, _addr(labels), N, V, int(ignore_index), _addr(teacher_ids),
                                   _addr(teacher_logprobs), ldt, K, int(bool(normalize)), float(ce_weight),
                                   float(kd_weight), float(temperature), float(denom), _addr(loss), _addr(row_ce),
@@ -845,7 +853,7 @@ def foak_distill_fwd_bwd(logits, labels, teacher_ids, teacher_logprobs, *, ce_we
     row_kd = torch.empty(N, dtype=f32, device=dev) if want_rows else None
     n_valid = torch.empty(1, dtype=torch.int32, device=dev)
     err = torch.empty(1, dtype=torch.int32, device=dev)
-    ws = workspace(N, dev) if workspace_tensor is None else workspace_tensor
+    ws = workspace(N, dev) if workspace_tensor is None else _workspace_arg(workspace_tensor, dev)
     st = lib.foak_distill_fwd_bwd(_addr(logits), _addr(dlogits), dt, ld, _addr(labels), N, V, int(ignore_index),
                                   _addr(teacher_ids), _addr(teacher_logprobs), ldt, K, int(bool(normalize)),
                                   float(ce_weight), float(kd_weight), float(temperature), float(g), float(denom),

@@ -143,3 +143,15 @@ def test_a_graph_has_a_workspace_of_its_own(cuda_lib):
         assert torch.equal(a["top_ids"], want[0]) and torch.equal(b["loss"], want[1]) and int(a["err"]) == int(b["err"]) == 0
         assert torch.equal(c["loss"], want_big) and torch.equal(d["top_ids"], want[0])
     assert bool((other == 0x5A).all())
+
+
+def test_a_workspace_in_host_memory_is_refused(cuda_lib):
+    ce = cuda_lib
+    x = torch.zeros(2, 8, device="cuda")
+    ids, t = torch.zeros(2, 1, dtype=torch.int32, device="cuda"), torch.zeros(2, 1, device="cuda")
+    for call in (lambda w: ce.foak_logprobs_forward(x, workspace_tensor=w),
+                 lambda w: ce.foak_distill_forward(x, None, ids, t, workspace_tensor=w),
+                 lambda w: ce.foak_distill_fwd_bwd(x, None, ids, t, workspace_tensor=w)):
+        with pytest.raises(ValueError):
+            call(torch.zeros(4096, dtype=torch.uint8))
+        call(torch.zeros(4096, dtype=torch.uint8, device="cuda"))

@@ -42,3 +42,11 @@ def test_captured_calls_get_buffers_of_their_own(so):
     assert int(b.count_nonzero()) == 0 and b.numel() >= ce.foak_ce_workspace_size(10)
     state["capturing"] = False
     assert ce.workspace(10, "cpu") is a
+
+
+def test_a_workspace_of_another_device_is_refused(so):
+    ce, _ = so
+    ws = torch.zeros(4096, dtype=torch.uint8)
+    assert ce._workspace_arg(ws, torch.device("cpu")) is ws
+    with pytest.raises(ValueError):
+        ce._workspace_arg(ws, torch.device("cuda", 0))
