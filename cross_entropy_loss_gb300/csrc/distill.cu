@@ -286,9 +286,9 @@ __global__ void __launch_bounds__(kDistillThreads<NT>, NT == 256 ? 2 : 1) distil
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars.row_empty[buf]);
                 if (k > 1) {
-                    stat_send(st, ex, buf, use, k, rank);
-                    if (!peers_meet(bars, buf, use, k, aborted ? 0 : p.src.wait_ns)) aborted = true;
-                    stat_merge(st, ex, buf, use, k, sc);
+                    stat_send(st, ex, k, rank);
+                    if (!peers_meet(bars, k, aborted ? 0 : p.src.wait_ns)) aborted = true;
+                    stat_merge(st, ex, k, sc);
                 }
                 st.correct(sc);
                 const bool empty = st.s == 0.f;  // nothing but -inf: every token's log probability is -inf
@@ -369,7 +369,7 @@ cudaError_t launch_typed(DistillParams prm, int per_sm, cudaStream_t stream) {
         }
     }
     const int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(s.N, static_cast<int64_t>(device_sm_count()) * per_sm / s.k));
-    set_rows(s, clusters);
+    if (!set_rows(s, clusters)) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(clusters * s.k), 1, 1);
     cfg.blockDim = dim3(kDistillThreads<NT>, 1, 1);

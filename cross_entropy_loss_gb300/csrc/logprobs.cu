@@ -718,9 +718,6 @@ __device__ __noinline__ void close_rows(const LogprobParams& p, StreamBars& bars
             unsigned long long* pushed = reinterpret_cast<unsigned long long*>(smem_pushed);  // the cluster's lists, K each
             if constexpr (TOPK) {  // this CTA's largest, in order
                 TopScratch& t = top[me];
-                // the last row's list may still be read by the cluster's other CTAs, and theirs written over ours
-                if (k > 1 && use > 0 && !peers_wait(bars, &bars.peers_done[buf], (use & 1u) ^ 1u, aborted ? 0 : p.src.wait_ns))
-                    aborted = true;
                 move_slice<ES>(p.src, row, rank, s);
                 if (st.s == st.s) n = top_list<ES>(s, maxima + buf * p.max_stride, thread_max[buf], K, t);
                 __syncwarp();
@@ -729,9 +726,9 @@ __device__ __noinline__ void close_rows(const LogprobParams& p, StreamBars& bars
                 if (k > 1) push_list(best, n, K, pushed, rank, k);
             }
             if (k > 1) {
-                stat_send(st, ex, buf, use, k, rank);
-                if (!peers_meet(bars, buf, use, k, aborted ? 0 : p.src.wait_ns)) aborted = true;
-                stat_merge(st, ex, buf, use, k, p.scale);
+                stat_send(st, ex, k, rank);
+                if (!peers_meet(bars, k, aborted ? 0 : p.src.wait_ns)) aborted = true;
+                stat_merge(st, ex, k, p.scale);
             }
             st.correct(p.scale);
             const float ln_s = logf(st.s);
@@ -759,10 +756,6 @@ __device__ __noinline__ void close_rows(const LogprobParams& p, StreamBars& bars
                     const unsigned long long item = best[i];
                     const int r = k > 1 ? pushed_rank(pushed, K, k, item) : i;
                     if (r < K) write(r, item);
-                }
-                if (k > 1) {  // the lists here may be written over
-                    __syncwarp();
-                    if (lane < k) remote_arrive(&bars.peers_done[buf], static_cast<uint32_t>(lane));
                 }
                 if (none && rank == 0) {
 #pragma unroll 1
@@ -958,7 +951,7 @@ cudaError_t launch_typed(LogprobParams prm, cudaStream_t stream) {
         }
     }
     const int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(s.N, static_cast<int64_t>(sms) * per_sm / s.k));
-    set_rows(s, clusters);
+    if (!set_rows(s, clusters)) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(clusters * s.k), 1, 1);
     cfg.blockDim = dim3(kLogprobThreads<TOPK>, 1, 1);

@@ -104,10 +104,12 @@ inline void set_cluster(StreamSrc& p, int k) {
     for (p.log2_k = 0; (1 << p.log2_k) < k;) ++p.log2_k;
 }
 
-// The rows shared out to `clusters`: cluster c takes c, c + clusters, ...
-inline void set_rows(StreamSrc& p, int64_t clusters) {
+// The rows shared out to `clusters`: cluster c takes c, c + clusters, ...  False where a
+// cluster of several CTAs would get a second row: what its CTAs exchange through is used once.
+inline bool set_rows(StreamSrc& p, int64_t clusters) {
     p.each = p.N / clusters;
     p.more = p.N % clusters;
+    return p.k == 1 || p.N <= clusters;
 }
 __device__ __forceinline__ int64_t stream_rows(const StreamSrc& p, int64_t cid) { return p.each + (cid < p.more); }
 
@@ -115,7 +117,8 @@ __device__ __forceinline__ int64_t stream_rows(const StreamSrc& p, int64_t cid) 
 // much faster, and one where there are rows for every SM.  A row of less than kWholeRowBytes
 // stays whole, as the exchange costs what the shorter read gains (1 x 32000 bf16: 5.1 us whole,
 // 5.4 by two, 5.2 by four or eight; 1 x 128256: 10.5, 8.3, 6.6 and 5.8), and so does a slice of
-// less than `least` elements.  `at_most` CTAs run at a time without waiting for one another.
+// less than `least` elements.  `at_most` CTAs run at a time without waiting for one another: a
+// shared row is its cluster's only one.
 constexpr int64_t kWholeRowBytes = 96 * 1024;
 inline int cluster_size(const StreamSrc& p, int es, int64_t least, int64_t at_most) {
     if (p.V * es < kWholeRowBytes) return 1;
@@ -175,8 +178,7 @@ struct StreamBars {
     uint64_t row_empty[kMaxBuffers];   // the closing warp has taken it
     uint64_t row_ready[kMaxBuffers];   // the closing warp has what the second sweep needs
     uint64_t row_stored[kMaxBuffers];  // the second sweep's stores are made: one arrival a consumer warp
-    uint64_t peers[kMaxBuffers];       // the cluster's CTAs have sent their part: one arrival a CTA
-    uint64_t peers_done[kMaxBuffers];  // and have read this CTA's
+    uint64_t peers;                    // the cluster's CTAs have sent their part of its row: one arrival a CTA
     int abort;              // a wait gave up: everyone stops waiting and winds down
 };
 
@@ -192,9 +194,8 @@ __device__ __forceinline__ void stream_init(StreamBars& b, int stages, int clust
             mbar_init(&b.row_empty[i], 1);
             mbar_init(&b.row_ready[i], 1);
             mbar_init(&b.row_stored[i], Shape<NT>::kWarps);
-            mbar_init(&b.peers[i], cluster);
-            mbar_init(&b.peers_done[i], cluster);
         }
+        mbar_init(&b.peers, cluster);
         b.abort = 0;
         fence_mbar_init();
     }
@@ -563,8 +564,8 @@ struct RunStat {
 
 // Shared memory through which the consumers' (and the cluster's) sets meet.
 struct StatExchange {
-    float4 warp[kMaxBuffers][kMaxWarps];            // (m, s, a, s2), by row buffer
-    float4 cta[kMaxBuffers][2][kStreamMaxCluster];  // the cluster's CTAs' sets, by buffer and parity of its use
+    float4 warp[kMaxBuffers][kMaxWarps];  // (m, s, a, s2), by row buffer
+    float4 cta[kStreamMaxCluster];        // the cluster's CTAs' sets of its row
 };
 
 // The sums of a long row's earlier runs of kRunChunks chunks, by consumer warp: each as two
@@ -646,30 +647,28 @@ __device__ __forceinline__ void stat_collect(RunStat<ENT, TWO>& st, const StatEx
         if (TWO) st.s2 += __shfl_xor_sync(0xffffffffu, st.s2, off);
     }
 }
-// In a cluster, by the closing warps of a row: this CTA's set to every CTA, then the row's
-// from all.  A slot's next use but one follows an exchange that every CTA enters only after
-// it has read the slot.
-__device__ __forceinline__ bool peers_meet(StreamBars& bars, int buf, uint32_t use, int k, uint64_t limit_ns) {
+// In a cluster, by the closing warps of its row: this CTA's set to every CTA, then, when all
+// have met, the row's from all.
+__device__ __forceinline__ bool peers_meet(StreamBars& bars, int k, uint64_t limit_ns) {
     const int lane = threadIdx.x & 31;
     __syncwarp();
-    if (lane < k) remote_arrive(&bars.peers[buf], static_cast<uint32_t>(lane));
+    if (lane < k) remote_arrive(&bars.peers, static_cast<uint32_t>(lane));
     __syncwarp();
-    return peers_wait(bars, &bars.peers[buf], use & 1u, limit_ns);
+    return peers_wait(bars, &bars.peers, 0, limit_ns);
 }
 template <bool ENT, bool TWO>
-__device__ __forceinline__ void stat_send(const RunStat<ENT, TWO>& st, StatExchange& ex, int buf, uint32_t use, int k, int rank) {
+__device__ __forceinline__ void stat_send(const RunStat<ENT, TWO>& st, StatExchange& ex, int k, int rank) {
     const int lane = threadIdx.x & 31;
     if (lane < k) {
-        const uint32_t to = mapa_u32(&ex.cta[buf][use & 1u][rank], static_cast<uint32_t>(lane));
+        const uint32_t to = mapa_u32(&ex.cta[rank], static_cast<uint32_t>(lane));
         asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(st.m), "f"(st.s), "f"(st.a),
                      "f"(st.s2)
                      : "memory");
     }
 }
 template <bool ENT, bool TWO>
-__device__ __forceinline__ void stat_merge(RunStat<ENT, TWO>& st, const StatExchange& ex, int buf, uint32_t use, int k,
-                                           const ExpScale& x) {
-    st.set(ex.cta[buf][use & 1u][threadIdx.x & (k - 1)], x);
+__device__ __forceinline__ void stat_merge(RunStat<ENT, TWO>& st, const StatExchange& ex, int k, const ExpScale& x) {
+    st.set(ex.cta[threadIdx.x & (k - 1)], x);
     st.raise(warp_max_redux(st.m), x);
 #pragma unroll 1
     for (int off = k / 2; off > 0; off >>= 1) {

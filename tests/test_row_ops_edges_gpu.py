@@ -235,3 +235,37 @@ def test_a_few_rows_a_cta(cuda_lib, per_sm, V, K):
         out = ce.foak_distill_fwd_bwd(xd.clone(), None, ids.cuda(), t.cuda(), temperature=2.0, g=0.25)
         assert int(out["n_valid"]) == N
         ref.grad_close(out["dlogits"], want["dlogits"], want["grad_size"])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_rows_about_the_borders_of_the_cluster_sizes(cuda_lib, dtype):
+    """8, 4, 2 and 1 CTAs a row as the rows get more: the largest number of rows at each size, and one more."""
+    ce = cuda_lib
+    sms, V, K = torch.cuda.get_device_properties(0).multi_processor_count, 100_003, 7
+    most = 2 * sms + 1
+    x = ref.make_logits(1, V, dtype, seed=1).repeat(most, 1)
+    x[0, torch.arange(1, K + 1) * 13_001] = 17.0 - torch.arange(K).to(dtype)  # no ties, whose order a turn would change
+    for i in range(most):  # rows that differ in a known way: a turn of one row
+        x[i] = torch.roll(x[0], i)
+    y = (torch.arange(most) * 7) % V
+    want = ref.logprobs(x[:1], None, K, 1.0)
+    lnp, top = want["lnp"][0], want["top_ids"][0]
+    assert len(set(x[0, top].tolist())) == K
+    xd, yd = ref.to_gpu(x), y.cuda()
+    ids = torch.stack([(top + i) % V for i in range(most)])
+    t = want["top_logprobs"].float().expand(most, K).contiguous().cuda()
+    logp = torch.stack([lnp[(y[i] - i) % V] for i in range(most)])
+    kd = ref.distill(x[:1], None, ids[:1].int(), t[:1].cpu(), 1.0, 0.0, 1.0, True)
+    for at_most in (2 * sms, sms):
+        for k in (8, 4, 2, 1):
+            for N in sorted({max(1, at_most // k), at_most // k + 1, 1}):
+                out = ce.foak_logprobs_forward(xd[:N], yd[:N], top_k=K)
+                assert torch.equal(out["top_ids"].cpu().long(), ids[:N])
+                ref.close(out["logp"], logp[:N], ref.value_tol(logp[:N]), "logp")
+                out = ce.foak_logprobs_forward(xd[:N], yd[:N])
+                ref.close(out["lse"], want["lse"].expand(N), ref.value_tol(want["lse"]).expand(N), "lse")
+                idd = ids[:N].int().cuda()
+                f = ce.foak_distill_forward(xd[:N], None, idd, t[:N], want_rows=True)
+                b = ce.foak_distill_fwd_bwd(xd[:N], None, idd, t[:N], want_rows=True, dlogits=torch.empty_like(xd[:N]))
+                for r in (f, b):
+                    ref.close(r["row_kd"], kd["row_kd"].expand(N), 2 * ref.EPS * kd["kd_size"].expand(N) + 1e-30, "row_kd")
