@@ -20,8 +20,6 @@
 // part; the loss alone 53 and 62.  HBM bounds the long rows, issue slots (64% taken, two
 // exponentials an element and sweep) the short ones at T = 2.
 #include <algorithm>
-#include <map>
-#include <mutex>
 
 #include "row_stream.cuh"
 #include "teacher.cuh"
@@ -343,15 +341,9 @@ __global__ void __launch_bounds__(kDistillThreads<NT>, NT == 256 ? 2 : 1) distil
     if (k > 1) cluster_sync_converged();  // no CTA leaves while its shared memory may be written
 }
 
-std::mutex g_ds_mu;
-std::map<std::pair<int, const void*>, size_t> g_ds_attr;  // (device, kernel): dynamic shared memory allowed
-
 template <int ES, bool GRAD, bool TWO, int NT>
 cudaError_t launch_typed(DistillParams prm, int per_sm, cudaStream_t stream) {
     auto* kern = &distill_kernel<ES, GRAD, TWO, NT>;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
     StreamSrc& s = prm.src;
     s.buffers = kClosers;
     const size_t fixed = 1024 + 512 + sizeof(StreamBars) + sizeof(StatExchange) + sizeof(LongSums) +
@@ -359,15 +351,9 @@ cudaError_t launch_typed(DistillParams prm, int per_sm, cudaStream_t stream) {
     const size_t room = std::min<size_t>((228 * 1024) / per_sm, 227 * 1024) - fixed;
     s.stages = static_cast<int>(std::min<size_t>(kStreamMaxStages, room / Shape<NT>::kStageBytes));
     const size_t smem = static_cast<size_t>(s.stages) * Shape<NT>::kStageBytes;
-    {
-        std::lock_guard<std::mutex> lock(g_ds_mu);
-        size_t& set = g_ds_attr[std::make_pair(dev, reinterpret_cast<const void*>(kern))];
-        if (set < smem) {
-            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-            if (e != cudaSuccess) return e;
-            set = smem;
-        }
-    }
+    static SmemLimit limit;
+    const cudaError_t e = limit.allow(reinterpret_cast<const void*>(kern), smem);
+    if (e != cudaSuccess) return e;
     const int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(s.N, static_cast<int64_t>(device_sm_count()) * per_sm / s.k));
     if (!set_rows(s, clusters)) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};

@@ -28,8 +28,6 @@
 // long rows.  With top tokens a row's end is some 10000 cycles alone, three times that
 // beside warps that sum: short rows and few rows pay for it.
 #include <algorithm>
-#include <map>
-#include <mutex>
 
 #include "row_stream.cuh"
 
@@ -896,15 +894,9 @@ __global__ void __launch_bounds__(kLogprobThreads<TOPK>, 3) logprobs_kernel(cons
     if (k > 1) cluster_sync_converged();  // no CTA leaves while its shared memory may be read
 }
 
-std::mutex g_lp_mu;
-std::map<std::pair<int, const void*>, size_t> g_lp_attr;  // (device, kernel): dynamic shared memory allowed
-
 template <int ES, bool ENT, bool TOPK>
 cudaError_t launch_typed(LogprobParams prm, cudaStream_t stream) {
     auto* kern = &logprobs_kernel<ES, ENT, TOPK>;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
     StreamSrc& s = prm.src;
     const int sms = device_sm_count();
     const int64_t nb = s.V * ES / 16 + 1;
@@ -941,15 +933,9 @@ cudaError_t launch_typed(LogprobParams prm, cudaStream_t stream) {
     s.stages = static_cast<int>(std::min<size_t>(kStreamMaxStages, room / Sh::kStageBytes));
     prm.max_bytes = static_cast<int>(buffer * s.buffers);
     const size_t smem = static_cast<size_t>(s.stages) * Sh::kStageBytes + prm.max_bytes + lists;
-    {
-        std::lock_guard<std::mutex> lock(g_lp_mu);
-        size_t& set = g_lp_attr[std::make_pair(dev, reinterpret_cast<const void*>(kern))];
-        if (set < smem) {
-            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-            if (e != cudaSuccess) return e;
-            set = smem;
-        }
-    }
+    static SmemLimit limit;
+    const cudaError_t e = limit.allow(reinterpret_cast<const void*>(kern), smem);
+    if (e != cudaSuccess) return e;
     const int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(s.N, static_cast<int64_t>(sms) * per_sm / s.k));
     if (!set_rows(s, clusters)) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};

@@ -31,6 +31,8 @@
 
 #include <float.h>
 
+#include <mutex>
+
 #include "common.cuh"
 #include "foak_ce.h"
 #include "internal.h"
@@ -97,6 +99,27 @@ __device__ __forceinline__ void cluster_sync_converged() {
     __syncwarp();
     cluster_sync();
 }
+
+// The dynamic shared memory that a kernel has been allowed on each device; it is only ever raised.
+// (A fixed array: nothing on the way to a launch allocates, so nothing can throw out of a C entry.)
+struct SmemLimit {
+    static constexpr int kDevices = 64;
+    std::mutex mu;
+    size_t allowed[kDevices] = {};
+
+    cudaError_t allow(const void* kern, size_t bytes) {
+        int dev = 0;
+        const cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
+        std::lock_guard<std::mutex> lock(mu);
+        if (allowed[dev] >= bytes) return cudaSuccess;
+        const cudaError_t set =
+            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+        if (set == cudaSuccess) allowed[dev] = bytes;
+        return set;
+    }
+};
 
 // Launch the work of a cluster size that is a power of two.
 inline void set_cluster(StreamSrc& p, int k) {
