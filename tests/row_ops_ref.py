@@ -132,6 +132,14 @@ def close(got, ref, tol, what):
                              f"reference {float(ref[i])!r}, tolerance {float(tol[i]):.3g}")
 
 
+def tops_equal(got, want):
+    """The top tokens' ids (int32, on the GPU or not) are the reference's, in its order."""
+    assert got.dtype == torch.int32 and got.shape == want.shape
+    got = got.detach().cpu().long()
+    off = (got != want).any(1)
+    assert not off.any(), f"top ids of {int(off.sum())} rows: {got[off][:2]}, reference {want[off][:2]}"
+
+
 def grad_close(got, ref, size, what="dlogits"):
     half = HALF_STEP[got.dtype]
     # 1e-37: an exponential below the least normal float is 0

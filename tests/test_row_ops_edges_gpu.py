@@ -85,12 +85,74 @@ def test_log_probabilities_at_far_exponents(cuda_lib, dtype, V, T):
     for k in ("lse", "logp", "top_logprobs"):
         ref.close(out[k], want[k], ref.value_tol(want[k]), k)
     ref.close(out["entropy"], want["entropy"], ref.entropy_tol(V), "entropy")
-    assert torch.equal(out["top_ids"].cpu().long(), want["top_ids"])
+    ref.tops_equal(out["top_ids"], want["top_ids"])
     gl, gh = torch.linspace(-1, 1, N), torch.linspace(0.5, -0.7, N)
     dx, _ = ce.foak_logprobs_backward(xd, y.cuda(), out["stats"], gl.cuda(), out["entropy"], gh.cuda(), temperature=T)
     g, size = ref.logprobs_grad(want, y, T, gl, gh)
     # p (ln p + H) of a flushed p has a factor up to 126 ln 2 + ln V more
     _close_gradient(dx, g, size, 101 * LEAST / T)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("N,V,K", [(1, 1, 1), (5, 7, 0), (7, 8192, 20), (3, 50257, 0), (2, 128263, 40), (300, 4099, 0),
+                                   (200, 40001, 17), (64, 128256, 0)])
+def test_without_the_entropy(cuda_lib, dtype, N, V, K):
+    """want_entropy=False and no other output: the same values, masks and infinities among them."""
+    low = torch.finfo(dtype).min
+    x = ref.make_logits(N, V, dtype, seed=N + V)
+    r = np.random.default_rng(7)
+    for i in range(N):
+        drop = torch.from_numpy(r.random(V) < 0.5)
+        kind = i % 8
+        if kind == 1:
+            x[i, drop] = -math.inf
+        elif kind == 2:
+            x[i, drop] = low
+        elif kind == 3:
+            x[i] = -math.inf
+        elif kind == 4:
+            x[i] = low
+        elif kind == 5:
+            x[i] = x[i] * 1e30
+        elif kind == 6:
+            x[i] = -math.inf
+            x[i, drop] = low
+    y = _labels(N, V, 8)
+    y[N // 3::11] = -100
+    T = 0.7 if V % 2 else 1.0
+    want = ref.logprobs(x, y, K, T)
+    for k in ("lse", "logp"):  # the lowest value over T < 1 is out of float32's range
+        want[k] = want[k].float().double()
+    xd = ref.to_gpu(x)
+    out = cuda_lib.foak_logprobs_forward(xd, y.cuda(), top_k=K, temperature=T, want_entropy=False)
+    assert out["entropy"] is None
+    keys = ("lse", "logp") + (("top_logprobs",) if K else ())
+    for k in keys:
+        ref.close(out[k], want[k], ref.value_tol(want[k]), k)
+    if K:
+        ref.tops_equal(out["top_ids"], want["top_ids"])
+    gl = torch.linspace(-1, 1, N)
+    dx, _ = cuda_lib.foak_logprobs_backward(xd, y.cuda(), out["stats"], gl.cuda(), temperature=T)
+    ref.grad_close(dx, *ref.logprobs_grad(want, y, T, gl, None))
+    only = cuda_lib.foak_logprobs_forward(xd, y.cuda(), top_k=K, temperature=T, want_entropy=False, want_lse=False,
+                                          want_stats=False)
+    assert only["lse"] is None and only["stats"] is None and torch.equal(only["logp"], out["logp"])
+    # every row, and no output at all but the top tokens
+    want = ref.logprobs(x, None, K, T)
+    out = cuda_lib.foak_logprobs_forward(xd, None, top_k=K, temperature=T, want_entropy=False)
+    want["lse"] = want["lse"].float().double()
+    ref.close(out["lse"], want["lse"], ref.value_tol(want["lse"]), "lse")
+    if K:
+        ref.tops_equal(out["top_ids"], want["top_ids"])
+
+
+def test_without_the_entropy_nan_stays_in_its_row(cuda_lib):
+    for dtype in (BF16, F32):
+        for N, V, K in ((5, 33000, 0), (5, 128256, 6)):
+            x = ref.make_logits(N, V, dtype, seed=2)
+            x[1, 20000], x[3, 31] = math.nan, math.inf
+            out = cuda_lib.foak_logprobs_forward(ref.to_gpu(x), None, top_k=K, want_entropy=False)
+            assert torch.isnan(out["lse"]).tolist() == [False, True, False, True, False]
 
 
 # Rows with a logit 0 at every 64th place and a logit c at the others: every warp's maximum is 0
@@ -260,7 +322,7 @@ def test_rows_about_the_borders_of_the_cluster_sizes(cuda_lib, dtype):
         for k in (8, 4, 2, 1):
             for N in sorted({max(1, at_most // k), at_most // k + 1, 1}):
                 out = ce.foak_logprobs_forward(xd[:N], yd[:N], top_k=K)
-                assert torch.equal(out["top_ids"].cpu().long(), ids[:N])
+                ref.tops_equal(out["top_ids"], ids[:N])
                 ref.close(out["logp"], logp[:N], ref.value_tol(logp[:N]), "logp")
                 out = ce.foak_logprobs_forward(xd[:N], yd[:N])
                 ref.close(out["lse"], want["lse"].expand(N), ref.value_tol(want["lse"]).expand(N), "lse")
