@@ -121,6 +121,7 @@ def _check(status: int, where: str):
         raise FoakError(status, where)
 
 
+@functools.lru_cache(maxsize=1024)  # a number of N alone; the foreign call takes as long as a small allocation
 def foak_ce_workspace_size(N: int) -> int:
     return int(lib.foak_ce_workspace_size(int(N)))
 
@@ -222,18 +223,18 @@ def _labels_arg(labels, N, device):
     return labels
 
 
-def _cached_workspace(cache: dict, need: int, device, fill=torch.zeros) -> torch.Tensor:
+def _cached_workspace(cache: dict, need: int, device, handle, fill=torch.zeros) -> torch.Tensor:
     """A buffer of ``need`` bytes or more, zeros before its first use: the current stream's own in
-    ``cache``, or a new one while that stream is captured into a graph.
+    ``cache`` (``handle`` is the stream's), or a new one while that stream is captured into a graph.
 
     The calls of a stream run one after another and leave the buffer zeroed; calls of
     two streams may overlap, and must not count in one header.  A graph's replays overlap with
     anything, and outlive a cached buffer that a larger call replaces: each captured call has a
     buffer of the graph's memory, filled by the graph.
     """
-    if torch.cuda.is_current_stream_capturing():
+    if handle and torch.cuda.is_current_stream_capturing():  # the legacy stream, 0, cannot be
         return fill(need, dtype=torch.uint8, device=device)
-    key = (device, _stream_handle(device, None))
+    key = (device, handle)
     ws = cache.get(key)
     if ws is None or ws.numel() < need:
         with _ws_lock:
@@ -252,13 +253,18 @@ def workspace(N: int, device) -> torch.Tensor:
     this function gives a new buffer, which the graph fills with zeros: pass ``workspace_tensor``
     to captured calls to be without that step, one buffer for the graph's calls on one stream.
     """
-    return _cached_workspace(_ws_cache, foak_ce_workspace_size(N), _device_of(device))
+    dev = _device_of(device)
+    return _cached_workspace(_ws_cache, foak_ce_workspace_size(N), dev, _stream_handle(dev, None))
 
 
 def _workspace_arg(ws, device) -> torch.Tensor:
     if ws.device != device:
         raise ValueError("workspace_tensor must live on the logits' device")
     return ws
+
+
+def _workspace_or_cached(ws, need: int, device, handle) -> torch.Tensor:
+    return _cached_workspace(_ws_cache, need, device, handle) if ws is None else _workspace_arg(ws, device)
 
 
 def _device_of(device) -> torch.device:
@@ -540,7 +546,9 @@ def foak_linear_ce_chunked(H, W, labels, *, chunk: int = 1024, g: float = 1.0, i
     n_valid = torch.empty(1, dtype=torch.int32, device=dev)
     err = torch.empty(1, dtype=torch.int32, device=dev)
     need = foak_linear_ce_workspace_size(N, V, D, chunk)
-    ws = _cached_workspace(_lin_ws, need, dev) if workspace_tensor is None else workspace_tensor
+    ws = workspace_tensor
+    if ws is None:
+        ws = _cached_workspace(_lin_ws, need, dev, _stream_handle(dev, None))
     st = lib.foak_linear_ce_chunked(_ptr(H), _ptr(W), _ptr(labels), N, V, D, int(ignore_index), int(chunk), float(g),
                                     float(denom), _ptr(loss), _ptr(dH), _ptr(dW), _ptr(n_valid), _ptr(err), _ptr(ws),
                                     ws.numel(), _stream(dev, stream))
@@ -588,7 +596,7 @@ def foak_rmsnorm_backward(dY, X, gamma, rstd, *, dX=None, want_dgamma: bool = Tr
     dgamma = torch.empty(D, dtype=torch.float32, device=dev) if want_dgamma else None
     need = int(lib.foak_rmsnorm_workspace_size(D))
     # partial sums only: each is written before it is read
-    ws = _cached_workspace(_norm_ws, need, dev, fill=torch.empty)
+    ws = _cached_workspace(_norm_ws, need, dev, _stream_handle(dev, None), fill=torch.empty)
     st = lib.foak_rmsnorm_backward(_ptr(dY), lddy, _ptr(X), ldx, _ptr(gamma), _ptr(rstd), _DT[X.dtype], N, D, _ptr(dX),
                                    lddx, _ptr(dgamma), _ptr(ws), ws.numel(), _stream(dev, stream))
     _check(st, "foak_rmsnorm_backward")
@@ -620,7 +628,9 @@ def foak_rmsnorm_linear_ce_chunked(X, gamma, W, labels, *, eps: float = 1e-5, ch
     n_valid = torch.empty(1, dtype=torch.int32, device=dev)
     err = torch.empty(1, dtype=torch.int32, device=dev)
     need = int(lib.foak_rmsnorm_linear_ce_workspace_size(N, V, D, chunk))
-    ws = _cached_workspace(_norm_lin_ws, need, dev) if workspace_tensor is None else workspace_tensor
+    ws = workspace_tensor
+    if ws is None:
+        ws = _cached_workspace(_norm_lin_ws, need, dev, _stream_handle(dev, None))
     st = lib.foak_rmsnorm_linear_ce_chunked(_ptr(X), _ptr(gamma), _ptr(W), _ptr(labels), N, V, D, int(ignore_index),
                                             int(chunk), float(eps), float(g), float(denom), _ptr(loss), _ptr(dX),
                                             _ptr(dgamma), _ptr(dW), _ptr(n_valid), _ptr(err), _ptr(ws), ws.numel(),
@@ -742,11 +752,11 @@ def foak_logprobs_forward(logits, labels=None, *, top_k: int = 0, temperature: f
     top_lp = torch.empty(N, K, dtype=f32, device=dev) if K else None
     top_ids = torch.empty(N, K, dtype=torch.int32, device=dev) if K else None
     err = torch.empty(1, dtype=torch.int32, device=dev)
-    ws = workspace_tensor
-    ws = _cached_workspace(_ws_cache, _HEADER_BYTES, dev) if ws is None else _workspace_arg(ws, dev)
+    handle = _stream_handle(dev, stream)
+    ws = _workspace_or_cached(workspace_tensor, _HEADER_BYTES, dev, handle)
     st = lib.foak_logprobs_forward(_addr(logits), dt, ld, _addr(labels), N, V, int(ignore_index), float(temperature), K,
                                    _addr(logp), _addr(entropy), _addr(lse), _addr(stats), _addr(top_lp),
-                                   _addr(top_ids), _addr(err), _addr(ws), ws.numel(), _stream_handle(dev, stream))
+                                   _addr(top_ids), _addr(err), _addr(ws), ws.numel(), handle)
     _check(st, "foak_logprobs_forward")
     return dict(logp=logp, entropy=entropy, lse=lse, stats=stats, top_logprobs=top_lp, top_ids=top_ids, err=err)
 
@@ -822,12 +832,12 @@ def foak_distill_forward(logits, labels, teacher_ids, teacher_logprobs, *, ce_we
     stats = torch.empty(N, 4, dtype=f32, device=dev) if want_stats else None
     n_valid = torch.empty(1, dtype=torch.int32, device=dev)
     err = torch.empty(1, dtype=torch.int32, device=dev)
-    ws = workspace(N, dev) if workspace_tensor is None else _workspace_arg(workspace_tensor, dev)
+    handle = _stream_handle(dev, stream)
+    ws = _workspace_or_cached(workspace_tensor, foak_ce_workspace_size(N), dev, handle)
     st = lib.foak_distill_forward(_addr(logits), dt, ld, _addr(labels), N, V, int(ignore_index), _addr(teacher_ids),
                                   _addr(teacher_logprobs), ldt, K, int(bool(normalize)), float(ce_weight),
                                   float(kd_weight), float(temperature), float(denom), _addr(loss), _addr(row_ce),
-                                  _addr(row_kd), _addr(stats), _addr(n_valid), _addr(err), _addr(ws), ws.numel(),
-                                  _stream_handle(dev, stream))
+                                  _addr(row_kd), _addr(stats), _addr(n_valid), _addr(err), _addr(ws), ws.numel(), handle)
     _check(st, "foak_distill_forward")
     return dict(loss=loss, row_ce=row_ce, row_kd=row_kd, stats=stats, n_valid=n_valid, err=err)
 
@@ -853,12 +863,13 @@ def foak_distill_fwd_bwd(logits, labels, teacher_ids, teacher_logprobs, *, ce_we
     row_kd = torch.empty(N, dtype=f32, device=dev) if want_rows else None
     n_valid = torch.empty(1, dtype=torch.int32, device=dev)
     err = torch.empty(1, dtype=torch.int32, device=dev)
-    ws = workspace(N, dev) if workspace_tensor is None else _workspace_arg(workspace_tensor, dev)
+    handle = _stream_handle(dev, stream)
+    ws = _workspace_or_cached(workspace_tensor, foak_ce_workspace_size(N), dev, handle)
     st = lib.foak_distill_fwd_bwd(_addr(logits), _addr(dlogits), dt, ld, _addr(labels), N, V, int(ignore_index),
                                   _addr(teacher_ids), _addr(teacher_logprobs), ldt, K, int(bool(normalize)),
                                   float(ce_weight), float(kd_weight), float(temperature), float(g), float(denom),
                                   _addr(loss), _addr(row_ce), _addr(row_kd), _addr(n_valid), _addr(err), _addr(ws),
-                                  ws.numel(), _stream_handle(dev, stream))
+                                  ws.numel(), handle)
     _check(st, "foak_distill_fwd_bwd")
     return dict(loss=loss, dlogits=dlogits, row_ce=row_ce, row_kd=row_kd, n_valid=n_valid, err=err)
 
