@@ -17,8 +17,9 @@
 //
 // Measured, bf16: 8192 x 128256, K = 128, loss and gradient 667 us (6.15 TB/s read and
 // written); 4096 x 32000, K = 64: 96 us at T = 1 (5.5 TB/s), 117 at T = 2 with a cross-entropy
-// part; the loss alone 53 and 62.  HBM bounds the long rows, issue slots (64% taken, two
-// exponentials an element and sweep) the short ones at T = 2.
+// part; the loss alone 53 and 62.  HBM bounds the long rows; the short ones at
+// T = 2 take two exponentials an element and sweep (64% of the issue slots) and wait between a
+// row's two sweeps.
 #include <algorithm>
 
 #include "row_stream.cuh"

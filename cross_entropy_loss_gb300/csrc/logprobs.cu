@@ -44,7 +44,8 @@ static_assert(kTopKMaxVocab <= static_cast<int64_t>(kRunVec<kThreads>) * 4, "row
 constexpr int kBodyAt = 8;      // place of the first body block's maximum; before it the head's and the tail's
 // Closing warps of a CTA.  The work on a row's top tokens is a chain of 10000 cycles or more,
 // so three take rows in turn (8192 x 128256, K = 128: two with two CTAs an SM 464 us, three
-// with three 454, four 487, as their registers spill); without top tokens one keeps up.
+// with three 454, four 487); without top tokens one keeps up.  At three CTAs an SM a thread
+// has 56 registers, and their code spills (about 320 bytes of stores in close_rows).
 template <bool TOPK>
 constexpr int kClosers = TOPK ? 3 : 1;
 

@@ -15,8 +15,9 @@
 //
 // HBM bounds both.  Log probabilities and entropy: 8192 x 128256 bf16 670 us (6.3 TB/s read and
 // written), 4096 x 32000 87 us (6.0).  Distillation, K = 128: 8192 x 128256
-// 725 us (5.8 TB/s), 4096 x 32000, K = 64: 91 us.  No ring here: a thread's own 128 bytes in flight times
-// 1024 threads an SM are twice what covers the latency, and nothing is read twice.
+// 725 us (5.8 TB/s), 4096 x 32000, K = 64: 91 us, and 1 to 3 us for clearing its error word.  No
+// ring here: a thread's own 128 bytes in flight times 1024 threads an SM are twice what covers
+// the latency, and nothing is read twice.
 #include <algorithm>
 
 #include "common.cuh"
@@ -33,7 +34,7 @@ constexpr int kGradThreads = 256;
 constexpr int kGradVpt = 8;
 constexpr int kGradSegVec = kGradThreads * kGradVpt;  // 32 KB
 constexpr int kGradBlocksPerSm = 4;
-constexpr int kTeacherBlocksPerSm = 3;  // 8192 x 128256 bf16, K = 128: 718 us, by four (their registers spill) 742
+constexpr int kTeacherBlocksPerSm = 3;  // 8192 x 128256 bf16, K = 128: 718 us, by four 742 (at three 24-60 bytes spill)
 
 struct RowsGradParams {
     StreamSrc src;
@@ -329,7 +330,8 @@ __global__ void __launch_bounds__(kGradThreads + 32, kTeacherBlocksPerSm) distil
             atomicOr(reinterpret_cast<unsigned*>(p.err), static_cast<unsigned>(FOAK_ERRBIT_LABEL_RANGE));
     }
     __syncthreads();
-    if (s_abort && tid == 0 && p.err) atomicOr(reinterpret_cast<unsigned*>(p.err), static_cast<unsigned>(FOAK_ERRBIT_TIMEOUT));
+    if (s_abort && tid == 0 && p.err)
+        atomicOr(reinterpret_cast<unsigned*>(p.err), static_cast<unsigned>(FOAK_ERRBIT_TIMEOUT));
 }
 
 RowsGradParams common_params(int es, const void* x, void* dx, int64_t ld, const int64_t* labels, int64_t N, int64_t V,
@@ -393,7 +395,7 @@ cudaError_t launch_distill_grad(int es, const void* x, void* dx, int64_t ld, con
     p.kd_w = kd_w;
     // Any CTA may have a bit for the error word, and no memory here is known to be 0 for a count
     // of those that are done: so the word is cleared by a step of its own (515 x 49159 fp32, the
-    // backward alone: 42.4 -> 45.5 us; behind its forward, which it no longer starts under, 69 -> 65).
+    // backward alone: 42.8 -> 45.8 us; behind its forward, which it no longer starts under, 69.8 -> 65.3).
     if (err) {
         const cudaError_t e = cudaMemsetAsync(err, 0, sizeof(int32_t), stream);
         if (e != cudaSuccess) return e;
