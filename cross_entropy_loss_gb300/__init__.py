@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 import threading
 
@@ -29,10 +30,12 @@ FOAK_ERR_LABEL_RANGE = 3
 FOAK_ERR_WORKSPACE = 4
 FOAK_ERR_CUDA = 5
 FOAK_ERR_TIMEOUT = 6
+FOAK_ERR_PAGE_RANGE = 7
 FOAK_F32 = 0
 FOAK_BF16 = 1
 FOAK_ERRBIT_LABEL_RANGE = 1
 FOAK_ERRBIT_TIMEOUT = 2
+FOAK_ERRBIT_PAGE_RANGE = 4
 
 # C entry points and their ctypes signatures (restype, argtypes).
 _vp, _i32, _i64, _f32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
@@ -83,6 +86,21 @@ SIGNATURES = {
                                     _f32, _f32, _f32, _f32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "foak_distill_backward": (_i32, [_vp, _vp, _i32, _i64, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _i32, _f32,
                                      _f32, _f32, _vp, _vp, _f32, _vp, _vp]),
+    "foak_residual_norm_forward": (_i32, [_vp, _i64, _vp, _i64, _i32, _i64, _i64, _vp, _i32, _i64, _vp, _vp, _f32, _f32,
+                                          _f32, _vp, _i64, _vp, _i64, _vp, _vp, _vp]),
+    "foak_residual_norm_workspace_size": (_sz, [_i64, _i64]),
+    "foak_residual_norm_backward": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i32, _i64, _i64, _vp, _i32, _i64,
+                                           _vp, _vp, _vp, _vp, _f32, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _sz,
+                                           _vp]),
+    "foak_rotary_inv_freq": (_i32, [ctypes.c_double, _i64, _i32, ctypes.c_double, ctypes.c_double, ctypes.c_double,
+                                    ctypes.c_double, _vp]),
+    "foak_rotary_turns": (_i32, [_vp, _i64, _vp]),
+    "foak_rotary_apply": (_i32, [_vp, _i64, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _i64, _i32,
+                                 _i64, _i64, _i64, _i32, _vp, _vp, _f32, _i32, _vp]),
+    "foak_kv_slots": (_i32, [_vp, _i64, _i64, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp]),
+    "foak_kv_append": (_i32, [_vp, _i64, _i64, _vp, _i64, _i64, _i64, _i32, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _i64,
+                              _vp, _i64, _i64, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _i64, _i64, _i32, _vp,
+                              _vp, _f32, _vp, _vp]),
     "foak_test_fail_next_launches": (None, [_i32]),
     "foak_test_set_wait_limit_ns": (None, [ctypes.c_uint64]),
     "foak_test_skip_row_load": (None, [_i64]),
@@ -168,7 +186,7 @@ def _tensors_of(out):
     if isinstance(out, torch.Tensor):
         return [out]
     values = out.values() if isinstance(out, dict) else out if isinstance(out, (tuple, list)) else ()
-    return [t for t in values if isinstance(t, torch.Tensor)]
+    return [t.turns if isinstance(t, RotaryPlan) else t for t in values if isinstance(t, (torch.Tensor, RotaryPlan))]
 
 
 def _on_stream(call):
@@ -897,3 +915,403 @@ def foak_distill_backward(logits, labels, teacher_ids, teacher_logprobs, stats, 
                                    _addr(grad_out), float(denom), _addr(err), _stream_handle(dev, stream))
     _check(st, "foak_distill_backward")
     return dlogits, err
+
+
+# --------------------------------------------------------------------- residual norms
+FOAK_GATE_NONE, FOAK_GATE_CHANNEL, FOAK_GATE_ROW, FOAK_GATE_FULL = 0, 1, 2, 3
+FOAK_RESIDUAL_NORM_MAX_D = 32768
+_resnorm_ws: dict = {}
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _launch(dev, call, *args):
+    """``call(*args)`` with the tensors' device as the current one, as a launch on its stream wants."""
+    if dev.index == _current_device():
+        return call(*args)
+    with torch.cuda.device(dev):
+        return call(*args)
+
+
+@functools.lru_cache(maxsize=1024)
+def foak_residual_norm_workspace_size(N: int, D: int) -> int:
+    return int(lib.foak_residual_norm_workspace_size(int(N), int(D)))
+
+
+def _like_rows(t, X, name):
+    """``t``'s row stride, for a tensor of X's shape, type and device."""
+    if t.shape != X.shape or t.dtype != X.dtype or t.device != X.device or t.stride(1) != 1:
+        raise ValueError(f"{name} must be like the block's rows: shape, dtype, device, unit column stride")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _channels(t, X, name):
+    if t is not None and (t.dim() != 1 or t.shape[0] != X.shape[1] or t.dtype != X.dtype or t.device != X.device
+                          or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous vector of D elements in the rows' dtype, on their device")
+    return t
+
+
+def _gate_arg(gate, X):
+    """(kind, stride): [D] is a gate a channel, [N, 1] one a row, [N, D] one an element."""
+    if gate is None:
+        return FOAK_GATE_NONE, 0
+    if gate.dim() == 1:
+        _channels(gate, X, "gate")
+        return FOAK_GATE_CHANNEL, 0
+    if gate.dim() == 2 and gate.shape[1] == 1 and gate.shape[0] == X.shape[0]:
+        if gate.dtype != X.dtype or gate.device != X.device:
+            raise ValueError("gate must have the rows' dtype and device")
+        return FOAK_GATE_ROW, (gate.stride(0) if gate.shape[0] > 1 else 1)
+    return FOAK_GATE_FULL, _like_rows(gate, X, "gate")
+
+
+def _rstd_arg(t, X, name):
+    if t.dtype != torch.float32 or t.numel() != X.shape[0] or not t.is_contiguous() or t.device != X.device:
+        raise ValueError(f"{name} must be a contiguous float32 vector of the N rows, on their device")
+    return t
+
+
+@_on_stream
+def foak_residual_norm_forward(X, R, gamma=None, *, gate=None, post_gamma=None, scale: float = 1.0, eps: float = 1e-5,
+                               post_eps: float | None = None, H=None, Y=None, want_rstd: bool = True, stream=None):
+    """H = R + scale * gate * u with u = X, or the RMSNorm of X by ``post_gamma``; Y = RMSNorm of H by ``gamma``.
+
+    X is a block's output, R the residual stream (bf16 or fp32, N x D), Y the next block's input,
+    computed from H before it is rounded.  ``gate`` is [D], [N, 1], [N, D] or None; without
+    ``gamma`` there is no Y.  ``H=R`` (or X) updates the stream in place.  ``post_eps`` defaults to
+    ``eps``.  Returns dict(H, Y, rstd, post_rstd); the last two (float32 [N]) are for
+    :func:`foak_residual_norm_backward`, None unless ``want_rstd`` and their norm is there.
+    """
+    N, D, ldx = _rows_arg(X, "X")
+    dev = X.device
+    ldr = _like_rows(R, X, "R")
+    _channels(gamma, X, "gamma")
+    _channels(post_gamma, X, "post_gamma")
+    kind, ldg = _gate_arg(gate, X)
+    if Y is not None and gamma is None:
+        raise ValueError("Y needs gamma")
+    H = torch.empty(N, D, dtype=X.dtype, device=dev) if H is None else H
+    ldh, ldy = _like_rows(H, X, "H"), 0
+    if gamma is not None:
+        Y = torch.empty(N, D, dtype=X.dtype, device=dev) if Y is None else Y
+        ldy = _like_rows(Y, X, "Y")
+    rstd = torch.empty(N, dtype=torch.float32, device=dev) if want_rstd and gamma is not None else None
+    post = torch.empty(N, dtype=torch.float32, device=dev) if want_rstd and post_gamma is not None else None
+    st = _launch(dev, lib.foak_residual_norm_forward, _addr(X), ldx, _addr(R), ldr, _DT[X.dtype], N, D, _addr(gate), kind,
+                 ldg, _addr(post_gamma), _addr(gamma), scale, eps if post_eps is None else post_eps, eps, _addr(H), ldh,
+                 _addr(Y), ldy, _addr(post), _addr(rstd), _stream_handle(dev, stream))
+    _check(st, "foak_residual_norm_forward")
+    return dict(H=H, Y=Y, rstd=rstd, post_rstd=post)
+
+
+@_on_stream
+def foak_residual_norm_backward(dY, dH, H=None, rstd=None, gamma=None, *, X=None, gate=None, post_gamma=None,
+                                post_rstd=None, scale: float = 1.0, dR=None, dX=None, want_dX: bool = True,
+                                want_dgate: bool = True, want_dgamma: bool = True, workspace_tensor=None, stream=None):
+    """Gradients of :func:`foak_residual_norm_forward` from ``dY`` and from ``dH``, what arrives along
+    the residual stream (either may be None: zero; without ``dY``, H, rstd and gamma are not needed).
+
+    H, rstd and post_rstd are the forward's; X is needed with ``post_gamma`` or for the gate's
+    gradient; the other arguments as given there.  Returns dict(dR, dX, dgamma, dgate,
+    dpost_gamma): dR and dX like the rows; dgamma, dpost_gamma float32 [D]; dgate float32 [D] or
+    [N, 1], or like a full gate.  Without gate and ``post_gamma`` and with ``scale`` 1, dX is dR,
+    the same tensor, unless ``dX`` is given.
+    """
+    like = dH if dY is None else dY
+    if like is None:
+        raise ValueError("dY or dH must be given")
+    N, D, _ = _rows_arg(like, "dY or dH")
+    dev, f32 = like.device, torch.float32
+    lddy = lddh = ldh = ldx = lddx = lddg = 0
+    kind, ldg = _gate_arg(gate, like)
+    want_dgate = want_dgate and gate is not None
+    if dY is not None:
+        lddy = _like_rows(dY, like, "dY")
+        if H is None or rstd is None or gamma is None:
+            raise ValueError("dY needs the forward's H, rstd and gamma")
+        ldh = _like_rows(H, like, "H")
+        _rstd_arg(rstd, like, "rstd")
+        _channels(gamma, like, "gamma")
+    if dH is not None:
+        lddh = _like_rows(dH, like, "dH")
+    if post_gamma is not None or want_dgate:
+        if X is None:
+            raise ValueError("post_gamma and the gate's gradient need X")
+        ldx = _like_rows(X, like, "X")
+    else:
+        X = None
+    if post_gamma is not None:
+        if post_rstd is None:
+            raise ValueError("post_gamma needs the forward's post_rstd")
+        _channels(post_gamma, like, "post_gamma")
+        _rstd_arg(post_rstd, like, "post_rstd")
+    dR = torch.empty(N, D, dtype=like.dtype, device=dev) if dR is None else dR
+    lddr = _like_rows(dR, like, "dR")
+    same = dX is None and gate is None and post_gamma is None and scale == 1.0
+    if want_dX and dX is None and not same:
+        dX = torch.empty(N, D, dtype=like.dtype, device=dev)
+    if dX is not None:
+        lddx = _like_rows(dX, like, "dX")
+    dgamma = torch.empty(D, dtype=f32, device=dev) if want_dgamma and dY is not None else None
+    dpost = torch.empty(D, dtype=f32, device=dev) if want_dgamma and post_gamma is not None else None
+    dgate = None
+    if want_dgate:
+        if kind == FOAK_GATE_FULL:
+            dgate, lddg = torch.empty(N, D, dtype=like.dtype, device=dev), D
+        else:
+            dgate = torch.empty((D,) if kind == FOAK_GATE_CHANNEL else (N, 1), dtype=f32, device=dev)
+    handle = _stream_handle(dev, stream)
+    need = foak_residual_norm_workspace_size(N, D)
+    if workspace_tensor is None:  # partial sums only: each is written before it is read
+        ws = _cached_workspace(_resnorm_ws, need, dev, handle, fill=torch.empty)
+    else:
+        ws = _workspace_arg(workspace_tensor, dev)
+    st = _launch(dev, lib.foak_residual_norm_backward, _addr(dY), lddy, _addr(dH), lddh, _addr(H) if lddy else None, ldh,
+                 _addr(X), ldx, _DT[like.dtype], N, D, _addr(gate), kind, ldg, _addr(post_gamma),
+                 _addr(gamma) if lddy else None, _addr(post_rstd), _addr(rstd) if lddy else None, scale, _addr(dR), lddr,
+                 _addr(dX), lddx, _addr(dgamma), _addr(dgate), lddg, _addr(dpost), _addr(ws), ws.numel(), handle)
+    _check(st, "foak_residual_norm_backward")
+    return dict(dR=dR, dX=dR if same and want_dX else dX, dgamma=dgamma, dgate=dgate, dpost_gamma=dpost)
+
+
+# --------------------------------------------------------------------- rotary positions
+FOAK_ROTARY_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "bands": 3, "ramp": 4}
+
+
+class RotaryPlan:
+    """What :func:`foak_rotary_apply` and :func:`foak_kv_append` need of a model's rotary embedding: made once
+    by :func:`foak_rotary_plan` and kept as long as a graph that was captured with it is replayed."""
+
+    __slots__ = ("turns", "rotary_dim", "interleaved", "factor", "inv_freq")
+
+    def __init__(self, turns, rotary_dim, interleaved, factor, inv_freq):
+        self.turns, self.rotary_dim, self.interleaved = turns, rotary_dim, interleaved
+        self.factor, self.inv_freq = factor, inv_freq
+
+
+def foak_rotary_inv_freq(rotary_dim: int, *, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                         low: float = 1.0, high: float | None = None, original: float = 0.0):
+    """The rotary_dim / 2 angles a position (a list of floats): base^(-2i / rotary_dim), scaled for contexts
+    ``factor`` times ``original`` positions.  ``scaling``: "none"; "linear" (positions divided by the factor);
+    "ntk" (a larger base); "bands" (by the turns a frequency makes over ``original`` positions: stretched below
+    ``low``, kept above ``high``, 4 unless given); "ramp" (the same along the frequencies' index, ``high`` 32).
+    """
+    if scaling not in FOAK_ROTARY_SCALINGS:
+        raise ValueError(f"scaling must be one of {', '.join(FOAK_ROTARY_SCALINGS)}")
+    if rotary_dim < 2 or rotary_dim % 2 or rotary_dim > 65536:
+        raise ValueError("rotary_dim must be even, between 2 and 65536")
+    out = (ctypes.c_double * (rotary_dim // 2))()
+    high = (32.0 if scaling == "ramp" else 4.0) if high is None else high
+    _check(lib.foak_rotary_inv_freq(base, rotary_dim, FOAK_ROTARY_SCALINGS[scaling], factor, low, high, original, out),
+           "foak_rotary_inv_freq")
+    return list(out)
+
+
+def foak_rotary_turns(inv_freq):
+    """Angles a position as the device calls take them: int64 (fractions of a turn, times 2^64), on the CPU."""
+    n = len(inv_freq)
+    turns = (ctypes.c_int64 * n)()
+    _check(lib.foak_rotary_turns((ctypes.c_double * n)(*inv_freq), n, turns), "foak_rotary_turns")
+    return torch.tensor(list(turns), dtype=torch.int64)
+
+
+def foak_rotary_plan(rotary_dim: int, *, base: float = 10000.0, interleaved: bool = False, scaling: str = "none",
+                     factor: float = 1.0, low: float = 1.0, high: float | None = None, original: float = 0.0,
+                     inv_freq=None, attention_factor: float | None = None, device="cuda") -> RotaryPlan:
+    """A rotary embedding of a head's first ``rotary_dim`` elements, in pairs (i, i + rotary_dim / 2), or
+    (2i, 2i + 1) where ``interleaved``.
+
+    The frequencies are :func:`foak_rotary_inv_freq`'s, or ``inv_freq`` itself (rotary_dim / 2 numbers).
+    ``attention_factor`` multiplies what is rotated; by default 1, and 0.1 ln(factor) + 1 for "ramp".
+    """
+    if inv_freq is None:
+        inv_freq = foak_rotary_inv_freq(rotary_dim, base=base, scaling=scaling, factor=factor, low=low, high=high,
+                                        original=original)
+    else:
+        inv_freq = [float(f) for f in inv_freq]
+        if rotary_dim < 2 or rotary_dim % 2 or rotary_dim > 65536 or len(inv_freq) != rotary_dim // 2:
+            raise ValueError("inv_freq must have rotary_dim / 2 numbers")
+    if attention_factor is None:
+        attention_factor = 0.1 * math.log(factor) + 1.0 if scaling == "ramp" else 1.0
+    if not math.isfinite(attention_factor):
+        raise ValueError("attention_factor must be finite")
+    dev = _device_of(device)
+    turns = foak_rotary_turns(inv_freq).to(dev)
+    if dev.type == "cuda":
+        torch.cuda.current_stream(dev).synchronize()  # any stream may use the plan from here on
+    return RotaryPlan(turns, int(rotary_dim), bool(interleaved), float(attention_factor), inv_freq)
+
+
+def _heads_arg(x, name):
+    """(heads, token stride, head stride) of a T x H x d CUDA view."""
+    if x.dim() != 3 or x.dtype not in _DT or not x.is_cuda or (x.shape[2] > 1 and x.stride(2) != 1):
+        raise ValueError(f"{name} must be a T x H x d bfloat16/float32 CUDA view whose heads have unit stride")
+    T, H, d = x.shape
+    ldh = x.stride(1) if H > 1 else d
+    return H, (x.stride(0) if T > 1 else max(1, H * d)), ldh
+
+
+def _heads_like(x, like, name):
+    if x.dtype != like.dtype or x.device != like.device or x.shape[0] != like.shape[0]:
+        raise ValueError(f"{name} disagrees with the others on tokens, dtype or device")
+    return _heads_arg(x, name)
+
+
+def _plan_arg(plan, d, device):
+    if plan.turns.device != device:
+        raise ValueError("the plan must live on the heads' device")
+    if plan.rotary_dim > d:
+        raise ValueError("the plan rotates more elements than a head has")
+
+
+def _tokens_arg(t, T, device, name):
+    if t.dtype != torch.int64 or t.dim() != 1 or t.shape[0] != T or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous int64 vector of the T tokens, on the heads' device")
+
+
+def _heads_out(x, out, name):
+    """(output, token stride, head stride): ``out``, x itself among them, or a new contiguous tensor."""
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    elif out.shape != x.shape:
+        raise ValueError(f"{name} must have its input's shape")
+    _, ld, ldh = _heads_like(out, x, name)
+    return out, ld, ldh
+
+
+@_on_stream
+def foak_rotary_apply(plan, positions, q, k=None, *, q_out=None, k_out=None, inverse: bool = False, stream=None):
+    """Rotate ``q`` (T x Hq x d) and ``k`` (T x Hk x d) by the angles of ``positions`` (int64 [T]) in one
+    launch; with ``inverse`` back by the same angles, which is the gradients' way.
+
+    Views of any token and head strides (a fused QKV product's parts, heads first or tokens first).
+    Returns (q_out, k_out): new tensors unless given; ``q_out=q`` rotates in place.  Either of q and k may be None.
+    """
+    x = k if q is None else q
+    if x is None:
+        raise ValueError("q or k must be given")
+    none = (0, 0, 0)
+    Hq, ldq, ldqh = none if q is None else _heads_like(q, x, "q")
+    Hk, ldk, ldkh = none if k is None else _heads_like(k, x, "k")
+    T, _, d = x.shape
+    dev = x.device
+    if k is not None and k.shape[2] != d:
+        raise ValueError("q and k disagree on the head dimension")
+    _plan_arg(plan, d, dev)
+    _tokens_arg(positions, T, dev, "positions")
+    q_out, ldqo, ldqoh = none if q is None else _heads_out(q, q_out, "q_out")
+    k_out, ldko, ldkoh = none if k is None else _heads_out(k, k_out, "k_out")
+    q_out, k_out = (None if q is None else q_out), (None if k is None else k_out)
+    st = _launch(dev, lib.foak_rotary_apply, _addr(q), ldq, ldqh, _addr(q_out), ldqo, ldqoh, Hq, _addr(k), ldk, ldkh,
+                 _addr(k_out), ldko, ldkoh, Hk, _DT[x.dtype], T, d, plan.rotary_dim, plan.interleaved, _addr(positions),
+                 _addr(plan.turns), plan.factor, inverse, _stream_handle(dev, stream))
+    _check(st, "foak_rotary_apply")
+    return q_out, k_out
+
+
+# --------------------------------------------------------------------- paged cache
+def _int32_arg(t, dim, device, name):
+    if t.dtype != torch.int32 or t.dim() != dim or t.device != device or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must be a {dim}-D int32 tensor with unit stride on the page table's device")
+
+
+def _err_arg(err, device):
+    """A given error word, or a new one, zero."""
+    if err is None:
+        return torch.zeros(1, dtype=torch.int32, device=device)
+    if err.dtype != torch.int32 or err.numel() != 1 or err.device != device:
+        raise ValueError("err must be a one-element int32 tensor on the tensors' device")
+    return err
+
+
+@_on_stream
+def foak_kv_slots(page_table, cache_lens, seq_starts, T: int, *, page_size: int, num_pages: int, err=None, stream=None):
+    """Slots and positions of a serving step's T tokens in a paged cache, for the appends of all its layers.
+
+    ``page_table`` (int32 [B, max_pages]) lists each sequence's pages, ``cache_lens`` (int32 [B]) its tokens
+    in the cache before the step, ``seq_starts`` (int32 [B + 1], ascending) its first row.  Token t of sequence
+    b has position cache_lens[b] + t - seq_starts[b] and slot page * page_size + place; rows of no sequence are
+    padding: slot -1.  Returns dict(slots, positions, err): int64 [T] each; a page that is missing or not in
+    [0, num_pages) gives slot -1 and sets FOAK_ERRBIT_PAGE_RANGE in ``err``, which is OR-ed into: pass
+    a zeroed int32 tensor to keep one for many calls.
+    """
+    dev = page_table.device
+    if dev.type != "cuda":
+        raise ValueError("page_table must be on a CUDA device")
+    _int32_arg(page_table, 2, dev, "page_table")
+    _int32_arg(cache_lens, 1, dev, "cache_lens")
+    _int32_arg(seq_starts, 1, dev, "seq_starts")
+    B, most = page_table.shape
+    if cache_lens.shape[0] != B or seq_starts.shape[0] != B + 1:
+        raise ValueError("page_table, cache_lens and seq_starts disagree on the sequences")
+    T = int(T)
+    slots = torch.empty(T, dtype=torch.int64, device=dev)
+    positions = torch.empty(T, dtype=torch.int64, device=dev)
+    err = _err_arg(err, dev)
+    st = _launch(dev, lib.foak_kv_slots, _addr(page_table), page_table.stride(0) if B > 1 else most, most,
+                 _addr(cache_lens), _addr(seq_starts), B, T, page_size, num_pages, _addr(slots), _addr(positions),
+                 _addr(err), _stream_handle(dev, stream))
+    _check(st, "foak_kv_slots")
+    return dict(slots=slots, positions=positions, err=err)
+
+
+def _cache_arg(cache, like, heads_first, name):
+    """(pages, places, page stride, place stride, head stride) of a cache of ``like``'s heads."""
+    if cache.dim() != 4 or cache.dtype != like.dtype or cache.device != like.device:
+        raise ValueError(f"{name} must be 4-D, of the heads' dtype and device")
+    page, head = (2, 1) if heads_first else (1, 2)
+    if cache.shape[head] != like.shape[1] or cache.shape[3] != like.shape[2]:
+        raise ValueError(f"{name} disagrees with its rows on the heads or their size")
+    if cache.shape[3] > 1 and cache.stride(3) != 1:
+        raise ValueError(f"{name} must have unit stride along a head")
+    return cache.shape[0], cache.shape[page], cache.stride(0), cache.stride(page), cache.stride(head)
+
+
+@_on_stream
+def foak_kv_append(k, v, k_cache, v_cache, slots, *, heads_first: bool = False, plan=None, positions=None, q=None,
+                   q_out=None, err=None, stream=None):
+    """Append a step's keys and values to one layer's paged cache; with ``plan`` the keys are rotated on
+    the way by ``positions``, and ``q`` beside them, in the same launch.
+
+    k (T x Hk x d) and v (T x Hk x dv) are views of any token and head strides; the caches are
+    (pages, page_size, Hk, d), or (pages, Hk, page_size, d) with ``heads_first``, views too.  ``slots`` and
+    ``positions`` are :func:`foak_kv_slots`'s; of a token with a negative slot nothing is written, q's row
+    of ``q_out`` neither.  Returns q_out (a new tensor unless given, None without q).  A slot past the cache
+    sets FOAK_ERRBIT_PAGE_RANGE in ``err`` (OR-ed into), if given, and is left out.
+    """
+    Hk, ldk, ldkh = _heads_arg(k, "k")
+    T, _, d = k.shape
+    dev = k.device
+    Hv, ldv, ldvh = _heads_like(v, k, "v")
+    if Hv != Hk:
+        raise ValueError("k and v disagree on the heads")
+    pages, places, ldk_page, ldk_place, ldk_head = _cache_arg(k_cache, k, heads_first, "k_cache")
+    v_pages, v_places, ldv_page, ldv_place, ldv_head = _cache_arg(v_cache, v, heads_first, "v_cache")
+    if pages != v_pages or places != v_places:
+        raise ValueError("k_cache and v_cache disagree on pages or page size")
+    _tokens_arg(slots, T, dev, "slots")
+    Hq = ldq = ldqh = ldqo = ldqoh = r = interleaved = 0
+    turns, factor = None, 1.0
+    if plan is not None:
+        _plan_arg(plan, d, dev)
+        if positions is None:
+            raise ValueError("a rotation needs positions")
+        _tokens_arg(positions, T, dev, "positions")
+        r, interleaved, factor, turns = plan.rotary_dim, plan.interleaved, plan.factor, plan.turns
+    if q is not None:
+        if plan is None:
+            raise ValueError("q is there to be rotated: it needs a plan")
+        Hq, ldq, ldqh = _heads_like(q, k, "q")
+        if q.shape[2] != d:
+            raise ValueError("q and k disagree on the head dimension")
+        q_out, ldqo, ldqoh = _heads_out(q, q_out, "q_out")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if err is not None:
+        _err_arg(err, dev)
+    st = _launch(dev, lib.foak_kv_append, _addr(k), ldk, ldkh, _addr(v), ldv, ldvh, Hk, _DT[k.dtype], T, d, v.shape[2],
+                 _addr(slots), _addr(k_cache), ldk_page, ldk_place, ldk_head, _addr(v_cache), ldv_page, ldv_place, ldv_head,
+                 pages, places, _addr(q), ldq, ldqh, _addr(q_out), ldqo, ldqoh, Hq, r, interleaved, _addr(positions),
+                 _addr(turns), factor, _addr(err), _stream_handle(dev, stream))
+    _check(st, "foak_kv_append")
+    return q_out

@@ -12,6 +12,8 @@
 #include "foak_ce.h"
 #include "gemm_tc.h"
 #include "internal.h"
+#include "residual_norm.h"
+#include "rotary.h"
 
 namespace foak {
 
@@ -94,6 +96,7 @@ foak_status finish(cudaError_t e, int32_t* err, cudaStream_t stream) {
     if (cudaMemcpy(&h, err, sizeof(h), cudaMemcpyDeviceToHost) != cudaSuccess) return FOAK_ERR_CUDA;
     if (h & FOAK_ERRBIT_TIMEOUT) return FOAK_ERR_TIMEOUT;
     if (h & FOAK_ERRBIT_LABEL_RANGE) return FOAK_ERR_LABEL_RANGE;
+    if (h & FOAK_ERRBIT_PAGE_RANGE) return FOAK_ERR_PAGE_RANGE;
     return FOAK_OK;
 }
 
@@ -207,6 +210,54 @@ NormLinWs norm_lin_layout(void* base, int64_t N, int64_t V, int64_t D, int64_t c
     return w;
 }
 
+// ---- residual norms
+// N x D rows of the residual norms that are there: 16-byte aligned, 16-byte row strides of D elements or more.
+bool rows_ok(const void* p, int64_t ld, int64_t D, int es) { return ld >= D && rows16(p, ld, es); }
+
+// Size, type and gate, as both directions take them.
+foak_status check_resnorm(int32_t dtype, int64_t N, int64_t D, const void* gate, int32_t gate_kind, int64_t ldg,
+                          const void* post_gamma, const void* gamma, float scale, int* es) {
+    *es = elem_bytes_of(dtype);
+    if (*es == 0) return FOAK_ERR_UNSUPPORTED;
+    if (N < 0 || D < 8 || !std::isfinite(scale)) return FOAK_ERR_INVALID_ARG;
+    if (D % 8 || D > kResNormMaxD) return FOAK_ERR_UNSUPPORTED;
+    if (gate_kind < FOAK_GATE_NONE || gate_kind > FOAK_GATE_FULL) return FOAK_ERR_INVALID_ARG;
+    if ((gate_kind == FOAK_GATE_NONE) != (gate == nullptr) && (N > 0 || gate)) return FOAK_ERR_INVALID_ARG;
+    if (gate_kind == FOAK_GATE_CHANNEL && !aligned(gate, 16)) return FOAK_ERR_INVALID_ARG;
+    if (gate_kind == FOAK_GATE_ROW && (!aligned(gate, static_cast<size_t>(*es)) || ldg < 1)) return FOAK_ERR_INVALID_ARG;
+    if (gate_kind == FOAK_GATE_FULL && N > 0 && !rows_ok(gate, ldg, D, *es)) return FOAK_ERR_INVALID_ARG;
+    if (!aligned(post_gamma, 16) || !aligned(gamma, 16)) return FOAK_ERR_INVALID_ARG;
+    return FOAK_OK;
+}
+
+// ---- rotary positions and the paged cache
+constexpr int64_t kMaxHeadElements = 1ll << 28;
+
+bool rotary_ok(int64_t d, int64_t r) { return r >= 2 && r % 2 == 0 && r <= 65536 && d >= r; }
+
+// Heads of T tokens from one place to another.
+foak_status head_move(int64_t T, const void* src, int64_t src_t, int64_t src_h, void* dst, int64_t dst_t, int64_t dst_h,
+                      int64_t H, int64_t d, int64_t r, int es, HeadMove* m) {
+    *m = HeadMove{};
+    if (H < 0 || d < 1 || H * d > kMaxHeadElements || H > kMaxHeadElements || d > kMaxHeadElements)
+        return FOAK_ERR_INVALID_ARG;
+    if (H == 0) return FOAK_OK;
+    if (!src || !dst || !aligned(src, static_cast<size_t>(es)) || !aligned(dst, static_cast<size_t>(es)))
+        return FOAK_ERR_INVALID_ARG;
+    if (src_t < 0 || src_h < 0 || dst_t < 1 || (H > 1 && dst_h < d)) return FOAK_ERR_INVALID_ARG;
+    m->src = static_cast<const char*>(src);
+    m->dst = static_cast<char*>(dst);
+    // the stride of a single token or head is never used, and does not narrow the accesses
+    m->src_t = T > 1 ? src_t : 0;
+    m->dst_t = dst_t;
+    m->src_h = H > 1 ? src_h : 0;
+    m->dst_h = H > 1 ? dst_h : 0;
+    m->H = static_cast<int>(H);
+    m->d = static_cast<int>(d);
+    m->r = static_cast<int>(r);
+    return FOAK_OK;
+}
+
 // ---- log probabilities and distillation
 bool temperature_ok(float t) { return t >= 1e-6f && t <= 1e6f; }  // also refuses NaN
 
@@ -316,6 +367,7 @@ const char* foak_status_string(int32_t status) {
         case FOAK_ERR_WORKSPACE: return "FOAK_ERR_WORKSPACE: workspace missing, misaligned or too small";
         case FOAK_ERR_CUDA: return "FOAK_ERR_CUDA: a CUDA call or kernel launch failed";
         case FOAK_ERR_TIMEOUT: return "FOAK_ERR_TIMEOUT: a device-side wait gave up";
+        case FOAK_ERR_PAGE_RANGE: return "FOAK_ERR_PAGE_RANGE: a page or slot was outside the cache";
         default: return "unknown foak_status";
     }
 }
@@ -541,6 +593,245 @@ foak_status foak_rope_apply_qk(void* Q, int64_t Hq, int64_t ldq, void* K, int64_
                               static_cast<int>(Hk), ldk, static_cast<int>(d), positions, cache, max_pos, inverse != 0,
                               err, s);
     return finish(e, err, s);
+}
+
+foak_status foak_residual_norm_forward(const void* X, int64_t ldx, const void* R, int64_t ldr, int32_t dtype, int64_t N,
+                                       int64_t D, const void* gate, int32_t gate_kind, int64_t ldg,
+                                       const void* post_gamma, const void* gamma, float scale, float post_eps, float eps,
+                                       void* H, int64_t ldh, void* Y, int64_t ldy, float* post_rstd, float* rstd,
+                                       void* stream) {
+    int es = 0;
+    const foak_status st = check_resnorm(dtype, N, D, gate, gate_kind, ldg, post_gamma, gamma, scale, &es);
+    if (st != FOAK_OK) return st;
+    if (!(eps >= 0.f) || !(post_eps >= 0.f) || !aligned(post_rstd, 4) || !aligned(rstd, 4)) return FOAK_ERR_INVALID_ARG;
+    if (N > 0 && (!X || !R || !H || !rows_ok(X, ldx, D, es) || !rows_ok(R, ldr, D, es) || !rows_ok(H, ldh, D, es)))
+        return FOAK_ERR_INVALID_ARG;
+    if (N > 0 && (gamma ? !Y || !rows_ok(Y, ldy, D, es) || Y == H : Y != nullptr || rstd != nullptr))
+        return FOAK_ERR_INVALID_ARG;
+    if (!post_gamma && post_rstd) return FOAK_ERR_INVALID_ARG;
+    // in place only row by row
+    for (const void* out : {static_cast<const void*>(H), static_cast<const void*>(Y)}) {
+        const int64_t ld = out == H ? ldh : ldy;
+        if (N > 1 && out && ((out == X && ld != ldx) || (out == R && ld != ldr))) return FOAK_ERR_INVALID_ARG;
+    }
+    if (take_injected_failure()) return FOAK_ERR_CUDA;
+    ResNormFwd a = {};
+    a.X = static_cast<const char*>(X);
+    a.R = static_cast<const char*>(R);
+    a.gate = static_cast<const char*>(gate);
+    a.post_gamma = static_cast<const char*>(post_gamma);
+    a.gamma = static_cast<const char*>(gamma);
+    a.H = static_cast<char*>(H);
+    a.Y = static_cast<char*>(Y);
+    a.post_rstd = post_rstd;
+    a.rstd = rstd;
+    a.ldx = ldx;
+    a.ldr = ldr;
+    a.ldg = ldg;
+    a.ldh = ldh;
+    a.ldy = ldy;
+    a.N = N;
+    a.D = D;
+    a.gate_kind = gate_kind;
+    a.scale = scale;
+    a.post_eps = post_eps;
+    a.eps = eps;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return finish(launch_resnorm_fwd(es, a, s), nullptr, s);
+}
+
+size_t foak_residual_norm_workspace_size(int64_t N, int64_t D) {
+    return N < 0 || D < 8 || D > kResNormMaxD ? 0 : resnorm_workspace_bytes(N, D);
+}
+
+foak_status foak_residual_norm_backward(const void* dY, int64_t lddy, const void* dH, int64_t lddh, const void* H,
+                                        int64_t ldh, const void* X, int64_t ldx, int32_t dtype, int64_t N, int64_t D,
+                                        const void* gate, int32_t gate_kind, int64_t ldg, const void* post_gamma,
+                                        const void* gamma, const float* post_rstd, const float* rstd, float scale,
+                                        void* dR, int64_t lddr, void* dX, int64_t lddx, float* dgamma, void* dgate,
+                                        int64_t lddg, float* dpost_gamma, void* workspace, size_t workspace_bytes,
+                                        void* stream) {
+    int es = 0;
+    const foak_status st = check_resnorm(dtype, N, D, gate, gate_kind, ldg, post_gamma, gamma, scale, &es);
+    if (st != FOAK_OK) return st;
+    if (!aligned(post_rstd, 4) || !aligned(rstd, 4) || !aligned(dgamma, 4) || !aligned(dpost_gamma, 4))
+        return FOAK_ERR_INVALID_ARG;
+    if ((dgate && gate_kind == FOAK_GATE_NONE) || (dpost_gamma && !post_gamma)) return FOAK_ERR_INVALID_ARG;
+    if (dgate && !aligned(dgate, 4)) return FOAK_ERR_INVALID_ARG;
+    if (N > 0) {
+        if ((!dY && !dH) || !dR || !rows_ok(dR, lddr, D, es)) return FOAK_ERR_INVALID_ARG;
+        if (dY ? !rows_ok(dY, lddy, D, es) || !H || !rows_ok(H, ldh, D, es) || !gamma || !rstd : dgamma != nullptr)
+            return FOAK_ERR_INVALID_ARG;
+        if (dH && !rows_ok(dH, lddh, D, es)) return FOAK_ERR_INVALID_ARG;
+        if ((post_gamma || dgate) && !X) return FOAK_ERR_INVALID_ARG;
+        if (X && !rows_ok(X, ldx, D, es)) return FOAK_ERR_INVALID_ARG;
+        if (post_gamma && !post_rstd) return FOAK_ERR_INVALID_ARG;
+        if (dX && (!rows_ok(dX, lddx, D, es) || dX == dR)) return FOAK_ERR_INVALID_ARG;
+        if (dgate && gate_kind == FOAK_GATE_FULL && (!rows_ok(dgate, lddg, D, es) || dgate == dR || dgate == dX))
+            return FOAK_ERR_INVALID_ARG;
+        // in place only row by row
+        const void* out[] = {dR, dX, gate_kind == FOAK_GATE_FULL ? dgate : nullptr};
+        const int64_t ldo[] = {lddr, lddx, lddg};
+        const void* in[] = {dY, dH, H, X, gate_kind == FOAK_GATE_FULL ? gate : nullptr};
+        const int64_t ldi[] = {lddy, lddh, ldh, ldx, ldg};
+        for (int o = 0; o < 3; ++o)
+            for (int i = 0; i < 5; ++i)
+                if (N > 1 && out[o] && out[o] == in[i] && ldo[o] != ldi[i]) return FOAK_ERR_INVALID_ARG;
+    }
+    if (!workspace || !aligned(workspace, kCeWsAlign) || workspace_bytes < resnorm_workspace_bytes(N, D))
+        return FOAK_ERR_WORKSPACE;
+    if (take_injected_failure()) return FOAK_ERR_CUDA;
+    ResNormBwd a = {};
+    a.dY = static_cast<const char*>(dY);
+    a.dH = static_cast<const char*>(dH);
+    a.H = static_cast<const char*>(H);
+    a.X = post_gamma || dgate ? static_cast<const char*>(X) : nullptr;
+    a.gate = static_cast<const char*>(gate);
+    a.post_gamma = static_cast<const char*>(post_gamma);
+    a.gamma = static_cast<const char*>(gamma);
+    a.post_rstd = post_rstd;
+    a.rstd = rstd;
+    a.dR = static_cast<char*>(dR);
+    a.dX = static_cast<char*>(dX);
+    a.dgamma = dgamma;
+    a.dgate = static_cast<char*>(dgate);
+    a.dpost_gamma = dpost_gamma;
+    a.lddy = lddy;
+    a.lddh = lddh;
+    a.ldh = ldh;
+    a.ldx = ldx;
+    a.ldg = ldg;
+    a.lddr = lddr;
+    a.lddx = lddx;
+    a.lddg = lddg;
+    a.N = N;
+    a.D = D;
+    a.gate_kind = gate_kind;
+    a.scale = scale;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return finish(launch_resnorm_bwd(es, a, workspace, s), nullptr, s);
+}
+
+foak_status foak_rotary_inv_freq(double base, int64_t rotary_dim, int32_t scaling, double scale, double low, double high,
+                                 double original, double* inv_freq) {
+    if (!inv_freq || !(base > 1.0) || !std::isfinite(base)) return FOAK_ERR_INVALID_ARG;
+    if (!rotary_ok(rotary_dim, rotary_dim)) return FOAK_ERR_UNSUPPORTED;
+    if (scaling < FOAK_ROTARY_NONE || scaling > FOAK_ROTARY_RAMP) return FOAK_ERR_INVALID_ARG;
+    if (scaling != FOAK_ROTARY_NONE && (!(scale >= 1.0) || !std::isfinite(scale))) return FOAK_ERR_INVALID_ARG;
+    if (scaling == FOAK_ROTARY_NTK && rotary_dim <= 2) return FOAK_ERR_UNSUPPORTED;
+    if ((scaling == FOAK_ROTARY_BANDS || scaling == FOAK_ROTARY_RAMP) &&
+        (!(low > 0.0) || !(high > low) || !std::isfinite(high) || !(original >= 1.0) || !std::isfinite(original)))
+        return FOAK_ERR_INVALID_ARG;
+    rotary_inv_freq(base, rotary_dim, scaling, scale, low, high, original, inv_freq);
+    return FOAK_OK;
+}
+
+foak_status foak_rotary_turns(const double* inv_freq, int64_t n, uint64_t* turns) {
+    if (n < 0 || (n > 0 && (!inv_freq || !turns))) return FOAK_ERR_INVALID_ARG;
+    for (int64_t i = 0; i < n; ++i)
+        if (!std::isfinite(inv_freq[i])) return FOAK_ERR_INVALID_ARG;
+    for (int64_t i = 0; i < n; ++i) turns[i] = rotary_turns(inv_freq[i]);
+    return FOAK_OK;
+}
+
+foak_status foak_rotary_apply(const void* Q, int64_t ldq, int64_t ldqh, void* Qo, int64_t ldqo, int64_t ldqoh, int64_t Hq,
+                              const void* K, int64_t ldk, int64_t ldkh, void* Ko, int64_t ldko, int64_t ldkoh, int64_t Hk,
+                              int32_t dtype, int64_t T, int64_t d, int64_t rotary_dim, int32_t interleaved,
+                              const int64_t* positions, const uint64_t* turns, float factor, int32_t inverse,
+                              void* stream) {
+    const int es = elem_bytes_of(dtype);
+    if (!es || !rotary_ok(d, rotary_dim)) return FOAK_ERR_UNSUPPORTED;
+    if (T < 0 || !std::isfinite(factor)) return FOAK_ERR_INVALID_ARG;
+    RotaryArgs a = {};
+    const struct {
+        const void *src, *dst;
+        int64_t src_t, src_h, dst_t, dst_h, H;
+    } in[2] = {{Q, Qo, ldq, ldqh, ldqo, ldqoh, Q ? Hq : 0}, {K, Ko, ldk, ldkh, ldko, ldkoh, K ? Hk : 0}};
+    if (T > 0) {
+        for (int m = 0; m < 2; ++m) {
+            const auto& q = in[m];
+            const bool in_place = q.src && q.src == q.dst;
+            if (in_place && ((T > 1 && q.src_t != q.dst_t) || (q.H > 1 && q.src_h != q.dst_h))) return FOAK_ERR_INVALID_ARG;
+            // in place the part that passes through stays where it is
+            const foak_status st = head_move(T, q.src, q.src_t, q.src_h, const_cast<void*>(q.dst), q.dst_t, q.dst_h, q.H, d,
+                                             rotary_dim, es, &a.move[m]);
+            if (st != FOAK_OK) return st;
+            if (in_place) a.move[m].d = static_cast<int>(rotary_dim);
+        }
+        if (!turns || !aligned(turns, 8) || !positions || !aligned(positions, 8)) return FOAK_ERR_INVALID_ARG;
+    }
+    if (take_injected_failure()) return FOAK_ERR_CUDA;
+    a.positions = positions;
+    a.turns = turns;
+    a.T = T;
+    a.factor = factor;
+    a.sign = inverse ? -1.f : 1.f;
+    a.interleaved = interleaved != 0;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return finish(launch_rotary(es, a, s), nullptr, s);
+}
+
+foak_status foak_kv_slots(const int32_t* page_table, int64_t ld_table, int64_t max_pages, const int32_t* cache_lens,
+                          const int32_t* seq_starts, int64_t B, int64_t T, int64_t page_size, int64_t num_pages,
+                          int64_t* slots, int64_t* positions, int32_t* err, void* stream) {
+    if (B < 0 || T < 0 || page_size < 1 || num_pages < 1 || max_pages < 0 || ld_table < max_pages)
+        return FOAK_ERR_INVALID_ARG;
+    if (B > 0x7fffffffLL || T > 0x7fffffffLL || num_pages > (1ll << 62) / page_size) return FOAK_ERR_UNSUPPORTED;
+    if (T > 0 && (!seq_starts || !slots || !positions || (B > 0 && (!cache_lens || (max_pages > 0 && !page_table)))))
+        return FOAK_ERR_INVALID_ARG;
+    if (!aligned(page_table, 4) || !aligned(cache_lens, 4) || !aligned(seq_starts, 4) || !aligned(slots, 8) ||
+        !aligned(positions, 8) || !aligned(err, 4))
+        return FOAK_ERR_INVALID_ARG;
+    if (take_injected_failure()) return FOAK_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return finish(launch_kv_slots(page_table, ld_table, max_pages, cache_lens, seq_starts, B, T, page_size, num_pages, slots,
+                                  positions, err, s),
+                  err, s);
+}
+
+foak_status foak_kv_append(const void* K, int64_t ldk, int64_t ldkh, const void* V, int64_t ldv, int64_t ldvh, int64_t Hk,
+                           int32_t dtype, int64_t T, int64_t d, int64_t dv, const int64_t* slots, void* k_cache,
+                           int64_t ldk_page, int64_t ldk_place, int64_t ldk_head, void* v_cache, int64_t ldv_page,
+                           int64_t ldv_place, int64_t ldv_head, int64_t num_pages, int64_t page_size, const void* Q,
+                           int64_t ldq, int64_t ldqh, void* Qo, int64_t ldqo, int64_t ldqoh, int64_t Hq,
+                           int64_t rotary_dim, int32_t interleaved, const int64_t* positions, const uint64_t* turns,
+                           float factor, int32_t* err, void* stream) {
+    const int es = elem_bytes_of(dtype);
+    if (!es || (rotary_dim != 0 && !rotary_ok(d, rotary_dim))) return FOAK_ERR_UNSUPPORTED;
+    if (T < 0 || Hk < 1 || page_size < 1 || num_pages < 1 || !aligned(err, 4) || !std::isfinite(factor))
+        return FOAK_ERR_INVALID_ARG;
+    if (num_pages > (1ll << 62) / page_size) return FOAK_ERR_UNSUPPORTED;
+    if (rotary_dim == 0 && Q) return FOAK_ERR_INVALID_ARG;
+    RotaryArgs a = {};
+    if (T > 0) {
+        if (!slots || !aligned(slots, 8)) return FOAK_ERR_INVALID_ARG;
+        if (rotary_dim && (!turns || !aligned(turns, 8) || !positions || !aligned(positions, 8)))
+            return FOAK_ERR_INVALID_ARG;
+        const bool in_place = Q && Q == Qo;
+        if (in_place && ((T > 1 && ldq != ldqo) || (Hq > 1 && ldqh != ldqoh))) return FOAK_ERR_INVALID_ARG;
+        foak_status st = head_move(T, Q, ldq, ldqh, Qo, ldqo, ldqoh, Q ? Hq : 0, d, rotary_dim, es, &a.move[0]);
+        if (st == FOAK_OK) st = head_move(T, K, ldk, ldkh, k_cache, ldk_place, ldk_head, Hk, d, rotary_dim, es, &a.move[1]);
+        if (st == FOAK_OK) st = head_move(T, V, ldv, ldvh, v_cache, ldv_place, ldv_head, Hk, dv, 0, es, &a.move[2]);
+        if (st != FOAK_OK) return st;
+        if (in_place) a.move[0].d = static_cast<int>(rotary_dim);
+        if (ldk_page < 1 || ldv_page < 1 || k_cache == v_cache) return FOAK_ERR_INVALID_ARG;
+        a.move[1].paged = a.move[2].paged = true;
+        a.move[1].dst_page = ldk_page;
+        a.move[2].dst_page = ldv_page;
+    }
+    if (take_injected_failure()) return FOAK_ERR_CUDA;
+    a.positions = positions;
+    a.turns = turns;
+    a.slots = slots;
+    a.err = err;
+    a.T = T;
+    a.capacity = num_pages * page_size;
+    a.page_size = page_size;
+    a.factor = factor;
+    a.sign = 1.f;
+    a.interleaved = interleaved != 0;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return finish(launch_rotary(es, a, s), err, s);
 }
 
 size_t foak_logprobs_workspace_size(void) { return ce_workspace_bytes(0); }

@@ -34,8 +34,8 @@
  * - stream is a cudaStream_t passed as void* (NULL = legacy default stream).  All
  *   work is enqueued asynchronously on it; nothing synchronises unless the
  *   environment variable FOAK_SYNC_CHECK=1 is set, in which case the call waits
- *   for its own work and turns a non-zero error word into FOAK_ERR_LABEL_RANGE or
- *   FOAK_ERR_TIMEOUT.
+ *   for its own work and turns a non-zero error word into FOAK_ERR_LABEL_RANGE,
+ *   FOAK_ERR_TIMEOUT or FOAK_ERR_PAGE_RANGE.
  * - Problems checkable on the host return a status before anything is enqueued.
  *   A failed launch returns FOAK_ERR_CUDA.  No C++ exception crosses the ABI.
  * - Scalar outputs (loss, n_valid, err) are single device elements written by the
@@ -65,7 +65,8 @@ typedef enum foak_status {
     FOAK_ERR_LABEL_RANGE = 3,   /* (FOAK_SYNC_CHECK only) a label was out of range */
     FOAK_ERR_WORKSPACE = 4,     /* workspace missing, misaligned or too small */
     FOAK_ERR_CUDA = 5,          /* a CUDA runtime call or launch failed */
-    FOAK_ERR_TIMEOUT = 6        /* (FOAK_SYNC_CHECK only) a device wait gave up */
+    FOAK_ERR_TIMEOUT = 6,       /* (FOAK_SYNC_CHECK only) a device wait gave up */
+    FOAK_ERR_PAGE_RANGE = 7     /* (FOAK_SYNC_CHECK only) a page or slot was out of range */
 } foak_status;
 
 typedef enum foak_dtype { FOAK_F32 = 0, FOAK_BF16 = 1 } foak_dtype;
@@ -73,6 +74,7 @@ typedef enum foak_dtype { FOAK_F32 = 0, FOAK_BF16 = 1 } foak_dtype;
 /* Bits of the device error word (int32) that calls write when err != NULL. */
 #define FOAK_ERRBIT_LABEL_RANGE 1
 #define FOAK_ERRBIT_TIMEOUT 2
+#define FOAK_ERRBIT_PAGE_RANGE 4
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* foak_status_string(int32_t status);
@@ -333,6 +335,161 @@ foak_status foak_rope_apply(void* X, int32_t dtype, int64_t T, int64_t H, int64_
 foak_status foak_rope_apply_qk(void* Q, int64_t Hq, int64_t ldq, void* K, int64_t Hk, int64_t ldk, int32_t dtype,
                                int64_t T, int64_t d, const int64_t* positions, const void* cache, int64_t max_pos,
                                int32_t inverse, int32_t* err, void* stream);
+
+/*
+ * The norms around a block with its gate and residual scale, in one pass over the rows:
+ *     u_i = X_i,  or with post_gamma  X_i r1_i post_gamma,  r1_i = 1 / sqrt(mean_j X_ij^2 + post_eps)
+ *     H_i = R_i + scale * g * u_i
+ *     Y_i = H_i r_i gamma,  r_i = 1 / sqrt(mean_j H_ij^2 + eps)      (from the unrounded H_i)
+ * in fp32, H and Y rounded once.  It is what stands between two blocks of a decoder beside
+ * foak_rmsnorm_forward: X is a block's output, R the residual stream, Y the next block's input.
+ *   X, R (device)       N x D in dtype, row strides ldx, ldr
+ *   gate (device)       by gate_kind: FOAK_GATE_NONE (NULL); FOAK_GATE_CHANNEL: D values;
+ *                       FOAK_GATE_ROW: N values, ldg elements apart; FOAK_GATE_FULL: N x D,
+ *                       row stride ldg; all in dtype
+ *   post_gamma (device) D in dtype, or NULL: no norm after the block
+ *   gamma (device)      D in dtype, or NULL: no norm before the next block (Y must be NULL)
+ *   H, Y (device)       N x D in dtype, row strides ldh, ldy.  H may equal R or X; Y may equal X
+ *                       or R, but not H; otherwise outputs overlap nothing
+ *   post_rstd, rstd (device) float[N] or NULL: r1 and r, for the backward
+ * D % 8 == 0, D <= FOAK_RESIDUAL_NORM_MAX_D; rows and vectors 16-byte aligned with 16-byte
+ * strides (a FOAK_GATE_ROW gate: its elements' own alignment); scale finite; eps, post_eps >= 0.
+ */
+#define FOAK_GATE_NONE 0
+#define FOAK_GATE_CHANNEL 1
+#define FOAK_GATE_ROW 2
+#define FOAK_GATE_FULL 3
+#define FOAK_RESIDUAL_NORM_MAX_D 32768
+foak_status foak_residual_norm_forward(const void* X, int64_t ldx, const void* R, int64_t ldr, int32_t dtype, int64_t N,
+                                       int64_t D, const void* gate, int32_t gate_kind, int64_t ldg,
+                                       const void* post_gamma, const void* gamma, float scale, float post_eps, float eps,
+                                       void* H, int64_t ldh, void* Y, int64_t ldy, float* post_rstd, float* rstd,
+                                       void* stream);
+
+/*
+ * Bytes of device workspace that foak_residual_norm_backward needs (partial sums over the
+ * rows).  256-byte aligned; its contents need no initialisation, and calls that follow one
+ * another on a stream may share it.
+ */
+size_t foak_residual_norm_workspace_size(int64_t N, int64_t D);
+
+/*
+ * Its backward, from H (as rounded), r and r1.  With t = gamma dY, hh = H r, xh = X r1:
+ *     dR = dh = dH + r (t - hh mean_j(hh t)),     dgamma_j = sum_i dY hh
+ *     du = scale g dh,     dgate = scale dh u, summed over the rows (channel) or a row (row)
+ *     dX = du,  or with post_gamma  r1 (post_gamma du - xh mean_j(xh post_gamma du)),
+ *     dpost_gamma_j = sum_i du xh
+ *   dY (device)         N x D, or NULL: zero (H, gamma and rstd are not read; dgamma must be NULL)
+ *   dH (device)         N x D, the gradient that arrives along the residual stream, or NULL: zero;
+ *                       not both NULL
+ *   X (device)          N x D; may be NULL where neither post_gamma nor dgate is given
+ *   gate, gate_kind, ldg, post_gamma, gamma, scale: as in the forward
+ *   dR (device)         N x D; may equal dH or dY
+ *   dX (device)         N x D or NULL: not wanted (without gate and post_gamma and with scale 1
+ *                       it would be dR)
+ *   dgamma, dpost_gamma (device) float[D] or NULL, overwritten
+ *   dgate (device)      float[D] (channel), float[N] (row) or N x D in dtype with row stride lddg
+ *                       (full), or NULL
+ * The sums over the rows have a fixed order: results are the same from run to run.  Sizes and
+ * alignment as in the forward.
+ */
+foak_status foak_residual_norm_backward(const void* dY, int64_t lddy, const void* dH, int64_t lddh, const void* H,
+                                        int64_t ldh, const void* X, int64_t ldx, int32_t dtype, int64_t N, int64_t D,
+                                        const void* gate, int32_t gate_kind, int64_t ldg, const void* post_gamma,
+                                        const void* gamma, const float* post_rstd, const float* rstd, float scale,
+                                        void* dR, int64_t lddr, void* dX, int64_t lddx, float* dgamma, void* dgate,
+                                        int64_t lddg, float* dpost_gamma, void* workspace, size_t workspace_bytes,
+                                        void* stream);
+
+/*
+ * Rotary positions beyond foak_rope_*: both layouts, part of the head, contexts longer than the
+ * trained one, out of place, and no table of positions.  Pair i < rotary_dim / 2 of a head --
+ * elements (i, i + rotary_dim / 2), or (2i, 2i + 1) where interleaved -- turns by
+ * positions[t] * inv_freq[i] and is multiplied by factor; the elements from rotary_dim on pass.
+ *
+ * foak_rotary_inv_freq (host): the frequencies base^(-2i / rotary_dim), scaled:
+ *   FOAK_ROTARY_NONE    as they are
+ *   FOAK_ROTARY_LINEAR  divided by scale (position interpolation)
+ *   FOAK_ROTARY_NTK     of the base  base * scale^(rotary_dim / (rotary_dim - 2))
+ *   FOAK_ROTARY_BANDS   by the turns n that a frequency makes over `original` positions: divided by
+ *                       scale below `low` turns, kept above `high`, linear in n between
+ *   FOAK_ROTARY_RAMP    the same, linear in the index i between the index of `high` turns, rounded
+ *                       down, and that of `low` turns, rounded up
+ *   inv_freq (host)     double[rotary_dim / 2]
+ * rotary_dim even, 2 .. 65536 (NTK: above 2); base > 1; scale >= 1; BANDS and RAMP: 0 < low < high,
+ * original >= 1.
+ *
+ * foak_rotary_turns (host): what the device calls take: turns[i] = inv_freq[i] / 2 pi as a
+ * fraction of 2^64, whole turns dropped.  inv_freq finite.
+ */
+#define FOAK_ROTARY_NONE 0
+#define FOAK_ROTARY_LINEAR 1
+#define FOAK_ROTARY_NTK 2
+#define FOAK_ROTARY_BANDS 3
+#define FOAK_ROTARY_RAMP 4
+foak_status foak_rotary_inv_freq(double base, int64_t rotary_dim, int32_t scaling, double scale, double low, double high,
+                                 double original, double* inv_freq);
+foak_status foak_rotary_turns(const double* inv_freq, int64_t n, uint64_t* turns);
+
+/*
+ * Rotate queries and keys in one launch (inverse != 0: back by the same angles, the backward pass).
+ *   Q, K (device)       T x H x d in dtype, element (t, h, j) at t * ld + h * ldh + j; either may be
+ *                       NULL.  Strides >= 0; what is 16-byte aligned moves 16 bytes at a time
+ *   Qo, Ko (device)     where they go, with their own strides; Q and K themselves (same strides) to
+ *                       rotate in place; otherwise they overlap nothing; heads d elements or more apart
+ *   positions (device)  int64[T], any value (the angle is exact to 2^-53 positions[t] turns)
+ *   turns (device)      uint64[rotary_dim / 2] of foak_rotary_turns
+ * d >= rotary_dim >= 2, rotary_dim even; H * d <= 2^28.
+ */
+foak_status foak_rotary_apply(const void* Q, int64_t ldq, int64_t ldqh, void* Qo, int64_t ldqo, int64_t ldqoh, int64_t Hq,
+                              const void* K, int64_t ldk, int64_t ldkh, void* Ko, int64_t ldko, int64_t ldkoh, int64_t Hk,
+                              int32_t dtype, int64_t T, int64_t d, int64_t rotary_dim, int32_t interleaved,
+                              const int64_t* positions, const uint64_t* turns, float factor, int32_t inverse,
+                              void* stream);
+
+/*
+ * Where a serving step's tokens go in a paged cache: once a step, for the appends of all layers.
+ * The T rows hold the step's tokens of B sequences one after another; sequence b has rows
+ * seq_starts[b] .. seq_starts[b + 1] - 1 and cache_lens[b] tokens in the cache already.  With
+ * pos = cache_lens[b] + t - seq_starts[b] its token goes to
+ *     slots[t] = page_table[b][pos / page_size] * page_size + pos % page_size,   positions[t] = pos
+ * Rows before the first sequence and behind the last one are padding: slot -1, position 0.
+ *   page_table (device) int32[B][ld_table], max_pages <= ld_table entries a sequence
+ *   cache_lens (device) int32[B];  seq_starts (device) int32[B + 1], ascending
+ *   slots, positions (device) int64[T]
+ *   err (device)        int32[1] or NULL: FOAK_ERRBIT_PAGE_RANGE is OR-ed in (the caller clears it)
+ *                       for a page that is not in [0, num_pages), not in the table or of a negative
+ *                       length; its tokens get slot -1
+ * page_size and num_pages >= 1, their product below 2^62; T, B <= 2^31 - 1.
+ */
+foak_status foak_kv_slots(const int32_t* page_table, int64_t ld_table, int64_t max_pages, const int32_t* cache_lens,
+                          const int32_t* seq_starts, int64_t B, int64_t T, int64_t page_size, int64_t num_pages,
+                          int64_t* slots, int64_t* positions, int32_t* err, void* stream);
+
+/*
+ * Append a step's keys and values to a layer's paged cache, the keys rotated on the way, and rotate
+ * its queries, in one launch.  Token t goes to slot slots[t]: page slots[t] / page_size, place
+ * slots[t] % page_size.  A token with a negative slot is padding: nothing of it is written.
+ *   K, V (device)       T x Hk x d and T x Hk x dv in dtype, strides as for foak_rotary_apply
+ *   k_cache, v_cache (device) element (page, place, h, j) at page * ld_page + place * ld_place +
+ *                       h * ld_head + j, so either of (page, place, head) and (page, head, place)
+ *   slots (device)      int64[T], distinct unless negative (of two equal ones, either token's
+ *                       elements stay)
+ *   Q, Qo (device)      T x Hq x d, as for foak_rotary_apply, or NULL
+ *   rotary_dim          0: keys go as they are (positions and turns are not read, Q must be NULL)
+ *   positions, turns, interleaved, factor: as for foak_rotary_apply
+ *   err (device)        int32[1] or NULL: FOAK_ERRBIT_PAGE_RANGE is OR-ed in (the caller clears it)
+ *                       for a slot of num_pages * page_size or more; nothing is written for it
+ * Hk * max(d, dv) and Hq * d at most 2^28; page_size, num_pages as for foak_kv_slots.  The caches
+ * overlap neither each other nor an input.
+ */
+foak_status foak_kv_append(const void* K, int64_t ldk, int64_t ldkh, const void* V, int64_t ldv, int64_t ldvh, int64_t Hk,
+                           int32_t dtype, int64_t T, int64_t d, int64_t dv, const int64_t* slots, void* k_cache,
+                           int64_t ldk_page, int64_t ldk_place, int64_t ldk_head, void* v_cache, int64_t ldv_page,
+                           int64_t ldv_place, int64_t ldv_head, int64_t num_pages, int64_t page_size, const void* Q,
+                           int64_t ldq, int64_t ldqh, void* Qo, int64_t ldqo, int64_t ldqoh, int64_t Hq,
+                           int64_t rotary_dim, int32_t interleaved, const int64_t* positions, const uint64_t* turns,
+                           float factor, int32_t* err, void* stream);
 
 /*
  * Log probabilities, entropy and most likely tokens of the rows of a logits matrix:
