@@ -918,18 +918,25 @@ def foak_distill_backward(logits, labels, teacher_ids, teacher_logprobs, stats, 
 
 
 # --------------------------------------------------------------------- residual norms
+# The calls from here on are often a few microseconds' work on the GPU, so what they check of a
+# tensor they ask once, and devices are compared by number (a CPU tensor's is -1).
 FOAK_GATE_NONE, FOAK_GATE_CHANNEL, FOAK_GATE_ROW, FOAK_GATE_FULL = 0, 1, 2, 3
 FOAK_RESIDUAL_NORM_MAX_D = 32768
 _resnorm_ws: dict = {}
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _launch(dev, call, *args):
-    """``call(*args)`` with the tensors' device as the current one, as a launch on its stream wants."""
-    if dev.index == _current_device():
-        return call(*args)
-    with torch.cuda.device(dev):
-        return call(*args)
+def _launch(di, call, *args):
+    """``call(*args, stream)`` on device ``di``'s current stream, with that device as the current one, as a
+    launch wants."""
+    if di == _current_device():
+        return call(*args, _handle_of(di))
+    with torch.cuda.device(di):
+        return call(*args, _handle_of(di))
+
+
+def _handle_of(di):
+    return torch.cuda.current_stream(di).cuda_stream if _raw_stream is None else _raw_stream(di)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -937,38 +944,41 @@ def foak_residual_norm_workspace_size(N: int, D: int) -> int:
     return int(lib.foak_residual_norm_workspace_size(int(N), int(D)))
 
 
-def _like_rows(t, X, name):
-    """``t``'s row stride, for a tensor of X's shape, type and device."""
-    if t.shape != X.shape or t.dtype != X.dtype or t.device != X.device or t.stride(1) != 1:
-        raise ValueError(f"{name} must be like the block's rows: shape, dtype, device, unit column stride")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _row_stride(t, shape, dtype, di, name):
+    """The row stride of a tensor of this shape, type and device."""
+    if t.shape != shape or t.dtype != dtype or t.get_device() != di:
+        raise ValueError(f"{name} must be like the other rows: shape, dtype and device")
+    ld, unit = t.stride()
+    if unit != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return ld if shape[0] > 1 else shape[1]
 
 
-def _channels(t, X, name):
-    if t is not None and (t.dim() != 1 or t.shape[0] != X.shape[1] or t.dtype != X.dtype or t.device != X.device
-                          or not t.is_contiguous()):
+def _channels(t, D, dtype, di, name):
+    """The address of a vector of D channels."""
+    if t.dim() != 1 or t.numel() != D or t.dtype != dtype or t.get_device() != di or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous vector of D elements in the rows' dtype, on their device")
-    return t
+    return t.data_ptr()
 
 
-def _gate_arg(gate, X):
-    """(kind, stride): [D] is a gate a channel, [N, 1] one a row, [N, D] one an element."""
+def _gate_arg(gate, shape, dtype, di):
+    """(address, kind, stride): [D] is a gate a channel, [N, 1] one a row, [N, D] one an element."""
     if gate is None:
-        return FOAK_GATE_NONE, 0
+        return None, FOAK_GATE_NONE, 0
+    N, D = shape
     if gate.dim() == 1:
-        _channels(gate, X, "gate")
-        return FOAK_GATE_CHANNEL, 0
-    if gate.dim() == 2 and gate.shape[1] == 1 and gate.shape[0] == X.shape[0]:
-        if gate.dtype != X.dtype or gate.device != X.device:
+        return _channels(gate, D, dtype, di, "gate"), FOAK_GATE_CHANNEL, 0
+    if gate.shape == (N, 1):
+        if gate.dtype != dtype or gate.get_device() != di:
             raise ValueError("gate must have the rows' dtype and device")
-        return FOAK_GATE_ROW, (gate.stride(0) if gate.shape[0] > 1 else 1)
-    return FOAK_GATE_FULL, _like_rows(gate, X, "gate")
+        return gate.data_ptr(), FOAK_GATE_ROW, (gate.stride(0) if N > 1 else 1)
+    return gate.data_ptr(), FOAK_GATE_FULL, _row_stride(gate, shape, dtype, di, "gate")
 
 
-def _rstd_arg(t, X, name):
-    if t.dtype != torch.float32 or t.numel() != X.shape[0] or not t.is_contiguous() or t.device != X.device:
+def _rstd_arg(t, N, di, name):
+    if t.dtype != torch.float32 or t.numel() != N or t.get_device() != di or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 vector of the N rows, on their device")
-    return t
+    return t.data_ptr()
 
 
 @_on_stream
@@ -983,24 +993,31 @@ def foak_residual_norm_forward(X, R, gamma=None, *, gate=None, post_gamma=None, 
     :func:`foak_residual_norm_backward`, None unless ``want_rstd`` and their norm is there.
     """
     N, D, ldx = _rows_arg(X, "X")
-    dev = X.device
-    ldr = _like_rows(R, X, "R")
-    _channels(gamma, X, "gamma")
-    _channels(post_gamma, X, "post_gamma")
-    kind, ldg = _gate_arg(gate, X)
-    if Y is not None and gamma is None:
-        raise ValueError("Y needs gamma")
-    H = torch.empty(N, D, dtype=X.dtype, device=dev) if H is None else H
-    ldh, ldy = _like_rows(H, X, "H"), 0
+    shape, dtype, di = X.shape, X.dtype, X.get_device()
+    ldr = _row_stride(R, shape, dtype, di, "R")
+    g, kind, ldg = _gate_arg(gate, shape, dtype, di)
+    pg = None if post_gamma is None else _channels(post_gamma, D, dtype, di, "post_gamma")
+    H = X.new_empty(shape) if H is None else H
+    ldh = _row_stride(H, shape, dtype, di, "H")
+    gm = y = rstd = post = r = r1 = None
+    ldy = 0
     if gamma is not None:
-        Y = torch.empty(N, D, dtype=X.dtype, device=dev) if Y is None else Y
-        ldy = _like_rows(Y, X, "Y")
-    rstd = torch.empty(N, dtype=torch.float32, device=dev) if want_rstd and gamma is not None else None
-    post = torch.empty(N, dtype=torch.float32, device=dev) if want_rstd and post_gamma is not None else None
-    st = _launch(dev, lib.foak_residual_norm_forward, _addr(X), ldx, _addr(R), ldr, _DT[X.dtype], N, D, _addr(gate), kind,
-                 ldg, _addr(post_gamma), _addr(gamma), scale, eps if post_eps is None else post_eps, eps, _addr(H), ldh,
-                 _addr(Y), ldy, _addr(post), _addr(rstd), _stream_handle(dev, stream))
-    _check(st, "foak_residual_norm_forward")
+        gm = _channels(gamma, D, dtype, di, "gamma")
+        Y = X.new_empty(shape) if Y is None else Y
+        ldy = _row_stride(Y, shape, dtype, di, "Y")
+        y = Y.data_ptr()
+        if want_rstd:
+            rstd = torch.empty(N, dtype=torch.float32, device=X.device)
+            r = rstd.data_ptr()
+    elif Y is not None:
+        raise ValueError("Y needs gamma")
+    if want_rstd and pg is not None:
+        post = torch.empty(N, dtype=torch.float32, device=X.device)
+        r1 = post.data_ptr()
+    st = _launch(di, lib.foak_residual_norm_forward, X.data_ptr(), ldx, R.data_ptr(), ldr, _DT[dtype], N, D, g, kind, ldg,
+                 pg, gm, scale, eps if post_eps is None else post_eps, eps, H.data_ptr(), ldh, y, ldy, r1, r)
+    if st:
+        _check(st, "foak_residual_norm_forward")
     return dict(H=H, Y=Y, rstd=rstd, post_rstd=post)
 
 
@@ -1020,57 +1037,56 @@ def foak_residual_norm_backward(dY, dH, H=None, rstd=None, gamma=None, *, X=None
     like = dH if dY is None else dY
     if like is None:
         raise ValueError("dY or dH must be given")
-    N, D, _ = _rows_arg(like, "dY or dH")
-    dev, f32 = like.device, torch.float32
+    N, D, ld = _rows_arg(like, "dY or dH")
+    shape, dtype, di, dev, f32 = like.shape, like.dtype, like.get_device(), like.device, torch.float32
     lddy = lddh = ldh = ldx = lddx = lddg = 0
-    kind, ldg = _gate_arg(gate, like)
-    want_dgate = want_dgate and gate is not None
+    dy = dh = h = x = pg = gm = r = r1 = dx = a = b = c = None
+    g, kind, ldg = _gate_arg(gate, shape, dtype, di)
+    dgamma = dpost = dgate = None
     if dY is not None:
-        lddy = _like_rows(dY, like, "dY")
         if H is None or rstd is None or gamma is None:
             raise ValueError("dY needs the forward's H, rstd and gamma")
-        ldh = _like_rows(H, like, "H")
-        _rstd_arg(rstd, like, "rstd")
-        _channels(gamma, like, "gamma")
+        dy, lddy, h, ldh = dY.data_ptr(), ld, H.data_ptr(), _row_stride(H, shape, dtype, di, "H")
+        r, gm = _rstd_arg(rstd, N, di, "rstd"), _channels(gamma, D, dtype, di, "gamma")
+        if want_dgamma:
+            dgamma = torch.empty(D, dtype=f32, device=dev)
+            a = dgamma.data_ptr()
     if dH is not None:
-        lddh = _like_rows(dH, like, "dH")
+        dh, lddh = dH.data_ptr(), (_row_stride(dH, shape, dtype, di, "dH") if dH is not like else ld)
+    want_dgate = want_dgate and gate is not None
     if post_gamma is not None or want_dgate:
         if X is None:
             raise ValueError("post_gamma and the gate's gradient need X")
-        ldx = _like_rows(X, like, "X")
-    else:
-        X = None
+        x, ldx = X.data_ptr(), _row_stride(X, shape, dtype, di, "X")
     if post_gamma is not None:
         if post_rstd is None:
             raise ValueError("post_gamma needs the forward's post_rstd")
-        _channels(post_gamma, like, "post_gamma")
-        _rstd_arg(post_rstd, like, "post_rstd")
-    dR = torch.empty(N, D, dtype=like.dtype, device=dev) if dR is None else dR
-    lddr = _like_rows(dR, like, "dR")
-    same = dX is None and gate is None and post_gamma is None and scale == 1.0
-    if want_dX and dX is None and not same:
-        dX = torch.empty(N, D, dtype=like.dtype, device=dev)
-    if dX is not None:
-        lddx = _like_rows(dX, like, "dX")
-    dgamma = torch.empty(D, dtype=f32, device=dev) if want_dgamma and dY is not None else None
-    dpost = torch.empty(D, dtype=f32, device=dev) if want_dgamma and post_gamma is not None else None
-    dgate = None
+        pg, r1 = _channels(post_gamma, D, dtype, di, "post_gamma"), _rstd_arg(post_rstd, N, di, "post_rstd")
+        if want_dgamma:
+            dpost = torch.empty(D, dtype=f32, device=dev)
+            c = dpost.data_ptr()
     if want_dgate:
         if kind == FOAK_GATE_FULL:
-            dgate, lddg = torch.empty(N, D, dtype=like.dtype, device=dev), D
+            dgate, lddg = like.new_empty(shape), D
         else:
             dgate = torch.empty((D,) if kind == FOAK_GATE_CHANNEL else (N, 1), dtype=f32, device=dev)
-    handle = _stream_handle(dev, stream)
+        b = dgate.data_ptr()
+    dR = like.new_empty(shape) if dR is None else dR
+    lddr = _row_stride(dR, shape, dtype, di, "dR")
+    same = dX is None and gate is None and post_gamma is None and scale == 1.0
+    if dX is None and want_dX and not same:
+        dX = like.new_empty(shape)
+    if dX is not None:
+        dx, lddx = dX.data_ptr(), _row_stride(dX, shape, dtype, di, "dX")
     need = foak_residual_norm_workspace_size(N, D)
     if workspace_tensor is None:  # partial sums only: each is written before it is read
-        ws = _cached_workspace(_resnorm_ws, need, dev, handle, fill=torch.empty)
+        ws = _cached_workspace(_resnorm_ws, need, dev, _handle_of(di), fill=torch.empty)
     else:
         ws = _workspace_arg(workspace_tensor, dev)
-    st = _launch(dev, lib.foak_residual_norm_backward, _addr(dY), lddy, _addr(dH), lddh, _addr(H) if lddy else None, ldh,
-                 _addr(X), ldx, _DT[like.dtype], N, D, _addr(gate), kind, ldg, _addr(post_gamma),
-                 _addr(gamma) if lddy else None, _addr(post_rstd), _addr(rstd) if lddy else None, scale, _addr(dR), lddr,
-                 _addr(dX), lddx, _addr(dgamma), _addr(dgate), lddg, _addr(dpost), _addr(ws), ws.numel(), handle)
-    _check(st, "foak_residual_norm_backward")
+    st = _launch(di, lib.foak_residual_norm_backward, dy, lddy, dh, lddh, h, ldh, x, ldx, _DT[dtype], N, D, g, kind, ldg,
+                 pg, gm, r1, r, scale, dR.data_ptr(), lddr, dx, lddx, a, b, lddg, c, ws.data_ptr(), ws.numel())
+    if st:
+        _check(st, "foak_residual_norm_backward")
     return dict(dR=dR, dX=dR if same and want_dX else dX, dgamma=dgamma, dgate=dgate, dpost_gamma=dpost)
 
 
@@ -1082,11 +1098,11 @@ class RotaryPlan:
     """What :func:`foak_rotary_apply` and :func:`foak_kv_append` need of a model's rotary embedding: made once
     by :func:`foak_rotary_plan` and kept as long as a graph that was captured with it is replayed."""
 
-    __slots__ = ("turns", "rotary_dim", "interleaved", "factor", "inv_freq")
+    __slots__ = ("turns", "rotary_dim", "interleaved", "factor", "inv_freq", "device_index")
 
     def __init__(self, turns, rotary_dim, interleaved, factor, inv_freq):
         self.turns, self.rotary_dim, self.interleaved = turns, rotary_dim, interleaved
-        self.factor, self.inv_freq = factor, inv_freq
+        self.factor, self.inv_freq, self.device_index = factor, inv_freq, turns.get_device()
 
 
 def foak_rotary_inv_freq(rotary_dim: int, *, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -1142,41 +1158,48 @@ def foak_rotary_plan(rotary_dim: int, *, base: float = 10000.0, interleaved: boo
     return RotaryPlan(turns, int(rotary_dim), bool(interleaved), float(attention_factor), inv_freq)
 
 
-def _heads_arg(x, name):
-    """(heads, token stride, head stride) of a T x H x d CUDA view."""
-    if x.dim() != 3 or x.dtype not in _DT or not x.is_cuda or (x.shape[2] > 1 and x.stride(2) != 1):
+def _heads_arg(x, dtype, di, T, name):
+    """(heads, elements, token stride, head stride) of a T x H x d view of this type, device and T."""
+    if x.dim() != 3 or x.dtype != dtype or x.get_device() != di:
+        raise ValueError(f"{name} must be T x H x d, of the other heads' dtype and device")
+    tokens, H, d = x.shape
+    ldt, ldh, unit = x.stride()
+    if tokens != T or (unit != 1 and d > 1):
+        raise ValueError(f"{name} must have the other heads' tokens, and unit stride along a head")
+    if H == 1:
+        ldh = d
+    return H, d, (ldt if T > 1 else max(1, H * d)), ldh
+
+
+def _first_heads(x, name):
+    """(type, device, tokens) that the other tensors have to share."""
+    if x.dim() != 3 or x.dtype not in _DT or not x.is_cuda:
         raise ValueError(f"{name} must be a T x H x d bfloat16/float32 CUDA view whose heads have unit stride")
-    T, H, d = x.shape
-    ldh = x.stride(1) if H > 1 else d
-    return H, (x.stride(0) if T > 1 else max(1, H * d)), ldh
+    return x.dtype, x.get_device(), x.shape[0]
 
 
-def _heads_like(x, like, name):
-    if x.dtype != like.dtype or x.device != like.device or x.shape[0] != like.shape[0]:
-        raise ValueError(f"{name} disagrees with the others on tokens, dtype or device")
-    return _heads_arg(x, name)
-
-
-def _plan_arg(plan, d, device):
-    if plan.turns.device != device:
+def _plan_arg(plan, d, di):
+    if plan.device_index != di:
         raise ValueError("the plan must live on the heads' device")
     if plan.rotary_dim > d:
         raise ValueError("the plan rotates more elements than a head has")
+    return plan.turns.data_ptr()
 
 
-def _tokens_arg(t, T, device, name):
-    if t.dtype != torch.int64 or t.dim() != 1 or t.shape[0] != T or not t.is_contiguous() or t.device != device:
+def _tokens_arg(t, T, di, name):
+    if t.dtype != torch.int64 or t.dim() != 1 or t.numel() != T or t.get_device() != di or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int64 vector of the T tokens, on the heads' device")
+    return t.data_ptr()
 
 
-def _heads_out(x, out, name):
+def _heads_out(x, out, dtype, di, T, name):
     """(output, token stride, head stride): ``out``, x itself among them, or a new contiguous tensor."""
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = torch.empty(x.shape, dtype=dtype, device=x.device)
     elif out.shape != x.shape:
         raise ValueError(f"{name} must have its input's shape")
-    _, ld, ldh = _heads_like(out, x, name)
-    return out, ld, ldh
+    _, _, ldt, ldh = _heads_arg(out, dtype, di, T, name)
+    return out, ldt, ldh
 
 
 @_on_stream
@@ -1187,41 +1210,44 @@ def foak_rotary_apply(plan, positions, q, k=None, *, q_out=None, k_out=None, inv
     Views of any token and head strides (a fused QKV product's parts, heads first or tokens first).
     Returns (q_out, k_out): new tensors unless given; ``q_out=q`` rotates in place.  Either of q and k may be None.
     """
-    x = k if q is None else q
-    if x is None:
+    if q is None and k is None:
         raise ValueError("q or k must be given")
-    none = (0, 0, 0)
-    Hq, ldq, ldqh = none if q is None else _heads_like(q, x, "q")
-    Hk, ldk, ldkh = none if k is None else _heads_like(k, x, "k")
-    T, _, d = x.shape
-    dev = x.device
-    if k is not None and k.shape[2] != d:
-        raise ValueError("q and k disagree on the head dimension")
-    _plan_arg(plan, d, dev)
-    _tokens_arg(positions, T, dev, "positions")
-    q_out, ldqo, ldqoh = none if q is None else _heads_out(q, q_out, "q_out")
-    k_out, ldko, ldkoh = none if k is None else _heads_out(k, k_out, "k_out")
-    q_out, k_out = (None if q is None else q_out), (None if k is None else k_out)
-    st = _launch(dev, lib.foak_rotary_apply, _addr(q), ldq, ldqh, _addr(q_out), ldqo, ldqoh, Hq, _addr(k), ldk, ldkh,
-                 _addr(k_out), ldko, ldkoh, Hk, _DT[x.dtype], T, d, plan.rotary_dim, plan.interleaved, _addr(positions),
-                 _addr(plan.turns), plan.factor, inverse, _stream_handle(dev, stream))
-    _check(st, "foak_rotary_apply")
+    if (q is None and q_out is not None) or (k is None and k_out is not None):
+        raise ValueError("an output without its input")
+    dtype, di, T = _first_heads(*((q, "q") if k is None or q is not None else (k, "k")))
+    qp = kp = qo = ko = None
+    Hq = ldq = ldqh = ldqo = ldqoh = Hk = ldk = ldkh = ldko = ldkoh = 0
+    if q is not None:
+        Hq, d, ldq, ldqh = _heads_arg(q, dtype, di, T, "q")
+        q_out, ldqo, ldqoh = _heads_out(q, q_out, dtype, di, T, "q_out")
+        qp, qo = q.data_ptr(), q_out.data_ptr()
+    if k is not None:
+        Hk, dk, ldk, ldkh = _heads_arg(k, dtype, di, T, "k")
+        if q is not None and dk != d:
+            raise ValueError("q and k disagree on the head dimension")
+        d = dk
+        k_out, ldko, ldkoh = _heads_out(k, k_out, dtype, di, T, "k_out")
+        kp, ko = k.data_ptr(), k_out.data_ptr()
+    st = _launch(di, lib.foak_rotary_apply, qp, ldq, ldqh, qo, ldqo, ldqoh, Hq, kp, ldk, ldkh, ko, ldko, ldkoh, Hk,
+                 _DT[dtype], T, d, plan.rotary_dim, plan.interleaved, _tokens_arg(positions, T, di, "positions"),
+                 _plan_arg(plan, d, di), plan.factor, inverse)
+    if st:
+        _check(st, "foak_rotary_apply")
     return q_out, k_out
 
 
 # --------------------------------------------------------------------- paged cache
-def _int32_arg(t, dim, device, name):
-    if t.dtype != torch.int32 or t.dim() != dim or t.device != device or (t.shape[-1] > 1 and t.stride(-1) != 1):
-        raise ValueError(f"{name} must be a {dim}-D int32 tensor with unit stride on the page table's device")
+def _int32_arg(t, di, name):
+    if t.dtype != torch.int32 or t.get_device() != di or t.stride()[-1] != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name} must be int32 with unit stride, on the page table's device")
+    return t.data_ptr()
 
 
-def _err_arg(err, device):
-    """A given error word, or a new one, zero."""
-    if err is None:
-        return torch.zeros(1, dtype=torch.int32, device=device)
-    if err.dtype != torch.int32 or err.numel() != 1 or err.device != device:
+def _err_arg(err, di):
+    """The address of a caller's error word."""
+    if err.dtype != torch.int32 or err.numel() != 1 or err.get_device() != di:
         raise ValueError("err must be a one-element int32 tensor on the tensors' device")
-    return err
+    return err.data_ptr()
 
 
 @_on_stream
@@ -1235,36 +1261,40 @@ def foak_kv_slots(page_table, cache_lens, seq_starts, T: int, *, page_size: int,
     [0, num_pages) gives slot -1 and sets FOAK_ERRBIT_PAGE_RANGE in ``err``, which is OR-ed into: pass
     a zeroed int32 tensor to keep one for many calls.
     """
-    dev = page_table.device
-    if dev.type != "cuda":
-        raise ValueError("page_table must be on a CUDA device")
-    _int32_arg(page_table, 2, dev, "page_table")
-    _int32_arg(cache_lens, 1, dev, "cache_lens")
-    _int32_arg(seq_starts, 1, dev, "seq_starts")
+    di = page_table.get_device()
+    if di < 0 or page_table.dim() != 2 or cache_lens.dim() != 1 or seq_starts.dim() != 1:
+        raise ValueError("page_table (2-D), cache_lens and seq_starts (1-D) must be on a CUDA device")
     B, most = page_table.shape
-    if cache_lens.shape[0] != B or seq_starts.shape[0] != B + 1:
+    if cache_lens.numel() != B or seq_starts.numel() != B + 1:
         raise ValueError("page_table, cache_lens and seq_starts disagree on the sequences")
-    T = int(T)
+    T, dev = int(T), page_table.device
+    if T < 0:
+        raise ValueError("T must not be negative")
     slots = torch.empty(T, dtype=torch.int64, device=dev)
     positions = torch.empty(T, dtype=torch.int64, device=dev)
-    err = _err_arg(err, dev)
-    st = _launch(dev, lib.foak_kv_slots, _addr(page_table), page_table.stride(0) if B > 1 else most, most,
-                 _addr(cache_lens), _addr(seq_starts), B, T, page_size, num_pages, _addr(slots), _addr(positions),
-                 _addr(err), _stream_handle(dev, stream))
-    _check(st, "foak_kv_slots")
+    if err is None:
+        err = torch.zeros(1, dtype=torch.int32, device=dev)
+    st = _launch(di, lib.foak_kv_slots, _int32_arg(page_table, di, "page_table"), page_table.stride(0) if B > 1 else most,
+                 most, _int32_arg(cache_lens, di, "cache_lens"), _int32_arg(seq_starts, di, "seq_starts"), B, T, page_size,
+                 num_pages, slots.data_ptr(), positions.data_ptr(), _err_arg(err, di))
+    if st:
+        _check(st, "foak_kv_slots")
     return dict(slots=slots, positions=positions, err=err)
 
 
-def _cache_arg(cache, like, heads_first, name):
-    """(pages, places, page stride, place stride, head stride) of a cache of ``like``'s heads."""
-    if cache.dim() != 4 or cache.dtype != like.dtype or cache.device != like.device:
+def _cache_arg(cache, dtype, di, H, d, heads_first, name):
+    """(pages, places, page stride, place stride, head stride) of a cache of H heads of d elements."""
+    if cache.dim() != 4 or cache.dtype != dtype or cache.get_device() != di:
         raise ValueError(f"{name} must be 4-D, of the heads' dtype and device")
-    page, head = (2, 1) if heads_first else (1, 2)
-    if cache.shape[head] != like.shape[1] or cache.shape[3] != like.shape[2]:
+    pages, places, heads, size = cache.shape
+    ld_page, ld_place, ld_head, unit = cache.stride()
+    if heads_first:
+        places, heads, ld_place, ld_head = heads, places, ld_head, ld_place
+    if heads != H or size != d:
         raise ValueError(f"{name} disagrees with its rows on the heads or their size")
-    if cache.shape[3] > 1 and cache.stride(3) != 1:
+    if unit != 1 and d > 1:
         raise ValueError(f"{name} must have unit stride along a head")
-    return cache.shape[0], cache.shape[page], cache.stride(0), cache.stride(page), cache.stride(head)
+    return pages, places, ld_page, ld_place, ld_head
 
 
 @_on_stream
@@ -1279,39 +1309,37 @@ def foak_kv_append(k, v, k_cache, v_cache, slots, *, heads_first: bool = False, 
     of ``q_out`` neither.  Returns q_out (a new tensor unless given, None without q).  A slot past the cache
     sets FOAK_ERRBIT_PAGE_RANGE in ``err`` (OR-ed into), if given, and is left out.
     """
-    Hk, ldk, ldkh = _heads_arg(k, "k")
-    T, _, d = k.shape
-    dev = k.device
-    Hv, ldv, ldvh = _heads_like(v, k, "v")
+    dtype, di, T = _first_heads(k, "k")
+    Hk, d, ldk, ldkh = _heads_arg(k, dtype, di, T, "k")
+    Hv, dv, ldv, ldvh = _heads_arg(v, dtype, di, T, "v")
     if Hv != Hk:
         raise ValueError("k and v disagree on the heads")
-    pages, places, ldk_page, ldk_place, ldk_head = _cache_arg(k_cache, k, heads_first, "k_cache")
-    v_pages, v_places, ldv_page, ldv_place, ldv_head = _cache_arg(v_cache, v, heads_first, "v_cache")
+    pages, places, ldk_page, ldk_place, ldk_head = _cache_arg(k_cache, dtype, di, Hk, d, heads_first, "k_cache")
+    v_pages, v_places, ldv_page, ldv_place, ldv_head = _cache_arg(v_cache, dtype, di, Hk, dv, heads_first, "v_cache")
     if pages != v_pages or places != v_places:
         raise ValueError("k_cache and v_cache disagree on pages or page size")
-    _tokens_arg(slots, T, dev, "slots")
-    Hq = ldq = ldqh = ldqo = ldqoh = r = interleaved = 0
-    turns, factor = None, 1.0
+    Hq = ldq = ldqh = ldqo = ldqoh = r = 0
+    qp = qo = at = turns = None
+    interleaved, factor = False, 1.0
     if plan is not None:
-        _plan_arg(plan, d, dev)
         if positions is None:
             raise ValueError("a rotation needs positions")
-        _tokens_arg(positions, T, dev, "positions")
-        r, interleaved, factor, turns = plan.rotary_dim, plan.interleaved, plan.factor, plan.turns
+        at, turns = _tokens_arg(positions, T, di, "positions"), _plan_arg(plan, d, di)
+        r, interleaved, factor = plan.rotary_dim, plan.interleaved, plan.factor
     if q is not None:
         if plan is None:
             raise ValueError("q is there to be rotated: it needs a plan")
-        Hq, ldq, ldqh = _heads_like(q, k, "q")
-        if q.shape[2] != d:
+        Hq, dq, ldq, ldqh = _heads_arg(q, dtype, di, T, "q")
+        if dq != d:
             raise ValueError("q and k disagree on the head dimension")
-        q_out, ldqo, ldqoh = _heads_out(q, q_out, "q_out")
+        q_out, ldqo, ldqoh = _heads_out(q, q_out, dtype, di, T, "q_out")
+        qp, qo = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
-    if err is not None:
-        _err_arg(err, dev)
-    st = _launch(dev, lib.foak_kv_append, _addr(k), ldk, ldkh, _addr(v), ldv, ldvh, Hk, _DT[k.dtype], T, d, v.shape[2],
-                 _addr(slots), _addr(k_cache), ldk_page, ldk_place, ldk_head, _addr(v_cache), ldv_page, ldv_place, ldv_head,
-                 pages, places, _addr(q), ldq, ldqh, _addr(q_out), ldqo, ldqoh, Hq, r, interleaved, _addr(positions),
-                 _addr(turns), factor, _addr(err), _stream_handle(dev, stream))
-    _check(st, "foak_kv_append")
+    st = _launch(di, lib.foak_kv_append, k.data_ptr(), ldk, ldkh, v.data_ptr(), ldv, ldvh, Hk, _DT[dtype], T, d, dv,
+                 _tokens_arg(slots, T, di, "slots"), k_cache.data_ptr(), ldk_page, ldk_place, ldk_head,
+                 v_cache.data_ptr(), ldv_page, ldv_place, ldv_head, pages, places, qp, ldq, ldqh, qo, ldqo, ldqoh, Hq, r,
+                 interleaved, at, turns, factor, None if err is None else _err_arg(err, di))
+    if st:
+        _check(st, "foak_kv_append")
     return q_out

@@ -11,6 +11,8 @@
 //
 // Both directions are bound by memory: each operand is read and each result written once.
 #include <algorithm>
+#include <array>
+#include <map>
 #include <mutex>
 
 #include "foak_ce.h"
@@ -244,9 +246,330 @@ __global__ void __launch_bounds__(128) resnorm_bwd_cols_kernel(const ResNormBwd 
     }
 }
 
+// ------------------------------------------------------------------ backward, one pass
+// The rows of up to eight slices of 512 vectors: a cluster of C CTAs takes a range of rows, each CTA a slice
+// of their columns; thread v owns vectors v and v + threads of its slice, so the sums over the rows stay
+// in registers until the CTA's end.  Every thread copies its own vectors of a row's operands into a ring
+// of shared memory, stages - 1 batches of RR rows ahead (cp.async: a hardware wait, no spin), sums
+// what the row needs, meets the others at one barrier a batch and reads its vectors again for the results.
+// The row's sums have r and r1 factored out (w = gp e x, e the gate of a channel or an element):
+//     S1 = sum h gamma dy,   S2 = sum w (dH + r gamma dy),   S3 = sum w h,   k1 = r^3 S1 / D
+//     dh = dH + r gamma dy - k1 h,   E = sum dh w r1 = r1 (S2 - k1 S3),   k2 = r1^2 q E / D
+//     dX = (r1) q gp e dh - (k2 x),   q = s, times the gate of a row
+// Arithmetic on pairs (two-wide FP32).
+constexpr int kVpt = 2;
+constexpr int kBwdThreads = 256;
+constexpr int kSliceVecs = kVpt * kBwdThreads;
+constexpr int kMaxCluster = 8;
+constexpr int kRingSmem = 104 * 1024;  // two CTAs an SM
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all_but(int pending) {
+    if (pending == 1) cp_async_wait<1>();
+    else if (pending == 2) cp_async_wait<2>();
+    else cp_async_wait<3>();
+}
+
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// A 16-byte vector as element pairs.
+template <int ES>
+struct Pairs {
+    static constexpr int N = 8 / ES;
+    float2 p[N];
+    __device__ __forceinline__ void unpack(const uint4& w) {
+        if constexpr (ES == 2) {
+            p[0] = make_float2(bf16_lo(w.x), bf16_hi(w.x));
+            p[1] = make_float2(bf16_lo(w.y), bf16_hi(w.y));
+            p[2] = make_float2(bf16_lo(w.z), bf16_hi(w.z));
+            p[3] = make_float2(bf16_lo(w.w), bf16_hi(w.w));
+        } else {
+            p[0] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+            p[1] = make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
+        }
+    }
+    __device__ __forceinline__ void store(char* dst) const {
+        uint4 w;
+        if constexpr (ES == 2)
+            w = make_uint4(pack_bf16x2(p[0].x, p[0].y), pack_bf16x2(p[1].x, p[1].y), pack_bf16x2(p[2].x, p[2].y),
+                           pack_bf16x2(p[3].x, p[3].y));
+        else
+            w = make_uint4(__float_as_uint(p[0].x), __float_as_uint(p[0].y), __float_as_uint(p[1].x),
+                           __float_as_uint(p[1].y));
+        *reinterpret_cast<uint4*>(dst) = w;
+    }
+    __device__ __forceinline__ void fill(float v) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) p[k] = make_float2(v, v);
+    }
+};
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// The warp's sums of four values with six shuffles: lanes 8 v .. 8 v + 7 get value v.
+__device__ __forceinline__ float warp_sum4(float a, float b, float c, float d, int lane) {
+    const bool hi = lane & 16, odd = lane & 8;
+    const float x = (hi ? c : a) + __shfl_xor_sync(0xffffffffu, hi ? a : c, 16);
+    const float y = (hi ? d : b) + __shfl_xor_sync(0xffffffffu, hi ? b : d, 16);
+    float z = (odd ? y : x) + __shfl_xor_sync(0xffffffffu, odd ? x : y, 8);
+#pragma unroll
+    for (int off = 4; off > 0; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
+    return z;
+}
+
+struct BwdSplit {
+    int cluster;    // CTAs a row
+    int stages;     // of the ring
+    int slice;      // vectors of a CTA's slice
+};
+
+// SUMS: S2 and S3 are wanted (the norm after the block, or the gradient of a row's gate).
+template <int ES, bool POST, bool FULL, bool HASX, bool SUMS, int RR>
+__global__ void __launch_bounds__(kBwdThreads, 2)
+    resnorm_bwd_ring_kernel(const ResNormBwd a, const BwdSplit sp, float* __restrict__ part1, float* __restrict__ part2) {
+    griddep_launch_dependents();  // programmatic dependent launch: no global access before the wait
+    using P = Pairs<ES>;
+    constexpr int EPV = 16 / ES, NP = P::N, NS = 3 + HASX + FULL, NSUM = SUMS ? 4 : 1;
+    extern __shared__ uint4 ring[];  // [stages][RR][NS][kVpt][threads]
+    __shared__ float red[2][RR][kMaxCluster * (kBwdThreads / 32)][NSUM];
+    const int v = threadIdx.x, lane = v & 31, warp = v >> 5, nt = blockDim.x, warps = nt >> 5;
+    const int C = sp.cluster, rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int64_t cid = C > 1 ? static_cast<int64_t>(blockIdx.x) / C : blockIdx.x, clusters = gridDim.x / C;
+    bool act[kVpt];
+    int64_t col[kVpt];  // in elements
+#pragma unroll
+    for (int j = 0; j < kVpt; ++j) {
+        const int at = v + j * nt;
+        col[j] = (static_cast<int64_t>(rank) * sp.slice + at) * EPV;
+        act[j] = at < sp.slice && col[j] < a.D;
+    }
+    const int64_t r_begin = a.N * cid / clusters, r_end = a.N * (cid + 1) / clusters;
+    const int64_t nb = (r_end - r_begin + RR - 1) / RR;
+    const float inv_d = 1.f / static_cast<float>(a.D);
+    const int stage_vecs = RR * NS * kVpt * nt;
+    const char* src[NS];
+    int64_t ld[NS];
+    src[0] = a.dY; ld[0] = a.lddy;
+    src[1] = a.dY ? a.H : nullptr; ld[1] = a.ldh;
+    src[2] = a.dH; ld[2] = a.lddh;
+    if constexpr (HASX) {
+        src[3] = a.X; ld[3] = a.ldx;
+    }
+    if constexpr (FULL) {
+        src[NS - 1] = a.gate; ld[NS - 1] = a.ldg;
+    }
+    // an operand that is not there reads as zeros
+    if (!a.dY || !a.dH) {
+        for (int i = v; i < sp.stages * stage_vecs; i += nt) ring[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (C > 1) cluster_sync();  // nobody writes into a CTA that has not begun
+    else __syncthreads();
+    griddep_wait();
+    // batch b's copies into stage s, one group a batch (empty past the last, so that the count stays in step)
+    auto issue = [&](int64_t b, int s) {
+        if (b < nb) {
+            uint4* slot = ring + s * stage_vecs;
+#pragma unroll
+            for (int q = 0; q < RR; ++q) {
+                const int64_t row = r_begin + b * RR + q;
+                if (row >= r_end) break;
+#pragma unroll
+                for (int i = 0; i < NS; ++i) {
+                    if (!src[i]) continue;
+                    const char* p = src[i] + row * ld[i] * ES;
+#pragma unroll
+                    for (int j = 0; j < kVpt; ++j)
+                        if (act[j]) cp_async16(slot + ((q * NS + i) * kVpt + j) * nt + v, p + col[j] * ES);
+                }
+            }
+        }
+        cp_async_commit();
+    };
+    for (int s = 0; s < sp.stages - 1; ++s) issue(s, s);
+    P gm[kVpt], pe[kVpt], acc1[kVpt], acc2[kVpt];
+#pragma unroll
+    for (int j = 0; j < kVpt; ++j) {
+        gm[j].fill(0.f);
+        pe[j].fill(1.f);
+        acc1[j].fill(0.f);
+        acc2[j].fill(0.f);
+        if (!act[j]) continue;
+        if (a.dY) gm[j].unpack(ld_global_v4(a.gamma + col[j] * ES));
+        if constexpr (POST) pe[j].unpack(ld_global_v4(a.post_gamma + col[j] * ES));
+        if (!FULL && a.gate_kind == FOAK_GATE_CHANNEL) {
+            P e;
+            e.unpack(ld_global_v4(a.gate + col[j] * ES));
+#pragma unroll
+            for (int k = 0; k < NP; ++k) pe[j].p[k] = __fmul2_rn(pe[j].p[k], e.p[k]);
+        }
+    }
+    float rn[RR], r1n[RR], qn[RR];  // the next batch's scalars
+    auto scalars = [&](int64_t row0) {
+#pragma unroll
+        for (int q = 0; q < RR; ++q) {
+            const int64_t row = row0 + q;
+            const bool in = row < r_end;
+            rn[q] = in && a.dY ? a.rstd[row] : 0.f;
+            r1n[q] = POST && in ? a.post_rstd[row] : 1.f;
+            qn[q] = in && !FULL ? row_factor<ES>(a, row) : a.scale;
+        }
+    };
+    scalars(r_begin);
+    const bool weighted = FULL || a.gate_kind == FOAK_GATE_ROW;
+    int par = 0, stage = 0;
+    for (int64_t b = 0; b < nb; ++b, par ^= 1) {
+        // the stage of batch b - 1, read before the last barrier, takes batch b + stages - 1
+        issue(b + sp.stages - 1, stage == 0 ? sp.stages - 1 : stage - 1);
+        const int64_t row0 = r_begin + b * RR;
+        float r[RR], r1[RR], fq[RR];
+#pragma unroll
+        for (int q = 0; q < RR; ++q) {
+            r[q] = rn[q];
+            r1[q] = r1n[q];
+            fq[q] = qn[q];
+        }
+        scalars(row0 + RR);
+        cp_async_wait_all_but(sp.stages - 1);  // this thread's copies of batch b have landed
+        const uint4* slot = ring + stage * stage_vecs;
+        stage = stage + 1 == sp.stages ? 0 : stage + 1;
+#pragma unroll
+        for (int q = 0; q < RR; ++q) {
+            float2 s1 = both(0.f), s2 = both(0.f), s3 = both(0.f);
+            if (row0 + q < r_end) {
+#pragma unroll
+                for (int j = 0; j < kVpt; ++j) {
+                    if (!act[j]) continue;
+                    const uint4* at = slot + (q * NS * kVpt + j) * nt + v;
+                    P dy, h;
+                    dy.unpack(at[0]);
+                    h.unpack(at[kVpt * nt]);
+                    P d, w;
+                    if constexpr (SUMS) {
+                        d.unpack(at[2 * kVpt * nt]);
+                        w.unpack(at[3 * kVpt * nt]);
+                        if constexpr (FULL) {
+                            P e;
+                            e.unpack(at[(NS - 1) * kVpt * nt]);
+#pragma unroll
+                            for (int k = 0; k < NP; ++k) w.p[k] = __fmul2_rn(w.p[k], e.p[k]);
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < NP; ++k) {
+                        const float2 t = __fmul2_rn(gm[j].p[k], dy.p[k]);
+                        s1 = __ffma2_rn(h.p[k], t, s1);
+                        if constexpr (SUMS) {
+                            w.p[k] = __fmul2_rn(w.p[k], pe[j].p[k]);
+                            s2 = __ffma2_rn(w.p[k], __ffma2_rn(both(r[q]), t, d.p[k]), s2);
+                            s3 = __ffma2_rn(w.p[k], h.p[k], s3);
+                        }
+                    }
+                }
+            }
+            float* mine = &red[par][q][rank * warps + warp][0];
+            float z;
+            if constexpr (SUMS) z = warp_sum4(s1.x + s1.y, s2.x + s2.y, s3.x + s3.y, 0.f, lane);
+            else z = warp_sum(s1.x + s1.y);
+            if (SUMS ? (lane & 7) == 0 : lane == 0) {
+                if constexpr (SUMS) mine += lane >> 3;
+                if (C == 1) *mine = z;
+                else
+                    for (int c = 0; c < C; ++c) st_cluster_f32(mapa_u32(mine, c), z);
+            }
+        }
+        if (C > 1) cluster_sync();
+        else __syncthreads();
+#pragma unroll
+        for (int q = 0; q < RR; ++q) {
+            const int64_t row = row0 + q;
+            float S1, S2 = 0.f, S3 = 0.f, z = 0.f;
+            const int entries = C * warps;
+            if constexpr (SUMS) {
+                for (int e = lane & 7; e < entries; e += 8) z += red[par][q][e][lane >> 3];
+#pragma unroll
+                for (int off = 4; off > 0; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
+                S1 = __shfl_sync(0xffffffffu, z, 0);
+                S2 = __shfl_sync(0xffffffffu, z, 8);
+                S3 = __shfl_sync(0xffffffffu, z, 16);
+            } else {
+                for (int e = lane; e < entries; e += 32) z += red[par][q][e][0];
+                S1 = warp_sum(z);
+            }
+            if (row >= r_end) continue;
+            const float k1 = r[q] * r[q] * (r[q] * S1 * inv_d);
+            float k2 = 0.f;
+            if constexpr (SUMS) {
+                const float E = r1[q] * (S2 - k1 * S3);
+                k2 = r1[q] * r1[q] * (fq[q] * E * inv_d);
+                if (rank == 0 && v == 0 && a.gate_kind == FOAK_GATE_ROW && a.dgate)
+                    reinterpret_cast<float*>(a.dgate)[row] = a.scale * E;
+            }
+            const float2 rr = both(r[q]), nk1 = both(-k1), nk2 = both(-k2), qq = both(fq[q]), rx = both(r1[q]);
+#pragma unroll
+            for (int j = 0; j < kVpt; ++j) {
+                if (!act[j]) continue;
+                const uint4* at = slot + (q * NS * kVpt + j) * nt + v;
+                P dy, h, d, x, e, o;
+                dy.unpack(at[0]);
+                h.unpack(at[kVpt * nt]);
+                d.unpack(at[2 * kVpt * nt]);
+                if constexpr (HASX) x.unpack(at[3 * kVpt * nt]);
+                if constexpr (FULL) e.unpack(at[(NS - 1) * kVpt * nt]);
+#pragma unroll
+                for (int k = 0; k < NP; ++k) {
+                    acc1[j].p[k] = __ffma2_rn(dy.p[k], __fmul2_rn(h.p[k], rr), acc1[j].p[k]);
+                    d.p[k] = __ffma2_rn(rr, __fmul2_rn(gm[j].p[k], dy.p[k]), d.p[k]);
+                    d.p[k] = __ffma2_rn(nk1, h.p[k], d.p[k]);
+                    float2 du = __fmul2_rn(qq, d.p[k]);
+                    if constexpr (FULL) {
+                        // the gate's gradient takes the gate's place
+                        float2 dg = __fmul2_rn(du, x.p[k]);
+                        if constexpr (POST) dg = __fmul2_rn(dg, __fmul2_rn(rx, pe[j].p[k]));
+                        du = __fmul2_rn(du, e.p[k]);
+                        e.p[k] = dg;
+                    }
+                    if constexpr (HASX) {
+                        float2 xh = x.p[k];
+                        if constexpr (POST) xh = __fmul2_rn(xh, rx);
+                        acc2[j].p[k] = __ffma2_rn(weighted ? du : d.p[k], xh, acc2[j].p[k]);
+                    }
+                    du = __fmul2_rn(du, pe[j].p[k]);
+                    if constexpr (POST) du = __ffma2_rn(nk2, x.p[k], __fmul2_rn(rx, du));
+                    o.p[k] = du;
+                }
+                d.store(a.dR + (row * a.lddr + col[j]) * ES);
+                if (a.dX) o.store(a.dX + (row * a.lddx + col[j]) * ES);
+                if constexpr (FULL)
+                    if (a.dgate) e.store(a.dgate + (row * a.lddg + col[j]) * ES);
+            }
+        }
+    }
+    cp_async_wait<0>();  // no copy outlives the CTA (the trailing groups are empty)
+#pragma unroll
+    for (int j = 0; j < kVpt; ++j) {
+        if (!act[j]) continue;
+        float* p1 = part1 + cid * a.D + col[j];
+        float* p2 = part2 + cid * a.D + col[j];
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+            if (a.dgamma) *reinterpret_cast<float2*>(p1 + 2 * k) = acc1[j].p[k];
+            if (HASX && part2) *reinterpret_cast<float2*>(p2 + 2 * k) = acc2[j].p[k];
+        }
+    }
+}
+
 // The sums over the groups in a fixed order: 32 slices of 32 columns a CTA, each adding every 32nd group,
 // then the slices in order.  blockIdx.y 0: dgamma; 1: the gate's and the post norm's from the same sums.
-constexpr int kRedCols = 32, kRedSlices = 32, kRedMaxG = 512;
+constexpr int kRedCols = 32, kRedSlices = 32, kRedBatch = 10;
 template <int ES>
 __global__ void __launch_bounds__(kRedCols * kRedSlices)
     resnorm_reduce_kernel(const ResNormBwd a, const float* part1, const float* part2, int G) {
@@ -260,14 +583,16 @@ __global__ void __launch_bounds__(kRedCols * kRedSlices)
     const int64_t j = static_cast<int64_t>(blockIdx.x) * kRedCols + c;
     float s = 0.f;
     if (j < a.D) {
-        float val[kRedMaxG / kRedSlices];
+        for (int g0 = sl; g0 < G; g0 += kRedBatch * kRedSlices) {  // a batch's loads go out together
+            float val[kRedBatch];
 #pragma unroll
-        for (int i = 0; i < kRedMaxG / kRedSlices; ++i) {
-            const int g = sl + i * kRedSlices;
-            val[i] = g < G ? part[static_cast<int64_t>(g) * a.D + j] : 0.f;
+            for (int i = 0; i < kRedBatch; ++i) {
+                const int g = g0 + i * kRedSlices;
+                val[i] = g < G ? part[static_cast<int64_t>(g) * a.D + j] : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < kRedBatch; ++i) s += val[i];
         }
-#pragma unroll
-        for (int i = 0; i < kRedMaxG / kRedSlices; ++i) s += val[i];
     }
     ss[sl][c] = s;
     __syncthreads();
@@ -315,6 +640,86 @@ cudaError_t fwd(const ResNormFwd& a, cudaStream_t s) {
     return launch_dependent(resnorm_fwd_row_kernel<ES>, dim3(grid), dim3(threads), static_cast<size_t>(a.D) * 4, s, a);
 }
 
+// Clusters of the ring kernel that are resident at once; asked once for a device and shape.
+template <typename K>
+cudaError_t resident_clusters(K kernel, int cluster, int threads, size_t smem, int* count) {
+    static std::mutex mu;
+    static std::map<std::array<int64_t, 5>, int> known;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    const std::array<int64_t, 5> key = {reinterpret_cast<int64_t>(kernel), dev, cluster, threads, static_cast<int64_t>(smem)};
+    const auto at = known.find(key);
+    if (at != known.end()) {
+        *count = at->second;
+        return cudaSuccess;
+    }
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem);
+    if (e != cudaSuccess) return e;
+    int n = 0;
+    if (cluster == 1) {
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem);
+        n *= device_sm_count();
+    } else {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(cluster));
+        cfg.blockDim = dim3(static_cast<unsigned>(threads));
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = static_cast<unsigned>(cluster);
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+    }
+    if (e != cudaSuccess) return e;
+    known[key] = *count = std::max(n, 1);
+    return cudaSuccess;
+}
+
+template <int ES, bool POST, bool FULL, bool HASX, bool SUMS, int RR>
+cudaError_t launch_ring(const ResNormBwd& a, const BwdSplit& sp, int threads, float* part1, float* part2, int* groups,
+                        cudaStream_t s) {
+    const auto kernel = resnorm_bwd_ring_kernel<ES, POST, FULL, HASX, SUMS, RR>;
+    const size_t smem = static_cast<size_t>(sp.stages) * RR * (3 + HASX + FULL) * kVpt * threads * 16;
+    int resident = 0;
+    cudaError_t e = resident_clusters(kernel, sp.cluster, threads, smem, &resident);
+    if (e != cudaSuccess) return e;
+    const int64_t G = std::min<int64_t>({(a.N + RR - 1) / RR, resident, resnorm_groups(a.D)});
+    *groups = static_cast<int>(G);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(G * sp.cluster));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(sp.cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = sp.cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a, sp, part1, part2);
+}
+
+template <int ES, bool POST, bool FULL, bool HASX, bool SUMS>
+cudaError_t ring(const ResNormBwd& a, float* part1, float* part2, int* groups, cudaStream_t s) {
+    const int nvec = static_cast<int>(a.D / (16 / ES));
+    BwdSplit sp = {1, 0, 0};
+    while ((nvec + sp.cluster - 1) / sp.cluster > kSliceVecs) sp.cluster *= 2;
+    sp.slice = (nvec + sp.cluster - 1) / sp.cluster;
+    const int threads = ((sp.slice + kVpt - 1) / kVpt + 31) / 32 * 32;
+    const int row = (3 + HASX + FULL) * kVpt * threads * 16;
+    // two rows a barrier where three batches of them are in the ring
+    const int rr = 6 * row <= kRingSmem ? 2 : 1;
+    sp.stages = std::min(kRingSmem / (rr * row), 4);
+    return rr == 2 ? launch_ring<ES, POST, FULL, HASX, SUMS, 2>(a, sp, threads, part1, part2, groups, s)
+                   : launch_ring<ES, POST, FULL, HASX, SUMS, 1>(a, sp, threads, part1, part2, groups, s);
+}
+
 template <int ES>
 cudaError_t bwd(const ResNormBwd& a, void* workspace, cudaStream_t s) {
     const int groups = resnorm_groups(a.D);
@@ -322,16 +727,27 @@ cudaError_t bwd(const ResNormBwd& a, void* workspace, cudaStream_t s) {
     float* part2 = part1 + static_cast<size_t>(groups) * a.D;
     RowStats* stats = reinterpret_cast<RowStats*>(part2 + static_cast<size_t>(groups) * a.D);
     const bool second = (a.gate_kind == FOAK_GATE_CHANNEL && a.dgate) || a.dpost_gamma;
+    const bool full = a.gate_kind == FOAK_GATE_FULL, row_grad = a.gate_kind == FOAK_GATE_ROW && a.dgate;
     const int64_t nvec = a.D / (16 / ES);
-    const int G = static_cast<int>(std::min<int64_t>(std::max<int64_t>(a.N, 1), 128));
+    int G = static_cast<int>(std::min<int64_t>(std::max<int64_t>(a.N, 1), 128));
     cudaError_t e = cudaSuccess;
-    if (a.N > 0) {
+    const bool one_pass = a.N > 0 && nvec <= static_cast<int64_t>(kSliceVecs) * kMaxCluster && (a.X || !full);
+    if (one_pass) {
+        float* p2 = second ? part2 : nullptr;
+        if (a.post_gamma)
+            e = full ? ring<ES, true, true, true, true>(a, part1, p2, &G, s) : ring<ES, true, false, true, true>(a, part1, p2, &G, s);
+        else if (!a.X) e = ring<ES, false, false, false, false>(a, part1, p2, &G, s);
+        else if (full) e = ring<ES, false, true, true, false>(a, part1, p2, &G, s);
+        else e = row_grad ? ring<ES, false, false, true, true>(a, part1, p2, &G, s) : ring<ES, false, false, true, false>(a, part1, p2, &G, s);
+        if (e != cudaSuccess) return e;
+    } else if (a.N > 0) {
         const int grid = static_cast<int>(std::min<int64_t>(a.N, static_cast<int64_t>(device_sm_count()) * 8));
         e = launch_dependent(resnorm_bwd_stats_kernel<ES>, dim3(grid), dim3(256), 0, s, a, stats);
         if (e != cudaSuccess) return e;
     }
-    e = launch_dependent(resnorm_bwd_cols_kernel<ES>, dim3(static_cast<unsigned>((nvec + 127) / 128), G), dim3(128), 0,
-                         s, a, static_cast<const RowStats*>(stats), part1, second ? part2 : nullptr);
+    if (!one_pass)
+        e = launch_dependent(resnorm_bwd_cols_kernel<ES>, dim3(static_cast<unsigned>((nvec + 127) / 128), G), dim3(128), 0,
+                             s, a, static_cast<const RowStats*>(stats), part1, second ? part2 : nullptr);
     if (e != cudaSuccess || (!a.dgamma && !second)) return e;
     const dim3 rgrid(static_cast<unsigned>((a.D + kRedCols - 1) / kRedCols), a.dgamma && second ? 2 : 1);
     return launch_dependent(resnorm_reduce_kernel<ES>, rgrid, dim3(kRedCols * kRedSlices), 0, s, a,

@@ -44,8 +44,12 @@ struct ResNormBwd {
 
 constexpr int64_t kResNormMaxD = 32768;  // a row of the forward as floats in shared memory
 
-// Partial sums of up to this many groups of rows, for the two gradients that are summed over the rows.
-inline int resnorm_groups(int64_t D) { return D <= 8192 ? 512 : 128; }
+// Partial sums of up to this many groups of rows, for the two gradients that are summed over the rows: 16 MB
+// each, which is as many groups as are resident at once, whatever D.
+inline int resnorm_groups(int64_t D) {
+    const int64_t n = (1 << 22) / D;
+    return static_cast<int>(n < 128 ? 128 : n > 2432 ? 2432 : n);
+}
 inline size_t resnorm_workspace_bytes(int64_t N, int64_t D) {
     const size_t part = static_cast<size_t>(resnorm_groups(D)) * static_cast<size_t>(D) * 4;
     return (2 * part + static_cast<size_t>(N) * 16 + 255) / 256 * 256;

@@ -12,9 +12,8 @@
 // and x^10, whose next terms are below 1.8e-9 and 1.2e-10.
 //
 // Work.  A unit is two vectors of a head whose pairs have the same frequencies: the vectors at
-// i and i + r/2, or two adjacent ones; of the part that passes through, two adjacent ones.  A
-// thread takes its unit in several heads of a token, so that an angle is formed once for them.
-// Bound by memory: each element is read and written once.
+// i and i + r/2, or two adjacent ones; of the part that passes through, two adjacent ones.  An
+// angle is formed once for many heads.  Each element is read and written once.
 #include <algorithm>
 #include <cmath>
 
@@ -148,112 +147,309 @@ __host__ __device__ __forceinline__ int units_of(int d, int r, bool interleaved)
     return turning + (d - r + 2 * W - 1) / (2 * W);
 }
 
-// The CTAs' ranges: move m has blocks [first[m], first[m + 1]) of kThreads (token, heads, unit)
-// items, units fastest.
-struct Split {
-    unsigned first[4];
-    unsigned units[3];
-    unsigned groups[3];  // of HPT heads
-    int64_t t0, t1;      // the launch's tokens
+// Division of numbers below 2^31 by one that a launch keeps: multiplied by 2^(31 + b) / d, rounded up,
+// where d <= 2^b; the product's excess stays below 1 / d of the quotient's unit.
+struct Divisor {
+    unsigned d, mul, shift;
 };
 
-template <int ES, int W, bool INTERLEAVED, int HPT>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a, const Split sp) {
-    griddep_launch_dependents();  // programmatic dependent launch: no global access before the wait
-    griddep_wait();
-    const unsigned m = blockIdx.x >= sp.first[2] ? 2 : blockIdx.x >= sp.first[1] ? 1 : 0;
-    const HeadMove& mv = a.move[m];
-    const unsigned item = (blockIdx.x - sp.first[m]) * kThreads + threadIdx.x;
-    const unsigned units = sp.units[m], groups = sp.groups[m];
-    const unsigned rest = item / units;
-    const int64_t t = sp.t0 + rest / groups;
-    if (t >= sp.t1) return;
-    const int h0 = static_cast<int>(rest % groups) * HPT;
-    const Unit u = unit_of<W, INTERLEAVED>(static_cast<int>(item % units), mv.d, mv.r);
-    const int64_t slot = a.slots ? a.slots[t] : 0;
-    const int64_t p = u.freq >= 0 ? a.positions[t] : 0;
-    const char* src = mv.src + (t * mv.src_t + h0 * mv.src_h) * ES;
-    Piece<ES, W> v[HPT][2];
+Divisor divisor(unsigned d) {
+    Divisor v = {d, 0, 0};
+    if (d == 1) return v;
+    unsigned b = 1;
+    while ((1ull << b) < d) ++b;
+    v.mul = static_cast<unsigned>((1ull << (31 + b)) / d + 1);
+    v.shift = b - 1;
+    return v;
+}
+
+__device__ __forceinline__ unsigned quotient(unsigned n, const Divisor& v) {
+    return v.d == 1 ? n : __umulhi(n, v.mul) >> v.shift;
+}
+
+// The rotation of a unit's two vectors by W cosines and sines.
+template <int W, bool INTERLEAVED>
+__device__ __forceinline__ void rotate(float (&x)[W], float (&y)[W], const float (&co)[W], const float (&si)[W]) {
+    if constexpr (INTERLEAVED && W > 1) {
 #pragma unroll
-    for (int i = 0; i < HPT; ++i) {
-        if (h0 + i < mv.H) {
-            v[i][0].load(src + (i * mv.src_h + u.at0) * ES);
-            if (u.two) v[i][1].load(src + (i * mv.src_h + u.at1) * ES);
-            else v[i][1] = v[i][0];
+        for (int k = 0; k < W / 2; ++k) {
+            const float a = x[2 * k], b = x[2 * k + 1], c = y[2 * k], d = y[2 * k + 1];
+            x[2 * k] = fmaf(a, co[k], -b * si[k]);
+            x[2 * k + 1] = fmaf(b, co[k], a * si[k]);
+            y[2 * k] = fmaf(c, co[W / 2 + k], -d * si[W / 2 + k]);
+            y[2 * k + 1] = fmaf(d, co[W / 2 + k], c * si[W / 2 + k]);
         }
-    }
-    if (a.slots && static_cast<uint64_t>(slot) >= static_cast<uint64_t>(a.capacity)) {  // not a token of the cache
-        if (slot >= 0 && a.err) atomicOr(reinterpret_cast<unsigned*>(a.err), FOAK_ERRBIT_PAGE_RANGE);
-        return;
-    }
-    int64_t to = t * mv.dst_t;
-    if (mv.paged) to = slot / a.page_size * mv.dst_page + slot % a.page_size * mv.dst_t;
-    char* dst = mv.dst + (to + h0 * mv.dst_h) * ES;
-    if (u.freq >= 0) {
-        float co[W], si[W];
-        constexpr int F = INTERLEAVED && W > 1 ? W / 2 : W;  // frequencies of one vector
+    } else {
 #pragma unroll
-        for (int k = 0; k < W; ++k)
-            if (k < F || u.turn1)
-                turn_cos_sin(static_cast<uint64_t>(p) * a.turns[u.freq + k], a.factor, a.sign, co[k], si[k]);
-#pragma unroll
-        for (int i = 0; i < HPT; ++i) {
-            if (h0 + i >= mv.H) continue;
-            float x[W], y[W], ox[W], oy[W];
-            v[i][0].get(x);
-            v[i][1].get(y);
-            if constexpr (INTERLEAVED && W > 1) {
-#pragma unroll
-                for (int k = 0; k < W / 2; ++k) {
-                    ox[2 * k] = fmaf(x[2 * k], co[k], -x[2 * k + 1] * si[k]);
-                    ox[2 * k + 1] = fmaf(x[2 * k + 1], co[k], x[2 * k] * si[k]);
-                    oy[2 * k] = fmaf(y[2 * k], co[F + k], -y[2 * k + 1] * si[F + k]);
-                    oy[2 * k + 1] = fmaf(y[2 * k + 1], co[F + k], y[2 * k] * si[F + k]);
-                }
-            } else {
-#pragma unroll
-                for (int k = 0; k < W; ++k) {
-                    ox[k] = fmaf(x[k], co[k], -y[k] * si[k]);
-                    oy[k] = fmaf(y[k], co[k], x[k] * si[k]);
-                }
-            }
-            v[i][0].set(ox);
-            v[i][1].set(oy);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < HPT; ++i) {
-        if (h0 + i < mv.H) {
-            v[i][0].store(dst + (i * mv.dst_h + u.at0) * ES);
-            if (u.two) v[i][1].store(dst + (i * mv.dst_h + u.at1) * ES);
+        for (int k = 0; k < W; ++k) {
+            const float a = x[k], b = y[k];
+            x[k] = fmaf(a, co[k], -b * si[k]);
+            y[k] = fmaf(b, co[k], a * si[k]);
         }
     }
 }
 
-template <int ES, int W, bool INTERLEAVED, int HPT>
-cudaError_t launch_heads(const RotaryArgs& a, cudaStream_t s) {
-    Split sp = {};
-    uint64_t items = 1;  // of a token, the largest move's
+// The items of a token are the units of its heads: those of move 0, then of 1 and 2, heads by heads,
+// units fastest.
+struct Items {
+    Divisor per_token;
+    Divisor units[3];
+    unsigned end[2];  // of a token's items of move 0, and of 1
+    unsigned count;   // of the launch
+    int freqs;        // r / 2
+    int64_t t0;       // the first token
+};
+
+struct Item {
+    unsigned m, h;  // move, head
+    Unit u;
+};
+
+template <int W, bool INTERLEAVED>
+__device__ __forceinline__ Item item_of(unsigned at, const RotaryArgs& a, const Items& it) {
+    Item x;
+    x.m = at >= it.end[1] ? 2 : at >= it.end[0] ? 1 : 0;
+    at -= x.m == 2 ? it.end[1] : x.m == 1 ? it.end[0] : 0;
+    x.h = quotient(at, it.units[x.m]);
+    x.u = unit_of<W, INTERLEAVED>(static_cast<int>(at - x.h * it.units[x.m].d), a.move[x.m].d, a.move[x.m].r);
+    return x;
+}
+
+// Where token t of a move goes, in elements; -1: nowhere.
+__device__ __forceinline__ int64_t place_of(const RotaryArgs& a, const HeadMove& mv, int64_t t) {
+    if (!a.slots) return t * mv.dst_t;
+    const int64_t slot = a.slots[t];
+    if (static_cast<uint64_t>(slot) >= static_cast<uint64_t>(a.capacity)) {  // padding, or past the cache
+        if (slot >= 0 && a.err) atomicOr(reinterpret_cast<unsigned*>(a.err), FOAK_ERRBIT_PAGE_RANGE);
+        return -1;
+    }
+    if (!mv.paged) return t * mv.dst_t;
+    const int64_t page = slot / a.page_size;
+    return page * mv.dst_page + (slot - page * a.page_size) * mv.dst_t;
+}
+
+// A pass is what a warp moves at a time: one unit a lane, of as many heads as 32 lanes hold (or 32
+// units of a head that has more).  A move has chunks x blocks passes a token, blocks of heads fastest.
+struct Passes {
+    Divisor jobs;      // of a token
+    unsigned share;    // passes of a job
+    unsigned count;    // jobs of the launch
+    unsigned end[3];   // of a token's passes of moves 0, 1, 2
+    int units[3];      // of a head
+    int lanes_head[3]; // heads of a pass
+    int blocks[3];
+    int turning;       // units of a head that turn
+    int freqs;         // r / 2
+    int64_t t0;        // the first token
+};
+
+// A warp's job is a run of a token's passes, kDepth of them in flight.  Behind the first loads it forms the
+// token's cosines and sines, once for all heads of the job, in its part of shared memory: for W > 1
+// vectors of (two cosines, two sines), those of one unit `turning` vectors apart, so that neighbouring
+// units read neighbouring 16 bytes; for W = 1 a cosine and a sine a unit.  A lane keeps its unit while it
+// goes through the heads, so that a pass is two loads, the rotation and two stores.
+//
+// Bound by memory latency: it is the warps in flight that count.  8192 tokens of 32 + 8 heads x 128
+// bf16: 32.7 us, 5.1 TB/s (a copy of as many bytes 26.2).  At 48 registers (five CTAs an SM) and the
+// table read at each pass; with it in registers (91) 49 us, without the bound (63) 39; each head's angles
+// by its own thread 47.6, by CTAs with a table a CTA 36.2.
+constexpr int kDepth = 2;
+constexpr int kWarpCtas = 5;
+constexpr int kMaxShare = 6;
+template <int ES, int W, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads, kWarpCtas)
+    rotary_warp_kernel(const __grid_constant__ RotaryArgs a, const __grid_constant__ Passes ps) {
+    griddep_launch_dependents();  // programmatic dependent launch: no global access before the wait
+    griddep_wait();
+    extern __shared__ float4 tables[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const unsigned job = blockIdx.x * (kThreads / 32) + warp;
+    if (job >= ps.count) return;
+    const unsigned token = quotient(job, ps.jobs);
+    const int64_t t = ps.t0 + token;
+    unsigned p = (job - token * ps.jobs.d) * ps.share;
+    const unsigned p_end = min(p + ps.share, ps.end[2]);
+    float* cs = reinterpret_cast<float*>(tables) + static_cast<size_t>(warp) * ps.turning * W * 2;
+    bool table = false;
+    while (p < p_end) {
+        const int m = p >= ps.end[1] ? 2 : p >= ps.end[0] ? 1 : 0;
+        const HeadMove& mv = a.move[m];
+        const unsigned at = p - (m == 2 ? ps.end[1] : m == 1 ? ps.end[0] : 0);
+        const unsigned chunk = at / ps.blocks[m], block = at - chunk * ps.blocks[m];
+        const int n = min(min(ps.blocks[m] - block, p_end - p), ps.end[m] - p);  // passes of this chunk
+        p += n;
+        const int units = ps.units[m], heads = ps.lanes_head[m];
+        const int hl = units < 32 ? lane / units : 0, j = static_cast<int>(chunk) * 32 + lane - hl * units;
+        const Unit u = unit_of<W, INTERLEAVED>(j, mv.d, mv.r);
+        const int h = static_cast<int>(block) * heads + hl;
+        // none past the last head, or for a lane without a unit
+        int rounds = hl < heads && j < units ? min(n, (mv.H - h + heads - 1) / heads) : 0;
+        const char* src = mv.src + (t * mv.src_t + h * mv.src_h + u.at0) * ES;
+        const int64_t src_step = heads * mv.src_h * ES, dst_step = heads * mv.dst_h * ES;
+        const int second = (u.at1 - u.at0) * ES;
+        Piece<ES, W> v[kDepth][2];
+        auto fetch = [&](Piece<ES, W> (&x)[2]) {
+            x[0].load(src);
+            if (u.two) x[1].load(src + second);
+            else x[1] = x[0];
+            src += src_step;
+        };
+#pragma unroll
+        for (int q = 0; q < kDepth; ++q)
+            if (q < rounds) fetch(v[q]);
+        const int64_t to = place_of(a, mv, t);
+        if (mv.r && !table) {
+            table = true;
+            const uint64_t pos = static_cast<uint64_t>(a.positions[t]);
+#pragma unroll 1
+            for (int f = lane; f < ps.freqs; f += 32) {
+                const int i = f / W, k = f % W;
+                float co, si;
+                turn_cos_sin(pos * a.turns[f], a.factor, a.sign, co, si);
+                float* c = cs + (W == 1 ? 2 * i : (k / 2 * ps.turning + i) * 4 + k % 2);
+                c[0] = co;
+                c[W == 1 ? 1 : 2] = si;
+            }
+            __syncwarp();
+        }
+        if (to < 0) rounds = 0;
+        char* dst = mv.dst + (to + h * mv.dst_h + u.at0) * ES;
+        for (int i = 0; i < rounds; i += kDepth) {
+#pragma unroll
+            for (int q = 0; q < kDepth; ++q) {
+                if (i + q >= rounds) break;
+                if (u.freq >= 0) {
+                    float x[W], y[W];
+                    float co[W], si[W];
+                    if constexpr (W == 1) {
+                        const float2 c = *reinterpret_cast<const float2*>(cs + 2 * j);
+                        co[0] = c.x;
+                        si[0] = c.y;
+                    } else {
+                        const float4* at_j = reinterpret_cast<const float4*>(cs) + j;
+#pragma unroll
+                        for (int k = 0; k < W / 2; ++k) {
+                            const float4 c = at_j[k * ps.turning];
+                            co[2 * k] = c.x;
+                            co[2 * k + 1] = c.y;
+                            si[2 * k] = c.z;
+                            si[2 * k + 1] = c.w;
+                        }
+                    }
+                    v[q][0].get(x);
+                    v[q][1].get(y);
+                    rotate<W, INTERLEAVED>(x, y, co, si);
+                    v[q][0].set(x);
+                    v[q][1].set(y);
+                }
+                v[q][0].store(dst);
+                if (u.two) v[q][1].store(dst + second);
+                dst += dst_step;
+                if (i + q + kDepth < rounds) fetch(v[q]);
+            }
+        }
+    }
+}
+
+// The same without shared memory, an item a thread: heads so large that a few tokens' tables do not fit.
+template <int ES, int W, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads)
+    rotary_kernel(const __grid_constant__ RotaryArgs a, const __grid_constant__ Items it) {
+    griddep_launch_dependents();  // programmatic dependent launch: no global access before the wait
+    griddep_wait();
+    const unsigned item = blockIdx.x * kThreads + threadIdx.x;
+    if (item >= it.count) return;
+    const unsigned token = quotient(item, it.per_token);
+    const Item x = item_of<W, INTERLEAVED>(item - token * it.per_token.d, a, it);
+    const HeadMove& mv = a.move[x.m];
+    const int64_t t = it.t0 + token, to = place_of(a, mv, t);
+    if (to < 0) return;
+    const char* src = mv.src + (t * mv.src_t + x.h * mv.src_h) * ES;
+    Piece<ES, W> v[2];
+    v[0].load(src + x.u.at0 * ES);
+    if (x.u.two) v[1].load(src + x.u.at1 * ES);
+    else v[1] = v[0];
+    if (x.u.freq >= 0) {
+        float co[W], si[W], p[W], q[W];
+        const uint64_t pos = static_cast<uint64_t>(a.positions[t]);
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            const int f = min(x.u.freq + k, it.freqs - 1);  // past the end only where there is no second vector
+            turn_cos_sin(pos * a.turns[f], a.factor, a.sign, co[k], si[k]);
+        }
+        v[0].get(p);
+        v[1].get(q);
+        rotate<W, INTERLEAVED>(p, q, co, si);
+        v[0].set(p);
+        v[1].set(q);
+    }
+    char* dst = mv.dst + (to + x.h * mv.dst_h) * ES;
+    v[0].store(dst + x.u.at0 * ES);
+    if (x.u.two) v[1].store(dst + x.u.at1 * ES);
+}
+
+constexpr size_t kTableSmem = 48 * 1024;
+
+template <int ES, int W, bool INTERLEAVED>
+cudaError_t launch_items(const RotaryArgs& a, cudaStream_t s) {
+    Items it = {};
+    unsigned end = 0;
     for (int m = 0; m < 3; ++m) {
         const HeadMove& mv = a.move[m];
-        sp.units[m] = 1;
-        sp.groups[m] = 1;
-        if (!mv.src) continue;
-        sp.units[m] = static_cast<unsigned>(units_of<W>(mv.d, mv.r, INTERLEAVED));
-        sp.groups[m] = static_cast<unsigned>((mv.H + HPT - 1) / HPT);
-        items = std::max(items, static_cast<uint64_t>(sp.units[m]) * sp.groups[m]);
-    }
-    // a launch's items of a move stay below 2^29, its blocks below 2^31
-    const int64_t step = std::max<int64_t>(1, static_cast<int64_t>((1u << 29) / items));
-    for (int64_t t0 = 0; t0 < a.T; t0 += step) {
-        sp.t0 = t0;
-        sp.t1 = std::min(a.T, t0 + step);
-        for (int m = 0; m < 3; ++m) {
-            const uint64_t n = a.move[m].src ? static_cast<uint64_t>(sp.t1 - t0) * sp.units[m] * sp.groups[m] : 0;
-            sp.first[m + 1] = sp.first[m] + static_cast<unsigned>((n + kThreads - 1) / kThreads);
+        it.units[m] = divisor(1);
+        if (mv.src) {
+            it.units[m] = divisor(static_cast<unsigned>(units_of<W>(mv.d, mv.r, INTERLEAVED)));
+            end += it.units[m].d * static_cast<unsigned>(mv.H);
+            if (mv.r) it.freqs = mv.r / 2;
         }
-        const cudaError_t e = launch_dependent(rotary_kernel<ES, W, INTERLEAVED, HPT>, dim3(sp.first[3]), dim3(kThreads),
-                                               0, s, a, sp);
+        if (m < 2) it.end[m] = end;
+    }
+    it.per_token = divisor(end);
+    const int64_t step = std::max<int64_t>(1, static_cast<int64_t>((1u << 30) / end));  // items of a launch below 2^31
+    for (it.t0 = 0; it.t0 < a.T; it.t0 += step) {
+        it.count = static_cast<unsigned>(std::min(a.T - it.t0, step)) * end;
+        const cudaError_t e = launch_dependent(rotary_kernel<ES, W, INTERLEAVED>, dim3((it.count + kThreads - 1) / kThreads),
+                                               dim3(kThreads), 0, s, a, it);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+template <int ES, int W, bool INTERLEAVED>
+cudaError_t launch_heads(const RotaryArgs& a, cudaStream_t s) {
+    Passes ps = {};
+    unsigned end = 0;
+    for (int m = 0; m < 3; ++m) {
+        const HeadMove& mv = a.move[m];
+        ps.units[m] = ps.lanes_head[m] = ps.blocks[m] = 1;
+        if (mv.src) {
+            ps.units[m] = units_of<W>(mv.d, mv.r, INTERLEAVED);
+            ps.lanes_head[m] = ps.units[m] < 32 ? 32 / ps.units[m] : 1;
+            ps.blocks[m] = (mv.H + ps.lanes_head[m] - 1) / ps.lanes_head[m];
+            end += static_cast<unsigned>((ps.units[m] + 31) / 32) * ps.blocks[m];
+            if (mv.r) {
+                ps.freqs = mv.r / 2;
+                ps.turning = INTERLEAVED ? (mv.r + 2 * W - 1) / (2 * W) : mv.r / 2 / W;
+            }
+        }
+        ps.end[m] = end;
+    }
+    const size_t smem = static_cast<size_t>(ps.turning) * W * 8 * (kThreads / 32);
+    if (smem > kTableSmem) return launch_items<ES, W, INTERLEAVED>(a, s);
+    // Small calls: a pass a job, for the latency (256 tokens of 48 + 8 + 8 heads 5.9 us, by twos 7.4).  Once the
+    // passes fill the resident warps several times over, up to six a job for the angles (3001 tokens of
+    // 9 passes: 13.5 us by ones, 10.7 by fives).
+    const int64_t share = a.T * end / (static_cast<int64_t>(device_sm_count()) * (kWarpCtas * kThreads / 32));
+    unsigned jobs = (end + kMaxShare - 1) / kMaxShare;
+    if (share < kMaxShare) jobs = share > 1 ? (end + share - 1) / share : end;
+    ps.share = (end + jobs - 1) / jobs;
+    jobs = (end + ps.share - 1) / ps.share;
+    ps.jobs = divisor(jobs);
+    const int64_t step = std::max<int64_t>(1, static_cast<int64_t>((1u << 30) / jobs));  // jobs of a launch below 2^31
+    for (ps.t0 = 0; ps.t0 < a.T; ps.t0 += step) {
+        ps.count = static_cast<unsigned>(std::min(a.T - ps.t0, step)) * jobs;
+        const dim3 grid((ps.count + kThreads / 32 - 1) / (kThreads / 32)), block(kThreads);
+        const cudaError_t e = launch_dependent(rotary_warp_kernel<ES, W, INTERLEAVED>, grid, block, smem, s, a, ps);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -261,7 +457,7 @@ cudaError_t launch_heads(const RotaryArgs& a, cudaStream_t s) {
 
 template <int ES, int W>
 cudaError_t launch_width(const RotaryArgs& a, cudaStream_t s) {
-    return a.interleaved ? launch_heads<ES, W, true, 1>(a, s) : launch_heads<ES, W, false, 1>(a, s);
+    return a.interleaved ? launch_heads<ES, W, true>(a, s) : launch_heads<ES, W, false>(a, s);
 }
 
 // The widest access that every vector of every head allows.

@@ -80,11 +80,11 @@ def test_parts_that_are_left_out(cuda_lib, D, dtype):
         _check_forward(ce, c, 0.5, gamma=False)
         _check_backward(ce, c, 0.5, with_dH=False)
         _check_backward(ce, c, 0.5, with_dY=False)
-        full = _check_backward(ce, c, 0.5)
         H, rstd, post_rstd = _saved(c, 0.5)
         g = _cuda(c)
         part = ce.foak_residual_norm_backward(g["dY"], g["dH"], H.cuda(), rstd.cuda(), g["gamma"], X=g["X"], gate=g["gate"], post_gamma=g["post_gamma"], post_rstd=None if post_rstd is None else post_rstd.cuda(), scale=0.5, want_dX=False, want_dgate=False, want_dgamma=False)
-        assert torch.equal(part["dR"], full["dR"])
+        # another variant, with its sums in another order: within the same bound
+        ref.assert_close(part["dR"], ref.norm_backward(c["dY"], c["dH"], H, rstd, c["gamma"], c["X"], c["gate"], c["post_gamma"], post_rstd, 0.5)["dR"], "dR")
         assert part["dX"] is None and part["dgate"] is None and part["dgamma"] is None and part["dpost_gamma"] is None
 
 
