@@ -34,72 +34,182 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
     return warp_sum(lane < static_cast<int>(blockDim.x >> 5) ? red[lane] : 0.f);
 }
 
-// Rows of any length up to kResNormMaxD, a CTA a row: h stays in shared memory as floats between
-// the sum of its squares and y.
+constexpr int kVpt = 2;
+constexpr int kRowThreads = 256;
+constexpr int kSliceVecs = kVpt * kRowThreads;
+constexpr int kMaxCluster = 8;
+constexpr int kRingSmem = 104 * 1024;  // two CTAs an SM
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all_but(int pending) {
+    if (pending == 1) cp_async_wait<1>();
+    else if (pending == 2) cp_async_wait<2>();
+    else cp_async_wait<3>();
+}
+
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// A 16-byte vector as element pairs.
 template <int ES>
-__global__ void __launch_bounds__(512) resnorm_fwd_row_kernel(const ResNormFwd a) {
+struct Pairs {
+    static constexpr int N = 8 / ES;
+    float2 p[N];
+    __device__ __forceinline__ void unpack(const uint4& w) {
+        if constexpr (ES == 2) {
+            p[0] = make_float2(bf16_lo(w.x), bf16_hi(w.x));
+            p[1] = make_float2(bf16_lo(w.y), bf16_hi(w.y));
+            p[2] = make_float2(bf16_lo(w.z), bf16_hi(w.z));
+            p[3] = make_float2(bf16_lo(w.w), bf16_hi(w.w));
+        } else {
+            p[0] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+            p[1] = make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
+        }
+    }
+    __device__ __forceinline__ void store(char* dst) const {
+        uint4 w;
+        if constexpr (ES == 2)
+            w = make_uint4(pack_bf16x2(p[0].x, p[0].y), pack_bf16x2(p[1].x, p[1].y), pack_bf16x2(p[2].x, p[2].y),
+                           pack_bf16x2(p[3].x, p[3].y));
+        else
+            w = make_uint4(__float_as_uint(p[0].x), __float_as_uint(p[0].y), __float_as_uint(p[1].x),
+                           __float_as_uint(p[1].y));
+        *reinterpret_cast<uint4*>(dst) = w;
+    }
+    __device__ __forceinline__ void fill(float v) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) p[k] = make_float2(v, v);
+    }
+};
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+
+// ------------------------------------------------------------------ forward
+// A CTA a row.  All of a row's loads go out before its first sum, kFwdBatch vectors of each operand a thread at
+// a time; shared memory keeps what later passes need, in slots that only their own thread touches: X and R
+// as loaded between the two sums of POST, h as floats (in their place) between its sum and y.  With the
+// norm after the block the second sum is of h itself: expanding it into sums of R and X would cancel
+// where the block takes the residual back.
+constexpr int kFwdBatch = 2;
+constexpr int kFwdSmem = static_cast<int>(kResNormMaxD) * 4;
+
+// Planes of 16 bytes a vector: h as floats, which with POST takes the place of X and R.
+constexpr int fwd_planes(int es, bool post, bool keep) { return es == 2 || (post && keep) ? 2 : 1; }
+
+// KEEP: R stays in shared memory too (POST); rows of more than 16384 floats have no room for it and read it again.
+template <int ES, bool POST, bool FULL, bool KEEP>
+__global__ void __launch_bounds__(512) resnorm_fwd_kernel(const ResNormFwd a) {
     griddep_launch_dependents();  // programmatic dependent launch: no global access before the wait
     griddep_wait();
-    using V = Vec16<ES>;
-    extern __shared__ float row_h[];
-    __shared__ float red[2][32];
-    const int nvec = static_cast<int>(a.D / V::N);
+    using P = Pairs<ES>;
+    constexpr int EPV = 16 / ES, NP = P::N;
+    extern __shared__ uint4 slots[];  // [planes][vectors]
+    __shared__ float red[4][32];
+    const int nvec = static_cast<int>(a.D / EPV), nt = blockDim.x;
     const float inv_d = 1.f / static_cast<float>(a.D);
-    for (int64_t i = blockIdx.x; i < a.N; i += gridDim.x) {
-        const char* x = a.X + i * a.ldx * ES;
-        const char* r = a.R + i * a.ldr * ES;
-        const char* g = a.gate_kind == FOAK_GATE_CHANNEL ? a.gate : a.gate + i * a.ldg * ES;
+    int buffer = 0;  // two rows in a row use different ones of `red`
+    for (int64_t i = blockIdx.x; i < a.N; i += gridDim.x, buffer ^= 2) {
+        const char* xr = a.X + i * a.ldx * ES;
+        const char* rr = a.R + i * a.ldr * ES;
+        const char* gr = a.gate_kind == FOAK_GATE_CHANNEL ? a.gate : a.gate + i * a.ldg * ES;
+        char* hr = a.H + i * a.ldh * ES;
         float q = a.scale;
-        if (a.gate_kind == FOAK_GATE_ROW) q *= V::load1(g);
-        if (a.post_gamma) {
-            float ss = 0.f;
-            for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
-                float f[V::N];
-                V::load(x + v * 16, f);
+        if (!FULL && a.gate_kind == FOAK_GATE_ROW) q *= Vec16<ES>::load1(gr);
+        float2 s2 = both(0.f);
+        // h of vector v from x and r, its square into s2
+        auto residual = [&](int v, P x, P h, const uint4& g) {
+            P w;
+            if constexpr (POST) {
+                w.unpack(ld_global_v4(a.post_gamma + v * 16));
 #pragma unroll
-                for (int k = 0; k < V::N; ++k) ss = fmaf(f[k], f[k], ss);
+                for (int k = 0; k < NP; ++k) x.p[k] = __fmul2_rn(x.p[k], w.p[k]);
             }
-            const float r1 = rsqrtf(block_sum(ss, red[0]) * inv_d + a.post_eps);
+            if (FULL || a.gate_kind == FOAK_GATE_CHANNEL) {
+                w.unpack(g);
+#pragma unroll
+                for (int k = 0; k < NP; ++k) x.p[k] = __fmul2_rn(x.p[k], w.p[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < NP; ++k) {
+                h.p[k] = __ffma2_rn(both(q), x.p[k], h.p[k]);
+                s2 = __ffma2_rn(h.p[k], h.p[k], s2);
+            }
+            h.store(hr + v * 16);
+            if (a.gamma) {
+#pragma unroll
+                for (int k = 0; k < NP; k += 2)
+                    reinterpret_cast<float4*>(slots)[k / 2 * nvec + v] =
+                        make_float4(h.p[k].x, h.p[k].y, h.p[k + 1].x, h.p[k + 1].y);
+            }
+        };
+        for (int v0 = threadIdx.x; v0 < nvec; v0 += kFwdBatch * nt) {
+            uint4 x[kFwdBatch], r[kFwdBatch], g[kFwdBatch];
+#pragma unroll
+            for (int j = 0; j < kFwdBatch; ++j) {
+                const int v = v0 + j * nt;
+                if (v >= nvec) break;
+                x[j] = ld_global_v4(xr + v * 16);
+                if (!POST || KEEP) r[j] = ld_global_v4(rr + v * 16);
+                if (!POST && (FULL || a.gate_kind == FOAK_GATE_CHANNEL)) g[j] = ld_global_v4(gr + v * 16);
+            }
+#pragma unroll
+            for (int j = 0; j < kFwdBatch; ++j) {
+                const int v = v0 + j * nt;
+                if (v >= nvec) break;
+                P p;
+                p.unpack(x[j]);
+                if constexpr (POST) {
+#pragma unroll
+                    for (int k = 0; k < NP; ++k) s2 = __ffma2_rn(p.p[k], p.p[k], s2);
+                    slots[v] = x[j];
+                    if constexpr (KEEP) slots[nvec + v] = r[j];
+                } else {
+                    P h;
+                    h.unpack(r[j]);
+                    residual(v, p, h, g[j]);
+                }
+            }
+        }
+        if constexpr (POST) {
+            const float r1 = rsqrtf(block_sum(s2.x + s2.y, red[buffer]) * inv_d + a.post_eps);
             if (threadIdx.x == 0 && a.post_rstd) a.post_rstd[i] = r1;
             q *= r1;
-        }
-        char* h = a.H + i * a.ldh * ES;
-        float ss = 0.f;
-        for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
-            float fx[V::N], fr[V::N], w[V::N];
-            V::load(x + v * 16, fx);
-            V::load(r + v * 16, fr);
-            if (a.post_gamma) {
-                V::load(a.post_gamma + v * 16, w);
-#pragma unroll
-                for (int k = 0; k < V::N; ++k) fx[k] *= w[k];
-            }
-            if (a.gate_kind == FOAK_GATE_CHANNEL || a.gate_kind == FOAK_GATE_FULL) {
-                V::load(g + v * 16, w);
-#pragma unroll
-                for (int k = 0; k < V::N; ++k) fx[k] *= w[k];
-            }
-#pragma unroll
-            for (int k = 0; k < V::N; ++k) {
-                fr[k] = fmaf(q, fx[k], fr[k]);
-                ss = fmaf(fr[k], fr[k], ss);
-                row_h[v * V::N + k] = fr[k];
-            }
-            V::store(h + v * 16, fr);
-        }
-        if (a.gamma) {
-            const float rstd = rsqrtf(block_sum(ss, red[1]) * inv_d + a.eps);
-            if (threadIdx.x == 0 && a.rstd) a.rstd[i] = rstd;
-            char* y = a.Y + i * a.ldy * ES;
-            for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
-                float w[V::N];
-                V::load(a.gamma + v * 16, w);
-#pragma unroll
-                for (int k = 0; k < V::N; ++k) w[k] *= row_h[v * V::N + k] * rstd;
-                V::store(y + v * 16, w);
+            s2 = both(0.f);
+            for (int v = threadIdx.x; v < nvec; v += nt) {
+                uint4 g = make_uint4(0u, 0u, 0u, 0u);
+                if (FULL || a.gate_kind == FOAK_GATE_CHANNEL) g = ld_global_v4(gr + v * 16);
+                P x, h;
+                x.unpack(slots[v]);
+                h.unpack(KEEP ? slots[nvec + v] : ld_global_v4(rr + v * 16));
+                residual(v, x, h, g);
             }
         }
-        __syncthreads();  // red is free again
+        if (!a.gamma) continue;
+        const float rstd = rsqrtf(block_sum(s2.x + s2.y, red[buffer + 1]) * inv_d + a.eps);
+        if (threadIdx.x == 0 && a.rstd) a.rstd[i] = rstd;
+        char* yr = a.Y + i * a.ldy * ES;
+        for (int v = threadIdx.x; v < nvec; v += nt) {
+            P w, h;
+            w.unpack(ld_global_v4(a.gamma + v * 16));
+#pragma unroll
+            for (int k = 0; k < NP; k += 2) {
+                const float4 f = reinterpret_cast<const float4*>(slots)[k / 2 * nvec + v];
+                h.p[k] = make_float2(f.x, f.y);
+                h.p[k + 1] = make_float2(f.z, f.w);
+            }
+#pragma unroll
+            for (int k = 0; k < NP; ++k) w.p[k] = __fmul2_rn(__fmul2_rn(h.p[k], both(rstd)), w.p[k]);
+            w.store(yr + v * 16);
+        }
     }
 }
 
@@ -257,64 +367,6 @@ __global__ void __launch_bounds__(128) resnorm_bwd_cols_kernel(const ResNormBwd 
 //     dh = dH + r gamma dy - k1 h,   E = sum dh w r1 = r1 (S2 - k1 S3),   k2 = r1^2 q E / D
 //     dX = (r1) q gp e dh - (k2 x),   q = s, times the gate of a row
 // Arithmetic on pairs (two-wide FP32).
-constexpr int kVpt = 2;
-constexpr int kBwdThreads = 256;
-constexpr int kSliceVecs = kVpt * kBwdThreads;
-constexpr int kMaxCluster = 8;
-constexpr int kRingSmem = 104 * 1024;  // two CTAs an SM
-
-__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int PENDING>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
-}
-__device__ __forceinline__ void cp_async_wait_all_but(int pending) {
-    if (pending == 1) cp_async_wait<1>();
-    else if (pending == 2) cp_async_wait<2>();
-    else cp_async_wait<3>();
-}
-
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
-
-// A 16-byte vector as element pairs.
-template <int ES>
-struct Pairs {
-    static constexpr int N = 8 / ES;
-    float2 p[N];
-    __device__ __forceinline__ void unpack(const uint4& w) {
-        if constexpr (ES == 2) {
-            p[0] = make_float2(bf16_lo(w.x), bf16_hi(w.x));
-            p[1] = make_float2(bf16_lo(w.y), bf16_hi(w.y));
-            p[2] = make_float2(bf16_lo(w.z), bf16_hi(w.z));
-            p[3] = make_float2(bf16_lo(w.w), bf16_hi(w.w));
-        } else {
-            p[0] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
-            p[1] = make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
-        }
-    }
-    __device__ __forceinline__ void store(char* dst) const {
-        uint4 w;
-        if constexpr (ES == 2)
-            w = make_uint4(pack_bf16x2(p[0].x, p[0].y), pack_bf16x2(p[1].x, p[1].y), pack_bf16x2(p[2].x, p[2].y),
-                           pack_bf16x2(p[3].x, p[3].y));
-        else
-            w = make_uint4(__float_as_uint(p[0].x), __float_as_uint(p[0].y), __float_as_uint(p[1].x),
-                           __float_as_uint(p[1].y));
-        *reinterpret_cast<uint4*>(dst) = w;
-    }
-    __device__ __forceinline__ void fill(float v) {
-#pragma unroll
-        for (int k = 0; k < N; ++k) p[k] = make_float2(v, v);
-    }
-};
-
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
-
 // The warp's sums of four values with six shuffles: lanes 8 v .. 8 v + 7 get value v.
 __device__ __forceinline__ float warp_sum4(float a, float b, float c, float d, int lane) {
     const bool hi = lane & 16, odd = lane & 8;
@@ -327,74 +379,73 @@ __device__ __forceinline__ float warp_sum4(float a, float b, float c, float d, i
 }
 
 struct BwdSplit {
-    int cluster;    // CTAs a row
-    int stages;     // of the ring
-    int slice;      // vectors of a CTA's slice
+    int cluster;  // CTAs a row
+    int stages;   // of the ring
+    int slice;    // vectors of a CTA's slice
+    uint32_t in[5], out[3];  // bytes from row to row of dY, H, dH, X, gate; dR, dX, dgate
 };
 
 // SUMS: S2 and S3 are wanted (the norm after the block, or the gradient of a row's gate).
-template <int ES, bool POST, bool FULL, bool HASX, bool SUMS, int RR>
-__global__ void __launch_bounds__(kBwdThreads, 2)
-    resnorm_bwd_ring_kernel(const ResNormBwd a, const BwdSplit sp, float* __restrict__ part1, float* __restrict__ part2) {
+template <int ES, bool POST, bool FULL, bool HASX, bool SUMS>
+__global__ void __launch_bounds__(kRowThreads, 2)
+    resnorm_bwd_ring_kernel(const __grid_constant__ ResNormBwd a, const BwdSplit sp, float* __restrict__ part1,
+                            float* __restrict__ part2) {
     griddep_launch_dependents();  // programmatic dependent launch: no global access before the wait
     using P = Pairs<ES>;
     constexpr int EPV = 16 / ES, NP = P::N, NS = 3 + HASX + FULL, NSUM = SUMS ? 4 : 1;
-    extern __shared__ uint4 ring[];  // [stages][RR][NS][kVpt][threads]
-    __shared__ float red[2][RR][kMaxCluster * (kBwdThreads / 32)][NSUM];
+    extern __shared__ uint4 ring[];  // [stages][NS][kVpt][threads]
+    __shared__ float red[2][kMaxCluster * (kRowThreads / 32)][NSUM];
     const int v = threadIdx.x, lane = v & 31, warp = v >> 5, nt = blockDim.x, warps = nt >> 5;
     const int C = sp.cluster, rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int64_t cid = C > 1 ? static_cast<int64_t>(blockIdx.x) / C : blockIdx.x, clusters = gridDim.x / C;
     bool act[kVpt];
-    int64_t col[kVpt];  // in elements
+    int off[kVpt];  // bytes from the row's begin
 #pragma unroll
     for (int j = 0; j < kVpt; ++j) {
         const int at = v + j * nt;
-        col[j] = (static_cast<int64_t>(rank) * sp.slice + at) * EPV;
-        act[j] = at < sp.slice && col[j] < a.D;
+        off[j] = (rank * sp.slice + at) * 16;
+        act[j] = at < sp.slice && off[j] < static_cast<int>(a.D) * ES;
     }
-    const int64_t r_begin = a.N * cid / clusters, r_end = a.N * (cid + 1) / clusters;
-    const int64_t nb = (r_end - r_begin + RR - 1) / RR;
+    const int64_t r_begin = a.N * cid / clusters;
+    const int rows = static_cast<int>(a.N * (cid + 1) / clusters - r_begin);
     const float inv_d = 1.f / static_cast<float>(a.D);
-    const int stage_vecs = RR * NS * kVpt * nt;
-    const char* src[NS];
-    int64_t ld[NS];
-    src[0] = a.dY; ld[0] = a.lddy;
-    src[1] = a.dY ? a.H : nullptr; ld[1] = a.ldh;
-    src[2] = a.dH; ld[2] = a.lddh;
-    if constexpr (HASX) {
-        src[3] = a.X; ld[3] = a.ldx;
-    }
-    if constexpr (FULL) {
-        src[NS - 1] = a.gate; ld[NS - 1] = a.ldg;
-    }
-    // an operand that is not there reads as zeros
-    if (!a.dY || !a.dH) {
-        for (int i = v; i < sp.stages * stage_vecs; i += nt) ring[i] = make_uint4(0u, 0u, 0u, 0u);
+    const int plane = kVpt * nt;  // vectors of an operand
+    // An operand that is not there reads as zeros, and so does a vector past the slice's end: the sums below
+    // go through all of a thread's vectors without a branch.
+#pragma unroll
+    for (int j = 0; j < kVpt; ++j) {
+        for (int i = 0; i < sp.stages * NS; ++i) {
+            const int operand = i % NS;
+            if (!act[j] || (operand < 2 && !a.dY) || (operand == 2 && !a.dH))
+                ring[i * plane + j * nt + v] = make_uint4(0u, 0u, 0u, 0u);
+        }
     }
     if (C > 1) cluster_sync();  // nobody writes into a CTA that has not begun
-    else __syncthreads();
     griddep_wait();
-    // batch b's copies into stage s, one group a batch (empty past the last, so that the count stays in step)
-    auto issue = [&](int64_t b, int s) {
-        if (b < nb) {
-            uint4* slot = ring + s * stage_vecs;
+    uint32_t next = static_cast<uint32_t>(r_begin);  // the row to copy
+    const uint32_t last = next + rows;
+    // its copies into stage s, one group a row (empty past the last, so that the count stays in step)
+    auto issue = [&](int s) {
+        if (next < last) {
+            uint4* to = ring + s * (NS * plane) + v;
+            auto copy = [&](int i, const char* base, uint32_t stride) {
+                const char* p = base + static_cast<uint64_t>(next) * stride;
 #pragma unroll
-            for (int q = 0; q < RR; ++q) {
-                const int64_t row = r_begin + b * RR + q;
-                if (row >= r_end) break;
-#pragma unroll
-                for (int i = 0; i < NS; ++i) {
-                    if (!src[i]) continue;
-                    const char* p = src[i] + row * ld[i] * ES;
-#pragma unroll
-                    for (int j = 0; j < kVpt; ++j)
-                        if (act[j]) cp_async16(slot + ((q * NS + i) * kVpt + j) * nt + v, p + col[j] * ES);
-                }
+                for (int j = 0; j < kVpt; ++j)
+                    if (act[j]) cp_async16(to + i * plane + j * nt, p + off[j]);
+            };
+            if (a.dY) {
+                copy(0, a.dY, sp.in[0]);
+                copy(1, a.H, sp.in[1]);
             }
+            if (a.dH) copy(2, a.dH, sp.in[2]);
+            if constexpr (HASX) copy(3, a.X, sp.in[3]);
+            if constexpr (FULL) copy(NS - 1, a.gate, sp.in[4]);
+            ++next;
         }
         cp_async_commit();
     };
-    for (int s = 0; s < sp.stages - 1; ++s) issue(s, s);
+    for (int s = 0; s < sp.stages - 1; ++s) issue(s);
     P gm[kVpt], pe[kVpt], acc1[kVpt], acc2[kVpt];
 #pragma unroll
     for (int j = 0; j < kVpt; ++j) {
@@ -403,153 +454,132 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
         acc1[j].fill(0.f);
         acc2[j].fill(0.f);
         if (!act[j]) continue;
-        if (a.dY) gm[j].unpack(ld_global_v4(a.gamma + col[j] * ES));
-        if constexpr (POST) pe[j].unpack(ld_global_v4(a.post_gamma + col[j] * ES));
+        if (a.dY) gm[j].unpack(ld_global_v4(a.gamma + off[j]));
+        if constexpr (POST) pe[j].unpack(ld_global_v4(a.post_gamma + off[j]));
         if (!FULL && a.gate_kind == FOAK_GATE_CHANNEL) {
             P e;
-            e.unpack(ld_global_v4(a.gate + col[j] * ES));
+            e.unpack(ld_global_v4(a.gate + off[j]));
 #pragma unroll
             for (int k = 0; k < NP; ++k) pe[j].p[k] = __fmul2_rn(pe[j].p[k], e.p[k]);
         }
     }
-    float rn[RR], r1n[RR], qn[RR];  // the next batch's scalars
-    auto scalars = [&](int64_t row0) {
-#pragma unroll
-        for (int q = 0; q < RR; ++q) {
-            const int64_t row = row0 + q;
-            const bool in = row < r_end;
-            rn[q] = in && a.dY ? a.rstd[row] : 0.f;
-            r1n[q] = POST && in ? a.post_rstd[row] : 1.f;
-            qn[q] = in && !FULL ? row_factor<ES>(a, row) : a.scale;
-        }
+    const bool row_gate = !FULL && a.gate_kind == FOAK_GATE_ROW;
+    float r_next = 0.f, r1_next = 1.f, q_next = a.scale;
+    auto scalars = [&](int n) {
+        if (n >= rows) return;
+        const int64_t row = r_begin + n;
+        if (a.dY) r_next = a.rstd[row];
+        if constexpr (POST) r1_next = a.post_rstd[row];
+        if (row_gate) q_next = row_factor<ES>(a, row);
     };
-    scalars(r_begin);
-    const bool weighted = FULL || a.gate_kind == FOAK_GATE_ROW;
-    int par = 0, stage = 0;
-    for (int64_t b = 0; b < nb; ++b, par ^= 1) {
-        // the stage of batch b - 1, read before the last barrier, takes batch b + stages - 1
-        issue(b + sp.stages - 1, stage == 0 ? sp.stages - 1 : stage - 1);
-        const int64_t row0 = r_begin + b * RR;
-        float r[RR], r1[RR], fq[RR];
-#pragma unroll
-        for (int q = 0; q < RR; ++q) {
-            r[q] = rn[q];
-            r1[q] = r1n[q];
-            fq[q] = qn[q];
-        }
-        scalars(row0 + RR);
-        cp_async_wait_all_but(sp.stages - 1);  // this thread's copies of batch b have landed
-        const uint4* slot = ring + stage * stage_vecs;
+    scalars(0);
+    int stage = 0;
+    for (int n = 0; n < rows; ++n) {
+        // the stage of the row before, read before the last barrier, takes the row stages - 1 ahead
+        issue(stage == 0 ? sp.stages - 1 : stage - 1);
+        const float r = r_next, r1 = r1_next, q = q_next;
+        scalars(n + 1);
+        cp_async_wait_all_but(sp.stages - 1);  // this thread's copies of the row have landed
+        const uint4* slot = ring + stage * (NS * plane) + v;
         stage = stage + 1 == sp.stages ? 0 : stage + 1;
+        float2 s1 = both(0.f), s2 = both(0.f), s3 = both(0.f);
+        const float2 rr = both(r);
 #pragma unroll
-        for (int q = 0; q < RR; ++q) {
-            float2 s1 = both(0.f), s2 = both(0.f), s3 = both(0.f);
-            if (row0 + q < r_end) {
+        for (int j = 0; j < kVpt; ++j) {
+            P dy, h, d, w;
+            dy.unpack(slot[j * nt]);
+            h.unpack(slot[plane + j * nt]);
+            if constexpr (SUMS) {
+                d.unpack(slot[2 * plane + j * nt]);
+                w.unpack(slot[3 * plane + j * nt]);
+                if constexpr (FULL) {
+                    P e;
+                    e.unpack(slot[(NS - 1) * plane + j * nt]);
 #pragma unroll
-                for (int j = 0; j < kVpt; ++j) {
-                    if (!act[j]) continue;
-                    const uint4* at = slot + (q * NS * kVpt + j) * nt + v;
-                    P dy, h;
-                    dy.unpack(at[0]);
-                    h.unpack(at[kVpt * nt]);
-                    P d, w;
-                    if constexpr (SUMS) {
-                        d.unpack(at[2 * kVpt * nt]);
-                        w.unpack(at[3 * kVpt * nt]);
-                        if constexpr (FULL) {
-                            P e;
-                            e.unpack(at[(NS - 1) * kVpt * nt]);
-#pragma unroll
-                            for (int k = 0; k < NP; ++k) w.p[k] = __fmul2_rn(w.p[k], e.p[k]);
-                        }
-                    }
-#pragma unroll
-                    for (int k = 0; k < NP; ++k) {
-                        const float2 t = __fmul2_rn(gm[j].p[k], dy.p[k]);
-                        s1 = __ffma2_rn(h.p[k], t, s1);
-                        if constexpr (SUMS) {
-                            w.p[k] = __fmul2_rn(w.p[k], pe[j].p[k]);
-                            s2 = __ffma2_rn(w.p[k], __ffma2_rn(both(r[q]), t, d.p[k]), s2);
-                            s3 = __ffma2_rn(w.p[k], h.p[k], s3);
-                        }
-                    }
+                    for (int k = 0; k < NP; ++k) w.p[k] = __fmul2_rn(w.p[k], e.p[k]);
                 }
             }
-            float* mine = &red[par][q][rank * warps + warp][0];
-            float z;
-            if constexpr (SUMS) z = warp_sum4(s1.x + s1.y, s2.x + s2.y, s3.x + s3.y, 0.f, lane);
-            else z = warp_sum(s1.x + s1.y);
-            if (SUMS ? (lane & 7) == 0 : lane == 0) {
-                if constexpr (SUMS) mine += lane >> 3;
-                if (C == 1) *mine = z;
-                else
-                    for (int c = 0; c < C; ++c) st_cluster_f32(mapa_u32(mine, c), z);
+#pragma unroll
+            for (int k = 0; k < NP; ++k) {
+                const float2 t = __fmul2_rn(gm[j].p[k], dy.p[k]);
+                s1 = __ffma2_rn(h.p[k], t, s1);
+                if constexpr (SUMS) {
+                    w.p[k] = __fmul2_rn(w.p[k], pe[j].p[k]);
+                    s2 = __ffma2_rn(w.p[k], __ffma2_rn(rr, t, d.p[k]), s2);
+                    s3 = __ffma2_rn(w.p[k], h.p[k], s3);
+                }
             }
+        }
+        float* mine = &red[n & 1][rank * warps + warp][0];
+        float z;
+        if constexpr (SUMS) z = warp_sum4(s1.x + s1.y, s2.x + s2.y, s3.x + s3.y, 0.f, lane);
+        else z = warp_sum(s1.x + s1.y);
+        if (SUMS ? (lane & 7) == 0 : lane == 0) {
+            if constexpr (SUMS) mine += lane >> 3;
+            if (C == 1) *mine = z;
+            else
+                for (int c = 0; c < C; ++c) st_cluster_f32(mapa_u32(mine, c), z);
         }
         if (C > 1) cluster_sync();
         else __syncthreads();
+        float S1, S2 = 0.f, S3 = 0.f;
+        const int entries = C * warps;
+        z = 0.f;
+        if constexpr (SUMS) {
+            for (int e = lane & 7; e < entries; e += 8) z += red[n & 1][e][lane >> 3];
 #pragma unroll
-        for (int q = 0; q < RR; ++q) {
-            const int64_t row = row0 + q;
-            float S1, S2 = 0.f, S3 = 0.f, z = 0.f;
-            const int entries = C * warps;
-            if constexpr (SUMS) {
-                for (int e = lane & 7; e < entries; e += 8) z += red[par][q][e][lane >> 3];
+            for (int o = 4; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+            S1 = __shfl_sync(0xffffffffu, z, 0);
+            S2 = __shfl_sync(0xffffffffu, z, 8);
+            S3 = __shfl_sync(0xffffffffu, z, 16);
+        } else {
+            for (int e = lane; e < entries; e += 32) z += red[n & 1][e][0];
+            S1 = warp_sum(z);
+        }
+        const float k1 = r * r * (r * S1 * inv_d);
+        float k2 = 0.f;
+        if constexpr (SUMS) {
+            const float E = r1 * (S2 - k1 * S3);
+            k2 = r1 * r1 * (q * E * inv_d);
+            if (row_gate && a.dgate && rank == 0 && v == 0) reinterpret_cast<float*>(a.dgate)[r_begin + n] = a.scale * E;
+        }
+        // dX = (r1 q) (gp e dh) - k2 x;  the sums over the rows take dh xh, weighted by a row's or an element's s e
+        const uint64_t row = static_cast<uint32_t>(r_begin) + static_cast<uint32_t>(n);
+        const float2 nk1 = both(-k1), nk2 = both(-k2), c = both(r1 * q), xw = both(FULL || row_gate ? r1 * q : r1);
 #pragma unroll
-                for (int off = 4; off > 0; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
-                S1 = __shfl_sync(0xffffffffu, z, 0);
-                S2 = __shfl_sync(0xffffffffu, z, 8);
-                S3 = __shfl_sync(0xffffffffu, z, 16);
-            } else {
-                for (int e = lane; e < entries; e += 32) z += red[par][q][e][0];
-                S1 = warp_sum(z);
-            }
-            if (row >= r_end) continue;
-            const float k1 = r[q] * r[q] * (r[q] * S1 * inv_d);
-            float k2 = 0.f;
-            if constexpr (SUMS) {
-                const float E = r1[q] * (S2 - k1 * S3);
-                k2 = r1[q] * r1[q] * (fq[q] * E * inv_d);
-                if (rank == 0 && v == 0 && a.gate_kind == FOAK_GATE_ROW && a.dgate)
-                    reinterpret_cast<float*>(a.dgate)[row] = a.scale * E;
-            }
-            const float2 rr = both(r[q]), nk1 = both(-k1), nk2 = both(-k2), qq = both(fq[q]), rx = both(r1[q]);
+        for (int j = 0; j < kVpt; ++j) {
+            P dy, h, u, x, e, o;
+            dy.unpack(slot[j * nt]);
+            h.unpack(slot[plane + j * nt]);
+            u.unpack(slot[2 * plane + j * nt]);
+            if constexpr (POST || (HASX && (FULL || !SUMS))) x.unpack(slot[3 * plane + j * nt]);
+            if constexpr (FULL) e.unpack(slot[(NS - 1) * plane + j * nt]);
 #pragma unroll
-            for (int j = 0; j < kVpt; ++j) {
-                if (!act[j]) continue;
-                const uint4* at = slot + (q * NS * kVpt + j) * nt + v;
-                P dy, h, d, x, e, o;
-                dy.unpack(at[0]);
-                h.unpack(at[kVpt * nt]);
-                d.unpack(at[2 * kVpt * nt]);
-                if constexpr (HASX) x.unpack(at[3 * kVpt * nt]);
-                if constexpr (FULL) e.unpack(at[(NS - 1) * kVpt * nt]);
-#pragma unroll
-                for (int k = 0; k < NP; ++k) {
-                    acc1[j].p[k] = __ffma2_rn(dy.p[k], __fmul2_rn(h.p[k], rr), acc1[j].p[k]);
-                    d.p[k] = __ffma2_rn(rr, __fmul2_rn(gm[j].p[k], dy.p[k]), d.p[k]);
-                    d.p[k] = __ffma2_rn(nk1, h.p[k], d.p[k]);
-                    float2 du = __fmul2_rn(qq, d.p[k]);
-                    if constexpr (FULL) {
-                        // the gate's gradient takes the gate's place
-                        float2 dg = __fmul2_rn(du, x.p[k]);
-                        if constexpr (POST) dg = __fmul2_rn(dg, __fmul2_rn(rx, pe[j].p[k]));
-                        du = __fmul2_rn(du, e.p[k]);
-                        e.p[k] = dg;
-                    }
-                    if constexpr (HASX) {
-                        float2 xh = x.p[k];
-                        if constexpr (POST) xh = __fmul2_rn(xh, rx);
-                        acc2[j].p[k] = __ffma2_rn(weighted ? du : d.p[k], xh, acc2[j].p[k]);
-                    }
-                    du = __fmul2_rn(du, pe[j].p[k]);
-                    if constexpr (POST) du = __ffma2_rn(nk2, x.p[k], __fmul2_rn(rx, du));
-                    o.p[k] = du;
+            for (int k = 0; k < NP; ++k) {
+                const float2 rdy = __fmul2_rn(rr, dy.p[k]);
+                acc1[j].p[k] = __ffma2_rn(rdy, h.p[k], acc1[j].p[k]);
+                const float2 d = __ffma2_rn(nk1, h.p[k], __ffma2_rn(gm[j].p[k], rdy, u.p[k]));
+                u.p[k] = d;
+                float2 g = pe[j].p[k];  // gp e
+                if constexpr (FULL) {
+                    const float2 dx = __fmul2_rn(d, __fmul2_rn(x.p[k], xw));  // s dh xh
+                    if constexpr (POST) acc2[j].p[k] = __ffma2_rn(dx, e.p[k], acc2[j].p[k]);
+                    if constexpr (POST) g = __fmul2_rn(g, e.p[k]);
+                    else g = e.p[k];
+                    e.p[k] = POST ? __fmul2_rn(dx, pe[j].p[k]) : dx;  // the gate's gradient
+                } else if constexpr (POST) {
+                    acc2[j].p[k] = __ffma2_rn(d, __fmul2_rn(x.p[k], xw), acc2[j].p[k]);
+                } else if constexpr (HASX && !SUMS) {  // a channel's gate
+                    acc2[j].p[k] = __ffma2_rn(d, x.p[k], acc2[j].p[k]);
                 }
-                d.store(a.dR + (row * a.lddr + col[j]) * ES);
-                if (a.dX) o.store(a.dX + (row * a.lddx + col[j]) * ES);
+                if constexpr (POST) o.p[k] = __ffma2_rn(g, __fmul2_rn(c, d), __fmul2_rn(nk2, x.p[k]));
+                else o.p[k] = __fmul2_rn(g, __fmul2_rn(c, d));
+            }
+            if (act[j]) {
+                u.store(a.dR + row * sp.out[0] + off[j]);
+                if (a.dX) o.store(a.dX + row * sp.out[1] + off[j]);
                 if constexpr (FULL)
-                    if (a.dgate) e.store(a.dgate + (row * a.lddg + col[j]) * ES);
+                    if (a.dgate) e.store(a.dgate + row * sp.out[2] + off[j]);
             }
         }
     }
@@ -557,12 +587,11 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
 #pragma unroll
     for (int j = 0; j < kVpt; ++j) {
         if (!act[j]) continue;
-        float* p1 = part1 + cid * a.D + col[j];
-        float* p2 = part2 + cid * a.D + col[j];
+        const int64_t at = cid * a.D + off[j] / ES;
 #pragma unroll
         for (int k = 0; k < NP; ++k) {
-            if (a.dgamma) *reinterpret_cast<float2*>(p1 + 2 * k) = acc1[j].p[k];
-            if (HASX && part2) *reinterpret_cast<float2*>(p2 + 2 * k) = acc2[j].p[k];
+            if (a.dgamma) *reinterpret_cast<float2*>(part1 + at + 2 * k) = acc1[j].p[k];
+            if (HASX && part2) *reinterpret_cast<float2*>(part2 + at + 2 * k) = acc2[j].p[k];
         }
     }
 }
@@ -629,18 +658,7 @@ cudaError_t allow_smem(K kernel, int bytes, bool (&done)[64]) {
     return e;
 }
 
-template <int ES>
-cudaError_t fwd(const ResNormFwd& a, cudaStream_t s) {
-    static bool done[64] = {};
-    const cudaError_t e = allow_smem(resnorm_fwd_row_kernel<ES>, static_cast<int>(kResNormMaxD) * 4, done);
-    if (e != cudaSuccess) return e;
-    const int64_t nvec = a.D / (16 / ES);
-    const int threads = nvec <= 256 ? static_cast<int>((nvec + 31) / 32 * 32) : nvec <= 1024 ? 256 : 512;
-    const int grid = static_cast<int>(std::min<int64_t>(a.N, static_cast<int64_t>(device_sm_count()) * 8));
-    return launch_dependent(resnorm_fwd_row_kernel<ES>, dim3(grid), dim3(threads), static_cast<size_t>(a.D) * 4, s, a);
-}
-
-// Clusters of the ring kernel that are resident at once; asked once for a device and shape.
+// Clusters of a kernel that are resident at once; asked once for a kernel, device and shape.
 template <typename K>
 cudaError_t resident_clusters(K kernel, int cluster, int threads, size_t smem, int* count) {
     static std::mutex mu;
@@ -655,7 +673,7 @@ cudaError_t resident_clusters(K kernel, int cluster, int threads, size_t smem, i
         *count = at->second;
         return cudaSuccess;
     }
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem);
+    if (smem) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem);
     if (e != cudaSuccess) return e;
     int n = 0;
     if (cluster == 1) {
@@ -679,18 +697,12 @@ cudaError_t resident_clusters(K kernel, int cluster, int threads, size_t smem, i
     return cudaSuccess;
 }
 
-template <int ES, bool POST, bool FULL, bool HASX, bool SUMS, int RR>
-cudaError_t launch_ring(const ResNormBwd& a, const BwdSplit& sp, int threads, float* part1, float* part2, int* groups,
-                        cudaStream_t s) {
-    const auto kernel = resnorm_bwd_ring_kernel<ES, POST, FULL, HASX, SUMS, RR>;
-    const size_t smem = static_cast<size_t>(sp.stages) * RR * (3 + HASX + FULL) * kVpt * threads * 16;
-    int resident = 0;
-    cudaError_t e = resident_clusters(kernel, sp.cluster, threads, smem, &resident);
-    if (e != cudaSuccess) return e;
-    const int64_t G = std::min<int64_t>({(a.N + RR - 1) / RR, resident, resnorm_groups(a.D)});
-    *groups = static_cast<int>(G);
+// The kernel on `clusters` clusters, as a programmatic dependent of the work before it.
+template <typename... KA, typename... A>
+cudaError_t launch_clusters(void (*kernel)(KA...), int64_t clusters, int cluster, int threads, size_t smem, cudaStream_t s,
+                            A&&... args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(G * sp.cluster));
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters * cluster));
     cfg.blockDim = dim3(static_cast<unsigned>(threads));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -698,26 +710,76 @@ cudaError_t launch_ring(const ResNormBwd& a, const BwdSplit& sp, int threads, fl
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(sp.cluster);
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = sp.cluster > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a, sp, part1, part2);
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+
+// How a row of nvec vectors is cut: CTAs, vectors of a CTA, its threads.
+struct Slices {
+    int cluster, slice, threads;
+};
+
+Slices slices_of(int64_t nvec) {
+    Slices c = {1, 0, 0};
+    while ((nvec + c.cluster - 1) / c.cluster > kSliceVecs) c.cluster *= 2;
+    c.slice = static_cast<int>((nvec + c.cluster - 1) / c.cluster);
+    c.threads = ((c.slice + kVpt - 1) / kVpt + 31) / 32 * 32;
+    return c;
+}
+
+template <int ES, bool POST, bool FULL, bool KEEP>
+cudaError_t launch_fwd(const ResNormFwd& a, cudaStream_t s) {
+    static bool done[64] = {};
+    const auto kernel = resnorm_fwd_kernel<ES, POST, FULL, KEEP>;
+    const cudaError_t e = allow_smem(kernel, kFwdSmem, done);
+    if (e != cudaSuccess) return e;
+    const int64_t nvec = a.D / (16 / ES);
+    const int threads = nvec <= 256 ? static_cast<int>((nvec + 31) / 32 * 32) : nvec <= 1024 ? 256 : 512;
+    const int grid = static_cast<int>(std::min<int64_t>(a.N, static_cast<int64_t>(device_sm_count()) * 8));
+    return launch_dependent(kernel, dim3(grid), dim3(threads), static_cast<size_t>(nvec) * 16 * fwd_planes(ES, POST, KEEP),
+                            s, a);
+}
+
+template <int ES>
+cudaError_t fwd(const ResNormFwd& a, cudaStream_t s) {
+    const bool full = a.gate_kind == FOAK_GATE_FULL;
+    if (ES == 4 && a.post_gamma && a.D * 8 > kFwdSmem)
+        return full ? launch_fwd<ES, true, true, ES == 2>(a, s) : launch_fwd<ES, true, false, ES == 2>(a, s);
+    if (a.post_gamma) return full ? launch_fwd<ES, true, true, true>(a, s) : launch_fwd<ES, true, false, true>(a, s);
+    return full ? launch_fwd<ES, false, true, true>(a, s) : launch_fwd<ES, false, false, true>(a, s);
+}
+
+template <int ES, bool POST, bool FULL, bool HASX, bool SUMS>
+cudaError_t launch_ring(const ResNormBwd& a, const BwdSplit& sp, int threads, float* part1, float* part2, int* groups,
+                        cudaStream_t s) {
+    const auto kernel = resnorm_bwd_ring_kernel<ES, POST, FULL, HASX, SUMS>;
+    const size_t smem = static_cast<size_t>(sp.stages) * (3 + HASX + FULL) * kVpt * threads * 16;
+    int resident = 0;
+    cudaError_t e = resident_clusters(kernel, sp.cluster, threads, smem, &resident);
+    if (e != cudaSuccess) return e;
+    const int64_t G = std::min<int64_t>({a.N, resident, resnorm_groups(a.D)});
+    *groups = static_cast<int>(G);
+    return launch_clusters(kernel, G, sp.cluster, threads, smem, s, a, sp, part1, part2);
+}
+
+template <int ES>
+uint32_t bytes_of(int64_t ld) {
+    return static_cast<uint32_t>(ld * ES);
 }
 
 template <int ES, bool POST, bool FULL, bool HASX, bool SUMS>
 cudaError_t ring(const ResNormBwd& a, float* part1, float* part2, int* groups, cudaStream_t s) {
-    const int nvec = static_cast<int>(a.D / (16 / ES));
-    BwdSplit sp = {1, 0, 0};
-    while ((nvec + sp.cluster - 1) / sp.cluster > kSliceVecs) sp.cluster *= 2;
-    sp.slice = (nvec + sp.cluster - 1) / sp.cluster;
-    const int threads = ((sp.slice + kVpt - 1) / kVpt + 31) / 32 * 32;
-    const int row = (3 + HASX + FULL) * kVpt * threads * 16;
-    // two rows a barrier where three batches of them are in the ring
-    const int rr = 6 * row <= kRingSmem ? 2 : 1;
-    sp.stages = std::min(kRingSmem / (rr * row), 4);
-    return rr == 2 ? launch_ring<ES, POST, FULL, HASX, SUMS, 2>(a, sp, threads, part1, part2, groups, s)
-                   : launch_ring<ES, POST, FULL, HASX, SUMS, 1>(a, sp, threads, part1, part2, groups, s);
+    const Slices c = slices_of(a.D / (16 / ES));
+    const int row = (3 + HASX + FULL) * kVpt * c.threads * 16;
+    // as much of the ring as leaves room for 512 threads an SM
+    const int room = std::min(kRingSmem, 2 * kRingSmem / 512 * c.threads);
+    const BwdSplit sp = {c.cluster, std::max(2, std::min(room / row, 4)), c.slice,
+                         {bytes_of<ES>(a.lddy), bytes_of<ES>(a.ldh), bytes_of<ES>(a.lddh), bytes_of<ES>(a.ldx), bytes_of<ES>(a.ldg)},
+                         {bytes_of<ES>(a.lddr), bytes_of<ES>(a.lddx), bytes_of<ES>(a.lddg)}};
+    return launch_ring<ES, POST, FULL, HASX, SUMS>(a, sp, c.threads, part1, part2, groups, s);
 }
 
 template <int ES>
@@ -731,7 +793,9 @@ cudaError_t bwd(const ResNormBwd& a, void* workspace, cudaStream_t s) {
     const int64_t nvec = a.D / (16 / ES);
     int G = static_cast<int>(std::min<int64_t>(std::max<int64_t>(a.N, 1), 128));
     cudaError_t e = cudaSuccess;
-    const bool one_pass = a.N > 0 && nvec <= static_cast<int64_t>(kSliceVecs) * kMaxCluster && (a.X || !full);
+    // rows and row strides of 32 bits
+    const int64_t ld = std::max({a.lddy, a.lddh, a.ldh, a.ldx, a.ldg, a.lddr, a.lddx, a.lddg});
+    const bool one_pass = a.N > 0 && a.N < (1ll << 31) && ld * ES < (1ll << 32) && nvec <= static_cast<int64_t>(kSliceVecs) * kMaxCluster && (a.X || !full);
     if (one_pass) {
         float* p2 = second ? part2 : nullptr;
         if (a.post_gamma)
