@@ -35,10 +35,10 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 }
 
 constexpr int kVpt = 2;
-constexpr int kRowThreads = 256;
-constexpr int kSliceVecs = kVpt * kRowThreads;
+constexpr int kRowThreads = 512;
 constexpr int kMaxCluster = 8;
-constexpr int kRingSmem = 104 * 1024;  // two CTAs an SM
+constexpr int kRingSmem = 208 * 1024;  // of an SM's CTAs together, 512 threads; beside it each CTA's sums
+constexpr int kRingSmemMax = 224 * 1024;
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
@@ -51,7 +51,8 @@ __device__ __forceinline__ void cp_async_wait() {
 __device__ __forceinline__ void cp_async_wait_all_but(int pending) {
     if (pending == 1) cp_async_wait<1>();
     else if (pending == 2) cp_async_wait<2>();
-    else cp_async_wait<3>();
+    else if (pending == 3) cp_async_wait<3>();
+    else cp_async_wait<0>();
 }
 
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
@@ -387,14 +388,13 @@ struct BwdSplit {
 
 // SUMS: S2 and S3 are wanted (the norm after the block, or the gradient of a row's gate).
 template <int ES, bool POST, bool FULL, bool HASX, bool SUMS>
-__global__ void __launch_bounds__(kRowThreads, 2)
+__global__ void __launch_bounds__(kRowThreads, 1)
     resnorm_bwd_ring_kernel(const __grid_constant__ ResNormBwd a, const BwdSplit sp, float* __restrict__ part1,
                             float* __restrict__ part2) {
     griddep_launch_dependents();  // programmatic dependent launch: no global access before the wait
     using P = Pairs<ES>;
     constexpr int EPV = 16 / ES, NP = P::N, NS = 3 + HASX + FULL, NSUM = SUMS ? 4 : 1;
-    extern __shared__ uint4 ring[];  // [stages][NS][kVpt][threads]
-    __shared__ float red[2][kMaxCluster * (kRowThreads / 32)][NSUM];
+    extern __shared__ uint4 ring[];  // [stages][NS][kVpt][threads], then the rows' sums: [2][warps of the cluster][NSUM]
     const int v = threadIdx.x, lane = v & 31, warp = v >> 5, nt = blockDim.x, warps = nt >> 5;
     const int C = sp.cluster, rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int64_t cid = C > 1 ? static_cast<int64_t>(blockIdx.x) / C : blockIdx.x, clusters = gridDim.x / C;
@@ -410,6 +410,7 @@ __global__ void __launch_bounds__(kRowThreads, 2)
     const int rows = static_cast<int>(a.N * (cid + 1) / clusters - r_begin);
     const float inv_d = 1.f / static_cast<float>(a.D);
     const int plane = kVpt * nt;  // vectors of an operand
+    float* red = reinterpret_cast<float*>(ring + sp.stages * NS * plane);
     // An operand that is not there reads as zeros, and so does a vector past the slice's end: the sums below
     // go through all of a thread's vectors without a branch.
 #pragma unroll
@@ -464,24 +465,21 @@ __global__ void __launch_bounds__(kRowThreads, 2)
         }
     }
     const bool row_gate = !FULL && a.gate_kind == FOAK_GATE_ROW;
-    float r_next = 0.f, r1_next = 1.f, q_next = a.scale;
-    auto scalars = [&](int n) {
-        if (n >= rows) return;
-        const int64_t row = r_begin + n;
-        if (a.dY) r_next = a.rstd[row];
-        if constexpr (POST) r1_next = a.post_rstd[row];
-        if (row_gate) q_next = row_factor<ES>(a, row);
+    struct Scalars {
+        float r, r1, q;
     };
-    scalars(0);
-    int stage = 0;
-    for (int n = 0; n < rows; ++n) {
-        // the stage of the row before, read before the last barrier, takes the row stages - 1 ahead
-        issue(stage == 0 ? sp.stages - 1 : stage - 1);
-        const float r = r_next, r1 = r1_next, q = q_next;
-        scalars(n + 1);
-        cp_async_wait_all_but(sp.stages - 1);  // this thread's copies of the row have landed
-        const uint4* slot = ring + stage * (NS * plane) + v;
-        stage = stage + 1 == sp.stages ? 0 : stage + 1;
+    auto scalars = [&](int n) {
+        Scalars c = {0.f, 1.f, a.scale};
+        if (n < rows) {
+            const int64_t row = r_begin + n;
+            if (a.dY) c.r = a.rstd[row];
+            if constexpr (POST) c.r1 = a.post_rstd[row];
+            if (row_gate) c.q = row_factor<ES>(a, row);
+        }
+        return c;
+    };
+    // the warp's part of row n's sums, from the stage that holds it
+    auto sums = [&](const uint4* slot, float r) {
         float2 s1 = both(0.f), s2 = both(0.f), s3 = both(0.f);
         const float2 rr = both(r);
 #pragma unroll
@@ -510,32 +508,61 @@ __global__ void __launch_bounds__(kRowThreads, 2)
                 }
             }
         }
-        float* mine = &red[n & 1][rank * warps + warp][0];
-        float z;
-        if constexpr (SUMS) z = warp_sum4(s1.x + s1.y, s2.x + s2.y, s3.x + s3.y, 0.f, lane);
-        else z = warp_sum(s1.x + s1.y);
+        if constexpr (SUMS) return warp_sum4(s1.x + s1.y, s2.x + s2.y, s3.x + s3.y, 0.f, lane);
+        else return warp_sum(s1.x + s1.y);
+    };
+    const int entries = C * warps;
+    // To every CTA of the row, and arrive at its barrier.  The buffer's last readers, two rows ago, have arrived at
+    // the barrier of the row before since, which this thread has passed.
+    auto post = [&](int n, float z) {
         if (SUMS ? (lane & 7) == 0 : lane == 0) {
-            if constexpr (SUMS) mine += lane >> 3;
+            float* mine = red + ((n & 1) * entries + rank * warps + warp) * NSUM + (SUMS ? lane >> 3 : 0);
             if (C == 1) *mine = z;
             else
                 for (int c = 0; c < C; ++c) st_cluster_f32(mapa_u32(mine, c), z);
         }
-        if (C > 1) cluster_sync();
-        else __syncthreads();
-        float S1, S2 = 0.f, S3 = 0.f;
-        const int entries = C * warps;
-        z = 0.f;
+        cluster_arrive_release();
+    };
+    // The next row's sums are taken between this one's arrival at its barrier and the wait there, where the ring
+    // holds three rows or more; two rows of five operands are taken one after the other.
+    constexpr bool kAhead = !FULL;
+    int stage = 0;
+    const auto slot_of = [&](int s) { return ring + s * (NS * plane) + v; };
+    Scalars now = scalars(0), next_row = scalars(1);
+    if constexpr (kAhead) {
+        cp_async_wait_all_but(sp.stages - 2);  // this thread's copies of the first row have landed
+        if (rows > 0) post(0, sums(slot_of(0), now.r));
+    }
+    for (int n = 0; n < rows; ++n) {
+        const Scalars ahead = scalars(n + 2);
+        const float r = now.r, r1 = now.r1, q = now.q;
+        const uint4* slot = slot_of(stage);
+        const int free_stage = stage == 0 ? sp.stages - 1 : stage - 1;  // the row before's
+        stage = stage + 1 == sp.stages ? 0 : stage + 1;
+        issue(free_stage);
+        cp_async_wait_all_but(sp.stages - (kAhead ? 2 : 1));
+        float z_next = 0.f;
+        if constexpr (kAhead) {
+            if (n + 1 < rows) z_next = sums(slot_of(stage), next_row.r);
+        } else post(n, sums(slot, r));
+        cluster_wait_acquire();
+        float S1, S2 = 0.f, S3 = 0.f, z = 0.f;
+        const float* total = red + (n & 1) * entries * NSUM;
         if constexpr (SUMS) {
-            for (int e = lane & 7; e < entries; e += 8) z += red[n & 1][e][lane >> 3];
+            for (int e = lane & 7; e < entries; e += 8) z += total[e * NSUM + (lane >> 3)];
 #pragma unroll
             for (int o = 4; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
             S1 = __shfl_sync(0xffffffffu, z, 0);
             S2 = __shfl_sync(0xffffffffu, z, 8);
             S3 = __shfl_sync(0xffffffffu, z, 16);
         } else {
-            for (int e = lane; e < entries; e += 32) z += red[n & 1][e][0];
+            for (int e = lane; e < entries; e += 32) z += total[e];
             S1 = warp_sum(z);
         }
+        if (kAhead && n + 1 < rows) post(n + 1, z_next);
+        now = next_row;
+        next_row = ahead;
+        const float2 rr = both(r);
         const float k1 = r * r * (r * S1 * inv_d);
         float k2 = 0.f;
         if constexpr (SUMS) {
@@ -673,7 +700,7 @@ cudaError_t resident_clusters(K kernel, int cluster, int threads, size_t smem, i
         *count = at->second;
         return cudaSuccess;
     }
-    if (smem) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem);
+    if (smem) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmemMax);
     if (e != cudaSuccess) return e;
     int n = 0;
     if (cluster == 1) {
@@ -724,7 +751,7 @@ struct Slices {
 
 Slices slices_of(int64_t nvec) {
     Slices c = {1, 0, 0};
-    while ((nvec + c.cluster - 1) / c.cluster > kSliceVecs) c.cluster *= 2;
+    while ((nvec + c.cluster - 1) / c.cluster > kVpt * kRowThreads) c.cluster *= 2;
     c.slice = static_cast<int>((nvec + c.cluster - 1) / c.cluster);
     c.threads = ((c.slice + kVpt - 1) / kVpt + 31) / 32 * 32;
     return c;
@@ -756,7 +783,8 @@ template <int ES, bool POST, bool FULL, bool HASX, bool SUMS>
 cudaError_t launch_ring(const ResNormBwd& a, const BwdSplit& sp, int threads, float* part1, float* part2, int* groups,
                         cudaStream_t s) {
     const auto kernel = resnorm_bwd_ring_kernel<ES, POST, FULL, HASX, SUMS>;
-    const size_t smem = static_cast<size_t>(sp.stages) * (3 + HASX + FULL) * kVpt * threads * 16;
+    const size_t smem = static_cast<size_t>(sp.stages) * (3 + HASX + FULL) * kVpt * threads * 16 +
+                        static_cast<size_t>(sp.cluster) * (threads / 32) * (SUMS ? 32 : 8);
     int resident = 0;
     cudaError_t e = resident_clusters(kernel, sp.cluster, threads, smem, &resident);
     if (e != cudaSuccess) return e;
@@ -774,9 +802,10 @@ template <int ES, bool POST, bool FULL, bool HASX, bool SUMS>
 cudaError_t ring(const ResNormBwd& a, float* part1, float* part2, int* groups, cudaStream_t s) {
     const Slices c = slices_of(a.D / (16 / ES));
     const int row = (3 + HASX + FULL) * kVpt * c.threads * 16;
-    // as much of the ring as leaves room for 512 threads an SM
-    const int room = std::min(kRingSmem, 2 * kRingSmem / 512 * c.threads);
-    const BwdSplit sp = {c.cluster, std::max(2, std::min(room / row, 4)), c.slice,
+    // as many stages as leave room for 512 threads an SM: four of three operands, three of four, two of five
+    const int stages = kRingSmem / kRowThreads * c.threads / row;
+    static_assert(kRingSmem / kRowThreads / (5 * kVpt * 16) >= 2, "two stages");
+    const BwdSplit sp = {c.cluster, std::min(stages, 4), c.slice,
                          {bytes_of<ES>(a.lddy), bytes_of<ES>(a.ldh), bytes_of<ES>(a.lddh), bytes_of<ES>(a.ldx), bytes_of<ES>(a.ldg)},
                          {bytes_of<ES>(a.lddr), bytes_of<ES>(a.lddx), bytes_of<ES>(a.lddg)}};
     return launch_ring<ES, POST, FULL, HASX, SUMS>(a, sp, c.threads, part1, part2, groups, s);
@@ -795,7 +824,7 @@ cudaError_t bwd(const ResNormBwd& a, void* workspace, cudaStream_t s) {
     cudaError_t e = cudaSuccess;
     // rows and row strides of 32 bits
     const int64_t ld = std::max({a.lddy, a.lddh, a.ldh, a.ldx, a.ldg, a.lddr, a.lddx, a.lddg});
-    const bool one_pass = a.N > 0 && a.N < (1ll << 31) && ld * ES < (1ll << 32) && nvec <= static_cast<int64_t>(kSliceVecs) * kMaxCluster && (a.X || !full);
+    const bool one_pass = a.N > 0 && a.N < (1ll << 31) && ld * ES < (1ll << 32) && nvec <= static_cast<int64_t>(kMaxCluster) * kVpt * kRowThreads && (a.X || !full);
     if (one_pass) {
         float* p2 = second ? part2 : nullptr;
         if (a.post_gamma)
