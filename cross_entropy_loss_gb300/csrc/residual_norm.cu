@@ -95,121 +95,122 @@ __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 
 // ------------------------------------------------------------------ forward
-// A CTA a row.  All of a row's loads go out before its first sum, kFwdBatch vectors of each operand a thread at
-// a time; shared memory keeps what later passes need, in slots that only their own thread touches: X and R
-// as loaded between the two sums of POST, h as floats (in their place) between its sum and y.  With the
-// norm after the block the second sum is of h itself: expanding it into sums of R and X would cancel
-// where the block takes the residual back.
-constexpr int kFwdBatch = 2;
-constexpr int kFwdSmem = static_cast<int>(kResNormMaxD) * 4;
+// A CTA a row at a time, h kept in shared memory as floats (each thread's own vectors) between the sum of
+// its squares and y; with the norm after the block X is read once more, from L1 or L2, for its own sum
+// first.  The second sum is of h itself: expanding it into sums of R and X would cancel where the
+// block takes the residual back.
+//
+// Bound by memory; what counts is how many rows an SM has under way, since a row waits for its loads and at
+// its barriers.  So: 32 registers, two vectors a thread and operand, their loads one vector at a time, and
+// grids of four times what is resident.  Measured (bf16, us): 8192 x 4096 41.0, 98% of the copy rate (one
+// vector a thread 42.6, four 49.3; 64 registers and two vectors at a time 43.6; a ring of cp.async rows
+// 44.8), with both norms 46.3 (ring 49.4, X and R kept in shared memory 53); 16384 x 1024 22.4.  BATCH 2 is
+// for rows of more than 1024 vectors: 2048 x 16384 45.2 against 50.0 (with both norms 58.8 and 56.5).
+constexpr int kFwdThreads = 512;
 
-// Planes of 16 bytes a vector: h as floats, which with POST takes the place of X and R.
-constexpr int fwd_planes(int es, bool post, bool keep) { return es == 2 || (post && keep) ? 2 : 1; }
-
-// KEEP: R stays in shared memory too (POST); rows of more than 16384 floats have no room for it and read it again.
-template <int ES, bool POST, bool FULL, bool KEEP>
-__global__ void __launch_bounds__(512) resnorm_fwd_kernel(const ResNormFwd a) {
+template <int ES, bool POST, bool FULL, int BATCH>
+__global__ void __launch_bounds__(kFwdThreads, BATCH == 1 ? 4 : 2) resnorm_fwd_kernel(const __grid_constant__ ResNormFwd a) {
     griddep_launch_dependents();  // programmatic dependent launch: no global access before the wait
     griddep_wait();
     using P = Pairs<ES>;
     constexpr int EPV = 16 / ES, NP = P::N;
-    extern __shared__ uint4 slots[];  // [planes][vectors]
+    extern __shared__ uint4 kept[];  // h: [4 / ES planes of 16 bytes][vectors]
     __shared__ float red[4][32];
     const int nvec = static_cast<int>(a.D / EPV), nt = blockDim.x;
     const float inv_d = 1.f / static_cast<float>(a.D);
+    const bool channel = !FULL && a.gate_kind == FOAK_GATE_CHANNEL;
+    auto squares = [](const uint4& w, float2 s) {
+        P p;
+        p.unpack(w);
+#pragma unroll
+        for (int k = 0; k < NP; ++k) s = __ffma2_rn(p.p[k], p.p[k], s);
+        return s;
+    };
     int buffer = 0;  // two rows in a row use different ones of `red`
     for (int64_t i = blockIdx.x; i < a.N; i += gridDim.x, buffer ^= 2) {
         const char* xr = a.X + i * a.ldx * ES;
         const char* rr = a.R + i * a.ldr * ES;
-        const char* gr = a.gate_kind == FOAK_GATE_CHANNEL ? a.gate : a.gate + i * a.ldg * ES;
+        const char* gr = channel ? a.gate : a.gate + i * a.ldg * ES;
         char* hr = a.H + i * a.ldh * ES;
         float q = a.scale;
         if (!FULL && a.gate_kind == FOAK_GATE_ROW) q *= Vec16<ES>::load1(gr);
+        if constexpr (POST) {
+            float2 sx = both(0.f);
+            for (int v0 = threadIdx.x; v0 < nvec; v0 += BATCH * nt) {
+                uint4 xw[BATCH];
+#pragma unroll
+                for (int j = 0; j < BATCH; ++j)
+                    if (v0 + j * nt < nvec) xw[j] = ld_global_v4(xr + (v0 + j * nt) * 16);
+#pragma unroll
+                for (int j = 0; j < BATCH; ++j)
+                    if (v0 + j * nt < nvec) sx = squares(xw[j], sx);
+            }
+            const float r1 = rsqrtf(block_sum(sx.x + sx.y, red[buffer]) * inv_d + a.post_eps);
+            if (threadIdx.x == 0 && a.post_rstd) a.post_rstd[i] = r1;
+            q *= r1;
+        }
         float2 s2 = both(0.f);
-        // h of vector v from x and r, its square into s2
-        auto residual = [&](int v, P x, P h, const uint4& g) {
-            P w;
-            if constexpr (POST) {
-                w.unpack(ld_global_v4(a.post_gamma + v * 16));
+        for (int v0 = threadIdx.x; v0 < nvec; v0 += BATCH * nt) {
+            uint4 xw[BATCH], rw[BATCH], gw[BATCH];
 #pragma unroll
-                for (int k = 0; k < NP; ++k) x.p[k] = __fmul2_rn(x.p[k], w.p[k]);
-            }
-            if (FULL || a.gate_kind == FOAK_GATE_CHANNEL) {
-                w.unpack(g);
-#pragma unroll
-                for (int k = 0; k < NP; ++k) x.p[k] = __fmul2_rn(x.p[k], w.p[k]);
-            }
-#pragma unroll
-            for (int k = 0; k < NP; ++k) {
-                h.p[k] = __ffma2_rn(both(q), x.p[k], h.p[k]);
-                s2 = __ffma2_rn(h.p[k], h.p[k], s2);
-            }
-            h.store(hr + v * 16);
-            if (a.gamma) {
-#pragma unroll
-                for (int k = 0; k < NP; k += 2)
-                    reinterpret_cast<float4*>(slots)[k / 2 * nvec + v] =
-                        make_float4(h.p[k].x, h.p[k].y, h.p[k + 1].x, h.p[k + 1].y);
-            }
-        };
-        for (int v0 = threadIdx.x; v0 < nvec; v0 += kFwdBatch * nt) {
-            uint4 x[kFwdBatch], r[kFwdBatch], g[kFwdBatch];
-#pragma unroll
-            for (int j = 0; j < kFwdBatch; ++j) {
+            for (int j = 0; j < BATCH; ++j) {
                 const int v = v0 + j * nt;
                 if (v >= nvec) break;
-                x[j] = ld_global_v4(xr + v * 16);
-                if (!POST || KEEP) r[j] = ld_global_v4(rr + v * 16);
-                if (!POST && (FULL || a.gate_kind == FOAK_GATE_CHANNEL)) g[j] = ld_global_v4(gr + v * 16);
+                xw[j] = ld_global_v4(xr + v * 16);
+                rw[j] = ld_global_v4(rr + v * 16);
+                if (FULL || channel) gw[j] = ld_global_v4(gr + v * 16);
             }
 #pragma unroll
-            for (int j = 0; j < kFwdBatch; ++j) {
+            for (int j = 0; j < BATCH; ++j) {
                 const int v = v0 + j * nt;
                 if (v >= nvec) break;
-                P p;
-                p.unpack(x[j]);
+                P x, h, w;
+                x.unpack(xw[j]);
+                h.unpack(rw[j]);
                 if constexpr (POST) {
+                    w.unpack(ld_global_v4(a.post_gamma + v * 16));
 #pragma unroll
-                    for (int k = 0; k < NP; ++k) s2 = __ffma2_rn(p.p[k], p.p[k], s2);
-                    slots[v] = x[j];
-                    if constexpr (KEEP) slots[nvec + v] = r[j];
-                } else {
-                    P h;
-                    h.unpack(r[j]);
-                    residual(v, p, h, g[j]);
+                    for (int k = 0; k < NP; ++k) x.p[k] = __fmul2_rn(x.p[k], w.p[k]);
+                }
+                if (FULL || channel) {
+                    w.unpack(gw[j]);
+#pragma unroll
+                    for (int k = 0; k < NP; ++k) x.p[k] = __fmul2_rn(x.p[k], w.p[k]);
+                }
+#pragma unroll
+                for (int k = 0; k < NP; ++k) {
+                    h.p[k] = __ffma2_rn(both(q), x.p[k], h.p[k]);
+                    s2 = __ffma2_rn(h.p[k], h.p[k], s2);
+                }
+                h.store(hr + v * 16);
+                if (a.gamma) {
+#pragma unroll
+                    for (int k = 0; k < NP; k += 2)
+                        kept[k / 2 * nvec + v] = make_uint4(__float_as_uint(h.p[k].x), __float_as_uint(h.p[k].y),
+                                                            __float_as_uint(h.p[k + 1].x), __float_as_uint(h.p[k + 1].y));
                 }
             }
         }
-        if constexpr (POST) {
-            const float r1 = rsqrtf(block_sum(s2.x + s2.y, red[buffer]) * inv_d + a.post_eps);
-            if (threadIdx.x == 0 && a.post_rstd) a.post_rstd[i] = r1;
-            q *= r1;
-            s2 = both(0.f);
-            for (int v = threadIdx.x; v < nvec; v += nt) {
-                uint4 g = make_uint4(0u, 0u, 0u, 0u);
-                if (FULL || a.gate_kind == FOAK_GATE_CHANNEL) g = ld_global_v4(gr + v * 16);
-                P x, h;
-                x.unpack(slots[v]);
-                h.unpack(KEEP ? slots[nvec + v] : ld_global_v4(rr + v * 16));
-                residual(v, x, h, g);
-            }
+        float rstd = 0.f;
+        if (a.gamma) {
+            rstd = rsqrtf(block_sum(s2.x + s2.y, red[buffer + 1]) * inv_d + a.eps);
+            if (threadIdx.x == 0 && a.rstd) a.rstd[i] = rstd;
         }
-        if (!a.gamma) continue;
-        const float rstd = rsqrtf(block_sum(s2.x + s2.y, red[buffer + 1]) * inv_d + a.eps);
-        if (threadIdx.x == 0 && a.rstd) a.rstd[i] = rstd;
-        char* yr = a.Y + i * a.ldy * ES;
-        for (int v = threadIdx.x; v < nvec; v += nt) {
-            P w, h;
-            w.unpack(ld_global_v4(a.gamma + v * 16));
+        if (a.gamma) {
+            char* yr = a.Y + i * a.ldy * ES;
+            for (int v = threadIdx.x; v < nvec; v += nt) {
+                P w;
+                w.unpack(ld_global_v4(a.gamma + v * 16));
 #pragma unroll
-            for (int k = 0; k < NP; k += 2) {
-                const float4 f = reinterpret_cast<const float4*>(slots)[k / 2 * nvec + v];
-                h.p[k] = make_float2(f.x, f.y);
-                h.p[k + 1] = make_float2(f.z, f.w);
+                for (int k = 0; k < NP; k += 2) {
+                    const uint4 f = kept[k / 2 * nvec + v];
+                    const float2 lo = make_float2(__uint_as_float(f.x), __uint_as_float(f.y));
+                    const float2 hi = make_float2(__uint_as_float(f.z), __uint_as_float(f.w));
+                    w.p[k] = __fmul2_rn(__fmul2_rn(lo, both(rstd)), w.p[k]);
+                    w.p[k + 1] = __fmul2_rn(__fmul2_rn(hi, both(rstd)), w.p[k + 1]);
+                }
+                w.store(yr + v * 16);
             }
-#pragma unroll
-            for (int k = 0; k < NP; ++k) w.p[k] = __fmul2_rn(__fmul2_rn(h.p[k], both(rstd)), w.p[k]);
-            w.store(yr + v * 16);
         }
     }
 }
@@ -670,21 +671,6 @@ __global__ void __launch_bounds__(kRedCols * kRedSlices)
     }
 }
 
-// Once per device: dynamic shared memory above 48 KB.
-template <typename K>
-cudaError_t allow_smem(K kernel, int bytes, bool (&done)[64]) {
-    static std::mutex mu;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    std::lock_guard<std::mutex> lock(mu);
-    if (done[dev]) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    done[dev] = e == cudaSuccess;
-    return e;
-}
-
 // Clusters of a kernel that are resident at once; asked once for a kernel, device and shape.
 template <typename K>
 cudaError_t resident_clusters(K kernel, int cluster, int threads, size_t smem, int* count) {
@@ -757,26 +743,28 @@ Slices slices_of(int64_t nvec) {
     return c;
 }
 
-template <int ES, bool POST, bool FULL, bool KEEP>
-cudaError_t launch_fwd(const ResNormFwd& a, cudaStream_t s) {
-    static bool done[64] = {};
-    const auto kernel = resnorm_fwd_kernel<ES, POST, FULL, KEEP>;
-    const cudaError_t e = allow_smem(kernel, kFwdSmem, done);
+template <int ES, bool POST, bool FULL, int BATCH>
+cudaError_t launch_fwd(const ResNormFwd& a, int threads, cudaStream_t s) {
+    const auto kernel = resnorm_fwd_kernel<ES, POST, FULL, BATCH>;
+    const size_t smem = a.gamma ? static_cast<size_t>(a.D) * 4 : 0;
+    int resident = 0;
+    const cudaError_t e = resident_clusters(kernel, 1, threads, smem, &resident);
     if (e != cudaSuccess) return e;
-    const int64_t nvec = a.D / (16 / ES);
-    const int threads = nvec <= 256 ? static_cast<int>((nvec + 31) / 32 * 32) : nvec <= 1024 ? 256 : 512;
-    const int grid = static_cast<int>(std::min<int64_t>(a.N, static_cast<int64_t>(device_sm_count()) * 8));
-    return launch_dependent(kernel, dim3(grid), dim3(threads), static_cast<size_t>(nvec) * 16 * fwd_planes(ES, POST, KEEP),
-                            s, a);
+    return launch_clusters(kernel, std::min<int64_t>(a.N, static_cast<int64_t>(resident) * 4), 1, threads, smem, s, a);
 }
 
 template <int ES>
 cudaError_t fwd(const ResNormFwd& a, cudaStream_t s) {
     const bool full = a.gate_kind == FOAK_GATE_FULL;
-    if (ES == 4 && a.post_gamma && a.D * 8 > kFwdSmem)
-        return full ? launch_fwd<ES, true, true, ES == 2>(a, s) : launch_fwd<ES, true, false, ES == 2>(a, s);
-    if (a.post_gamma) return full ? launch_fwd<ES, true, true, true>(a, s) : launch_fwd<ES, true, false, true>(a, s);
-    return full ? launch_fwd<ES, false, true, true>(a, s) : launch_fwd<ES, false, false, true>(a, s);
+    const int64_t nvec = a.D / (16 / ES);
+    // two vectors a thread; one where the rows do not fill the GPU (1 row of 4096 bf16 1.8 us against 2.2, 300 rows 3.1
+    // against 4.4)
+    const int64_t each = a.N <= 2 * static_cast<int64_t>(device_sm_count()) ? 1 : 2;
+    const int threads = static_cast<int>(std::min<int64_t>(((nvec + each - 1) / each + 31) / 32 * 32, kFwdThreads));
+    if (a.post_gamma) return full ? launch_fwd<ES, true, true, 1>(a, threads, s) : launch_fwd<ES, true, false, 1>(a, threads, s);
+    if (nvec > 2 * kFwdThreads)
+        return full ? launch_fwd<ES, false, true, 2>(a, threads, s) : launch_fwd<ES, false, false, 2>(a, threads, s);
+    return full ? launch_fwd<ES, false, true, 1>(a, threads, s) : launch_fwd<ES, false, false, 1>(a, threads, s);
 }
 
 template <int ES, bool POST, bool FULL, bool HASX, bool SUMS>
