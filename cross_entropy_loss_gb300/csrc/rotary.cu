@@ -16,6 +16,9 @@
 // angle is formed once for many heads.  Each element is read and written once.
 #include <algorithm>
 #include <cmath>
+#include <mutex>
+#include <set>
+#include <utility>
 
 #include "common.cuh"
 #include "foak_ce.h"
@@ -44,6 +47,19 @@ struct Piece {
             asm volatile("ld.global.b32 %0, [%1];" : "=r"(w[0]) : "l"(p) : "memory");
         } else {
             asm volatile("ld.global.u16 %0, [%1];" : "=r"(w[0]) : "l"(p) : "memory");
+        }
+    }
+    __device__ __forceinline__ void load_shared(const char* p) {
+        if constexpr (kBytes == 16) {
+            const uint4 v = *reinterpret_cast<const uint4*>(p);
+            w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+        } else if constexpr (kBytes == 8) {
+            const uint2 v = *reinterpret_cast<const uint2*>(p);
+            w[0] = v.x; w[1] = v.y;
+        } else if constexpr (kBytes == 4) {
+            w[0] = *reinterpret_cast<const uint32_t*>(p);
+        } else {
+            w[0] = *reinterpret_cast<const unsigned short*>(p);
         }
     }
     __device__ __forceinline__ void store(char* p) const {
@@ -215,6 +231,12 @@ __device__ __forceinline__ Item item_of(unsigned at, const RotaryArgs& a, const 
     return x;
 }
 
+// a / b of numbers that are not negative, by the 32-bit division where both fit (they nearly always do).
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+    if (static_cast<uint64_t>(a | b) >> 32) return a / b;
+    return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+}
+
 // Where token t of a move goes, in elements; -1: nowhere.
 __device__ __forceinline__ int64_t place_of(const RotaryArgs& a, const HeadMove& mv, int64_t t) {
     if (!a.slots) return t * mv.dst_t;
@@ -224,7 +246,7 @@ __device__ __forceinline__ int64_t place_of(const RotaryArgs& a, const HeadMove&
         return -1;
     }
     if (!mv.paged) return t * mv.dst_t;
-    const int64_t page = slot / a.page_size;
+    const int64_t page = divide(slot, a.page_size);
     return page * mv.dst_page + (slot - page * a.page_size) * mv.dst_t;
 }
 
@@ -240,115 +262,140 @@ struct Passes {
     int blocks[3];
     int turning;       // units of a head that turn
     int freqs;         // r / 2
+    int table_bytes;   // of a warp's shared memory
+    int warp_bytes;
     int64_t t0;        // the first token
 };
 
-// A warp's job is a run of a token's passes, kDepth of them in flight.  Behind the first loads it forms the
-// token's cosines and sines, once for all heads of the job, in its part of shared memory: for W > 1
-// vectors of (two cosines, two sines), those of one unit `turning` vectors apart, so that neighbouring
-// units read neighbouring 16 bytes; for W = 1 a cosine and a sine a unit.  A lane keeps its unit while it
-// goes through the heads, so that a pass is two loads, the rotation and two stores.
-//
-// Bound by memory latency: it is the warps in flight that count.  8192 tokens of 32 + 8 heads x 128
-// bf16: 32.7 us, 5.1 TB/s (a copy of as many bytes 26.2).  At 48 registers (five CTAs an SM) and the
-// table read at each pass; with it in registers (91) 49 us, without the bound (63) 39; each head's angles
-// by its own thread 47.6, by CTAs with a table a CTA 36.2.
-constexpr int kDepth = 2;
 constexpr int kWarpCtas = 5;
-constexpr int kMaxShare = 6;
+constexpr int kMaxShare = 4;
+
+// One piece from global to shared memory, completed by this thread's wait_group (a hardware wait, no spin), or
+// at once where a piece is smaller than the asynchronous copy's four bytes.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const char* src) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+    else if constexpr (BYTES >= 4)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES) : "memory");
+    else *static_cast<unsigned short*>(dst) = *reinterpret_cast<const unsigned short*>(src);
+}
+
+// A warp's job is a run of a token's passes.  The loads of all of them go out at once, to the warp's part of
+// shared memory, each lane its own; behind them the warp forms the token's cosines and sines, once for all
+// heads of the job, beside: for W > 1 vectors of (two cosines, two sines), those of one unit `turning`
+// vectors apart, so that neighbouring units read neighbouring 16 bytes; for W = 1 a cosine and a sine a
+// unit.
+//
+// Bound by memory latency: it is the bytes in flight that count, and shared memory holds more of them than
+// registers would.  8192 tokens of 32 + 8 heads x 128 bf16: 27.4 us, 6.1 TB/s (a copy of as many bytes 26.2); with the
+// loads in registers, two passes ahead, 32.0; each head's angles by its own thread 47.6, by CTAs with a table a
+// CTA 36.2.
 template <int ES, int W, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads, kWarpCtas)
     rotary_warp_kernel(const __grid_constant__ RotaryArgs a, const __grid_constant__ Passes ps) {
     griddep_launch_dependents();  // programmatic dependent launch: no global access before the wait
     griddep_wait();
-    extern __shared__ float4 tables[];
+    constexpr int kBytes = ES * W;
+    using Vec = Piece<ES, W>;
+    extern __shared__ float4 shared[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const unsigned job = blockIdx.x * (kThreads / 32) + warp;
     if (job >= ps.count) return;
     const unsigned token = quotient(job, ps.jobs);
     const int64_t t = ps.t0 + token;
-    unsigned p = (job - token * ps.jobs.d) * ps.share;
-    const unsigned p_end = min(p + ps.share, ps.end[2]);
-    float* cs = reinterpret_cast<float*>(tables) + static_cast<size_t>(warp) * ps.turning * W * 2;
-    bool table = false;
-    while (p < p_end) {
-        const int m = p >= ps.end[1] ? 2 : p >= ps.end[0] ? 1 : 0;
-        const HeadMove& mv = a.move[m];
-        const unsigned at = p - (m == 2 ? ps.end[1] : m == 1 ? ps.end[0] : 0);
-        const unsigned chunk = at / ps.blocks[m], block = at - chunk * ps.blocks[m];
-        const int n = min(min(ps.blocks[m] - block, p_end - p), ps.end[m] - p);  // passes of this chunk
-        p += n;
-        const int units = ps.units[m], heads = ps.lanes_head[m];
-        const int hl = units < 32 ? lane / units : 0, j = static_cast<int>(chunk) * 32 + lane - hl * units;
-        const Unit u = unit_of<W, INTERLEAVED>(j, mv.d, mv.r);
-        const int h = static_cast<int>(block) * heads + hl;
-        // none past the last head, or for a lane without a unit
-        int rounds = hl < heads && j < units ? min(n, (mv.H - h + heads - 1) / heads) : 0;
+    const unsigned p_begin = (job - token * ps.jobs.d) * ps.share, p_end = min(p_begin + ps.share, ps.end[2]);
+    char* mine = reinterpret_cast<char*>(shared) + warp * ps.warp_bytes;
+    float* cs = reinterpret_cast<float*>(mine);
+    char* data = mine + ps.table_bytes + lane * kBytes;  // [pass][two vectors][lanes]
+    // body(move, its number, the lane's unit and its number, first head, heads a pass, passes, first pass of the job)
+    auto segments = [&](auto&& body) {
+        for (unsigned p = p_begin; p < p_end;) {
+            const int m = p >= ps.end[1] ? 2 : p >= ps.end[0] ? 1 : 0;
+            const HeadMove& mv = a.move[m];
+            const unsigned at = p - (m == 2 ? ps.end[1] : m == 1 ? ps.end[0] : 0);
+            const unsigned chunk = at / ps.blocks[m], block = at - chunk * ps.blocks[m];
+            const unsigned n = min(min(ps.blocks[m] - block, p_end - p), ps.end[m] - p);  // passes of this chunk
+            const int units = ps.units[m], heads = ps.lanes_head[m];
+            const int hl = units < 32 ? lane / units : 0, j = static_cast<int>(chunk) * 32 + lane - hl * units;
+            const int h = static_cast<int>(block) * heads + hl;
+            // none past the last head, or for a lane without a unit
+            const int rounds = hl < heads && j < units ? min(static_cast<int>(n), (mv.H - h + heads - 1) / heads) : 0;
+            body(mv, m, unit_of<W, INTERLEAVED>(j, mv.d, mv.r), j, h, heads, rounds, p - p_begin);
+            p += n;
+        }
+    };
+    bool turns = false;
+    unsigned moves = 0;  // of the job
+    segments([&](const HeadMove& mv, int m, const Unit& u, int, int h, int heads, int rounds, unsigned pass) {
+        turns |= mv.r > 0;
+        moves |= 1u << m;
         const char* src = mv.src + (t * mv.src_t + h * mv.src_h + u.at0) * ES;
-        const int64_t src_step = heads * mv.src_h * ES, dst_step = heads * mv.dst_h * ES;
-        const int second = (u.at1 - u.at0) * ES;
-        Piece<ES, W> v[kDepth][2];
-        auto fetch = [&](Piece<ES, W> (&x)[2]) {
-            x[0].load(src);
-            if (u.two) x[1].load(src + second);
-            else x[1] = x[0];
-            src += src_step;
-        };
+        char* to = data + pass * (64 * kBytes);
+        for (int i = 0; i < rounds; ++i) {
+            copy_async<kBytes>(to, src);
+            if (u.two) copy_async<kBytes>(to + 32 * kBytes, src + (u.at1 - u.at0) * ES);
+            src += heads * mv.src_h * ES;
+            to += 64 * kBytes;
+        }
+    });
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    int64_t place[3];
 #pragma unroll
-        for (int q = 0; q < kDepth; ++q)
-            if (q < rounds) fetch(v[q]);
-        const int64_t to = place_of(a, mv, t);
-        if (mv.r && !table) {
-            table = true;
-            const uint64_t pos = static_cast<uint64_t>(a.positions[t]);
+    for (int m = 0; m < 3; ++m) place[m] = moves >> m & 1 ? place_of(a, a.move[m], t) : -1;
+    if (turns) {
+        const uint64_t pos = static_cast<uint64_t>(a.positions[t]);
 #pragma unroll 1
-            for (int f = lane; f < ps.freqs; f += 32) {
-                const int i = f / W, k = f % W;
-                float co, si;
-                turn_cos_sin(pos * a.turns[f], a.factor, a.sign, co, si);
-                float* c = cs + (W == 1 ? 2 * i : (k / 2 * ps.turning + i) * 4 + k % 2);
-                c[0] = co;
-                c[W == 1 ? 1 : 2] = si;
-            }
-            __syncwarp();
+        for (int f = lane; f < ps.freqs; f += 32) {
+            const int i = f / W, k = f % W;
+            float co, si;
+            turn_cos_sin(pos * a.turns[f], a.factor, a.sign, co, si);
+            float* c = cs + (W == 1 ? 2 * i : (k / 2 * ps.turning + i) * 4 + k % 2);
+            c[0] = co;
+            c[W == 1 ? 1 : 2] = si;
         }
-        if (to < 0) rounds = 0;
-        char* dst = mv.dst + (to + h * mv.dst_h + u.at0) * ES;
-        for (int i = 0; i < rounds; i += kDepth) {
-#pragma unroll
-            for (int q = 0; q < kDepth; ++q) {
-                if (i + q >= rounds) break;
-                if (u.freq >= 0) {
-                    float x[W], y[W];
-                    float co[W], si[W];
-                    if constexpr (W == 1) {
-                        const float2 c = *reinterpret_cast<const float2*>(cs + 2 * j);
-                        co[0] = c.x;
-                        si[0] = c.y;
-                    } else {
-                        const float4* at_j = reinterpret_cast<const float4*>(cs) + j;
-#pragma unroll
-                        for (int k = 0; k < W / 2; ++k) {
-                            const float4 c = at_j[k * ps.turning];
-                            co[2 * k] = c.x;
-                            co[2 * k + 1] = c.y;
-                            si[2 * k] = c.z;
-                            si[2 * k + 1] = c.w;
-                        }
-                    }
-                    v[q][0].get(x);
-                    v[q][1].get(y);
-                    rotate<W, INTERLEAVED>(x, y, co, si);
-                    v[q][0].set(x);
-                    v[q][1].set(y);
-                }
-                v[q][0].store(dst);
-                if (u.two) v[q][1].store(dst + second);
-                dst += dst_step;
-                if (i + q + kDepth < rounds) fetch(v[q]);
-            }
-        }
+        __syncwarp();
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    segments([&](const HeadMove& mv, int m, const Unit& u, int j, int h, int heads, int rounds, unsigned pass) {
+        const int64_t to = m == 2 ? place[2] : m == 1 ? place[1] : place[0];
+        if (to < 0) return;
+        char* dst = mv.dst + (to + h * mv.dst_h + u.at0) * ES;
+        const char* from = data + pass * (64 * kBytes);
+        for (int i = 0; i < rounds; ++i) {
+            Vec v, w;
+            v.load_shared(from);
+            if (u.two) w.load_shared(from + 32 * kBytes);
+            else w = v;
+            if (u.freq >= 0) {
+                float x[W], y[W], co[W], si[W];
+                if constexpr (W == 1) {
+                    const float2 c = *reinterpret_cast<const float2*>(cs + 2 * j);
+                    co[0] = c.x;
+                    si[0] = c.y;
+                } else {
+                    const float4* table = reinterpret_cast<const float4*>(cs) + j;
+#pragma unroll
+                    for (int k = 0; k < W / 2; ++k) {
+                        const float4 c = table[k * ps.turning];
+                        co[2 * k] = c.x;
+                        co[2 * k + 1] = c.y;
+                        si[2 * k] = c.z;
+                        si[2 * k + 1] = c.w;
+                    }
+                }
+                v.get(x);
+                w.get(y);
+                rotate<W, INTERLEAVED>(x, y, co, si);
+                v.set(x);
+                w.set(y);
+            }
+            v.store(dst);
+            if (u.two) w.store(dst + (u.at1 - u.at0) * ES);
+            dst += heads * mv.dst_h * ES;
+            from += 64 * kBytes;
+        }
+    });
 }
 
 // The same without shared memory, an item a thread: heads so large that a few tokens' tables do not fit.
@@ -388,7 +435,23 @@ __global__ void __launch_bounds__(kThreads)
     if (x.u.two) v[1].store(dst + x.u.at1 * ES);
 }
 
-constexpr size_t kTableSmem = 48 * 1024;
+constexpr int kTableSmem = 200 * 1024;
+
+// Shared memory above 48 KB, once for a kernel and device.
+template <typename K>
+cudaError_t allow_shared(K kernel) {
+    static std::mutex mu;
+    static std::set<std::pair<int64_t, int>> done;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    if (done.count({reinterpret_cast<int64_t>(kernel), dev})) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTableSmem);
+    if (e == cudaSuccess) done.insert({reinterpret_cast<int64_t>(kernel), dev});
+    return e;
+}
+
 
 template <int ES, int W, bool INTERLEAVED>
 cudaError_t launch_items(const RotaryArgs& a, cudaStream_t s) {
@@ -434,16 +497,20 @@ cudaError_t launch_heads(const RotaryArgs& a, cudaStream_t s) {
         }
         ps.end[m] = end;
     }
-    const size_t smem = static_cast<size_t>(ps.turning) * W * 8 * (kThreads / 32);
-    if (smem > kTableSmem) return launch_items<ES, W, INTERLEAVED>(a, s);
-    // Small calls: a pass a job, for the latency (256 tokens of 48 + 8 + 8 heads 5.9 us, by twos 7.4).  Once the
-    // passes fill the resident warps several times over, up to six a job for the angles (3001 tokens of
-    // 9 passes: 13.5 us by ones, 10.7 by fives).
+    // Small calls: a pass a job, for the latency.  Once the passes fill the resident warps several times over, up to
+    // four a job for the angles (8192 tokens of 10 passes: 27.4 us by four or fewer, by two 32, by one 53).
     const int64_t share = a.T * end / (static_cast<int64_t>(device_sm_count()) * (kWarpCtas * kThreads / 32));
     unsigned jobs = (end + kMaxShare - 1) / kMaxShare;
     if (share < kMaxShare) jobs = share > 1 ? (end + share - 1) / share : end;
     ps.share = (end + jobs - 1) / jobs;
     jobs = (end + ps.share - 1) / ps.share;
+    const int64_t table = (static_cast<int64_t>(ps.turning) * W * 8 + 15) / 16 * 16, bytes = table + ps.share * (64 * ES * W);
+    if (bytes * (kThreads / 32) > kTableSmem) return launch_items<ES, W, INTERLEAVED>(a, s);
+    ps.table_bytes = static_cast<int>(table);
+    ps.warp_bytes = static_cast<int>(bytes);
+    const size_t smem = static_cast<size_t>(bytes) * (kThreads / 32);
+    const cudaError_t allowed = allow_shared(rotary_warp_kernel<ES, W, INTERLEAVED>);
+    if (allowed != cudaSuccess) return allowed;
     ps.jobs = divisor(jobs);
     const int64_t step = std::max<int64_t>(1, static_cast<int64_t>((1u << 30) / jobs));  // jobs of a launch below 2^31
     for (ps.t0 = 0; ps.t0 < a.T; ps.t0 += step) {
@@ -481,8 +548,10 @@ int width_of(int es, const RotaryArgs& a) {
     return w;
 }
 
-// Slots and positions of a step's tokens, a thread a token: the token's sequence is the last one
-// that starts at or before it.
+// Slots and positions of a step's tokens, a thread a token: the token's sequence is the last one that starts at
+// or before it, found by bisection, in shared memory where the starts fit (256 sequences of one token: 8
+// dependent loads of an L2 latency each otherwise).
+constexpr int kSlotStarts = 4096;
 __global__ void __launch_bounds__(kThreads)
     kv_slots_kernel(const int32_t* __restrict__ page_table, int64_t ld_table, int64_t max_pages,
                     const int32_t* __restrict__ cache_lens, const int32_t* __restrict__ seq_starts, int64_t B, int64_t T,
@@ -490,21 +559,30 @@ __global__ void __launch_bounds__(kThreads)
                     int32_t* err) {
     griddep_launch_dependents();  // programmatic dependent launch: no global access before the wait
     griddep_wait();
+    __shared__ int32_t kept[kSlotStarts];
+    const int32_t* starts = seq_starts;
+    if (B < kSlotStarts) {
+        for (int i = threadIdx.x; i <= B; i += kThreads) kept[i] = seq_starts[i];
+        __syncthreads();
+        starts = kept;
+    }
     const int64_t t = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x;
     if (t >= T) return;
     int64_t lo = 0, hi = B + 1;  // starts before lo are <= t, those from hi on are not
     while (lo < hi) {
         const int64_t mid = (lo + hi) / 2;
-        if (seq_starts[mid] <= t) lo = mid + 1;
+        if (starts[mid] <= t) lo = mid + 1;
         else hi = mid;
     }
     int64_t slot = -1, pos = 0;
     if (lo > 0 && lo <= B) {  // behind no start, or before the first: padding
         const int64_t b = lo - 1, len = cache_lens[b];
-        pos = len + (t - seq_starts[b]);
-        const int64_t page = pos / page_size;
-        int64_t id = -1;
-        if (len >= 0 && page < max_pages) id = page_table[b * ld_table + page];
+        pos = len + (t - starts[b]);
+        int64_t id = -1, page = 0;
+        if (len >= 0) {
+            page = divide(pos, page_size);
+            if (page < max_pages) id = page_table[b * ld_table + page];
+        }
         if (id >= 0 && id < num_pages) slot = id * page_size + (pos - page * page_size);
         else {
             pos = 0;
