@@ -117,50 +117,53 @@ __device__ __forceinline__ void turn_cos_sin(uint64_t turn, float c, float sign,
     si = (quarter & 2u) ? -c * sign * b : c * sign * b;
 }
 
-// Where a unit's vectors lie in its head.
+// Where a unit's vectors lie in its head, and whose angles they take.
 struct Unit {
-    int at0, at1;  // elements
-    int freq;      // of the first pair; -1: passes through
-    bool two;      // the second vector is there
-    bool turn1;    // and turns
+    int at0, at1;      // elements
+    int freq0, freq1;  // of the first pair of each vector (half layout and single elements: of both); -1: passes through
+    bool two;          // the second vector is there
 };
+
+// Units of a head that turn: pairs of vectors in the half layout (or of single elements); of interleaved vectors
+// the j-th with the j-th of the second half, so that neighbouring units lie side by side.
+template <int W, bool INTERLEAVED>
+__host__ __device__ __forceinline__ int turning_of(int r) {
+    return INTERLEAVED && W > 1 ? (r / W + 1) / 2 : r / 2 / W;
+}
+
+template <int W, bool INTERLEAVED>
+__host__ __device__ __forceinline__ int units_of(int d, int r) {
+    return turning_of<W, INTERLEAVED>(r) + ((d - r) / W + 1) / 2;
+}
 
 template <int W, bool INTERLEAVED>
 __device__ __forceinline__ Unit unit_of(int j, int d, int r) {
+    const int turning = turning_of<W, INTERLEAVED>(r);
     Unit u;
-    if constexpr (!INTERLEAVED) {
-        const int half = r / 2, turning = half / W;
-        if (j < turning) {
+    if (j < turning) {
+        if constexpr (!INTERLEAVED) {
             u.at0 = j * W;
-            u.at1 = half + j * W;
-            u.freq = j * W;
-            u.two = u.turn1 = true;
-            return u;
+            u.at1 = r / 2 + j * W;
+            u.freq0 = u.freq1 = j * W;
+        } else if constexpr (W == 1) {
+            u.at0 = 2 * j;
+            u.at1 = 2 * j + 1;
+            u.freq0 = u.freq1 = j;
+        } else {
+            u.at0 = j * W;
+            u.at1 = (j + turning) * W;
+            u.freq0 = u.at0 / 2;
+            u.freq1 = u.at1 / 2;
         }
-        j -= turning;
-    } else {
-        const int turning = (r + 2 * W - 1) / (2 * W);
-        if (j < turning) {
-            u.at0 = j * 2 * W;
-            u.at1 = u.at0 + W;
-            u.freq = j * W;
-            u.two = u.turn1 = u.at1 < r;
-            return u;
-        }
-        j -= turning;
+        u.two = u.at1 < r;
+        return u;
     }
-    u.at0 = r + j * 2 * W;
-    u.at1 = u.at0 + W;
-    u.freq = -1;
+    j -= turning;
+    u.at0 = r + j * W;
+    u.at1 = u.at0 + ((d - r) / W + 1) / 2 * W;
+    u.freq0 = u.freq1 = -1;
     u.two = u.at1 < d;
-    u.turn1 = false;
     return u;
-}
-
-template <int W>
-__host__ __device__ __forceinline__ int units_of(int d, int r, bool interleaved) {
-    const int turning = interleaved ? (r + 2 * W - 1) / (2 * W) : r / 2 / W;
-    return turning + (d - r + 2 * W - 1) / (2 * W);
 }
 
 // Division of numbers below 2^31 by one that a launch keeps: multiplied by 2^(31 + b) / d, rounded up,
@@ -211,13 +214,19 @@ struct Items {
     Divisor per_token;
     Divisor units[3];
     unsigned end[2];  // of a token's items of move 0, and of 1
-    unsigned count;   // of the launch
+    Divisor jobs;     // a token's runs of items, a warp each
+    unsigned share;   // items of a job, a multiple of 32
+    unsigned count;   // of the launch: jobs, or items
+    int turning;      // units of a head that turn
     int freqs;        // r / 2
+    int table_bytes;  // of a warp's shared memory
+    int warp_bytes;
     int64_t t0;       // the first token
 };
 
 struct Item {
     unsigned m, h;  // move, head
+    int j;          // unit of the head
     Unit u;
 };
 
@@ -227,7 +236,8 @@ __device__ __forceinline__ Item item_of(unsigned at, const RotaryArgs& a, const 
     x.m = at >= it.end[1] ? 2 : at >= it.end[0] ? 1 : 0;
     at -= x.m == 2 ? it.end[1] : x.m == 1 ? it.end[0] : 0;
     x.h = quotient(at, it.units[x.m]);
-    x.u = unit_of<W, INTERLEAVED>(static_cast<int>(at - x.h * it.units[x.m].d), a.move[x.m].d, a.move[x.m].r);
+    x.j = static_cast<int>(at - x.h * it.units[x.m].d);
+    x.u = unit_of<W, INTERLEAVED>(x.j, a.move[x.m].d, a.move[x.m].r);
     return x;
 }
 
@@ -250,25 +260,8 @@ __device__ __forceinline__ int64_t place_of(const RotaryArgs& a, const HeadMove&
     return page * mv.dst_page + (slot - page * a.page_size) * mv.dst_t;
 }
 
-// A pass is what a warp moves at a time: one unit a lane, of as many heads as 32 lanes hold (or 32
-// units of a head that has more).  A move has chunks x blocks passes a token, blocks of heads fastest.
-struct Passes {
-    Divisor jobs;      // of a token
-    unsigned share;    // passes of a job
-    unsigned count;    // jobs of the launch
-    unsigned end[3];   // of a token's passes of moves 0, 1, 2
-    int units[3];      // of a head
-    int lanes_head[3]; // heads of a pass
-    int blocks[3];
-    int turning;       // units of a head that turn
-    int freqs;         // r / 2
-    int table_bytes;   // of a warp's shared memory
-    int warp_bytes;
-    int64_t t0;        // the first token
-};
-
 constexpr int kWarpCtas = 5;
-constexpr int kMaxShare = 4;
+constexpr int kMaxShare = 4;  // items of a lane (8192 tokens of 40 heads: 27.9 us; three 28.7, six 28.5)
 
 // One piece from global to shared memory, completed by this thread's wait_group (a hardware wait, no spin), or
 // at once where a piece is smaller than the asynchronous copy's four bytes.
@@ -281,19 +274,19 @@ __device__ __forceinline__ void copy_async(void* dst, const char* src) {
     else *static_cast<unsigned short*>(dst) = *reinterpret_cast<const unsigned short*>(src);
 }
 
-// A warp's job is a run of a token's passes.  The loads of all of them go out at once, to the warp's part of
+// A warp's job is a run of a token's items.  The loads of all of them go out at once, to the warp's part of
 // shared memory, each lane its own; behind them the warp forms the token's cosines and sines, once for all
 // heads of the job, beside: for W > 1 vectors of (two cosines, two sines), those of one unit `turning`
 // vectors apart, so that neighbouring units read neighbouring 16 bytes; for W = 1 a cosine and a sine a
 // unit.
 //
 // Bound by memory latency: it is the bytes in flight that count, and shared memory holds more of them than
-// registers would.  8192 tokens of 32 + 8 heads x 128 bf16: 27.4 us, 6.1 TB/s (a copy of as many bytes 26.2); with the
-// loads in registers, two passes ahead, 32.0; each head's angles by its own thread 47.6, by CTAs with a table a
+// registers would.  8192 tokens of 32 + 8 heads x 128 bf16: 27.9 us, 6.0 TB/s (a copy of as many bytes 26.2); with the
+// loads in registers, two rounds ahead, 32.0; each item's angles by its own thread 41.5, by CTAs with a table a
 // CTA 36.2.
 template <int ES, int W, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads, kWarpCtas)
-    rotary_warp_kernel(const __grid_constant__ RotaryArgs a, const __grid_constant__ Passes ps) {
+    rotary_warp_kernel(const __grid_constant__ RotaryArgs a, const __grid_constant__ Items it) {
     griddep_launch_dependents();  // programmatic dependent launch: no global access before the wait
     griddep_wait();
     constexpr int kBytes = ES * W;
@@ -301,104 +294,92 @@ __global__ void __launch_bounds__(kThreads, kWarpCtas)
     extern __shared__ float4 shared[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const unsigned job = blockIdx.x * (kThreads / 32) + warp;
-    if (job >= ps.count) return;
-    const unsigned token = quotient(job, ps.jobs);
-    const int64_t t = ps.t0 + token;
-    const unsigned p_begin = (job - token * ps.jobs.d) * ps.share, p_end = min(p_begin + ps.share, ps.end[2]);
-    char* mine = reinterpret_cast<char*>(shared) + warp * ps.warp_bytes;
+    if (job >= it.count) return;
+    const unsigned token = quotient(job, it.jobs);
+    const int64_t t = it.t0 + token;
+    const unsigned begin = (job - token * it.jobs.d) * it.share, end = min(begin + it.share, it.per_token.d);
+    char* mine = reinterpret_cast<char*>(shared) + warp * it.warp_bytes;
     float* cs = reinterpret_cast<float*>(mine);
-    char* data = mine + ps.table_bytes + lane * kBytes;  // [pass][two vectors][lanes]
-    // body(move, its number, the lane's unit and its number, first head, heads a pass, passes, first pass of the job)
-    auto segments = [&](auto&& body) {
-        for (unsigned p = p_begin; p < p_end;) {
-            const int m = p >= ps.end[1] ? 2 : p >= ps.end[0] ? 1 : 0;
-            const HeadMove& mv = a.move[m];
-            const unsigned at = p - (m == 2 ? ps.end[1] : m == 1 ? ps.end[0] : 0);
-            const unsigned chunk = at / ps.blocks[m], block = at - chunk * ps.blocks[m];
-            const unsigned n = min(min(ps.blocks[m] - block, p_end - p), ps.end[m] - p);  // passes of this chunk
-            const int units = ps.units[m], heads = ps.lanes_head[m];
-            const int hl = units < 32 ? lane / units : 0, j = static_cast<int>(chunk) * 32 + lane - hl * units;
-            const int h = static_cast<int>(block) * heads + hl;
-            // none past the last head, or for a lane without a unit
-            const int rounds = hl < heads && j < units ? min(static_cast<int>(n), (mv.H - h + heads - 1) / heads) : 0;
-            body(mv, m, unit_of<W, INTERLEAVED>(j, mv.d, mv.r), j, h, heads, rounds, p - p_begin);
-            p += n;
-        }
-    };
-    bool turns = false;
-    unsigned moves = 0;  // of the job
-    segments([&](const HeadMove& mv, int m, const Unit& u, int, int h, int heads, int rounds, unsigned pass) {
-        turns |= mv.r > 0;
-        moves |= 1u << m;
-        const char* src = mv.src + (t * mv.src_t + h * mv.src_h + u.at0) * ES;
-        char* to = data + pass * (64 * kBytes);
-        for (int i = 0; i < rounds; ++i) {
-            copy_async<kBytes>(to, src);
-            if (u.two) copy_async<kBytes>(to + 32 * kBytes, src + (u.at1 - u.at0) * ES);
-            src += heads * mv.src_h * ES;
-            to += 64 * kBytes;
-        }
-    });
+    char* data = mine + it.table_bytes + lane * kBytes;  // [round][two vectors][lanes]
+    char* to = data;
+    for (unsigned at = begin + lane; at < end; at += 32) {
+        const Item x = item_of<W, INTERLEAVED>(at, a, it);
+        const HeadMove& mv = a.move[x.m];
+        const char* src = mv.src + (t * mv.src_t + x.h * mv.src_h) * ES;
+        copy_async<kBytes>(to, src + x.u.at0 * ES);
+        if (x.u.two) copy_async<kBytes>(to + 32 * kBytes, src + x.u.at1 * ES);
+        to += 64 * kBytes;
+    }
     asm volatile("cp.async.commit_group;" ::: "memory");
-    int64_t place[3];
-#pragma unroll
-    for (int m = 0; m < 3; ++m) place[m] = moves >> m & 1 ? place_of(a, a.move[m], t) : -1;
-    if (turns) {
+    // the moves that the job has items of
+    int64_t place[3] = {-1, -1, -1};
+    if (begin < it.end[0]) place[0] = place_of(a, a.move[0], t);
+    if (begin < it.end[1] && end > it.end[0]) place[1] = place_of(a, a.move[1], t);
+    if (end > it.end[1]) place[2] = place_of(a, a.move[2], t);
+    if (it.freqs && begin < it.end[1]) {
         const uint64_t pos = static_cast<uint64_t>(a.positions[t]);
 #pragma unroll 1
-        for (int f = lane; f < ps.freqs; f += 32) {
-            const int i = f / W, k = f % W;
+        for (int f = lane; f < it.freqs; f += 32) {
+            // frequency f is number k of unit i
+            int i = f / W, k = f % W;
+            if constexpr (INTERLEAVED && W > 1) {
+                i = f / (W / 2);
+                k = f % (W / 2);
+                if (i >= it.turning) {
+                    i -= it.turning;
+                    k += W / 2;
+                }
+            }
             float co, si;
             turn_cos_sin(pos * a.turns[f], a.factor, a.sign, co, si);
-            float* c = cs + (W == 1 ? 2 * i : (k / 2 * ps.turning + i) * 4 + k % 2);
+            float* c = cs + (W == 1 ? 2 * i : (k / 2 * it.turning + i) * 4 + k % 2);
             c[0] = co;
             c[W == 1 ? 1 : 2] = si;
         }
         __syncwarp();
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-    segments([&](const HeadMove& mv, int m, const Unit& u, int j, int h, int heads, int rounds, unsigned pass) {
-        const int64_t to = m == 2 ? place[2] : m == 1 ? place[1] : place[0];
-        if (to < 0) return;
-        char* dst = mv.dst + (to + h * mv.dst_h + u.at0) * ES;
-        const char* from = data + pass * (64 * kBytes);
-        for (int i = 0; i < rounds; ++i) {
-            Vec v, w;
-            v.load_shared(from);
-            if (u.two) w.load_shared(from + 32 * kBytes);
-            else w = v;
-            if (u.freq >= 0) {
-                float x[W], y[W], co[W], si[W];
-                if constexpr (W == 1) {
-                    const float2 c = *reinterpret_cast<const float2*>(cs + 2 * j);
-                    co[0] = c.x;
-                    si[0] = c.y;
-                } else {
-                    const float4* table = reinterpret_cast<const float4*>(cs) + j;
+    const char* from = data;
+    for (unsigned at = begin + lane; at < end; at += 32, from += 64 * kBytes) {
+        const Item x = item_of<W, INTERLEAVED>(at, a, it);
+        const HeadMove& mv = a.move[x.m];
+        const int64_t p = x.m == 2 ? place[2] : x.m == 1 ? place[1] : place[0];
+        if (p < 0) continue;
+        Vec v, w;
+        v.load_shared(from);
+        if (x.u.two) w.load_shared(from + 32 * kBytes);
+        else w = v;
+        if (x.u.freq0 >= 0) {
+            float e[W], f[W], co[W], si[W];
+            if constexpr (W == 1) {
+                const float2 c = *reinterpret_cast<const float2*>(cs + 2 * x.j);
+                co[0] = c.x;
+                si[0] = c.y;
+            } else {
+                const float4* table = reinterpret_cast<const float4*>(cs) + x.j;
 #pragma unroll
-                    for (int k = 0; k < W / 2; ++k) {
-                        const float4 c = table[k * ps.turning];
-                        co[2 * k] = c.x;
-                        co[2 * k + 1] = c.y;
-                        si[2 * k] = c.z;
-                        si[2 * k + 1] = c.w;
-                    }
+                for (int k = 0; k < W / 2; ++k) {
+                    const float4 c = table[k * it.turning];
+                    co[2 * k] = c.x;
+                    co[2 * k + 1] = c.y;
+                    si[2 * k] = c.z;
+                    si[2 * k + 1] = c.w;
                 }
-                v.get(x);
-                w.get(y);
-                rotate<W, INTERLEAVED>(x, y, co, si);
-                v.set(x);
-                w.set(y);
             }
-            v.store(dst);
-            if (u.two) w.store(dst + (u.at1 - u.at0) * ES);
-            dst += heads * mv.dst_h * ES;
-            from += 64 * kBytes;
+            v.get(e);
+            w.get(f);
+            rotate<W, INTERLEAVED>(e, f, co, si);
+            v.set(e);
+            w.set(f);
         }
-    });
+        char* dst = mv.dst + (p + x.h * mv.dst_h) * ES;
+        v.store(dst + x.u.at0 * ES);
+        if (x.u.two) w.store(dst + x.u.at1 * ES);
+    }
 }
 
-// The same without shared memory, an item a thread: heads so large that a few tokens' tables do not fit.
+// The same without shared memory, an item a thread with its own angles: calls too small to fill the GPU, whose
+// latency this shortens (a token of 32 + 8 heads 1.9 us against 2.6), and heads whose table does not fit.
 template <int ES, int W, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads)
     rotary_kernel(const __grid_constant__ RotaryArgs a, const __grid_constant__ Items it) {
@@ -416,12 +397,13 @@ __global__ void __launch_bounds__(kThreads)
     v[0].load(src + x.u.at0 * ES);
     if (x.u.two) v[1].load(src + x.u.at1 * ES);
     else v[1] = v[0];
-    if (x.u.freq >= 0) {
+    if (x.u.freq0 >= 0) {
         float co[W], si[W], p[W], q[W];
         const uint64_t pos = static_cast<uint64_t>(a.positions[t]);
 #pragma unroll
         for (int k = 0; k < W; ++k) {
-            const int f = min(x.u.freq + k, it.freqs - 1);  // past the end only where there is no second vector
+            int f = x.u.freq0 + k;
+            if (INTERLEAVED && W > 1 && k >= W / 2) f = x.u.two ? x.u.freq1 + k - W / 2 : x.u.freq0;
             turn_cos_sin(pos * a.turns[f], a.factor, a.sign, co[k], si[k]);
         }
         v[0].get(p);
@@ -454,69 +436,46 @@ cudaError_t allow_shared(K kernel) {
 
 
 template <int ES, int W, bool INTERLEAVED>
-cudaError_t launch_items(const RotaryArgs& a, cudaStream_t s) {
+cudaError_t launch_heads(const RotaryArgs& a, cudaStream_t s) {
     Items it = {};
     unsigned end = 0;
     for (int m = 0; m < 3; ++m) {
         const HeadMove& mv = a.move[m];
         it.units[m] = divisor(1);
         if (mv.src) {
-            it.units[m] = divisor(static_cast<unsigned>(units_of<W>(mv.d, mv.r, INTERLEAVED)));
+            it.units[m] = divisor(static_cast<unsigned>(units_of<W, INTERLEAVED>(mv.d, mv.r)));
             end += it.units[m].d * static_cast<unsigned>(mv.H);
-            if (mv.r) it.freqs = mv.r / 2;
+            if (mv.r) {
+                it.freqs = mv.r / 2;
+                it.turning = turning_of<W, INTERLEAVED>(mv.r);
+            }
         }
         if (m < 2) it.end[m] = end;
     }
     it.per_token = divisor(end);
-    const int64_t step = std::max<int64_t>(1, static_cast<int64_t>((1u << 30) / end));  // items of a launch below 2^31
-    for (it.t0 = 0; it.t0 < a.T; it.t0 += step) {
-        it.count = static_cast<unsigned>(std::min(a.T - it.t0, step)) * end;
-        const cudaError_t e = launch_dependent(rotary_kernel<ES, W, INTERLEAVED>, dim3((it.count + kThreads - 1) / kThreads),
-                                               dim3(kThreads), 0, s, a, it);
+    const unsigned rounds = (end + 31) / 32;  // of a warp
+    const unsigned jobs = (rounds + kMaxShare - 1) / kMaxShare;
+    it.share = (rounds + jobs - 1) / jobs * 32;
+    it.jobs = divisor((end + it.share - 1) / it.share);
+    it.table_bytes = static_cast<int>((static_cast<int64_t>(it.turning) * W * 8 + 15) / 16 * 16);
+    it.warp_bytes = it.table_bytes + static_cast<int>(it.share) * (2 * ES * W);
+    const size_t smem = static_cast<size_t>(it.warp_bytes) * (kThreads / 32);
+    // Warps with a table once the rounds fill the GPU several times over, a few times more where an item has four
+    // angles or fewer of its own (32 + 8 heads x 128 bf16: 1024 tokens, 10240 rounds, 7.5 us against 6.5 by items, 2048
+    // 10.1 against 12.0; 8 + 2 heads x 96 fp32: 4096 tokens, 16384 rounds, 8.7 against 6.5, 8192 12.9 against 13.2)
+    const int64_t enough = static_cast<int64_t>(device_sm_count()) * (W == 8 ? 96 : 256);
+    const bool by_warps = smem <= kTableSmem && a.T * rounds >= enough;
+    if (by_warps) {
+        const cudaError_t e = allow_shared(rotary_warp_kernel<ES, W, INTERLEAVED>);
         if (e != cudaSuccess) return e;
     }
-    return cudaSuccess;
-}
-
-template <int ES, int W, bool INTERLEAVED>
-cudaError_t launch_heads(const RotaryArgs& a, cudaStream_t s) {
-    Passes ps = {};
-    unsigned end = 0;
-    for (int m = 0; m < 3; ++m) {
-        const HeadMove& mv = a.move[m];
-        ps.units[m] = ps.lanes_head[m] = ps.blocks[m] = 1;
-        if (mv.src) {
-            ps.units[m] = units_of<W>(mv.d, mv.r, INTERLEAVED);
-            ps.lanes_head[m] = ps.units[m] < 32 ? 32 / ps.units[m] : 1;
-            ps.blocks[m] = (mv.H + ps.lanes_head[m] - 1) / ps.lanes_head[m];
-            end += static_cast<unsigned>((ps.units[m] + 31) / 32) * ps.blocks[m];
-            if (mv.r) {
-                ps.freqs = mv.r / 2;
-                ps.turning = INTERLEAVED ? (mv.r + 2 * W - 1) / (2 * W) : mv.r / 2 / W;
-            }
-        }
-        ps.end[m] = end;
-    }
-    // Small calls: a pass a job, for the latency.  Once the passes fill the resident warps several times over, up to
-    // four a job for the angles (8192 tokens of 10 passes: 27.4 us by four or fewer, by two 32, by one 53).
-    const int64_t share = a.T * end / (static_cast<int64_t>(device_sm_count()) * (kWarpCtas * kThreads / 32));
-    unsigned jobs = (end + kMaxShare - 1) / kMaxShare;
-    if (share < kMaxShare) jobs = share > 1 ? (end + share - 1) / share : end;
-    ps.share = (end + jobs - 1) / jobs;
-    jobs = (end + ps.share - 1) / ps.share;
-    const int64_t table = (static_cast<int64_t>(ps.turning) * W * 8 + 15) / 16 * 16, bytes = table + ps.share * (64 * ES * W);
-    if (bytes * (kThreads / 32) > kTableSmem) return launch_items<ES, W, INTERLEAVED>(a, s);
-    ps.table_bytes = static_cast<int>(table);
-    ps.warp_bytes = static_cast<int>(bytes);
-    const size_t smem = static_cast<size_t>(bytes) * (kThreads / 32);
-    const cudaError_t allowed = allow_shared(rotary_warp_kernel<ES, W, INTERLEAVED>);
-    if (allowed != cudaSuccess) return allowed;
-    ps.jobs = divisor(jobs);
-    const int64_t step = std::max<int64_t>(1, static_cast<int64_t>((1u << 30) / jobs));  // jobs of a launch below 2^31
-    for (ps.t0 = 0; ps.t0 < a.T; ps.t0 += step) {
-        ps.count = static_cast<unsigned>(std::min(a.T - ps.t0, step)) * jobs;
-        const dim3 grid((ps.count + kThreads / 32 - 1) / (kThreads / 32)), block(kThreads);
-        const cudaError_t e = launch_dependent(rotary_warp_kernel<ES, W, INTERLEAVED>, grid, block, smem, s, a, ps);
+    const unsigned each = by_warps ? it.jobs.d : end, per_cta = by_warps ? kThreads / 32 : kThreads;
+    const int64_t step = std::max<int64_t>(1, static_cast<int64_t>((1u << 30) / each));  // a launch's count below 2^31
+    for (it.t0 = 0; it.t0 < a.T; it.t0 += step) {
+        it.count = static_cast<unsigned>(std::min(a.T - it.t0, step)) * each;
+        const dim3 grid((it.count + per_cta - 1) / per_cta), block(kThreads);
+        const cudaError_t e = by_warps ? launch_dependent(rotary_warp_kernel<ES, W, INTERLEAVED>, grid, block, smem, s, a, it)
+                                       : launch_dependent(rotary_kernel<ES, W, INTERLEAVED>, grid, block, 0, s, a, it);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
