@@ -11,12 +11,10 @@
 //
 // Both directions are bound by memory: each operand is read and each result written once.
 #include <algorithm>
-#include <array>
-#include <map>
-#include <mutex>
 
 #include "foak_ce.h"
 #include "internal.h"
+#include "launch_once.h"
 #include "residual_norm.h"
 #include "vec16.cuh"
 
@@ -39,6 +37,7 @@ constexpr int kRowThreads = 512;
 constexpr int kMaxCluster = 8;
 constexpr int kRingSmem = 208 * 1024;  // of an SM's CTAs together, 512 threads; beside it each CTA's sums
 constexpr int kRingSmemMax = 224 * 1024;
+constexpr size_t kSmSmem = 228 * 1024;
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
@@ -671,45 +670,6 @@ __global__ void __launch_bounds__(kRedCols * kRedSlices)
     }
 }
 
-// Clusters of a kernel that are resident at once; asked once for a kernel, device and shape.
-template <typename K>
-cudaError_t resident_clusters(K kernel, int cluster, int threads, size_t smem, int* count) {
-    static std::mutex mu;
-    static std::map<std::array<int64_t, 5>, int> known;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    std::lock_guard<std::mutex> lock(mu);
-    const std::array<int64_t, 5> key = {reinterpret_cast<int64_t>(kernel), dev, cluster, threads, static_cast<int64_t>(smem)};
-    const auto at = known.find(key);
-    if (at != known.end()) {
-        *count = at->second;
-        return cudaSuccess;
-    }
-    if (smem) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmemMax);
-    if (e != cudaSuccess) return e;
-    int n = 0;
-    if (cluster == 1) {
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem);
-        n *= device_sm_count();
-    } else {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(static_cast<unsigned>(cluster));
-        cfg.blockDim = dim3(static_cast<unsigned>(threads));
-        cfg.dynamicSmemBytes = smem;
-        cudaLaunchAttribute attr;
-        attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = static_cast<unsigned>(cluster);
-        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
-        e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
-    }
-    if (e != cudaSuccess) return e;
-    known[key] = *count = std::max(n, 1);
-    return cudaSuccess;
-}
-
 // The kernel on `clusters` clusters, as a programmatic dependent of the work before it.
 template <typename... KA, typename... A>
 cudaError_t launch_clusters(void (*kernel)(KA...), int64_t clusters, int cluster, int threads, size_t smem, cudaStream_t s,
@@ -745,12 +705,18 @@ Slices slices_of(int64_t nvec) {
 
 template <int ES, bool POST, bool FULL, int BATCH>
 cudaError_t launch_fwd(const ResNormFwd& a, int threads, cudaStream_t s) {
+    static SmemOnce limit;
+    static ResidentOnce resident;
     const auto kernel = resnorm_fwd_kernel<ES, POST, FULL, BATCH>;
     const size_t smem = a.gamma ? static_cast<size_t>(a.D) * 4 : 0;
-    int resident = 0;
-    const cudaError_t e = resident_clusters(kernel, 1, threads, smem, &resident);
+    int ctas = 0;
+    cudaError_t e = limit.allow(kernel, static_cast<int>(kResNormMaxD) * 4);
+    if (e == cudaSuccess) e = resident.count(kernel, 1, threads, 0, &ctas);
     if (e != cudaSuccess) return e;
-    return launch_clusters(kernel, std::min<int64_t>(a.N, static_cast<int64_t>(resident) * 4), 1, threads, smem, s, a);
+    // as many as the registers and threads allow, and the rows' shared memory
+    const int64_t room = static_cast<int64_t>(kSmSmem / (smem + 2048)) * device_sm_count();
+    const int64_t grid = std::min<int64_t>(a.N, std::min<int64_t>(ctas, room) * 4);
+    return launch_clusters(kernel, grid, 1, threads, smem, s, a);
 }
 
 template <int ES>
@@ -773,10 +739,13 @@ cudaError_t launch_ring(const ResNormBwd& a, const BwdSplit& sp, int threads, fl
     const auto kernel = resnorm_bwd_ring_kernel<ES, POST, FULL, HASX, SUMS>;
     const size_t smem = static_cast<size_t>(sp.stages) * (3 + HASX + FULL) * kVpt * threads * 16 +
                         static_cast<size_t>(sp.cluster) * (threads / 32) * (SUMS ? 32 : 8);
-    int resident = 0;
-    cudaError_t e = resident_clusters(kernel, sp.cluster, threads, smem, &resident);
+    static SmemOnce limit;
+    static ResidentOnce resident;
+    int clusters = 0;
+    cudaError_t e = limit.allow(kernel, kRingSmemMax);
+    if (e == cudaSuccess) e = resident.count(kernel, sp.cluster, threads, smem, &clusters);
     if (e != cudaSuccess) return e;
-    const int64_t G = std::min<int64_t>({a.N, resident, resnorm_groups(a.D)});
+    const int64_t G = std::min<int64_t>({a.N, clusters, resnorm_groups(a.D)});
     *groups = static_cast<int>(G);
     return launch_clusters(kernel, G, sp.cluster, threads, smem, s, a, sp, part1, part2);
 }

@@ -16,13 +16,11 @@
 // angle is formed once for many heads.  Each element is read and written once.
 #include <algorithm>
 #include <cmath>
-#include <mutex>
-#include <set>
-#include <utility>
 
 #include "common.cuh"
 #include "foak_ce.h"
 #include "internal.h"
+#include "launch_once.h"
 #include "rotary.h"
 
 namespace foak {
@@ -419,22 +417,6 @@ __global__ void __launch_bounds__(kThreads)
 
 constexpr int kTableSmem = 200 * 1024;
 
-// Shared memory above 48 KB, once for a kernel and device.
-template <typename K>
-cudaError_t allow_shared(K kernel) {
-    static std::mutex mu;
-    static std::set<std::pair<int64_t, int>> done;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    std::lock_guard<std::mutex> lock(mu);
-    if (done.count({reinterpret_cast<int64_t>(kernel), dev})) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTableSmem);
-    if (e == cudaSuccess) done.insert({reinterpret_cast<int64_t>(kernel), dev});
-    return e;
-}
-
-
 template <int ES, int W, bool INTERLEAVED>
 cudaError_t launch_heads(const RotaryArgs& a, cudaStream_t s) {
     Items it = {};
@@ -466,7 +448,8 @@ cudaError_t launch_heads(const RotaryArgs& a, cudaStream_t s) {
     const int64_t enough = static_cast<int64_t>(device_sm_count()) * (W == 8 ? 96 : 256);
     const bool by_warps = smem <= kTableSmem && a.T * rounds >= enough;
     if (by_warps) {
-        const cudaError_t e = allow_shared(rotary_warp_kernel<ES, W, INTERLEAVED>);
+        static SmemOnce limit;
+        const cudaError_t e = limit.allow(rotary_warp_kernel<ES, W, INTERLEAVED>, kTableSmem);
         if (e != cudaSuccess) return e;
     }
     const unsigned each = by_warps ? it.jobs.d : end, per_cta = by_warps ? kThreads / 32 : kThreads;
