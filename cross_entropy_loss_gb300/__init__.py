@@ -201,24 +201,27 @@ def _on_stream(call):
     """
     @functools.wraps(call)
     def run(*args, stream=None, **kwargs):
-        if stream is None:
-            return call(*args, **kwargs)
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(stream.cuda_stream)
-        before = torch.cuda.current_stream(stream.device)
-        if before.cuda_stream == stream.cuda_stream:
-            return call(*args, **kwargs)
-        with torch.cuda.stream(stream):
-            out = call(*args, **kwargs)
-        for t in _tensors_of(args) + _tensors_of(kwargs):
-            if t.is_cuda:
-                t.record_stream(stream)
-        for t in _tensors_of(out):
-            if t.is_cuda:
-                t.record_stream(before)
-        return out
+        return call(*args, **kwargs) if stream is None else _run_on(stream, call, args, kwargs)
 
     return run
+
+
+def _run_on(stream, call, args, kwargs):
+    """What :func:`_on_stream` does with a stream that was given."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    before = torch.cuda.current_stream(stream.device)
+    if before.cuda_stream == stream.cuda_stream:
+        return call(*args, **kwargs)
+    with torch.cuda.stream(stream):
+        out = call(*args, **kwargs)
+    for t in _tensors_of(args) + _tensors_of(kwargs):
+        if t.is_cuda:
+            t.record_stream(stream)
+    for t in _tensors_of(out):
+        if t.is_cuda:
+            t.record_stream(before)
+    return out
 
 
 def _logits_args(logits):
@@ -919,7 +922,8 @@ def foak_distill_backward(logits, labels, teacher_ids, teacher_logprobs, stats, 
 
 # --------------------------------------------------------------------- residual norms
 # The calls from here on are often a few microseconds' work on the GPU, so what they check of a
-# tensor they ask once, and devices are compared by number (a CPU tensor's is -1).
+# tensor they ask once, devices are compared by number (a CPU tensor's is -1), and the step that a
+# ``stream`` of the caller's takes (:func:`_on_stream`) stands in the call itself.
 FOAK_GATE_NONE, FOAK_GATE_CHANNEL, FOAK_GATE_ROW, FOAK_GATE_FULL = 0, 1, 2, 3
 FOAK_RESIDUAL_NORM_MAX_D = 32768
 _resnorm_ws: dict = {}
@@ -981,7 +985,6 @@ def _rstd_arg(t, N, di, name):
     return t.data_ptr()
 
 
-@_on_stream
 def foak_residual_norm_forward(X, R, gamma=None, *, gate=None, post_gamma=None, scale: float = 1.0, eps: float = 1e-5,
                                post_eps: float | None = None, H=None, Y=None, want_rstd: bool = True, stream=None):
     """H = R + scale * gate * u with u = X, or the RMSNorm of X by ``post_gamma``; Y = RMSNorm of H by ``gamma``.
@@ -992,6 +995,10 @@ def foak_residual_norm_forward(X, R, gamma=None, *, gate=None, post_gamma=None, 
     ``eps``.  Returns dict(H, Y, rstd, post_rstd); the last two (float32 [N]) are for
     :func:`foak_residual_norm_backward`, None unless ``want_rstd`` and their norm is there.
     """
+    if stream is not None:
+        return _run_on(stream, foak_residual_norm_forward, (X, R, gamma),
+                       dict(gate=gate, post_gamma=post_gamma, scale=scale, eps=eps, post_eps=post_eps, H=H, Y=Y,
+                            want_rstd=want_rstd))
     N, D, ldx = _rows_arg(X, "X")
     shape, dtype, di = X.shape, X.dtype, X.get_device()
     ldr = _row_stride(R, shape, dtype, di, "R")
@@ -1021,7 +1028,6 @@ def foak_residual_norm_forward(X, R, gamma=None, *, gate=None, post_gamma=None, 
     return dict(H=H, Y=Y, rstd=rstd, post_rstd=post)
 
 
-@_on_stream
 def foak_residual_norm_backward(dY, dH, H=None, rstd=None, gamma=None, *, X=None, gate=None, post_gamma=None,
                                 post_rstd=None, scale: float = 1.0, dR=None, dX=None, want_dX: bool = True,
                                 want_dgate: bool = True, want_dgamma: bool = True, workspace_tensor=None, stream=None):
@@ -1034,6 +1040,11 @@ def foak_residual_norm_backward(dY, dH, H=None, rstd=None, gamma=None, *, X=None
     [N, 1], or like a full gate.  Without gate and ``post_gamma`` and with ``scale`` 1, dX is dR,
     the same tensor, unless ``dX`` is given.
     """
+    if stream is not None:
+        return _run_on(stream, foak_residual_norm_backward, (dY, dH, H, rstd, gamma),
+                       dict(X=X, gate=gate, post_gamma=post_gamma, post_rstd=post_rstd, scale=scale, dR=dR, dX=dX,
+                            want_dX=want_dX, want_dgate=want_dgate, want_dgamma=want_dgamma,
+                            workspace_tensor=workspace_tensor))
     like = dH if dY is None else dY
     if like is None:
         raise ValueError("dY or dH must be given")
@@ -1202,7 +1213,6 @@ def _heads_out(x, out, dtype, di, T, name):
     return out, ldt, ldh
 
 
-@_on_stream
 def foak_rotary_apply(plan, positions, q, k=None, *, q_out=None, k_out=None, inverse: bool = False, stream=None):
     """Rotate ``q`` (T x Hq x d) and ``k`` (T x Hk x d) by the angles of ``positions`` (int64 [T]) in one
     launch; with ``inverse`` back by the same angles, which is the gradients' way.
@@ -1210,6 +1220,9 @@ def foak_rotary_apply(plan, positions, q, k=None, *, q_out=None, k_out=None, inv
     Views of any token and head strides (a fused QKV product's parts, heads first or tokens first).
     Returns (q_out, k_out): new tensors unless given; ``q_out=q`` rotates in place.  Either of q and k may be None.
     """
+    if stream is not None:
+        return _run_on(stream, foak_rotary_apply, (plan, positions, q, k),
+                       dict(q_out=q_out, k_out=k_out, inverse=inverse))
     if q is None and k is None:
         raise ValueError("q or k must be given")
     if (q is None and q_out is not None) or (k is None and k_out is not None):
@@ -1250,7 +1263,6 @@ def _err_arg(err, di):
     return err.data_ptr()
 
 
-@_on_stream
 def foak_kv_slots(page_table, cache_lens, seq_starts, T: int, *, page_size: int, num_pages: int, err=None, stream=None):
     """Slots and positions of a serving step's T tokens in a paged cache, for the appends of all its layers.
 
@@ -1261,6 +1273,9 @@ def foak_kv_slots(page_table, cache_lens, seq_starts, T: int, *, page_size: int,
     [0, num_pages) gives slot -1 and sets FOAK_ERRBIT_PAGE_RANGE in ``err``, which is OR-ed into: pass
     a zeroed int32 tensor to keep one for many calls.
     """
+    if stream is not None:
+        return _run_on(stream, foak_kv_slots, (page_table, cache_lens, seq_starts, T),
+                       dict(page_size=page_size, num_pages=num_pages, err=err))
     di = page_table.get_device()
     if di < 0 or page_table.dim() != 2 or cache_lens.dim() != 1 or seq_starts.dim() != 1:
         raise ValueError("page_table (2-D), cache_lens and seq_starts (1-D) must be on a CUDA device")
@@ -1297,7 +1312,6 @@ def _cache_arg(cache, dtype, di, H, d, heads_first, name):
     return pages, places, ld_page, ld_place, ld_head
 
 
-@_on_stream
 def foak_kv_append(k, v, k_cache, v_cache, slots, *, heads_first: bool = False, plan=None, positions=None, q=None,
                    q_out=None, err=None, stream=None):
     """Append a step's keys and values to one layer's paged cache; with ``plan`` the keys are rotated on
@@ -1309,6 +1323,9 @@ def foak_kv_append(k, v, k_cache, v_cache, slots, *, heads_first: bool = False, 
     of ``q_out`` neither.  Returns q_out (a new tensor unless given, None without q).  A slot past the cache
     sets FOAK_ERRBIT_PAGE_RANGE in ``err`` (OR-ed into), if given, and is left out.
     """
+    if stream is not None:
+        return _run_on(stream, foak_kv_append, (k, v, k_cache, v_cache, slots),
+                       dict(heads_first=heads_first, plan=plan, positions=positions, q=q, q_out=q_out, err=err))
     dtype, di, T = _first_heads(k, "k")
     Hk, d, ldk, ldkh = _heads_arg(k, dtype, di, T, "k")
     Hv, dv, ldv, ldvh = _heads_arg(v, dtype, di, T, "v")

@@ -9,7 +9,8 @@
 //     du = s e dh,   dg = s dh u summed over what shares g
 //     dX = du  or  r1 (gp du - xh mean(xh gp du)),   dgp = sum_i du xh
 //
-// Both directions are bound by memory: each operand is read and each result written once.
+// Both directions are bound by memory: each operand is read and each result written once (fp32 sums in
+// a fixed order: results are the same from run to run).
 #include <algorithm>
 
 #include "foak_ce.h"
@@ -214,8 +215,10 @@ __global__ void __launch_bounds__(kFwdThreads, BATCH == 1 ? 4 : 2) resnorm_fwd_k
     }
 }
 
-// What a row's elements need of the row's sums: dh = dH + r gamma dY - k1 H, and with the norm after
-// the block dX = r1 gp du - k2 X.
+// ------------------------------------------------------------------ backward, any rows
+// Sums first, then the columns: for no rows at all, for row strides or counts past 32 bits, and for a full gate
+// whose gradient nobody wants.  What a row's elements need of the row's sums: dh = dH + r gamma dY - k1 H, and with
+// the norm after the block dX = r1 gp du - k2 X.
 struct RowStats {
     float k1, k2;
 };
@@ -358,16 +361,22 @@ __global__ void __launch_bounds__(128) resnorm_bwd_cols_kernel(const ResNormBwd 
 }
 
 // ------------------------------------------------------------------ backward, one pass
-// The rows of up to eight slices of 512 vectors: a cluster of C CTAs takes a range of rows, each CTA a slice
-// of their columns; thread v owns vectors v and v + threads of its slice, so the sums over the rows stay
-// in registers until the CTA's end.  Every thread copies its own vectors of a row's operands into a ring
-// of shared memory, stages - 1 batches of RR rows ahead (cp.async: a hardware wait, no spin), sums
-// what the row needs, meets the others at one barrier a batch and reads its vectors again for the results.
-// The row's sums have r and r1 factored out (w = gp e x, e the gate of a channel or an element):
+// Rows in slices of at most 1024 vectors, a CTA each, those of a row one cluster; a cluster takes a range of
+// rows.  Thread v owns vectors v and v + threads of its slice, so the sums over the rows stay in registers
+// until the end.  Every thread copies its own vectors of a row's operands into a ring of shared
+// memory, stages - 1 rows ahead (cp.async: a hardware wait, no spin), takes its part of what the row needs,
+// meets the others at one barrier a row and reads its vectors again for the results.  The row's sums have r
+// and r1 factored out (w = gp e x, e the gate of a channel or an element; q = s, times the gate of a row):
 //     S1 = sum h gamma dy,   S2 = sum w (dH + r gamma dy),   S3 = sum w h,   k1 = r^3 S1 / D
 //     dh = dH + r gamma dy - k1 h,   E = sum dh w r1 = r1 (S2 - k1 S3),   k2 = r1^2 q E / D
-//     dX = (r1) q gp e dh - (k2 x),   q = s, times the gate of a row
+//     dX = r1 q gp e dh - k2 x
 // Arithmetic on pairs (two-wide FP32).
+//
+// Bound by memory and, in bf16, by how many instructions 16 warps an SM get out (half of the issue slots).  bf16,
+// us: 8192 x 4096 60 (0.84 of the copy rate; the reduce 3.5 of them), both norms and a channel gate 73; 4096 x
+// 8192 58 (256 threads and clusters of two 70); 2048 x 16384 66 (waiting at the barrier for the row's sums, not
+// with the next row's sums in between, 87); 8192 x 4096 reading each operand twice, sums first, 139.  An element's
+// intermediate results kept across the barrier spill: 86 against 71 with both norms.
 // The warp's sums of four values with six shuffles: lanes 8 v .. 8 v + 7 get value v.
 __device__ __forceinline__ float warp_sum4(float a, float b, float c, float d, int lane) {
     const bool hi = lane & 16, odd = lane & 8;
