@@ -212,14 +212,23 @@ struct Items {
     Divisor per_token;
     Divisor units[3];
     unsigned end[2];  // of a token's items of move 0, and of 1
-    Divisor jobs;     // a token's runs of items, a warp each
-    unsigned share;   // items of a job, a multiple of 32
-    unsigned count;   // of the launch: jobs, or items
-    int turning;      // units of a head that turn
-    int freqs;        // r / 2
-    int table_bytes;  // of a warp's shared memory
-    int warp_bytes;
+    unsigned count;   // of the launch
     int64_t t0;       // the first token
+};
+
+// Jobs of warps: a token's are runs of the items of move 0, then of 1 and 2.
+struct Jobs {
+    Divisor per_token;
+    Divisor units[3];
+    unsigned end[3];    // of a token's jobs of each move
+    unsigned share[3];  // items of a job, a multiple of 32
+    unsigned items[3];  // of a token
+    unsigned count;     // of the launch
+    int turning;        // units of a head that turn
+    int freqs;          // r / 2
+    int table_bytes;    // of a warp's shared memory
+    int warp_bytes;
+    int64_t t0;         // the first token
 };
 
 struct Item {
@@ -259,7 +268,7 @@ __device__ __forceinline__ int64_t place_of(const RotaryArgs& a, const HeadMove&
 }
 
 constexpr int kWarpCtas = 5;
-constexpr int kMaxShare = 4;  // items of a lane (8192 tokens of 40 heads: 27.9 us; three 28.7, six 28.5)
+constexpr int kMaxShare = 4;  // items of a lane (8192 tokens of 40 heads: 27.1 us; two 31, six 28)
 
 // One piece from global to shared memory, completed by this thread's wait_group (a hardware wait, no spin), or
 // at once where a piece is smaller than the asynchronous copy's four bytes.
@@ -272,19 +281,19 @@ __device__ __forceinline__ void copy_async(void* dst, const char* src) {
     else *static_cast<unsigned short*>(dst) = *reinterpret_cast<const unsigned short*>(src);
 }
 
-// A warp's job is a run of a token's items.  The loads of all of them go out at once, to the warp's part of
-// shared memory, each lane its own; behind them the warp forms the token's cosines and sines, once for all
-// heads of the job, beside: for W > 1 vectors of (two cosines, two sines), those of one unit `turning`
+// A warp's job is a run of the items of a token's move.  The loads of all of them go out at once, to the warp's
+// part of shared memory, each lane its own; behind them the warp forms the token's cosines and sines, once for
+// all heads of the job, beside: for W > 1 vectors of (two cosines, two sines), those of one unit `turning`
 // vectors apart, so that neighbouring units read neighbouring 16 bytes; for W = 1 a cosine and a sine a
-// unit.
+// unit.  A lane keeps its unit from round to round where the units of a head divide 32.
 //
-// Bound by memory latency: it is the bytes in flight that count, and shared memory holds more of them than
-// registers would.  8192 tokens of 32 + 8 heads x 128 bf16: 27.9 us, 6.0 TB/s (a copy of as many bytes 26.2); with the
-// loads in registers, two rounds ahead, 32.0; each item's angles by its own thread 41.5, by CTAs with a table a
-// CTA 36.2.
+// Bound by memory latency (it is the bytes in flight that count, and shared memory holds more of them than
+// registers would) and by the issue slots.  8192 tokens of 32 + 8 heads x 128 bf16: 27.1 us, 6.2 TB/s (a copy of as
+// many bytes 26.2); with jobs over all moves' items 27.9 (290 instructions a round, now 251), with the loads in
+// registers, two rounds ahead, 32.0; each item's angles by its own thread 41.5, by CTAs with a table a CTA 36.2.
 template <int ES, int W, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads, kWarpCtas)
-    rotary_warp_kernel(const __grid_constant__ RotaryArgs a, const __grid_constant__ Items it) {
+    rotary_warp_kernel(const __grid_constant__ RotaryArgs a, const __grid_constant__ Jobs jb) {
     griddep_launch_dependents();  // programmatic dependent launch: no global access before the wait
     griddep_wait();
     constexpr int kBytes = ES * W;
@@ -292,72 +301,87 @@ __global__ void __launch_bounds__(kThreads, kWarpCtas)
     extern __shared__ float4 shared[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const unsigned job = blockIdx.x * (kThreads / 32) + warp;
-    if (job >= it.count) return;
-    const unsigned token = quotient(job, it.jobs);
-    const int64_t t = it.t0 + token;
-    const unsigned begin = (job - token * it.jobs.d) * it.share, end = min(begin + it.share, it.per_token.d);
-    char* mine = reinterpret_cast<char*>(shared) + warp * it.warp_bytes;
+    if (job >= jb.count) return;
+    const unsigned token = quotient(job, jb.per_token);
+    const int64_t t = jb.t0 + token;
+    unsigned run = job - token * jb.per_token.d;
+    const int m = run >= jb.end[1] ? 2 : run >= jb.end[0] ? 1 : 0;
+    run -= m == 2 ? jb.end[1] : m == 1 ? jb.end[0] : 0;
+    const HeadMove& mv = a.move[m];
+    const unsigned begin = run * jb.share[m], end = min(begin + jb.share[m], jb.items[m]), units = jb.units[m].d;
+    const bool steady = 32 % units == 0;  // a lane's unit is the same in every round
+    const unsigned h_first = quotient(begin + lane, jb.units[m]);
+    const int j_first = static_cast<int>(begin + lane - h_first * units);
+    const Unit u_first = unit_of<W, INTERLEAVED>(j_first, mv.d, mv.r);
+    char* mine = reinterpret_cast<char*>(shared) + warp * jb.warp_bytes;
     float* cs = reinterpret_cast<float*>(mine);
-    char* data = mine + it.table_bytes + lane * kBytes;  // [round][two vectors][lanes]
-    char* to = data;
-    for (unsigned at = begin + lane; at < end; at += 32) {
-        const Item x = item_of<W, INTERLEAVED>(at, a, it);
-        const HeadMove& mv = a.move[x.m];
-        const char* src = mv.src + (t * mv.src_t + x.h * mv.src_h) * ES;
-        copy_async<kBytes>(to, src + x.u.at0 * ES);
-        if (x.u.two) copy_async<kBytes>(to + 32 * kBytes, src + x.u.at1 * ES);
-        to += 64 * kBytes;
-    }
+    char* const data = mine + jb.table_bytes + lane * kBytes;  // [round][two vectors][lanes]
+    // body(unit, its number, head, the lane's place in `data`) for each of the lane's items
+    auto rounds = [&](auto&& body) {
+        Unit u = u_first;
+        int j = j_first;
+        unsigned h = h_first;
+        char* at = data;
+        for (unsigned i = begin + lane; i < end; i += 32, at += 64 * kBytes) {
+            body(u, j, h, at);
+            if (steady) h += 32 / units;
+            else {
+                h = quotient(i + 32, jb.units[m]);
+                j = static_cast<int>(i + 32 - h * units);
+                u = unit_of<W, INTERLEAVED>(j, mv.d, mv.r);
+            }
+        }
+    };
+    const char* src = mv.src + t * mv.src_t * ES;
+    const int64_t src_h = mv.src_h * ES, dst_h = mv.dst_h * ES;
+    rounds([&](const Unit& u, int, unsigned h, char* at) {
+        const char* from = src + h * src_h;
+        copy_async<kBytes>(at, from + u.at0 * ES);
+        if (u.two) copy_async<kBytes>(at + 32 * kBytes, from + u.at1 * ES);
+    });
     asm volatile("cp.async.commit_group;" ::: "memory");
-    // the moves that the job has items of
-    int64_t place[3] = {-1, -1, -1};
-    if (begin < it.end[0]) place[0] = place_of(a, a.move[0], t);
-    if (begin < it.end[1] && end > it.end[0]) place[1] = place_of(a, a.move[1], t);
-    if (end > it.end[1]) place[2] = place_of(a, a.move[2], t);
-    if (it.freqs && begin < it.end[1]) {
+    const int64_t place = place_of(a, mv, t);
+    if (mv.r) {
         const uint64_t pos = static_cast<uint64_t>(a.positions[t]);
 #pragma unroll 1
-        for (int f = lane; f < it.freqs; f += 32) {
+        for (int f = lane; f < jb.freqs; f += 32) {
             // frequency f is number k of unit i
             int i = f / W, k = f % W;
             if constexpr (INTERLEAVED && W > 1) {
                 i = f / (W / 2);
                 k = f % (W / 2);
-                if (i >= it.turning) {
-                    i -= it.turning;
+                if (i >= jb.turning) {
+                    i -= jb.turning;
                     k += W / 2;
                 }
             }
             float co, si;
             turn_cos_sin(pos * a.turns[f], a.factor, a.sign, co, si);
-            float* c = cs + (W == 1 ? 2 * i : (k / 2 * it.turning + i) * 4 + k % 2);
+            float* c = cs + (W == 1 ? 2 * i : (k / 2 * jb.turning + i) * 4 + k % 2);
             c[0] = co;
             c[W == 1 ? 1 : 2] = si;
         }
         __syncwarp();
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-    const char* from = data;
-    for (unsigned at = begin + lane; at < end; at += 32, from += 64 * kBytes) {
-        const Item x = item_of<W, INTERLEAVED>(at, a, it);
-        const HeadMove& mv = a.move[x.m];
-        const int64_t p = x.m == 2 ? place[2] : x.m == 1 ? place[1] : place[0];
-        if (p < 0) continue;
+    if (place < 0) return;
+    char* dst = mv.dst + place * ES;
+    rounds([&](const Unit& u, int j, unsigned h, char* at) {
         Vec v, w;
-        v.load_shared(from);
-        if (x.u.two) w.load_shared(from + 32 * kBytes);
+        v.load_shared(at);
+        if (u.two) w.load_shared(at + 32 * kBytes);
         else w = v;
-        if (x.u.freq0 >= 0) {
+        if (u.freq0 >= 0) {
             float e[W], f[W], co[W], si[W];
             if constexpr (W == 1) {
-                const float2 c = *reinterpret_cast<const float2*>(cs + 2 * x.j);
+                const float2 c = *reinterpret_cast<const float2*>(cs + 2 * j);
                 co[0] = c.x;
                 si[0] = c.y;
             } else {
-                const float4* table = reinterpret_cast<const float4*>(cs) + x.j;
+                const float4* table = reinterpret_cast<const float4*>(cs) + j;
 #pragma unroll
                 for (int k = 0; k < W / 2; ++k) {
-                    const float4 c = table[k * it.turning];
+                    const float4 c = table[k * jb.turning];
                     co[2 * k] = c.x;
                     co[2 * k + 1] = c.y;
                     si[2 * k] = c.z;
@@ -370,10 +394,10 @@ __global__ void __launch_bounds__(kThreads, kWarpCtas)
             v.set(e);
             w.set(f);
         }
-        char* dst = mv.dst + (p + x.h * mv.dst_h) * ES;
-        v.store(dst + x.u.at0 * ES);
-        if (x.u.two) w.store(dst + x.u.at1 * ES);
-    }
+        char* to = dst + h * dst_h;
+        v.store(to + u.at0 * ES);
+        if (u.two) w.store(to + u.at1 * ES);
+    });
 }
 
 // The same without shared memory, an item a thread with its own angles: calls too small to fill the GPU, whose
@@ -420,31 +444,37 @@ constexpr int kTableSmem = 200 * 1024;
 template <int ES, int W, bool INTERLEAVED>
 cudaError_t launch_heads(const RotaryArgs& a, cudaStream_t s) {
     Items it = {};
-    unsigned end = 0;
+    Jobs jb = {};
+    unsigned items = 0, rounds = 0, jobs = 0, most = 0;
     for (int m = 0; m < 3; ++m) {
         const HeadMove& mv = a.move[m];
         it.units[m] = divisor(1);
         if (mv.src) {
             it.units[m] = divisor(static_cast<unsigned>(units_of<W, INTERLEAVED>(mv.d, mv.r)));
-            end += it.units[m].d * static_cast<unsigned>(mv.H);
+            jb.items[m] = it.units[m].d * static_cast<unsigned>(mv.H);
+            items += jb.items[m];
+            const unsigned n = (jb.items[m] + 31) / 32, parts = (n + kMaxShare - 1) / kMaxShare;
+            jb.share[m] = (n + parts - 1) / parts * 32;
+            jobs += (jb.items[m] + jb.share[m] - 1) / jb.share[m];
+            rounds += n;
+            most = std::max(most, jb.share[m]);
             if (mv.r) {
-                it.freqs = mv.r / 2;
-                it.turning = turning_of<W, INTERLEAVED>(mv.r);
+                jb.freqs = mv.r / 2;
+                jb.turning = turning_of<W, INTERLEAVED>(mv.r);
             }
         }
-        if (m < 2) it.end[m] = end;
+        if (m < 2) it.end[m] = items;
+        jb.end[m] = jobs;
+        jb.units[m] = it.units[m];
     }
-    it.per_token = divisor(end);
-    const unsigned rounds = (end + 31) / 32;  // of a warp
-    const unsigned jobs = (rounds + kMaxShare - 1) / kMaxShare;
-    it.share = (rounds + jobs - 1) / jobs * 32;
-    it.jobs = divisor((end + it.share - 1) / it.share);
-    it.table_bytes = static_cast<int>((static_cast<int64_t>(it.turning) * W * 8 + 15) / 16 * 16);
-    it.warp_bytes = it.table_bytes + static_cast<int>(it.share) * (2 * ES * W);
-    const size_t smem = static_cast<size_t>(it.warp_bytes) * (kThreads / 32);
+    it.per_token = divisor(items);
+    jb.per_token = divisor(jobs);
+    jb.table_bytes = static_cast<int>((static_cast<int64_t>(jb.turning) * W * 8 + 15) / 16 * 16);
+    jb.warp_bytes = jb.table_bytes + static_cast<int>(most) * (2 * ES * W);
+    const size_t smem = static_cast<size_t>(jb.warp_bytes) * (kThreads / 32);
     // Warps with a table once the rounds fill the GPU several times over, a few times more where an item has four
     // angles or fewer of its own (32 + 8 heads x 128 bf16: 1024 tokens, 10240 rounds, 7.5 us against 6.5 by items, 2048
-    // 10.1 against 12.0; 8 + 2 heads x 96 fp32: 4096 tokens, 16384 rounds, 8.7 against 6.5, 8192 12.9 against 13.2)
+    // 9.3 against 12.0; 8 + 2 heads x 96 fp32: 4096 tokens, 16384 rounds, 8.7 against 6.5, 8192 12.9 against 13.2)
     const int64_t enough = static_cast<int64_t>(device_sm_count()) * (W == 8 ? 96 : 256);
     const bool by_warps = smem <= kTableSmem && a.T * rounds >= enough;
     if (by_warps) {
@@ -452,12 +482,13 @@ cudaError_t launch_heads(const RotaryArgs& a, cudaStream_t s) {
         const cudaError_t e = limit.allow(rotary_warp_kernel<ES, W, INTERLEAVED>, kTableSmem);
         if (e != cudaSuccess) return e;
     }
-    const unsigned each = by_warps ? it.jobs.d : end, per_cta = by_warps ? kThreads / 32 : kThreads;
+    const unsigned each = by_warps ? jobs : items, per_cta = by_warps ? kThreads / 32 : kThreads;
     const int64_t step = std::max<int64_t>(1, static_cast<int64_t>((1u << 30) / each));  // a launch's count below 2^31
-    for (it.t0 = 0; it.t0 < a.T; it.t0 += step) {
-        it.count = static_cast<unsigned>(std::min(a.T - it.t0, step)) * each;
+    for (int64_t t0 = 0; t0 < a.T; t0 += step) {
+        it.t0 = jb.t0 = t0;
+        it.count = jb.count = static_cast<unsigned>(std::min(a.T - t0, step)) * each;
         const dim3 grid((it.count + per_cta - 1) / per_cta), block(kThreads);
-        const cudaError_t e = by_warps ? launch_dependent(rotary_warp_kernel<ES, W, INTERLEAVED>, grid, block, smem, s, a, it)
+        const cudaError_t e = by_warps ? launch_dependent(rotary_warp_kernel<ES, W, INTERLEAVED>, grid, block, smem, s, a, jb)
                                        : launch_dependent(rotary_kernel<ES, W, INTERLEAVED>, grid, block, 0, s, a, it);
         if (e != cudaSuccess) return e;
     }

@@ -391,7 +391,8 @@ size_t foak_residual_norm_workspace_size(int64_t N, int64_t D);
  *   dgate (device)      float[D] (channel), float[N] (row) or N x D in dtype with row stride lddg
  *                       (full), or NULL
  * The sums over the rows have a fixed order: results are the same from run to run.  Sizes and
- * alignment as in the forward.
+ * alignment as in the forward.  An output may be one of the N x D inputs (same stride), no two
+ * outputs the same.
  */
 foak_status foak_residual_norm_backward(const void* dY, int64_t lddy, const void* dH, int64_t lddh, const void* H,
                                         int64_t ldh, const void* X, int64_t ldx, int32_t dtype, int64_t N, int64_t D,
@@ -439,7 +440,8 @@ foak_status foak_rotary_turns(const double* inv_freq, int64_t n, uint64_t* turns
  *                       rotate in place; otherwise they overlap nothing; heads d elements or more apart
  *   positions (device)  int64[T], any value (the angle is exact to 2^-53 positions[t] turns)
  *   turns (device)      uint64[rotary_dim / 2] of foak_rotary_turns
- * d >= rotary_dim >= 2, rotary_dim even; H * d <= 2^28.
+ * d >= rotary_dim >= 2, rotary_dim even; H * d <= 2^28.  Every element is computed the same way in every
+ * call: it depends on its own pair, position and frequency alone.
  */
 foak_status foak_rotary_apply(const void* Q, int64_t ldq, int64_t ldqh, void* Qo, int64_t ldqo, int64_t ldqoh, int64_t Hq,
                               const void* K, int64_t ldk, int64_t ldkh, void* Ko, int64_t ldko, int64_t ldkoh, int64_t Hk,
