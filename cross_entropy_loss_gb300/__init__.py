@@ -1320,8 +1320,9 @@ def foak_kv_append(k, v, k_cache, v_cache, slots, *, heads_first: bool = False, 
     k (T x Hk x d) and v (T x Hk x dv) are views of any token and head strides; the caches are
     (pages, page_size, Hk, d), or (pages, Hk, page_size, d) with ``heads_first``, views too.  ``slots`` and
     ``positions`` are :func:`foak_kv_slots`'s; of a token with a negative slot nothing is written, q's row
-    of ``q_out`` neither.  Returns q_out (a new tensor unless given, None without q).  A slot past the cache
-    sets FOAK_ERRBIT_PAGE_RANGE in ``err`` (OR-ed into), if given, and is left out.
+    of ``q_out`` neither (in a new tensor it is undefined).  Returns q_out (a new tensor unless given, None
+    without q).  A slot past the cache sets FOAK_ERRBIT_PAGE_RANGE in ``err`` (OR-ed into), if given, and is
+    left out.
     """
     if stream is not None:
         return _run_on(stream, foak_kv_append, (k, v, k_cache, v_cache, slots),
