@@ -632,39 +632,41 @@ __global__ void __launch_bounds__(kRowThreads, 1)
     }
 }
 
-// The sums over the groups in a fixed order: 32 slices of 32 columns a CTA, each adding every 32nd group,
-// then the slices in order.  blockIdx.y 0: dgamma; 1: the gate's and the post norm's from the same sums.
-constexpr int kRedCols = 32, kRedSlices = 32, kRedBatch = 10;
+// The sums over the groups in a fixed order: a CTA has 32 columns, its warps a slice of the groups each, whose sums the
+// first warp adds in order.  blockIdx.y 0: dgamma; 1: the gate's and the post norm's from the same sums.  Bound by the
+// latency of a round or two of loads from L2: as many warps as leave each about ten groups (76 groups of
+// 2 x 16384 columns 10.2 us with 32 warps, 6.3 with 8; 304 of 2 x 4096 5.5 with 32, 6.3 with 16).  CTAs of 8 columns,
+// or clusters over the groups, take 1 to 9 us longer.
+constexpr int kRedCols = 32, kRedMaxWarps = 32, kRedBatch = 20;
 template <int ES>
-__global__ void __launch_bounds__(kRedCols * kRedSlices)
-    resnorm_reduce_kernel(const ResNormBwd a, const float* part1, const float* part2, int G) {
+__global__ void __launch_bounds__(kRedCols * kRedMaxWarps)
+    resnorm_reduce_kernel(const __grid_constant__ ResNormBwd a, const float* part1, const float* part2, int G) {
     griddep_launch_dependents();  // programmatic dependent launch: no global access before the wait
     griddep_wait();
     using V = Vec16<ES>;
-    __shared__ float ss[kRedSlices][kRedCols];
+    __shared__ float ss[kRedMaxWarps][kRedCols];
     const bool second = blockIdx.y == 1 || !a.dgamma;
     const float* part = second ? part2 : part1;
-    const int c = threadIdx.x % kRedCols, sl = threadIdx.x / kRedCols;
-    const int64_t j = static_cast<int64_t>(blockIdx.x) * kRedCols + c;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int64_t j = static_cast<int64_t>(blockIdx.x) * kRedCols + lane;
     float s = 0.f;
     if (j < a.D) {
-        for (int g0 = sl; g0 < G; g0 += kRedBatch * kRedSlices) {  // a batch's loads go out together
+        for (int g0 = warp; g0 < G; g0 += kRedBatch * warps) {  // a batch's loads go out together
             float val[kRedBatch];
 #pragma unroll
             for (int i = 0; i < kRedBatch; ++i) {
-                const int g = g0 + i * kRedSlices;
+                const int g = g0 + i * warps;
                 val[i] = g < G ? part[static_cast<int64_t>(g) * a.D + j] : 0.f;
             }
 #pragma unroll
             for (int i = 0; i < kRedBatch; ++i) s += val[i];
         }
     }
-    ss[sl][c] = s;
+    ss[warp][lane] = s;
     __syncthreads();
-    if (sl != 0 || j >= a.D) return;
+    if (warp != 0 || j >= a.D) return;
     float t = 0.f;
-#pragma unroll
-    for (int k = 0; k < kRedSlices; ++k) t += ss[k][c];
+    for (int k = 0; k < warps; ++k) t += ss[k][lane];
     if (!second) {
         a.dgamma[j] = t;
         return;
@@ -809,8 +811,9 @@ cudaError_t bwd(const ResNormBwd& a, void* workspace, cudaStream_t s) {
                              s, a, static_cast<const RowStats*>(stats), part1, second ? part2 : nullptr);
     if (e != cudaSuccess || (!a.dgamma && !second)) return e;
     const dim3 rgrid(static_cast<unsigned>((a.D + kRedCols - 1) / kRedCols), a.dgamma && second ? 2 : 1);
-    return launch_dependent(resnorm_reduce_kernel<ES>, rgrid, dim3(kRedCols * kRedSlices), 0, s, a,
-                            static_cast<const float*>(part1), static_cast<const float*>(part2), G);
+    const int warps = G >= 256 ? kRedMaxWarps : G >= 128 ? kRedMaxWarps / 2 : kRedMaxWarps / 4;
+    return launch_dependent(resnorm_reduce_kernel<ES>, rgrid, dim3(32 * warps), 0, s, a, static_cast<const float*>(part1),
+                            static_cast<const float*>(part2), G);
 }
 
 }  // namespace
