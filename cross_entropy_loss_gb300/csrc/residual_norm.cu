@@ -637,8 +637,8 @@ __global__ void __launch_bounds__(kRowThreads, 1)
 // latency of a round or two of loads from L2: as many warps as leave each about ten groups (76 groups of
 // 2 x 16384 columns 10.2 us with 32 warps, 6.3 with 8; 304 of 2 x 4096 5.5 with 32, 6.3 with 16).  CTAs of 8 columns,
 // or clusters over the groups, take 1 to 9 us longer.
-constexpr int kRedCols = 32, kRedMaxWarps = 32, kRedBatch = 20;
-template <int ES>
+constexpr int kRedCols = 32, kRedMaxWarps = 32;
+template <int ES, int BATCH>
 __global__ void __launch_bounds__(kRedCols * kRedMaxWarps)
     resnorm_reduce_kernel(const __grid_constant__ ResNormBwd a, const float* part1, const float* part2, int G) {
     griddep_launch_dependents();  // programmatic dependent launch: no global access before the wait
@@ -651,22 +651,25 @@ __global__ void __launch_bounds__(kRedCols * kRedMaxWarps)
     const int64_t j = static_cast<int64_t>(blockIdx.x) * kRedCols + lane;
     float s = 0.f;
     if (j < a.D) {
-        for (int g0 = warp; g0 < G; g0 += kRedBatch * warps) {  // a batch's loads go out together
-            float val[kRedBatch];
+        for (int g0 = warp; g0 < G; g0 += BATCH * warps) {  // a batch's loads go out together
+            float val[BATCH];
 #pragma unroll
-            for (int i = 0; i < kRedBatch; ++i) {
+            for (int i = 0; i < BATCH; ++i) {
                 const int g = g0 + i * warps;
                 val[i] = g < G ? part[static_cast<int64_t>(g) * a.D + j] : 0.f;
             }
 #pragma unroll
-            for (int i = 0; i < kRedBatch; ++i) s += val[i];
+            for (int i = 0; i < BATCH; ++i) s += val[i];
         }
     }
     ss[warp][lane] = s;
     __syncthreads();
     if (warp != 0 || j >= a.D) return;
     float t = 0.f;
-    for (int k = 0; k < warps; ++k) t += ss[k][lane];
+    for (int k = 0; k < warps; k += 8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t += ss[k + i][lane];
+    }
     if (!second) {
         a.dgamma[j] = t;
         return;
@@ -812,7 +815,8 @@ cudaError_t bwd(const ResNormBwd& a, void* workspace, cudaStream_t s) {
     if (e != cudaSuccess || (!a.dgamma && !second)) return e;
     const dim3 rgrid(static_cast<unsigned>((a.D + kRedCols - 1) / kRedCols), a.dgamma && second ? 2 : 1);
     const int warps = G >= 256 ? kRedMaxWarps : G >= 128 ? kRedMaxWarps / 2 : kRedMaxWarps / 4;
-    return launch_dependent(resnorm_reduce_kernel<ES>, rgrid, dim3(32 * warps), 0, s, a, static_cast<const float*>(part1),
+    const auto reduce = G <= 10 * warps ? resnorm_reduce_kernel<ES, 10> : resnorm_reduce_kernel<ES, 20>;
+    return launch_dependent(reduce, rgrid, dim3(32 * warps), 0, s, a, static_cast<const float*>(part1),
                             static_cast<const float*>(part2), G);
 }
 
