@@ -33,10 +33,10 @@ struct SmemOnce {
     }
 };
 
-// Clusters of one kernel that are resident at once, by cluster size (1, 2, 4, 8) and threads (32 .. 512); the
+// Clusters of one kernel that are resident at once, by cluster size (1, 2, 4, 8) and threads (32 .. 1024); the
 // caller's shared memory goes by those two.
 struct ResidentOnce {
-    std::atomic<int> known[kMaxDevices][4][16] = {};
+    std::atomic<int> known[kMaxDevices][4][32] = {};
 
     template <typename K>
     cudaError_t count(K kernel, int cluster, int threads, size_t smem, int* clusters) {

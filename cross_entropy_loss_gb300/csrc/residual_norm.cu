@@ -103,13 +103,13 @@ __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 // Bound by memory; what counts is how many rows an SM has under way, since a row waits for its loads and at
 // its barriers.  So: 32 registers, two vectors a thread and operand, their loads one vector at a time, and
 // grids of four times what is resident.  Measured (bf16, us): 8192 x 4096 41.0, 98% of the copy rate (one
-// vector a thread 42.6, four 49.3; 64 registers and two vectors at a time 43.6; a ring of cp.async rows
-// 44.8), with both norms 46.3 (ring 49.4, X and R kept in shared memory 53); 16384 x 1024 22.4.  BATCH 2 is
-// for rows of more than 1024 vectors: 2048 x 16384 45.2 against 50.0 (with both norms 58.8 and 56.5).
-constexpr int kFwdThreads = 512;
+// vector a thread 42.5, four 49.3; 64 registers and two vectors at a time 43.6; a ring of cp.async rows
+// 44.8), with both norms 44.9 (ring 49.4, X and R kept in shared memory 53); 16384 x 1024 22.4; 3000 x 10240
+// 39.3 and 2048 x 16384 43.6 (512 threads for wide rows 40.6 and 50.0, with 64 registers 47.2 and 45.2).
+constexpr int kFwdThreads = 1024;
 
-template <int ES, bool POST, bool FULL, int BATCH>
-__global__ void __launch_bounds__(kFwdThreads, BATCH == 1 ? 4 : 2) resnorm_fwd_kernel(const __grid_constant__ ResNormFwd a) {
+template <int ES, bool POST, bool FULL>
+__global__ void __launch_bounds__(kFwdThreads, 2) resnorm_fwd_kernel(const __grid_constant__ ResNormFwd a) {
     griddep_launch_dependents();  // programmatic dependent launch: no global access before the wait
     griddep_wait();
     using P = Pairs<ES>;
@@ -136,59 +136,37 @@ __global__ void __launch_bounds__(kFwdThreads, BATCH == 1 ? 4 : 2) resnorm_fwd_k
         if (!FULL && a.gate_kind == FOAK_GATE_ROW) q *= Vec16<ES>::load1(gr);
         if constexpr (POST) {
             float2 sx = both(0.f);
-            for (int v0 = threadIdx.x; v0 < nvec; v0 += BATCH * nt) {
-                uint4 xw[BATCH];
-#pragma unroll
-                for (int j = 0; j < BATCH; ++j)
-                    if (v0 + j * nt < nvec) xw[j] = ld_global_v4(xr + (v0 + j * nt) * 16);
-#pragma unroll
-                for (int j = 0; j < BATCH; ++j)
-                    if (v0 + j * nt < nvec) sx = squares(xw[j], sx);
-            }
+            for (int v = threadIdx.x; v < nvec; v += nt) sx = squares(ld_global_v4(xr + v * 16), sx);
             const float r1 = rsqrtf(block_sum(sx.x + sx.y, red[buffer]) * inv_d + a.post_eps);
             if (threadIdx.x == 0 && a.post_rstd) a.post_rstd[i] = r1;
             q *= r1;
         }
         float2 s2 = both(0.f);
-        for (int v0 = threadIdx.x; v0 < nvec; v0 += BATCH * nt) {
-            uint4 xw[BATCH], rw[BATCH], gw[BATCH];
+        for (int v = threadIdx.x; v < nvec; v += nt) {
+            P x, h, w;
+            x.unpack(ld_global_v4(xr + v * 16));
+            h.unpack(ld_global_v4(rr + v * 16));
+            if constexpr (POST) {
+                w.unpack(ld_global_v4(a.post_gamma + v * 16));
 #pragma unroll
-            for (int j = 0; j < BATCH; ++j) {
-                const int v = v0 + j * nt;
-                if (v >= nvec) break;
-                xw[j] = ld_global_v4(xr + v * 16);
-                rw[j] = ld_global_v4(rr + v * 16);
-                if (FULL || channel) gw[j] = ld_global_v4(gr + v * 16);
+                for (int k = 0; k < NP; ++k) x.p[k] = __fmul2_rn(x.p[k], w.p[k]);
+            }
+            if (FULL || channel) {
+                w.unpack(ld_global_v4(gr + v * 16));
+#pragma unroll
+                for (int k = 0; k < NP; ++k) x.p[k] = __fmul2_rn(x.p[k], w.p[k]);
             }
 #pragma unroll
-            for (int j = 0; j < BATCH; ++j) {
-                const int v = v0 + j * nt;
-                if (v >= nvec) break;
-                P x, h, w;
-                x.unpack(xw[j]);
-                h.unpack(rw[j]);
-                if constexpr (POST) {
-                    w.unpack(ld_global_v4(a.post_gamma + v * 16));
+            for (int k = 0; k < NP; ++k) {
+                h.p[k] = __ffma2_rn(both(q), x.p[k], h.p[k]);
+                s2 = __ffma2_rn(h.p[k], h.p[k], s2);
+            }
+            h.store(hr + v * 16);
+            if (a.gamma) {
 #pragma unroll
-                    for (int k = 0; k < NP; ++k) x.p[k] = __fmul2_rn(x.p[k], w.p[k]);
-                }
-                if (FULL || channel) {
-                    w.unpack(gw[j]);
-#pragma unroll
-                    for (int k = 0; k < NP; ++k) x.p[k] = __fmul2_rn(x.p[k], w.p[k]);
-                }
-#pragma unroll
-                for (int k = 0; k < NP; ++k) {
-                    h.p[k] = __ffma2_rn(both(q), x.p[k], h.p[k]);
-                    s2 = __ffma2_rn(h.p[k], h.p[k], s2);
-                }
-                h.store(hr + v * 16);
-                if (a.gamma) {
-#pragma unroll
-                    for (int k = 0; k < NP; k += 2)
-                        kept[k / 2 * nvec + v] = make_uint4(__float_as_uint(h.p[k].x), __float_as_uint(h.p[k].y),
-                                                            __float_as_uint(h.p[k + 1].x), __float_as_uint(h.p[k + 1].y));
-                }
+                for (int k = 0; k < NP; k += 2)
+                    kept[k / 2 * nvec + v] = make_uint4(__float_as_uint(h.p[k].x), __float_as_uint(h.p[k].y),
+                                                        __float_as_uint(h.p[k + 1].x), __float_as_uint(h.p[k + 1].y));
             }
         }
         float rstd = 0.f;
@@ -373,7 +351,7 @@ __global__ void __launch_bounds__(128) resnorm_bwd_cols_kernel(const ResNormBwd 
 // Arithmetic on pairs (two-wide FP32).
 //
 // Bound by memory and, in bf16, by how many instructions 16 warps an SM get out (half of the issue slots).  bf16,
-// us: 8192 x 4096 60 (0.84 of the copy rate; the reduce 3.5 of them), both norms and a channel gate 73; 4096 x
+// us: 8192 x 4096 60 (0.84 of the copy rate; the reduce 4 to 6 of them), both norms and a channel gate 73; 4096 x
 // 8192 58 (256 threads and clusters of two 70); 2048 x 16384 66 (waiting at the barrier for the row's sums, not
 // with the next row's sums in between, 87); 8192 x 4096 reading each operand twice, sums first, 139.  An element's
 // intermediate results kept across the barrier spill: 86 against 71 with both norms.
@@ -717,11 +695,11 @@ Slices slices_of(int64_t nvec) {
     return c;
 }
 
-template <int ES, bool POST, bool FULL, int BATCH>
+template <int ES, bool POST, bool FULL>
 cudaError_t launch_fwd(const ResNormFwd& a, int threads, cudaStream_t s) {
     static SmemOnce limit;
     static ResidentOnce resident;
-    const auto kernel = resnorm_fwd_kernel<ES, POST, FULL, BATCH>;
+    const auto kernel = resnorm_fwd_kernel<ES, POST, FULL>;
     const size_t smem = a.gamma ? static_cast<size_t>(a.D) * 4 : 0;
     int ctas = 0;
     cudaError_t e = limit.allow(kernel, static_cast<int>(kResNormMaxD) * 4);
@@ -737,14 +715,16 @@ template <int ES>
 cudaError_t fwd(const ResNormFwd& a, cudaStream_t s) {
     const bool full = a.gate_kind == FOAK_GATE_FULL;
     const int64_t nvec = a.D / (16 / ES);
-    // two vectors a thread; one where the rows do not fill the GPU (1 row of 4096 bf16 1.8 us against 2.2, 300 rows 3.1
-    // against 4.4)
-    const int64_t each = a.N <= 2 * static_cast<int64_t>(device_sm_count()) ? 1 : 2;
+    // Two vectors a thread; one where the rows do not fill the GPU (1 row of 4096 bf16 1.8 us against 2.2, 300 rows
+    // 3.0 against 4.5).  Of fp32 rows with a norm after the block, which come by three times and keep half as much in
+    // shared memory, four where that leaves CTAs of 256 to 512 threads (1537 x 5000 27.2 us against 29.4, 1500 x 7168
+    // 35.7 against 38.7; 2048 vectors of bf16 57.9 against 52.1).
+    const bool small = a.N <= 2 * static_cast<int64_t>(device_sm_count());
+    const bool four = ES == 4 && a.post_gamma && nvec > 1024 && nvec < 2048;
+    const int64_t each = small ? 1 : four ? 4 : 2;
     const int threads = static_cast<int>(std::min<int64_t>(((nvec + each - 1) / each + 31) / 32 * 32, kFwdThreads));
-    if (a.post_gamma) return full ? launch_fwd<ES, true, true, 1>(a, threads, s) : launch_fwd<ES, true, false, 1>(a, threads, s);
-    if (nvec > 2 * kFwdThreads)
-        return full ? launch_fwd<ES, false, true, 2>(a, threads, s) : launch_fwd<ES, false, false, 2>(a, threads, s);
-    return full ? launch_fwd<ES, false, true, 1>(a, threads, s) : launch_fwd<ES, false, false, 1>(a, threads, s);
+    if (a.post_gamma) return full ? launch_fwd<ES, true, true>(a, threads, s) : launch_fwd<ES, true, false>(a, threads, s);
+    return full ? launch_fwd<ES, false, true>(a, threads, s) : launch_fwd<ES, false, false>(a, threads, s);
 }
 
 template <int ES, bool POST, bool FULL, bool HASX, bool SUMS>

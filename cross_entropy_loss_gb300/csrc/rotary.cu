@@ -11,9 +11,10 @@
 // split off, and sine and cosine of the rest, |x| <= pi/4, are their Taylor polynomials to x^9
 // and x^10, whose next terms are below 1.8e-9 and 1.2e-10.
 //
-// Work.  A unit is two vectors of a head whose pairs have the same frequencies: the vectors at
-// i and i + r/2, or two adjacent ones; of the part that passes through, two adjacent ones.  An
-// angle is formed once for many heads.  Each element is read and written once.
+// Work.  A unit is two vectors of a head: those at i and i + r/2, or interleaved pairs' vectors j and
+// j + half of them (side by side, each lane would touch half of every 32 bytes: 36 us against 28 for
+// 8192 tokens of 40 heads); of the part that passes through likewise.  An angle is formed once for
+// many heads.  Each element is read and written once.
 #include <algorithm>
 #include <cmath>
 
