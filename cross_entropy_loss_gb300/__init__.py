@@ -927,6 +927,7 @@ def foak_distill_backward(logits, labels, teacher_ids, teacher_logprobs, stats, 
 FOAK_GATE_NONE, FOAK_GATE_CHANNEL, FOAK_GATE_ROW, FOAK_GATE_FULL = 0, 1, 2, 3
 FOAK_RESIDUAL_NORM_MAX_D = 32768
 _resnorm_ws: dict = {}
+_resnorm_lock = threading.Lock()  # a backward's two launches, which hand partial sums on in a workspace
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
@@ -1094,8 +1095,9 @@ def foak_residual_norm_backward(dY, dH, H=None, rstd=None, gamma=None, *, X=None
         ws = _cached_workspace(_resnorm_ws, need, dev, _handle_of(di), fill=torch.empty)
     else:
         ws = _workspace_arg(workspace_tensor, dev)
-    st = _launch(di, lib.foak_residual_norm_backward, dy, lddy, dh, lddh, h, ldh, x, ldx, _DT[dtype], N, D, g, kind, ldg,
-                 pg, gm, r1, r, scale, dR.data_ptr(), lddr, dx, lddx, a, b, lddg, c, ws.data_ptr(), ws.numel())
+    with _resnorm_lock:
+        st = _launch(di, lib.foak_residual_norm_backward, dy, lddy, dh, lddh, h, ldh, x, ldx, _DT[dtype], N, D, g, kind,
+                     ldg, pg, gm, r1, r, scale, dR.data_ptr(), lddr, dx, lddx, a, b, lddg, c, ws.data_ptr(), ws.numel())
     if st:
         _check(st, "foak_residual_norm_backward")
     return dict(dR=dR, dX=dR if same and want_dX else dX, dgamma=dgamma, dgate=dgate, dpost_gamma=dpost)

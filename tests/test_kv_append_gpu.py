@@ -49,6 +49,17 @@ def test_slots_of_bad_tables(cuda_lib):
     assert all(-1 <= s < 24 for s in messy["slots"].tolist())
 
 
+@pytest.mark.parametrize("B", [4095, 4096, 5000])
+def test_slots_of_many_sequences(cuda_lib, B):
+    """As many starts as one block keeps at hand, and more."""
+    g = torch.Generator().manual_seed(B)
+    lens, new = torch.randint(0, 40, (B,), generator=g).tolist(), torch.randint(0, 3, (B,), generator=g).tolist()
+    table, cl, starts, T, pages = _step(lens, new, 16, seed=B, padding=300)
+    out = _slots(cuda_lib, table, cl, starts, T, 16, pages)
+    at, pos, bad = ref.slots(table, cl, starts, T, 16, pages)
+    assert not bad and out["slots"].tolist() == at and out["positions"].tolist() == pos and int(out["err"]) == 0
+
+
 def test_slots_without_sequences_or_tokens(cuda_lib):
     empty = torch.zeros(0, 3, dtype=torch.int32), torch.zeros(0, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
     out = _slots(cuda_lib, *empty, 5, 16, 4)

@@ -1,5 +1,7 @@
 """Residual norms, rotary positions and the paged cache together, as a decoder layer's training and serving use
 them; on streams of their own and in captured graphs."""
+import threading
+
 import pytest
 import torch
 
@@ -280,6 +282,35 @@ def test_overlapping_backwards_and_graphs_have_workspaces_of_their_own(cuda_lib)
     torch.cuda.synchronize()
     for i, o in got + [(0, outs[0]), (1, outs[1])]:
         assert all(torch.equal(a, b) for a, b in zip(o, want[i], strict=True))
+
+
+def test_backwards_of_two_host_threads_on_one_stream(cuda_lib):
+    """Their launches do not come between one another's, whose partial sums lie in the stream's workspace."""
+    ce = cuda_lib
+    cases, want, wrong = [], [], [0, 0]
+    for seed in range(2):
+        c = {k: None if v is None else v.cuda() for k, v in ref.make_norm(400, 1024, "bf16", "none", True, seed=seed).items()}
+        f = ce.foak_residual_norm_forward(c["X"], c["R"], c["gamma"], post_gamma=c["post_gamma"])
+        cases.append((c, f))
+
+    def back(i):
+        c, f = cases[i]
+        b = ce.foak_residual_norm_backward(c["dY"], c["dH"], f["H"], f["rstd"], c["gamma"], X=c["X"], post_gamma=c["post_gamma"], post_rstd=f["post_rstd"])
+        return torch.cat([b["dgamma"], b["dpost_gamma"]])
+
+    def many(i):
+        for _ in range(20):
+            outs = [back(i) for _ in range(50)]
+            wrong[i] += sum(not torch.equal(o, want[i]) for o in outs)
+
+    want.extend(back(i) for i in range(2))
+    threads = [threading.Thread(target=many, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert wrong == [0, 0]
 
 
 def test_the_shared_workspace_of_calls_in_a_row(cuda_lib):
