@@ -222,7 +222,9 @@ foak_status check_resnorm(int32_t dtype, int64_t N, int64_t D, const void* gate,
     if (N < 0 || D < 8 || !std::isfinite(scale)) return FOAK_ERR_INVALID_ARG;
     if (D % 8 || D > kResNormMaxD) return FOAK_ERR_UNSUPPORTED;
     if (gate_kind < FOAK_GATE_NONE || gate_kind > FOAK_GATE_FULL) return FOAK_ERR_INVALID_ARG;
-    if ((gate_kind == FOAK_GATE_NONE) != (gate == nullptr) && (N > 0 || gate)) return FOAK_ERR_INVALID_ARG;
+    // a gate a row or an element of no rows may be null, one a channel is read by its own
+    const bool no_gate = gate_kind == FOAK_GATE_NONE || (N == 0 && gate_kind != FOAK_GATE_CHANNEL);
+    if (gate ? gate_kind == FOAK_GATE_NONE : !no_gate) return FOAK_ERR_INVALID_ARG;
     if (gate_kind == FOAK_GATE_CHANNEL && !aligned(gate, 16)) return FOAK_ERR_INVALID_ARG;
     if (gate_kind == FOAK_GATE_ROW && (!aligned(gate, static_cast<size_t>(*es)) || ldg < 1)) return FOAK_ERR_INVALID_ARG;
     if (gate_kind == FOAK_GATE_FULL && N > 0 && !rows_ok(gate, ldg, D, *es)) return FOAK_ERR_INVALID_ARG;
@@ -657,10 +659,10 @@ foak_status foak_residual_norm_backward(const void* dY, int64_t lddy, const void
     if (!aligned(post_rstd, 4) || !aligned(rstd, 4) || !aligned(dgamma, 4) || !aligned(dpost_gamma, 4))
         return FOAK_ERR_INVALID_ARG;
     if ((dgate && gate_kind == FOAK_GATE_NONE) || (dpost_gamma && !post_gamma)) return FOAK_ERR_INVALID_ARG;
-    if (dgate && !aligned(dgate, 4)) return FOAK_ERR_INVALID_ARG;
+    if ((dgate && !aligned(dgate, 4)) || (dY && !gamma)) return FOAK_ERR_INVALID_ARG;
     if (N > 0) {
         if ((!dY && !dH) || !dR || !rows_ok(dR, lddr, D, es)) return FOAK_ERR_INVALID_ARG;
-        if (dY ? !rows_ok(dY, lddy, D, es) || !H || !rows_ok(H, ldh, D, es) || !gamma || !rstd : dgamma != nullptr)
+        if (dY ? !rows_ok(dY, lddy, D, es) || !H || !rows_ok(H, ldh, D, es) || !rstd : dgamma != nullptr)
             return FOAK_ERR_INVALID_ARG;
         if (dH && !rows_ok(dH, lddh, D, es)) return FOAK_ERR_INVALID_ARG;
         if ((post_gamma || dgate) && !X) return FOAK_ERR_INVALID_ARG;

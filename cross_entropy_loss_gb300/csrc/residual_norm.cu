@@ -194,8 +194,8 @@ __global__ void __launch_bounds__(kFwdThreads, 2) resnorm_fwd_kernel(const __gri
 }
 
 // ------------------------------------------------------------------ backward, any rows
-// Sums first, then the columns: for no rows at all, for row strides or counts past 32 bits, and for a full gate
-// whose gradient nobody wants.  What a row's elements need of the row's sums: dh = dH + r gamma dY - k1 H, and with
+// Sums first, then the columns: for row strides or counts past 32 bits, and for a full gate whose gradient nobody
+// wants.  What a row's elements need of the row's sums: dh = dH + r gamma dY - k1 H, and with
 // the norm after the block dX = r1 gp du - k2 X.
 struct RowStats {
     float k1, k2;
@@ -762,6 +762,17 @@ cudaError_t ring(const ResNormBwd& a, float* part1, float* part2, int* groups, c
     return launch_ring<ES, POST, FULL, HASX, SUMS>(a, sp, c.threads, part1, part2, groups, s);
 }
 
+// The sums over no rows.  No operand is read: nothing says that there are any.
+cudaError_t bwd_of_no_rows(const ResNormBwd& a, cudaStream_t s) {
+    const auto zero = [&](void* sums) {
+        return sums ? cudaMemsetAsync(sums, 0, static_cast<size_t>(a.D) * sizeof(float), s) : cudaSuccess;
+    };
+    cudaError_t e = zero(a.dgamma);
+    if (e == cudaSuccess) e = zero(a.dpost_gamma);
+    if (e == cudaSuccess && a.gate_kind == FOAK_GATE_CHANNEL) e = zero(a.dgate);
+    return e;
+}
+
 template <int ES>
 cudaError_t bwd(const ResNormBwd& a, void* workspace, cudaStream_t s) {
     const int groups = resnorm_groups(a.D);
@@ -771,11 +782,11 @@ cudaError_t bwd(const ResNormBwd& a, void* workspace, cudaStream_t s) {
     const bool second = (a.gate_kind == FOAK_GATE_CHANNEL && a.dgate) || a.dpost_gamma;
     const bool full = a.gate_kind == FOAK_GATE_FULL, row_grad = a.gate_kind == FOAK_GATE_ROW && a.dgate;
     const int64_t nvec = a.D / (16 / ES);
-    int G = static_cast<int>(std::min<int64_t>(std::max<int64_t>(a.N, 1), 128));
+    int G = static_cast<int>(std::min<int64_t>(a.N, 128));
     cudaError_t e = cudaSuccess;
     // rows and row strides of 32 bits
     const int64_t ld = std::max({a.lddy, a.lddh, a.ldh, a.ldx, a.ldg, a.lddr, a.lddx, a.lddg});
-    const bool one_pass = a.N > 0 && a.N < (1ll << 31) && ld * ES < (1ll << 32) && nvec <= static_cast<int64_t>(kMaxCluster) * kVpt * kRowThreads && (a.X || !full);
+    const bool one_pass = a.N < (1ll << 31) && ld * ES < (1ll << 32) && nvec <= static_cast<int64_t>(kMaxCluster) * kVpt * kRowThreads && (a.X || !full);
     if (one_pass) {
         float* p2 = second ? part2 : nullptr;
         if (a.post_gamma)
@@ -784,14 +795,13 @@ cudaError_t bwd(const ResNormBwd& a, void* workspace, cudaStream_t s) {
         else if (full) e = ring<ES, false, true, true, false>(a, part1, p2, &G, s);
         else e = row_grad ? ring<ES, false, false, true, true>(a, part1, p2, &G, s) : ring<ES, false, false, true, false>(a, part1, p2, &G, s);
         if (e != cudaSuccess) return e;
-    } else if (a.N > 0) {
+    } else {
         const int grid = static_cast<int>(std::min<int64_t>(a.N, static_cast<int64_t>(device_sm_count()) * 8));
         e = launch_dependent(resnorm_bwd_stats_kernel<ES>, dim3(grid), dim3(256), 0, s, a, stats);
         if (e != cudaSuccess) return e;
-    }
-    if (!one_pass)
         e = launch_dependent(resnorm_bwd_cols_kernel<ES>, dim3(static_cast<unsigned>((nvec + 127) / 128), G), dim3(128), 0,
                              s, a, static_cast<const RowStats*>(stats), part1, second ? part2 : nullptr);
+    }
     if (e != cudaSuccess || (!a.dgamma && !second)) return e;
     const dim3 rgrid(static_cast<unsigned>((a.D + kRedCols - 1) / kRedCols), a.dgamma && second ? 2 : 1);
     const int warps = G >= 256 ? kRedMaxWarps : G >= 128 ? kRedMaxWarps / 2 : kRedMaxWarps / 4;
@@ -808,6 +818,7 @@ cudaError_t launch_resnorm_fwd(int es, const ResNormFwd& a, cudaStream_t s) {
 }
 
 cudaError_t launch_resnorm_bwd(int es, const ResNormBwd& a, void* workspace, cudaStream_t s) {
+    if (a.N == 0) return bwd_of_no_rows(a, s);
     return es == 2 ? bwd<2>(a, workspace, s) : bwd<4>(a, workspace, s);
 }
 

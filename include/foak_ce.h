@@ -379,7 +379,8 @@ size_t foak_residual_norm_workspace_size(int64_t N, int64_t D);
  *     du = scale g dh,     dgate = scale dh u, summed over the rows (channel) or a row (row)
  *     dX = du,  or with post_gamma  r1 (post_gamma du - xh mean_j(xh post_gamma du)),
  *     dpost_gamma_j = sum_i du xh
- *   dY (device)         N x D, or NULL: zero (H, gamma and rstd are not read; dgamma must be NULL)
+ *   dY (device)         N x D, or NULL: zero (H, gamma and rstd are not read; dgamma must be NULL
+ *                       unless N is 0)
  *   dH (device)         N x D, the gradient that arrives along the residual stream, or NULL: zero;
  *                       not both NULL
  *   X (device)          N x D; may be NULL where neither post_gamma nor dgate is given
@@ -390,7 +391,8 @@ size_t foak_residual_norm_workspace_size(int64_t N, int64_t D);
  *   dgamma, dpost_gamma (device) float[D] or NULL, overwritten
  *   dgate (device)      float[D] (channel), float[N] (row) or N x D in dtype with row stride lddg
  *                       (full), or NULL
- * The sums over the rows have a fixed order: results are the same from run to run.  Sizes and
+ * The sums over the rows have a fixed order: results are the same from run to run.  Without rows
+ * they are zeros, and N x D operands, statistics and gates of rows or elements may be NULL.  Sizes and
  * alignment as in the forward.  An output may be one of the N x D inputs (same stride), no two
  * outputs the same.
  */
