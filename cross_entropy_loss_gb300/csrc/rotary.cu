@@ -95,12 +95,16 @@ struct Piece {
     }
 };
 
-// c times cosine and sine of `turn` 2^-64 turns.
+// c times cosine and sine of `turn` 2^-64 turns.  What is left of the nearest quarter turn is taken to 2^-55 turn, and to
+// 24 bits where it is larger: the upper word as a float, less 1, and 1.f with the lower word's first 23 bits behind it,
+// whose sum is exact where the upper word is 0 or -1.  (Of the upper word alone, 2^-32 turn, the sine of a slow pair near
+// position 0 would be off by half a percent; a 64-bit conversion instead: 3001 fp32 tokens 11.1 us against 9.9.)
 __device__ __forceinline__ void turn_cos_sin(uint64_t turn, float c, float sign, float& co, float& si) {
-    const uint32_t hi = static_cast<uint32_t>(turn >> 32);
-    const uint32_t quarter = (hi + 0x20000000u) >> 30;
-    const int32_t rest = static_cast<int32_t>(hi - (quarter << 30));  // [-2^29, 2^29]: an eighth of a turn
-    const float x = static_cast<float>(rest) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+    const uint32_t hi = static_cast<uint32_t>(turn >> 32), lo = static_cast<uint32_t>(turn);
+    const uint32_t quarter = (hi + 0x20000000u) & 0xc0000000u;
+    const int32_t below = static_cast<int32_t>(hi - quarter - 1u);  // [-2^29 - 1, 2^29): an eighth of a turn
+    const float rest = static_cast<float>(below) + __uint_as_float(0x3f800000u | lo >> 9);
+    const float x = rest * 1.4629180792671596e-9f;  // 2 pi / 2^32
     const float z = x * x;
     float s = fmaf(z, 2.7557319223985893e-6f, -1.9841269841269841e-4f);
     s = fmaf(z, s, 8.3333333333333333e-3f);
@@ -111,9 +115,9 @@ __device__ __forceinline__ void turn_cos_sin(uint64_t turn, float c, float sign,
     k = fmaf(z, k, 4.1666666666666667e-2f);
     k = fmaf(z, k, -0.5f);
     k = fmaf(z, k, 1.f);
-    const float a = (quarter & 1u) ? s : k, b = (quarter & 1u) ? k : s;
-    co = ((quarter + 1u) & 2u) ? -c * a : c * a;
-    si = (quarter & 2u) ? -c * sign * b : c * sign * b;
+    const bool odd = quarter & 0x40000000u;
+    co = __uint_as_float(__float_as_uint(c * (odd ? s : k)) ^ ((quarter + 0x40000000u) & 0x80000000u));
+    si = __uint_as_float(__float_as_uint(c * sign * (odd ? k : s)) ^ (quarter & 0x80000000u));
 }
 
 // Where a unit's vectors lie in its head, and whose angles they take.
@@ -403,8 +407,10 @@ __global__ void __launch_bounds__(kThreads, kWarpCtas)
 
 // The same without shared memory, an item a thread with its own angles: calls too small to fill the GPU, whose
 // latency this shortens (a token of 32 + 8 heads 1.9 us against 2.6), and heads whose table does not fit.
+// At most 32 registers, 40 for eight angles (3001 fp32 tokens, four angles: 9.9 us, unbounded 10.7; 300 bf16 tokens of
+// 56 heads x 96, eight: 3.9, unbounded 4.0, with 32 registers 4.0; 512 of 40 x 128 4.3, unbounded 4.3, 32 registers 5.8).
 template <int ES, int W, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, W == 8 ? 6 : 8)
     rotary_kernel(const __grid_constant__ RotaryArgs a, const __grid_constant__ Items it) {
     griddep_launch_dependents();  // programmatic dependent launch: no global access before the wait
     griddep_wait();
