@@ -6,10 +6,10 @@
 //
 // The angle.  f_i / 2 pi, the turns that a position adds, is kept as a fraction of 2^64, so the
 // angle modulo a turn is the low 64 bits of one integer product: exact but for the fraction's
-// own rounding, p 2^-53 turns at most, whatever the position.  No table of positions is built,
+// own rounding, |p| 2^-63 turns at most.  No table of positions is built,
 // read or outgrown (at 131072 positions of 64 frequencies one would fill half the L2).  The nearest quarter turn is
-// split off, and sine and cosine of the rest, |x| <= pi/4, are their Taylor polynomials to x^9
-// and x^10, whose next terms are below 1.8e-9 and 1.2e-10.
+// split off, the rest taken to 2^-55 turn and 24 bits, and its sine and cosine, |x| <= pi/4, are their Taylor
+// polynomials to x^9 and x^10, whose next terms are below 1.8e-9 and 1.2e-10.
 //
 // Work.  A unit is two vectors of a head: those at i and i + r/2, or interleaved pairs' vectors j and
 // j + half of them (side by side, each lane would touch half of every 32 bytes: 36 us against 28 for
@@ -598,10 +598,17 @@ void rotary_inv_freq(double base, int64_t r, int scaling, double factor, double 
     }
 }
 
+// The quotient by 2 pi as two numbers, the second from the first one's remainder, with 2 pi as two numbers as well.
 uint64_t rotary_turns(double inv_freq) {
-    const double turns = inv_freq / 6.283185307179586476925;
-    const double scaled = std::ldexp(turns - std::floor(turns), 64);
-    return scaled < 18446744073709551616.0 ? static_cast<uint64_t>(scaled) : 0;  // a whole turn is none
+    constexpr double kTwoPi = 6.283185307179586, kTwoPiRest = 2.4492935982947064e-16;
+    const auto fraction = [](double turns) {  // times 2^64, cut off; of the absolute value, whose fraction is exact
+        const double size = std::fabs(turns);
+        const uint64_t scaled = static_cast<uint64_t>(std::ldexp(size - std::floor(size), 64));
+        return turns < 0.0 ? 0 - scaled : scaled;
+    };
+    const double turns = inv_freq / kTwoPi;
+    const double rest = std::fma(-turns, kTwoPiRest, std::fma(-turns, kTwoPi, inv_freq));
+    return fraction(turns) + fraction(rest / kTwoPi);
 }
 
 cudaError_t launch_rotary(int es, const RotaryArgs& a, cudaStream_t s) {

@@ -423,7 +423,8 @@ foak_status foak_residual_norm_backward(const void* dY, int64_t lddy, const void
  * original >= 1.
  *
  * foak_rotary_turns (host): what the device calls take: turns[i] = inv_freq[i] / 2 pi as a
- * fraction of 2^64, whole turns dropped.  inv_freq finite.
+ * fraction of 2^64, whole turns dropped: within 2^-63 turn where |inv_freq[i]| <= 2^40 (above, its
+ * 106 bits are not enough).  inv_freq finite.
  */
 #define FOAK_ROTARY_NONE 0
 #define FOAK_ROTARY_LINEAR 1
@@ -440,8 +441,11 @@ foak_status foak_rotary_turns(const double* inv_freq, int64_t n, uint64_t* turns
  *                       NULL.  Strides >= 0; what is 16-byte aligned moves 16 bytes at a time
  *   Qo, Ko (device)     where they go, with their own strides; Q and K themselves (same strides) to
  *                       rotate in place; otherwise they overlap nothing; heads d elements or more apart
- *   positions (device)  int64[T], any value (the angle is exact to 2^-53 positions[t] turns)
+ *   positions (device)  int64[T], any value: the angle modulo a turn is an integer product, off by
+ *                       |positions[t]| times what the fraction is off (2^-63 turn at most)
  *   turns (device)      uint64[rotary_dim / 2] of foak_rotary_turns
+ * Sine and cosine of that angle are within 4e-9 and a few fp32 roundings of themselves, and 2^-55
+ * turn of the angle.
  * d >= rotary_dim >= 2, rotary_dim even; H * d <= 2^28.  Every element is computed the same way in every
  * call: it depends on its own pair, position and frequency alone.
  */

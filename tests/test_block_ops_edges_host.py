@@ -1,5 +1,8 @@
 """Calls of the residual norms and of rotary positions at the edges of what is allowed, as far as the host decides
 them.  No GPU: pointers are never dereferenced."""
+import math
+from fractions import Fraction
+
 import pytest
 
 from test_block_ops_host import BWD, FWD, P, _call, so  # noqa: F401  (the library, a fixture)
@@ -22,3 +25,15 @@ def test_gamma_of_an_empty_batch(so):  # noqa: F811
     assert _call(so, "foak_residual_norm_backward", BWD, **none, dY=P, gamma=None, dgamma=None) == so.FOAK_ERR_INVALID_ARG
     assert _call(so, "foak_residual_norm_backward", BWD, **none, dY=P) == so.FOAK_ERR_CUDA
     assert _call(so, "foak_residual_norm_backward", BWD, **none, dY=None, gamma=None) == so.FOAK_ERR_CUDA
+
+
+def test_turns_to_the_last_bit_but_one(so):  # noqa: F811
+    """Each of the two parts that a fraction is made of is cut off below 2^-64 of a turn, and neither the constant's
+    106 bits nor the second part's roundings add a hundredth of that below 2^40: less than 2^-63 in all."""
+    pi = Fraction("3.141592653589793238462643383279502884197169399375105820974944592307816406286")
+    freqs = [1.0, 0.5, -0.25, 1e-3, 3.7e-7, 1.9e-8, 6.0, 100.0, -100.0, 12345.678, 2.0 ** 39 + 0.1, 0.0, -1e-30, 5e-324, 2 * math.pi, 8 * math.pi]
+    freqs += so.foak_rotary_inv_freq(128, base=500000.0) + so.foak_rotary_inv_freq(96, base=1e7, scaling="linear", factor=32.0)
+    for f, t in zip(freqs, so.foak_rotary_turns(freqs).tolist()):
+        off = (Fraction(t, 2 ** 64) - Fraction(f) / (2 * pi)) % 1
+        assert min(off, 1 - off) <= Fraction(1, 2 ** 63), f
+    assert len(so.foak_rotary_turns([1e300, -1e300, 1.7976931348623157e308])) == 3  # any number of turns is taken
