@@ -195,12 +195,8 @@ __global__ void __launch_bounds__(kFwdThreads, 2) resnorm_fwd_kernel(const __gri
 
 // ------------------------------------------------------------------ backward, any rows
 // Sums first, then the columns: for row strides or counts past 32 bits, and for a full gate whose gradient nobody
-// wants.  What a row's elements need of the row's sums: dh = dH + r gamma dY - k1 H, and with
-// the norm after the block dX = r1 gp du - k2 X.
-struct RowStats {
-    float k1, k2;
-};
-
+// wants.  What a row's elements need of the row's sums (RowStats): dh = dH + r gamma dY - k1 H, and with the norm
+// after the block dX = r1 gp du - k2 X.
 template <int ES>
 __device__ __forceinline__ const char* gate_row(const ResNormBwd& a, int64_t i) {
     return a.gate_kind == FOAK_GATE_CHANNEL ? a.gate : a.gate + i * a.ldg * ES;
@@ -739,7 +735,7 @@ cudaError_t launch_ring(const ResNormBwd& a, const BwdSplit& sp, int threads, fl
     cudaError_t e = limit.allow(kernel, kRingSmemMax);
     if (e == cudaSuccess) e = resident.count(kernel, sp.cluster, threads, smem, &clusters);
     if (e != cudaSuccess) return e;
-    const int64_t G = std::min<int64_t>({a.N, clusters, resnorm_groups(a.D)});
+    const int64_t G = std::min<int64_t>({a.N, clusters, resnorm_groups(a.N, a.D)});
     *groups = static_cast<int>(G);
     return launch_clusters(kernel, G, sp.cluster, threads, smem, s, a, sp, part1, part2);
 }
@@ -775,14 +771,14 @@ cudaError_t bwd_of_no_rows(const ResNormBwd& a, cudaStream_t s) {
 
 template <int ES>
 cudaError_t bwd(const ResNormBwd& a, void* workspace, cudaStream_t s) {
-    const int groups = resnorm_groups(a.D);
+    const int groups = resnorm_groups(a.N, a.D);
     float* part1 = static_cast<float*>(workspace);
     float* part2 = part1 + static_cast<size_t>(groups) * a.D;
     RowStats* stats = reinterpret_cast<RowStats*>(part2 + static_cast<size_t>(groups) * a.D);
     const bool second = (a.gate_kind == FOAK_GATE_CHANNEL && a.dgate) || a.dpost_gamma;
     const bool full = a.gate_kind == FOAK_GATE_FULL, row_grad = a.gate_kind == FOAK_GATE_ROW && a.dgate;
     const int64_t nvec = a.D / (16 / ES);
-    int G = static_cast<int>(std::min<int64_t>(a.N, 128));
+    int G = std::min(groups, kResNormColsGroups);
     cudaError_t e = cudaSuccess;
     // rows and row strides of 32 bits
     const int64_t ld = std::max({a.lddy, a.lddh, a.ldh, a.ldx, a.ldg, a.lddr, a.lddx, a.lddg});

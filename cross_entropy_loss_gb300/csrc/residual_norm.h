@@ -44,15 +44,21 @@ struct ResNormBwd {
 
 constexpr int64_t kResNormMaxD = 32768;  // a row of the forward as floats in shared memory
 
-// Partial sums of up to this many groups of rows, for the two gradients that are summed over the rows: 16 MB
-// each, which is as many groups as are resident at once, whatever D.
-inline int resnorm_groups(int64_t D) {
-    const int64_t n = (1 << 22) / D;
-    return static_cast<int>(n < 128 ? 128 : n > 2432 ? 2432 : n);
+// Groups of rows that the two gradients which are summed over the rows have partial sums of, at most: one a row, 16 MB
+// each, and 16 an SM.  The backward has as many as are resident at once (rows over a cluster far fewer), or 128.
+constexpr int kResNormColsGroups = 128, kResNormMaxGroups = 2432;
+inline int resnorm_groups(int64_t N, int64_t D) {
+    static_assert((1 << 22) / kResNormMaxD >= kResNormColsGroups, "the groups of the longest rows");
+    const int64_t room = (1 << 22) / D, most = room < kResNormMaxGroups ? room : kResNormMaxGroups;
+    return static_cast<int>(N < 1 ? 1 : N < most ? N : most);
 }
+// What a row's elements need of the row's sums, where those are taken first (residual_norm.cu).
+struct RowStats {
+    float k1, k2;
+};
 inline size_t resnorm_workspace_bytes(int64_t N, int64_t D) {
-    const size_t part = static_cast<size_t>(resnorm_groups(D)) * static_cast<size_t>(D) * 4;
-    return (2 * part + static_cast<size_t>(N) * 16 + 255) / 256 * 256;
+    const size_t part = static_cast<size_t>(resnorm_groups(N, D)) * static_cast<size_t>(D) * 4;
+    return (2 * part + static_cast<size_t>(N) * sizeof(RowStats) + 255) / 256 * 256;
 }
 
 cudaError_t launch_resnorm_fwd(int es, const ResNormFwd& a, cudaStream_t s);

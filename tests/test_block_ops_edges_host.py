@@ -37,3 +37,19 @@ def test_turns_to_the_last_bit_but_one(so):  # noqa: F811
         off = (Fraction(t, 2 ** 64) - Fraction(f) / (2 * pi)) % 1
         assert min(off, 1 - off) <= Fraction(1, 2 ** 63), f
     assert len(so.foak_rotary_turns([1e300, -1e300, 1.7976931348623157e308])) == 3  # any number of turns is taken
+
+
+def test_workspace_goes_by_the_rows(so):  # noqa: F811
+    """Partial sums of as many groups as there can be, two of D floats each, and two floats a row; up to 255 bytes of
+    rounding.  Of few rows little, of more rows no less."""
+    size = so.foak_residual_norm_workspace_size
+    for D in (8, 4096, 16384, 32768):
+        assert 0 < size(0, D) <= size(1, D) <= 2 * D * 4 + 8 + 255
+        assert size(100, D) <= 100 * (2 * D * 4 + 8) + 255
+        sizes = [size(N, D) for N in (0, 1, 2, 127, 128, 129, 2431, 2432, 2433, 100000, 100001)]
+        assert sizes == sorted(sizes)
+        assert size(100001, D) >= 2 * 128 * D * 4
+        change = {k: 1 << 16 for k in ("ldx", "lddy", "lddh", "ldh", "lddr", "lddx")}
+        for N in (1, 100, 100001):
+            assert _call(so, "foak_residual_norm_backward", BWD, N=N, D=D, wsb=size(N, D), **change) == so.FOAK_ERR_CUDA
+            assert _call(so, "foak_residual_norm_backward", BWD, N=N, D=D, wsb=size(N, D) - 1, **change) == so.FOAK_ERR_WORKSPACE
