@@ -48,13 +48,6 @@ template <int PENDING>
 __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
 }
-__device__ __forceinline__ void cp_async_wait_all_but(int pending) {
-    if (pending == 1) cp_async_wait<1>();
-    else if (pending == 2) cp_async_wait<2>();
-    else if (pending == 3) cp_async_wait<3>();
-    else cp_async_wait<0>();
-}
-
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
@@ -362,10 +355,16 @@ __device__ __forceinline__ float warp_sum4(float a, float b, float c, float d, i
     return z;
 }
 
+// Stages of the ring, of `operands` each: as many as leave room for 512 threads an SM.
+constexpr int ring_stages(int operands) {
+    const int n = kRingSmem / kRowThreads / (operands * kVpt * 16);
+    return n < 4 ? n : 4;
+}
+static_assert(ring_stages(3) == 4 && ring_stages(4) == 3 && ring_stages(5) == 2, "two stages or more");
+
 struct BwdSplit {
-    int cluster;  // CTAs a row
-    int stages;   // of the ring
-    int slice;    // vectors of a CTA's slice
+    int cluster;             // CTAs a row
+    int slice;               // vectors of a CTA's slice
     uint32_t in[5], out[3];  // bytes from row to row of dY, H, dH, X, gate; dR, dX, dgate
 };
 
@@ -376,7 +375,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
                             float* __restrict__ part2) {
     griddep_launch_dependents();  // programmatic dependent launch: no global access before the wait
     using P = Pairs<ES>;
-    constexpr int EPV = 16 / ES, NP = P::N, NS = 3 + HASX + FULL, NSUM = SUMS ? 4 : 1;
+    constexpr int EPV = 16 / ES, NP = P::N, NS = 3 + HASX + FULL, NSUM = SUMS ? 4 : 1, kStages = ring_stages(NS);
     extern __shared__ uint4 ring[];  // [stages][NS][kVpt][threads], then the rows' sums: [2][warps of the cluster][NSUM]
     const int v = threadIdx.x, lane = v & 31, warp = v >> 5, nt = blockDim.x, warps = nt >> 5;
     const int C = sp.cluster, rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -393,12 +392,12 @@ __global__ void __launch_bounds__(kRowThreads, 1)
     const int rows = static_cast<int>(a.N * (cid + 1) / clusters - r_begin);
     const float inv_d = 1.f / static_cast<float>(a.D);
     const int plane = kVpt * nt;  // vectors of an operand
-    float* red = reinterpret_cast<float*>(ring + sp.stages * NS * plane);
+    float* red = reinterpret_cast<float*>(ring + kStages * NS * plane);
     // An operand that is not there reads as zeros, and so does a vector past the slice's end: the sums below
     // go through all of a thread's vectors without a branch.
 #pragma unroll
     for (int j = 0; j < kVpt; ++j) {
-        for (int i = 0; i < sp.stages * NS; ++i) {
+        for (int i = 0; i < kStages * NS; ++i) {
             const int operand = i % NS;
             if (!act[j] || (operand < 2 && !a.dY) || (operand == 2 && !a.dH))
                 ring[i * plane + j * nt + v] = make_uint4(0u, 0u, 0u, 0u);
@@ -429,7 +428,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
         }
         cp_async_commit();
     };
-    for (int s = 0; s < sp.stages - 1; ++s) issue(s);
+    for (int s = 0; s < kStages - 1; ++s) issue(s);
     P gm[kVpt], pe[kVpt], acc1[kVpt], acc2[kVpt];
 #pragma unroll
     for (int j = 0; j < kVpt; ++j) {
@@ -513,17 +512,17 @@ __global__ void __launch_bounds__(kRowThreads, 1)
     const auto slot_of = [&](int s) { return ring + s * (NS * plane) + v; };
     Scalars now = scalars(0), next_row = scalars(1);
     if constexpr (kAhead) {
-        cp_async_wait_all_but(sp.stages - 2);  // this thread's copies of the first row have landed
+        cp_async_wait<kStages - 2>();  // this thread's copies of the first row have landed
         if (rows > 0) post(0, sums(slot_of(0), now.r));
     }
     for (int n = 0; n < rows; ++n) {
         const Scalars ahead = scalars(n + 2);
         const float r = now.r, r1 = now.r1, q = now.q;
         const uint4* slot = slot_of(stage);
-        const int free_stage = stage == 0 ? sp.stages - 1 : stage - 1;  // the row before's
-        stage = stage + 1 == sp.stages ? 0 : stage + 1;
+        const int free_stage = stage == 0 ? kStages - 1 : stage - 1;  // the row before's
+        stage = stage + 1 == kStages ? 0 : stage + 1;
         issue(free_stage);
-        cp_async_wait_all_but(sp.stages - (kAhead ? 2 : 1));
+        cp_async_wait<kStages - (kAhead ? 2 : 1)>();
         float z_next = 0.f;
         if constexpr (kAhead) {
             if (n + 1 < rows) z_next = sums(slot_of(stage), next_row.r);
@@ -727,7 +726,7 @@ template <int ES, bool POST, bool FULL, bool HASX, bool SUMS>
 cudaError_t launch_ring(const ResNormBwd& a, const BwdSplit& sp, int threads, float* part1, float* part2, int* groups,
                         cudaStream_t s) {
     const auto kernel = resnorm_bwd_ring_kernel<ES, POST, FULL, HASX, SUMS>;
-    const size_t smem = static_cast<size_t>(sp.stages) * (3 + HASX + FULL) * kVpt * threads * 16 +
+    const size_t smem = static_cast<size_t>(ring_stages(3 + HASX + FULL)) * (3 + HASX + FULL) * kVpt * threads * 16 +
                         static_cast<size_t>(sp.cluster) * (threads / 32) * (SUMS ? 32 : 8);
     static SmemOnce limit;
     static ResidentOnce resident;
@@ -748,11 +747,7 @@ uint32_t bytes_of(int64_t ld) {
 template <int ES, bool POST, bool FULL, bool HASX, bool SUMS>
 cudaError_t ring(const ResNormBwd& a, float* part1, float* part2, int* groups, cudaStream_t s) {
     const Slices c = slices_of(a.D / (16 / ES));
-    const int row = (3 + HASX + FULL) * kVpt * c.threads * 16;
-    // as many stages as leave room for 512 threads an SM: four of three operands, three of four, two of five
-    const int stages = kRingSmem / kRowThreads * c.threads / row;
-    static_assert(kRingSmem / kRowThreads / (5 * kVpt * 16) >= 2, "two stages");
-    const BwdSplit sp = {c.cluster, std::min(stages, 4), c.slice,
+    const BwdSplit sp = {c.cluster, c.slice,
                          {bytes_of<ES>(a.lddy), bytes_of<ES>(a.ldh), bytes_of<ES>(a.lddh), bytes_of<ES>(a.ldx), bytes_of<ES>(a.ldg)},
                          {bytes_of<ES>(a.lddr), bytes_of<ES>(a.lddx), bytes_of<ES>(a.lddg)}};
     return launch_ring<ES, POST, FULL, HASX, SUMS>(a, sp, c.threads, part1, part2, groups, s);
@@ -782,7 +777,8 @@ cudaError_t bwd(const ResNormBwd& a, void* workspace, cudaStream_t s) {
     cudaError_t e = cudaSuccess;
     // rows and row strides of 32 bits
     const int64_t ld = std::max({a.lddy, a.lddh, a.ldh, a.ldx, a.ldg, a.lddr, a.lddx, a.lddg});
-    const bool one_pass = a.N < (1ll << 31) && ld * ES < (1ll << 32) && nvec <= static_cast<int64_t>(kMaxCluster) * kVpt * kRowThreads && (a.X || !full);
+    const bool one_pass = a.N < (1ll << 31) && ld * ES < (1ll << 32) && (a.X || !full);
+    static_assert(kResNormMaxD / (16 / ES) <= kMaxCluster * kVpt * kRowThreads, "a row fits a cluster");
     if (one_pass) {
         float* p2 = second ? part2 : nullptr;
         if (a.post_gamma)
