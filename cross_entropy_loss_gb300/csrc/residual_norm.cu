@@ -188,8 +188,9 @@ __global__ void __launch_bounds__(kFwdThreads, 2) resnorm_fwd_kernel(const __gri
 
 // ------------------------------------------------------------------ backward, any rows
 // Sums first, then the columns: for row strides or counts past 32 bits, and for a full gate whose gradient nobody
-// wants.  What a row's elements need of the row's sums (RowStats): dh = dH + r gamma dY - k1 H, and with the norm
-// after the block dX = r1 gp du - k2 X.
+// wants (bf16 8192 x 4096 163 us, where the one-pass kernel takes 92 with that gradient; 13534 x 560 198 and 26).
+// What a row's elements need of the row's sums (RowStats): dh = dH + r gamma dY - k1 H, and with the norm after the
+// block dX = r1 gp du - k2 X.
 template <int ES>
 __device__ __forceinline__ const char* gate_row(const ResNormBwd& a, int64_t i) {
     return a.gate_kind == FOAK_GATE_CHANNEL ? a.gate : a.gate + i * a.ldg * ES;
@@ -340,8 +341,8 @@ __global__ void __launch_bounds__(128) resnorm_bwd_cols_kernel(const ResNormBwd 
 // Arithmetic on pairs (two-wide FP32).
 //
 // Bound by memory and, in bf16, by how many instructions 16 warps an SM get out (half of the issue slots).  bf16,
-// us: 8192 x 4096 60 (0.84 of the copy rate; the reduce 4 to 6 of them), both norms and a channel gate 73; 4096 x
-// 8192 58 (256 threads and clusters of two 70); 2048 x 16384 66 (waiting at the barrier for the row's sums, not
+// us: 8192 x 4096 60 (0.83 of the copy rate; the reduce 4 to 6 of them), both norms and a channel gate 73; 4096 x
+// 8192 59 (256 threads and clusters of two 70); 2048 x 16384 64 (waiting at the barrier for the row's sums, not
 // with the next row's sums in between, 87); 8192 x 4096 reading each operand twice, sums first, 139.  An element's
 // intermediate results kept across the barrier spill: 86 against 71 with both norms.
 // The warp's sums of four values with six shuffles: lanes 8 v .. 8 v + 7 get value v.
@@ -713,7 +714,9 @@ cudaError_t fwd(const ResNormFwd& a, cudaStream_t s) {
     // Two vectors a thread; one where the rows do not fill the GPU (1 row of 4096 bf16 1.8 us against 2.2, 300 rows
     // 3.0 against 4.5).  Of fp32 rows with a norm after the block, which come by three times and keep half as much in
     // shared memory, four where that leaves CTAs of 256 to 512 threads (1537 x 5000 27.2 us against 29.4, 1500 x 7168
-    // 35.7 against 38.7; 2048 vectors of bf16 57.9 against 52.1).
+    // 35.7 against 38.7; near the ends 5482 x 4104 58.6 against 71.5, 2749 x 8184 59.5 against 67.1; bf16 of 2048
+    // vectors 57.9 against 52.1).  Beyond either end four is faster as well where it was tried: 6250 x 3600 57.8
+    // against 64.8, 2197 x 10240 56.4 against 63.9.
     const bool small = a.N <= 2 * static_cast<int64_t>(device_sm_count());
     const bool four = ES == 4 && a.post_gamma && nvec > 1024 && nvec < 2048;
     const int64_t each = small ? 1 : four ? 4 : 2;

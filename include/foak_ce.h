@@ -347,7 +347,8 @@ foak_status foak_rope_apply_qk(void* Q, int64_t Hq, int64_t ldq, void* K, int64_
  *   gate (device)       by gate_kind: FOAK_GATE_NONE (NULL); FOAK_GATE_CHANNEL: D values;
  *                       FOAK_GATE_ROW: N values, ldg elements apart; FOAK_GATE_FULL: N x D,
  *                       row stride ldg; all in dtype
- *   post_gamma (device) D in dtype, or NULL: no norm after the block
+ *   post_gamma (device) D in dtype (gains kept in fp32 beside bf16 rows are not taken), or NULL: no
+ *                       norm after the block
  *   gamma (device)      D in dtype, or NULL: no norm before the next block (Y must be NULL)
  *   H, Y (device)       N x D in dtype, row strides ldh, ldy.  H may equal R or X; Y may equal X
  *                       or R, but not H; otherwise outputs overlap nothing
